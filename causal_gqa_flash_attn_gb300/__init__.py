@@ -25,10 +25,14 @@ KV_FP8_E4M3 = 3
 Q4_SINK_MAX = 8
 Q4_RING_ROWS = 256
 
+T_F32, T_F16, T_BF16 = 0, 1, 2
+_TYPES = {torch.float32: T_F32, torch.float16: T_F16, torch.bfloat16: T_BF16}
+
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE, ERR_TIMEOUT, ERR_WORKSPACE = range(7)
 
 # Public entry points of include/fa.h with their ctypes signatures.
 _P, _I, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_L, _F = ctypes.c_int64, ctypes.c_float
 SIGNATURES = {
     "fa_kv_plane_bytes": (_SZ, [_I, _I, _I, _I]),
     "fa_kv_plane_layout": (_I, [_I, _I, _I, _I, _P, _P, _P, _P]),
@@ -53,6 +57,16 @@ SIGNATURES = {
     "fa_decode_combine": (_I, [_P, _P, _I, _I, _I, _I, _P]),
     "fa_decode_noalloc": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I,
                                _P, _P]),
+    "fa_page_bytes": (_SZ, [_I, _I, _I]),
+    "fa_page_plan": (_I, [_P, _P, _I, _P, _I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _I, _P]),
+    "fa_rope_table": (_I, [_P, _P, _I, _P, _I, _I]),
+    "fa_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _L, _P, _L, _I, _P, _I,
+                     _I, _P]),
+    "fa_paged_append": (_I, [_P, _P, _I, _L, _L, _P, _I, _P, _I, _I, _I, _I, _P]),
+    "fa_paged_gather": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "fa_paged_attn_workspace_bytes": (_SZ, [_I]),
+    "fa_paged_attn": (_I, [_P, _P, _P, _I, _L, _L, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                           _I, _I, _I, _F, _P, _SZ, _P]),
     "fa_set_kernel_events": (_I, [_P, _P]),
     "fa_get_device_error": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -294,6 +308,204 @@ def decode_noalloc(q, k_planes, v_planes, pos, out, *, n_q_heads: int, n_kv_head
         n_q_heads, n_kv_heads, head_dim, max_seq, sink, win, kv_fmt, shadow_sink, shadow_win,
         split_keys, max_splits, _dev(out, torch.float32, "out"), _stream(stream)),
         "fa_decode_noalloc")
+
+
+# ----------------------------------------------------------- paged serving
+
+def _here(*tensors):
+    """The tensors are on the current device, where the call launches."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"every tensor must be on the current device, cuda:{here}; "
+                             f"got one on {t.device}")
+
+
+def _heads(t: torch.Tensor, name: str, dtype=None):
+    """(pointer, token stride) of a [tokens][heads][head_dim] tensor whose tokens
+    may lie apart (a slice of a fused projection's output)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
+    tokens, heads, hd = t.shape
+    row = heads * hd
+    step, head, one = t.stride()
+    if (one != 1 and hd > 1) or (head != hd and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    if tokens > 1:
+        if step < row:
+            raise ValueError(f"{name}: tokens overlap")
+        return t.data_ptr(), step
+    return t.data_ptr(), max(step, row)
+
+
+def _ints(t: torch.Tensor, name: str, shape):
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return _dev(t, torch.int32, name)
+
+
+def page_bytes(n_kv_heads: int, head_dim: int, page_rows: int) -> int:
+    return int(lib().fa_page_bytes(n_kv_heads, head_dim, page_rows))
+
+
+def alloc_pages(n_pages: int, n_kv_heads: int, head_dim: int, page_rows: int,
+                device="cuda") -> torch.Tensor:
+    """n_pages 4-bit pages as one uint8 tensor (their contents need no preparation)."""
+    pb = page_bytes(n_kv_heads, head_dim, page_rows)
+    if pb == 0:
+        raise ValueError("invalid page geometry")
+    return torch.empty(n_pages * pb, dtype=torch.uint8, device=device)
+
+
+def _pages(pages, n_kv_heads: int, head_dim: int, page_rows: int):
+    pb = lib().fa_page_bytes(n_kv_heads, head_dim, page_rows)
+    n = pages.numel()
+    if pb == 0 or n == 0 or n % pb:
+        raise ValueError("pages is not a whole number of pages of this geometry")
+    return _dev(pages, torch.uint8, "pages"), n // pb
+
+
+def page_plan(cached, fresh, free_ring, ring_state, block_table, ring_state_out, seq_lens,
+              cu_fresh, slot_map, positions, *, page_rows: int, stream=None):
+    """fa_page_plan: one step's block-table entries, slots and positions from the
+    requests' lengths. All int32: cached, fresh, seq_lens [R], block_table
+    [R][max_pages], free_ring [n_pages], ring_state [2], ring_state_out [3],
+    cu_fresh [R + 1], slot_map and positions [max_tokens]."""
+    R, T = cached.numel(), slot_map.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
+                         f"{tuple(block_table.shape)}")
+    _here(cached, fresh, free_ring, ring_state, block_table, ring_state_out, seq_lens, cu_fresh,
+          slot_map, positions)
+    _check(lib().fa_page_plan(
+        _ints(cached, "cached", (R,)), _ints(fresh, "fresh", (R,)), R,
+        _dev(free_ring, torch.int32, "free_ring"), free_ring.numel(),
+        _ints(ring_state, "ring_state", (2,)), _ints(ring_state_out, "ring_state_out", (3,)),
+        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], page_rows,
+        _ints(seq_lens, "seq_lens", (R,)), _ints(cu_fresh, "cu_fresh", (R + 1,)),
+        _ints(slot_map, "slot_map", (T,)), _ints(positions, "positions", (T,)), T,
+        _stream(stream)), "fa_page_plan")
+
+
+def rope_table(inv_freq, sections=None, *, interleaved: bool = False,
+               device="cuda") -> torch.Tensor:
+    """fa_rope_table on the device, [pairs][4] int32: inv_freq in radians per
+    position (any sequence of floats), sections the pairs that turn with each
+    position axis (default: all with one axis)."""
+    freq = [float(f) for f in inv_freq]
+    n = len(freq)
+    sections = [n] if sections is None else [int(x) for x in sections]
+    host = torch.empty((n, 4), dtype=torch.int32)
+    _check(lib().fa_rope_table(host.data_ptr(), (ctypes.c_double * n)(*freq), n,
+                               (ctypes.c_int * len(sections))(*sections), len(sections),
+                               int(interleaved)), "fa_rope_table")
+    return host.to(device)
+
+
+def rope(q, k, q_out, k_out, positions, table, *, adjacent: bool = False, inverse: bool = False,
+         stream=None):
+    """fa_rope: q [T][Hq][hd] and k [T][Hkv][hd] (either pair may be None) rotated
+    into q_out and k_out (the same tensors: in place) by positions [n_axes][T]
+    int32 ([T] for one axis) and a table of rope_table, whose length is half the
+    rotated dims."""
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("rope needs q or k")
+    T, _, hd = some.shape
+    ptrs, strides, heads = [], [], []
+    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
+        if (x is None) != (y is None):
+            raise ValueError(f"{name} and {name}_out go together")
+        if x is None:
+            ptrs += [None, None]
+            strides += [0, 0]
+            heads.append(0)
+            continue
+        if x.shape != y.shape or x.shape[0] != T or x.shape[2] != hd:
+            raise ValueError(f"{name} and {name}_out must have shape ({T}, heads, {hd})")
+        for t, what in ((x, name), (y, name + "_out")):
+            p, step = _heads(t, what, some.dtype)
+            ptrs.append(p)
+            strides.append(step)
+        heads.append(x.shape[1])
+    if positions.dim() == 1:
+        positions = positions.unsqueeze(0)
+    if positions.shape[1] != T:
+        raise ValueError(f"positions must have shape (n_axes, {T}), got {tuple(positions.shape)}")
+    if table.dim() != 2 or table.shape[1] != 4:
+        raise ValueError("table must come from rope_table")
+    _here(q, k, q_out, k_out, positions, table)
+    _check(lib().fa_rope(
+        *ptrs, _TYPES[some.dtype], T, *heads, hd, 2 * table.shape[0], *strides,
+        _dev(positions, torch.int32, "positions"), T, positions.shape[0],
+        _dev(table, torch.int32, "table"), adjacent, inverse, _stream(stream)), "fa_rope")
+
+
+def paged_append(k_new, v_new, slot_map, pages, *, page_rows: int, stream=None):
+    """fa_paged_append: k_new, v_new [T][Hkv][hd] into the rows slot_map [T] int32."""
+    T, hkv, hd = k_new.shape
+    if v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must have the same shape")
+    kp, ks = _heads(k_new, "k_new")
+    vp, vs = _heads(v_new, "v_new", k_new.dtype)
+    pp, n_pages = _pages(pages, hkv, hd, page_rows)
+    _here(k_new, v_new, slot_map, pages)
+    _check(lib().fa_paged_append(kp, vp, _TYPES[k_new.dtype], ks, vs,
+                                 _ints(slot_map, "slot_map", (T,)), T, pp, n_pages, hkv, hd,
+                                 page_rows, _stream(stream)), "fa_paged_append")
+
+
+def paged_gather(pages, block_table, seq_lens, k_planes, v_planes, *, n_kv_heads: int,
+                 head_dim: int, page_rows: int, max_seq: int, stream=None):
+    """fa_paged_gather: rows 0 .. seq_lens[r]-1 of each request into KV_F16 planes
+    (uint8, one plane for each request)."""
+    R = seq_lens.numel()
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
+                         f"{tuple(block_table.shape)}")
+    pb = lib().fa_kv_plane_bytes(KV_F16, n_kv_heads, max_seq, head_dim)
+    if pb == 0 or k_planes.numel() != R * pb or v_planes.numel() != R * pb:
+        raise ValueError("k_planes and v_planes must be one KV_F16 plane for each request")
+    pp, n_pages = _pages(pages, n_kv_heads, head_dim, page_rows)
+    _here(pages, block_table, seq_lens, k_planes, v_planes)
+    _check(lib().fa_paged_gather(
+        pp, n_pages, _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
+        _ints(seq_lens, "seq_lens", (R,)), R, n_kv_heads, head_dim, page_rows,
+        _dev(k_planes, torch.uint8, "k_planes"), _dev(v_planes, torch.uint8, "v_planes"),
+        max_seq, _stream(stream)), "fa_paged_gather")
+
+
+def paged_attn_workspace_bytes(head_dim: int) -> int:
+    return int(lib().fa_paged_attn_workspace_bytes(head_dim))
+
+
+def paged_attn(q, out, cu_q, seq_lens, block_table, pages, *, n_kv_heads: int, page_rows: int,
+               sink: int = 0, win: int = 0, scale: float = 0.0, lse=None, workspace,
+               stream=None):
+    """fa_paged_attn: q, out [T][Hq][hd] (tokens may lie apart), cu_q [R + 1] and
+    seq_lens [R] int32, block_table [R][max_pages] int32, lse [Hq][T] fp32 or None."""
+    T, hq, hd = q.shape
+    R = seq_lens.numel()
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
+                         f"{tuple(block_table.shape)}")
+    if lse is not None and lse.shape != (hq, T):
+        raise ValueError(f"lse must have shape ({hq}, {T}), got {tuple(lse.shape)}")
+    qp, qs = _heads(q, "q")
+    op, os_ = _heads(out, "out", q.dtype)
+    pp, n_pages = _pages(pages, n_kv_heads, hd, page_rows)
+    _here(q, out, cu_q, seq_lens, block_table, pages, lse, workspace)
+    _check(lib().fa_paged_attn(
+        qp, op, _dev(lse, torch.float32, "lse"), _TYPES[q.dtype], qs, os_,
+        _ints(cu_q, "cu_q", (R + 1,)), _ints(seq_lens, "seq_lens", (R,)),
+        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], pp, n_pages,
+        page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale,
+        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
+        "fa_paged_attn")
 
 
 def set_kernel_events(start, stop):

@@ -119,6 +119,62 @@ cudaError_t launch_merge_attn_states(float *out, float *out_lse, const float *pr
                                      const float *suffix_lse, int T, int H, int D,
                                      int with_context, cudaStream_t stream);
 
+// ---- element types of activations (include/fa.h FA_T_*)
+constexpr int kTypeF32 = 0;
+constexpr int kTypeF16 = 1;
+constexpr int kTypeBF16 = 2;
+
+// ---- paged_plan.cu
+struct PlanArgs {
+    const int32_t *cached, *fresh;  // [n_reqs]
+    int n_reqs;
+    int32_t *ring;         // [n_pages]
+    const int32_t *state;  // {head, count}
+    int n_pages;
+    int32_t *state_out;    // {head, count, pages missing}
+    int32_t *block_table;  // [n_reqs][max_pages]
+    int max_pages, page_shift;
+    int32_t *seq_lens, *cu_fresh, *slot_map, *positions;
+    int max_tokens;
+    unsigned *err;
+};
+constexpr int kPlanMaxReqs = 16384;
+cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream);
+
+// ---- rope.cu
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements between tokens
+    int dtype, n_tokens, n_q_heads, n_kv_heads, head_dim, rotary_dim;
+    const int32_t *positions;  // [n_axes] rows, pos_stride apart
+    long long pos_stride;
+    int n_axes;
+    const void *table;  // [rotary_dim / 2] entries of 16 bytes
+    bool adjacent, inverse;
+    int n_copy = 0, heads_per_block = 0;  // set by the launch
+};
+cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);
+
+// ---- paged_kv.cu, paged_attn.cu (byte order of the pages: paged_layout.cuh)
+struct Pages;
+struct PagedAppendArgs {
+    const void *k, *v;
+    long long k_stride, v_stride;
+    const int32_t *slot_map;
+    int n_tokens, n_kv;
+    uint8_t *pages;
+    int n_pages, page_shift;
+    unsigned *err;
+};
+cudaError_t launch_paged_append(const PagedAppendArgs &a, int dtype, int hd, cudaStream_t stream);
+struct PagedGatherArgs;
+cudaError_t launch_paged_gather(const PagedGatherArgs &a, int n_reqs, int hd,
+                                cudaStream_t stream);
+struct PagedAttnArgs;
+size_t paged_attn_ws_bytes(int hd);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream);
+
 // ---- decode.cu
 struct DecodeArgs {
     const float *q;

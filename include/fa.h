@@ -370,6 +370,184 @@ fa_status fa_decode_noalloc(const float *q, const void *k_planes, const void *v_
                             int shadow_sink, int shadow_win, int split_keys, int max_splits,
                             float *out, fa_stream_t stream);
 
+/* ---------------------------------------------------------- paged serving
+ *
+ * A server whose requests grow and end at different times keeps its cache in
+ * pages: a step is planned from the requests' lengths (fa_page_plan), q and k
+ * are rotated to the tokens' positions (fa_rope), the new rows are written by
+ * slot (fa_paged_append), and attention reads the pages through the block
+ * table (fa_paged_attn). For long chunks the pages become fp16 planes
+ * (fa_paged_gather) that fa_prefill_chunk reads in place.
+ *
+ * Element types of activations: */
+enum { FA_T_F32 = 0, FA_T_F16 = 1, FA_T_BF16 = 2 };
+
+/* 4-bit pages
+ *
+ * A page holds page_rows rows (16, 32, 64, 128 or 256) of K and V of every kv
+ * head; n_pages pages are one contiguous buffer, 16-byte aligned:
+ *   [n_pages][n_kv_heads][page_rows / 16] groups of 16 rows.
+ * A group is a K part and then a V part, 9 * head_dim + 32 bytes each:
+ *   codes    8 * head_dim bytes, 4 bits a value
+ *   scales   binary16, one for each row and 32-value block
+ *   factors  bfloat16 powers of two, one for each row
+ * and a value is (code - 8) * scale * factor, the product in fp32. The encoder
+ * is that of FA_KV_Q4_0 (d = amax / -8, code = clamp(round_half_even(x / d) +
+ * 8, 0, 15) with the fp32 reciprocal 1 / d), with the row's largest |d| brought
+ * into [1, 2) by the factor: rows of any magnitude keep their precision.
+ *
+ * Byte order inside a part (nb = head_dim / 32, row r = 0..15, block b, dims
+ * counted from 0 inside a block; the lower dim has the lower 4 bits of a byte):
+ *   K codes  j = (r / 8) * nb + b: dims 8t .. 8t+7 (t = 0..3) are the 4 bytes at
+ *            ((j / 4) * 32 + (r % 8) * 4 + t) * 16 + (j % 4) * 4
+ *   V codes  x = r % 2 + 2 * (r / 8), j = x * nb + b: dims 4g .. 4g+3 (g = 0..7)
+ *            are the 2 bytes at
+ *            ((j / 8) * 32 + g * 4 + (r % 8) / 2) * 16 + (j % 8) * 2
+ *   K scale  8 * head_dim + 2 * (r * nb + b)
+ *   V scale  8 * head_dim + 2 * (((b / 2) * 4 + (r % 8) / 2) * 8 + (b % 2) * 4 + x)
+ *   factor   9 * head_dim + 2 * r
+ * This is the order in which the tensor cores take the codes. The bytes are an
+ * interface, as those of the planes are. Pages need no initialisation: rows
+ * past a request's length are never used. */
+
+/* Bytes of one page, or 0 for an invalid or unsupported geometry. */
+size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
+
+/* Plan one step of n_reqs requests from their lengths: which pages the fresh
+ * rows take, where each token's row goes, and at which position it sits.
+ *
+ *   cached     [n_reqs] int32 (device): rows that request r has in its pages.
+ *   fresh      [n_reqs] int32 (device): rows it appends in this step (0 for a
+ *              request that waits or pads the batch), or -1: it is finished and
+ *              gives its pages back.
+ *   free_ring  [n_pages] int32 (device): the free pages, a ring; read from its
+ *              head, written behind its tail.
+ *   ring_state [2] int32 (device): {head, count}. ring_state_out [3]: {head,
+ *              count} after the step and the number of pages that were missing.
+ *   block_table [n_reqs][max_pages] int32 (device): pages of each request in
+ *              order; the entries of new pages are written, all others stay as
+ *              they are (those of a finished request are stale).
+ *   seq_lens   [n_reqs] int32, written: cached + fresh; 0 for a finished request.
+ *   cu_fresh   [n_reqs + 1] int32, written: where each request's tokens begin in
+ *              the packed batch (sums of max(fresh, 0)).
+ *   slot_map, positions  [max_tokens] int32, written: page * page_rows + row of
+ *              each token of the packed batch, and its position; -1 and 0 for
+ *              tokens past the last one.
+ *
+ * Pages are handed out in request order from the head. A request whose new
+ * pages are not all left, counting those of every request before it, gets none:
+ * its tokens' slots are -1 and its seq_lens entry stays at cached. Pages given
+ * back in this step are handed out from the next one on.
+ *
+ * FA_ERR_DEVICE is flagged for lengths out of range (cached < 0, fresh < -1,
+ * more than max_pages pages: the request gets no slots and length 0), a state
+ * out of range (nothing is handed out or taken back), more returned pages than
+ * the ring has room for, a table entry outside [0, n_pages) under a fresh token
+ * (slot -1), or more than max_tokens tokens (cu_fresh is cut there).
+ * No output may overlap an input or another output; free_ring and block_table
+ * are updated in place. n_reqs <= 16384 (FA_ERR_UNSUPPORTED); max_pages *
+ * page_rows <= 2^30, n_pages * page_rows < 2^31. */
+fa_status fa_page_plan(const int32_t *cached, const int32_t *fresh, int n_reqs,
+                       int32_t *free_ring, int n_pages, const int32_t *ring_state,
+                       int32_t *ring_state_out, int32_t *block_table, int max_pages,
+                       int page_rows, int32_t *seq_lens, int32_t *cu_fresh, int32_t *slot_map,
+                       int32_t *positions, int max_tokens, fa_stream_t stream);
+
+/* Entries of a rotation table, made once for a model: `table` is HOST memory
+ * for pairs entries of 16 bytes, {low, high word of 2^64 * (inv_freq[i] / (2 pi)
+ * mod 1), axis, 0}; copy it to the device for fa_rope. inv_freq[i] is the angle
+ * in radians per position of pair i (finite, >= 0). sections[n_axes] says how
+ * many pairs turn with each axis (sum = pairs): in order, or, interleaved, pair
+ * i with axis i % n_axes while i < n_axes * sections[i % n_axes] and with axis
+ * 0 otherwise (sections that leave another count than stated are refused). */
+fa_status fa_rope_table(uint32_t *table, const double *inv_freq, int pairs, const int *sections,
+                        int n_axes, int interleaved);
+
+/* Rotary positions: pair i of every head of token t is rotated by
+ * positions[axis(i)][t] * inv_freq[i]; the first rotary_dim values of a head
+ * are its pairs, (i, i + rotary_dim / 2), or (2i, 2i + 1) with adjacent != 0,
+ * the others are copied. inverse != 0 rotates back: the gradient of q and k
+ * from that of the rotated ones. Arithmetic is fp32, rounded once.
+ *   q, k       token t's heads start at element t * stride; a head is head_dim
+ *              contiguous values and heads follow each other. n_q_heads or
+ *              n_kv_heads may be 0, its pointers then NULL.
+ *   q_out, k_out  the same layout with their own strides; equal to q or k (with
+ *              the same stride) for rotation in place, else not overlapping.
+ *   dtype      FA_T_*. Pointers aligned to the element; where pointers, strides,
+ *              head_dim and rotary_dim / 2 are multiples of 16 bytes the call
+ *              moves 16 bytes at a time.
+ *   positions  [n_axes][pos_stride] int32 (device), n_axes 1..8, any value.
+ *   table      [rotary_dim / 2] entries of fa_rope_table (device, 16-byte aligned). */
+fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dtype, int n_tokens,
+                  int n_q_heads, int n_kv_heads, int head_dim, int rotary_dim, int64_t q_stride,
+                  int64_t q_out_stride, int64_t k_stride, int64_t k_out_stride,
+                  const int32_t *positions, int64_t pos_stride, int n_axes, const void *table,
+                  int adjacent, int inverse, fa_stream_t stream);
+
+/* Write new K/V rows into 4-bit pages.
+ *   k_new, v_new  [n_tokens] rows of [n_kv_heads][head_dim] values of dtype,
+ *              k_stride and v_stride elements apart; 16-byte aligned rows.
+ *   slot_map   [n_tokens] int32 (device): page * page_rows + row, or -1 to leave
+ *              the token out. Other values outside the pages flag FA_ERR_DEVICE
+ *              and are left out. Slots of one call must differ (those of
+ *              fa_page_plan do): a row written twice by one call holds a mixture
+ *              of both.
+ *   pages      n_pages pages of this geometry. */
+fa_status fa_paged_append(const void *k_new, const void *v_new, int dtype, int64_t k_stride,
+                          int64_t v_stride, const int32_t *slot_map, int n_tokens, void *pages,
+                          int n_pages, int n_kv_heads, int head_dim, int page_rows,
+                          fa_stream_t stream);
+
+/* Dequantise the pages of n_reqs requests into FA_KV_F16 planes (n_reqs
+ * consecutive K planes and V planes of [n_kv_heads][max_seq][head_dim]), rows
+ * 0 .. seq_lens[r] - 1 of each; the other rows stay as they are. Values past the
+ * binary16 range become infinite. A length below 0, above max_seq or above the
+ * table's rows is cut and flags FA_ERR_DEVICE; a table entry outside [0,
+ * n_pages) flags it too, and its rows stay as they are. n_reqs <= 65535. */
+fa_status fa_paged_gather(const void *pages, int n_pages, const int32_t *block_table,
+                          int max_pages, const int32_t *seq_lens, int n_reqs, int n_kv_heads,
+                          int head_dim, int page_rows, void *k_planes, void *v_planes,
+                          int max_seq, fa_stream_t stream);
+
+/* Workspace bytes of fa_paged_attn for a head_dim (at most 64 MiB, whatever the
+ * batch), or 0 for an unsupported one. */
+size_t fa_paged_attn_workspace_bytes(int head_dim);
+
+/* Attention of a packed batch of queries over 4-bit pages, one launch for
+ * requests of every length: decode steps, a few rows to verify a draft, short
+ * chunks.
+ *   q          token t's heads start at element t * q_stride, [n_q_heads]
+ *              [head_dim] values of dtype; 16-byte aligned rows.
+ *   out        written, the same layout with out_stride.
+ *   lse        [n_q_heads][n_tokens] fp32 (device) or NULL, written: the natural
+ *              log-sum-exp of each row's scores (-inf where nothing is attended).
+ *   cu_q       [n_reqs + 1] int32 (device), not decreasing: request r's queries
+ *              are tokens cu_q[r] .. cu_q[r+1]-1. Tokens outside every request
+ *              (padding) are neither read nor written.
+ *   seq_lens   [n_reqs] int32 (device): rows in r's pages, those of its queries
+ *              included: with n queries, query i sits at position
+ *              seq_lens[r] - n + i (below 0: it attends nothing).
+ *   block_table [n_reqs][max_pages] int32 (device). Only entries of pages with an
+ *              attended row are read: pages that left the window may be given back.
+ *   sink, win  the attended set, as for fa_prefill.
+ *   scale      of q . k, > 0; 0 means 1 / sqrt(head_dim).
+ *   workspace  >= fa_paged_attn_workspace_bytes(head_dim), 16-byte aligned; scratch.
+ *              Calls that share a workspace must not overlap on the GPU.
+ * A row that attends nothing gives 0 (lse -inf). Scores, softmax and sums are
+ * fp32. With FA_T_F32 every product is exact to about 2^-21; with FA_T_F16 and
+ * FA_T_BF16 the softmax weights are rounded to binary16 before the product with
+ * V, once for FA_T_BF16 and as a pair of terms (about 2^-21) for FA_T_F16.
+ * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_reqs <= 65536.
+ * FA_ERR_DEVICE is flagged for a request whose cu_q or seq_lens are out of range
+ * (its rows are not written), and for a table entry outside [0, n_pages) (its
+ * rows count as not attended). */
+fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
+                        int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
+                        const int32_t *block_table, int max_pages, const void *pages, int n_pages,
+                        int page_rows, int n_reqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                        int head_dim, int sink, int win, float scale, void *workspace,
+                        size_t workspace_bytes, fa_stream_t stream);
+
 /* ---------------------------------------------------------------- profiling */
 
 /* Optional timing hook. While both events are non-NULL (cudaEvent_t handles

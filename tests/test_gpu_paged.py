@@ -1,0 +1,778 @@
+"""Paged serving on the GPU against the definition in 64 bits (paged_ref.py)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from gpu_util import POISON_BYTE, check_guards, fa, guarded
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+def ints(a):
+    a = np.asarray(a, np.int32)
+    t = guarded(a.shape, torch.int32)
+    t.copy_(torch.from_numpy(a))
+    return t
+
+
+def on_gpu(x, dtype, spare=0):
+    """float64 numpy -> the GPU in a type; spare: values between the rows of dim 0 (a strided tensor)."""
+    x = ref.round_type(x, dtype)
+    if not spare:
+        return torch.from_numpy(x).to(DT[dtype]).cuda(), x
+    row = int(np.prod(x.shape[1:]))
+    wide = torch.full((x.shape[0], row + spare), float("nan"), dtype=DT[dtype], device="cuda")
+    t = wide[:, :row].unflatten(1, x.shape[1:])
+    t.copy_(torch.from_numpy(x))
+    return t, x
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+# --------------------------------------------------------------------- plan
+
+def random_step(rng, n_reqs, page_rows, max_pages, n_pages, most_fresh, short=0):
+    """A consistent state: lengths, a ring in the middle of its life, a table."""
+    most = max_pages * page_rows
+    fresh = np.where(rng.random(n_reqs) < 0.3, rng.integers(0, most_fresh + 1, n_reqs), 1)
+    fresh = np.where(rng.random(n_reqs) < 0.15, -1, np.minimum(fresh, most))
+    cached = np.minimum(rng.integers(0, most + 1, n_reqs), most - np.maximum(fresh, 0))
+    used = -(-cached // page_rows)
+    order = rng.permutation(n_pages)
+    assert used.sum() <= n_pages
+    table = np.full((n_reqs, max_pages), -1)
+    at = 0
+    for r in range(n_reqs):
+        table[r, :used[r]] = order[at:at + used[r]]
+        at += used[r]
+    free = order[at:len(order) - short] if short else order[at:]
+    head = int(rng.integers(n_pages))
+    ring = np.full(n_pages, -7)
+    ring[(head + np.arange(len(free))) % n_pages] = free
+    return cached, fresh, ring, [head, len(free)], table
+
+
+def run_plan(cached, fresh, ring, state, table, page_rows, max_tokens):
+    m = fa()
+    R = len(cached)
+    t = dict(cached=ints(cached), fresh=ints(fresh), free_ring=ints(ring), ring_state=ints(state),
+             block_table=ints(table), ring_state_out=ints([-9] * 3), seq_lens=ints([-9] * R),
+             cu_fresh=ints([-9] * (R + 1)), slot_map=ints([-9] * max_tokens),
+             positions=ints([-9] * max_tokens))
+    m.page_plan(*t.values(), page_rows=page_rows)
+    torch.cuda.synchronize()
+    check_guards(*t.items())
+    return t, dict(ring=t["free_ring"].tolist(), table=t["block_table"].tolist(), lens=t["seq_lens"].tolist(),
+                   cu=t["cu_fresh"].tolist(), slots=t["slot_map"].tolist(),
+                   positions=t["positions"].tolist(), state=t["ring_state_out"].tolist())
+
+
+@pytest.mark.parametrize("n_reqs,page_rows,max_pages,most_fresh,pad", [
+    (1, 16, 1, 16, 0), (1, 256, 3, 700, 9), (2, 16, 4, 3, 1), (33, 32, 5, 100, 0), (511, 16, 9, 40, 3),
+    (513, 64, 4, 90, 2), (1025, 128, 3, 11, 70), (5000, 16, 3, 30, 1)])
+def test_plan(n_reqs, page_rows, max_pages, most_fresh, pad):
+    rng = np.random.default_rng(n_reqs)
+    step = random_step(rng, n_reqs, page_rows, max_pages, n_reqs * max_pages + 3, most_fresh)
+    tokens = int(np.maximum(step[1], 0).sum()) + pad
+    _, got = run_plan(*step, page_rows, tokens)
+    want = ref.plan(*step, page_rows, tokens)
+    for name in want:
+        assert got[name] == [list(map(int, x)) if name == "table" else int(x) for x in want[name]], name
+    assert fa().get_device_error() == fa().OK
+
+
+def test_plan_with_too_few_pages_gives_them_in_order():
+    rng = np.random.default_rng(3)
+    for n_free in (0, 1, 5, 17):
+        cached = np.array([0, 16, 3, 31, 32, 7, 0, 64])
+        fresh = np.array([20, 1, 2, 1, 33, -1, 0, 1])
+        used = -(-cached // 16)
+        order = rng.permutation(40)
+        table, at = np.full((8, 6), -1), 0
+        for r in range(8):
+            table[r, :used[r]] = order[at:at + used[r]]
+            at += used[r]
+        ring = np.full(40, -7)
+        ring[(38 + np.arange(n_free)) % 40] = order[at:at + n_free]
+        step = (cached, fresh, ring, [38, n_free], table)
+        _, got = run_plan(*step, 16, 60)
+        want = ref.plan(*step, 16, 60)
+        for name in want:
+            assert got[name] == [list(map(int, x)) if name == "table" else int(x) for x in want[name]], (n_free, name)
+        assert fa().get_device_error() == fa().OK
+
+
+def test_plan_flags_bad_device_data_and_stays_in_bounds():
+    m = fa()
+    good = ([3, 20], [1, 1], [5, 4, 3, 2, 1, 0], [0, 3], [[0, -1], [1, 2]])
+
+    def flagged(cached=None, fresh=None, ring=None, state=None, table=None, tokens=4):
+        step = [x if y is None else y for x, y in zip(good, (cached, fresh, ring, state, table))]
+        _, got = run_plan(*step, 16, tokens)
+        assert m.get_device_error() == m.ERR_DEVICE
+        return got
+
+    got = flagged(cached=[-1, 20])
+    assert got["lens"] == [0, 21] and got["slots"] == [-1, 2 * 16 + 4, -1, -1] and got["cu"] == [0, 1, 2]
+    got = flagged(fresh=[30, 1], tokens=32)               # more rows than the table has pages for
+    assert got["lens"] == [0, 21] and got["slots"][:30] == [-1] * 30 and got["slots"][30] == 36
+    got = flagged(fresh=[1 << 30, 1])                     # and more tokens than there is room for
+    assert got["cu"] == [0, 4, 4] and got["slots"] == [-1] * 4
+    got = flagged(fresh=[-2, 1])
+    assert got["lens"] == [0, 21] and got["cu"] == [0, 0, 1]
+    for state in ([-1, 3], [6, 3], [0, 7], [0, -1]):
+        got = flagged(state=state, fresh=[14, -1], tokens=14)
+        assert got["lens"] == [3, 0] and got["state"][1] == 0 and got["state"][2] == 1
+        assert got["ring"] == good[2]
+    got = flagged(table=[[6, -1], [1, -1]])               # pages out of range under fresh tokens
+    assert got["slots"] == [-1] * 4 and got["lens"] == [4, 21]
+    got = flagged(state=[0, 5], fresh=[-1, -1])           # more pages back than the ring has room for
+    assert got["state"][1] == 6 and sorted(got["ring"][:5]) == [1, 2, 3, 4, 5] and got["ring"][5] == 0
+    got = flagged(tokens=1)                               # two tokens, room for one
+    assert got["cu"] == [0, 1, 1] and got["slots"] == [3]
+
+
+def test_plan_refuses_shapes():
+    m = fa()
+    z = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    args = [z(2), z(2), z(8), z(2), z(2, 3), z(3), z(2), z(3), z(4), z(4)]
+    for i, bad in ((1, z(3)), (3, z(3)), (4, z(3, 3)), (4, z(6)), (5, z(2)), (7, z(2)), (9, z(5)),
+                   (0, z(2).long()), (2, z(16)[::2]), (6, z(2).cpu())):
+        with pytest.raises(ValueError):
+            m.page_plan(*[bad if j == i else a for j, a in enumerate(args)], page_rows=16)
+
+
+# --------------------------------------------------------------------- rope
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("T,hq,hkv,hd,rd,sections,interleaved,adjacent,inverse,spare", [
+    (1, 1, 1, 64, 64, [32], False, False, False, 0),
+    (7, 8, 2, 64, 32, [16], False, True, False, 64),
+    (33, 16, 2, 256, 64, [12, 10, 10], True, False, True, 512),
+    (130, 4, 4, 128, 128, [16, 24, 24], False, False, False, 0),
+    (5, 3, 1, 96, 96, [24, 8, 8, 8], True, True, True, 8),
+    (3, 5, 0, 80, 20, [10], False, False, False, 3),      # nothing a multiple of 16 bytes
+    (2, 0, 3, 7, 6, [2, 1], False, True, True, 1),
+    (1000, 32, 8, 128, 128, [64], False, True, False, 0)])
+def test_rope(dtype, T, hq, hkv, hd, rd, sections, interleaved, adjacent, inverse, spare):
+    m = fa()
+    rng = np.random.default_rng(T * hd + rd)
+    half = rd // 2
+    freq = 1e4 ** (-np.arange(half) / half)
+    freq[0] = 1.0
+    # near positions, far ones and negative ones
+    pos = rng.integers(0, 5000, (len(sections), T))
+    pos[0, :: 3] = rng.integers(2 ** 30, 2 ** 31 - 1, len(pos[0, ::3]))
+    pos[-1, 1::3] = -rng.integers(0, 2 ** 31 - 1, len(pos[-1, 1::3]))
+    axis = ref.axes_of(half, sections, interleaved)
+    table = m.rope_table(freq, sections, interleaved=interleaved)
+    pairs = []
+    for heads in (hq, hkv):
+        if heads == 0:
+            pairs.append((None, None, None))
+            continue
+        x, exact = on_gpu(rng.standard_normal((T, heads, hd)) * 3, dtype, spare)
+        pairs.append((x, guarded((T, heads, hd), DT[dtype], fill=float("nan")), exact))
+    (q, qo, qx), (k, ko, kx) = pairs
+    m.rope(q, k, qo, ko, ints(pos), table, adjacent=adjacent, inverse=inverse)
+    for x, y, exact in pairs:
+        if x is None:
+            continue
+        check_guards(("out", y))
+        want = ref.rope(exact, pos, freq, axis, adjacent, inverse)
+        # In turns the angle is off by at most 2^-33 (32 bits kept, rounded), by |pos| (2^-64 + f 2^-53) through
+        # its table entry, and by 2^-26 where it becomes an fp32 argument; times 2 pi. The 64-bit reference's own
+        # |pos| f 2^-53 comes on top. sincospif is off by 2 steps (2^-23), two products and a sum by 2^-23 of |x| + |y|.
+        f = freq / (2 * math.pi)
+        angle = 2 * math.pi * (2.0 ** -33 + 2.0 ** -26 + np.abs(pos[axis, :]).T * (2.0 ** -64 + 2 * f * 2.0 ** -53))
+        i = np.arange(half)
+        lo, hi = (2 * i, 2 * i + 1) if adjacent else (i, i + half)
+        size = np.zeros_like(exact)
+        size[..., lo] = size[..., hi] = np.abs(exact[..., lo]) + np.abs(exact[..., hi])
+        slack = np.zeros_like(exact)
+        slack[..., lo] = slack[..., hi] = (angle + 2.0 ** -23 + 2.0 ** -23)[:, None, :]
+        tol = size * slack
+        tol += ref.HALF_STEP[dtype] * (np.abs(want) + tol) * (size > 0) + 2.0 ** -25 * (dtype == "f16")
+        assert np.all(np.abs(host(y) - want) <= tol)
+        assert np.array_equal(host(y)[..., rd:], exact[..., rd:])
+        # in place: the same bits
+        z = x.clone()
+        m.rope(*((z, None, z, None) if x is q else (None, z, None, z)), ints(pos), table, adjacent=adjacent,
+               inverse=inverse)
+        assert torch.equal(z, y)
+
+
+def test_rope_inverse_is_the_gradient():
+    """The inverse rotation of g is the gradient of <g, rope(x)>: against differences, and it undoes the rotation."""
+    m = fa()
+    rng = np.random.default_rng(9)
+    T, H, hd = 6, 3, 64
+    table = m.rope_table(1e4 ** (-np.arange(32) / 32), [12, 10, 10], interleaved=True)
+    pos = ints(rng.integers(0, 900, (3, T)))
+    x, g = (torch.from_numpy(rng.standard_normal((T, H, hd)).astype(np.float32)).cuda() for _ in range(2))
+    grad, y = torch.empty_like(g), torch.empty_like(x)
+    m.rope(g, None, grad, None, pos, table, inverse=True)
+
+    def loss(v):
+        m.rope(v, None, y, None, pos, table)
+        return float((y.double() * g.double()).sum())
+
+    for t, h, e in rng.integers(0, [T, H, hd], (12, 3)):
+        up, down = x.clone(), x.clone()
+        up[t, h, e] += 0.5
+        down[t, h, e] -= 0.5
+        # linear in x: the difference over a step of 1 has fp32 rounding alone, 2^-22 of the two rotated values
+        # (|x| + 1 and |g| at most 5 here) in each of the two losses
+        assert abs(loss(up) - loss(down) - float(grad[t, h, e])) <= 2 * 2 * 6 * 5 * 2.0 ** -22
+    m.rope(x, None, y, None, pos, table)
+    m.rope(y, None, y, None, pos, table, inverse=True)
+    assert float((y - x).abs().max()) <= 5 * 2 * 2 * 2.0 ** -21
+
+
+def test_rope_refuses():
+    m = fa()
+    table = m.rope_table([1.0] * 16)
+    x = torch.zeros(4, 2, 32, device="cuda")
+    pos = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for bad in (lambda: m.rope(None, None, None, None, pos, table),
+                lambda: m.rope(x, None, None, None, pos, table),
+                lambda: m.rope(x, x.half(), x, x.half(), pos, table),
+                lambda: m.rope(x, None, x[:, :1], None, pos, table),
+                lambda: m.rope(x, None, x, None, pos[:3], table),
+                lambda: m.rope(x, None, x, None, pos.long(), table),
+                lambda: m.rope(x.transpose(0, 1), None, x.transpose(0, 1), None, pos, table),
+                lambda: m.rope(x, None, x, None, pos, table[:, :3]),
+                lambda: m.rope(x.double(), None, x.double(), None, pos, table),
+                lambda: m.rope(x.cpu(), None, x.cpu(), None, pos, table)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(m.FAError):  # more rotated dims than a head has
+        m.rope(x, None, x, None, pos, m.rope_table([1.0] * 17))
+
+
+# ------------------------------------------------------------ append, gather
+
+def pool_of(m, n_pages, hkv, hd, page_rows):
+    """Pages of 0xff bytes: NaN scales and factors wherever nothing was written."""
+    return guarded(n_pages * m.page_bytes(hkv, hd, page_rows), torch.uint8, fill_byte=POISON_BYTE)
+
+
+def append(m, pages, k, v, slots, page_rows):
+    m.paged_append(k, v, ints(slots), pages, page_rows=page_rows)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd,hkv,page_rows,T,spare", [
+    (64, 1, 16, 1, 0), (64, 3, 32, 37, 128), (128, 2, 16, 50, 0), (256, 2, 64, 19, 64), (256, 1, 256, 70, 0)])
+def test_append_bytes(dtype, hd, hkv, page_rows, T, spare):
+    """Every byte of the pages: rows in scattered slots, the rest as it was."""
+    m = fa()
+    rng = np.random.default_rng(hd + T)
+    n_pages = 2 * T // page_rows + 3
+    pages = pool_of(m, n_pages, hkv, hd, page_rows)
+    slots = rng.permutation(n_pages * page_rows)[:T]
+    if T > 4:
+        slots[3] = -1  # a padded token
+    x = rng.standard_normal((2, T, hkv, hd))
+    x[0, 0, 0, :32] = 0                                   # an empty block
+    x[1, T // 2] = 0                                      # an empty row
+    x[0, T // 2] *= 300
+    x[1, T - 1, :, 32:] *= 1e-4                           # blocks far below the row's largest
+    k, kx = on_gpu(x[0], dtype, spare)
+    v, vx = on_gpu(x[1], dtype, 2 * spare)
+    append(m, pages, k, v, slots, page_rows)
+    torch.cuda.synchronize()
+    check_guards(("pages", pages))
+    want = np.full(pages.numel(), POISON_BYTE, np.uint8)
+    for t, slot in enumerate(slots):
+        for h in range(hkv):
+            if slot >= 0:
+                ref.put_row(want, page_rows, hkv, hd, int(slot), h, kx[t, h], 0)
+                ref.put_row(want, page_rows, hkv, hd, int(slot), h, vx[t, h], 1)
+    assert np.array_equal(pages.cpu().numpy(), want)
+    assert m.get_device_error() == m.OK
+
+
+def test_append_any_magnitude_and_values_without_one():
+    """Rows of 1e-30 and 1e30, of infinities and NaN: the factor keeps the first, the others stay in their row."""
+    m = fa()
+    hd, rng = 64, np.random.default_rng(1)
+    x = rng.standard_normal((6, 1, hd)).astype(np.float32)
+    x[0] *= np.float32(1e-30)
+    x[1] *= np.float32(1e30)
+    x[2] *= np.float32(1e-42)                             # below fp32's normal range
+    x[3, 0, 5] = np.inf
+    x[4, 0, 40] = np.nan
+    pages = pool_of(m, 1, 1, hd, 16)
+    t = torch.from_numpy(x).cuda()
+    append(m, pages, t, t, range(6), 16)
+    got = pages.cpu().numpy()
+    want = np.full_like(got, POISON_BYTE)
+    for r in (0, 1, 5):
+        ref.put_row(want, 16, 1, hd, r, 0, x[r, 0], 0)
+        ref.put_row(want, 16, 1, hd, r, 0, x[r, 0], 1)
+    for r in (0, 1, 5):
+        for v in (0, 1):
+            base = v * (9 * hd + 32)
+            places = [base + ref.code_place(hd, r, e, v)[0] for e in range(hd)]
+            places += [base + ref.scale_place(hd, r, b, v) + i for b in range(2) for i in (0, 1)]
+            places += [base + 9 * hd + 2 * r, base + 9 * hd + 2 * r + 1]
+            assert np.array_equal(got[places], want[places])
+
+
+def test_append_slots_out_of_range():
+    m = fa()
+    pages = pool_of(m, 2, 1, 64, 16)
+    x = torch.randn(5, 1, 64, device="cuda")
+    append(m, pages, x, x, [-1, 32, -2, 2 ** 31 - 1, -2 ** 31], 16)
+    torch.cuda.synchronize()
+    check_guards(("pages", pages))
+    assert bool((pages == POISON_BYTE).all())
+    assert m.get_device_error() == m.ERR_DEVICE
+    append(m, pages, x[:1], x[:1], [-1], 16)
+    assert m.get_device_error() == m.OK
+
+
+def filled(m, rng, lens, hkv, hd, page_rows, spare_pages=2, k_size=1.0, v_size=1.0):
+    """A pool with one request for each length, filled by appends in random pages.
+    Returns pages, table (numpy, -1 past the rows), and each request's K, V as the values they stand for."""
+    used = [-(-L // page_rows) for L in lens]
+    n_pages = sum(used) + spare_pages
+    order = rng.permutation(n_pages)
+    table = np.full((len(lens), max(1, max(used))), -1)
+    at, slots, ks, vs = 0, [], [], []
+    for r, L in enumerate(lens):
+        table[r, :used[r]] = order[at:at + used[r]]
+        at += used[r]
+        p = np.arange(L)
+        slots.append(table[r, p // page_rows] * page_rows + p % page_rows)
+        ks.append((rng.standard_normal((L, hkv, hd)) * k_size).astype(np.float32))
+        vs.append((rng.standard_normal((L, hkv, hd)) * v_size).astype(np.float32))
+    pages = pool_of(m, n_pages, hkv, hd, page_rows)
+    if at:
+        append(m, pages, torch.from_numpy(np.concatenate(ks)).cuda(), torch.from_numpy(np.concatenate(vs)).cuda(),
+               np.concatenate(slots), page_rows)
+    return pages, table, [ref.decode(*ref.encode(k)) for k in ks], [ref.decode(*ref.encode(v)) for v in vs]
+
+
+@pytest.mark.parametrize("hd,hkv,page_rows,lens", [
+    (64, 2, 16, [1, 0, 16, 17, 100]), (128, 3, 64, [63, 64, 65]), (256, 2, 256, [500]), (256, 1, 32, [31, 0, 33])])
+def test_gather_bits(hd, hkv, page_rows, lens):
+    """The planes hold the rows' values rounded to binary16, bit for bit; other rows stay as they were."""
+    m = fa()
+    pages, table, ks, vs = filled(m, np.random.default_rng(hd), lens, hkv, hd, page_rows)
+    max_seq = max(lens) + 5
+    pb = m.kv_plane_bytes(m.KV_F16, hkv, max_seq, hd)
+    kp, vp = (guarded(len(lens) * pb, torch.uint8, fill_byte=POISON_BYTE) for _ in range(2))
+    m.paged_gather(pages, ints(table), ints(lens), kp, vp, n_kv_heads=hkv, head_dim=hd, page_rows=page_rows,
+                   max_seq=max_seq)
+    assert m.get_device_error() == m.OK
+    check_guards(("k", kp), ("v", vp))
+    for planes, want in ((kp, ks), (vp, vs)):
+        got = planes.cpu().numpy().reshape(len(lens), pb)
+        for r, L in enumerate(lens):
+            rows = got[r][:hkv * max_seq * hd * 2].reshape(hkv, max_seq, hd * 2)
+            x = np.ascontiguousarray(want[r].astype(np.float16).transpose(1, 0, 2)).view(np.uint8)
+            assert np.array_equal(rows[:, :L], x.reshape(hkv, L, hd * 2))
+            assert np.all(rows[:, L:] == POISON_BYTE) and np.all(got[r][hkv * max_seq * hd * 2:] == POISON_BYTE)
+
+
+def test_gather_flags_lengths_and_pages():
+    m = fa()
+    hd, hkv, P, max_seq = 64, 1, 16, 40
+    pages, table, ks, _ = filled(m, np.random.default_rng(2), [32, 32, 32], hkv, hd, P)
+    pb = m.kv_plane_bytes(m.KV_F16, hkv, max_seq, hd)
+    kp, vp = (guarded(3 * pb, torch.uint8, fill_byte=POISON_BYTE) for _ in range(2))
+    table[2, 0] = 99
+    m.paged_gather(pages, ints(table), ints([-4, 33, 32]), kp, vp, n_kv_heads=hkv, head_dim=hd, page_rows=P,
+                   max_seq=max_seq)
+    assert m.get_device_error() == m.ERR_DEVICE
+    check_guards(("k", kp), ("v", vp))
+    got = kp.cpu().numpy().reshape(3, pb)[:, :max_seq * hd * 2].reshape(3, max_seq, hd * 2)
+    assert np.all(got[0] == POISON_BYTE) and np.all(got[1, 32:] == POISON_BYTE)
+    assert np.all(got[2, :16] == POISON_BYTE) and np.all(got[2, 32:] == POISON_BYTE)
+    for r, lo in ((1, 0), (2, 16)):
+        assert np.array_equal(got[r, lo:32], ks[r][lo:32, 0].astype(np.float16).view(np.uint8).reshape(32 - lo, -1))
+
+
+# ---------------------------------------------------------------- attention
+
+def attn_bounds(q, k, v, dtype, scale):
+    """How far out and lse may be off, from the kernel's arithmetic: per (query, head).
+
+    Scores. A block's products are summed in fp32 with the codes 0..15 (their offset 8 is subtracted by the sum's
+    start), so a term is at most 15 |q| + 8 |q| code steps; every sum in the tensor core may lose a step (2^-23) in
+    each of 4 additions, and the blocks' sums and the scale another 2^-23 each. With B = sum over dims of 23 |q| |s|
+    the score is off by (4 + 2) 2^-23 B; the pair of binary16 terms of an fp32 q adds 2^-22 B (one term is exact
+    for f16 and bf16 queries). The exponential adds 2^-22 + |score| 2^-23 <= 2^-22 + 2^-23 B.
+    Weights: rounded twice to binary16 (2 * 2^-11) for bf16, to a pair of terms (2^-20) otherwise. V codes enter
+    with their offset: sums of 16 w |s| at most, 2^-23 lost in each addition of 16 rows, and the sum of weights too.
+    """
+    g = q.shape[1] // k.shape[1]
+    step = lambda x: np.repeat(np.abs(x).reshape(*x.shape[:2], x.shape[2] // 32, 32).max(-1) / 7, 32, -1)  # noqa: E731
+    kb, vb = step(k), step(v)
+    B = 23 * scale * np.einsum("nhd,jhd->nhj", np.abs(q), np.repeat(kb, g, 1)).max(-1) if len(k) else np.zeros(q.shape[:2])
+    d = 2.0 ** -23 * (8 + 1) * B + 2.0 ** -21
+    eps = 2 * 2.0 ** -11 if dtype == "bf16" else 2.0 ** -20
+    n = -(-len(k) // 16) + 40
+    top = 16 * np.repeat(vb, g, 1).max(0) if len(k) else np.zeros(q.shape[1:])
+    return (2 * d + eps + 2 * n * 2.0 ** -23)[..., None] * top, d + n * 2.0 ** -23 + 2.0 ** -22
+
+
+def check_attn(lens, nqs, hq, hkv, hd, page_rows, dtype, *, sink=0, win=0, scale=0.0, spare=0, pad=0, k_size=1.0,
+               v_size=1.0, q_size=1.0, drop=True, seed=0, extra_pages=2):
+    """One call against the reference; returns the largest out and lse errors over their bounds."""
+    m = fa()
+    rng = np.random.default_rng(seed + 7 * hd + len(lens))
+    pages, table, ks, vs = filled(m, rng, lens, hkv, hd, page_rows, k_size=k_size, v_size=v_size,
+                                  spare_pages=extra_pages)
+    if win > 0 and drop:  # pages that no query attends are gone
+        for r, (L, n) in enumerate(zip(lens, nqs)):
+            for i in range(-(-L // page_rows)):
+                if i * page_rows >= sink and (i + 1) * page_rows - 1 < L - n - win + 1:
+                    table[r, i] = -1
+    T = sum(nqs)
+    q, qx = on_gpu(rng.standard_normal((T + pad, hq, hd)) * q_size, dtype, spare)
+    if spare:
+        out = torch.full((T + pad, hq * hd + spare), 7.0, dtype=DT[dtype], device="cuda")
+        o = out[:, :hq * hd].unflatten(1, (hq, hd))
+    else:
+        o = guarded((T + pad, hq, hd), DT[dtype], fill=7.0)
+    lse = guarded((hq, T + pad), torch.float32, fill=7.0)
+    ws = guarded(m.paged_attn_workspace_bytes(hd), torch.uint8, fill_byte=POISON_BYTE)
+    cu = np.concatenate([[0], np.cumsum(nqs)])
+    m.paged_attn(q, o, ints(cu), ints(lens), ints(table), pages, n_kv_heads=hkv, page_rows=page_rows, sink=sink,
+                 win=win, scale=scale, lse=lse, workspace=ws)
+    assert m.get_device_error() == m.OK
+    check_guards(("lse", lse), ("workspace", ws))
+    if spare:
+        assert bool((out[:, hq * hd:] == 7.0).all())
+    else:
+        check_guards(("out", o))
+    got, gl = host(o), host(lse)
+    assert np.all(got[T:] == 7.0) and np.all(gl[:, T:] == 7.0)  # padding is left as it was
+    sc = scale or 1 / math.sqrt(hd)
+    num = den = 0.0
+    for r, (L, n) in enumerate(zip(lens, nqs)):
+        if n == 0:
+            continue
+        t = slice(cu[r], cu[r + 1])
+        want, wl = ref.attend(qx[t], L, ks[r], vs[r], L - n, sink, win, sc)
+        tol, ltol = attn_bounds(qx[t], ks[r], vs[r], dtype, sc)
+        tol = tol + ref.HALF_STEP[dtype] * (np.abs(want) + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
+        assert np.all(np.isfinite(got[t]))
+        assert np.all(np.abs(got[t] - want) <= tol), f"request {r}: {np.max(np.abs(got[t] - want) / tol)}"
+        dead = wl == -math.inf
+        assert np.array_equal(gl[:, t] == -math.inf, dead) and np.all(got[t].transpose(1, 0, 2)[dead] == 0)
+        ltol = ltol.T + np.abs(np.where(dead, 0, wl)) * 2.0 ** -22
+        assert np.all(np.abs(gl[:, t][~dead] - wl[~dead]) <= ltol[~dead])
+        num, den = num + ((got[t] - want) ** 2).sum(), den + (want ** 2).sum()
+    if den:
+        # Roundings are independent, so the 2-norm stays below half a step of the type; fp32's sums of a few
+        # hundred terms stay below 2^-17. Binary16 below its normal range has steps of 2^-24 however small the
+        # value is: half a step, 2^-25, for each of the T * hq * hd outputs.
+        floor = 2.0 ** -25 * math.sqrt(T * hq * hd) if dtype == "f16" else 0.0
+        assert math.sqrt(num) <= {"f32": 2.0 ** -17, "f16": 2.0 ** -10, "bf16": 2.0 ** -8}[dtype] * math.sqrt(den) + floor
+    return q, o, lse
+
+
+SHAPES = [
+    # lens, queries, hq, hkv, hd, page_rows, sink, win
+    ([1], [1], 1, 1, 64, 16, 0, 0),
+    ([600], [1], 8, 2, 64, 16, 0, 0),
+    ([15, 16, 17, 0, 33], [1, 1, 1, 1, 1], 16, 2, 256, 16, 0, 0),
+    ([300, 5, 1000, 64], [1, 0, 1, 1], 16, 2, 256, 64, 0, 0),
+    ([200, 3, 77], [5, 3, 2], 32, 8, 128, 32, 0, 0),
+    ([2, 130], [4, 7], 16, 1, 128, 128, 0, 0),            # more queries than rows; groups of 16
+    ([90, 500], [9, 1], 4, 4, 128, 256, 0, 0),            # heads that share nothing
+    ([40, 700], [3, 2], 4, 2, 64, 16, 0, 0),
+    ([500, 90, 40], [1, 2, 3], 8, 2, 256, 32, 4, 100),
+    ([1000, 30], [2, 1], 8, 1, 64, 16, 37, 61),
+    ([400], [3], 2, 2, 128, 16, 0, 1),
+    ([700, 20, 0, 260], [1, 1, 1, 1], 4, 1, 128, 64, 500, 3),
+]
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("case", SHAPES, ids=lambda c: f"h{c[2]}x{c[3]}d{c[4]}p{c[5]}w{c[7]}n{len(c[0])}")
+def test_attn(case, dtype):
+    lens, nqs, hq, hkv, hd, page_rows, sink, win = case
+    check_attn(lens, nqs, hq, hkv, hd, page_rows, dtype, sink=sink, win=win)
+
+
+@pytest.mark.parametrize("hd", (64, 128, 256))
+def test_attn_strides_padding_and_scale(hd):
+    check_attn([100, 31], [2, 1], 8, 2, hd, 16, "bf16", spare=3 * hd, pad=3, scale=0.3)
+    check_attn([100, 31], [2, 1], 8, 2, hd, 16, "f32", spare=hd, pad=1, scale=1.0)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("k_size,v_size,q_size", [(1e-3, 1e-5, 1.0), (1.0, 3000.0, 1e-4), (30.0, 1.0, 2.0)])
+def test_attn_magnitudes(dtype, k_size, v_size, q_size):
+    """Small and large rows keep their precision; steep scores too."""
+    check_attn([300, 1000], [1, 2], 16, 2, 128, 16, dtype, k_size=k_size, v_size=v_size, q_size=q_size, seed=3)
+
+
+def test_attn_many_requests_of_every_length():
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 200, 300).tolist()
+    check_attn(lens, rng.integers(0, 3, 300).tolist(), 8, 2, 64, 16, "f32")
+    lens = np.round(np.exp(rng.uniform(0, 8.5, 60))).astype(int).tolist()
+    check_attn(lens, [1] * 60, 16, 2, 256, 32, "bf16")
+
+
+def test_attn_more_requests_than_threads():
+    rng = np.random.default_rng(12)
+    n = 3000
+    lens = np.where(rng.random(n) < 0.9, rng.integers(0, 20, n), 90).tolist()
+    check_attn(lens, np.where(rng.random(n) < 0.2, 0, 1).tolist(), 2, 1, 64, 16, "f16")
+
+
+def test_attn_long_request():
+    """A cache long enough that its rows are shared by every SM; a peak of scores at its far end."""
+    check_attn([70001], [1], 8, 1, 128, 64, "f32", seed=4)
+    check_attn([20000, 1], [2, 1], 16, 1, 256, 16, "bf16", seed=5)
+
+
+def test_attn_pool_past_32_bits_of_bytes():
+    """Pages beyond 4 GiB of the pool (and beyond 2^32 bytes of offset)."""
+    m = fa()
+    hkv, hd, P = 2, 256, 256
+    pb = m.page_bytes(hkv, hd, P)
+    n_pages = (5 << 30) // pb
+    pages = torch.empty(n_pages * pb, dtype=torch.uint8, device="cuda")
+    rng = np.random.default_rng(4)
+    L = 300
+    table = np.array([[n_pages - 1, n_pages - 7]])
+    p = np.arange(L)
+    slots = table[0, p // P] * P + p % P
+    k, v = rng.standard_normal((2, L, hkv, hd)).astype(np.float32)
+    append(m, pages, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), slots, P)
+    q, qx = on_gpu(rng.standard_normal((1, 16, hd)), "f32")
+    out = torch.empty_like(q)
+    m.paged_attn(q, out, ints([0, 1]), ints([L]), ints(table), pages, n_kv_heads=hkv, page_rows=P,
+                 workspace=torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda"))
+    want, _ = ref.attend(qx, L, ref.decode(*ref.encode(k)), ref.decode(*ref.encode(v)), L - 1, 0, 0, 1 / 16)
+    assert np.linalg.norm(host(out) - want) <= 2.0 ** -17 * np.linalg.norm(want)
+    pbf = m.kv_plane_bytes(m.KV_F16, hkv, L, hd)
+    kp, vp = (torch.zeros(pbf, dtype=torch.uint8, device="cuda") for _ in range(2))
+    m.paged_gather(pages, ints(table), ints([L]), kp, vp, n_kv_heads=hkv, head_dim=hd, page_rows=P, max_seq=L)
+    got = kp[:hkv * L * hd * 2].view(torch.float16).view(hkv, L, hd).cpu().numpy()
+    assert np.array_equal(got, ref.decode(*ref.encode(k)).astype(np.float16).transpose(1, 0, 2))
+    assert m.get_device_error() == m.OK
+
+
+def call_attn(m, q, table, pages, lens, cu, hkv, page_rows, out=None, ws=None, **kw):
+    out = torch.empty_like(q) if out is None else out
+    ws = torch.empty(m.paged_attn_workspace_bytes(q.shape[2]), dtype=torch.uint8, device="cuda") if ws is None else ws
+    m.paged_attn(q, out, cu, lens, table, pages, n_kv_heads=hkv, page_rows=page_rows, workspace=ws, **kw)
+    return out
+
+
+def test_attn_bad_device_data_is_flagged_and_skipped():
+    m = fa()
+    rng = np.random.default_rng(2)
+    hq, hkv, hd, P = 4, 2, 64, 16
+    pages, table, ks, vs = filled(m, rng, [40, 40, 40], hkv, hd, P)
+    q, qx = on_gpu(rng.standard_normal((3, hq, hd)), "f32")
+
+    def run(lens=(40, 40, 40), cu=(0, 1, 2, 3), table=table):
+        out = guarded((3, hq, hd), torch.float32, fill=7.0)
+        call_attn(m, q, ints(table), pages, ints(lens), ints(cu), hkv, P, out=out)
+        assert m.get_device_error() == m.ERR_DEVICE
+        check_guards(("out", out))
+        return host(out)
+
+    good = [ref.attend(qx[i:i + 1], 40, ks[i], vs[i], 39, 0, 0, 1 / 8)[0][0] for i in range(3)]
+    ok = lambda x, i: np.linalg.norm(x - good[i]) <= 2.0 ** -17 * np.linalg.norm(good[i])  # noqa: E731
+    for lens in ((40, -1, 40), (40, 49, 40), (40, 2 ** 31 - 1, 40)):
+        got = run(lens=lens)
+        assert np.all(got[1] == 7.0) and ok(got[0], 0) and ok(got[2], 2)
+    for cu in ((0, 1, 2, 4), (0, 1, 2, 2 ** 31 - 1)):
+        got = run(cu=cu)
+        assert np.all(got[2] == 7.0) and ok(got[0], 0) and ok(got[1], 1)
+    got = run(cu=(0, 1, 0, 3))                            # a request that ends before it begins, and one that
+    assert np.all(np.isfinite(got))                       # then holds another's token: that one's row is either's
+    got = run(cu=(-1, 1, 2, 3))
+    assert ok(got[1], 1) and ok(got[2], 2)
+    bad = table.copy()
+    bad[1, 1] = 10 ** 6                                   # rows 16..31 of request 1 do not count
+    got = run(table=bad)
+    keep = np.r_[0:16, 32:40]
+    want = ref.attend(qx[1:2], 24, ks[1][keep], vs[1][keep], 23, 0, 0, 1 / 8)[0][0]
+    assert ok(got[0], 0) and ok(got[2], 2)
+    assert np.linalg.norm(got[1] - want) <= 2.0 ** -17 * np.linalg.norm(want)
+
+
+def test_attn_same_bits_again_and_with_other_requests_beside():
+    """Two calls give the same bits; nothing depends on what the workspace holds."""
+    m = fa()
+    rng = np.random.default_rng(31)
+    lens = [3000, 17, 900]
+    pages, table, _, _ = filled(m, rng, lens, 2, 128, 32)
+    q, _ = on_gpu(rng.standard_normal((3, 16, 128)), "bf16")
+    ws = torch.full((m.paged_attn_workspace_bytes(128),), 0xff, dtype=torch.uint8, device="cuda")
+    args = (m, q, ints(table), pages, ints(lens), ints([0, 1, 2, 3]), 2, 32)
+    first = call_attn(*args, ws=ws)
+    for _ in range(3):
+        assert torch.equal(call_attn(*args, ws=ws), first)
+
+
+def test_attn_graphs_and_streams():
+    """A captured call replays with new queries, lengths and tables; two streams run two calls at once."""
+    m = fa()
+    rng = np.random.default_rng(13)
+    hq, hkv, hd, P = 16, 2, 256, 16
+    lens = [400, 90]
+    pages, table, ks, vs = filled(m, rng, lens, hkv, hd, P)
+    q, qx = on_gpu(rng.standard_normal((2, hq, hd)), "f32")
+    t, n, cu = ints(table), ints(lens), ints([0, 1, 2])
+    out, ws = torch.zeros_like(q), torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda")
+    call_attn(m, q, t, pages, n, cu, hkv, P, out=out, ws=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call_attn(m, q, t, pages, n, cu, hkv, P, out=out, ws=ws)
+    for cut in (0, 37):
+        qx = ref.round_type(rng.standard_normal(qx.shape), "f32")
+        q.copy_(torch.from_numpy(qx))
+        n.copy_(torch.tensor([lens[0] - cut, lens[1] - cut], dtype=torch.int32))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for r in (0, 1):
+            want, _ = ref.attend(qx[r:r + 1], lens[r] - cut, ks[r], vs[r], lens[r] - cut - 1, 0, 0, 1 / 16)
+            assert np.linalg.norm(host(out)[r] - want[0]) <= 2.0 ** -17 * np.linalg.norm(want)
+    n.copy_(torch.tensor(lens, dtype=torch.int32))
+    want = call_attn(m, q, t, pages, n, cu, hkv, P, ws=ws).clone()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.zeros_like(q) for _ in streams]
+    spaces = [torch.empty_like(ws) for _ in streams]
+    for _ in range(20):
+        for s, o, w in zip(streams, outs, spaces):
+            call_attn(m, q, t, pages, n, cu, hkv, P, out=o, ws=w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_paged_refuses_shapes_and_types():
+    m = fa()
+    P, hkv, hd = 16, 2, 64
+    pages = m.alloc_pages(4, hkv, hd, P)
+    x = torch.zeros(3, hkv, hd, device="cuda")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    slots, table, lens, cu = i32(3), i32(2, 2), i32(2), i32(3)
+    planes = torch.zeros(2 * m.kv_plane_bytes(m.KV_F16, hkv, 32, hd), dtype=torch.uint8, device="cuda")
+    ws = torch.zeros(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda")
+    q = torch.zeros(3, 4, hd, device="cuda")
+    bad_calls = [
+        lambda: m.paged_append(x, x[:2], slots, pages, page_rows=P),
+        lambda: m.paged_append(x, x.half(), slots, pages, page_rows=P),
+        lambda: m.paged_append(x, x, slots[:2], pages, page_rows=P),
+        lambda: m.paged_append(x, x, slots, pages[:-1], page_rows=P),
+        lambda: m.paged_append(x, x, slots, pages, page_rows=17),
+        lambda: m.paged_append(x.double(), x.double(), slots, pages, page_rows=P),
+        lambda: m.paged_append(x.transpose(1, 2), x.transpose(1, 2), slots, pages, page_rows=P),
+        lambda: m.paged_append(x[:1].expand(3, hkv, hd), x, slots, pages, page_rows=P),
+        lambda: m.paged_append(x.cpu(), x, slots, pages, page_rows=P),
+        lambda: m.paged_gather(pages, table, i32(3), planes, planes, n_kv_heads=hkv, head_dim=hd, page_rows=P,
+                               max_seq=32),
+        lambda: m.paged_gather(pages, table, lens, planes[:-256], planes, n_kv_heads=hkv, head_dim=hd, page_rows=P,
+                               max_seq=32),
+        lambda: m.paged_gather(pages, table.long(), lens, planes, planes, n_kv_heads=hkv, head_dim=hd, page_rows=P,
+                               max_seq=32),
+        lambda: m.paged_attn(q, q[:2], cu, lens, table, pages, n_kv_heads=hkv, page_rows=P, workspace=ws),
+        lambda: m.paged_attn(q, q.half(), cu, lens, table, pages, n_kv_heads=hkv, page_rows=P, workspace=ws),
+        lambda: m.paged_attn(q, q, cu[:2], lens, table, pages, n_kv_heads=hkv, page_rows=P, workspace=ws),
+        lambda: m.paged_attn(q, q, cu, lens, table[0], pages, n_kv_heads=hkv, page_rows=P, workspace=ws),
+        lambda: m.paged_attn(q, q, cu, lens, table, pages, n_kv_heads=hkv, page_rows=P, workspace=ws,
+                             lse=torch.zeros(3, 4, device="cuda")),
+        lambda: m.paged_attn(q, q, cu, lens, table, pages.cpu(), n_kv_heads=hkv, page_rows=P, workspace=ws),
+    ]
+    for i, bad in enumerate(bad_calls):
+        with pytest.raises(ValueError):
+            bad()
+            pytest.fail(f"call {i} was taken")
+    for kw in (dict(n_kv_heads=hkv, workspace=ws[:64]), dict(n_kv_heads=hkv, workspace=ws, sink=-1),
+               dict(n_kv_heads=hkv, workspace=ws, scale=-0.5)):
+        with pytest.raises(m.FAError):
+            m.paged_attn(q, q, cu, lens, table, pages, page_rows=P, **kw)
+    with pytest.raises(m.FAError):  # rows that 16-byte loads cannot read
+        y = torch.zeros(3, hkv * hd + 1, device="cuda")[:, :hkv * hd].unflatten(1, (hkv, hd))
+        m.paged_append(y, y, slots, pages, page_rows=P)
+
+
+# ------------------------------------------------- a run of them together
+
+def test_serving_steps(oracle_mod):
+    """Five steps of a small server: prompts, a chunk, decodes, a finished request whose pages go to the next.
+    Every step plans, rotates, appends and attends; the prompts also go through fp16 planes and fa_prefill_chunk."""
+    m = fa()
+    rng = np.random.default_rng(77)
+    R, P, max_pages, n_pages, hq, hkv, hd = 4, 16, 12, 20, 8, 2, 64
+    freq = 1e4 ** (-np.arange(16) / 16)
+    axis = ref.axes_of(16, [16], False)
+    table_rope = m.rope_table(freq)
+    pages = pool_of(m, n_pages, hkv, hd, P)
+    ring, table = ints(rng.permutation(n_pages)), ints(np.full((R, max_pages), -1))
+    lens, state = [ints([0] * R), ints([0] * R)], [ints([5, n_pages, 0]), ints([0, 0, 0])]
+    cache = [(np.zeros((0, hkv, hd)), np.zeros((0, hkv, hd))) for _ in range(R)]
+    ws = torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda")
+    max_tokens = 170
+    steps = [[70, 33, 0, 5], [1, 1, 90, 1], [1, -1, 1, 1], [1, 120, 1, 2], [1, 1, -1, 1]]
+    for i, fresh in enumerate(steps):
+        now, after = i % 2, 1 - i % 2
+        cu, slots, pos = ints([0] * (R + 1)), ints([0] * max_tokens), ints([0] * max_tokens)
+        m.page_plan(lens[now], ints(fresh), ring, state[now][:2], table, state[after], lens[after], cu, slots, pos,
+                    page_rows=P)
+        T = sum(max(f, 0) for f in fresh)
+        # the batch is padded to max_tokens, as a captured step's is
+        qkv = torch.from_numpy(rng.standard_normal((max_tokens, hq + 2 * hkv, hd)).astype(np.float32)).cuda()
+        q, k, v = qkv.split([hq, hkv, hkv], 1)
+        qx, kx, vx = (host(x)[:T] for x in (q, k, v))
+        positions = pos.cpu().numpy()[None, :T]
+        m.rope(q, k, q, k, pos, table_rope)
+        m.paged_append(k, v, slots, pages, page_rows=P)
+        out, lse = torch.full((max_tokens, hq, hd), 7.0, device="cuda"), torch.empty(hq, max_tokens, device="cuda")
+        m.paged_attn(q, out, cu, lens[after], table, pages, n_kv_heads=hkv, page_rows=P, lse=lse, workspace=ws)
+        assert m.get_device_error() == m.OK
+        assert bool((out[T:] == 7.0).all())
+        qx = ref.rope(qx, positions, freq, axis, False, False)
+        kr = host(k)[:T]  # as rotated in fp32: the codes follow it bit for bit
+        assert np.allclose(kr, ref.rope(kx, positions, freq, axis, False, False), atol=2e-6, rtol=0)
+        t = 0
+        for r, f in enumerate(fresh):
+            if f < 0:
+                cache[r] = (np.zeros((0, hkv, hd)), np.zeros((0, hkv, hd)))
+                continue
+            new = [ref.decode(*ref.encode(x[t:t + f].astype(np.float32))) for x in (kr, vx)]
+            cache[r] = tuple(np.concatenate([a, b]) for a, b in zip(cache[r], new))
+            L = len(cache[r][0])
+            assert int(lens[after][r]) == L
+            want, _ = ref.attend(qx[t:t + f], L, *cache[r], L - f, 0, 0, 1 / 8)
+            got = host(out)[t:t + f]
+            if f:
+                # 2^-17 of the kernel, and rope's 2e-6 on q: scores of |q| |k| / 8 <= 2e-6 * 64 * 3 / 8
+                assert np.linalg.norm(got - want) <= (2.0 ** -17 + 1e-4) * np.linalg.norm(want)
+            if f > 1:  # the chunk by way of planes
+                max_seq = L + 2
+                pb = m.kv_plane_bytes(m.KV_F16, hkv, max_seq, hd)
+                kp, vp = (torch.zeros(pb, dtype=torch.uint8, device="cuda") for _ in range(2))
+                m.paged_gather(pages, table[r:r + 1], lens[after][r:r + 1], kp, vp, n_kv_heads=hkv, head_dim=hd,
+                               page_rows=P, max_seq=max_seq)
+                o = torch.empty(f, hq, hd, device="cuda")
+                m.prefill_chunk(q[t:t + f].contiguous(), kp, vp, o, L - f, f, hq, hkv, hd, 0, 0, m.KV_F16,
+                                max_seq=max_seq, workspace=torch.empty(
+                                    m.prefill_chunk_workspace_bytes(L - f, f, hq, hkv, hd), dtype=torch.uint8,
+                                    device="cuda"))
+                assert np.abs(host(o) - want).max() <= 5e-3  # the prefill's own tolerance (fp16 operands)
+                assert m.get_device_error() == m.OK
+            t += f
