@@ -276,7 +276,9 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
         !(scale >= 0.0f) || !std::isfinite(scale))
         return FA_ERR_INVALID;
     const int group = n_q_heads / n_kv_heads;
-    if (group > 16 || (group & (group - 1)) || n_reqs > 65536) return FA_ERR_UNSUPPORTED;
+    if (group > 16 || (group & (group - 1)) || n_reqs > 65536 || n_tokens > 1 << 26 ||
+        static_cast<long long>(n_tokens) * n_q_heads > 1 << 30)
+        return FA_ERR_UNSUPPORTED;
     if (n_reqs == 0 || n_tokens == 0) return FA_OK;
     if (!q || !out || !cu_q || !seq_lens || !block_table || !pages || !workspace ||
         !aligned4(lse) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(block_table) ||
@@ -299,7 +301,7 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
     a.n_tokens = n_tokens;
     a.n_q_heads = n_q_heads;
     a.sink = sink;
-    a.win = win;
+    a.win = win < 1 << 30 ? win : 1 << 30;  // the most rows a request can have
     a.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     a.workspace = static_cast<uint8_t *>(workspace);
     a.err = fa::device_error_word();

@@ -537,7 +537,8 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  * fp32. With FA_T_F32 every product is exact to about 2^-21; with FA_T_F16 and
  * FA_T_BF16 the softmax weights are rounded to binary16 before the product with
  * V, once for FA_T_BF16 and as a pair of terms (about 2^-21) for FA_T_F16.
- * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_reqs <= 65536.
+ * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_reqs <= 65536,
+ * n_tokens <= 2^26, n_tokens * n_q_heads <= 2^30.
  * FA_ERR_DEVICE is flagged for a request whose cu_q or seq_lens are out of range
  * (its rows are not written), and for a table entry outside [0, n_pages) (its
  * rows count as not attended). */
