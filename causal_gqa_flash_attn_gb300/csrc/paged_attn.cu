@@ -54,6 +54,7 @@ constexpr float kLift = 6.0f;      // log2 of the largest weight right after a m
 constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 constexpr int kMinGroups = 4;      // groups per warp below which fewer warps work
 constexpr int kRows = 8;           // query rows of a row group
+constexpr int kMostWarps = 16;     // computing warps of a block that the workspace is made for
 
 template <typename T, int HD>
 struct Cfg {
@@ -61,22 +62,34 @@ struct Cfg {
     static constexpr bool PSPLIT = !std::is_same<T, __nv_bfloat16>::value;
     static constexpr int NB = HD / 32;
     static constexpr int GB = group_bytes(HD);
-    static constexpr int WARPS = PSPLIT ? 8 : 12;
-    static constexpr int STAGES = HD == 256 ? (PSPLIT ? 5 : 4) : HD == 128 ? 7 : 12;
+    // Warps that compute, and one more that copies; registers for one block of
+    // them per SM, ring stages for what is left of shared memory.
+#ifdef PA_WARPS
+    static constexpr bool PP = sizeof(T) == PA_SIZE && HD == PA_HD;
+    static constexpr int WARPS = PP ? PA_WARPS : 7;
+    static constexpr int STAGES = PP ? PA_STAGES : 4;
+#else
+    static constexpr int WARPS = HD == 256 ? (PSPLIT ? 7 : 11) : PSPLIT ? 11 : 15;
+    static constexpr int STAGES = HD == 256 ? (PSPLIT ? 4 : 3) : HD == 128 ? 4 : 8;
+#endif
     static constexpr int RING = STAGES * GB;
-    static constexpr int QLO = QSPLIT ? NB * 32 * 16 : 0;  // low terms of q, per warp
-    static constexpr int OFF_BAR = WARPS * RING;
-    static constexpr int OFF_BIAS = OFF_BAR + WARPS * STAGES * 8;
-    static constexpr int OFF_QLO = OFF_BIAS + WARPS * NB * kRows * 4;
-    static constexpr int SMEM = (OFF_QLO + WARPS * QLO + 127) / 128 * 128;
-    static constexpr int THREADS = WARPS * 32;
+    static constexpr int QF = NB * 32 * 16;           // q as B fragments
+    static constexpr int QB = QF * (QSPLIT ? 2 : 1);  // and their low terms
+    static constexpr int BIAS = NB * 4 * 16;          // the accumulators' start, as lanes hold it
+    static constexpr int OFF_Q = WARPS * RING;
+    static constexpr int OFF_BIAS = OFF_Q + WARPS * QB;
+    static constexpr int OFF_BAR = OFF_BIAS + WARPS * BIAS;
+    static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 16;  // full and empty barriers
+    static constexpr int SMEM = OFF_DEAD + WARPS * STAGES * 4;
+    static constexpr int THREADS = (WARPS + 1) * 32;
     // a partial: m and l of 8 rows, then O as the lanes hold it
     static constexpr int PARTIAL = 2 * kRows + kRows * HD;  // floats
-    static_assert(OFF_BAR % 8 == 0 && OFF_QLO % 16 == 0, "alignment");
+    static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
+    static_assert(2 * WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
+    static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
     static_assert(RING >= kRows * HD * 4, "a warp's O fits its ring");
     static_assert(SMEM <= 225 * 1024, "shared memory");
 };
-constexpr int kMostWarps = 12;
 
 // How a request's rows are read, from its lengths.
 struct Req {
@@ -167,6 +180,14 @@ __device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16 *p, float4 v
                                                *reinterpret_cast<uint32_t *>(&hi));
 }
 
+template <int N>
+__device__ __forceinline__ void lds_words(uint32_t *w, const uint8_t *p) {
+    if (N == 2)
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[N - 1]) : "r"(smem_u32(p)));
+    else
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(smem_u32(p)));
+}
+
 // 8 consecutive values as fp32.
 __device__ __forceinline__ void load8(const float *p, float *x) {
     const float4 a = *reinterpret_cast<const float4 *>(p);
@@ -212,10 +233,14 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
 __device__ __forceinline__ float2 half2_f(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
+// D (16x8 fp32) += A (16x16 fp16) * B (16x8 fp16); not volatile, so that the
+// compiler may interleave the chains of different blocks.
 __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                     uint32_t b0, uint32_t b1) {
-    const uint32_t a[4] = {a0, a1, a2, a3}, b[2] = {b0, b1};
-    mma_16816(d, a, b);
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // 2^-24 and 2^-20 come out of O's rows g and g + 8.
@@ -268,6 +293,20 @@ __device__ __forceinline__ float4 scaled(float4 v, float s) {
     return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
 }
 
+// A warp's place in its run and what the unit it is in needs once per piece or
+// in the groups that not every row sees whole. In shared memory: the loop over
+// the groups has no registers to spare.
+struct Piece {
+    int r, unit, gi, todo;      // request, unit (kv head and row group), group, groups left in the run
+    int n, end;                 // groups of the unit, and where the piece ends
+    int pos[kRows];             // the columns' positions
+    int p_min, p_max;           // of all of them
+    int ns, skip;               // group i of the unit is i, or i + skip from ns on
+    int fin_r, fin_unit;        // the piece that ends the run, if other warps have more of its unit (else -1)
+    long long fin_first, fin_last;  // that unit's groups in the cut
+    float m[kRows], l[kRows];   // and the piece's references and sums
+};
+
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
 
 template <typename T, int HD>
@@ -275,29 +314,27 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     using C = Cfg<T, HD>;
     constexpr int NB = C::NB, S = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long scan_part[C::WARPS];
+    __shared__ long long scan_part[C::WARPS + 1];
     __shared__ int start_r[C::WARPS];
     __shared__ long long start_x[C::WARPS];
-    __shared__ long long fin_first[C::WARPS], fin_last[C::WARPS];  // its last unit's groups
-    __shared__ int fin_r[C::WARPS], fin_unit[C::WARPS];            // fin_unit -1: none
-    __shared__ float fin_m[C::WARPS][kRows], fin_l[C::WARPS][kRows];
+    __shared__ Piece pieces[C::WARPS];
     __shared__ int abort_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
-    const int n_kv = a.pages.n_kv;
+    const int n_kv = a.pages.n_kv, page_groups = n_kv * a.pages.groups;
     const int log_group = 31 - __clz(a.n_q_heads / n_kv);
     uint8_t *ring = smem + warp * C::RING;
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR) + warp * S;
-    float *bias = reinterpret_cast<float *>(smem + C::OFF_BIAS) + warp * NB * kRows;
-    uint8_t *qlo = smem + C::OFF_QLO + warp * C::QLO;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [warp][stage]
+    uint64_t *empty = full + C::WARPS * S;
+    volatile int *dead = reinterpret_cast<int *>(smem + C::OFF_DEAD);  // stages without rows
+    uint8_t *qs = smem + C::OFF_Q + warp * C::QB;
+    uint8_t *bias = smem + C::OFF_BIAS + warp * C::BIAS;
     const Ws ws = carve(a.workspace, gridDim.x);
 
-    if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(bars + i, 1);
-        mbar_fence_init();
-    }
+    if (tid < 2 * C::WARPS * S) mbar_init(full + tid, 1);
     if (tid == 0) abort_flag = 0;
+    mbar_fence_init();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the cut: sums over all requests, each thread a run of them
@@ -320,7 +357,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
     long long base = 0, N = 0;
-    for (int i = 0; i < C::WARPS; ++i) {
+    for (int i = 0; i <= C::WARPS; ++i) {
         if (i == warp) base = N;
         N += scan_part[i];
     }
@@ -344,105 +381,131 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
     __syncthreads();
 
-    const int wid = blockIdx.x * cut.A + warp;
-    const bool works = warp < cut.A && wid < cut.W && N > 0;
+    if (warp == C::WARPS) {
+        // ---- the copying warp: lane w walks the run of warp w, up to S groups ahead of it
+        const int wid = blockIdx.x * cut.A + lane;
+        int left = 0;  // groups to copy
+        int r = 0, unit = 0, units = 1, rgs = 1, ci = 0, cn = 1, ns = 0, skip = 0, head = 0;
+        const int32_t *table = a.pages.table;
+        auto enter = [&](const Req &q) {
+            cn = max(q.ng, 1);
+            ns = q.ng > 0 ? q.ns : -1;  // -1: nothing to read
+            skip = q.skip;
+            rgs = q.rgs;
+            units = q.rgs * n_kv;
+            table = a.pages.table + static_cast<size_t>(r) * a.pages.max_pages;
+        };
+        if (lane < cut.A && wid < cut.W && N > 0) {
+            const long long x0 = cut.start(wid);
+            left = static_cast<int>(cut.start(wid + 1) - x0);
+            r = start_r[lane];
+            enter(load_req(a, r, log_group));
+            const long long off = x0 - start_x[lane];
+            unit = static_cast<int>(off / cn);
+            ci = static_cast<int>(off - static_cast<long long>(unit) * cn);
+            head = unit / rgs * a.pages.groups;
+        }
+        int stage = 0, lap = 0, page = 0, group = 0;
+        auto look = [&]() {  // the table entry of the next group, one step before its copy
+            group = ci < ns ? ci : ci + skip;
+            page = ns >= 0 ? __ldg(table + (group >> a.pages.group_shift)) : -2;
+            group = (group & (a.pages.groups - 1)) + head;
+        };
+        if (left > 0) look();
+        long long t0 = clock64();
+        while (__any_sync(~0u, left > 0)) {
+            bool went = false;
+            uint64_t *bar = full + lane * S + stage;
+            if (left > 0 && (lap == 0 || mbar_try_wait(empty + lane * S + stage, (lap - 1) & 1))) {
+                went = true;
+                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages.n_pages)) {
+                    dead[lane * S + stage] = 0;
+                    mbar_arrive_expect_tx(bar, C::GB);
+                    bulk_copy_g2s(smem + lane * C::RING + stage * C::GB,
+                                  a.pages.base + (static_cast<size_t>(page) * page_groups + group) * C::GB,
+                                  C::GB, bar);
+                } else {
+                    dead[lane * S + stage] = 1;
+                    mbar_arrive(bar);
+                    if (page != -2) flag_error(a.err, FA_ERRBIT_DEVICE);
+                }
+                if (++stage == S) stage = 0, ++lap;
+                if (--left > 0) {
+                    if (++ci == cn) {
+                        ci = 0;
+                        if (++unit == units) {
+                            unit = 0;
+                            Req q;
+                            do q = load_req(a, ++r, log_group); while (q.rgs == 0);
+                            enter(q);
+                        }
+                        head = unit / rgs * a.pages.groups;
+                    }
+                    look();
+                }
+            }
+            if (__any_sync(~0u, went)) {
+                t0 = clock64();
+            } else {
+                __nanosleep(40);
+                const bool late = clock64() - t0 > 2 * kSpinCycles;
+                if (late && lane == 0) {
+                    abort_flag = 1;
+                    flag_error(a.err, FA_ERRBIT_TIMEOUT);
+                }
+                if (__any_sync(~0u, late || *static_cast<volatile int *>(&abort_flag))) break;
+            }
+        }
+    }
+
+    volatile Piece *pc = pieces + min(warp, C::WARPS - 1);
     State<NB> st;
     st.clear();
-    int last_unit = -1, last_r = 0;  // the piece that ends the run, when other warps have more of its unit
-    long long last_first = 0, last_last = 0;
-    const int slot = blockIdx.x * C::WARPS + warp;
-    if (lane == 0) ws.tasks[slot].valid = 0;
-
-    if (works) {
-        const long long x0 = cut.start(wid), x1 = cut.start(wid + 1);
-        int todo = static_cast<int>(x1 - x0);  // groups to compute
-        // ---- copies: their own walk over the run, S groups ahead
-        int cr = start_r[warp];
-        Req cq = load_req(a, cr, log_group);
-        int cn = max(cq.ng, 1);
-        long long off = x0 - start_x[warp];
-        int cu = static_cast<int>(off / cn), ci = static_cast<int>(off - static_cast<long long>(cu) * cn);
-        int ch = cu / cq.rgs;
-        int left = todo;               // groups not yet looked up
-        uint32_t dead = 0, parity = 0; // stages without a copy; barrier phases
-        int page = 0, group = 0;       // of the next copy, looked up one step early
-        bool has = false;
-        auto look = [&]() {            // table entry of the walk's next group, then a step on
-            has = left > 0;
-            if (!has) return;
-            --left;
-            const bool any = ci < cq.ng;
-            group = ci < cq.ns ? ci : ci + cq.skip;
-            page = any ? __ldg(a.pages.table + static_cast<size_t>(cr) * a.pages.max_pages +
-                               (group >> a.pages.group_shift)) : -2;
-            group = (group & (a.pages.groups - 1)) + ch * a.pages.groups;
-            if (++ci == cn && left > 0) {
-                ci = 0;
-                if (++cu == cq.rgs * n_kv) {
-                    cu = 0;
-                    do cq = load_req(a, ++cr, log_group); while (cq.rgs == 0);
-                    cn = max(cq.ng, 1);
-                }
-                ch = cu / cq.rgs;
+    if (warp < C::WARPS) {
+        const int wid = blockIdx.x * cut.A + warp;
+        if (lane == 0) {
+            ws.tasks[blockIdx.x * C::WARPS + warp].valid = 0;
+            pc->fin_unit = -1;
+            pc->todo = 0;
+            if (warp < cut.A && wid < cut.W && N > 0) {
+                const long long x0 = cut.start(wid), off = x0 - start_x[warp];
+                const int n = max(load_req(a, start_r[warp], log_group).ng, 1);
+                const int unit = static_cast<int>(off / n);
+                pc->r = start_r[warp];
+                pc->unit = unit;
+                pc->gi = static_cast<int>(off - static_cast<long long>(unit) * n);
+                pc->todo = static_cast<int>(cut.start(wid + 1) - x0);
             }
-        };
-        auto issue = [&](int stage) {  // the looked-up group into a stage, and the next look-up
-            if (!has) return;
-            const bool live = page >= 0 && page < a.pages.n_pages;
-            if (live) {
-                dead &= ~(1u << stage);
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(bars + stage, C::GB);
-                    bulk_copy_g2s(ring + stage * C::GB,
-                                  a.pages.base + (static_cast<size_t>(page) * n_kv *
-                                                      a.pages.groups + group) * C::GB,
-                                  C::GB, bars + stage);
-                }
-            } else {
-                dead |= 1u << stage;
-                if (page != -2 && lane == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
-            }
-            look();
-        };
-        look();
-#pragma unroll 1
-        for (int i = 0; i < S; ++i) issue(i);
-
+        }
+        __syncwarp();
         // ---- the run, piece by piece
-        int r = start_r[warp];
-        Req q = load_req(a, r, log_group);
-        int n = max(q.ng, 1);
-        int unit = static_cast<int>((x0 - start_x[warp]) / n);
-        int gi = static_cast<int>((x0 - start_x[warp]) - static_cast<long long>(unit) * n);
         int stage = 0;
+        uint32_t phase = 0;
         bool ok = true;
 #pragma unroll 1
-        while (todo > 0) {
-            const int h = unit / q.rgs, rg = unit - h * q.rgs;
-            const int g_first = gi;
-            const int g_end = min(n, gi + todo);
-            // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
-            // the second and fourth times 2^-4; brought to a maximum in [2^10, 2^11)
-            uint32_t qf[NB][4];
+        while (pc->todo > 0) {
+            int gi = pc->gi, g_end, f0, f1;
             float km[2];
             {
+            const Req q = load_req(a, pc->r, log_group);
+            const int n = max(q.ng, 1), unit = pc->unit;
+            const int h = unit / q.rgs, rg = unit - h * q.rgs;
+            g_end = min(n, gi + pc->todo);
+            // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
+            // the second and fourth times 2^-4; brought to a maximum in [2^10, 2^11)
+            {
                 const Col c = column(q, rg, g, h, log_group);
-                float x[NB][8], top = 0.0f;
+                const T *src = static_cast<const T *>(a.q) + max(c.token, 0) * a.q_stride +
+                               static_cast<long long>(c.head) * HD + 8 * t;
+                float x[8], top = 0.0f;
                 if (c.token >= 0) {
-                    const T *src = static_cast<const T *>(a.q) + c.token * a.q_stride +
-                                   static_cast<long long>(c.head) * HD + 8 * t;
+#pragma unroll 4
+                    for (int b = 0; b < NB; ++b) {
+                        load8(src + 32 * b, x);
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) load8(src + 32 * b, x[b]);
-                } else {
-#pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) x[b][i] = 0.0f;
+                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+                    }
                 }
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[b][i]));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                 int up = 0;
@@ -454,86 +517,108 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                                   16777216.0f;  // 2^24
                 km[0] = __shfl_sync(~0u, mul, 8 * t);
                 km[1] = __shfl_sync(~0u, mul, 8 * t + 4);
-#pragma unroll
+#pragma unroll 2
                 for (int b = 0; b < NB; ++b) {
                     float sum = 0.0f;
+                    if (c.token >= 0) load8(src + 32 * b, x);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        x[b][i] *= lift;
-                        sum += x[b][i];
+                        x[i] = c.token >= 0 ? x[i] * lift : 0.0f;
+                        sum += x[i];
                     }
                     sum += __shfl_xor_sync(~0u, sum, 1);
                     sum += __shfl_xor_sync(~0u, sum, 2);
-                    if (t == 0) bias[b * kRows + g] = sum * -4.76837158203125e-7f;  // -8 * 2^-24
-                    uint32_t lo[4];
+                    // -8 * 2^-24 of columns 2 t, 2 t + 1 in the order of an accumulator
+                    sum *= -4.76837158203125e-7f;
+                    const float s0 = __shfl_sync(~0u, sum, 8 * t), s1 = __shfl_sync(~0u, sum, 8 * t + 4);
+                    if (g == 0)
+                        *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) = make_float4(s0, s1, s0, s1);
+                    uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const uint32_t hi = pack_half2(x[b][i], x[b][i + 4]);
-                        const float2 f = half2_f(hi);
+                        hi[i] = pack_half2(x[i], x[i + 4]);
+                        const float2 f = half2_f(hi[i]);
                         const float sc = i & 1 ? 0.0625f : 1.0f;
-                        qf[b][i] = i & 1 ? pack_half2(f.x * sc, f.y * sc) : hi;
-                        if (C::QSPLIT)
-                            lo[i] = pack_half2((x[b][i] - f.x) * sc, (x[b][i + 4] - f.y) * sc);
+                        if (i & 1) hi[i] = pack_half2(f.x * sc, f.y * sc);
+                        lo[i] = pack_half2((x[i] - f.x) * sc, (x[i + 4] - f.y) * sc);
                     }
+                    *reinterpret_cast<uint4 *>(qs + (b * 32 + lane) * 16) =
+                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     if (C::QSPLIT)
-                        *reinterpret_cast<uint4 *>(qlo + (b * 32 + lane) * 16) =
+                        *reinterpret_cast<uint4 *>(qs + C::QF + (b * 32 + lane) * 16) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-            __syncwarp();
-            const int p0 = column(q, rg, 2 * t, h, log_group).pos;
-            const int p1 = column(q, rg, 2 * t + 1, h, log_group).pos;
             const int p_min = q.rows - q.nq + ((rg * kRows) >> log_group);
             const int p_max = q.rows - q.nq +
                               min(q.nq - 1, (rg * kRows + kRows - 1) >> log_group);
+            if (lane < kRows) pc->pos[lane] = column(q, rg, lane, h, log_group).pos;
+            if (lane == 0) {
+                pc->n = n;
+                pc->end = g_end;
+                pc->p_min = p_min;
+                pc->p_max = p_max;
+                pc->ns = q.ns;
+                pc->skip = q.skip;
+            }
+            // groups [f0, f1) of the unit are seen whole by every row
+            f0 = 0;
+            f1 = max(0, p_min + 1) / kGroupRows - q.skip;
+            if (a.win > 0)
+                f0 = max(q.ns, (max(-1, p_max - a.win) + kGroupRows) / kGroupRows - q.skip);
+            }
+            __syncwarp();
             st.clear();
 
 #pragma unroll 1
             for (; gi < g_end; ++gi) {
-                const bool live = !(dead >> stage & 1);
-                if (live && ok) {
-                    ok = mbar_wait(bars + stage, parity >> stage & 1, &abort_flag, a.err);
-                    parity ^= 1u << stage;
-                }
-                if (live && ok) {
+                uint64_t *bar = full + warp * S + stage;
+                if (ok) ok = mbar_wait(bar, phase, &abort_flag, a.err);
+                if (ok && !dead[warp * S + stage]) {
                     const uint8_t *kp = ring + stage * C::GB, *vp = kp + part_bytes(HD);
                     // ---- scores of rows g, g + 8 (y[0..1], y[2..3]) and columns 2 t, 2 t + 1
-                    uint32_t kw[2 * NB];
-#pragma unroll
-                    for (int c = 0; c < NB / 2; ++c) {
-                        const uint4 w = lds_v4(kp + (c * 32 + lane) * 16);
-                        kw[4 * c] = w.x; kw[4 * c + 1] = w.y; kw[4 * c + 2] = w.z; kw[4 * c + 3] = w.w;
-                    }
                     float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const uint32_t *ks = reinterpret_cast<const uint32_t *>(kp + scale_offset(HD));
+                    // codes of rows g, g + 8 and their block scales, 4 blocks (2 of head_dim 64)
+                    // at a time: with all of a group's at once the registers do not suffice
+                    constexpr int KB = NB < 4 ? NB : 4;
+                    uint32_t wAs[KB], wBs[KB], sA[KB / 2], sB[KB / 2];
 #pragma unroll
-                    for (int b2 = 0; b2 < NB / 2; ++b2) {
-                        const float2 sA = half2_f(ks[g * (NB / 2) + b2]);
-                        const float2 sB = half2_f(ks[(g + 8) * (NB / 2) + b2]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int b = 2 * b2 + k;
-                            const float2 c0 = *reinterpret_cast<const float2 *>(bias + b * kRows + 2 * t);
-                            float d[4] = {c0.x, c0.y, c0.x, c0.y};
-                            const uint32_t wA = kw[b], wB = kw[NB + b];
-                            const uint32_t vA = wA >> 8, vB = wB >> 8;
-                            const uint32_t e0 = wA & 0x000f000fu, e1 = wB & 0x000f000fu;
-                            const uint32_t e2 = wA & 0x00f000f0u, e3 = wB & 0x00f000f0u;
-                            const uint32_t f0 = vA & 0x000f000fu, f1 = vB & 0x000f000fu;
-                            const uint32_t f2 = vA & 0x00f000f0u, f3 = vB & 0x00f000f0u;
-                            mma(d, e0, e1, e2, e3, qf[b][0], qf[b][1]);
-                            mma(d, f0, f1, f2, f3, qf[b][2], qf[b][3]);
-                            if (C::QSPLIT) {
-                                const uint4 lo = lds_v4(qlo + (b * 32 + lane) * 16);
-                                mma(d, e0, e1, e2, e3, lo.x, lo.y);
-                                mma(d, f0, f1, f2, f3, lo.z, lo.w);
+                    for (int b = 0; b < NB; ++b) {
+                        if (b % KB == 0) {
+                            if (NB == 2) {
+                                const uint4 w = lds_v4(kp + lane * 16);
+                                wAs[0] = w.x; wAs[1] = w.y; wBs[0] = w.z; wBs[1] = w.w;
+                            } else {
+                                const uint4 w = lds_v4(kp + ((b / 4) * 32 + lane) * 16);
+                                const uint4 x = lds_v4(kp + (((NB + b) / 4) * 32 + lane) * 16);
+                                wAs[0] = w.x; wAs[1] = w.y; wAs[2 % KB] = w.z; wAs[3 % KB] = w.w;
+                                wBs[0] = x.x; wBs[1] = x.y; wBs[2 % KB] = x.z; wBs[3 % KB] = x.w;
                             }
-                            const float a0 = k ? sA.y : sA.x, a1 = k ? sB.y : sB.x;
-                            y[0] = fmaf(a0, d[0], y[0]);
-                            y[1] = fmaf(a0, d[1], y[1]);
-                            y[2] = fmaf(a1, d[2], y[2]);
-                            y[3] = fmaf(a1, d[3], y[3]);
+                            lds_words<KB / 2>(sA, kp + scale_offset(HD) + g * (2 * NB) + 2 * b);
+                            lds_words<KB / 2>(sB, kp + scale_offset(HD) + (g + 8) * (2 * NB) + 2 * b);
                         }
+                        const uint4 qf = lds_v4(qs + (b * 32 + lane) * 16);
+                        const float4 c0 = lds_f4(bias + (b * 4 + t) * 16);
+                        float d[4] = {c0.x, c0.y, c0.z, c0.w};
+                        const uint32_t wA = wAs[b % KB], wB = wBs[b % KB];
+                        const uint32_t vA = wA >> 8, vB = wB >> 8;
+                        const uint32_t e0 = wA & 0x000f000fu, e1 = wB & 0x000f000fu;
+                        const uint32_t e2 = wA & 0x00f000f0u, e3 = wB & 0x00f000f0u;
+                        const uint32_t f0 = vA & 0x000f000fu, f1 = vB & 0x000f000fu;
+                        const uint32_t f2 = vA & 0x00f000f0u, f3 = vB & 0x00f000f0u;
+                        mma(d, e0, e1, e2, e3, qf.x, qf.y);
+                        mma(d, f0, f1, f2, f3, qf.z, qf.w);
+                        if (C::QSPLIT) {
+                            const uint4 lo = lds_v4(qs + C::QF + (b * 32 + lane) * 16);
+                            mma(d, e0, e1, e2, e3, lo.x, lo.y);
+                            mma(d, f0, f1, f2, f3, lo.z, lo.w);
+                        }
+                        const float2 uA = half2_f(sA[b % KB / 2]), uB = half2_f(sB[b % KB / 2]);
+                        const float a0 = b & 1 ? uA.y : uA.x, a1 = b & 1 ? uB.y : uB.x;
+                        y[0] = fmaf(a0, d[0], y[0]);
+                        y[1] = fmaf(a0, d[1], y[1]);
+                        y[2] = fmaf(a1, d[2], y[2]);
+                        y[3] = fmaf(a1, d[3], y[3]);
                     }
                     const uint16_t *kf = reinterpret_cast<const uint16_t *>(kp + factor_offset(HD));
                     const uint16_t *vf = reinterpret_cast<const uint16_t *>(vp + factor_offset(HD));
@@ -547,18 +632,10 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     y[1] = fmaf(y[1] * fA, km[1], eA);
                     y[2] = fmaf(y[2] * fB, km[0], eB);
                     y[3] = fmaf(y[3] * fB, km[1], eB);
-                    // V's block scales of rows 2t, 2t+1 | 2t+8, 2t+9
-                    uint32_t vs[2 * NB];
-#pragma unroll
-                    for (int c = 0; c < NB / 2; ++c) {
-                        const uint4 w = lds_v4(vp + scale_offset(HD) + (c * 4 + t) * 16);
-                        vs[4 * c] = w.x; vs[4 * c + 1] = w.y; vs[4 * c + 2] = w.z; vs[4 * c + 3] = w.w;
-                    }
-                    const int j0 = (gi < q.ns ? gi : gi + q.skip) * kGroupRows;
-                    const bool whole = j0 + kGroupRows - 1 <= p_min &&
-                                       (a.win <= 0 || j0 + kGroupRows <= a.sink ||
-                                        j0 > p_max - a.win);
-                    if (!whole) {
+                    if (gi < f0 || gi >= f1) {
+                        const int j0 = (gi < pc->ns ? gi : gi + pc->skip) * kGroupRows;
+                        const int p0 = pc->pos[2 * t], p1 = pc->pos[2 * t + 1];
+                        const int p_min = pc->p_min, p_max = pc->p_max;
                         // rows that no query sees may hold anything: their scales and
                         // sums must not reach a product, not even with a zero
                         auto seen = [&](int j) {
@@ -574,11 +651,13 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         const int k0 = j0 + 2 * t;
                         const uint32_t m01 = (seen(k0) ? 0xffffu : 0u) | (seen(k0 + 1) ? 0xffff0000u : 0u);
                         const uint32_t m23 = (seen(k0 + 8) ? 0xffffu : 0u) | (seen(k0 + 9) ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            vs[2 * b] &= m01;
-                            vs[2 * b + 1] &= m23;
+                        if (g < NB / 2) {  // V's scales of rows 2t, 2t+1 | 2t+8, 2t+9 and two blocks
+                            uint4 *w = reinterpret_cast<uint4 *>(ring + stage * C::GB + part_bytes(HD) +
+                                                                 scale_offset(HD) + (g * 4 + t) * 16);
+                            *w = make_uint4(w->x & m01, w->y & m23, w->z & m01, w->w & m23);
                         }
+                        fence_proxy_async_smem();  // before the next copy into the stage
+                        __syncwarp();
                     }
                     // ---- weights relative to the reference
                     float d0 = y[0] - st.m[0], d1 = y[1] - st.m[1], d2 = y[2] - st.m[0],
@@ -627,6 +706,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     }
                     // ---- O += V^T P
                     uint32_t vw[2 * NB];
+                    uint4 vs;
 #pragma unroll
                     for (int c = 0; c < NB / 2; ++c) {
                         const uint4 w = lds_v4(vp + (c * 32 + lane) * 16);
@@ -639,7 +719,8 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         const uint32_t x01 = __byte_perm(vw[b / 2], vw[(NB + b) / 2], sel);
                         const uint32_t x23 = __byte_perm(vw[(2 * NB + b) / 2], vw[(3 * NB + b) / 2], sel);
                         const uint32_t z01 = x01 >> 8, z23 = x23 >> 8;
-                        const uint32_t s01 = vs[2 * b], s23 = vs[2 * b + 1];
+                        if (b % 2 == 0) vs = lds_v4(vp + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
+                        const uint32_t s01 = b & 1 ? vs.z : vs.x, s23 = b & 1 ? vs.w : vs.y;
                         const uint32_t w0 = hmul2(b0, s01), w1 = hmul2(b1, s23);
                         const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
                         const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
@@ -673,16 +754,18 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     }
                 }
                 __syncwarp();  // every lane has read the stage
-                if (ok) issue(stage);
-                if (++stage == S) stage = 0;
+                if (ok && lane == 0) mbar_arrive(bar + C::WARPS * S);
+                if (++stage == S) stage = 0, phase ^= 1;
             }
-            todo -= g_end - g_first;
 
             // ---- the piece is done
-            const bool begins = g_first == 0, ends = g_end == n;
-            const long long first = x1 - todo - g_end;  // the unit's first group in the cut
-            if (begins && ends) {
-                st.sum_lanes();
+            st.sum_lanes();
+            const int r = pc->r, unit = pc->unit, n = pc->n, first = pc->gi, end = pc->end;
+            const int todo = pc->todo - (end - first);
+            const int wid = blockIdx.x * cut.A + warp;
+            const Req q = load_req(a, r, log_group);
+            if (first == 0 && end == n) {
+                const int h = unit / q.rgs, rg = unit - h * q.rgs;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const Col col = column(q, rg, 2 * t + c, h, log_group);
@@ -697,7 +780,6 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                             (st.m[c] + log2f(st.l[c])) * kLn2;
                 }
             } else if (todo > 0) {  // the start of the run: to the workspace
-                st.sum_lanes();
                 float *dst = ws.partial + (static_cast<size_t>(wid) * 2 + 1) * C::PARTIAL;
                 if (g == 0) {
 #pragma unroll
@@ -712,82 +794,70 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     for (int c = 0; c < 2; ++c)
                         *reinterpret_cast<float4 *>(dst + 2 * kRows + ((b * 2 + c) * 32 + lane) * 4) =
                             st.quad(b, c);
-            } else {
-                last_unit = unit;
-                last_r = r;
-                last_first = first;
-                last_last = first + n;
-            }
-            if (todo > 0) {
-                gi = 0;
-                if (++unit == q.rgs * n_kv) {
-                    unit = 0;
-                    do q = load_req(a, ++r, log_group); while (q.rgs == 0);
-                    n = max(q.ng, 1);
+            } else {  // the end of the run: into the ring, whose copies have all been used
+                if (g == 0) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        pc->m[2 * t + c] = st.m[c];
+                        pc->l[2 * t + c] = st.l[c];
+                    }
                 }
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c)
+                        *reinterpret_cast<float4 *>(ring + ((b * 2 + c) * 32 + lane) * 16) = st.quad(b, c);
             }
+            __syncwarp();
+            if (lane == 0) {
+                if (todo == 0 && !(first == 0 && end == n)) {
+                    pc->fin_r = r;
+                    pc->fin_unit = unit;
+                    pc->fin_first = cut.start(wid + 1) - end;
+                    pc->fin_last = cut.start(wid + 1) - end + n;
+                }
+                int next = unit + 1, nr = r;
+                if (todo > 0 && next == q.rgs * n_kv) {
+                    next = 0;
+                    while (load_req(a, ++nr, log_group).rgs == 0) {}
+                }
+                pc->r = nr;
+                pc->unit = next;
+                pc->gi = 0;
+                pc->todo = todo;
+            }
+            __syncwarp();
         }
-        if (!ok) {  // a wait ran out: let this warp's copies end before its memory is given up
-            const long long t0 = clock64();
-            for (int i = 0; i < S; ++i)
-                while (!(dead >> i & 1) && !mbar_try_wait(bars + i, parity >> i & 1) &&
-                       clock64() - t0 < kSpinCycles) {}
-        }
+    }
+    if (*static_cast<volatile int *>(&abort_flag)) {
+        // a wait ran out: give copies in flight half a millisecond before their memory is given up
+        const long long t0 = clock64();
+        while (clock64() - t0 < 1000000) {}
     }
 
     // ---- join the pieces that end the warps' runs, unit by unit
-    if (last_unit >= 0) st.sum_lanes();
-    if (lane == 0) {
-        fin_unit[warp] = last_unit;
-        fin_r[warp] = last_r;
-        fin_first[warp] = last_first;
-        fin_last[warp] = last_last;
-    }
-    if (g == 0) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            fin_m[warp][2 * t + c] = st.m[c];
-            fin_l[warp][2 * t + c] = st.l[c];
-        }
-    }
-    if (last_unit >= 0) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-                *reinterpret_cast<float4 *>(ring + ((b * 2 + c) * 32 + lane) * 16) = st.quad(b, c);
-    }
     __syncthreads();
-    if (last_unit < 0) return;
-    auto same = [&](int w) { return fin_unit[w] == last_unit && fin_r[w] == last_r; };
+    if (warp >= C::WARPS || pc->fin_unit < 0) return;
+    const int r = pc->fin_r, unit = pc->fin_unit;
+    const long long first = pc->fin_first, last = pc->fin_last;
+    auto same = [&](int w) { return pieces[w].fin_unit == unit && pieces[w].fin_r == r; };
     int w0 = warp, w1 = warp + 1;  // warps [w0, w1) hold pieces of this unit
     while (w0 > 0 && same(w0 - 1)) --w0;
     while (w1 < C::WARPS && same(w1)) ++w1;
     const int id0 = blockIdx.x * cut.A + w0, id1 = blockIdx.x * cut.A + w1;
-    const bool from_start = cut.start(id0) <= last_first, to_end = cut.start(id1) >= last_last;
+    const bool from_start = cut.start(id0) <= first, direct = from_start && cut.start(id1) >= last;
     float M[2] = {kLowest, kLowest}, L[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        for (int w = w0; w < w1; ++w) M[c] = fmaxf(M[c], fin_m[w][2 * t + c]);
-        for (int w = w0; w < w1; ++w) L[c] += fin_l[w][2 * t + c] * ex2(fin_m[w][2 * t + c] - M[c]);
+        const int n = 2 * t + c;
+        for (int w = w0; w < w1; ++w) M[c] = fmaxf(M[c], pieces[w].m[n]);
+        for (int w = w0; w < w1; ++w) L[c] += pieces[w].l[n] * ex2(pieces[w].m[n] - M[c]);
     }
-    const Req q = load_req(a, last_r, log_group);
-    const int h = last_unit / q.rgs, rg = last_unit - h * q.rgs;
+    const Req q = load_req(a, r, log_group);
+    const int h = unit / q.rgs, rg = unit - h * q.rgs;
     float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
-    if (from_start && !to_end && warp == w0 && lane == 0) {
-        Task k;
-        k.valid = 1;
-        k.r = last_r;
-        k.unit = last_unit;
-        k.w = id0;
-        k.first = last_first;
-        k.last = last_last;
-        k.N = N;
-        k.W = cut.W;
-        k.A = cut.A;
-        ws.tasks[slot] = k;
-    }
-    const bool direct = from_start && to_end;
+    if (from_start && !direct && warp == w0 && lane == 0)
+        ws.tasks[blockIdx.x * C::WARPS + warp] = Task{1, r, unit, id0, first, last, cut.N, cut.W, cut.A};
     if (!direct && warp == w0 && g == 0) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -800,7 +870,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int w = w0; w < w1; ++w) {
             const float4 y = *reinterpret_cast<const float4 *>(smem + w * C::RING + (i * 32 + lane) * 16);
-            const float f = ex2(fin_m[w][2 * t + c] - M[c]);
+            const float f = ex2(pieces[w].m[2 * t + c] - M[c]);
             x.x = fmaf(y.x, f, x.x);
             x.y = fmaf(y.y, f, x.y);
             x.z = fmaf(y.z, f, x.z);
