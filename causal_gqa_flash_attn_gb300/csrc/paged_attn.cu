@@ -25,22 +25,23 @@
 //     values' magnitude. The sum of weights takes 2^-e back out.
 //   - The reference that scores are taken relative to is moved only when a score
 //     passes it by 2^14 (kLift above the last maximum, up to binary16's range):
-//     one vote per 16 rows instead of a reduction.
+//     one vote per tile instead of a reduction.
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
 // the scaled weights; their products go through a fresh accumulator per 16 rows
 // that fp32 adds collect, as the tensor core's own sums lose a step per addition.
 //
 // Work split. The 16-row groups that are read, over all (request, kv head, row
 // group) units, are cut into equal runs, one per warp of one block per SM; a
-// warp streams its run through its own ring of bulk copies and starts the next
-// unit's rows while it works on this one's. A unit inside one warp's run is
-// written directly. Pieces of longer units are joined: those that end the runs
-// of neighbouring warps of a block in shared memory, the others (at most two per
-// warp) through the workspace by a second kernel, in a fixed order.
+// warp streams its run through its own ring of bulk copies, which one more warp
+// issues. A unit inside one warp's run is written directly. Pieces of longer
+// units are joined: those that end the runs of neighbouring warps of a block in
+// shared memory, the others (at most two per warp) through the workspace by a
+// second kernel, in a fixed order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
@@ -55,6 +56,7 @@ constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 constexpr int kMinGroups = 4;      // groups per warp below which fewer warps work
 constexpr int kRows = 8;           // query rows of a row group
 constexpr int kMostWarps = 16;     // computing warps of a block that the workspace is made for
+constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
 
 template <typename T, int HD>
 struct Cfg {
@@ -62,33 +64,37 @@ struct Cfg {
     static constexpr bool PSPLIT = !std::is_same<T, __nv_bfloat16>::value;
     static constexpr int NB = HD / 32;
     static constexpr int GB = group_bytes(HD);
-    // Warps that compute, and one more that copies; registers for one block of
-    // them per SM, ring stages for what is left of shared memory.
+    // Warps that compute (and one more that copies): what the registers of one
+    // block per SM allow without spills. Groups that are taken at once (TILE),
+    // and tiles of a warp's ring.
 #ifdef PA_WARPS
     static constexpr bool PP = sizeof(T) == PA_SIZE && HD == PA_HD;
     static constexpr int WARPS = PP ? PA_WARPS : 7;
-    static constexpr int STAGES = PP ? PA_STAGES : 4;
+    static constexpr int TILE = PP ? PA_TILE : 1;
+    static constexpr int STAGES = PP ? PA_STAGES : 2;
 #else
-    static constexpr int WARPS = HD == 256 ? (PSPLIT ? 7 : 11) : PSPLIT ? 11 : 15;
-    static constexpr int STAGES = HD == 256 ? (PSPLIT ? 4 : 3) : HD == 128 ? 4 : 8;
+    static constexpr int WARPS = HD == 256 ? 11 : PSPLIT ? 11 : 15;
+    static constexpr int TILE = HD == 256 ? 1 : HD == 128 ? 2 : 4;
+    static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : 2;
 #endif
-    static constexpr int RING = STAGES * GB;
+    static constexpr int STAGE = TILE * GB;
+    static constexpr int RING = STAGES * STAGE;
     static constexpr int QF = NB * 32 * 16;           // q as B fragments
     static constexpr int QB = QF * (QSPLIT ? 2 : 1);  // and their low terms
     static constexpr int BIAS = NB * 4 * 16;          // the accumulators' start, as lanes hold it
     static constexpr int OFF_Q = WARPS * RING;
     static constexpr int OFF_BIAS = OFF_Q + WARPS * QB;
     static constexpr int OFF_BAR = OFF_BIAS + WARPS * BIAS;
-    static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 16;  // full and empty barriers
+    static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 8;
     static constexpr int SMEM = OFF_DEAD + WARPS * STAGES * 4;
     static constexpr int THREADS = (WARPS + 1) * 32;
     // a partial: m and l of 8 rows, then O as the lanes hold it
     static constexpr int PARTIAL = 2 * kRows + kRows * HD;  // floats
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
-    static_assert(2 * WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
+    static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
     static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
     static_assert(RING >= kRows * HD * 4, "a warp's O fits its ring");
-    static_assert(SMEM <= 225 * 1024, "shared memory");
+    static_assert(SMEM <= 224 * 1024, "shared memory");
 };
 
 // How a request's rows are read, from its lengths.
@@ -127,29 +133,41 @@ __device__ __forceinline__ long long req_work(const Req &q, int n_kv) {
     return static_cast<long long>(max(q.ng, 1)) * q.rgs * n_kv;
 }
 
-// The cut of the work: N groups over W warps, A of them in each block.
+// Quotients of 64-bit counts, which mostly have 32.
+__device__ __forceinline__ long long quotient(long long n, int d) {
+    return n >> 32 ? n / d : static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(d));
+}
+
+// The cut of the work: N groups, c for each of B blocks, cw of those for each
+// of A warps (the last ones may have fewer, or none).
 struct Cut {
-    long long N;
-    int W, A;
-    __device__ __forceinline__ long long start(int w) const { return N * w / W; }
+    long long N, c;
+    int cw, B, A;
+    __device__ __forceinline__ long long start(int b, int i) const {
+        return min(b * c + min(static_cast<long long>(i) * cw, c), N);
+    }
+    __device__ __forceinline__ int warp_of(long long x) const {  // c < 2^31: 2^40 groups at most
+        const int b = static_cast<int>(quotient(x, static_cast<int>(c)));
+        return b * A + static_cast<int>(quotient(x - b * c, cw));
+    }
 };
 __device__ __forceinline__ Cut make_cut(long long N, int blocks, int warps) {
-    Cut c;
-    c.N = N;
-    const long long want = (N + kMinGroups - 1) / kMinGroups;
-    c.W = static_cast<int>(min(static_cast<long long>(blocks) * warps, max(want, 1ll)));
-    c.A = (c.W + blocks - 1) / blocks;
-    c.W = min(c.W, c.A * blocks);
-    return c;
+    Cut t;
+    t.N = N;
+    const long long want = max((N + kMinGroups - 1) / kMinGroups, 1ll);
+    t.B = static_cast<int>(min(static_cast<long long>(blocks), want));
+    t.c = max(quotient(N + t.B - 1, t.B), 1ll);
+    t.A = static_cast<int>(min(static_cast<long long>(warps), (t.c + kMinGroups - 1) / kMinGroups));
+    t.cw = static_cast<int>(quotient(t.c + t.A - 1, t.A));
+    return t;
 }
 
 // A unit that other blocks share, for the join: written by the warp whose run
 // holds its first group.
 struct Task {
-    int valid, r, unit, w;  // w: that warp
+    int valid, r, unit, w;  // w: that warp, counted over the blocks
     long long first, last;  // its groups [first, last)
-    long long N;            // the cut
-    int W, A;
+    Cut cut;
 };
 struct Ws {
     Task *tasks;     // one per warp
@@ -188,32 +206,38 @@ __device__ __forceinline__ void lds_words(uint32_t *w, const uint8_t *p) {
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[0]) : "r"(smem_u32(p)));
 }
 
-// 8 consecutive values as fp32.
-__device__ __forceinline__ void load8(const float *p, float *x) {
-    const float4 a = *reinterpret_cast<const float4 *>(p);
-    const float4 b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __half *p, float *x) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const __half2 *h = reinterpret_cast<const __half2 *>(&w);
+// 8 consecutive values as they lie in memory.
+template <typename T>
+struct Raw8 {
+    static constexpr int N = sizeof(T) / 2;
+    uint4 w[N];
+    __device__ __forceinline__ void load(const T *p, bool there) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        for (int i = 0; i < N; ++i)
+            w[i] = there ? *(reinterpret_cast<const uint4 *>(p) + i) : make_uint4(0, 0, 0, 0);
     }
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float *x) {
-    const uint4 w = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t h[4] = {w.x, w.y, w.z, w.w};
+    __device__ __forceinline__ void get(float *x) const {
+        if constexpr (N == 2) {
+            x[0] = __uint_as_float(w[0].x); x[1] = __uint_as_float(w[0].y);
+            x[2] = __uint_as_float(w[0].z); x[3] = __uint_as_float(w[0].w);
+            x[4] = __uint_as_float(w[1].x); x[5] = __uint_as_float(w[1].y);
+            x[6] = __uint_as_float(w[1].z); x[7] = __uint_as_float(w[1].w);
+        } else {
+            const uint32_t h[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(h[i] << 16);
-        x[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (std::is_same<T, __half>::value) {
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
+                } else {
+                    x[2 * i] = __uint_as_float(h[i] << 16);
+                    x[2 * i + 1] = __uint_as_float(h[i] & 0xffff0000u);
+                }
+            }
+        }
     }
-}
+};
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -243,6 +267,8 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// -8 * 2^-24 and -8 * 2^-20, twice.
+constexpr uint32_t kM8a = 0x80088008u, kM8b = 0x80808080u;
 // 2^-24 and 2^-20 come out of O's rows g and g + 8.
 constexpr float kUnshift0 = 16777216.0f, kUnshift1 = 1048576.0f;
 
@@ -288,9 +314,30 @@ struct State {
     }
 };
 
-__device__ __forceinline__ float scaled(float x, float inv) { return x * inv; }
 __device__ __forceinline__ float4 scaled(float4 v, float s) {
     return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
+}
+
+// Four dims of a finished row, and with the first ones its log-sum-exp.
+template <typename T>
+__device__ __forceinline__ void write_row(const PagedAttnArgs &a, const Col &col, int hd, int dim,
+                                          float4 x, float m, float l) {
+    if (col.token < 0) return;
+    store4<T>(static_cast<T *>(a.out) + col.token * a.out_stride +
+                  static_cast<long long>(col.head) * hd + dim,
+              scaled(x, l > 0.0f ? 1.0f / l : l));  // nothing attended: 0 (a NaN stays one)
+    if (a.lse && dim == 0)
+        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (m + log2f(l)) * kLn2;
+}
+
+// Groups that are taken at once from group i of a unit on, which is read up to
+// group `end`: a tile begins at a multiple of TILE, and at its page's if the
+// page has TILE groups or more.
+template <int TILE>
+__device__ __forceinline__ int tile_size(int i, int end, int ns, int skip) {
+    if (TILE == 1) return 1;
+    const int most = i < ns ? min(ns, end) - i : end - i;
+    return min(TILE - ((i < ns ? i : i + skip) & (TILE - 1)), most);
 }
 
 // A warp's place in its run and what the unit it is in needs once per piece or
@@ -302,12 +349,214 @@ struct Piece {
     int pos[kRows];             // the columns' positions
     int p_min, p_max;           // of all of them
     int ns, skip;               // group i of the unit is i, or i + skip from ns on
+    int holes;                  // the run has met a group without rows to read
+    int gone;                   // tiles of the run that are done, whose stages are free
     int fin_r, fin_unit;        // the piece that ends the run, if other warps have more of its unit (else -1)
     long long fin_first, fin_last;  // that unit's groups in the cut
     float m[kRows], l[kRows];   // and the piece's references and sums
 };
 
-constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
+// M groups of the run, at kp[0..M-1] in shared memory: scores, weights, O.
+// EDGE: not every row of the unit sees the (one) group whole; j0 is its first
+// key and pc says what is seen.
+template <typename C, int M, bool EDGE>
+__device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
+                                     const uint8_t *bias, float km0, float km1,
+                                     const volatile Piece *pc, int j0, int sink, int win) {
+    constexpr int NB = C::NB, HD = NB * 32;
+    static_assert(M == 1 || !EDGE, "edges are taken one by one");
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // ---- scores of rows g, g + 8 (y[0..1], y[2..3]) and columns 2 t, 2 t + 1
+    float y[M][4];
+#pragma unroll
+    for (int k = 0; k < M; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
+    // codes of rows g, g + 8 and their block scales, 4 blocks (2 of head_dim 64) at
+    // a time: with all of a group's at once the registers do not suffice
+    constexpr int KB = NB < 4 ? NB : 4;
+    uint32_t wA[M][KB], wB[M][KB], sA[M][KB / 2], sB[M][KB / 2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        if (b % KB == 0) {
+#pragma unroll
+            for (int k = 0; k < M; ++k) {
+                if (NB == 2) {
+                    const uint4 w = lds_v4(kp[k] + lane * 16);
+                    wA[k][0] = w.x; wA[k][1] = w.y; wB[k][0] = w.z; wB[k][1] = w.w;
+                } else {
+                    const uint4 w = lds_v4(kp[k] + ((b / 4) * 32 + lane) * 16);
+                    const uint4 x = lds_v4(kp[k] + (((NB + b) / 4) * 32 + lane) * 16);
+                    wA[k][0] = w.x; wA[k][1] = w.y; wA[k][2 % KB] = w.z; wA[k][3 % KB] = w.w;
+                    wB[k][0] = x.x; wB[k][1] = x.y; wB[k][2 % KB] = x.z; wB[k][3 % KB] = x.w;
+                }
+                lds_words<KB / 2>(sA[k], kp[k] + scale_offset(HD) + g * (2 * NB) + 2 * b);
+                lds_words<KB / 2>(sB[k], kp[k] + scale_offset(HD) + (g + 8) * (2 * NB) + 2 * b);
+            }
+        }
+        const uint4 qf = lds_v4(qs + (b * 32 + lane) * 16);
+        uint4 lo = make_uint4(0, 0, 0, 0);
+        if (C::QSPLIT) lo = lds_v4(qs + C::QF + (b * 32 + lane) * 16);
+        const float4 c0 = lds_f4(bias + (b * 4 + t) * 16);
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            float d[4] = {c0.x, c0.y, c0.z, c0.w};
+            const uint32_t a = wA[k][b % KB], c = wB[k][b % KB], a8 = a >> 8, c8 = c >> 8;
+            const uint32_t e0 = a & 0x000f000fu, e1 = c & 0x000f000fu;
+            const uint32_t e2 = a & 0x00f000f0u, e3 = c & 0x00f000f0u;
+            const uint32_t f0 = a8 & 0x000f000fu, f1 = c8 & 0x000f000fu;
+            const uint32_t f2 = a8 & 0x00f000f0u, f3 = c8 & 0x00f000f0u;
+            mma(d, e0, e1, e2, e3, qf.x, qf.y);
+            mma(d, f0, f1, f2, f3, qf.z, qf.w);
+            if (C::QSPLIT) {
+                mma(d, e0, e1, e2, e3, lo.x, lo.y);
+                mma(d, f0, f1, f2, f3, lo.z, lo.w);
+            }
+            const float2 uA = half2_f(sA[k][b % KB / 2]), uB = half2_f(sB[k][b % KB / 2]);
+            const float a0 = b & 1 ? uA.y : uA.x, a1 = b & 1 ? uB.y : uB.x;
+            y[k][0] = fmaf(a0, d[0], y[k][0]);
+            y[k][1] = fmaf(a0, d[1], y[k][1]);
+            y[k][2] = fmaf(a1, d[2], y[k][2]);
+            y[k][3] = fmaf(a1, d[3], y[k][3]);
+        }
+    }
+    float iA[M], iB[M];  // 2^-e of V's rows
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+        const uint8_t *kf = kp[k] + factor_offset(HD) + 2 * g, *vf = kf + part_bytes(HD);
+        const float fA = __uint_as_float(lds_u16(kf) << 16), fB = __uint_as_float(lds_u16(kf + 16) << 16);
+        const int xA = lds_u16(vf) >> 7, xB = lds_u16(vf + 16) >> 7;  // biased exponents
+        const float eA = static_cast<float>(xA - 127), eB = static_cast<float>(xB - 127);
+        iA[k] = __uint_as_float(static_cast<uint32_t>(254 - xA) << 23);
+        iB[k] = __uint_as_float(static_cast<uint32_t>(254 - xB) << 23);
+        y[k][0] = fmaf(y[k][0] * fA, km0, eA);
+        y[k][1] = fmaf(y[k][1] * fA, km1, eA);
+        y[k][2] = fmaf(y[k][2] * fB, km0, eB);
+        y[k][3] = fmaf(y[k][3] * fB, km1, eB);
+    }
+    if (EDGE) {
+        const int p0 = pc->pos[2 * t], p1 = pc->pos[2 * t + 1], p_min = pc->p_min, p_max = pc->p_max;
+        // rows that no query sees may hold anything: their scales and sums must not
+        // reach a product, not even with a zero
+        auto seen = [&](int j) { return j <= p_max && (win <= 0 || j < sink || j > p_min - win); };
+        const int jA = j0 + g, jB = jA + 8;
+        if (!key_visible(p0, jA, sink, win)) y[0][0] = -INFINITY;
+        if (!key_visible(p1, jA, sink, win)) y[0][1] = -INFINITY;
+        if (!key_visible(p0, jB, sink, win)) y[0][2] = -INFINITY;
+        if (!key_visible(p1, jB, sink, win)) y[0][3] = -INFINITY;
+        if (!seen(jA)) iA[0] = 0.0f;
+        if (!seen(jB)) iB[0] = 0.0f;
+        const int k0 = j0 + 2 * t;
+        const uint32_t m01 = (seen(k0) ? 0xffffu : 0u) | (seen(k0 + 1) ? 0xffff0000u : 0u);
+        const uint32_t m23 = (seen(k0 + 8) ? 0xffffu : 0u) | (seen(k0 + 9) ? 0xffff0000u : 0u);
+        if (g < NB / 2) {  // V's scales of rows 2t, 2t+1 | 2t+8, 2t+9 and two blocks
+            uint4 *w = reinterpret_cast<uint4 *>(kp[0] + part_bytes(HD) + scale_offset(HD) +
+                                                 (g * 4 + t) * 16);
+            *w = make_uint4(w->x & m01, w->y & m23, w->z & m01, w->w & m23);
+        }
+        fence_proxy_async_smem();  // before the next copy into the stage
+        __syncwarp();
+    }
+    // ---- weights relative to the reference
+    float top = kLowest;
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+        top = fmaxf(top, fmaxf(fmaxf(y[k][0], y[k][2]) - st.m[0], fmaxf(y[k][1], y[k][3]) - st.m[1]));
+    if (__any_sync(~0u, top > kMost)) {
+        float u0 = y[0][0], u1 = y[0][1];
+#pragma unroll
+        for (int k = 0; k < M; ++k) {
+            u0 = fmaxf(u0, fmaxf(y[k][0], y[k][2]));
+            u1 = fmaxf(u1, fmaxf(y[k][1], y[k][3]));
+        }
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+            u0 = fmaxf(u0, __shfl_xor_sync(~0u, u0, d));
+            u1 = fmaxf(u1, __shfl_xor_sync(~0u, u1, d));
+        }
+        const float n0 = u0 - st.m[0] > kMost ? u0 - kLift : st.m[0];
+        const float n1 = u1 - st.m[1] > kMost ? u1 - kLift : st.m[1];
+        const float c0 = ex2(st.m[0] - n0), c1 = ex2(st.m[1] - n1);
+        st.m[0] = n0;
+        st.m[1] = n1;
+        st.l[0] *= c0;
+        st.l[1] *= c1;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                st.o[b][i][0] *= c0;
+                st.o[b][i][1] *= c1;
+                st.o[b][i][2] *= c0;
+                st.o[b][i][3] *= c1;
+            }
+    }
+    uint32_t b0[M], b1[M], l0[M], l1[M];
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+        const float d0 = ex2(y[k][0] - st.m[0]), d1 = ex2(y[k][1] - st.m[1]);
+        const float d2 = ex2(y[k][2] - st.m[0]), d3 = ex2(y[k][3] - st.m[1]);
+        st.l[0] += fmaf(d0, iA[k], d2 * iB[k]);
+        st.l[1] += fmaf(d1, iA[k], d3 * iB[k]);
+        const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
+        b0[k] = movmatrix_trans(hA);
+        b1[k] = movmatrix_trans(hB);
+        if (C::PSPLIT) {
+            const float2 rA = half2_f(hA), rB = half2_f(hB);
+            l0[k] = movmatrix_trans(pack_half2(d0 - rA.x, d1 - rA.y));
+            l1[k] = movmatrix_trans(pack_half2(d2 - rB.x, d3 - rB.y));
+        }
+    }
+    // ---- O += V^T P
+#pragma unroll
+    for (int k = 0; k < M; ++k) {
+        const uint8_t *vp = kp[k] + part_bytes(HD);
+        uint32_t vw[2 * NB];
+        uint4 vs = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < NB / 2; ++c) {
+            const uint4 w = lds_v4(vp + (c * 32 + lane) * 16);
+            vw[4 * c] = w.x; vw[4 * c + 1] = w.y; vw[4 * c + 2] = w.z; vw[4 * c + 3] = w.w;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
+            const uint32_t x01 = __byte_perm(vw[b / 2], vw[(NB + b) / 2], sel);
+            const uint32_t x23 = __byte_perm(vw[(2 * NB + b) / 2], vw[(3 * NB + b) / 2], sel);
+            const uint32_t z01 = x01 >> 8, z23 = x23 >> 8;
+            if (b % 2 == 0) vs = lds_v4(vp + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
+            const uint32_t s01 = b & 1 ? vs.z : vs.x, s23 = b & 1 ? vs.w : vs.y;
+            const uint32_t w0 = hmul2(b0[k], s01), w1 = hmul2(b1[k], s23);
+            const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
+            const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
+            const uint32_t f0 = z01 & 0x000f000fu, f1 = z01 & 0x00f000f0u;
+            const uint32_t f2 = z23 & 0x000f000fu, f3 = z23 & 0x00f000f0u;
+            if (C::PSPLIT) {
+                const uint32_t v0 = hfma2(l0[k], s01, hfma2(b0[k], s01, w0 ^ 0x80008000u));
+                const uint32_t v1 = hfma2(l1[k], s23, hfma2(b1[k], s23, w1 ^ 0x80008000u));
+                // c - 8 exactly: the tensor core's sums lose a step towards zero per
+                // addition, which an offset taken out afterwards would leave behind
+                float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const uint32_t g0 = hadd2(e0, kM8a), g1 = hadd2(e1, kM8b);
+                const uint32_t g2 = hadd2(e2, kM8a), g3 = hadd2(e3, kM8b);
+                mma(u, g0, g1, g2, g3, w0, w1);
+                mma(u, g0, g1, g2, g3, v0, v1);
+                const uint32_t h0 = hadd2(f0, kM8a), h1 = hadd2(f1, kM8b);
+                const uint32_t h2 = hadd2(f2, kM8a), h3 = hadd2(f3, kM8b);
+                mma(v, h0, h1, h2, h3, w0, w1);
+                mma(v, h0, h1, h2, h3, v0, v1);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    st.o[b][0][i] += u[i];
+                    st.o[b][1][i] += v[i];
+                }
+            } else {
+                mma(st.o[b][0], e0, e1, e2, e3, w0, w1);
+                mma(st.o[b][1], f0, f1, f2, f3, w0, w1);
+                mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
+                mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
+            }
+        }
+    }
+}
 
 template <typename T, int HD>
 __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(PagedAttnArgs a) {
@@ -326,15 +575,19 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     const int log_group = 31 - __clz(a.n_q_heads / n_kv);
     uint8_t *ring = smem + warp * C::RING;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [warp][stage]
-    uint64_t *empty = full + C::WARPS * S;
-    volatile int *dead = reinterpret_cast<int *>(smem + C::OFF_DEAD);  // stages without rows
+    uint64_t *bars = full + min(warp, C::WARPS - 1) * S;
+    volatile uint32_t *dead = reinterpret_cast<uint32_t *>(smem + C::OFF_DEAD);  // groups without rows
     uint8_t *qs = smem + C::OFF_Q + warp * C::QB;
     uint8_t *bias = smem + C::OFF_BIAS + warp * C::BIAS;
     const Ws ws = carve(a.workspace, gridDim.x);
 
-    if (tid < 2 * C::WARPS * S) mbar_init(full + tid, 1);
+    if (tid < C::WARPS * S) mbar_init(full + tid, 1);
     if (tid == 0) abort_flag = 0;
+    if (tid < C::WARPS) pieces[tid].holes = pieces[tid].gone = 0;
     mbar_fence_init();
+    // programmatic dependent launch: what came before is done from here on, and
+    // the join may be set up while this kernel drains
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the cut: sums over all requests, each thread a run of them
@@ -357,22 +610,24 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     if (lane == 31) scan_part[warp] = inc;
     __syncthreads();
     long long base = 0, N = 0;
+#pragma unroll
     for (int i = 0; i <= C::WARPS; ++i) {
         if (i == warp) base = N;
         N += scan_part[i];
     }
     const Cut cut = make_cut(N, gridDim.x, C::WARPS);
     {
+        // the request in which each of this block's runs begins
         long long x = base + inc - mine;
-        const int w0 = blockIdx.x * cut.A, w1 = min(w0 + cut.A, cut.W);
-        if (w0 < w1 && x < cut.start(w1) && x + mine > cut.start(w0)) {
+        const long long s0 = cut.start(blockIdx.x, 0), s1 = cut.start(blockIdx.x, cut.A);
+        if (mine > 0 && x < s1 && x + mine > s0) {
             for (int r = r0; r < r1; ++r) {
-                const long long n = req_work(load_req(a, r, log_group), n_kv);
-                for (int w = w0; w < w1; ++w) {
-                    const long long s = cut.start(w);
+                const long long n = per == 1 ? mine : req_work(load_req(a, r, log_group), n_kv);
+                for (int i = 0; i < cut.A; ++i) {
+                    const long long s = cut.start(blockIdx.x, i);
                     if (x <= s && s < x + n) {
-                        start_r[w - w0] = r;
-                        start_x[w - w0] = x;
+                        start_r[i] = r;
+                        start_x[i] = x;
                     }
                 }
                 x += n;
@@ -382,56 +637,74 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     __syncthreads();
 
     if (warp == C::WARPS) {
-        // ---- the copying warp: lane w walks the run of warp w, up to S groups ahead of it
-        const int wid = blockIdx.x * cut.A + lane;
+        // ---- the copying warp: lane w walks the run of warp w, up to S tiles ahead of it.
+        // (A walk costs a warp registers that it needs for O.) The copy instruction takes
+        // one lane at a time, about 140 cycles each: a tile has one where its page has room.
         int left = 0;  // groups to copy
         int r = 0, unit = 0, units = 1, rgs = 1, ci = 0, cn = 1, ns = 0, skip = 0, head = 0;
+        bool any = false;
         const int32_t *table = a.pages.table;
         auto enter = [&](const Req &q) {
             cn = max(q.ng, 1);
-            ns = q.ng > 0 ? q.ns : -1;  // -1: nothing to read
+            any = q.ng > 0;
+            ns = q.ns;
             skip = q.skip;
             rgs = q.rgs;
             units = q.rgs * n_kv;
             table = a.pages.table + static_cast<size_t>(r) * a.pages.max_pages;
         };
-        if (lane < cut.A && wid < cut.W && N > 0) {
-            const long long x0 = cut.start(wid);
-            left = static_cast<int>(cut.start(wid + 1) - x0);
-            r = start_r[lane];
-            enter(load_req(a, r, log_group));
-            const long long off = x0 - start_x[lane];
-            unit = static_cast<int>(off / cn);
-            ci = static_cast<int>(off - static_cast<long long>(unit) * cn);
-            head = unit / rgs * a.pages.groups;
+        if (lane < cut.A && blockIdx.x < cut.B) {
+            const long long x0 = cut.start(blockIdx.x, lane);
+            left = static_cast<int>(cut.start(blockIdx.x, lane + 1) - x0);
+            if (left > 0) {
+                r = start_r[lane];
+                enter(load_req(a, r, log_group));
+                const long long off = x0 - start_x[lane];
+                unit = static_cast<int>(quotient(off, cn));
+                ci = static_cast<int>(off - static_cast<long long>(unit) * cn);
+                head = unit / rgs * a.pages.groups;
+            }
         }
-        int stage = 0, lap = 0, page = 0, group = 0;
-        auto look = [&]() {  // the table entry of the next group, one step before its copy
+        int page = 0, group = 0, made = 0, stage = 0;
+        auto look = [&]() {  // the table entry of the next tile, one step before its copy
             group = ci < ns ? ci : ci + skip;
-            page = ns >= 0 ? __ldg(table + (group >> a.pages.group_shift)) : -2;
-            group = (group & (a.pages.groups - 1)) + head;
+            page = any ? __ldg(table + (group >> a.pages.group_shift)) : -2;
         };
         if (left > 0) look();
+        volatile Piece *its = pieces + min(lane, C::WARPS - 1);
         long long t0 = clock64();
         while (__any_sync(~0u, left > 0)) {
-            bool went = false;
-            uint64_t *bar = full + lane * S + stage;
-            if (left > 0 && (lap == 0 || mbar_try_wait(empty + lane * S + stage, (lap - 1) & 1))) {
-                went = true;
-                if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages.n_pages)) {
-                    dead[lane * S + stage] = 0;
-                    mbar_arrive_expect_tx(bar, C::GB);
-                    bulk_copy_g2s(smem + lane * C::RING + stage * C::GB,
-                                  a.pages.base + (static_cast<size_t>(page) * page_groups + group) * C::GB,
-                                  C::GB, bar);
-                } else {
-                    dead[lane * S + stage] = 1;
-                    mbar_arrive(bar);
-                    if (page != -2) flag_error(a.err, FA_ERRBIT_DEVICE);
+            const bool went = left > 0 && made - its->gone < S;
+            if (went) {
+                const int n = tile_size<C::TILE>(ci, min(cn, ci + left), ns, skip);
+                uint32_t holes = 0;
+                uint64_t *bar = full + lane * S + stage;
+                uint8_t *dst = smem + lane * C::RING + stage * C::STAGE;
+                // the tile's pages: one if pages have TILE groups or more, else up to TILE
+                for (int k = 0;;) {
+                    const int sub = group & (a.pages.groups - 1);
+                    const int run = min(n - k, a.pages.groups - sub);
+                    if (static_cast<unsigned>(page) < static_cast<unsigned>(a.pages.n_pages)) {
+                        mbar_expect_tx(bar, run * C::GB);
+                        bulk_copy_g2s(dst + k * C::GB,
+                                      a.pages.base + (static_cast<size_t>(page) * page_groups + head + sub) * C::GB,
+                                      run * C::GB, bar);
+                    } else {  // no rows: rows of no request, or a bad entry of the table
+                        holes |= ((1u << run) - 1u) << k;
+                        if (page != -2) flag_error(a.err, FA_ERRBIT_DEVICE);
+                    }
+                    k += run;
+                    if (k == n) break;
+                    group += run;
+                    page = __ldg(table + (group >> a.pages.group_shift));
                 }
-                if (++stage == S) stage = 0, ++lap;
-                if (--left > 0) {
-                    if (++ci == cn) {
+                dead[lane * S + stage] = holes;
+                if (holes) its->holes = 1;
+                mbar_arrive(bar);
+                if (++stage == S) stage = 0;
+                ++made;
+                if ((left -= n) > 0) {
+                    if ((ci += n) == cn) {
                         ci = 0;
                         if (++unit == units) {
                             unit = 0;
@@ -462,24 +735,27 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     State<NB> st;
     st.clear();
     if (warp < C::WARPS) {
-        const int wid = blockIdx.x * cut.A + warp;
         if (lane == 0) {
             ws.tasks[blockIdx.x * C::WARPS + warp].valid = 0;
             pc->fin_unit = -1;
             pc->todo = 0;
-            if (warp < cut.A && wid < cut.W && N > 0) {
-                const long long x0 = cut.start(wid), off = x0 - start_x[warp];
-                const int n = max(load_req(a, start_r[warp], log_group).ng, 1);
-                const int unit = static_cast<int>(off / n);
-                pc->r = start_r[warp];
-                pc->unit = unit;
-                pc->gi = static_cast<int>(off - static_cast<long long>(unit) * n);
-                pc->todo = static_cast<int>(cut.start(wid + 1) - x0);
+            if (warp < cut.A) {
+                const long long x0 = cut.start(blockIdx.x, warp);
+                const int todo = static_cast<int>(cut.start(blockIdx.x, warp + 1) - x0);
+                if (todo > 0) {
+                    const long long off = x0 - start_x[warp];
+                    const int n = max(load_req(a, start_r[warp], log_group).ng, 1);
+                    const int unit = static_cast<int>(quotient(off, n));
+                    pc->r = start_r[warp];
+                    pc->unit = unit;
+                    pc->gi = static_cast<int>(off - static_cast<long long>(unit) * n);
+                    pc->todo = todo;
+                }
             }
         }
         __syncwarp();
         // ---- the run, piece by piece
-        int stage = 0;
+        int stage = 0, tiles = 0;  // tiles: done
         uint32_t phase = 0;
         bool ok = true;
 #pragma unroll 1
@@ -487,24 +763,25 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             int gi = pc->gi, g_end, f0, f1;
             float km[2];
             {
-            const Req q = load_req(a, pc->r, log_group);
-            const int n = max(q.ng, 1), unit = pc->unit;
-            const int h = unit / q.rgs, rg = unit - h * q.rgs;
-            g_end = min(n, gi + pc->todo);
-            // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
-            // the second and fourth times 2^-4; brought to a maximum in [2^10, 2^11)
-            {
+                const Req q = load_req(a, pc->r, log_group);
+                const int n = max(q.ng, 1), unit = pc->unit;
+                const int h = unit / q.rgs, rg = unit - h * q.rgs;
+                g_end = min(n, gi + pc->todo);
+                // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
+                // the second and fourth times 2^-4; brought to a maximum in [2^10, 2^11)
                 const Col c = column(q, rg, g, h, log_group);
                 const T *src = static_cast<const T *>(a.q) + max(c.token, 0) * a.q_stride +
                                static_cast<long long>(c.head) * HD + 8 * t;
-                float x[8], top = 0.0f;
-                if (c.token >= 0) {
-#pragma unroll 4
-                    for (int b = 0; b < NB; ++b) {
-                        load8(src + 32 * b, x);
+                Raw8<T> raw[NB];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-                    }
+                for (int b = 0; b < NB; ++b) raw[b].load(src + 32 * b, c.token >= 0);
+                float top = 0.0f;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    float x[8];
+                    raw[b].get(x);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
                 }
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -517,244 +794,84 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                                   16777216.0f;  // 2^24
                 km[0] = __shfl_sync(~0u, mul, 8 * t);
                 km[1] = __shfl_sync(~0u, mul, 8 * t + 4);
-#pragma unroll 2
-                for (int b = 0; b < NB; ++b) {
-                    float sum = 0.0f;
-                    if (c.token >= 0) load8(src + 32 * b, x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        x[i] = c.token >= 0 ? x[i] * lift : 0.0f;
-                        sum += x[i];
-                    }
-                    sum += __shfl_xor_sync(~0u, sum, 1);
-                    sum += __shfl_xor_sync(~0u, sum, 2);
-                    // -8 * 2^-24 of columns 2 t, 2 t + 1 in the order of an accumulator
-                    sum *= -4.76837158203125e-7f;
-                    const float s0 = __shfl_sync(~0u, sum, 8 * t), s1 = __shfl_sync(~0u, sum, 8 * t + 4);
-                    if (g == 0)
-                        *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) = make_float4(s0, s1, s0, s1);
+                for (int b = 0; b < NB; ++b) {
+                    float x[8];
+                    raw[b].get(x);
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        hi[i] = pack_half2(x[i], x[i + 4]);
+                        const float u = x[i] * lift, v = x[i + 4] * lift, sc = i & 1 ? 0.0625f : 1.0f;
+                        hi[i] = pack_half2(u, v);
                         const float2 f = half2_f(hi[i]);
-                        const float sc = i & 1 ? 0.0625f : 1.0f;
                         if (i & 1) hi[i] = pack_half2(f.x * sc, f.y * sc);
-                        lo[i] = pack_half2((x[i] - f.x) * sc, (x[i + 4] - f.y) * sc);
+                        lo[i] = pack_half2((u - f.x) * sc, (v - f.y) * sc);
                     }
                     *reinterpret_cast<uint4 *>(qs + (b * 32 + lane) * 16) =
                         make_uint4(hi[0], hi[1], hi[2], hi[3]);
                     if (C::QSPLIT)
                         *reinterpret_cast<uint4 *>(qs + C::QF + (b * 32 + lane) * 16) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                    // -8 times the block's sum, where the accumulators start: "code -8" in every row
+                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
+                    mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
+                    if (C::QSPLIT) {
+                        mma(d, kM8a, kM8a, kM8b, kM8b, lo[0], lo[1]);
+                        mma(d, kM8a, kM8a, kM8b, kM8b, lo[2], lo[3]);
+                    }
+                    if (g == 0)
+                        *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) =
+                            make_float4(d[0], d[1], d[2], d[3]);
                 }
-            }
-            const int p_min = q.rows - q.nq + ((rg * kRows) >> log_group);
-            const int p_max = q.rows - q.nq +
-                              min(q.nq - 1, (rg * kRows + kRows - 1) >> log_group);
-            if (lane < kRows) pc->pos[lane] = column(q, rg, lane, h, log_group).pos;
-            if (lane == 0) {
-                pc->n = n;
-                pc->end = g_end;
-                pc->p_min = p_min;
-                pc->p_max = p_max;
-                pc->ns = q.ns;
-                pc->skip = q.skip;
-            }
-            // groups [f0, f1) of the unit are seen whole by every row
-            f0 = 0;
-            f1 = max(0, p_min + 1) / kGroupRows - q.skip;
-            if (a.win > 0)
-                f0 = max(q.ns, (max(-1, p_max - a.win) + kGroupRows) / kGroupRows - q.skip);
+                const int p_min = q.rows - q.nq + ((rg * kRows) >> log_group);
+                const int p_max = q.rows - q.nq +
+                                  min(q.nq - 1, (rg * kRows + kRows - 1) >> log_group);
+                if (lane < kRows) pc->pos[lane] = column(q, rg, lane, h, log_group).pos;
+                if (lane == 0) {
+                    pc->n = n;
+                    pc->end = g_end;
+                    pc->p_min = p_min;
+                    pc->p_max = p_max;
+                    pc->ns = q.ns;
+                    pc->skip = q.skip;
+                }
+                // groups [f0, f1) of the unit are seen whole by every row
+                f0 = 0;
+                f1 = max(0, p_min + 1) / kGroupRows - q.skip;
+                if (a.win > 0)
+                    f0 = max(q.ns, (max(-1, p_max - a.win) + kGroupRows) / kGroupRows - q.skip);
             }
             __syncwarp();
             st.clear();
 
 #pragma unroll 1
-            for (; gi < g_end; ++gi) {
-                uint64_t *bar = full + warp * S + stage;
-                if (ok) ok = mbar_wait(bar, phase, &abort_flag, a.err);
-                if (ok && !dead[warp * S + stage]) {
-                    const uint8_t *kp = ring + stage * C::GB, *vp = kp + part_bytes(HD);
-                    // ---- scores of rows g, g + 8 (y[0..1], y[2..3]) and columns 2 t, 2 t + 1
-                    float y[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    // codes of rows g, g + 8 and their block scales, 4 blocks (2 of head_dim 64)
-                    // at a time: with all of a group's at once the registers do not suffice
-                    constexpr int KB = NB < 4 ? NB : 4;
-                    uint32_t wAs[KB], wBs[KB], sA[KB / 2], sB[KB / 2];
+            while (gi < g_end) {
+                const int n = tile_size<C::TILE>(gi, g_end, pc->ns, pc->skip);
+                uint8_t *kp = ring + stage * C::STAGE;
+                if (ok) ok = mbar_wait(bars + stage, phase, &abort_flag, a.err);
+                if (ok) {
+                    const uint32_t holes = pc->holes ? dead[warp * S + stage] : 0u;
+                    if (n == C::TILE && !holes && gi >= f0 && gi + n <= f1) {
+                        uint8_t *tile[C::TILE];
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        if (b % KB == 0) {
-                            if (NB == 2) {
-                                const uint4 w = lds_v4(kp + lane * 16);
-                                wAs[0] = w.x; wAs[1] = w.y; wBs[0] = w.z; wBs[1] = w.w;
-                            } else {
-                                const uint4 w = lds_v4(kp + ((b / 4) * 32 + lane) * 16);
-                                const uint4 x = lds_v4(kp + (((NB + b) / 4) * 32 + lane) * 16);
-                                wAs[0] = w.x; wAs[1] = w.y; wAs[2 % KB] = w.z; wAs[3 % KB] = w.w;
-                                wBs[0] = x.x; wBs[1] = x.y; wBs[2 % KB] = x.z; wBs[3 % KB] = x.w;
-                            }
-                            lds_words<KB / 2>(sA, kp + scale_offset(HD) + g * (2 * NB) + 2 * b);
-                            lds_words<KB / 2>(sB, kp + scale_offset(HD) + (g + 8) * (2 * NB) + 2 * b);
-                        }
-                        const uint4 qf = lds_v4(qs + (b * 32 + lane) * 16);
-                        const float4 c0 = lds_f4(bias + (b * 4 + t) * 16);
-                        float d[4] = {c0.x, c0.y, c0.z, c0.w};
-                        const uint32_t wA = wAs[b % KB], wB = wBs[b % KB];
-                        const uint32_t vA = wA >> 8, vB = wB >> 8;
-                        const uint32_t e0 = wA & 0x000f000fu, e1 = wB & 0x000f000fu;
-                        const uint32_t e2 = wA & 0x00f000f0u, e3 = wB & 0x00f000f0u;
-                        const uint32_t f0 = vA & 0x000f000fu, f1 = vB & 0x000f000fu;
-                        const uint32_t f2 = vA & 0x00f000f0u, f3 = vB & 0x00f000f0u;
-                        mma(d, e0, e1, e2, e3, qf.x, qf.y);
-                        mma(d, f0, f1, f2, f3, qf.z, qf.w);
-                        if (C::QSPLIT) {
-                            const uint4 lo = lds_v4(qs + C::QF + (b * 32 + lane) * 16);
-                            mma(d, e0, e1, e2, e3, lo.x, lo.y);
-                            mma(d, f0, f1, f2, f3, lo.z, lo.w);
-                        }
-                        const float2 uA = half2_f(sA[b % KB / 2]), uB = half2_f(sB[b % KB / 2]);
-                        const float a0 = b & 1 ? uA.y : uA.x, a1 = b & 1 ? uB.y : uB.x;
-                        y[0] = fmaf(a0, d[0], y[0]);
-                        y[1] = fmaf(a0, d[1], y[1]);
-                        y[2] = fmaf(a1, d[2], y[2]);
-                        y[3] = fmaf(a1, d[3], y[3]);
-                    }
-                    const uint16_t *kf = reinterpret_cast<const uint16_t *>(kp + factor_offset(HD));
-                    const uint16_t *vf = reinterpret_cast<const uint16_t *>(vp + factor_offset(HD));
-                    const float fA = __uint_as_float(static_cast<uint32_t>(kf[g]) << 16);
-                    const float fB = __uint_as_float(static_cast<uint32_t>(kf[g + 8]) << 16);
-                    const int xA = vf[g] >> 7, xB = vf[g + 8] >> 7;  // biased exponents of V's factors
-                    const float eA = static_cast<float>(xA - 127), eB = static_cast<float>(xB - 127);
-                    float iA = __uint_as_float(static_cast<uint32_t>(254 - xA) << 23);
-                    float iB = __uint_as_float(static_cast<uint32_t>(254 - xB) << 23);
-                    y[0] = fmaf(y[0] * fA, km[0], eA);
-                    y[1] = fmaf(y[1] * fA, km[1], eA);
-                    y[2] = fmaf(y[2] * fB, km[0], eB);
-                    y[3] = fmaf(y[3] * fB, km[1], eB);
-                    if (gi < f0 || gi >= f1) {
-                        const int j0 = (gi < pc->ns ? gi : gi + pc->skip) * kGroupRows;
-                        const int p0 = pc->pos[2 * t], p1 = pc->pos[2 * t + 1];
-                        const int p_min = pc->p_min, p_max = pc->p_max;
-                        // rows that no query sees may hold anything: their scales and
-                        // sums must not reach a product, not even with a zero
-                        auto seen = [&](int j) {
-                            return j <= p_max && (a.win <= 0 || j < a.sink || j > p_min - a.win);
-                        };
-                        const int jA = j0 + g, jB = jA + 8;
-                        if (!key_visible(p0, jA, a.sink, a.win)) y[0] = -INFINITY;
-                        if (!key_visible(p1, jA, a.sink, a.win)) y[1] = -INFINITY;
-                        if (!key_visible(p0, jB, a.sink, a.win)) y[2] = -INFINITY;
-                        if (!key_visible(p1, jB, a.sink, a.win)) y[3] = -INFINITY;
-                        if (!seen(jA)) iA = 0.0f;
-                        if (!seen(jB)) iB = 0.0f;
-                        const int k0 = j0 + 2 * t;
-                        const uint32_t m01 = (seen(k0) ? 0xffffu : 0u) | (seen(k0 + 1) ? 0xffff0000u : 0u);
-                        const uint32_t m23 = (seen(k0 + 8) ? 0xffffu : 0u) | (seen(k0 + 9) ? 0xffff0000u : 0u);
-                        if (g < NB / 2) {  // V's scales of rows 2t, 2t+1 | 2t+8, 2t+9 and two blocks
-                            uint4 *w = reinterpret_cast<uint4 *>(ring + stage * C::GB + part_bytes(HD) +
-                                                                 scale_offset(HD) + (g * 4 + t) * 16);
-                            *w = make_uint4(w->x & m01, w->y & m23, w->z & m01, w->w & m23);
-                        }
-                        fence_proxy_async_smem();  // before the next copy into the stage
-                        __syncwarp();
-                    }
-                    // ---- weights relative to the reference
-                    float d0 = y[0] - st.m[0], d1 = y[1] - st.m[1], d2 = y[2] - st.m[0],
-                          d3 = y[3] - st.m[1];
-                    if (__any_sync(~0u, fmaxf(fmaxf(d0, d1), fmaxf(d2, d3)) > kMost)) {
-                        float u0 = fmaxf(y[0], y[2]), u1 = fmaxf(y[1], y[3]);
-#pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) {
-                            u0 = fmaxf(u0, __shfl_xor_sync(~0u, u0, d));
-                            u1 = fmaxf(u1, __shfl_xor_sync(~0u, u1, d));
-                        }
-                        const float n0 = u0 - st.m[0] > kMost ? u0 - kLift : st.m[0];
-                        const float n1 = u1 - st.m[1] > kMost ? u1 - kLift : st.m[1];
-                        const float c0 = ex2(st.m[0] - n0), c1 = ex2(st.m[1] - n1);
-                        st.m[0] = n0;
-                        st.m[1] = n1;
-                        st.l[0] *= c0;
-                        st.l[1] *= c1;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                st.o[b][i][0] *= c0;
-                                st.o[b][i][1] *= c1;
-                                st.o[b][i][2] *= c0;
-                                st.o[b][i][3] *= c1;
-                            }
-                        d0 = y[0] - n0;
-                        d1 = y[1] - n1;
-                        d2 = y[2] - n0;
-                        d3 = y[3] - n1;
-                    }
-                    d0 = ex2(d0);
-                    d1 = ex2(d1);
-                    d2 = ex2(d2);
-                    d3 = ex2(d3);
-                    st.l[0] += fmaf(d0, iA, d2 * iB);
-                    st.l[1] += fmaf(d1, iA, d3 * iB);
-                    const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
-                    const uint32_t b0 = movmatrix_trans(hA), b1 = movmatrix_trans(hB);
-                    uint32_t l0 = 0, l1 = 0;
-                    if (C::PSPLIT) {
-                        const float2 rA = half2_f(hA), rB = half2_f(hB);
-                        l0 = movmatrix_trans(pack_half2(d0 - rA.x, d1 - rA.y));
-                        l1 = movmatrix_trans(pack_half2(d2 - rB.x, d3 - rB.y));
-                    }
-                    // ---- O += V^T P
-                    uint32_t vw[2 * NB];
-                    uint4 vs;
-#pragma unroll
-                    for (int c = 0; c < NB / 2; ++c) {
-                        const uint4 w = lds_v4(vp + (c * 32 + lane) * 16);
-                        vw[4 * c] = w.x; vw[4 * c + 1] = w.y; vw[4 * c + 2] = w.z; vw[4 * c + 3] = w.w;
-                    }
-                    constexpr uint32_t kM8a = 0x80088008u, kM8b = 0x80808080u;  // -8 * 2^-24, -8 * 2^-20
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
-                        const uint32_t x01 = __byte_perm(vw[b / 2], vw[(NB + b) / 2], sel);
-                        const uint32_t x23 = __byte_perm(vw[(2 * NB + b) / 2], vw[(3 * NB + b) / 2], sel);
-                        const uint32_t z01 = x01 >> 8, z23 = x23 >> 8;
-                        if (b % 2 == 0) vs = lds_v4(vp + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
-                        const uint32_t s01 = b & 1 ? vs.z : vs.x, s23 = b & 1 ? vs.w : vs.y;
-                        const uint32_t w0 = hmul2(b0, s01), w1 = hmul2(b1, s23);
-                        const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
-                        const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
-                        const uint32_t f0 = z01 & 0x000f000fu, f1 = z01 & 0x00f000f0u;
-                        const uint32_t f2 = z23 & 0x000f000fu, f3 = z23 & 0x00f000f0u;
-                        if (C::PSPLIT) {
-                            const uint32_t v0 = hfma2(l0, s01, hfma2(b0, s01, w0 ^ 0x80008000u));
-                            const uint32_t v1 = hfma2(l1, s23, hfma2(b1, s23, w1 ^ 0x80008000u));
-                            // c - 8 exactly: the tensor core's sums lose a step towards zero per
-                            // addition, which an offset taken out afterwards would leave behind
-                            float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                            const uint32_t g0 = hadd2(e0, kM8a), g1 = hadd2(e1, kM8b);
-                            const uint32_t g2 = hadd2(e2, kM8a), g3 = hadd2(e3, kM8b);
-                            mma(u, g0, g1, g2, g3, w0, w1);
-                            mma(u, g0, g1, g2, g3, v0, v1);
-                            const uint32_t h0 = hadd2(f0, kM8a), h1 = hadd2(f1, kM8b);
-                            const uint32_t h2 = hadd2(f2, kM8a), h3 = hadd2(f3, kM8b);
-                            mma(v, h0, h1, h2, h3, w0, w1);
-                            mma(v, h0, h1, h2, h3, v0, v1);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                st.o[b][0][i] += u[i];
-                                st.o[b][1][i] += v[i];
-                            }
-                        } else {
-                            mma(st.o[b][0], e0, e1, e2, e3, w0, w1);
-                            mma(st.o[b][1], f0, f1, f2, f3, w0, w1);
-                            mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
-                            mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
+                        for (int k = 0; k < C::TILE; ++k) tile[k] = kp + k * C::GB;
+                        step<C, C::TILE, false>(st, tile, qs, bias, km[0], km[1], pc, 0, a.sink, a.win);
+                    } else {
+#pragma unroll 1
+                        for (int k = 0; k < n; ++k) {
+                            if (holes >> k & 1) continue;
+                            const int i = gi + k;
+                            uint8_t *const one[1] = {kp + k * C::GB};
+                            step<C, 1, true>(st, one, qs, bias, km[0], km[1], pc,
+                                             (i < pc->ns ? i : i + pc->skip) * kGroupRows, a.sink, a.win);
                         }
                     }
                 }
                 __syncwarp();  // every lane has read the stage
-                if (ok && lane == 0) mbar_arrive(bar + C::WARPS * S);
+                gi += n;
+                ++tiles;
+                if (lane == 0) pc->gone = tiles;
                 if (++stage == S) stage = 0, phase ^= 1;
             }
 
@@ -762,25 +879,19 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             st.sum_lanes();
             const int r = pc->r, unit = pc->unit, n = pc->n, first = pc->gi, end = pc->end;
             const int todo = pc->todo - (end - first);
-            const int wid = blockIdx.x * cut.A + warp;
-            const Req q = load_req(a, r, log_group);
             if (first == 0 && end == n) {
+                const Req q = load_req(a, r, log_group);
                 const int h = unit / q.rgs, rg = unit - h * q.rgs;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const Col col = column(q, rg, 2 * t + c, h, log_group);
-                    if (col.token < 0) continue;
-                    const float inv = st.l[c] > 0.0f ? 1.0f / st.l[c] : st.l[c];
-                    T *dst = static_cast<T *>(a.out) + col.token * a.out_stride +
-                             static_cast<long long>(col.head) * HD + 4 * g;
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) store4<T>(dst + 32 * b, scaled(st.quad(b, c), inv));
-                    if (a.lse && g == 0)
-                        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] =
-                            (st.m[c] + log2f(st.l[c])) * kLn2;
+                    for (int b = 0; b < NB; ++b)
+                        write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(b, c), st.m[c], st.l[c]);
                 }
             } else if (todo > 0) {  // the start of the run: to the workspace
-                float *dst = ws.partial + (static_cast<size_t>(wid) * 2 + 1) * C::PARTIAL;
+                float *dst = ws.partial +
+                             (static_cast<size_t>(blockIdx.x * cut.A + warp) * 2 + 1) * C::PARTIAL;
                 if (g == 0) {
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
@@ -810,20 +921,23 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             }
             __syncwarp();
             if (lane == 0) {
-                if (todo == 0 && !(first == 0 && end == n)) {
+                if (todo > 0) {
+                    const Req q = load_req(a, r, log_group);
+                    int next = unit + 1, nr = r;
+                    if (next == q.rgs * n_kv) {
+                        next = 0;
+                        while (load_req(a, ++nr, log_group).rgs == 0) {}
+                    }
+                    pc->r = nr;
+                    pc->unit = next;
+                    pc->gi = 0;
+                } else if (first > 0 || end < n) {
+                    const long long x1 = cut.start(blockIdx.x, warp + 1);
                     pc->fin_r = r;
                     pc->fin_unit = unit;
-                    pc->fin_first = cut.start(wid + 1) - end;
-                    pc->fin_last = cut.start(wid + 1) - end + n;
+                    pc->fin_first = x1 - end;
+                    pc->fin_last = x1 - end + n;
                 }
-                int next = unit + 1, nr = r;
-                if (todo > 0 && next == q.rgs * n_kv) {
-                    next = 0;
-                    while (load_req(a, ++nr, log_group).rgs == 0) {}
-                }
-                pc->r = nr;
-                pc->unit = next;
-                pc->gi = 0;
                 pc->todo = todo;
             }
             __syncwarp();
@@ -844,20 +958,27 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     int w0 = warp, w1 = warp + 1;  // warps [w0, w1) hold pieces of this unit
     while (w0 > 0 && same(w0 - 1)) --w0;
     while (w1 < C::WARPS && same(w1)) ++w1;
-    const int id0 = blockIdx.x * cut.A + w0, id1 = blockIdx.x * cut.A + w1;
-    const bool from_start = cut.start(id0) <= first, direct = from_start && cut.start(id1) >= last;
-    float M[2] = {kLowest, kLowest}, L[2] = {0.0f, 0.0f};
+    const int id0 = blockIdx.x * cut.A + w0;
+    const bool from_start = cut.start(blockIdx.x, w0) <= first;
+    const bool direct = from_start && cut.start(blockIdx.x, w1) >= last;
+    const Req q = load_req(a, r, log_group);
+    const int h = unit / q.rgs, rg = unit - h * q.rgs;
+    float M[2], L[2];  // of columns 2 t, 2 t + 1
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int n = 2 * t + c;
-        for (int w = w0; w < w1; ++w) M[c] = fmaxf(M[c], pieces[w].m[n]);
-        for (int w = w0; w < w1; ++w) L[c] += pieces[w].l[n] * ex2(pieces[w].m[n] - M[c]);
+        M[c] = kLowest;
+        L[c] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w)
+            if (w >= w0 && w < w1) M[c] = fmaxf(M[c], pieces[w].m[n]);
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w)
+            if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], ex2(pieces[w].m[n] - M[c]), L[c]);
     }
-    const Req q = load_req(a, r, log_group);
-    const int h = unit / q.rgs, rg = unit - h * q.rgs;
     float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
     if (from_start && !direct && warp == w0 && lane == 0)
-        ws.tasks[blockIdx.x * C::WARPS + warp] = Task{1, r, unit, id0, first, last, cut.N, cut.W, cut.A};
+        ws.tasks[blockIdx.x * C::WARPS + warp] = Task{1, r, unit, id0, first, last, cut};
     if (!direct && warp == w0 && g == 0) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -867,93 +988,114 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
     for (int i = warp - w0; i < 2 * NB; i += w1 - w0) {  // (block, column) pairs
         const int b = i >> 1, c = i & 1;
+        const float top = c ? M[1] : M[0];
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int w = w0; w < w1; ++w) {
+#pragma unroll
+        for (int w = 0; w < C::WARPS; ++w) {
+            if (w < w0 || w >= w1) continue;
             const float4 y = *reinterpret_cast<const float4 *>(smem + w * C::RING + (i * 32 + lane) * 16);
-            const float f = ex2(pieces[w].m[2 * t + c] - M[c]);
+            const float f = ex2(pieces[w].m[2 * t + c] - top);
             x.x = fmaf(y.x, f, x.x);
             x.y = fmaf(y.y, f, x.y);
             x.z = fmaf(y.z, f, x.z);
             x.w = fmaf(y.w, f, x.w);
         }
-        if (direct) {
-            const Col col = column(q, rg, 2 * t + c, h, log_group);
-            if (col.token < 0) continue;
-            const float inv = L[c] > 0.0f ? 1.0f / L[c] : L[c];
-            store4<T>(static_cast<T *>(a.out) + col.token * a.out_stride +
-                          static_cast<long long>(col.head) * HD + 32 * b + 4 * g, scaled(x, inv));
-            if (a.lse && g == 0 && b == 0)
-                a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] =
-                    (M[c] + log2f(L[c])) * kLn2;
-        } else {
+        if (direct)
+            write_row<T>(a, column(q, rg, 2 * t + c, h, log_group), HD, 32 * b + 4 * g, x, top,
+                         c ? L[1] : L[0]);
+        else
             *reinterpret_cast<float4 *>(dst + 2 * kRows + (i * 32 + lane) * 4) = x;
-        }
     }
 }
 
-// One block per warp of the first kernel: the pieces of the unit that begins
-// in its run, in ascending order.
-constexpr int kJoinThreads = 128;
+// One block for each of the first kernel: the units that begin in its runs and
+// that it could not finish. A warp takes one (unit, block of 32 dims, column
+// half) after another; a unit's pieces are added in ascending order.
+constexpr int kJoinThreads = 512;
 template <typename T, int HD>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs a, int blocks) {
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs a) {
     using C = Cfg<T, HD>;
+    constexpr int ITEMS = 2 * C::NB, BATCH = 8;
+    __shared__ Task tasks[C::WARPS];
+    __shared__ int n_tasks;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Ws ws = carve(a.workspace, blocks);
-    const Task k = ws.tasks[blockIdx.x];
-    if (!k.valid) return;
-    const int w0 = k.w;
-    Cut cut;
-    cut.N = k.N;
-    cut.W = k.W;
-    cut.A = k.A;
-    // pieces: the joined one of each block from w0's on, and the last warp's
-    // first piece if its run goes on past the unit
-    int w1 = w0;  // the warp that holds the unit's last group
-    {
-        int lo = w0, hi = k.W;  // the last w with start(w) < last
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cut.start(mid) < k.last) lo = mid; else hi = mid;
-        }
-        w1 = lo;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const Ws ws = carve(a.workspace, gridDim.x);
+    if (threadIdx.x < 32) {
+        const int i = threadIdx.x;
+        const Task *k = ws.tasks + blockIdx.x * C::WARPS + i;
+        const bool valid = i < C::WARPS && k->valid;
+        const unsigned all = __ballot_sync(~0u, valid);
+        if (valid) tasks[__popc(all & ((1u << i) - 1u))] = *k;
+        if (i == 0) n_tasks = __popc(all);
     }
-    const bool tail = cut.start(w1 + 1) > k.last;
-    const int b0 = w0 / k.A, b1 = (tail ? w1 - 1 : w1) / k.A;
-    const int pieces = b1 - b0 + 1 + (tail ? 1 : 0);
-    auto piece = [&](int i) {
-        const size_t slot = i > b1 - b0 ? static_cast<size_t>(w1) * 2 + 1
-                            : i == 0    ? static_cast<size_t>(w0) * 2
-                                        : static_cast<size_t>(b0 + i) * k.A * 2;
-        return ws.partial + slot * C::PARTIAL;
-    };
+    __syncthreads();
     const int log_group = 31 - __clz(a.n_q_heads / a.pages.n_kv);
-    const Req q = load_req(a, k.r, log_group);
-    const int h = k.unit / q.rgs, rg = k.unit - h * q.rgs;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    for (int i = threadIdx.x >> 5; i < 2 * C::NB; i += kJoinThreads / 32) {
-        const int b = i >> 1, n = 2 * t + (i & 1);
+    for (int j = threadIdx.x >> 5; j < n_tasks * ITEMS; j += kJoinThreads / 32) {
+        const Task &k = tasks[j / ITEMS];
+        const int i = j % ITEMS, b = i >> 1, n = 2 * t + (i & 1);
+        const Cut &cut = k.cut;
+        // pieces: the joined one of each block from k.w's on, and the last warp's first
+        // piece if its run goes on past the unit
+        const int w1 = cut.warp_of(k.last - 1);  // the warp that holds the unit's last group
+        const bool tail = cut.start(w1 / cut.A, w1 % cut.A + 1) > k.last;
+        const int b0 = k.w / cut.A, b1 = (tail ? w1 - 1 : w1) / cut.A;
+        const int pieces = b1 - b0 + 1 + (tail ? 1 : 0);
+        auto piece = [&](int e) {
+            const int slot = e > b1 - b0 ? w1 * 2 + 1 : e == 0 ? k.w * 2 : (b0 + e) * cut.A * 2;
+            return ws.partial + static_cast<size_t>(slot) * C::PARTIAL;
+        };
         float M = kLowest, L = 0.0f;
-        for (int e = 0; e < pieces; ++e) M = fmaxf(M, piece(e)[n]);
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-        for (int e = 0; e < pieces; ++e) {
-            const float *p = piece(e);
-            const float f = ex2(p[n] - M);
-            const float4 y = *reinterpret_cast<const float4 *>(p + 2 * kRows + (i * 32 + lane) * 4);
-            L = fmaf(p[kRows + n], f, L);
-            x.x = fmaf(y.x, f, x.x);
-            x.y = fmaf(y.y, f, x.y);
-            x.z = fmaf(y.z, f, x.z);
-            x.w = fmaf(y.w, f, x.w);
+        for (int e0 = 0; e0 < pieces; e0 += BATCH) {
+            float m[BATCH], l[BATCH];
+            float4 y[BATCH];
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) {
+                const float *p = piece(min(e0 + e, pieces - 1));
+                m[e] = p[n];
+                l[e] = p[kRows + n];
+                y[e] = *reinterpret_cast<const float4 *>(p + 2 * kRows + (i * 32 + lane) * 4);
+            }
+            float top = M;
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) top = fmaxf(top, m[e]);
+            const float s = ex2(M - top);
+            M = top;
+            L *= s;
+            x = scaled(x, s);
+#pragma unroll
+            for (int e = 0; e < BATCH; ++e) {
+                if (e0 + e >= pieces) continue;
+                const float f = ex2(m[e] - top);
+                L = fmaf(l[e], f, L);
+                x.x = fmaf(y[e].x, f, x.x);
+                x.y = fmaf(y[e].y, f, x.y);
+                x.z = fmaf(y[e].z, f, x.z);
+                x.w = fmaf(y[e].w, f, x.w);
+            }
         }
-        const Col col = column(q, rg, n, h, log_group);
-        if (col.token < 0) continue;
-        const float inv = L > 0.0f ? 1.0f / L : L;
-        store4<T>(static_cast<T *>(a.out) + col.token * a.out_stride +
-                      static_cast<long long>(col.head) * HD + 32 * b + 4 * g, scaled(x, inv));
-        if (a.lse && g == 0 && b == 0)
-            a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (M + log2f(L)) * kLn2;
+        const Req q = load_req(a, k.r, log_group);
+        const int h = k.unit / q.rgs, rg = k.unit - h * q.rgs;
+        write_row<T>(a, column(q, rg, n, h, log_group), HD, 32 * b + 4 * g, x, M, L);
     }
+}
+
+template <typename K>
+cudaError_t launch_after(K *kernel, int blocks, int threads, size_t smem, cudaStream_t stream,
+                         const PagedAttnArgs &a) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename T, int HD>
@@ -961,22 +1103,12 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t stream) {
     using C = Cfg<T, HD>;
     cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, HD>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
     const int blocks = device_sm_count();
-    paged_attn_kernel<T, HD><<<blocks, C::THREADS, C::SMEM, stream>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // programmatic dependent launch: the join's blocks are set up while the
-    // first kernel drains, and wait for it at their start
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks * C::WARPS);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_join_kernel<T, HD>, a, blocks);
+    if (e == cudaSuccess)
+        e = launch_after(paged_attn_kernel<T, HD>, blocks, C::THREADS, C::SMEM, stream, a);
+    if (e == cudaSuccess)
+        e = launch_after(paged_join_kernel<T, HD>, blocks, kJoinThreads, 0, stream, a);
+    return e;
 }
 
 template <typename T>
