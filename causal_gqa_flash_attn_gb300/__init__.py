@@ -311,39 +311,69 @@ def decode_noalloc(q, k_planes, v_planes, pos, out, *, n_q_heads: int, n_kv_head
 
 
 # ----------------------------------------------------------- paged serving
+# These calls are made once per layer of a step that may take microseconds, so
+# their checks read each property of a tensor once.
 
-def _here(*tensors):
-    """The tensors are on the current device, where the call launches."""
-    here = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != here:
-            raise ValueError(f"every tensor must be on the current device, cuda:{here}; "
-                             f"got one on {t.device}")
+_I32, _U8, _F32 = torch.int32, torch.uint8, torch.float32
 
 
-def _heads(t: torch.Tensor, name: str, dtype=None):
+def _here(t: torch.Tensor, name: str) -> int:
+    """The index of t's device, which must be the current one: calls launch there."""
+    here = t.get_device()
+    if here < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if here != torch.cuda.current_device():
+        raise ValueError(f"{name} must be on the current device, "
+                         f"cuda:{torch.cuda.current_device()}, got {t.device}")
+    return here
+
+
+def _arg(t: torch.Tensor, name: str, dtype, shape, here: int) -> int:
+    """Pointer of a contiguous tensor of this dtype and shape (None: any) on device `here`."""
+    if (t.dtype is dtype and t.get_device() == here and (shape is None or t.shape == shape)
+            and t.is_contiguous()):
+        return t.data_ptr()
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on cuda:{here}, as the call's other tensors are, "
+                         f"got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _heads(t: torch.Tensor, name: str, dtype, shape, here: int):
     """(pointer, token stride) of a [tokens][heads][head_dim] tensor whose tokens
     may lie apart (a slice of a fused projection's output)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in _TYPES or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be {dtype or 'float32, float16 or bfloat16'}, got {t.dtype}")
-    tokens, heads, hd = t.shape
-    row = heads * hd
+    tokens, heads, hd = shape
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, got {t.dtype} of "
+                         f"{tuple(t.shape)}")
+    if t.get_device() != here:
+        raise ValueError(f"{name} must be on cuda:{here}, as the call's other tensors are, "
+                         f"got {t.device}")
     step, head, one = t.stride()
+    row = heads * hd
     if (one != 1 and hd > 1) or (head != hd and heads > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    if tokens > 1:
-        if step < row:
+    if step < row:
+        if tokens > 1:
             raise ValueError(f"{name}: tokens overlap")
-        return t.data_ptr(), step
-    return t.data_ptr(), max(step, row)
+        step = row
+    return t.data_ptr(), step
 
 
-def _ints(t: torch.Tensor, name: str, shape):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    return _dev(t, torch.int32, name)
+def _type(t: torch.Tensor, name: str) -> int:
+    code = _TYPES.get(t.dtype)
+    if code is None or t.dim() != 3:
+        raise ValueError(f"{name} must be float32, float16 or bfloat16 of shape (tokens, heads, "
+                         f"head_dim), got {t.dtype} of {tuple(t.shape)}")
+    return code
+
+
+def _raw_stream(stream, here: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(here) if stream is None else _stream(stream)
 
 
 def page_bytes(n_kv_heads: int, head_dim: int, page_rows: int) -> int:
@@ -359,12 +389,19 @@ def alloc_pages(n_pages: int, n_kv_heads: int, head_dim: int, page_rows: int,
     return torch.empty(n_pages * pb, dtype=torch.uint8, device=device)
 
 
-def _pages(pages, n_kv_heads: int, head_dim: int, page_rows: int):
+def _pages(pages, n_kv_heads: int, head_dim: int, page_rows: int, here: int):
     pb = lib().fa_page_bytes(n_kv_heads, head_dim, page_rows)
     n = pages.numel()
     if pb == 0 or n == 0 or n % pb:
         raise ValueError("pages is not a whole number of pages of this geometry")
-    return _dev(pages, torch.uint8, "pages"), n // pb
+    return _arg(pages, "pages", _U8, None, here), n // pb
+
+
+def _table(block_table, n_reqs: int, here: int):
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != n_reqs:
+        raise ValueError(f"block_table must have shape ({n_reqs}, max_pages), got {tuple(shape)}")
+    return _arg(block_table, "block_table", _I32, None, here), shape[1]
 
 
 def page_plan(cached, fresh, free_ring, ring_state, block_table, ring_state_out, seq_lens,
@@ -373,20 +410,19 @@ def page_plan(cached, fresh, free_ring, ring_state, block_table, ring_state_out,
     requests' lengths. All int32: cached, fresh, seq_lens [R], block_table
     [R][max_pages], free_ring [n_pages], ring_state [2], ring_state_out [3],
     cu_fresh [R + 1], slot_map and positions [max_tokens]."""
+    here = _here(cached, "cached")
     R, T = cached.numel(), slot_map.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
-                         f"{tuple(block_table.shape)}")
-    _here(cached, fresh, free_ring, ring_state, block_table, ring_state_out, seq_lens, cu_fresh,
-          slot_map, positions)
+    table, max_pages = _table(block_table, R, here)
     _check(lib().fa_page_plan(
-        _ints(cached, "cached", (R,)), _ints(fresh, "fresh", (R,)), R,
-        _dev(free_ring, torch.int32, "free_ring"), free_ring.numel(),
-        _ints(ring_state, "ring_state", (2,)), _ints(ring_state_out, "ring_state_out", (3,)),
-        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], page_rows,
-        _ints(seq_lens, "seq_lens", (R,)), _ints(cu_fresh, "cu_fresh", (R + 1,)),
-        _ints(slot_map, "slot_map", (T,)), _ints(positions, "positions", (T,)), T,
-        _stream(stream)), "fa_page_plan")
+        _arg(cached, "cached", _I32, (R,), here), _arg(fresh, "fresh", _I32, (R,), here), R,
+        _arg(free_ring, "free_ring", _I32, None, here), free_ring.numel(),
+        _arg(ring_state, "ring_state", _I32, (2,), here),
+        _arg(ring_state_out, "ring_state_out", _I32, (3,), here), table, max_pages, page_rows,
+        _arg(seq_lens, "seq_lens", _I32, (R,), here),
+        _arg(cu_fresh, "cu_fresh", _I32, (R + 1,), here),
+        _arg(slot_map, "slot_map", _I32, (T,), here),
+        _arg(positions, "positions", _I32, (T,), here), T, _raw_stream(stream, here)),
+        "fa_page_plan")
 
 
 def rope_table(inv_freq, sections=None, *, interleaved: bool = False,
@@ -413,68 +449,65 @@ def rope(q, k, q_out, k_out, positions, table, *, adjacent: bool = False, invers
     some = q if q is not None else k
     if some is None:
         raise ValueError("rope needs q or k")
+    if (q is None) != (q_out is None) or (k is None) != (k_out is None):
+        raise ValueError("q and q_out go together, and k and k_out")
+    here = _here(some, "q" if q is not None else "k")
+    code, dtype = _type(some, "q" if q is not None else "k"), some.dtype
     T, _, hd = some.shape
-    ptrs, strides, heads = [], [], []
-    for x, y, name in ((q, q_out, "q"), (k, k_out, "k")):
-        if (x is None) != (y is None):
-            raise ValueError(f"{name} and {name}_out go together")
-        if x is None:
-            ptrs += [None, None]
-            strides += [0, 0]
-            heads.append(0)
-            continue
-        if x.shape != y.shape or x.shape[0] != T or x.shape[2] != hd:
-            raise ValueError(f"{name} and {name}_out must have shape ({T}, heads, {hd})")
-        for t, what in ((x, name), (y, name + "_out")):
-            p, step = _heads(t, what, some.dtype)
-            ptrs.append(p)
-            strides.append(step)
-        heads.append(x.shape[1])
-    if positions.dim() == 1:
-        positions = positions.unsqueeze(0)
-    if positions.shape[1] != T:
-        raise ValueError(f"positions must have shape (n_axes, {T}), got {tuple(positions.shape)}")
-    if table.dim() != 2 or table.shape[1] != 4:
-        raise ValueError("table must come from rope_table")
-    _here(q, k, q_out, k_out, positions, table)
+    qp = qo = kp = ko = None
+    qs = qos = ks = kos = hq = hkv = 0
+    if q is not None:
+        hq = q.shape[1]
+        shape = (T, hq, hd)
+        qp, qs = _heads(q, "q", dtype, shape, here)
+        qo, qos = (qp, qs) if q_out is q else _heads(q_out, "q_out", dtype, shape, here)
+    if k is not None:
+        _type(k, "k")
+        hkv = k.shape[1]
+        shape = (T, hkv, hd)
+        kp, ks = _heads(k, "k", dtype, shape, here)
+        ko, kos = (kp, ks) if k_out is k else _heads(k_out, "k_out", dtype, shape, here)
+    where = positions.shape
+    axes = 1 if len(where) == 1 else where[0]
+    if len(where) > 2 or where[-1] != T:
+        raise ValueError(f"positions must have shape (n_axes, {T}), got {tuple(where)}")
+    pairs = table.shape[0]
     _check(lib().fa_rope(
-        *ptrs, _TYPES[some.dtype], T, *heads, hd, 2 * table.shape[0], *strides,
-        _dev(positions, torch.int32, "positions"), T, positions.shape[0],
-        _dev(table, torch.int32, "table"), adjacent, inverse, _stream(stream)), "fa_rope")
+        qp, qo, kp, ko, code, T, hq, hkv, hd, 2 * pairs, qs, qos, ks, kos,
+        _arg(positions, "positions", _I32, None, here), T, axes,
+        _arg(table, "table", _I32, (pairs, 4), here), adjacent, inverse,
+        _raw_stream(stream, here)), "fa_rope")
 
 
 def paged_append(k_new, v_new, slot_map, pages, *, page_rows: int, stream=None):
     """fa_paged_append: k_new, v_new [T][Hkv][hd] into the rows slot_map [T] int32."""
-    T, hkv, hd = k_new.shape
-    if v_new.shape != k_new.shape:
-        raise ValueError("k_new and v_new must have the same shape")
-    kp, ks = _heads(k_new, "k_new")
-    vp, vs = _heads(v_new, "v_new", k_new.dtype)
-    pp, n_pages = _pages(pages, hkv, hd, page_rows)
-    _here(k_new, v_new, slot_map, pages)
-    _check(lib().fa_paged_append(kp, vp, _TYPES[k_new.dtype], ks, vs,
-                                 _ints(slot_map, "slot_map", (T,)), T, pp, n_pages, hkv, hd,
-                                 page_rows, _stream(stream)), "fa_paged_append")
+    here = _here(k_new, "k_new")
+    code, dtype, shape = _type(k_new, "k_new"), k_new.dtype, k_new.shape
+    T, hkv, hd = shape
+    kp, ks = _heads(k_new, "k_new", dtype, shape, here)
+    vp, vs = _heads(v_new, "v_new", dtype, shape, here)
+    pp, n_pages = _pages(pages, hkv, hd, page_rows, here)
+    _check(lib().fa_paged_append(kp, vp, code, ks, vs, _arg(slot_map, "slot_map", _I32, (T,), here),
+                                 T, pp, n_pages, hkv, hd, page_rows, _raw_stream(stream, here)),
+           "fa_paged_append")
 
 
 def paged_gather(pages, block_table, seq_lens, k_planes, v_planes, *, n_kv_heads: int,
                  head_dim: int, page_rows: int, max_seq: int, stream=None):
     """fa_paged_gather: rows 0 .. seq_lens[r]-1 of each request into KV_F16 planes
     (uint8, one plane for each request)."""
+    here = _here(pages, "pages")
     R = seq_lens.numel()
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
-                         f"{tuple(block_table.shape)}")
     pb = lib().fa_kv_plane_bytes(KV_F16, n_kv_heads, max_seq, head_dim)
     if pb == 0 or k_planes.numel() != R * pb or v_planes.numel() != R * pb:
         raise ValueError("k_planes and v_planes must be one KV_F16 plane for each request")
-    pp, n_pages = _pages(pages, n_kv_heads, head_dim, page_rows)
-    _here(pages, block_table, seq_lens, k_planes, v_planes)
+    pp, n_pages = _pages(pages, n_kv_heads, head_dim, page_rows, here)
+    table, max_pages = _table(block_table, R, here)
     _check(lib().fa_paged_gather(
-        pp, n_pages, _dev(block_table, torch.int32, "block_table"), block_table.shape[1],
-        _ints(seq_lens, "seq_lens", (R,)), R, n_kv_heads, head_dim, page_rows,
-        _dev(k_planes, torch.uint8, "k_planes"), _dev(v_planes, torch.uint8, "v_planes"),
-        max_seq, _stream(stream)), "fa_paged_gather")
+        pp, n_pages, table, max_pages, _arg(seq_lens, "seq_lens", _I32, (R,), here), R,
+        n_kv_heads, head_dim, page_rows, _arg(k_planes, "k_planes", _U8, None, here),
+        _arg(v_planes, "v_planes", _U8, None, here), max_seq, _raw_stream(stream, here)),
+        "fa_paged_gather")
 
 
 def paged_attn_workspace_bytes(head_dim: int) -> int:
@@ -486,26 +519,20 @@ def paged_attn(q, out, cu_q, seq_lens, block_table, pages, *, n_kv_heads: int, p
                stream=None):
     """fa_paged_attn: q, out [T][Hq][hd] (tokens may lie apart), cu_q [R + 1] and
     seq_lens [R] int32, block_table [R][max_pages] int32, lse [Hq][T] fp32 or None."""
-    T, hq, hd = q.shape
+    here = _here(q, "q")
+    code, dtype, shape = _type(q, "q"), q.dtype, q.shape
+    T, hq, hd = shape
     R = seq_lens.numel()
-    if out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError(f"block_table must have shape ({R}, max_pages), got "
-                         f"{tuple(block_table.shape)}")
-    if lse is not None and lse.shape != (hq, T):
-        raise ValueError(f"lse must have shape ({hq}, {T}), got {tuple(lse.shape)}")
-    qp, qs = _heads(q, "q")
-    op, os_ = _heads(out, "out", q.dtype)
-    pp, n_pages = _pages(pages, n_kv_heads, hd, page_rows)
-    _here(q, out, cu_q, seq_lens, block_table, pages, lse, workspace)
+    qp, qs = _heads(q, "q", dtype, shape, here)
+    op, os_ = _heads(out, "out", dtype, shape, here)
+    pp, n_pages = _pages(pages, n_kv_heads, hd, page_rows, here)
+    table, max_pages = _table(block_table, R, here)
     _check(lib().fa_paged_attn(
-        qp, op, _dev(lse, torch.float32, "lse"), _TYPES[q.dtype], qs, os_,
-        _ints(cu_q, "cu_q", (R + 1,)), _ints(seq_lens, "seq_lens", (R,)),
-        _dev(block_table, torch.int32, "block_table"), block_table.shape[1], pp, n_pages,
-        page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale,
-        _dev(workspace, torch.uint8, "workspace"), workspace.numel(), _stream(stream)),
-        "fa_paged_attn")
+        qp, op, None if lse is None else _arg(lse, "lse", _F32, (hq, T), here), code, qs, os_,
+        _arg(cu_q, "cu_q", _I32, (R + 1,), here), _arg(seq_lens, "seq_lens", _I32, (R,), here),
+        table, max_pages, pp, n_pages, page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale,
+        _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
+        _raw_stream(stream, here)), "fa_paged_attn")
 
 
 def set_kernel_events(start, stop):

@@ -40,6 +40,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -165,9 +166,11 @@ __device__ __forceinline__ Cut make_cut(long long N, int blocks, int warps) {
 // A unit that other blocks share, for the join: written by the warp whose run
 // holds its first group.
 struct Task {
-    int valid, r, unit, w;  // w: that warp, counted over the blocks
-    long long first, last;  // its groups [first, last)
-    Cut cut;
+    int valid, h, rg;
+    int first, blocks, stride;  // partials of its joined pieces: `first`, and each later block's first
+    int tail;                   // and of the piece that begins the last warp's run, or -1
+    int next;                   // partial of the second block's piece
+    Req q;
 };
 struct Ws {
     Task *tasks;     // one per warp
@@ -615,6 +618,10 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         if (i == warp) base = N;
         N += scan_part[i];
     }
+    if (N >> 30 >= gridDim.x) {  // runs are counted in 31 bits (2^34 rows an SM)
+        if (tid == 0 && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
+        N = 0;
+    }
     const Cut cut = make_cut(N, gridDim.x, C::WARPS);
     {
         // the request in which each of this block's runs begins
@@ -623,13 +630,14 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         if (mine > 0 && x < s1 && x + mine > s0) {
             for (int r = r0; r < r1; ++r) {
                 const long long n = per == 1 ? mine : req_work(load_req(a, r, log_group), n_kv);
-                for (int i = 0; i < cut.A; ++i) {
-                    const long long s = cut.start(blockIdx.x, i);
-                    if (x <= s && s < x + n) {
+                // relative to the block's run: 31 bits
+                const long long lo = x - s0, hi = min(x + n, s1) - s0;
+                int s = 0;
+                for (int i = 0; i < cut.A; ++i, s += cut.cw)
+                    if (lo <= s && s < hi) {
                         start_r[i] = r;
                         start_x[i] = x;
                     }
-                }
                 x += n;
             }
         }
@@ -745,7 +753,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                 if (todo > 0) {
                     const long long off = x0 - start_x[warp];
                     const int n = max(load_req(a, start_r[warp], log_group).ng, 1);
-                    const int unit = static_cast<int>(quotient(off, n));
+                    const int unit = off < n ? 0 : static_cast<int>(quotient(off, n));
                     pc->r = start_r[warp];
                     pc->unit = unit;
                     pc->gi = static_cast<int>(off - static_cast<long long>(unit) * n);
@@ -954,31 +962,40 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     if (warp >= C::WARPS || pc->fin_unit < 0) return;
     const int r = pc->fin_r, unit = pc->fin_unit;
     const long long first = pc->fin_first, last = pc->fin_last;
-    auto same = [&](int w) { return pieces[w].fin_unit == unit && pieces[w].fin_r == r; };
-    int w0 = warp, w1 = warp + 1;  // warps [w0, w1) hold pieces of this unit
-    while (w0 > 0 && same(w0 - 1)) --w0;
-    while (w1 < C::WARPS && same(w1)) ++w1;
+    // warps [w0, w1) hold pieces of this unit: neighbours, as runs follow each other
+    const unsigned same = __ballot_sync(~0u, lane < C::WARPS && pieces[min(lane, C::WARPS - 1)].fin_unit == unit &&
+                                                 pieces[min(lane, C::WARPS - 1)].fin_r == r);
+    const int w0 = __ffs(same) - 1, w1 = 32 - __clz(same);
     const int id0 = blockIdx.x * cut.A + w0;
     const bool from_start = cut.start(blockIdx.x, w0) <= first;
     const bool direct = from_start && cut.start(blockIdx.x, w1) >= last;
     const Req q = load_req(a, r, log_group);
     const int h = unit / q.rgs, rg = unit - h * q.rgs;
-    float M[2], L[2];  // of columns 2 t, 2 t + 1
+    float M[2], L[2], f[2][C::WARPS];  // of columns 2 t, 2 t + 1
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
         const int n = 2 * t + c;
         M[c] = kLowest;
         L[c] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w)
-            if (w >= w0 && w < w1) M[c] = fmaxf(M[c], pieces[w].m[n]);
+        for (int w = 0; w < C::WARPS; ++w) {
+            f[c][w] = w >= w0 && w < w1 ? pieces[w].m[n] : kLowest;
+            M[c] = fmaxf(M[c], f[c][w]);
+        }
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w)
-            if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], ex2(pieces[w].m[n] - M[c]), L[c]);
+        for (int w = 0; w < C::WARPS; ++w) {
+            f[c][w] = ex2(f[c][w] - M[c]);
+            if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], f[c][w], L[c]);
+        }
     }
     float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
-    if (from_start && !direct && warp == w0 && lane == 0)
-        ws.tasks[blockIdx.x * C::WARPS + warp] = Task{1, r, unit, id0, first, last, cut};
+    if (from_start && !direct && warp == w0 && lane == 0) {
+        const int e = cut.warp_of(last - 1);  // the warp that holds the unit's last group
+        const bool tail = cut.start(e / cut.A, e % cut.A + 1) > last;  // whose run goes on
+        ws.tasks[blockIdx.x * C::WARPS + warp] =
+            Task{1, h, rg, id0 * 2, (tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1,
+                 cut.A * 2, tail ? e * 2 + 1 : -1, static_cast<int>(blockIdx.x + 1) * cut.A * 2, q};
+    }
     if (!direct && warp == w0 && g == 0) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -994,11 +1011,11 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         for (int w = 0; w < C::WARPS; ++w) {
             if (w < w0 || w >= w1) continue;
             const float4 y = *reinterpret_cast<const float4 *>(smem + w * C::RING + (i * 32 + lane) * 16);
-            const float f = ex2(pieces[w].m[2 * t + c] - top);
-            x.x = fmaf(y.x, f, x.x);
-            x.y = fmaf(y.y, f, x.y);
-            x.z = fmaf(y.z, f, x.z);
-            x.w = fmaf(y.w, f, x.w);
+            const float k = c ? f[1][w] : f[0][w];
+            x.x = fmaf(y.x, k, x.x);
+            x.y = fmaf(y.y, k, x.y);
+            x.z = fmaf(y.z, k, x.z);
+            x.w = fmaf(y.w, k, x.w);
         }
         if (direct)
             write_row<T>(a, column(q, rg, 2 * t + c, h, log_group), HD, 32 * b + 4 * g, x, top,
@@ -1035,15 +1052,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
     for (int j = threadIdx.x >> 5; j < n_tasks * ITEMS; j += kJoinThreads / 32) {
         const Task &k = tasks[j / ITEMS];
         const int i = j % ITEMS, b = i >> 1, n = 2 * t + (i & 1);
-        const Cut &cut = k.cut;
-        // pieces: the joined one of each block from k.w's on, and the last warp's first
-        // piece if its run goes on past the unit
-        const int w1 = cut.warp_of(k.last - 1);  // the warp that holds the unit's last group
-        const bool tail = cut.start(w1 / cut.A, w1 % cut.A + 1) > k.last;
-        const int b0 = k.w / cut.A, b1 = (tail ? w1 - 1 : w1) / cut.A;
-        const int pieces = b1 - b0 + 1 + (tail ? 1 : 0);
+        const int pieces = k.blocks + (k.tail >= 0);
         auto piece = [&](int e) {
-            const int slot = e > b1 - b0 ? w1 * 2 + 1 : e == 0 ? k.w * 2 : (b0 + e) * cut.A * 2;
+            const int slot = e == 0 ? k.first : e < k.blocks ? k.next + (e - 1) * k.stride : k.tail;
             return ws.partial + static_cast<size_t>(slot) * C::PARTIAL;
         };
         float M = kLowest, L = 0.0f;
@@ -1076,9 +1087,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                 x.w = fmaf(y[e].w, f, x.w);
             }
         }
-        const Req q = load_req(a, k.r, log_group);
-        const int h = k.unit / q.rgs, rg = k.unit - h * q.rgs;
-        write_row<T>(a, column(q, rg, n, h, log_group), HD, 32 * b + 4 * g, x, M, L);
+        write_row<T>(a, column(k.q, k.rg, n, k.h, log_group), HD, 32 * b + 4 * g, x, M, L);
     }
 }
 
@@ -1101,8 +1110,16 @@ cudaError_t launch_after(K *kernel, int blocks, int threads, size_t smem, cudaSt
 template <typename T, int HD>
 cudaError_t launch(const PagedAttnArgs &a, cudaStream_t stream) {
     using C = Cfg<T, HD>;
-    cudaError_t e = cudaFuncSetAttribute(paged_attn_kernel<T, HD>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    // once for each device, as the call takes a microsecond; two threads that are first may both
+    // make it
+    static std::atomic<uint64_t> made{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(made.load(std::memory_order_acquire) >> dev & 1))) {
+        e = cudaFuncSetAttribute(paged_attn_kernel<T, HD>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+        if (e == cudaSuccess && dev < 64) made.fetch_or(1ull << dev, std::memory_order_release);
+    }
     const int blocks = device_sm_count();
     if (e == cudaSuccess)
         e = launch_after(paged_attn_kernel<T, HD>, blocks, C::THREADS, C::SMEM, stream, a);
