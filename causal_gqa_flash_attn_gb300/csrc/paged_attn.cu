@@ -54,7 +54,16 @@ namespace {
 constexpr float kLowest = -1e30f;  // reference of a row that has seen no key
 constexpr float kLift = 6.0f;      // log2 of the largest weight right after a move
 constexpr float kMost = 14.0f;     // log2 weight that moves the reference
-constexpr int kMinGroups = 4;      // groups per warp below which fewer warps work
+// The start and end of a unit (its rows of q as operands, its output) cost a
+// warp about as much as kUnitCost groups: 6000 against 2200 cycles.
+#ifndef PA_UNIT
+#define PA_UNIT 3
+#endif
+#ifndef PA_MIN
+#define PA_MIN 6
+#endif
+constexpr int kUnitCost = PA_UNIT;
+constexpr int kMinWork = PA_MIN;  // work per warp below which fewer warps work; > kUnitCost
 constexpr int kRows = 8;           // query rows of a row group
 constexpr int kMostWarps = 16;     // computing warps of a block that the workspace is made for
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
@@ -93,6 +102,7 @@ struct Cfg {
     static constexpr int PARTIAL = 2 * kRows + kRows * HD;  // floats
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
     static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
+    static_assert(kMinWork > kUnitCost, "a part of the cut has a group, but for a block's last");
     static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
     static_assert(RING >= kRows * HD * 4, "a warp's O fits its ring");
     static_assert(SMEM <= 224 * 1024, "shared memory");
@@ -128,19 +138,19 @@ __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_g
     }
     return q;
 }
-// Groups a request counts for: at least one per unit, so that rows without any
-// key are visited and written too.
-__device__ __forceinline__ long long req_work(const Req &q, int n_kv) {
-    return static_cast<long long>(max(q.ng, 1)) * q.rgs * n_kv;
-}
+// Groups of a unit: at least one, so that rows without any key are visited and
+// written too.
+__device__ __forceinline__ int unit_groups(const Req &q) { return max(q.ng, 1); }
 
 // Quotients of 64-bit counts, which mostly have 32.
 __device__ __forceinline__ long long quotient(long long n, int d) {
     return n >> 32 ? n / d : static_cast<long long>(static_cast<unsigned>(n) / static_cast<unsigned>(d));
 }
 
-// The cut of the work: N groups, c for each of B blocks, cw of those for each
-// of A warps (the last ones may have fewer, or none).
+// The cut of the work. Its measure is a group, and kUnitCost ahead of those of
+// each unit: N in all, c for each of B blocks, cw of those for each of A warps
+// (the last ones may have fewer, or none). A warp's run is the groups whose
+// measure lies in its part.
 struct Cut {
     long long N, c;
     int cw, B, A;
@@ -155,10 +165,10 @@ struct Cut {
 __device__ __forceinline__ Cut make_cut(long long N, int blocks, int warps) {
     Cut t;
     t.N = N;
-    const long long want = max((N + kMinGroups - 1) / kMinGroups, 1ll);
+    const long long want = max((N + kMinWork - 1) / kMinWork, 1ll);
     t.B = static_cast<int>(min(static_cast<long long>(blocks), want));
     t.c = max(quotient(N + t.B - 1, t.B), 1ll);
-    t.A = static_cast<int>(min(static_cast<long long>(warps), (t.c + kMinGroups - 1) / kMinGroups));
+    t.A = static_cast<int>(min(static_cast<long long>(warps), (t.c + kMinWork - 1) / kMinWork));
     t.cw = static_cast<int>(quotient(t.c + t.A - 1, t.A));
     return t;
 }
@@ -171,6 +181,12 @@ struct Task {
     int tail;                   // and of the piece that begins the last warp's run, or -1
     int next;                   // partial of the second block's piece
     Req q;
+};
+// Where a part of the cut begins.
+struct Place {
+    int r, unit, gi;   // its first group
+    int ahead;         // measure of the unit's start that lies before it (of kUnitCost)
+    long long groups;  // groups before it
 };
 struct Ws {
     Task *tasks;     // one per warp
@@ -348,6 +364,7 @@ __device__ __forceinline__ int tile_size(int i, int end, int ns, int skip) {
 // the groups has no registers to spare.
 struct Piece {
     int r, unit, gi, todo;      // request, unit (kv head and row group), group, groups left in the run
+    int ahead;                  // measure between the run's last group and the end of its part
     int n, end;                 // groups of the unit, and where the piece ends
     int pos[kRows];             // the columns' positions
     int p_min, p_max;           // of all of them
@@ -355,7 +372,7 @@ struct Piece {
     int holes;                  // the run has met a group without rows to read
     int gone;                   // tiles of the run that are done, whose stages are free
     int fin_r, fin_unit;        // the piece that ends the run, if other warps have more of its unit (else -1)
-    long long fin_first, fin_last;  // that unit's groups in the cut
+    long long fin_first, fin_last;  // that unit's groups in the cut's measure
     float m[kRows], l[kRows];   // and the piece's references and sums
 };
 
@@ -566,9 +583,9 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     using C = Cfg<T, HD>;
     constexpr int NB = C::NB, S = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ long long scan_part[C::WARPS + 1];
-    __shared__ int start_r[C::WARPS];
-    __shared__ long long start_x[C::WARPS];
+    __shared__ long long scan_part[2][C::WARPS + 1];
+    __shared__ int start_r[C::WARPS + 1];                // the request in which part i begins,
+    __shared__ long long start_x[2][C::WARPS + 1];       // and what lies before it (measure, groups)
     __shared__ Piece pieces[C::WARPS];
     __shared__ int abort_flag;
 
@@ -596,27 +613,30 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     // ---- the cut: sums over all requests, each thread a run of them
     const int per = (a.n_reqs + C::THREADS - 1) / C::THREADS;
     const int r0 = min(a.n_reqs, tid * per), r1 = min(a.n_reqs, r0 + per);
-    long long mine = 0;
+    long long work = 0, count = 0;  // measure and groups
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
         const Req q = load_req(a, r, log_group);
+        const long long units = static_cast<long long>(q.rgs) * n_kv;
         bad |= q.bad;
-        mine += req_work(q, n_kv);
+        work += units * (unit_groups(q) + kUnitCost);
+        count += units * unit_groups(q);
     }
     if (bad && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
-    long long inc = mine;
+    long long inc = work, inc_g = count;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(~0u, inc, d);
-        if (lane >= d) inc += o;
+        const long long o = __shfl_up_sync(~0u, inc, d), p = __shfl_up_sync(~0u, inc_g, d);
+        if (lane >= d) inc += o, inc_g += p;
     }
-    if (lane == 31) scan_part[warp] = inc;
+    if (lane == 31) scan_part[0][warp] = inc, scan_part[1][warp] = inc_g;
     __syncthreads();
-    long long base = 0, N = 0;
+    long long base = 0, base_g = 0, N = 0, all_groups = 0;
 #pragma unroll
     for (int i = 0; i <= C::WARPS; ++i) {
-        if (i == warp) base = N;
-        N += scan_part[i];
+        if (i == warp) base = N, base_g = all_groups;
+        N += scan_part[0][i];
+        all_groups += scan_part[1][i];
     }
     if (N >> 30 >= gridDim.x) {  // runs are counted in 31 bits (2^34 rows an SM)
         if (tid == 0 && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
@@ -624,25 +644,50 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
     const Cut cut = make_cut(N, gridDim.x, C::WARPS);
     {
-        // the request in which each of this block's runs begins
-        long long x = base + inc - mine;
+        // the requests in which the block's parts begin, and the one after them
+        long long x = base + inc - work, xg = base_g + inc_g - count;
         const long long s0 = cut.start(blockIdx.x, 0), s1 = cut.start(blockIdx.x, cut.A);
-        if (mine > 0 && x < s1 && x + mine > s0) {
+        if (work > 0 && x <= s1 && x + work > s0) {
             for (int r = r0; r < r1; ++r) {
-                const long long n = per == 1 ? mine : req_work(load_req(a, r, log_group), n_kv);
-                // relative to the block's run: 31 bits
-                const long long lo = x - s0, hi = min(x + n, s1) - s0;
-                int s = 0;
-                for (int i = 0; i < cut.A; ++i, s += cut.cw)
+                long long n = work, ng = count;
+                if (per > 1) {
+                    const Req q = load_req(a, r, log_group);
+                    ng = static_cast<long long>(q.rgs) * n_kv * unit_groups(q);
+                    n = ng + static_cast<long long>(q.rgs) * n_kv * kUnitCost;
+                }
+                const long long lo = x - s0, hi = x + n - s0;
+                for (int i = 0; i <= cut.A; ++i) {
+                    const long long s = cut.start(blockIdx.x, i) - s0;
                     if (lo <= s && s < hi) {
                         start_r[i] = r;
-                        start_x[i] = x;
+                        start_x[0][i] = x;
+                        start_x[1][i] = xg;
                     }
+                }
                 x += n;
+                xg += ng;
             }
         }
     }
     __syncthreads();
+    // where part i of the block begins: request, unit, group, and the groups before it
+    auto place = [&](int i) {
+        Place p;
+        const long long s = cut.start(blockIdx.x, i);
+        p.r = -1;
+        p.unit = p.gi = p.ahead = 0;
+        p.groups = all_groups;
+        if (s >= N) return p;
+        p.r = start_r[i];
+        const int n = unit_groups(load_req(a, p.r, log_group));
+        const long long off = s - start_x[0][i];
+        p.unit = off < n + kUnitCost ? 0 : static_cast<int>(quotient(off, n + kUnitCost));
+        const int at = static_cast<int>(off - static_cast<long long>(p.unit) * (n + kUnitCost));
+        p.gi = max(0, at - kUnitCost);
+        p.ahead = min(at, kUnitCost);
+        p.groups = start_x[1][i] + static_cast<long long>(p.unit) * n + p.gi;
+        return p;
+    };
 
     if (warp == C::WARPS) {
         // ---- the copying warp: lane w walks the run of warp w, up to S tiles ahead of it.
@@ -653,7 +698,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         bool any = false;
         const int32_t *table = a.pages.table;
         auto enter = [&](const Req &q) {
-            cn = max(q.ng, 1);
+            cn = unit_groups(q);
             any = q.ng > 0;
             ns = q.ns;
             skip = q.skip;
@@ -661,15 +706,15 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             units = q.rgs * n_kv;
             table = a.pages.table + static_cast<size_t>(r) * a.pages.max_pages;
         };
-        if (lane < cut.A && blockIdx.x < cut.B) {
-            const long long x0 = cut.start(blockIdx.x, lane);
-            left = static_cast<int>(cut.start(blockIdx.x, lane + 1) - x0);
+        {
+            const Place p = place(min(lane, cut.A));
+            const long long end = __shfl_down_sync(~0u, p.groups, 1);
+            if (lane < cut.A) left = static_cast<int>(end - p.groups);
             if (left > 0) {
-                r = start_r[lane];
+                r = p.r;
                 enter(load_req(a, r, log_group));
-                const long long off = x0 - start_x[lane];
-                unit = static_cast<int>(quotient(off, cn));
-                ci = static_cast<int>(off - static_cast<long long>(unit) * cn);
+                unit = p.unit;
+                ci = p.gi;
                 head = unit / rgs * a.pages.groups;
             }
         }
@@ -747,18 +792,18 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             ws.tasks[blockIdx.x * C::WARPS + warp].valid = 0;
             pc->fin_unit = -1;
             pc->todo = 0;
-            if (warp < cut.A) {
-                const long long x0 = cut.start(blockIdx.x, warp);
-                const int todo = static_cast<int>(cut.start(blockIdx.x, warp + 1) - x0);
-                if (todo > 0) {
-                    const long long off = x0 - start_x[warp];
-                    const int n = max(load_req(a, start_r[warp], log_group).ng, 1);
-                    const int unit = off < n ? 0 : static_cast<int>(quotient(off, n));
-                    pc->r = start_r[warp];
-                    pc->unit = unit;
-                    pc->gi = static_cast<int>(off - static_cast<long long>(unit) * n);
-                    pc->todo = todo;
-                }
+        }
+        __syncwarp();
+        if (warp < cut.A) {
+            const Place p = place(warp + (lane & 1));  // where the run begins, and where the next one does
+            const long long end = __shfl_down_sync(~0u, p.groups, 1);
+            const int ahead = __shfl_down_sync(~0u, p.ahead, 1), gi_end = __shfl_down_sync(~0u, p.gi, 1);
+            if (lane == 0) {
+                pc->r = p.r;
+                pc->unit = p.unit;
+                pc->gi = p.gi;
+                pc->ahead = gi_end > 0 ? 0 : ahead;
+                pc->todo = static_cast<int>(end - p.groups);
             }
         }
         __syncwarp();
@@ -772,7 +817,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             float km[2];
             {
                 const Req q = load_req(a, pc->r, log_group);
-                const int n = max(q.ng, 1), unit = pc->unit;
+                const int n = unit_groups(q), unit = pc->unit;
                 const int h = unit / q.rgs, rg = unit - h * q.rgs;
                 g_end = min(n, gi + pc->todo);
                 // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
@@ -940,7 +985,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     pc->unit = next;
                     pc->gi = 0;
                 } else if (first > 0 || end < n) {
-                    const long long x1 = cut.start(blockIdx.x, warp + 1);
+                    const long long x1 = cut.start(blockIdx.x, warp + 1) - pc->ahead;
                     pc->fin_r = r;
                     pc->fin_unit = unit;
                     pc->fin_first = x1 - end;
@@ -991,7 +1036,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
     if (from_start && !direct && warp == w0 && lane == 0) {
         const int e = cut.warp_of(last - 1);  // the warp that holds the unit's last group
-        const bool tail = cut.start(e / cut.A, e % cut.A + 1) > last;  // whose run goes on
+        const bool tail = cut.start(e / cut.A, e % cut.A + 1) > last + kUnitCost;  // whose run goes on
         ws.tasks[blockIdx.x * C::WARPS + warp] =
             Task{1, h, rg, id0 * 2, (tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1,
                  cut.A * 2, tail ? e * 2 + 1 : -1, static_cast<int>(blockIdx.x + 1) * cut.A * 2, q};
