@@ -83,7 +83,7 @@ struct Cfg {
     static constexpr int TILE = PP ? PA_TILE : 1;
     static constexpr int STAGES = PP ? PA_STAGES : 2;
 #else
-    static constexpr int WARPS = HD == 256 ? 11 : PSPLIT ? 11 : 15;
+    static constexpr int WARPS = HD == 256 || (PSPLIT && HD == 128) ? 11 : 15;
     static constexpr int TILE = HD == 256 ? 1 : HD == 128 ? 2 : 4;
     static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : 2;
 #endif
@@ -273,6 +273,12 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// a * b - c
+__device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("{.reg .b32 n; neg.f16x2 n, %3; fma.rn.f16x2 %0, %1, %2, n;}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 __device__ __forceinline__ float2 half2_f(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
@@ -284,6 +290,15 @@ __device__ __forceinline__ void mma(float *d, uint32_t a0, uint32_t a1, uint32_t
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// D = A * B
+__device__ __forceinline__ void mma0(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                     uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // -8 * 2^-24 and -8 * 2^-20, twice.
@@ -525,54 +540,70 @@ __device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], 
             l1[k] = movmatrix_trans(pack_half2(d2 - rB.x, d3 - rB.y));
         }
     }
-    // ---- O += V^T P
+    // ---- O += V^T P. Groups that are taken together stay together per block where the
+    // products go through a fresh accumulator (its sum is added once), else one by one.
+    constexpr int MI = C::PSPLIT ? M : 1;
 #pragma unroll
-    for (int k = 0; k < M; ++k) {
-        const uint8_t *vp = kp[k] + part_bytes(HD);
-        uint32_t vw[2 * NB];
-        uint4 vs = make_uint4(0, 0, 0, 0);
+    for (int k0 = 0; k0 < M; k0 += MI) {
+        uint32_t vw[MI][2 * NB];
+        uint4 vs[MI];
 #pragma unroll
-        for (int c = 0; c < NB / 2; ++c) {
-            const uint4 w = lds_v4(vp + (c * 32 + lane) * 16);
-            vw[4 * c] = w.x; vw[4 * c + 1] = w.y; vw[4 * c + 2] = w.z; vw[4 * c + 3] = w.w;
-        }
+        for (int k = 0; k < MI; ++k)
+#pragma unroll
+            for (int c = 0; c < NB / 2; ++c) {
+                const uint4 w = lds_v4(kp[k0 + k] + part_bytes(HD) + (c * 32 + lane) * 16);
+                vw[k][4 * c] = w.x; vw[k][4 * c + 1] = w.y; vw[k][4 * c + 2] = w.z; vw[k][4 * c + 3] = w.w;
+            }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
-            const uint32_t x01 = __byte_perm(vw[b / 2], vw[(NB + b) / 2], sel);
-            const uint32_t x23 = __byte_perm(vw[(2 * NB + b) / 2], vw[(3 * NB + b) / 2], sel);
-            const uint32_t z01 = x01 >> 8, z23 = x23 >> 8;
-            if (b % 2 == 0) vs = lds_v4(vp + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
-            const uint32_t s01 = b & 1 ? vs.z : vs.x, s23 = b & 1 ? vs.w : vs.y;
-            const uint32_t w0 = hmul2(b0[k], s01), w1 = hmul2(b1[k], s23);
-            const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
-            const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
-            const uint32_t f0 = z01 & 0x000f000fu, f1 = z01 & 0x00f000f0u;
-            const uint32_t f2 = z23 & 0x000f000fu, f3 = z23 & 0x00f000f0u;
+            float u[4], v[4];
+#pragma unroll
+            for (int k = 0; k < MI; ++k) {
+                const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
+                const uint32_t x01 = __byte_perm(vw[k][b / 2], vw[k][(NB + b) / 2], sel);
+                const uint32_t x23 = __byte_perm(vw[k][(2 * NB + b) / 2], vw[k][(3 * NB + b) / 2], sel);
+                const uint32_t z01 = x01 >> 8, z23 = x23 >> 8;
+                if (b % 2 == 0)
+                    vs[k] = lds_v4(kp[k0 + k] + part_bytes(HD) + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
+                const uint32_t s01 = b & 1 ? vs[k].z : vs[k].x, s23 = b & 1 ? vs[k].w : vs[k].y;
+                const uint32_t p0 = b0[k0 + k], p1 = b1[k0 + k];
+                const uint32_t w0 = hmul2(p0, s01), w1 = hmul2(p1, s23);
+                const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
+                const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
+                const uint32_t f0 = z01 & 0x000f000fu, f1 = z01 & 0x00f000f0u;
+                const uint32_t f2 = z23 & 0x000f000fu, f3 = z23 & 0x00f000f0u;
+                if (C::PSPLIT) {
+                    // the product's low term, exact but for the weight's own low term
+                    const uint32_t v0 = hfma2(l0[k0 + k], s01, hfms2(p0, s01, w0));
+                    const uint32_t v1 = hfma2(l1[k0 + k], s23, hfms2(p1, s23, w1));
+                    // c - 8 exactly: the tensor core's sums lose a step towards zero per
+                    // addition, which an offset taken out afterwards would leave behind
+                    const uint32_t g0 = hadd2(e0, kM8a), g1 = hadd2(e1, kM8b);
+                    const uint32_t g2 = hadd2(e2, kM8a), g3 = hadd2(e3, kM8b);
+                    const uint32_t h0 = hadd2(f0, kM8a), h1 = hadd2(f1, kM8b);
+                    const uint32_t h2 = hadd2(f2, kM8a), h3 = hadd2(f3, kM8b);
+                    if (k == 0) {
+                        mma0(u, g0, g1, g2, g3, v0, v1);
+                        mma0(v, h0, h1, h2, h3, v0, v1);
+                    } else {
+                        mma(u, g0, g1, g2, g3, v0, v1);
+                        mma(v, h0, h1, h2, h3, v0, v1);
+                    }
+                    mma(u, g0, g1, g2, g3, w0, w1);
+                    mma(v, h0, h1, h2, h3, w0, w1);
+                } else {
+                    mma(st.o[b][0], e0, e1, e2, e3, w0, w1);
+                    mma(st.o[b][1], f0, f1, f2, f3, w0, w1);
+                    mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
+                    mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
+                }
+            }
             if (C::PSPLIT) {
-                const uint32_t v0 = hfma2(l0[k], s01, hfma2(b0[k], s01, w0 ^ 0x80008000u));
-                const uint32_t v1 = hfma2(l1[k], s23, hfma2(b1[k], s23, w1 ^ 0x80008000u));
-                // c - 8 exactly: the tensor core's sums lose a step towards zero per
-                // addition, which an offset taken out afterwards would leave behind
-                float u[4] = {0.0f, 0.0f, 0.0f, 0.0f}, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                const uint32_t g0 = hadd2(e0, kM8a), g1 = hadd2(e1, kM8b);
-                const uint32_t g2 = hadd2(e2, kM8a), g3 = hadd2(e3, kM8b);
-                mma(u, g0, g1, g2, g3, w0, w1);
-                mma(u, g0, g1, g2, g3, v0, v1);
-                const uint32_t h0 = hadd2(f0, kM8a), h1 = hadd2(f1, kM8b);
-                const uint32_t h2 = hadd2(f2, kM8a), h3 = hadd2(f3, kM8b);
-                mma(v, h0, h1, h2, h3, w0, w1);
-                mma(v, h0, h1, h2, h3, v0, v1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     st.o[b][0][i] += u[i];
                     st.o[b][1][i] += v[i];
                 }
-            } else {
-                mma(st.o[b][0], e0, e1, e2, e3, w0, w1);
-                mma(st.o[b][1], f0, f1, f2, f3, w0, w1);
-                mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
-                mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
             }
         }
     }
@@ -866,8 +897,8 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         *reinterpret_cast<uint4 *>(qs + C::QF + (b * 32 + lane) * 16) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     // -8 times the block's sum, where the accumulators start: "code -8" in every row
-                    float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    mma(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
+                    float d[4];
+                    mma0(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
                     mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
                     if (C::QSPLIT) {
                         mma(d, kM8a, kM8a, kM8b, kM8b, lo[0], lo[1]);
