@@ -151,7 +151,7 @@ fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dt
                   const int32_t *positions, int64_t pos_stride, int n_axes, const void *table,
                   int adjacent, int inverse, fa_stream_t stream) {
     if (!known_type(dtype) || n_tokens < 0 || n_q_heads < 0 || n_kv_heads < 0 ||
-        head_dim < 2 || head_dim > 65536 || rotary_dim < 2 || rotary_dim % 2 ||
+        head_dim < 2 || head_dim > 8192 || rotary_dim < 2 || rotary_dim % 2 ||
         rotary_dim > head_dim || n_axes < 1 || n_axes > 8 || n_q_heads > 65536 ||
         n_kv_heads > 65536)
         return FA_ERR_INVALID;

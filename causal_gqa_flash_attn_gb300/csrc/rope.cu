@@ -10,9 +10,10 @@
 // far the position is, without the 64-bit floating-point units (a few per SM).
 // sincospif then sees an argument in [-1, 1).
 //
-// The call is bound by HBM: every element is read and written once. A thread
-// owns one 16-byte vector of pairs of one token: it computes their sines and
-// cosines once and walks the heads, whose loads are independent.
+// The call is bound by HBM: every element is read and written once. A block
+// takes a few tokens, puts their sines and cosines into shared memory (one for
+// all heads) and streams the heads through with 16-byte loads, a thread two
+// vectors of each of kRopeUnroll heads at a time.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -23,8 +24,10 @@
 namespace fa {
 namespace {
 
-constexpr int kRopeThreads = 128;
-constexpr int kRopeUnroll = 4;  // heads whose loads are in flight together
+constexpr int kRopeThreads = 256;
+constexpr int kRopeUnroll = 2;      // heads whose loads are in flight together
+constexpr int kRopeItems = 2048;    // items (two vectors) that a block is given
+constexpr int kRopeTokens = 16;     // tokens of a block at most
 
 template <typename T> struct Conv;
 template <> struct Conv<float> {
@@ -50,102 +53,126 @@ struct alignas(V * sizeof(T)) Vec {
 template <typename T, int V, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     using W = Vec<T, V>;
+    extern __shared__ float4 rope_smem[];
     const int half = a.rotary_dim / 2;
     const int n_rot = half / V;            // items of V pairs
     const int n_items = n_rot + a.n_copy;  // and of 2 V values that stay as they are
-    const long long id = blockIdx.x * static_cast<long long>(kRopeThreads) + threadIdx.x;
-    const int tok = static_cast<int>(id / n_items);
-    if (tok >= a.n_tokens) return;
-    const int item = static_cast<int>(id - static_cast<long long>(tok) * n_items);
-    const int h0 = blockIdx.y * a.heads_per_block;
-    const int h1 = min(h0 + a.heads_per_block, a.n_q_heads + a.n_kv_heads);
-    // element offsets of the item's two vectors inside a head
-    int o0, o1;
-    bool second = true;
-    float c[V], s[V];
-    if (item < n_rot) {
-        o0 = ADJ ? 2 * V * item : V * item;
-        o1 = ADJ ? o0 + V : half + o0;
-#pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const uint4 f = __ldg(static_cast<const uint4 *>(a.table) + item * V + k);
-            const int axis = min(static_cast<int>(f.z), a.n_axes - 1);
-            const long long pos = __ldg(a.positions + axis * a.pos_stride + tok);
-            const unsigned long long F = (static_cast<unsigned long long>(f.y) << 32) | f.x;
-            const unsigned long long turn = static_cast<unsigned long long>(pos) * F;
-            const int top = static_cast<int>((turn + 0x80000000ull) >> 32);
-            sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s[k], &c[k]);  // 2^-31
-            if (a.inverse) s[k] = -s[k];
-        }
-    } else {
-        o0 = a.rotary_dim + 2 * V * (item - n_rot);
-        o1 = o0 + V;
-        second = o1 < a.head_dim;
-#pragma unroll
-        for (int k = 0; k < V; ++k) c[k] = 1.0f, s[k] = 0.0f;
+    float *cs = reinterpret_cast<float *>(rope_smem);  // [tokens][half] cosines, then sines
+    float *sn = cs + a.tokens_per_block * half;
+    const int tok0 = blockIdx.x * a.tokens_per_block;
+    const int n_tok = min(a.tokens_per_block, a.n_tokens - tok0);
+    for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
+        const int tok = i / half, pair = i - tok * half;
+        const uint4 f = __ldg(static_cast<const uint4 *>(a.table) + pair);
+        const int axis = min(static_cast<int>(f.z), a.n_axes - 1);
+        const long long pos = __ldg(a.positions + axis * a.pos_stride + tok0 + tok);
+        const unsigned long long F = (static_cast<unsigned long long>(f.y) << 32) | f.x;
+        const unsigned long long turn = static_cast<unsigned long long>(pos) * F;
+        const int top = static_cast<int>((turn + 0x80000000ull) >> 32);
+        float s, c;
+        sincospif(static_cast<float>(top) * 4.656612873077393e-10f, &s, &c);  // 2^-31
+        cs[i] = c;
+        sn[i] = a.inverse ? -s : s;
     }
-    const bool copy = item >= n_rot;
-    const T *qi = static_cast<const T *>(a.q) + tok * a.q_stride;
-    const T *ki = static_cast<const T *>(a.k) + tok * a.k_stride;
-    T *qo = static_cast<T *>(a.q_out) + tok * a.q_out_stride;
-    T *ko = static_cast<T *>(a.k_out) + tok * a.k_out_stride;
-    for (int h = h0; h < h1; h += kRopeUnroll) {
-        W x[kRopeUnroll], y[kRopeUnroll];
+    __syncthreads();
+    const int h0 = blockIdx.y * a.heads_per_block;
+    const int heads = min(a.heads_per_block, a.n_q_heads + a.n_kv_heads - h0);
+    // threads of a head, heads that the block takes at once, and this thread's first one
+    const int lanes = min(n_items, kRopeThreads), rows = kRopeThreads / lanes;
+    const int row = threadIdx.x / lanes, lane = threadIdx.x - row * lanes;
+    if (row >= rows) return;
+    int tok = row / heads, head = row - tok * heads;
+    while (tok < n_tok) {
+        const T *in[kRopeUnroll];
         T *out[kRopeUnroll];
+        const float *c[kRopeUnroll];
+        int n = 0;  // heads of this turn
 #pragma unroll
         for (int u = 0; u < kRopeUnroll; ++u) {
-            const int hh = h + u;
-            if (hh >= h1) break;
+            if (tok >= n_tok) break;
+            const int hh = h0 + head;
             const bool isq = hh < a.n_q_heads;
+            const long long t = tok0 + tok;
             const long long off = static_cast<long long>(isq ? hh : hh - a.n_q_heads) * a.head_dim;
-            const T *in = (isq ? qi : ki) + off;
-            out[u] = (isq ? qo : ko) + off;
-            x[u] = *reinterpret_cast<const W *>(in + o0);
-            if (second) y[u] = *reinterpret_cast<const W *>(in + o1);
+            in[u] = static_cast<const T *>(isq ? a.q : a.k) + t * (isq ? a.q_stride : a.k_stride) + off;
+            out[u] = static_cast<T *>(isq ? a.q_out : a.k_out) +
+                     t * (isq ? a.q_out_stride : a.k_out_stride) + off;
+            c[u] = cs + tok * half;
+            n = u + 1;
+            head += rows;
+            while (head >= heads) head -= heads, ++tok;
         }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            if (h + u >= h1) break;
-            if (!copy) {
-                T *xs = x[u].x, *ys = y[u].x;
-#pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    // halves: pair k is (xs[k], ys[k]); adjacent: it is values 2 k and
-                    // 2 k + 1 of the two vectors taken one after the other
-                    T *p = ADJ ? (2 * k < V ? xs + 2 * k : ys + 2 * k - V) : xs + k;
-                    T *q = ADJ ? (2 * k + 1 < V ? xs + 2 * k + 1 : ys + 2 * k + 1 - V) : ys + k;
-                    const float u0 = Conv<T>::get(*p), u1 = Conv<T>::get(*q);
-                    *p = Conv<T>::put(u0 * c[k] - u1 * s[k]);
-                    *q = Conv<T>::put(u0 * s[k] + u1 * c[k]);
-                }
+        for (int item = lane; item < n_items; item += lanes) {
+            // An item's two vectors lie apart, so that neighbouring threads' are neighbours: in the
+            // two halves of the rotated dims (for adjacent pairs, V / 2 pairs in each), or of the rest.
+            const bool turns = item < n_rot;
+            int o0, o1;
+            if (turns) {
+                o0 = ADJ && V == 1 ? 2 * item : V * item;
+                o1 = ADJ && V == 1 ? o0 + 1 : half + o0;
+            } else {
+                o0 = a.rotary_dim + V * (item - n_rot);
+                o1 = o0 + V * a.n_copy;
             }
-            *reinterpret_cast<W *>(out[u] + o0) = x[u];
-            if (second) *reinterpret_cast<W *>(out[u] + o1) = y[u];
+            const bool second = o1 < a.head_dim;
+            W x[kRopeUnroll], y[kRopeUnroll];
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u) {
+                if (u >= n) break;
+                x[u] = *reinterpret_cast<const W *>(in[u] + o0);
+                if (second) y[u] = *reinterpret_cast<const W *>(in[u] + o1);
+            }
+#pragma unroll
+            for (int u = 0; u < kRopeUnroll; ++u) {
+                if (u >= n) break;
+                if (turns) {
+                    T *xs = x[u].x, *ys = y[u].x;
+                    const float *cu = c[u], *su = cu + a.tokens_per_block * half;
+#pragma unroll
+                    for (int k = 0; k < V; ++k) {
+                        // halves: pair k is (xs[k], ys[k]); adjacent: it is two neighbours of one vector
+                        const int pair = !ADJ || V == 1 ? item * V + k
+                                         : k < V / 2    ? item * (V / 2) + k
+                                                        : half / 2 + item * (V / 2) + k - V / 2;
+                        T *p = ADJ && V > 1 ? (k < V / 2 ? xs + 2 * k : ys + 2 * k - V) : xs + k;
+                        T *q = ADJ && V > 1 ? p + 1 : ys + k;
+                        const float u0 = Conv<T>::get(*p), u1 = Conv<T>::get(*q);
+                        const float co = cu[pair], si = su[pair];
+                        *p = Conv<T>::put(u0 * co - u1 * si);
+                        *q = Conv<T>::put(u0 * si + u1 * co);
+                    }
+                }
+                *reinterpret_cast<W *>(out[u] + o0) = x[u];
+                if (second) *reinterpret_cast<W *>(out[u] + o1) = y[u];
+            }
         }
     }
 }
 
 template <typename T, int V>
 cudaError_t launch(RopeArgs a, cudaStream_t stream) {
-    const bool in_place = a.q == a.q_out && (a.n_kv_heads == 0 || a.k == a.k_out);
-    const int rest = a.head_dim - a.rotary_dim;
-    a.n_copy = in_place ? 0 : (rest + 2 * V - 1) / (2 * V);
-    const long long threads = static_cast<long long>(a.rotary_dim / 2 / V + a.n_copy) * a.n_tokens;
-    const long long blocks = (threads + kRopeThreads - 1) / kRopeThreads;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const bool in_place = (a.n_q_heads == 0 || a.q == a.q_out) && (a.n_kv_heads == 0 || a.k == a.k_out);
+    const int rest = a.head_dim - a.rotary_dim, half = a.rotary_dim / 2;
+    a.n_copy = in_place ? 0 : (rest / V + 1) / 2;
     const int heads = a.n_q_heads + a.n_kv_heads;
-    // Few tokens: the heads are split over blocks too, so that the GPU's SMs
-    // all have some.
-    const long long want = static_cast<long long>(device_sm_count()) * 8;
-    int parts = static_cast<int>(std::min<long long>((want + blocks - 1) / blocks,
-                                                     (heads + kRopeUnroll - 1) / kRopeUnroll));
+    const long long row = static_cast<long long>(heads) * (half / V + a.n_copy);  // items of a token
+    const int fit = std::min<int>(kRopeTokens, 48 * 1024 / (half * 8));
+    int tokens = static_cast<int>(std::min<long long>(fit, std::max<long long>(1, kRopeItems / row)));
+    // few tokens: a block takes one, and the heads are split over blocks too, so that
+    // the GPU's SMs all have some
+    const int sms = device_sm_count();
+    if (a.n_tokens <= sms * tokens) tokens = std::max(1, a.n_tokens / sms);
+    a.tokens_per_block = tokens;
+    const int blocks = (a.n_tokens + tokens - 1) / tokens;
+    int parts = std::max(1, std::min(sms * 2 / blocks, heads / 2));
     a.heads_per_block = (heads + parts - 1) / parts;
     parts = (heads + a.heads_per_block - 1) / a.heads_per_block;
     const dim3 grid(static_cast<unsigned>(blocks), parts);
+    const size_t smem = static_cast<size_t>(tokens) * half * 8;
     if (a.adjacent)
-        rope_kernel<T, V, true><<<grid, kRopeThreads, 0, stream>>>(a);
+        rope_kernel<T, V, true><<<grid, kRopeThreads, smem, stream>>>(a);
     else
-        rope_kernel<T, V, false><<<grid, kRopeThreads, 0, stream>>>(a);
+        rope_kernel<T, V, false><<<grid, kRopeThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -476,6 +476,7 @@ fa_status fa_rope_table(uint32_t *table, const double *inv_freq, int pairs, cons
  *   dtype      FA_T_*. Pointers aligned to the element; where pointers, strides,
  *              head_dim and rotary_dim / 2 are multiples of 16 bytes the call
  *              moves 16 bytes at a time.
+ *   head_dim   2..8192, rotary_dim even and at most head_dim.
  *   positions  [n_axes][pos_stride] int32 (device), n_axes 1..8, any value.
  *   table      [rotary_dim / 2] entries of fa_rope_table (device, 16-byte aligned). */
 fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dtype, int n_tokens,
