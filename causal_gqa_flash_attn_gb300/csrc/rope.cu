@@ -12,8 +12,13 @@
 //
 // The call is bound by HBM: every element is read and written once. A block
 // takes a few tokens, puts their sines and cosines into shared memory (one for
-// all heads) and streams the heads through with 16-byte loads, a thread two
-// vectors of each of kRopeUnroll heads at a time.
+// all heads) and streams the heads through, a thread two 16-byte vectors of a
+// head at a time. What hides the latency is the number of threads, so these
+// have few registers: with two or four heads in flight per thread (64 and 100
+// registers), 20011 tokens of 40 heads took 71 and 105 us against 66. Sines in
+// registers, a thread walking all heads of its pairs, took 88 us.
+// 8192 tokens x 18 heads x 256 in bf16, a quarter rotated: 31 us (0.72 of HBM;
+// launch and the sines take 5 us of it); 20011 x 40 x 128 in fp16: 66 us (0.92).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -25,8 +30,7 @@ namespace fa {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeUnroll = 2;      // heads whose loads are in flight together
-constexpr int kRopeItems = 2048;    // items (two vectors) that a block is given
+constexpr int kRopeItems = 1024;    // items (two vectors) that a block is given
 constexpr int kRopeTokens = 16;     // tokens of a block at most
 
 template <typename T> struct Conv;
@@ -51,7 +55,7 @@ struct alignas(V * sizeof(T)) Vec {
 // V values a thread moves at a time: 16 bytes, or 1 where a size, a stride or
 // a pointer is not a multiple of that.
 template <typename T, int V, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     using W = Vec<T, V>;
     extern __shared__ float4 rope_smem[];
     const int half = a.rotary_dim / 2;
@@ -83,25 +87,14 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
     if (row >= rows) return;
     int tok = row / heads, head = row - tok * heads;
     while (tok < n_tok) {
-        const T *in[kRopeUnroll];
-        T *out[kRopeUnroll];
-        const float *c[kRopeUnroll];
-        int n = 0;  // heads of this turn
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-            if (tok >= n_tok) break;
-            const int hh = h0 + head;
-            const bool isq = hh < a.n_q_heads;
-            const long long t = tok0 + tok;
-            const long long off = static_cast<long long>(isq ? hh : hh - a.n_q_heads) * a.head_dim;
-            in[u] = static_cast<const T *>(isq ? a.q : a.k) + t * (isq ? a.q_stride : a.k_stride) + off;
-            out[u] = static_cast<T *>(isq ? a.q_out : a.k_out) +
-                     t * (isq ? a.q_out_stride : a.k_out_stride) + off;
-            c[u] = cs + tok * half;
-            n = u + 1;
-            head += rows;
-            while (head >= heads) head -= heads, ++tok;
-        }
+        const int hh = h0 + head;
+        const bool isq = hh < a.n_q_heads;
+        const long long at = tok0 + tok;
+        const long long off = static_cast<long long>(isq ? hh : hh - a.n_q_heads) * a.head_dim;
+        const T *in = static_cast<const T *>(isq ? a.q : a.k) + at * (isq ? a.q_stride : a.k_stride) + off;
+        T *out = static_cast<T *>(isq ? a.q_out : a.k_out) +
+                 at * (isq ? a.q_out_stride : a.k_out_stride) + off;
+        const float *c = cs + tok * half, *s = sn + tok * half;
         for (int item = lane; item < n_items; item += lanes) {
             // An item's two vectors lie apart, so that neighbouring threads' are neighbours: in the
             // two halves of the rotated dims (for adjacent pairs, V / 2 pairs in each), or of the rest.
@@ -115,37 +108,28 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(RopeArgs a) {
                 o1 = o0 + V * a.n_copy;
             }
             const bool second = o1 < a.head_dim;
-            W x[kRopeUnroll], y[kRopeUnroll];
+            W x, y;
+            x = *reinterpret_cast<const W *>(in + o0);
+            if (second) y = *reinterpret_cast<const W *>(in + o1);
+            if (turns) {
 #pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u) {
-                if (u >= n) break;
-                x[u] = *reinterpret_cast<const W *>(in[u] + o0);
-                if (second) y[u] = *reinterpret_cast<const W *>(in[u] + o1);
-            }
-#pragma unroll
-            for (int u = 0; u < kRopeUnroll; ++u) {
-                if (u >= n) break;
-                if (turns) {
-                    T *xs = x[u].x, *ys = y[u].x;
-                    const float *cu = c[u], *su = cu + a.tokens_per_block * half;
-#pragma unroll
-                    for (int k = 0; k < V; ++k) {
-                        // halves: pair k is (xs[k], ys[k]); adjacent: it is two neighbours of one vector
-                        const int pair = !ADJ || V == 1 ? item * V + k
-                                         : k < V / 2    ? item * (V / 2) + k
-                                                        : half / 2 + item * (V / 2) + k - V / 2;
-                        T *p = ADJ && V > 1 ? (k < V / 2 ? xs + 2 * k : ys + 2 * k - V) : xs + k;
-                        T *q = ADJ && V > 1 ? p + 1 : ys + k;
-                        const float u0 = Conv<T>::get(*p), u1 = Conv<T>::get(*q);
-                        const float co = cu[pair], si = su[pair];
-                        *p = Conv<T>::put(u0 * co - u1 * si);
-                        *q = Conv<T>::put(u0 * si + u1 * co);
-                    }
+                for (int k = 0; k < V; ++k) {
+                    // halves: pair k is (x[k], y[k]); adjacent: it is two neighbours of one vector
+                    const int pair = !ADJ || V == 1 ? item * V + k
+                                     : k < V / 2    ? item * (V / 2) + k
+                                                    : half / 2 + item * (V / 2) + k - V / 2;
+                    T *p = ADJ && V > 1 ? (k < V / 2 ? x.x + 2 * k : y.x + 2 * k - V) : x.x + k;
+                    T *q = ADJ && V > 1 ? p + 1 : y.x + k;
+                    const float u0 = Conv<T>::get(*p), u1 = Conv<T>::get(*q);
+                    *p = Conv<T>::put(u0 * c[pair] - u1 * s[pair]);
+                    *q = Conv<T>::put(u0 * s[pair] + u1 * c[pair]);
                 }
-                *reinterpret_cast<W *>(out[u] + o0) = x[u];
-                if (second) *reinterpret_cast<W *>(out[u] + o1) = y[u];
             }
+            *reinterpret_cast<W *>(out + o0) = x;
+            if (second) *reinterpret_cast<W *>(out + o1) = y;
         }
+        head += rows;
+        while (head >= heads) head -= heads, ++tok;
     }
 }
 
@@ -163,7 +147,7 @@ cudaError_t launch(RopeArgs a, cudaStream_t stream) {
     const int sms = device_sm_count();
     if (a.n_tokens <= sms * tokens) tokens = std::max(1, a.n_tokens / sms);
     a.tokens_per_block = tokens;
-    const int blocks = (a.n_tokens + tokens - 1) / tokens;
+    const int blocks = (a.n_tokens - 1) / tokens + 1;
     int parts = std::max(1, std::min(sms * 2 / blocks, heads / 2));
     a.heads_per_block = (heads + parts - 1) / parts;
     parts = (heads + a.heads_per_block - 1) / a.heads_per_block;
