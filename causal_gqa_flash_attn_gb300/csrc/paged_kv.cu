@@ -121,22 +121,58 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs 
             static_cast<uint16_t>(__float_as_uint(factor) >> 16);
 }
 
-// 4 codes (the low 16 bits) -> 4 binary16 values (c - 8) * s, the product in
-// fp32 as the attention's definition has it.
-__device__ __forceinline__ uint2 dequant4(uint32_t c, float s) {
-    float v[4];
+// 8 codes c of a word -> (c - 8) * s rounded to binary16, in order. The product
+// is exact in fp32 (4 bits times 11); in binary16 arithmetic it is the same,
+// rounded once, where s itself is a binary16 number. A code in bits 0-3 or 4-7
+// of a half word under the bits of 1024 is 1024 + c or 1024 + 16 c.
+__device__ __forceinline__ uint32_t lop_or(uint32_t w, uint32_t mask, uint32_t bits) {
+    return (w & mask) | bits;
+}
+__device__ __forceinline__ __half2 as_half2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+
+__device__ __forceinline__ uint4 dequant8(uint32_t w, float s) {
+    const __half sh = __float2half_rn(s);
+    if (__half2float(sh) != s) {  // beyond binary16's range, or below its normal one
+        uint32_t o[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        v[i] = __fmul_rn(static_cast<float>(static_cast<int>((c >> (4 * i)) & 15u) - 8), s);
-    return make_uint2(pack_half2(v[0], v[1]), pack_half2(v[2], v[3]));
+        for (int i = 0; i < 4; ++i)
+            o[i] = pack_half2(static_cast<float>(static_cast<int>(w >> (8 * i) & 15u) - 8) * s,
+                              static_cast<float>(static_cast<int>(w >> (8 * i + 4) & 15u) - 8) * s);
+        return make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    const __half2 s2 = __half2half2(sh);
+    const __half2 off = __float2half2_rn(-1032.0f), sixteenth = __float2half2_rn(0.0625f);
+    const __half2 off16 = __float2half2_rn(-72.0f);
+    const uint32_t v = w >> 8;
+    // codes (0, 4), (1, 5), (2, 6), (3, 7)
+    const uint32_t a = as_u32(__hmul2(__hadd2(as_half2(lop_or(w, 0x000f000fu, 0x64006400u)), off), s2));
+    const uint32_t b = as_u32(
+        __hmul2(__hfma2(as_half2(lop_or(w, 0x00f000f0u, 0x64006400u)), sixteenth, off16), s2));
+    const uint32_t c = as_u32(__hmul2(__hadd2(as_half2(lop_or(v, 0x000f000fu, 0x64006400u)), off), s2));
+    const uint32_t d = as_u32(
+        __hmul2(__hfma2(as_half2(lop_or(v, 0x00f000f0u, 0x64006400u)), sixteenth, off16), s2));
+    return make_uint4(__byte_perm(a, b, 0x5410), __byte_perm(c, d, 0x5410), __byte_perm(a, b, 0x7632),
+                      __byte_perm(c, d, 0x7632));
 }
 
-__device__ __forceinline__ float row_factor(const uint8_t *part, int hd, int r) {
-    const uint32_t w = __ldg(reinterpret_cast<const uint16_t *>(part + factor_offset(hd)) + r);
-    return __uint_as_float(w << 16);
+__device__ __forceinline__ float half_of(uint32_t w, int hi) {
+    return __half2float(__ushort_as_half(static_cast<unsigned short>(hi ? w >> 16 : w & 0xffffu)));
 }
-__device__ __forceinline__ float block_scale(const uint8_t *p) {
-    return __half2float(__ldg(reinterpret_cast<const __half *>(p)));
+__device__ __forceinline__ float factor_of(uint32_t w, int hi) {  // bfloat16
+    return __uint_as_float(hi ? w & 0xffff0000u : w << 16);
+}
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *p) {
+    if constexpr (N == 4) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    } else if constexpr (N == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        w[0] = x.x; w[1] = x.y;
+    } else {
+        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    }
 }
 
 template <int HD>
@@ -157,39 +193,47 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherArgs 
          i += gridDim.x * (kThreads / 32)) {
         const uint8_t *src = group_at<HD>(a.pages, r, h, i, lane ? nullptr : a.err);
         if (!src) continue;
+        const uint8_t *sv = src + part_bytes(HD);
         const int left = rows - i * kGroupRows;  // rows of the group that exist
         const size_t at = static_cast<size_t>(r) * a.plane_bytes +
                           (static_cast<size_t>(h) * a.max_seq + i * kGroupRows) * (HD * 2);
+        // everything the lane needs of the group: codes, scales and factors
+        uint32_t kw[2 * NB], vw[2 * NB], ks[NB], vs[2 * NB];
 #pragma unroll
         for (int c = 0; c < NB / 2; ++c) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src) + c * 32 + lane);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int j = 4 * c + k, row = g + (j / NB) * 8, b = j % NB;
-                if (row >= left) continue;
-                const float s = block_scale(src + k_scale_at<HD>(row, b)) *
-                                row_factor(src, HD, row);
-                const uint2 lo = dequant4(ws[k], s), hi = dequant4(ws[k] >> 16, s);
-                *reinterpret_cast<uint4 *>(a.k_planes + at + (row * HD + 32 * b + 8 * t) * 2) =
-                    make_uint4(lo.x, lo.y, hi.x, hi.y);
-            }
+            load_words<4>(kw + 4 * c, src + (c * 32 + lane) * 16);
+            load_words<4>(vw + 4 * c, sv + (c * 32 + lane) * 16);
+            load_words<4>(vs + 4 * c, sv + scale_offset(HD) + (c * 4 + t) * 16);
         }
-        const uint8_t *sv = src + part_bytes(HD);
+        load_words<NB / 2>(ks, src + scale_offset(HD) + g * (2 * NB));
+        load_words<NB / 2>(ks + NB / 2, src + scale_offset(HD) + (g + 8) * (2 * NB));
+        const uint16_t *kf = reinterpret_cast<const uint16_t *>(src + factor_offset(HD)) + g;
+        const uint32_t *vf = reinterpret_cast<const uint32_t *>(sv + factor_offset(HD)) + t;
+        const uint32_t kf01 = __ldg(kf) | static_cast<uint32_t>(__ldg(kf + 8)) << 16;
+        const uint32_t vf01 = __ldg(vf), vf23 = __ldg(vf + 4);
+        // K: the lane's word (row g or g + 8, block b) is dims 32 b + 8 t ..
 #pragma unroll
-        for (int c = 0; c < NB / 2; ++c) {
-            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(sv) + c * 32 + lane);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+        for (int j = 0; j < 2 * NB; ++j) {
+            const int row = g + (j / NB) * 8, b = j % NB;
+            if (row >= left) continue;
+            const float s = half_of(ks[(j / NB) * (NB / 2) + b / 2], b & 1) * factor_of(kf01, j / NB);
+            *reinterpret_cast<uint4 *>(a.k_planes + at + (row * HD + 32 * b + 8 * t) * 2) =
+                dequant8(kw[j], s);
+        }
+        // V: a word is two blocks of row 2 t + (x & 1) + 8 (x >> 1), dims 32 b + 4 g .. of each
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int j = 8 * c + k, x = j / NB, b = j % NB;
-                const int row = 2 * t + (x & 1) + 8 * (x >> 1);
-                if (row >= left) continue;
-                const float s = block_scale(sv + v_scale_at<HD>(row, b)) *
-                                row_factor(sv, HD, row);
-                *reinterpret_cast<uint2 *>(a.v_planes + at + (row * HD + 32 * b + 4 * g) * 2) =
-                    dequant4(ws[k >> 1] >> (16 * (k & 1)), s);
-            }
+        for (int j = 0; j < 2 * NB; ++j) {
+            const int x = 2 * j / NB, b = 2 * j % NB;
+            const int row = 2 * t + (x & 1) + 8 * (x >> 1);
+            if (row >= left) continue;
+            // scales of blocks b, b + 1: four rows each in words b and b + 1
+            const float f = factor_of(x < 2 ? vf01 : vf23, x & 1);
+            const float s0 = half_of(vs[2 * b + (x >> 1)], x & 1) * f;
+            const float s1 = half_of(vs[2 * b + 2 + (x >> 1)], x & 1) * f;
+            const uint4 lo = dequant8(vw[j], s0), hi = dequant8(vw[j], s1);
+            uint8_t *dst = a.v_planes + at + (row * HD + 32 * b + 4 * g) * 2;
+            *reinterpret_cast<uint2 *>(dst) = make_uint2(lo.x, lo.y);
+            *reinterpret_cast<uint2 *>(dst + 64) = make_uint2(hi.z, hi.w);
         }
     }
 }
@@ -221,7 +265,7 @@ cudaError_t launch_paged_gather(const PagedGatherArgs &a, int n_reqs, int hd,
     const int groups = (a.max_seq + kGroupRows - 1) / kGroupRows;
     const long long pairs = static_cast<long long>(n_reqs) * a.pages.n_kv;
     const int need = (groups + kThreads / 32 - 1) / (kThreads / 32);
-    const long long cap = std::max<long long>(1, device_sm_count() * 16ll / pairs);
+    const long long cap = std::max<long long>(1, device_sm_count() * 64ll / pairs);
     const dim3 grid(static_cast<unsigned>(std::min<long long>(need, cap)), a.pages.n_kv, n_reqs);
     auto kernel = hd == 64    ? paged_gather_kernel<64>
                   : hd == 128 ? paged_gather_kernel<128>

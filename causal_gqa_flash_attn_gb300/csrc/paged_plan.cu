@@ -21,61 +21,41 @@
 namespace fa {
 namespace {
 
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr unsigned kMost = 0x7fffffffu;  // where sums stop (bad lengths can pass 32 bits)
 
-struct PlanLen {
-    long long tokens;  // fresh tokens (in the packed batch, whatever becomes of them)
-    int need, back;    // pages to take from the ring, pages to return to it
-    bool bad;          // lengths out of range
+// Tokens of the packed batch (whatever becomes of them), pages to take from
+// the ring and pages to return to it.
+struct Len3 {
+    unsigned v[3];
+    bool bad;  // lengths out of range: no pages
 };
 
-__device__ __forceinline__ PlanLen plan_len(const PlanArgs &a, int r) {
-    const int c = __ldg(a.cached + r), f = __ldg(a.fresh + r);
-    PlanLen p{f > 0 ? f : 0, 0, 0, false};
-    const long long rows = static_cast<long long>(c) + p.tokens;
+__device__ __forceinline__ Len3 plan_len(const PlanArgs &a, int c, int f) {
+    Len3 p{{f > 0 ? static_cast<unsigned>(f) : 0u, 0u, 0u}, false};
+    const long long rows = static_cast<long long>(c) + p.v[0];
     p.bad = c < 0 || f < -1 || rows > static_cast<long long>(a.max_pages) << a.page_shift;
     if (p.bad) return p;
-    const int used = static_cast<int>((c + (1ll << a.page_shift) - 1) >> a.page_shift);
+    const unsigned mask = (1u << a.page_shift) - 1u;  // rows and the table's rows are below 2^30
+    const unsigned used = (static_cast<unsigned>(c) + mask) >> a.page_shift;
     if (f < 0)
-        p.back = used;
+        p.v[2] = used;
     else
-        p.need = static_cast<int>((rows + (1ll << a.page_shift) - 1) >> a.page_shift) - used;
+        p.v[1] = ((static_cast<unsigned>(rows) + mask) >> a.page_shift) - used;
     return p;
 }
 
-// Inclusive scan of three values over the block; returns this thread's
-// exclusive sums and the block totals.
-struct Sum3 {
-    long long v[3];
-};
-__device__ __forceinline__ Sum3 block_scan(Sum3 mine, Sum3 *total) {
-    __shared__ long long part[3][kPlanWarps];
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    Sum3 inc = mine;
+// a + b, at most kMost (both are): sums that stop there can be taken in any order.
+__device__ __forceinline__ unsigned add(unsigned a, unsigned b) { return min(a + b, kMost); }
+
+__device__ __forceinline__ unsigned warp_scan(unsigned x) {  // inclusive
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(~0u, inc.v[k], d);
-            if (lane >= d) inc.v[k] += o;
-        }
-        if (lane == 31) part[k][w] = inc.v[k];
+    for (int d = 1; d < 32; d <<= 1) {
+        const unsigned o = __shfl_up_sync(~0u, x, d);
+        if ((threadIdx.x & 31) >= d) x = add(x, o);
     }
-    __syncthreads();
-    Sum3 ex;
-#pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        long long base = 0, all = 0;
-#pragma unroll
-        for (int i = 0; i < kPlanWarps; ++i) {
-            if (i == w) base = all;
-            all += part[k][i];
-        }
-        ex.v[k] = base + inc.v[k] - mine.v[k];
-        total->v[k] = all;
-    }
-    return ex;
+    return x;
 }
 
 // The last index r < n with start[r] <= x (start[0] = 0 <= x).
@@ -88,57 +68,76 @@ __device__ __forceinline__ int find(const int *start, int n, int x) {
     return lo;
 }
 
-__device__ __forceinline__ int clip(long long x, int most) {
-    return static_cast<int>(x < most ? x : most);
-}
-
 __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     extern __shared__ int sm[];
     int *tok0 = sm, *need0 = sm + a.n_reqs + 1, *back0 = need0 + a.n_reqs + 1;
     const int R = a.n_reqs, N = a.n_pages;
-    // each thread sums a run of requests
-    const int per = (R + kPlanThreads - 1) / kPlanThreads;
-    const int r0 = min(R, static_cast<int>(threadIdx.x) * per), r1 = min(R, r0 + per);
     int head = __ldg(a.state), count = __ldg(a.state + 1);
     const bool bad_ring = head < 0 || head >= N || count < 0 || count > N;
     if (bad_ring) head = count = 0;  // hand out nothing, take nothing back
-    Sum3 mine{{0, 0, 0}}, total;
-    for (int r = r0; r < r1; ++r) {
-        const PlanLen p = plan_len(a, r);
-        mine.v[0] += p.tokens;
-        mine.v[1] += p.need;
-        mine.v[2] += p.back;
-    }
-    Sum3 at = block_scan(mine, &total);
-    const int most = 0x7fffffff;
+    // Each warp takes a run of requests, 32 at a time, and leaves the sums before
+    // each of them within its run; then the runs before it are added.
+    __shared__ unsigned part[3][kPlanWarps];
+    __shared__ unsigned taken_sh;
+    __shared__ int bad_sh;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per = ((R + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
+    const int r0 = min(R, warp * per), r1 = min(R, r0 + per);
+    if (threadIdx.x == 0) taken_sh = 0, bad_sh = 0;
+    int *const sums[3] = {tok0, need0, back0};
+    unsigned run[3] = {0, 0, 0};
     bool bad = false;
-    for (int r = r0; r < r1; ++r) {
-        const PlanLen p = plan_len(a, r);
+#pragma unroll 4
+    for (int b = r0; b < r1; b += 32) {
+        const int r = b + lane;
+        Len3 p{{0, 0, 0}, false};
+        if (r < r1) p = plan_len(a, __ldg(a.cached + r), __ldg(a.fresh + r));
         bad |= p.bad;
-        tok0[r] = clip(at.v[0], a.max_tokens);
-        need0[r] = clip(at.v[1], most);
-        back0[r] = clip(at.v[2], most);
-        at.v[0] += p.tokens;
-        at.v[1] += p.need;
-        at.v[2] += p.back;
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const unsigned inc = warp_scan(min(p.v[k], kMost));
+            // exclusive: the inclusive sum of the lane before
+            const unsigned ex = __shfl_up_sync(~0u, inc, 1);
+            if (r < r1) sums[k][r] = static_cast<int>(add(run[k], lane ? ex : 0u));
+            run[k] = add(run[k], __shfl_sync(~0u, inc, 31));
+        }
     }
-    // the pages handed out: those of the requests whose whole need is left
-    __shared__ int taken_sh;
+    if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) part[k][warp] = run[k];
+    __syncthreads();
+    if (bad) bad_sh = 1;
+    unsigned all[3], before[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+        const unsigned inc = warp_scan(part[k][lane]);
+        all[k] = __shfl_sync(~0u, inc, 31);
+        before[k] = warp ? __shfl_sync(~0u, inc, warp - 1) : 0u;
+    }
+    const unsigned room = static_cast<unsigned>(a.max_tokens);
+    for (int r = r0 + lane; r < r1; r += 32) {
+        tok0[r] = static_cast<int>(min(add(tok0[r], before[0]), room));
+        need0[r] = static_cast<int>(add(need0[r], before[1]));
+        back0[r] = static_cast<int>(add(back0[r], before[2]));
+    }
     if (threadIdx.x == 0) {
-        tok0[R] = clip(total.v[0], a.max_tokens);
-        need0[R] = clip(total.v[1], most);
-        back0[R] = clip(total.v[2], most);
-        taken_sh = 0;
+        tok0[R] = static_cast<int>(min(all[0], room));
+        need0[R] = static_cast<int>(all[1]);
+        back0[R] = static_cast<int>(all[2]);
     }
     __syncthreads();
-    for (int r = r0; r < r1; ++r)
-        if (need0[r + 1] > need0[r] && need0[r + 1] <= count) atomicMax(&taken_sh, need0[r + 1]);
+    // the pages handed out: those of the requests whose whole need is left
+    unsigned fits_to = 0;
+    for (int r = threadIdx.x; r < R; r += kPlanThreads)
+        if (need0[r + 1] > need0[r] && need0[r + 1] <= count)
+            fits_to = max(fits_to, static_cast<unsigned>(need0[r + 1]));
+    fits_to = __reduce_max_sync(~0u, fits_to);
+    if (lane == 0 && fits_to) atomicMax(&taken_sh, fits_to);
     __syncthreads();
-    const int taken = taken_sh;
+    const int taken = static_cast<int>(taken_sh);
     const int returned = bad_ring ? 0 : min(back0[R], N - count);
     if (blockIdx.x == 0) {
-        if (bad || (threadIdx.x == 0 &&
-                    (bad_ring || back0[R] > returned || total.v[0] > a.max_tokens)))
+        if (threadIdx.x == 0 && (bad_sh || bad_ring || back0[R] > returned || all[0] > room))
             flag_error(a.err, FA_ERRBIT_DEVICE);
         if (threadIdx.x == 0) {
             const int next = head + taken;
@@ -150,11 +149,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     }
     const int i0 = blockIdx.x * kPlanThreads + threadIdx.x, step = gridDim.x * kPlanThreads;
     for (int r = i0; r < R; r += step) {
-        const int c = __ldg(a.cached + r);
-        const PlanLen p = plan_len(a, r);
-        const bool fits = !p.bad && (p.need == 0 || need0[r + 1] <= count);
-        a.seq_lens[r] = p.bad || __ldg(a.fresh + r) < 0 ? 0
-                        : fits ? c + static_cast<int>(p.tokens) : c;
+        const int c = __ldg(a.cached + r), f = __ldg(a.fresh + r);
+        const Len3 p = plan_len(a, c, f);
+        const bool fits = !p.bad && (p.v[1] == 0 || need0[r + 1] <= count);
+        a.seq_lens[r] = p.bad || f < 0 ? 0
+                        : fits ? c + static_cast<int>(p.v[0]) : c;
         a.cu_fresh[r] = tok0[r];
     }
     const int mask = (1 << a.page_shift) - 1;
@@ -166,11 +165,11 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
         int slot = -1, pos = 0;
         if (t < tok0[R]) {
             const int r = find(tok0, R, t);
-            const PlanLen p = plan_len(a, r);
             const int c = __ldg(a.cached + r);
+            const Len3 p = plan_len(a, c, __ldg(a.fresh + r));
             if (!p.bad) {
                 pos = c + (t - tok0[r]);
-                if (p.need == 0 || need0[r + 1] <= count) {
+                if (p.v[1] == 0 || need0[r + 1] <= count) {
                     const int k = pos >> a.page_shift;
                     const int used = (c + mask) >> a.page_shift;
                     const int page =
