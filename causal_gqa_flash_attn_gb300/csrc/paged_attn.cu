@@ -15,8 +15,7 @@
 //   - A code c in bits 0-3 or 4-7 of a half word IS a binary16 subnormal, c *
 //     2^-24 or c * 2^-20, exact: one AND makes two operands. The factors 2^-24
 //     and 2^-20 are undone in q (by 2^-4) and at the end; the offset -8 enters as
-//     the accumulator's start (K), by a constant operand (V) or, for fp32 and
-//     fp16, by one packed addition.
+//     the accumulator's start (K) or by a constant operand (V).
 //   - The columns (N = 8) are 8 query rows of one kv head: the group's q heads,
 //     times as many tokens as fit ("row group").
 //   - V's block scales multiply the softmax weights (8 columns) instead of the
@@ -27,8 +26,12 @@
 //     passes it by 2^14 (kLift above the last maximum, up to binary16's range):
 //     one vote per tile instead of a reduction.
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
-// the scaled weights; their products go through a fresh accumulator per 16 rows
-// that fp32 adds collect, as the tensor core's own sums lose a step per addition.
+// the scaled weights. Their codes become (c - 8) * 2^-9 (one AND and one packed
+// multiply-add for two): the tensor core aligns a sum's terms by their
+// exponents and cuts them, so that subnormal operands, whose leading bits are
+// zeros, and an offset that is taken out later lose bits (outputs off by 3e-6
+// instead of 3e-7). Its sums lose a step towards zero per addition, too: a tile's
+// products with V go through a fresh accumulator that is added in fp32.
 //
 // Work split. The 16-row groups that are read, over all (request, kv head, row
 // group) units, are cut into equal runs, one per warp of one block per SM; a
@@ -65,6 +68,7 @@ constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 constexpr int kUnitCost = PA_UNIT;
 constexpr int kMinWork = PA_MIN;  // work per warp below which fewer warps work; > kUnitCost
 constexpr int kRows = 8;           // query rows of a row group
+constexpr int kMostBlocks = 256;   // blocks, whose warps' tasks the join lists
 constexpr int kMostWarps = 16;     // computing warps of a block that the workspace is made for
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
 
@@ -91,7 +95,7 @@ struct Cfg {
     static constexpr int RING = STAGES * STAGE;
     static constexpr int QF = NB * 32 * 16;           // q as B fragments
     static constexpr int QB = QF * (QSPLIT ? 2 : 1);  // and their low terms
-    static constexpr int BIAS = NB * 4 * 16;          // the accumulators' start, as lanes hold it
+    static constexpr int BIAS = QSPLIT ? 0 : NB * 4 * 16;  // the accumulators' start, as lanes hold it
     static constexpr int OFF_Q = WARPS * RING;
     static constexpr int OFF_BIAS = OFF_Q + WARPS * QB;
     static constexpr int OFF_BAR = OFF_BIAS + WARPS * BIAS;
@@ -138,6 +142,16 @@ __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_g
     }
     return q;
 }
+// The next request with queries, whose index goes into *r: there is one, as the
+// run goes on (and no reading past the last one, should lengths change meanwhile).
+__device__ __forceinline__ Req next_req(const PagedAttnArgs &a, int *r, int log_group) {
+    Req q;
+    do {
+        *r = min(*r + 1, a.n_reqs - 1);
+        q = load_req(a, *r, log_group);
+    } while (q.rgs == 0 && *r < a.n_reqs - 1);
+    return q;
+}
 // Groups of a unit: at least one, so that rows without any key are visited and
 // written too.
 __device__ __forceinline__ int unit_groups(const Req &q) { return max(q.ng, 1); }
@@ -174,14 +188,19 @@ __device__ __forceinline__ Cut make_cut(long long N, int blocks, int warps) {
 }
 
 // A unit that other blocks share, for the join: written by the warp whose run
-// holds its first group.
+// holds its first group. Where its pieces lie is one word:
+//   bits 0-8    the blocks that hold joined pieces (0: no task)
+//   bits 9-13   the warps of a block that work
+//   bits 14-26  1 + the warp (over all blocks) that begins its run with the unit's
+//               last piece and goes on, or 0
 struct Task {
-    int valid, h, rg;
-    int first, blocks, stride;  // partials of its joined pieces: `first`, and each later block's first
-    int tail;                   // and of the piece that begins the last warp's run, or -1
-    int next;                   // partial of the second block's piece
+    int h, rg;
     Req q;
 };
+__device__ __forceinline__ uint32_t pack_pieces(int blocks, int warps, int tail) {
+    return static_cast<uint32_t>(blocks) | static_cast<uint32_t>(warps) << 9 |
+           static_cast<uint32_t>(tail + 1) << 14;
+}
 // Where a part of the cut begins.
 struct Place {
     int r, unit, gi;   // its first group
@@ -189,14 +208,18 @@ struct Place {
     long long groups;  // groups before it
 };
 struct Ws {
-    Task *tasks;     // one per warp
+    uint32_t *pieces;   // [block][kMostWarps]: pack_pieces, or 0
+    Task *tasks;        // [block][kMostWarps]
     float *partial;  // two per warp: the end of its run, the start of its run
 };
+__host__ __device__ constexpr size_t ws_head(int blocks, size_t each) {
+    return (static_cast<size_t>(blocks) * kMostWarps * each + 255) / 256 * 256;
+}
 __host__ __device__ inline Ws carve(uint8_t *ws, int blocks) {
     Ws w;
-    w.tasks = reinterpret_cast<Task *>(ws);
-    w.partial = reinterpret_cast<float *>(
-        ws + (static_cast<size_t>(blocks) * kMostWarps * sizeof(Task) + 255) / 256 * 256);
+    w.pieces = reinterpret_cast<uint32_t *>(ws);
+    w.tasks = reinterpret_cast<Task *>(ws + ws_head(blocks, 4));
+    w.partial = reinterpret_cast<float *>(ws + ws_head(blocks, 4) + ws_head(blocks, sizeof(Task)));
     return w;
 }
 
@@ -263,11 +286,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
     return d;
 }
-__device__ __forceinline__ uint32_t hadd2(uint32_t a, uint32_t b) {
-    uint32_t d;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-    return d;
-}
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -303,10 +321,21 @@ __device__ __forceinline__ void mma0(float *d, uint32_t a0, uint32_t a1, uint32_
 
 // -8 * 2^-24 and -8 * 2^-20, twice.
 constexpr uint32_t kM8a = 0x80088008u, kM8b = 0x80808080u;
-// 2^-24 and 2^-20 come out of O's rows g and g + 8.
-constexpr float kUnshift0 = 16777216.0f, kUnshift1 = 1048576.0f;
+constexpr uint32_t kLo = 0x000f000fu, kHi = 0x00f000f0u;  // codes c * 2^-24, c * 2^-20
+
+// Two codes (bits 0-3, or 4-7, of each half of w) as (c - 8) * 2^-9: normal
+// numbers, from c * 2^-24 and c * 2^-20.
+__device__ __forceinline__ uint32_t minus8_lo(uint32_t w) {
+    return hfma2(w & kLo, 0x78007800u, 0xa400a400u);  // * 2^15 - 2^-6
+}
+__device__ __forceinline__ uint32_t minus8_hi(uint32_t w) {
+    return hfma2(w & kHi, 0x68006800u, 0xa400a400u);  // * 2^11 - 2^-6
+}
 
 // Row and head of a unit's column n; token < 0 past the unit's last row.
+__device__ __forceinline__ int log_group_of(const PagedAttnArgs &a) {
+    return 31 - __clz(a.n_q_heads / a.pages.n_kv);
+}
 struct Col {
     int token, head, pos;
 };
@@ -322,8 +351,10 @@ __device__ __forceinline__ Col column(const Req &q, int rg, int n, int h, int lo
 // The state of one piece: O, reference and weight sum of the lane's columns
 // 2 t and 2 t + 1 (O: dims 32 b + 4 g + 0, 2 in rows g of tiles 0, 1 and
 // 32 b + 4 g + 1, 3 in rows g + 8).
-template <int NB>
+template <int NB, bool SPLIT>
 struct State {
+    // the codes' factors come out of rows g and g + 8
+    static constexpr float U0 = SPLIT ? 512.0f : 16777216.0f, U1 = SPLIT ? 512.0f : 1048576.0f;
     float o[NB][2][4];
     float m[2], l[2];
     __device__ __forceinline__ void clear() {
@@ -336,8 +367,8 @@ struct State {
     }
     // four consecutive dims of column 2 t + c in block b
     __device__ __forceinline__ float4 quad(int b, int c) const {
-        return make_float4(o[b][0][c] * kUnshift0, o[b][0][2 + c] * kUnshift1,
-                           o[b][1][c] * kUnshift0, o[b][1][2 + c] * kUnshift1);
+        return make_float4(o[b][0][c] * U0, o[b][0][2 + c] * U1,
+                           o[b][1][c] * U0, o[b][1][2 + c] * U1);
     }
     __device__ __forceinline__ void sum_lanes() {
 #pragma unroll
@@ -395,7 +426,7 @@ struct Piece {
 // EDGE: not every row of the unit sees the (one) group whole; j0 is its first
 // key and pc says what is seen.
 template <typename C, int M, bool EDGE>
-__device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
+__device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
                                      const uint8_t *bias, float km0, float km1,
                                      const volatile Piece *pc, int j0, int sink, int win) {
     constexpr int NB = C::NB, HD = NB * 32;
@@ -430,20 +461,24 @@ __device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], 
         const uint4 qf = lds_v4(qs + (b * 32 + lane) * 16);
         uint4 lo = make_uint4(0, 0, 0, 0);
         if (C::QSPLIT) lo = lds_v4(qs + C::QF + (b * 32 + lane) * 16);
-        const float4 c0 = lds_f4(bias + (b * 4 + t) * 16);
+        float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (!C::QSPLIT) c0 = lds_f4(bias + (b * 4 + t) * 16);
 #pragma unroll
         for (int k = 0; k < M; ++k) {
-            float d[4] = {c0.x, c0.y, c0.z, c0.w};
             const uint32_t a = wA[k][b % KB], c = wB[k][b % KB], a8 = a >> 8, c8 = c >> 8;
-            const uint32_t e0 = a & 0x000f000fu, e1 = c & 0x000f000fu;
-            const uint32_t e2 = a & 0x00f000f0u, e3 = c & 0x00f000f0u;
-            const uint32_t f0 = a8 & 0x000f000fu, f1 = c8 & 0x000f000fu;
-            const uint32_t f2 = a8 & 0x00f000f0u, f3 = c8 & 0x00f000f0u;
-            mma(d, e0, e1, e2, e3, qf.x, qf.y);
-            mma(d, f0, f1, f2, f3, qf.z, qf.w);
+            float d[4];
             if (C::QSPLIT) {
-                mma(d, e0, e1, e2, e3, lo.x, lo.y);
+                const uint32_t e0 = minus8_lo(a), e1 = minus8_lo(c), e2 = minus8_hi(a), e3 = minus8_hi(c);
+                const uint32_t f0 = minus8_lo(a8), f1 = minus8_lo(c8);
+                const uint32_t f2 = minus8_hi(a8), f3 = minus8_hi(c8);
+                mma0(d, e0, e1, e2, e3, lo.x, lo.y);  // the low terms first: sums stay small
                 mma(d, f0, f1, f2, f3, lo.z, lo.w);
+                mma(d, e0, e1, e2, e3, qf.x, qf.y);
+                mma(d, f0, f1, f2, f3, qf.z, qf.w);
+            } else {
+                d[0] = c0.x, d[1] = c0.y, d[2] = c0.z, d[3] = c0.w;
+                mma(d, a & kLo, c & kLo, a & kHi, c & kHi, qf.x, qf.y);
+                mma(d, a8 & kLo, c8 & kLo, a8 & kHi, c8 & kHi, qf.z, qf.w);
             }
             const float2 uA = half2_f(sA[k][b % KB / 2]), uB = half2_f(sB[k][b % KB / 2]);
             const float a0 = b & 1 ? uA.y : uA.x, a1 = b & 1 ? uB.y : uB.x;
@@ -568,20 +603,12 @@ __device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], 
                 const uint32_t s01 = b & 1 ? vs[k].z : vs[k].x, s23 = b & 1 ? vs[k].w : vs[k].y;
                 const uint32_t p0 = b0[k0 + k], p1 = b1[k0 + k];
                 const uint32_t w0 = hmul2(p0, s01), w1 = hmul2(p1, s23);
-                const uint32_t e0 = x01 & 0x000f000fu, e1 = x01 & 0x00f000f0u;
-                const uint32_t e2 = x23 & 0x000f000fu, e3 = x23 & 0x00f000f0u;
-                const uint32_t f0 = z01 & 0x000f000fu, f1 = z01 & 0x00f000f0u;
-                const uint32_t f2 = z23 & 0x000f000fu, f3 = z23 & 0x00f000f0u;
                 if (C::PSPLIT) {
                     // the product's low term, exact but for the weight's own low term
                     const uint32_t v0 = hfma2(l0[k0 + k], s01, hfms2(p0, s01, w0));
                     const uint32_t v1 = hfma2(l1[k0 + k], s23, hfms2(p1, s23, w1));
-                    // c - 8 exactly: the tensor core's sums lose a step towards zero per
-                    // addition, which an offset taken out afterwards would leave behind
-                    const uint32_t g0 = hadd2(e0, kM8a), g1 = hadd2(e1, kM8b);
-                    const uint32_t g2 = hadd2(e2, kM8a), g3 = hadd2(e3, kM8b);
-                    const uint32_t h0 = hadd2(f0, kM8a), h1 = hadd2(f1, kM8b);
-                    const uint32_t h2 = hadd2(f2, kM8a), h3 = hadd2(f3, kM8b);
+                    const uint32_t g0 = minus8_lo(x01), g1 = minus8_hi(x01), g2 = minus8_lo(x23), g3 = minus8_hi(x23);
+                    const uint32_t h0 = minus8_lo(z01), h1 = minus8_hi(z01), h2 = minus8_lo(z23), h3 = minus8_hi(z23);
                     if (k == 0) {
                         mma0(u, g0, g1, g2, g3, v0, v1);
                         mma0(v, h0, h1, h2, h3, v0, v1);
@@ -592,8 +619,8 @@ __device__ __forceinline__ void step(State<C::NB> &st, uint8_t *const (&kp)[M], 
                     mma(u, g0, g1, g2, g3, w0, w1);
                     mma(v, h0, h1, h2, h3, w0, w1);
                 } else {
-                    mma(st.o[b][0], e0, e1, e2, e3, w0, w1);
-                    mma(st.o[b][1], f0, f1, f2, f3, w0, w1);
+                    mma(st.o[b][0], x01 & kLo, x01 & kHi, x23 & kLo, x23 & kHi, w0, w1);
+                    mma(st.o[b][1], z01 & kLo, z01 & kHi, z23 & kLo, z23 & kHi, w0, w1);
                     mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
                     mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
                 }
@@ -615,15 +642,16 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     constexpr int NB = C::NB, S = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan_part[2][C::WARPS + 1];
-    __shared__ int start_r[C::WARPS + 1];                // the request in which part i begins,
-    __shared__ long long start_x[2][C::WARPS + 1];       // and what lies before it (measure, groups)
+    __shared__ int start_r[C::WARPS + 1], start_n[C::WARPS + 1];  // the request in which part i
+                                                                  // begins, groups of its units
+    __shared__ long long start_x[2][C::WARPS + 1];  // and what lies before it (measure, groups)
     __shared__ Piece pieces[C::WARPS];
     __shared__ int abort_flag;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int n_kv = a.pages.n_kv, page_groups = n_kv * a.pages.groups;
-    const int log_group = 31 - __clz(a.n_q_heads / n_kv);
+    const int log_group = log_group_of(a);
     uint8_t *ring = smem + warp * C::RING;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);  // [warp][stage]
     uint64_t *bars = full + min(warp, C::WARPS - 1) * S;
@@ -645,13 +673,15 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     const int per = (a.n_reqs + C::THREADS - 1) / C::THREADS;
     const int r0 = min(a.n_reqs, tid * per), r1 = min(a.n_reqs, r0 + per);
     long long work = 0, count = 0;  // measure and groups
+    int of_unit = 1;                // groups of a unit of the last request
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
         const Req q = load_req(a, r, log_group);
+        of_unit = unit_groups(q);
         const long long units = static_cast<long long>(q.rgs) * n_kv;
         bad |= q.bad;
-        work += units * (unit_groups(q) + kUnitCost);
-        count += units * unit_groups(q);
+        work += units * (of_unit + kUnitCost);
+        count += units * of_unit;
     }
     if (bad && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
     long long inc = work, inc_g = count;
@@ -683,7 +713,8 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                 long long n = work, ng = count;
                 if (per > 1) {
                     const Req q = load_req(a, r, log_group);
-                    ng = static_cast<long long>(q.rgs) * n_kv * unit_groups(q);
+                    of_unit = unit_groups(q);
+                    ng = static_cast<long long>(q.rgs) * n_kv * of_unit;
                     n = ng + static_cast<long long>(q.rgs) * n_kv * kUnitCost;
                 }
                 const long long lo = x - s0, hi = x + n - s0;
@@ -691,6 +722,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     const long long s = cut.start(blockIdx.x, i) - s0;
                     if (lo <= s && s < hi) {
                         start_r[i] = r;
+                        start_n[i] = of_unit;
                         start_x[0][i] = x;
                         start_x[1][i] = xg;
                     }
@@ -710,7 +742,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         p.groups = all_groups;
         if (s >= N) return p;
         p.r = start_r[i];
-        const int n = unit_groups(load_req(a, p.r, log_group));
+        const int n = start_n[i];
         const long long off = s - start_x[0][i];
         p.unit = off < n + kUnitCost ? 0 : static_cast<int>(quotient(off, n + kUnitCost));
         const int at = static_cast<int>(off - static_cast<long long>(p.unit) * (n + kUnitCost));
@@ -793,7 +825,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         if (++unit == units) {
                             unit = 0;
                             Req q;
-                            do q = load_req(a, ++r, log_group); while (q.rgs == 0);
+                            q = next_req(a, &r, log_group);
                             enter(q);
                         }
                         head = unit / rgs * a.pages.groups;
@@ -816,11 +848,11 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
 
     volatile Piece *pc = pieces + min(warp, C::WARPS - 1);
-    State<NB> st;
+    State<NB, C::PSPLIT> st;
     st.clear();
     if (warp < C::WARPS) {
         if (lane == 0) {
-            ws.tasks[blockIdx.x * C::WARPS + warp].valid = 0;
+            ws.pieces[blockIdx.x * kMostWarps + warp] = 0;
             pc->fin_unit = -1;
             pc->todo = 0;
         }
@@ -875,7 +907,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                 const float lift = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
                 const float mul = a.scale * kLog2e *
                                   __uint_as_float(static_cast<uint32_t>(127 - up) << 23) *
-                                  16777216.0f;  // 2^24
+                                  (C::QSPLIT ? 512.0f : 16777216.0f);  // 2^9, 2^24
                 km[0] = __shfl_sync(~0u, mul, 8 * t);
                 km[1] = __shfl_sync(~0u, mul, 8 * t + 4);
 #pragma unroll
@@ -885,28 +917,26 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     uint32_t hi[4], lo[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float u = x[i] * lift, v = x[i + 4] * lift, sc = i & 1 ? 0.0625f : 1.0f;
+                        const float u = x[i] * lift, v = x[i + 4] * lift;
                         hi[i] = pack_half2(u, v);
                         const float2 f = half2_f(hi[i]);
-                        if (i & 1) hi[i] = pack_half2(f.x * sc, f.y * sc);
-                        lo[i] = pack_half2((u - f.x) * sc, (v - f.y) * sc);
+                        if (!C::QSPLIT && (i & 1)) hi[i] = pack_half2(f.x * 0.0625f, f.y * 0.0625f);
+                        lo[i] = pack_half2(u - f.x, v - f.y);
                     }
                     *reinterpret_cast<uint4 *>(qs + (b * 32 + lane) * 16) =
                         make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (C::QSPLIT)
+                    if (C::QSPLIT) {
                         *reinterpret_cast<uint4 *>(qs + C::QF + (b * 32 + lane) * 16) =
                             make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    // -8 times the block's sum, where the accumulators start: "code -8" in every row
-                    float d[4];
-                    mma0(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
-                    mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
-                    if (C::QSPLIT) {
-                        mma(d, kM8a, kM8a, kM8b, kM8b, lo[0], lo[1]);
-                        mma(d, kM8a, kM8a, kM8b, kM8b, lo[2], lo[3]);
+                    } else {
+                        // -8 times the block's sum, where the accumulators start: "code -8" in every row
+                        float d[4];
+                        mma0(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
+                        mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
+                        if (g == 0)
+                            *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) =
+                                make_float4(d[0], d[1], d[2], d[3]);
                     }
-                    if (g == 0)
-                        *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) =
-                            make_float4(d[0], d[1], d[2], d[3]);
                 }
                 const int p_min = q.rows - q.nq + ((rg * kRows) >> log_group);
                 const int p_max = q.rows - q.nq +
@@ -1010,7 +1040,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                     int next = unit + 1, nr = r;
                     if (next == q.rgs * n_kv) {
                         next = 0;
-                        while (load_req(a, ++nr, log_group).rgs == 0) {}
+                        next_req(a, &nr, log_group);
                     }
                     pc->r = nr;
                     pc->unit = next;
@@ -1068,9 +1098,9 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     if (from_start && !direct && warp == w0 && lane == 0) {
         const int e = cut.warp_of(last - 1);  // the warp that holds the unit's last group
         const bool tail = cut.start(e / cut.A, e % cut.A + 1) > last + kUnitCost;  // whose run goes on
-        ws.tasks[blockIdx.x * C::WARPS + warp] =
-            Task{1, h, rg, id0 * 2, (tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1,
-                 cut.A * 2, tail ? e * 2 + 1 : -1, static_cast<int>(blockIdx.x + 1) * cut.A * 2, q};
+        ws.pieces[blockIdx.x * kMostWarps + warp] =
+            pack_pieces((tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1, cut.A, tail ? e : -1);
+        ws.tasks[blockIdx.x * kMostWarps + warp] = Task{h, rg, q};
     }
     if (!direct && warp == w0 && g == 0) {
 #pragma unroll
@@ -1101,46 +1131,95 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
 }
 
-// One block for each of the first kernel: the units that begin in its runs and
-// that it could not finish. A warp takes one (unit, block of 32 dims, column
-// half) after another; a unit's pieces are added in ascending order.
-constexpr int kJoinThreads = 512;
+// The units that no block of the first kernel could finish, each as items (block
+// of 32 dims, column half) that are shared out over all blocks, one a warp. Where
+// a block gets fewer items than it has warps, several take slices of an item's
+// pieces: a long request in a small batch is in many. When a block took the units
+// that begin in its own runs, one request of 70000 rows (152 pieces) took 29 us
+// instead of 17, 128 windowed requests of all lengths 24 instead of 21, and 32
+// equal ones, where there is nothing to even out, 20.5 instead of 21.9. The pieces
+// of a slice are added in ascending order, and so are the slices.
+constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
 template <typename T, int HD>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs a) {
     using C = Cfg<T, HD>;
     constexpr int ITEMS = 2 * C::NB, BATCH = 8;
-    __shared__ Task tasks[C::WARPS];
-    __shared__ int n_tasks;
+    __shared__ int counts[kJoinWarps];
+    constexpr int MOST = kMostBlocks * kMostWarps;
+    __shared__ uint32_t list[MOST], where[MOST];  // tasks: their words, and whose they are
+    static_assert(kMostBlocks <= kJoinThreads && kMostBlocks < 512 && kMostBlocks * kMostWarps < 8191 &&
+                      kMostWarps < 32 && kMostWarps % 4 == 0,
+                  "a thread reads a block's words, whose fields hold these");
+    __shared__ float4 part_o[kJoinWarps][32];
+    __shared__ float part_m[kJoinWarps][kRows / 2], part_l[kJoinWarps][kRows / 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Ws ws = carve(a.workspace, gridDim.x);
-    if (threadIdx.x < 32) {
-        const int i = threadIdx.x;
-        const Task *k = ws.tasks + blockIdx.x * C::WARPS + i;
-        const bool valid = i < C::WARPS && k->valid;
-        const unsigned all = __ballot_sync(~0u, valid);
-        if (valid) tasks[__popc(all & ((1u << i) - 1u))] = *k;
-        if (i == 0) n_tasks = __popc(all);
+    // the tasks, in order of the warps
+    unsigned has = 0;
+    uint32_t words[kMostWarps];
+    if (threadIdx.x < gridDim.x) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(ws.pieces + threadIdx.x * kMostWarps);
+#pragma unroll
+        for (int i = 0; i < kMostWarps / 4; ++i) {
+            const uint4 f = src[i];
+            words[4 * i] = f.x; words[4 * i + 1] = f.y; words[4 * i + 2] = f.z; words[4 * i + 3] = f.w;
+        }
+#pragma unroll
+        for (int i = 0; i < C::WARPS; ++i) has |= (words[i] ? 1u : 0u) << i;
     }
+    int before = __popc(has);  // inclusive, then exclusive
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(~0u, before, d);
+        if (lane >= d) before += o;
+    }
+    if (lane == 31) counts[warp] = before;
     __syncthreads();
-    const int log_group = 31 - __clz(a.n_q_heads / a.pages.n_kv);
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    for (int j = threadIdx.x >> 5; j < n_tasks * ITEMS; j += kJoinThreads / 32) {
-        const Task &k = tasks[j / ITEMS];
-        const int i = j % ITEMS, b = i >> 1, n = 2 * t + (i & 1);
-        const int pieces = k.blocks + (k.tail >= 0);
+    const int of_warp = lane < kJoinWarps ? counts[lane] : 0;
+    const int n_tasks = __reduce_add_sync(~0u, of_warp);
+    before += __reduce_add_sync(~0u, lane < warp ? of_warp : 0) - __popc(has);
+#pragma unroll
+    for (int i = 0; i < C::WARPS; ++i)
+        if (has >> i & 1) {
+            where[before] = threadIdx.x * kMostWarps + i;
+            list[before++] = words[i];
+        }
+    __syncthreads();
+    if (n_tasks == 0) return;
+    const int items = n_tasks * ITEMS;
+    const int mine = (items + gridDim.x - 1) / gridDim.x;
+    const int j0 = blockIdx.x * mine, j1 = min(items, j0 + mine);
+    // slices of an item: the largest power of two with slices * mine <= kJoinWarps, or 1
+    const int log_slices = mine <= 1 ? 4 : mine <= 2 ? 3 : mine <= 4 ? 2 : mine <= 8 ? 1 : 0;
+    static_assert(kJoinWarps == 16, "log_slices");
+    const int slices = 1 << log_slices, at_once = kJoinWarps >> log_slices, slice = warp & (slices - 1);
+    for (int jb = j0; jb < j1; jb += at_once) {  // the same turns for every warp of the block
+        const int j = jb + (warp >> log_slices);
+        const bool in = j < j1;
+        const int nth = static_cast<unsigned>(in ? j : jb) / ITEMS;
+        const uint32_t id = where[nth], word = list[nth];
+        const int i = (in ? j : jb) & (ITEMS - 1), b = i >> 1, n = 2 * t + (i & 1);
+        const Task k = ws.tasks[id];
+        const int block = id / kMostWarps, blocks = word & 511u, warps = word >> 9 & 31u;
+        const int tail = static_cast<int>(word >> 14) - 1, pieces = blocks + (tail >= 0);
+        // this slice's pieces
+        const int e0 = pieces * slice >> log_slices, e1 = pieces * (slice + 1) >> log_slices;
         auto piece = [&](int e) {
-            const int slot = e == 0 ? k.first : e < k.blocks ? k.next + (e - 1) * k.stride : k.tail;
+            const int slot = e == 0       ? (block * warps + static_cast<int>(id % kMostWarps)) * 2
+                             : e < blocks ? (block + e) * warps * 2
+                                          : tail * 2 + 1;
             return ws.partial + static_cast<size_t>(slot) * C::PARTIAL;
         };
         float M = kLowest, L = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int e0 = 0; e0 < pieces; e0 += BATCH) {
+        for (int eb = e0; in && eb < e1; eb += BATCH) {
             float m[BATCH], l[BATCH];
             float4 y[BATCH];
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
-                const float *p = piece(min(e0 + e, pieces - 1));
+                const float *p = piece(min(eb + e, e1 - 1));
                 m[e] = p[n];
                 l[e] = p[kRows + n];
                 y[e] = *reinterpret_cast<const float4 *>(p + 2 * kRows + (i * 32 + lane) * 4);
@@ -1154,7 +1233,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
             x = scaled(x, s);
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
-                if (e0 + e >= pieces) continue;
+                if (eb + e >= e1) continue;
                 const float f = ex2(m[e] - top);
                 L = fmaf(l[e], f, L);
                 x.x = fmaf(y[e].x, f, x.x);
@@ -1163,7 +1242,28 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                 x.w = fmaf(y[e].w, f, x.w);
             }
         }
-        write_row<T>(a, column(k.q, k.rg, n, k.h, log_group), HD, 32 * b + 4 * g, x, M, L);
+        if (slices > 1) {
+            __syncthreads();  // the turn before has been read
+            part_o[warp][lane] = x;
+            if (g == 0) {
+                part_m[warp][t] = M;
+                part_l[warp][t] = L;
+            }
+            __syncthreads();
+            if (slice == 0) {
+                for (int s = 1; s < slices; ++s) {
+                    const float m = part_m[warp + s][t], top = fmaxf(M, m);
+                    const float f0 = ex2(M - top), f1 = ex2(m - top);
+                    const float4 y = part_o[warp + s][lane];
+                    M = top;
+                    L = fmaf(part_l[warp + s][t], f1, L * f0);
+                    x = make_float4(fmaf(y.x, f1, x.x * f0), fmaf(y.y, f1, x.y * f0),
+                                    fmaf(y.z, f1, x.z * f0), fmaf(y.w, f1, x.w * f0));
+                }
+            }
+        }
+        if (in && slice == 0)
+            write_row<T>(a, column(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
     }
 }
 
@@ -1196,7 +1296,7 @@ cudaError_t launch(const PagedAttnArgs &a, cudaStream_t stream) {
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e == cudaSuccess && dev < 64) made.fetch_or(1ull << dev, std::memory_order_release);
     }
-    const int blocks = device_sm_count();
+    const int blocks = std::min(device_sm_count(), kMostBlocks);
     if (e == cudaSuccess)
         e = launch_after(paged_attn_kernel<T, HD>, blocks, C::THREADS, C::SMEM, stream, a);
     if (e == cudaSuccess)
@@ -1215,7 +1315,8 @@ cudaError_t launch_type(const PagedAttnArgs &a, int hd, cudaStream_t stream) {
 
 size_t paged_attn_ws_bytes(int hd) {
     const size_t warps = static_cast<size_t>(device_sm_count()) * kMostWarps;
-    return (warps * sizeof(Task) + 255) / 256 * 256 + warps * 2 * (2 * kRows + kRows * hd) * 4;
+    return ws_head(device_sm_count(), 4) + ws_head(device_sm_count(), sizeof(Task)) +
+           warps * 2 * (2 * kRows + kRows * hd) * 4;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream) {
