@@ -29,7 +29,8 @@ int page_shift(int page_rows) {
 fa_status check_geometry(int n_kv_heads, int head_dim, int page_rows) {
     if (n_kv_heads < 1 || head_dim < 32 || head_dim % 32 || page_shift(page_rows) < 0)
         return FA_ERR_INVALID;
-    if (head_dim != 64 && head_dim != 128 && head_dim != 256) return FA_ERR_UNSUPPORTED;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || n_kv_heads > 65535)
+        return FA_ERR_UNSUPPORTED;
     return FA_OK;
 }
 
@@ -89,7 +90,7 @@ fa_status fa_page_plan(const int32_t *cached, const int32_t *fresh, int n_reqs,
         !aligned4(ring_state_out) || !aligned4(block_table) || !aligned4(seq_lens) ||
         !aligned4(cu_fresh) || !aligned4(slot_map) || !aligned4(positions))
         return FA_ERR_INVALID;
-    if (ring_state == ring_state_out || cached == seq_lens || fresh == seq_lens)
+    if (ring_state == ring_state_out || (n_reqs > 0 && (cached == seq_lens || fresh == seq_lens)))
         return FA_ERR_INVALID;
     fa::PlanArgs a;
     a.cached = cached;
@@ -237,7 +238,7 @@ fa_status fa_paged_gather(const void *pages, int n_pages, const int32_t *block_t
     if (st != FA_OK) return st;
     if (n_reqs < 0 || max_seq < 1 || !good_pages(n_pages, max_pages, page_rows))
         return FA_ERR_INVALID;
-    if (n_reqs > 65535 || n_kv_heads > 65535) return FA_ERR_UNSUPPORTED;
+    if (n_reqs > 65535) return FA_ERR_UNSUPPORTED;
     if (n_reqs == 0) return FA_OK;
     if (!pages || !block_table || !seq_lens || !k_planes || !v_planes || !aligned(pages, 16) ||
         !aligned4(block_table) || !aligned4(seq_lens) || !aligned(k_planes, 16) ||
@@ -288,6 +289,7 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
         !row_aligned(q, q_stride, dtype) || !row_aligned(out, out_stride, dtype))
         return FA_ERR_INVALID;
     if (workspace_bytes < fa::paged_attn_ws_bytes(head_dim)) return FA_ERR_WORKSPACE;
+    if (q == out) return FA_ERR_INVALID;  // a row's q may be read after its neighbours' out is written
     fa::PagedAttnArgs a;
     a.q = q;
     a.out = out;

@@ -394,7 +394,8 @@ enum { FA_T_F32 = 0, FA_T_F16 = 1, FA_T_BF16 = 2 };
  * and a value is (code - 8) * scale * factor, the product in fp32. The encoder
  * is that of FA_KV_Q4_0 (d = amax / -8, code = clamp(round_half_even(x / d) +
  * 8, 0, 15) with the fp32 reciprocal 1 / d), with the row's largest |d| brought
- * into [1, 2) by the factor: rows of any magnitude keep their precision.
+ * into [1, 2) by the factor: rows of any magnitude keep their precision. As
+ * there, a NaN is stored as 0, and an infinity makes its block's values NaN.
  *
  * Byte order inside a part (nb = head_dim / 32, row r = 0..15, block b, dims
  * counted from 0 inside a block; the lower dim has the lower 4 bits of a byte):
@@ -519,7 +520,7 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  * chunks.
  *   q          token t's heads start at element t * q_stride, [n_q_heads]
  *              [head_dim] values of dtype; 16-byte aligned rows.
- *   out        written, the same layout with out_stride.
+ *   out        written, the same layout with out_stride; may not overlap an input.
  *   lse        [n_q_heads][n_tokens] fp32 (device) or NULL, written: the natural
  *              log-sum-exp of each row's scores (-inf where nothing is attended).
  *   cu_q       [n_reqs + 1] int32 (device), not decreasing: request r's queries
@@ -535,14 +536,16 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  *   workspace  >= fa_paged_attn_workspace_bytes(head_dim), 16-byte aligned; scratch.
  *              Calls that share a workspace must not overlap on the GPU.
  * A row that attends nothing gives 0 (lse -inf). Scores, softmax and sums are
- * fp32. With FA_T_F32 every product is exact to about 2^-21; with FA_T_F16 and
- * FA_T_BF16 the softmax weights are rounded to binary16 before the product with
- * V, once for FA_T_BF16 and as a pair of terms (about 2^-21) for FA_T_F16.
+ * fp32. With FA_T_F32 queries and the softmax weights of V's products are pairs
+ * of binary16 terms, and so are the weights with FA_T_F16 (both exact to about
+ * 2^-21); with FA_T_BF16 a weight is rounded to binary16, and again after its
+ * product with V's block scale.
  * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_reqs <= 65536,
  * n_tokens <= 2^26, n_tokens * n_q_heads <= 2^30.
  * FA_ERR_DEVICE is flagged for a request whose cu_q or seq_lens are out of range
  * (its rows are not written), and for a table entry outside [0, n_pages) (its
- * rows count as not attended). */
+ * rows count as not attended), and for requests of more than 2^30 16-row groups
+ * an SM in all (nothing is written). */
 fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
                         int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
                         const int32_t *block_table, int max_pages, const void *pages, int n_pages,

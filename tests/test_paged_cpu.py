@@ -130,6 +130,8 @@ def test_attn_refusals(fa):
     for bad in (dict(hd=96), dict(hq=24), dict(hq=64), dict(n_reqs=65537)):
         assert call(**bad) == fa.ERR_UNSUPPORTED, bad
     assert call(wsb=fa.paged_attn_workspace_bytes(64) - 1) == fa.ERR_WORKSPACE
+    assert call(q=32, out=32) == fa.ERR_INVALID           # in place
+    assert call(hq=1 << 17, hkv=1 << 16, qs=1 << 23, os=1 << 23, n_tokens=1) == fa.ERR_UNSUPPORTED
     assert call(n_reqs=0) == fa.OK
     assert call(n_tokens=0) == fa.OK
     for hd in (64, 128, 256):
