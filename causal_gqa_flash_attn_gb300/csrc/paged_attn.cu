@@ -17,7 +17,7 @@
 //     and 2^-20 are undone in q (by 2^-4) and at the end; the offset -8 enters as
 //     the accumulator's start (K) or by a constant operand (V).
 //   - The columns (N = 8) are 8 query rows of one kv head: the group's q heads,
-//     times as many tokens as fit ("row group").
+//     times as many tokens as fit ("row group"; 16 rows where 16 heads share).
 //   - V's block scales multiply the softmax weights (8 columns) instead of the
 //     codes; each V row's power-of-two factor 2^e is added to its score's
 //     exponent, so the scaled weights stay in binary16's range whatever the
@@ -59,56 +59,46 @@ constexpr float kLift = 6.0f;      // log2 of the largest weight right after a m
 constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 // The start and end of a unit (its rows of q as operands, its output) cost a
 // warp about as much as kUnitCost groups: 6000 against 2200 cycles.
-#ifndef PA_UNIT
-#define PA_UNIT 3
-#endif
-#ifndef PA_MIN
-#define PA_MIN 6
-#endif
-constexpr int kUnitCost = PA_UNIT;
-constexpr int kMinWork = PA_MIN;  // work per warp below which fewer warps work; > kUnitCost
-constexpr int kRows = 8;           // query rows of a row group
+constexpr int kUnitCost = 3;
+constexpr int kMinWork = 6;       // work per warp below which fewer warps work; > kUnitCost
 constexpr int kMostBlocks = 256;   // blocks, whose warps' tasks the join lists
 constexpr int kMostWarps = 16;     // computing warps of a block that the workspace is made for
 constexpr float kLn2 = 0.693147180559945309f, kLog2e = 1.442695040888963407f;
 
-template <typename T, int HD>
+template <typename T, int HD, int NT_>
 struct Cfg {
+    static constexpr int NT = NT_, ROWS = 8 * NT;  // columns of a unit, in eights and all
     static constexpr bool QSPLIT = sizeof(T) == 4;
     static constexpr bool PSPLIT = !std::is_same<T, __nv_bfloat16>::value;
     static constexpr int NB = HD / 32;
     static constexpr int GB = group_bytes(HD);
-    // Warps that compute (and one more that copies): what the registers of one
-    // block per SM allow without spills. Groups that are taken at once (TILE),
-    // and tiles of a warp's ring.
-#ifdef PA_WARPS
-    static constexpr bool PP = sizeof(T) == PA_SIZE && HD == PA_HD;
-    static constexpr int WARPS = PP ? PA_WARPS : 7;
-    static constexpr int TILE = PP ? PA_TILE : 1;
-    static constexpr int STAGES = PP ? PA_STAGES : 2;
-#else
-    static constexpr int WARPS = HD == 256 || (PSPLIT && HD == 128) ? 11 : 15;
-    static constexpr int TILE = HD == 256 ? 1 : HD == 128 ? 2 : 4;
-    static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : 2;
-#endif
+    // Warps that compute (and one more that copies), groups that are taken at once (TILE) and
+    // tiles of a warp's ring, as measured: as many warps as have registers for their state, and
+    // tiles that give the copying warp few copies to issue. Head_dim 256, bf16: 11 warps 109 us
+    // (32 x 32768 rows, 2 kv heads), 15 112, 7 130, 11 with tiles of 2 114; head_dim 128, fp32: 11
+    // warps 82 us (32 x 16384 rows, 4 kv heads), 15 with single groups 84; head_dim 64, bf16:
+    // single groups 124 us (64 x 16384 rows, 4 kv heads), tiles of 4 68.
+    static constexpr int WARPS = HD == 256 || (HD == 128 ? PSPLIT || NT == 2 : PSPLIT && NT == 2) ? 11 : 15;
+    static constexpr int TILE = HD == 256 ? 1 : HD == 128 || NT == 2 ? 2 : 4;
+    static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : HD == 64 && NT == 2 ? 4 : 2;
     static constexpr int STAGE = TILE * GB;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int QF = NB * 32 * 16;           // q as B fragments
-    static constexpr int QB = QF * (QSPLIT ? 2 : 1);  // and their low terms
-    static constexpr int BIAS = QSPLIT ? 0 : NB * 4 * 16;  // the accumulators' start, as lanes hold it
+    static constexpr int QB = QF * NT * (QSPLIT ? 2 : 1);  // of each eight, and their low terms
+    static constexpr int BIAS = QSPLIT ? 0 : NT * NB * 4 * 16;  // the accumulators' start, as lanes hold it
     static constexpr int OFF_Q = WARPS * RING;
     static constexpr int OFF_BIAS = OFF_Q + WARPS * QB;
     static constexpr int OFF_BAR = OFF_BIAS + WARPS * BIAS;
     static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 8;
     static constexpr int SMEM = OFF_DEAD + WARPS * STAGES * 4;
     static constexpr int THREADS = (WARPS + 1) * 32;
-    // a partial: m and l of 8 rows, then O as the lanes hold it
-    static constexpr int PARTIAL = 2 * kRows + kRows * HD;  // floats
+    // a partial: m and l of the rows, then O as the lanes hold it
+    static constexpr int PARTIAL = 2 * ROWS + ROWS * HD;  // floats
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
     static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
     static_assert(kMinWork > kUnitCost, "a part of the cut has a group, but for a block's last");
     static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
-    static_assert(RING >= kRows * HD * 4, "a warp's O fits its ring");
+    static_assert(RING >= ROWS * HD * 4, "a warp's O fits its ring");
     static_assert(SMEM <= 224 * 1024, "shared memory");
 };
 
@@ -120,6 +110,7 @@ struct Req {
     bool bad;
 };
 
+template <int ROWS>
 __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_group) {
     Req q;
     q.q0 = __ldg(a.cu_q + r);
@@ -128,7 +119,7 @@ __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_g
     const long long room = static_cast<long long>(a.pages.max_pages) * a.pages.groups * kGroupRows;
     q.bad = q.q0 < 0 || q1 < q.q0 || q1 > a.n_tokens || q.rows < 0 || q.rows > room;
     q.nq = q.bad ? 0 : q1 - q.q0;
-    q.rgs = static_cast<int>(((static_cast<long long>(q.nq) << log_group) + kRows - 1) / kRows);
+    q.rgs = static_cast<int>(((static_cast<long long>(q.nq) << log_group) + ROWS - 1) / ROWS);
     const int all = (q.rows + kGroupRows - 1) / kGroupRows;
     q.ns = q.skip = 0;
     q.ng = all;
@@ -144,11 +135,12 @@ __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_g
 }
 // The next request with queries, whose index goes into *r: there is one, as the
 // run goes on (and no reading past the last one, should lengths change meanwhile).
+template <int ROWS>
 __device__ __forceinline__ Req next_req(const PagedAttnArgs &a, int *r, int log_group) {
     Req q;
     do {
         *r = min(*r + 1, a.n_reqs - 1);
-        q = load_req(a, *r, log_group);
+        q = load_req<ROWS>(a, *r, log_group);
     } while (q.rgs == 0 && *r < a.n_reqs - 1);
     return q;
 }
@@ -297,6 +289,10 @@ __device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
     asm("{.reg .b32 n; neg.f16x2 n, %3; fma.rn.f16x2 %0, %1, %2, n;}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
+// All bits of each half that is not zero (or a NaN).
+__device__ __forceinline__ uint32_t not_zero2(uint32_t h) {
+    return (h & 0x7fffu ? 0xffffu : 0u) | (h & 0x7fff0000u ? 0xffff0000u : 0u);
+}
 __device__ __forceinline__ float2 half2_f(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
@@ -332,6 +328,17 @@ __device__ __forceinline__ uint32_t minus8_hi(uint32_t w) {
     return hfma2(w & kHi, 0x68006800u, 0xa400a400u);  // * 2^11 - 2^-6
 }
 
+// A count in shared memory from warp to warp: what its writer did before is done
+// for who reads it.
+__device__ __forceinline__ void release_s32(volatile int *p, int v) {
+    asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(const_cast<int *>(p))), "r"(v) : "memory");
+}
+__device__ __forceinline__ int acquire_s32(volatile int *p) {
+    int v;
+    asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(const_cast<int *>(p))) : "memory");
+    return v;
+}
+
 // Row and head of a unit's column n; token < 0 past the unit's last row.
 __device__ __forceinline__ int log_group_of(const PagedAttnArgs &a) {
     return 31 - __clz(a.n_q_heads / a.pages.n_kv);
@@ -339,8 +346,9 @@ __device__ __forceinline__ int log_group_of(const PagedAttnArgs &a) {
 struct Col {
     int token, head, pos;
 };
+template <int ROWS>
 __device__ __forceinline__ Col column(const Req &q, int rg, int n, int h, int log_group) {
-    const int row = rg * kRows + n, i = row >> log_group;
+    const int row = rg * ROWS + n, i = row >> log_group;
     Col c;
     c.token = i < q.nq ? q.q0 + i : -1;
     c.head = (h << log_group) + (row & ((1 << log_group) - 1));
@@ -349,34 +357,42 @@ __device__ __forceinline__ Col column(const Req &q, int rg, int n, int h, int lo
 }
 
 // The state of one piece: O, reference and weight sum of the lane's columns
-// 2 t and 2 t + 1 (O: dims 32 b + 4 g + 0, 2 in rows g of tiles 0, 1 and
-// 32 b + 4 g + 1, 3 in rows g + 8).
-template <int NB, bool SPLIT>
+// 8 e + 2 t and 8 e + 2 t + 1 (O: dims 32 b + 4 g + 0, 2 in rows g of tiles 0, 1
+// and 32 b + 4 g + 1, 3 in rows g + 8).
+template <typename C>
 struct State {
+    static constexpr int NB = C::NB, NT = C::NT;
     // the codes' factors come out of rows g and g + 8
-    static constexpr float U0 = SPLIT ? 512.0f : 16777216.0f, U1 = SPLIT ? 512.0f : 1048576.0f;
-    float o[NB][2][4];
-    float m[2], l[2];
+    static constexpr float U0 = C::PSPLIT ? 512.0f : 16777216.0f, U1 = C::PSPLIT ? 512.0f : 1048576.0f;
+    float o[NT][NB][2][4];
+    float m[NT][2], l[NT][2];
     __device__ __forceinline__ void clear() {
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
+        for (int e = 0; e < NT; ++e) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[b][i >> 2][i & 3] = 0.0f;
-        m[0] = m[1] = kLowest;
-        l[0] = l[1] = 0.0f;
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[e][b][i >> 2][i & 3] = 0.0f;
+            m[e][0] = m[e][1] = kLowest;
+            l[e][0] = l[e][1] = 0.0f;
+        }
     }
-    // four consecutive dims of column 2 t + c in block b
-    __device__ __forceinline__ float4 quad(int b, int c) const {
-        return make_float4(o[b][0][c] * U0, o[b][0][2 + c] * U1,
-                           o[b][1][c] * U0, o[b][1][2 + c] * U1);
+    // four consecutive dims of column 8 e + 2 t + c in block b
+    __device__ __forceinline__ float4 quad(int e, int b, int c) const {
+        return make_float4(o[e][b][0][c] * U0, o[e][b][0][2 + c] * U1, o[e][b][1][c] * U0,
+                           o[e][b][1][2 + c] * U1);
     }
     __device__ __forceinline__ void sum_lanes() {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            l[0] += __shfl_xor_sync(~0u, l[0], d);
-            l[1] += __shfl_xor_sync(~0u, l[1], d);
-        }
+        for (int e = 0; e < NT; ++e)
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                l[e][0] += __shfl_xor_sync(~0u, l[e][0], d);
+                l[e][1] += __shfl_xor_sync(~0u, l[e][1], d);
+            }
     }
+    // where quad(e, b, c) lies in a partial or a ring, in float4s of the warp's lanes
+    __device__ __forceinline__ static int quad_at(int e, int b, int c) { return (e * NB + b) * 2 + c; }
 };
 
 __device__ __forceinline__ float4 scaled(float4 v, float s) {
@@ -412,30 +428,29 @@ struct Piece {
     int r, unit, gi, todo;      // request, unit (kv head and row group), group, groups left in the run
     int ahead;                  // measure between the run's last group and the end of its part
     int n, end;                 // groups of the unit, and where the piece ends
-    int pos[kRows];             // the columns' positions
-    int p_min, p_max;           // of all of them
+    int pos[16];                // the columns' positions
     int ns, skip;               // group i of the unit is i, or i + skip from ns on
     int holes;                  // the run has met a group without rows to read
-    int gone;                   // tiles of the run that are done, whose stages are free
+    int gone;                   // tiles of the run that are done, whose stages are free (released, acquired)
     int fin_r, fin_unit;        // the piece that ends the run, if other warps have more of its unit (else -1)
     long long fin_first, fin_last;  // that unit's groups in the cut's measure
-    float m[kRows], l[kRows];   // and the piece's references and sums
+    float m[16], l[16];         // and the piece's references and sums
 };
 
 // M groups of the run, at kp[0..M-1] in shared memory: scores, weights, O.
 // EDGE: not every row of the unit sees the (one) group whole; j0 is its first
 // key and pc says what is seen.
 template <typename C, int M, bool EDGE>
-__device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
-                                     const uint8_t *bias, float km0, float km1,
+__device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
+                                     const uint8_t *bias, const float (&km)[C::NT][2],
                                      const volatile Piece *pc, int j0, int sink, int win) {
-    constexpr int NB = C::NB, HD = NB * 32;
+    constexpr int NB = C::NB, HD = NB * 32, NT = C::NT;
     static_assert(M == 1 || !EDGE, "edges are taken one by one");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // ---- scores of rows g, g + 8 (y[0..1], y[2..3]) and columns 2 t, 2 t + 1
-    float y[M][4];
+    float y[M][NT][4];
 #pragma unroll
-    for (int k = 0; k < M; ++k) y[k][0] = y[k][1] = y[k][2] = y[k][3] = 0.0f;
+    for (int k = 0; k < M * NT * 4; ++k) y[k / (NT * 4)][k / 4 % NT][k % 4] = 0.0f;
     // codes of rows g, g + 8 and their block scales, 4 blocks (2 of head_dim 64) at
     // a time: with all of a group's at once the registers do not suffice
     constexpr int KB = NB < 4 ? NB : 4;
@@ -458,34 +473,45 @@ __device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const
                 lds_words<KB / 2>(sB[k], kp[k] + scale_offset(HD) + (g + 8) * (2 * NB) + 2 * b);
             }
         }
-        const uint4 qf = lds_v4(qs + (b * 32 + lane) * 16);
-        uint4 lo = make_uint4(0, 0, 0, 0);
-        if (C::QSPLIT) lo = lds_v4(qs + C::QF + (b * 32 + lane) * 16);
-        float4 c0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (!C::QSPLIT) c0 = lds_f4(bias + (b * 4 + t) * 16);
+        uint4 qf[NT], lo[NT];
+        float4 c0[NT];
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+            qf[e] = lds_v4(qs + (e * NB + b) * 512 + lane * 16);
+            if (C::QSPLIT)
+                lo[e] = lds_v4(qs + NT * C::QF + (e * NB + b) * 512 + lane * 16);
+            else
+                c0[e] = lds_f4(bias + ((e * NB + b) * 4 + t) * 16);
+        }
 #pragma unroll
         for (int k = 0; k < M; ++k) {
             const uint32_t a = wA[k][b % KB], c = wB[k][b % KB], a8 = a >> 8, c8 = c >> 8;
-            float d[4];
-            if (C::QSPLIT) {
-                const uint32_t e0 = minus8_lo(a), e1 = minus8_lo(c), e2 = minus8_hi(a), e3 = minus8_hi(c);
-                const uint32_t f0 = minus8_lo(a8), f1 = minus8_lo(c8);
-                const uint32_t f2 = minus8_hi(a8), f3 = minus8_hi(c8);
-                mma0(d, e0, e1, e2, e3, lo.x, lo.y);  // the low terms first: sums stay small
-                mma(d, f0, f1, f2, f3, lo.z, lo.w);
-                mma(d, e0, e1, e2, e3, qf.x, qf.y);
-                mma(d, f0, f1, f2, f3, qf.z, qf.w);
-            } else {
-                d[0] = c0.x, d[1] = c0.y, d[2] = c0.z, d[3] = c0.w;
-                mma(d, a & kLo, c & kLo, a & kHi, c & kHi, qf.x, qf.y);
-                mma(d, a8 & kLo, c8 & kLo, a8 & kHi, c8 & kHi, qf.z, qf.w);
-            }
             const float2 uA = half2_f(sA[k][b % KB / 2]), uB = half2_f(sB[k][b % KB / 2]);
             const float a0 = b & 1 ? uA.y : uA.x, a1 = b & 1 ? uB.y : uB.x;
-            y[k][0] = fmaf(a0, d[0], y[k][0]);
-            y[k][1] = fmaf(a0, d[1], y[k][1]);
-            y[k][2] = fmaf(a1, d[2], y[k][2]);
-            y[k][3] = fmaf(a1, d[3], y[k][3]);
+            uint32_t x[8];
+            if (C::QSPLIT) {
+                x[0] = minus8_lo(a), x[1] = minus8_lo(c), x[2] = minus8_hi(a), x[3] = minus8_hi(c);
+                x[4] = minus8_lo(a8), x[5] = minus8_lo(c8), x[6] = minus8_hi(a8), x[7] = minus8_hi(c8);
+            } else {
+                x[0] = a & kLo, x[1] = c & kLo, x[2] = a & kHi, x[3] = c & kHi;
+                x[4] = a8 & kLo, x[5] = c8 & kLo, x[6] = a8 & kHi, x[7] = c8 & kHi;
+            }
+#pragma unroll
+            for (int e = 0; e < NT; ++e) {
+                float d[4];
+                if (C::QSPLIT) {  // the low terms first: sums stay small
+                    mma0(d, x[0], x[1], x[2], x[3], lo[e].x, lo[e].y);
+                    mma(d, x[4], x[5], x[6], x[7], lo[e].z, lo[e].w);
+                } else {
+                    d[0] = c0[e].x, d[1] = c0[e].y, d[2] = c0[e].z, d[3] = c0[e].w;
+                }
+                mma(d, x[0], x[1], x[2], x[3], qf[e].x, qf[e].y);
+                mma(d, x[4], x[5], x[6], x[7], qf[e].z, qf[e].w);
+                y[k][e][0] = fmaf(a0, d[0], y[k][e][0]);
+                y[k][e][1] = fmaf(a0, d[1], y[k][e][1]);
+                y[k][e][2] = fmaf(a1, d[2], y[k][e][2]);
+                y[k][e][3] = fmaf(a1, d[3], y[k][e][3]);
+            }
         }
     }
     float iA[M], iB[M];  // 2^-e of V's rows
@@ -497,84 +523,83 @@ __device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const
         const float eA = static_cast<float>(xA - 127), eB = static_cast<float>(xB - 127);
         iA[k] = __uint_as_float(static_cast<uint32_t>(254 - xA) << 23);
         iB[k] = __uint_as_float(static_cast<uint32_t>(254 - xB) << 23);
-        y[k][0] = fmaf(y[k][0] * fA, km0, eA);
-        y[k][1] = fmaf(y[k][1] * fA, km1, eA);
-        y[k][2] = fmaf(y[k][2] * fB, km0, eB);
-        y[k][3] = fmaf(y[k][3] * fB, km1, eB);
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+            y[k][e][0] = fmaf(y[k][e][0] * fA, km[e][0], eA);
+            y[k][e][1] = fmaf(y[k][e][1] * fA, km[e][1], eA);
+            y[k][e][2] = fmaf(y[k][e][2] * fB, km[e][0], eB);
+            y[k][e][3] = fmaf(y[k][e][3] * fB, km[e][1], eB);
+        }
     }
     if (EDGE) {
-        const int p0 = pc->pos[2 * t], p1 = pc->pos[2 * t + 1], p_min = pc->p_min, p_max = pc->p_max;
-        // rows that no query sees may hold anything: their scales and sums must not
-        // reach a product, not even with a zero
-        auto seen = [&](int j) { return j <= p_max && (win <= 0 || j < sink || j > p_min - win); };
         const int jA = j0 + g, jB = jA + 8;
-        if (!key_visible(p0, jA, sink, win)) y[0][0] = -INFINITY;
-        if (!key_visible(p1, jA, sink, win)) y[0][1] = -INFINITY;
-        if (!key_visible(p0, jB, sink, win)) y[0][2] = -INFINITY;
-        if (!key_visible(p1, jB, sink, win)) y[0][3] = -INFINITY;
-        if (!seen(jA)) iA[0] = 0.0f;
-        if (!seen(jB)) iB[0] = 0.0f;
-        const int k0 = j0 + 2 * t;
-        const uint32_t m01 = (seen(k0) ? 0xffffu : 0u) | (seen(k0 + 1) ? 0xffff0000u : 0u);
-        const uint32_t m23 = (seen(k0 + 8) ? 0xffffu : 0u) | (seen(k0 + 9) ? 0xffff0000u : 0u);
-        if (g < NB / 2) {  // V's scales of rows 2t, 2t+1 | 2t+8, 2t+9 and two blocks
-            uint4 *w = reinterpret_cast<uint4 *>(kp[0] + part_bytes(HD) + scale_offset(HD) +
-                                                 (g * 4 + t) * 16);
-            *w = make_uint4(w->x & m01, w->y & m23, w->z & m01, w->w & m23);
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+            const int p0 = pc->pos[8 * e + 2 * t], p1 = pc->pos[8 * e + 2 * t + 1];
+            if (!key_visible(p0, jA, sink, win)) y[0][e][0] = -INFINITY;
+            if (!key_visible(p1, jA, sink, win)) y[0][e][1] = -INFINITY;
+            if (!key_visible(p0, jB, sink, win)) y[0][e][2] = -INFINITY;
+            if (!key_visible(p1, jB, sink, win)) y[0][e][3] = -INFINITY;
         }
-        fence_proxy_async_smem();  // before the next copy into the stage
-        __syncwarp();
     }
     // ---- weights relative to the reference
     float top = kLowest;
 #pragma unroll
     for (int k = 0; k < M; ++k)
-        top = fmaxf(top, fmaxf(fmaxf(y[k][0], y[k][2]) - st.m[0], fmaxf(y[k][1], y[k][3]) - st.m[1]));
+#pragma unroll
+        for (int e = 0; e < NT; ++e)
+            top = fmaxf(top, fmaxf(fmaxf(y[k][e][0], y[k][e][2]) - st.m[e][0],
+                                   fmaxf(y[k][e][1], y[k][e][3]) - st.m[e][1]));
     if (__any_sync(~0u, top > kMost)) {
-        float u0 = y[0][0], u1 = y[0][1];
 #pragma unroll
-        for (int k = 0; k < M; ++k) {
-            u0 = fmaxf(u0, fmaxf(y[k][0], y[k][2]));
-            u1 = fmaxf(u1, fmaxf(y[k][1], y[k][3]));
-        }
+        for (int e = 0; e < NT; ++e) {
+            float u0 = y[0][e][0], u1 = y[0][e][1];
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) {
-            u0 = fmaxf(u0, __shfl_xor_sync(~0u, u0, d));
-            u1 = fmaxf(u1, __shfl_xor_sync(~0u, u1, d));
-        }
-        const float n0 = u0 - st.m[0] > kMost ? u0 - kLift : st.m[0];
-        const float n1 = u1 - st.m[1] > kMost ? u1 - kLift : st.m[1];
-        const float c0 = ex2(st.m[0] - n0), c1 = ex2(st.m[1] - n1);
-        st.m[0] = n0;
-        st.m[1] = n1;
-        st.l[0] *= c0;
-        st.l[1] *= c1;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                st.o[b][i][0] *= c0;
-                st.o[b][i][1] *= c1;
-                st.o[b][i][2] *= c0;
-                st.o[b][i][3] *= c1;
+            for (int k = 0; k < M; ++k) {
+                u0 = fmaxf(u0, fmaxf(y[k][e][0], y[k][e][2]));
+                u1 = fmaxf(u1, fmaxf(y[k][e][1], y[k][e][3]));
             }
-    }
-    uint32_t b0[M], b1[M], l0[M], l1[M];
 #pragma unroll
-    for (int k = 0; k < M; ++k) {
-        const float d0 = ex2(y[k][0] - st.m[0]), d1 = ex2(y[k][1] - st.m[1]);
-        const float d2 = ex2(y[k][2] - st.m[0]), d3 = ex2(y[k][3] - st.m[1]);
-        st.l[0] += fmaf(d0, iA[k], d2 * iB[k]);
-        st.l[1] += fmaf(d1, iA[k], d3 * iB[k]);
-        const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
-        b0[k] = movmatrix_trans(hA);
-        b1[k] = movmatrix_trans(hB);
-        if (C::PSPLIT) {
-            const float2 rA = half2_f(hA), rB = half2_f(hB);
-            l0[k] = movmatrix_trans(pack_half2(d0 - rA.x, d1 - rA.y));
-            l1[k] = movmatrix_trans(pack_half2(d2 - rB.x, d3 - rB.y));
+            for (int d = 4; d < 32; d <<= 1) {
+                u0 = fmaxf(u0, __shfl_xor_sync(~0u, u0, d));
+                u1 = fmaxf(u1, __shfl_xor_sync(~0u, u1, d));
+            }
+            const float n0 = u0 - st.m[e][0] > kMost ? u0 - kLift : st.m[e][0];
+            const float n1 = u1 - st.m[e][1] > kMost ? u1 - kLift : st.m[e][1];
+            const float c0 = ex2(st.m[e][0] - n0), c1 = ex2(st.m[e][1] - n1);
+            st.m[e][0] = n0;
+            st.m[e][1] = n1;
+            st.l[e][0] *= c0;
+            st.l[e][1] *= c1;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    st.o[e][b][i][0] *= c0;
+                    st.o[e][b][i][1] *= c1;
+                    st.o[e][b][i][2] *= c0;
+                    st.o[e][b][i][3] *= c1;
+                }
         }
     }
+    uint32_t b0[M][NT], b1[M][NT], l0[M][NT], l1[M][NT];
+#pragma unroll
+    for (int k = 0; k < M; ++k)
+#pragma unroll
+        for (int e = 0; e < NT; ++e) {
+            const float d0 = ex2(y[k][e][0] - st.m[e][0]), d1 = ex2(y[k][e][1] - st.m[e][1]);
+            const float d2 = ex2(y[k][e][2] - st.m[e][0]), d3 = ex2(y[k][e][3] - st.m[e][1]);
+            st.l[e][0] += fmaf(d0, EDGE && d0 == 0.0f ? 0.0f : iA[k], EDGE && d2 == 0.0f ? 0.0f : d2 * iB[k]);
+            st.l[e][1] += fmaf(d1, EDGE && d1 == 0.0f ? 0.0f : iA[k], EDGE && d3 == 0.0f ? 0.0f : d3 * iB[k]);
+            const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
+            b0[k][e] = movmatrix_trans(hA);
+            b1[k][e] = movmatrix_trans(hB);
+            if (C::PSPLIT) {
+                const float2 rA = half2_f(hA), rB = half2_f(hB);
+                l0[k][e] = movmatrix_trans(pack_half2(d0 - rA.x, d1 - rA.y));
+                l1[k][e] = movmatrix_trans(pack_half2(d2 - rB.x, d3 - rB.y));
+            }
+        }
     // ---- O += V^T P. Groups that are taken together stay together per block where the
     // products go through a fresh accumulator (its sum is added once), else one by one.
     constexpr int MI = C::PSPLIT ? M : 1;
@@ -591,7 +616,7 @@ __device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const
             }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            float u[4], v[4];
+            float u[NT][4], v[NT][4];
 #pragma unroll
             for (int k = 0; k < MI; ++k) {
                 const uint32_t sel = b & 1 ? 0x7632u : 0x5410u;
@@ -601,44 +626,66 @@ __device__ __forceinline__ void step(State<C::NB, C::PSPLIT> &st, uint8_t *const
                 if (b % 2 == 0)
                     vs[k] = lds_v4(kp[k0 + k] + part_bytes(HD) + scale_offset(HD) + ((b / 2) * 4 + t) * 16);
                 const uint32_t s01 = b & 1 ? vs[k].z : vs[k].x, s23 = b & 1 ? vs[k].w : vs[k].y;
-                const uint32_t p0 = b0[k0 + k], p1 = b1[k0 + k];
-                const uint32_t w0 = hmul2(p0, s01), w1 = hmul2(p1, s23);
-                if (C::PSPLIT) {
-                    // the product's low term, exact but for the weight's own low term
-                    const uint32_t v0 = hfma2(l0[k0 + k], s01, hfms2(p0, s01, w0));
-                    const uint32_t v1 = hfma2(l1[k0 + k], s23, hfms2(p1, s23, w1));
-                    const uint32_t g0 = minus8_lo(x01), g1 = minus8_hi(x01), g2 = minus8_lo(x23), g3 = minus8_hi(x23);
-                    const uint32_t h0 = minus8_lo(z01), h1 = minus8_hi(z01), h2 = minus8_lo(z23), h3 = minus8_hi(z23);
-                    if (k == 0) {
-                        mma0(u, g0, g1, g2, g3, v0, v1);
-                        mma0(v, h0, h1, h2, h3, v0, v1);
-                    } else {
-                        mma(u, g0, g1, g2, g3, v0, v1);
-                        mma(v, h0, h1, h2, h3, v0, v1);
+                uint32_t w0[NT], w1[NT], v0[NT], v1[NT];
+#pragma unroll
+                for (int e = 0; e < NT; ++e) {
+                    const uint32_t p0 = b0[k0 + k][e], p1 = b1[k0 + k][e];
+                    // rows that a query does not see may hold anything, also where another of the
+                    // unit sees them: what they give is 0 even if their scales are not finite
+                    const uint32_t n0 = EDGE ? not_zero2(p0) : ~0u, n1 = EDGE ? not_zero2(p1) : ~0u;
+                    w0[e] = hmul2(p0, s01) & n0;
+                    w1[e] = hmul2(p1, s23) & n1;
+                    if (C::PSPLIT) {
+                        // the product's low term, exact but for the weight's own low term
+                        v0[e] = hfma2(l0[k0 + k][e], s01, hfms2(p0, s01, w0[e])) & n0;
+                        v1[e] = hfma2(l1[k0 + k][e], s23, hfms2(p1, s23, w1[e])) & n1;
                     }
-                    mma(u, g0, g1, g2, g3, w0, w1);
-                    mma(v, h0, h1, h2, h3, w0, w1);
+                }
+                uint32_t x[8];
+                if (C::PSPLIT) {
+                    x[0] = minus8_lo(x01), x[1] = minus8_hi(x01), x[2] = minus8_lo(x23), x[3] = minus8_hi(x23);
+                    x[4] = minus8_lo(z01), x[5] = minus8_hi(z01), x[6] = minus8_lo(z23), x[7] = minus8_hi(z23);
                 } else {
-                    mma(st.o[b][0], x01 & kLo, x01 & kHi, x23 & kLo, x23 & kHi, w0, w1);
-                    mma(st.o[b][1], z01 & kLo, z01 & kHi, z23 & kLo, z23 & kHi, w0, w1);
-                    mma(st.o[b][0], kM8a, kM8b, kM8a, kM8b, w0, w1);
-                    mma(st.o[b][1], kM8a, kM8b, kM8a, kM8b, w0, w1);
+                    x[0] = x01 & kLo, x[1] = x01 & kHi, x[2] = x23 & kLo, x[3] = x23 & kHi;
+                    x[4] = z01 & kLo, x[5] = z01 & kHi, x[6] = z23 & kLo, x[7] = z23 & kHi;
+                }
+#pragma unroll
+                for (int e = 0; e < NT; ++e) {
+                    if (C::PSPLIT) {
+                        if (k == 0) {
+                            mma0(u[e], x[0], x[1], x[2], x[3], v0[e], v1[e]);
+                            mma0(v[e], x[4], x[5], x[6], x[7], v0[e], v1[e]);
+                        } else {
+                            mma(u[e], x[0], x[1], x[2], x[3], v0[e], v1[e]);
+                            mma(v[e], x[4], x[5], x[6], x[7], v0[e], v1[e]);
+                        }
+                        mma(u[e], x[0], x[1], x[2], x[3], w0[e], w1[e]);
+                        mma(v[e], x[4], x[5], x[6], x[7], w0[e], w1[e]);
+                    } else {
+                        mma(st.o[e][b][0], x[0], x[1], x[2], x[3], w0[e], w1[e]);
+                        mma(st.o[e][b][1], x[4], x[5], x[6], x[7], w0[e], w1[e]);
+                        mma(st.o[e][b][0], kM8a, kM8b, kM8a, kM8b, w0[e], w1[e]);
+                        mma(st.o[e][b][1], kM8a, kM8b, kM8a, kM8b, w0[e], w1[e]);
+                    }
                 }
             }
             if (C::PSPLIT) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    st.o[b][0][i] += u[i];
-                    st.o[b][1][i] += v[i];
-                }
+                for (int e = 0; e < NT; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        st.o[e][b][0][i] += u[e][i];
+                        st.o[e][b][1][i] += v[e][i];
+                    }
             }
         }
     }
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(PagedAttnArgs a) {
-    using C = Cfg<T, HD>;
+template <typename T, int HD, int NT>
+__global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kernel(PagedAttnArgs a) {
+    using C = Cfg<T, HD, NT>;
+    constexpr int ROWS = C::ROWS;
     constexpr int NB = C::NB, S = C::STAGES;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ long long scan_part[2][C::WARPS + 1];
@@ -676,7 +723,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     int of_unit = 1;                // groups of a unit of the last request
     bool bad = false;
     for (int r = r0; r < r1; ++r) {
-        const Req q = load_req(a, r, log_group);
+        const Req q = load_req<ROWS>(a, r, log_group);
         of_unit = unit_groups(q);
         const long long units = static_cast<long long>(q.rgs) * n_kv;
         bad |= q.bad;
@@ -684,6 +731,10 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         count += units * of_unit;
     }
     if (bad && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
+    // lengths that contradict each other (overlapping requests) must not wrap the sums: what is
+    // cut here is refused below
+    work = min(work, 1ll << 41);
+    count = min(count, 1ll << 41);
     long long inc = work, inc_g = count;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -699,7 +750,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         N += scan_part[0][i];
         all_groups += scan_part[1][i];
     }
-    if (N >> 30 >= gridDim.x) {  // runs are counted in 31 bits (2^34 rows an SM)
+    if (N >> 30 >= gridDim.x) {  // runs are counted in 31 bits (2^34 rows an SM), and B < 2^11
         if (tid == 0 && blockIdx.x == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
         N = 0;
     }
@@ -712,7 +763,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             for (int r = r0; r < r1; ++r) {
                 long long n = work, ng = count;
                 if (per > 1) {
-                    const Req q = load_req(a, r, log_group);
+                    const Req q = load_req<ROWS>(a, r, log_group);
                     of_unit = unit_groups(q);
                     ng = static_cast<long long>(q.rgs) * n_kv * of_unit;
                     n = ng + static_cast<long long>(q.rgs) * n_kv * kUnitCost;
@@ -775,7 +826,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             if (lane < cut.A) left = static_cast<int>(end - p.groups);
             if (left > 0) {
                 r = p.r;
-                enter(load_req(a, r, log_group));
+                enter(load_req<ROWS>(a, r, log_group));
                 unit = p.unit;
                 ci = p.gi;
                 head = unit / rgs * a.pages.groups;
@@ -790,7 +841,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
         volatile Piece *its = pieces + min(lane, C::WARPS - 1);
         long long t0 = clock64();
         while (__any_sync(~0u, left > 0)) {
-            const bool went = left > 0 && made - its->gone < S;
+            const bool went = left > 0 && made - acquire_s32(&its->gone) < S;
             if (went) {
                 const int n = tile_size<C::TILE>(ci, min(cn, ci + left), ns, skip);
                 uint32_t holes = 0;
@@ -825,7 +876,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         if (++unit == units) {
                             unit = 0;
                             Req q;
-                            q = next_req(a, &r, log_group);
+                            q = next_req<ROWS>(a, &r, log_group);
                             enter(q);
                         }
                         head = unit / rgs * a.pages.groups;
@@ -848,7 +899,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     }
 
     volatile Piece *pc = pieces + min(warp, C::WARPS - 1);
-    State<NB, C::PSPLIT> st;
+    State<C> st;
     st.clear();
     if (warp < C::WARPS) {
         if (lane == 0) {
@@ -877,76 +928,77 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
 #pragma unroll 1
         while (pc->todo > 0) {
             int gi = pc->gi, g_end, f0, f1;
-            float km[2];
+            float km[NT][2];
             {
-                const Req q = load_req(a, pc->r, log_group);
+                const Req q = load_req<ROWS>(a, pc->r, log_group);
                 const int n = unit_groups(q), unit = pc->unit;
                 const int h = unit / q.rgs, rg = unit - h * q.rgs;
                 g_end = min(n, gi + pc->todo);
                 // ---- q of row g as B fragments: dims 32 b + 8 t + (0,4 | 1,5 | 2,6 | 3,7),
                 // the second and fourth times 2^-4; brought to a maximum in [2^10, 2^11)
-                const Col c = column(q, rg, g, h, log_group);
-                const T *src = static_cast<const T *>(a.q) + max(c.token, 0) * a.q_stride +
-                               static_cast<long long>(c.head) * HD + 8 * t;
-                Raw8<T> raw[NB];
+#pragma unroll 1
+                for (int e = 0; e < NT; ++e) {
+                    const Col c = column<ROWS>(q, rg, 8 * e + g, h, log_group);
+                    const T *src = static_cast<const T *>(a.q) + max(c.token, 0) * a.q_stride +
+                                   static_cast<long long>(c.head) * HD + 8 * t;
+                    Raw8<T> raw[NB];
 #pragma unroll
-                for (int b = 0; b < NB; ++b) raw[b].load(src + 32 * b, c.token >= 0);
-                float top = 0.0f;
+                    for (int b = 0; b < NB; ++b) raw[b].load(src + 32 * b, c.token >= 0);
+                    float top = 0.0f;
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float x[8];
-                    raw[b].get(x);
+                    for (int b = 0; b < NB; ++b) {
+                        float x[8];
+                        raw[b].get(x);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-                }
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                int up = 0;
-                if (top > 0.0f)
-                    up = min(max(137 - static_cast<int>(__float_as_uint(top) >> 23), -96), 126);
-                const float lift = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-                const float mul = a.scale * kLog2e *
-                                  __uint_as_float(static_cast<uint32_t>(127 - up) << 23) *
-                                  (C::QSPLIT ? 512.0f : 16777216.0f);  // 2^9, 2^24
-                km[0] = __shfl_sync(~0u, mul, 8 * t);
-                km[1] = __shfl_sync(~0u, mul, 8 * t + 4);
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float x[8];
-                    raw[b].get(x);
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float u = x[i] * lift, v = x[i + 4] * lift;
-                        hi[i] = pack_half2(u, v);
-                        const float2 f = half2_f(hi[i]);
-                        if (!C::QSPLIT && (i & 1)) hi[i] = pack_half2(f.x * 0.0625f, f.y * 0.0625f);
-                        lo[i] = pack_half2(u - f.x, v - f.y);
+                        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
                     }
-                    *reinterpret_cast<uint4 *>(qs + (b * 32 + lane) * 16) =
-                        make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (C::QSPLIT) {
-                        *reinterpret_cast<uint4 *>(qs + C::QF + (b * 32 + lane) * 16) =
-                            make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                    } else {
-                        // -8 times the block's sum, where the accumulators start: "code -8" in every row
-                        float d[4];
-                        mma0(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
-                        mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
-                        if (g == 0)
-                            *reinterpret_cast<float4 *>(bias + (b * 4 + t) * 16) =
-                                make_float4(d[0], d[1], d[2], d[3]);
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    int up = 0;
+                    if (top > 0.0f)
+                        up = min(max(137 - static_cast<int>(__float_as_uint(top) >> 23), -96), 126);
+                    const float lift = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                    const float mul = a.scale * kLog2e *
+                                      __uint_as_float(static_cast<uint32_t>(127 - up) << 23) *
+                                      (C::QSPLIT ? 512.0f : 16777216.0f);  // 2^9, 2^24
+                    km[e][0] = __shfl_sync(~0u, mul, 8 * t);
+                    km[e][1] = __shfl_sync(~0u, mul, 8 * t + 4);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        float x[8];
+                        raw[b].get(x);
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float u = x[i] * lift, v = x[i + 4] * lift;
+                            hi[i] = pack_half2(u, v);
+                            const float2 f = half2_f(hi[i]);
+                            if (!C::QSPLIT && (i & 1)) hi[i] = pack_half2(f.x * 0.0625f, f.y * 0.0625f);
+                            lo[i] = pack_half2(u - f.x, v - f.y);
+                        }
+                        *reinterpret_cast<uint4 *>(qs + (e * NB + b) * 512 + lane * 16) =
+                            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (C::QSPLIT) {
+                            *reinterpret_cast<uint4 *>(qs + NT * C::QF + (e * NB + b) * 512 + lane * 16) =
+                                make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        } else {
+                            // -8 times the block's sum, where the accumulators start: "code -8" in every row
+                            float d[4];
+                            mma0(d, kM8a, kM8a, kM8b, kM8b, hi[0], hi[1]);
+                            mma(d, kM8a, kM8a, kM8b, kM8b, hi[2], hi[3]);
+                            if (g == 0)
+                                *reinterpret_cast<float4 *>(bias + ((e * NB + b) * 4 + t) * 16) =
+                                    make_float4(d[0], d[1], d[2], d[3]);
+                        }
                     }
                 }
-                const int p_min = q.rows - q.nq + ((rg * kRows) >> log_group);
+                const int p_min = q.rows - q.nq + ((rg * ROWS) >> log_group);
                 const int p_max = q.rows - q.nq +
-                                  min(q.nq - 1, (rg * kRows + kRows - 1) >> log_group);
-                if (lane < kRows) pc->pos[lane] = column(q, rg, lane, h, log_group).pos;
+                                  min(q.nq - 1, (rg * ROWS + ROWS - 1) >> log_group);
+                if (lane < ROWS) pc->pos[lane] = column<ROWS>(q, rg, lane, h, log_group).pos;
                 if (lane == 0) {
                     pc->n = n;
                     pc->end = g_end;
-                    pc->p_min = p_min;
-                    pc->p_max = p_max;
                     pc->ns = q.ns;
                     pc->skip = q.skip;
                 }
@@ -970,14 +1022,14 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                         uint8_t *tile[C::TILE];
 #pragma unroll
                         for (int k = 0; k < C::TILE; ++k) tile[k] = kp + k * C::GB;
-                        step<C, C::TILE, false>(st, tile, qs, bias, km[0], km[1], pc, 0, a.sink, a.win);
+                        step<C, C::TILE, false>(st, tile, qs, bias, km, pc, 0, a.sink, a.win);
                     } else {
 #pragma unroll 1
                         for (int k = 0; k < n; ++k) {
                             if (holes >> k & 1) continue;
                             const int i = gi + k;
                             uint8_t *const one[1] = {kp + k * C::GB};
-                            step<C, 1, true>(st, one, qs, bias, km[0], km[1], pc,
+                            step<C, 1, true>(st, one, qs, bias, km, pc,
                                              (i < pc->ns ? i : i + pc->skip) * kGroupRows, a.sink, a.win);
                         }
                     }
@@ -985,7 +1037,7 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
                 __syncwarp();  // every lane has read the stage
                 gi += n;
                 ++tiles;
-                if (lane == 0) pc->gone = tiles;
+                if (lane == 0) release_s32(&pc->gone, tiles);
                 if (++stage == S) stage = 0, phase ^= 1;
             }
 
@@ -994,53 +1046,56 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             const int r = pc->r, unit = pc->unit, n = pc->n, first = pc->gi, end = pc->end;
             const int todo = pc->todo - (end - first);
             if (first == 0 && end == n) {
-                const Req q = load_req(a, r, log_group);
+                const Req q = load_req<ROWS>(a, r, log_group);
                 const int h = unit / q.rgs, rg = unit - h * q.rgs;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const Col col = column(q, rg, 2 * t + c, h, log_group);
+                for (int e = 0; e < NT; ++e)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-                        write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(b, c), st.m[c], st.l[c]);
-                }
-            } else if (todo > 0) {  // the start of the run: to the workspace
+                    for (int c = 0; c < 2; ++c) {
+                        const Col col = column<ROWS>(q, rg, 8 * e + 2 * t + c, h, log_group);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+                            write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(e, b, c), st.m[e][c], st.l[e][c]);
+                    }
+            } else {
+                // the start of the run: to the workspace; its end: into the ring, whose copies
+                // have all been used
+                const bool start = todo > 0;
                 float *dst = ws.partial +
                              (static_cast<size_t>(blockIdx.x * cut.A + warp) * 2 + 1) * C::PARTIAL;
                 if (g == 0) {
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        dst[2 * t + c] = st.m[c];
-                        dst[kRows + 2 * t + c] = st.l[c];
-                    }
+                    for (int e = 0; e < NT; ++e)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int i = 8 * e + 2 * t + c;
+                            if (start) {
+                                dst[i] = st.m[e][c];
+                                dst[ROWS + i] = st.l[e][c];
+                            } else {
+                                pc->m[i] = st.m[e][c];
+                                pc->l[i] = st.l[e][c];
+                            }
+                        }
                 }
+                float4 *quads = start ? reinterpret_cast<float4 *>(dst + 2 * ROWS)
+                                      : reinterpret_cast<float4 *>(ring);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int e = 0; e < NT; ++e)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<float4 *>(dst + 2 * kRows + ((b * 2 + c) * 32 + lane) * 4) =
-                            st.quad(b, c);
-            } else {  // the end of the run: into the ring, whose copies have all been used
-                if (g == 0) {
+                    for (int b = 0; b < NB; ++b)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        pc->m[2 * t + c] = st.m[c];
-                        pc->l[2 * t + c] = st.l[c];
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c)
-                        *reinterpret_cast<float4 *>(ring + ((b * 2 + c) * 32 + lane) * 16) = st.quad(b, c);
+                        for (int c = 0; c < 2; ++c)
+                            quads[st.quad_at(e, b, c) * 32 + lane] = st.quad(e, b, c);
             }
             __syncwarp();
             if (lane == 0) {
                 if (todo > 0) {
-                    const Req q = load_req(a, r, log_group);
+                    const Req q = load_req<ROWS>(a, r, log_group);
                     int next = unit + 1, nr = r;
                     if (next == q.rgs * n_kv) {
                         next = 0;
-                        next_req(a, &nr, log_group);
+                        next_req<ROWS>(a, &nr, log_group);
                     }
                     pc->r = nr;
                     pc->unit = next;
@@ -1075,25 +1130,8 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
     const int id0 = blockIdx.x * cut.A + w0;
     const bool from_start = cut.start(blockIdx.x, w0) <= first;
     const bool direct = from_start && cut.start(blockIdx.x, w1) >= last;
-    const Req q = load_req(a, r, log_group);
+    const Req q = load_req<ROWS>(a, r, log_group);
     const int h = unit / q.rgs, rg = unit - h * q.rgs;
-    float M[2], L[2], f[2][C::WARPS];  // of columns 2 t, 2 t + 1
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int n = 2 * t + c;
-        M[c] = kLowest;
-        L[c] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-            f[c][w] = w >= w0 && w < w1 ? pieces[w].m[n] : kLowest;
-            M[c] = fmaxf(M[c], f[c][w]);
-        }
-#pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-            f[c][w] = ex2(f[c][w] - M[c]);
-            if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], f[c][w], L[c]);
-        }
-    }
     float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
     if (from_start && !direct && warp == w0 && lane == 0) {
         const int e = cut.warp_of(last - 1);  // the warp that holds the unit's last group
@@ -1102,32 +1140,48 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
             pack_pieces((tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1, cut.A, tail ? e : -1);
         ws.tasks[blockIdx.x * kMostWarps + warp] = Task{h, rg, q};
     }
-    if (!direct && warp == w0 && g == 0) {
+#pragma unroll 1
+    for (int e = 0; e < NT; ++e) {
+        float M[2], L[2], f[2][C::WARPS];  // of columns 8 e + 2 t + 0, 1
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            dst[2 * t + c] = M[c];
-            dst[kRows + 2 * t + c] = L[c];
-        }
-    }
-    for (int i = warp - w0; i < 2 * NB; i += w1 - w0) {  // (block, column) pairs
-        const int b = i >> 1, c = i & 1;
-        const float top = c ? M[1] : M[0];
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int n = 8 * e + 2 * t + c;
+            M[c] = kLowest;
+            L[c] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < C::WARPS; ++w) {
-            if (w < w0 || w >= w1) continue;
-            const float4 y = *reinterpret_cast<const float4 *>(smem + w * C::RING + (i * 32 + lane) * 16);
-            const float k = c ? f[1][w] : f[0][w];
-            x.x = fmaf(y.x, k, x.x);
-            x.y = fmaf(y.y, k, x.y);
-            x.z = fmaf(y.z, k, x.z);
-            x.w = fmaf(y.w, k, x.w);
+            for (int w = 0; w < C::WARPS; ++w) {
+                f[c][w] = w >= w0 && w < w1 ? pieces[w].m[n] : kLowest;
+                M[c] = fmaxf(M[c], f[c][w]);
+            }
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w) {
+                f[c][w] = ex2(f[c][w] - M[c]);
+                if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], f[c][w], L[c]);
+            }
+            if (!direct && warp == w0 && g == 0) {
+                dst[n] = M[c];
+                dst[ROWS + n] = L[c];
+            }
         }
-        if (direct)
-            write_row<T>(a, column(q, rg, 2 * t + c, h, log_group), HD, 32 * b + 4 * g, x, top,
-                         c ? L[1] : L[0]);
-        else
-            *reinterpret_cast<float4 *>(dst + 2 * kRows + (i * 32 + lane) * 4) = x;
+        for (int i = warp - w0; i < 2 * NB; i += w1 - w0) {  // (block, column) pairs
+            const int b = i >> 1, c = i & 1, at = st.quad_at(e, b, c) * 32 + lane;
+            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < C::WARPS; ++w) {
+                if (w < w0 || w >= w1) continue;
+                const float4 y = *(reinterpret_cast<const float4 *>(smem + w * C::RING) + at);
+                const float k = c ? f[1][w] : f[0][w];
+                x.x = fmaf(y.x, k, x.x);
+                x.y = fmaf(y.y, k, x.y);
+                x.z = fmaf(y.z, k, x.z);
+                x.w = fmaf(y.w, k, x.w);
+            }
+            if (direct)
+                write_row<T>(a, column<ROWS>(q, rg, 8 * e + 2 * t + c, h, log_group), HD, 32 * b + 4 * g, x,
+                             c ? M[1] : M[0], c ? L[1] : L[0]);
+            else
+                *(reinterpret_cast<float4 *>(dst + 2 * ROWS) + at) = x;
+        }
     }
 }
 
@@ -1140,10 +1194,10 @@ __global__ void __launch_bounds__((Cfg<T, HD>::THREADS), 1) paged_attn_kernel(Pa
 // equal ones, where there is nothing to even out, 20.5 instead of 21.9. The pieces
 // of a slice are added in ascending order, and so are the slices.
 constexpr int kJoinThreads = 512, kJoinWarps = kJoinThreads / 32;
-template <typename T, int HD>
+template <typename T, int HD, int NT>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs a) {
-    using C = Cfg<T, HD>;
-    constexpr int ITEMS = 2 * C::NB, BATCH = 8;
+    using C = Cfg<T, HD, NT>;
+    constexpr int ITEMS = 2 * C::NB * NT, BATCH = 8;
     __shared__ int counts[kJoinWarps];
     constexpr int MOST = kMostBlocks * kMostWarps;
     __shared__ uint32_t list[MOST], where[MOST];  // tasks: their words, and whose they are
@@ -1151,7 +1205,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                       kMostWarps < 32 && kMostWarps % 4 == 0,
                   "a thread reads a block's words, whose fields hold these");
     __shared__ float4 part_o[kJoinWarps][32];
-    __shared__ float part_m[kJoinWarps][kRows / 2], part_l[kJoinWarps][kRows / 2];
+    __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1200,7 +1254,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
         const bool in = j < j1;
         const int nth = static_cast<unsigned>(in ? j : jb) / ITEMS;
         const uint32_t id = where[nth], word = list[nth];
-        const int i = (in ? j : jb) & (ITEMS - 1), b = i >> 1, n = 2 * t + (i & 1);
+        const int i = (in ? j : jb) & (ITEMS - 1), b = (i >> 1) % C::NB;
+        const int n = 8 * (i / (2 * C::NB)) + 2 * t + (i & 1);  // i = quad_at of the item
         const Task k = ws.tasks[id];
         const int block = id / kMostWarps, blocks = word & 511u, warps = word >> 9 & 31u;
         const int tail = static_cast<int>(word >> 14) - 1, pieces = blocks + (tail >= 0);
@@ -1221,8 +1276,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
             for (int e = 0; e < BATCH; ++e) {
                 const float *p = piece(min(eb + e, e1 - 1));
                 m[e] = p[n];
-                l[e] = p[kRows + n];
-                y[e] = *reinterpret_cast<const float4 *>(p + 2 * kRows + (i * 32 + lane) * 4);
+                l[e] = p[C::ROWS + n];
+                y[e] = *reinterpret_cast<const float4 *>(p + 2 * C::ROWS + (i * 32 + lane) * 4);
             }
             float top = M;
 #pragma unroll
@@ -1263,7 +1318,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
             }
         }
         if (in && slice == 0)
-            write_row<T>(a, column(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
+            write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
     }
 }
 
@@ -1283,40 +1338,56 @@ cudaError_t launch_after(K *kernel, int blocks, int threads, size_t smem, cudaSt
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
-template <typename T, int HD>
+template <typename T, int HD, int NT>
 cudaError_t launch(const PagedAttnArgs &a, cudaStream_t stream) {
-    using C = Cfg<T, HD>;
+    using C = Cfg<T, HD, NT>;
     // once for each device, as the call takes a microsecond; two threads that are first may both
     // make it
     static std::atomic<uint64_t> made{0};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess && (dev >= 64 || !(made.load(std::memory_order_acquire) >> dev & 1))) {
-        e = cudaFuncSetAttribute(paged_attn_kernel<T, HD>,
+        e = cudaFuncSetAttribute(paged_attn_kernel<T, HD, NT>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e == cudaSuccess && dev < 64) made.fetch_or(1ull << dev, std::memory_order_release);
     }
     const int blocks = std::min(device_sm_count(), kMostBlocks);
     if (e == cudaSuccess)
-        e = launch_after(paged_attn_kernel<T, HD>, blocks, C::THREADS, C::SMEM, stream, a);
+        e = launch_after(paged_attn_kernel<T, HD, NT>, blocks, C::THREADS, C::SMEM, stream, a);
     if (e == cudaSuccess)
-        e = launch_after(paged_join_kernel<T, HD>, blocks, kJoinThreads, 0, stream, a);
+        e = launch_after(paged_join_kernel<T, HD, NT>, blocks, kJoinThreads, 0, stream, a);
     return e;
+}
+
+// Where 16 or more q heads share a kv head a unit is 16 rows: its codes become
+// operands once for both eights (32 x 16384 rows of 2 kv heads, bf16: head_dim 128
+// 64.2 us with 8 rows, 58.5 with 16; head_dim 64 42.5 and 39.0; fp16 76.5 and 72.0,
+// 48.5 and 44.5). With fewer heads 16 rows may be half empty, which costs more than
+// full ones save (8 heads, bf16: 113 us with 8 rows, 176 with 16). For fp32 the
+// saving went to the registers (batches of all lengths: 111 us with 8 rows, 115 with
+// 16), and with head_dim 256 O would take all of them.
+template <typename T, int HD>
+cudaError_t launch_rows(const PagedAttnArgs &a, cudaStream_t stream) {
+    if constexpr (HD < 256 && sizeof(T) == 2) {
+        if (a.n_q_heads / a.pages.n_kv >= 16) return launch<T, HD, 2>(a, stream);
+    }
+    return launch<T, HD, 1>(a, stream);
 }
 
 template <typename T>
 cudaError_t launch_type(const PagedAttnArgs &a, int hd, cudaStream_t stream) {
-    return hd == 64    ? launch<T, 64>(a, stream)
-           : hd == 128 ? launch<T, 128>(a, stream)
-                       : launch<T, 256>(a, stream);
+    return hd == 64    ? launch_rows<T, 64>(a, stream)
+           : hd == 128 ? launch_rows<T, 128>(a, stream)
+                       : launch_rows<T, 256>(a, stream);
 }
 
 }  // namespace
 
 size_t paged_attn_ws_bytes(int hd) {
     const size_t warps = static_cast<size_t>(device_sm_count()) * kMostWarps;
+    const size_t rows = hd < 256 ? 16 : 8;  // of a unit
     return ws_head(device_sm_count(), 4) + ws_head(device_sm_count(), sizeof(Task)) +
-           warps * 2 * (2 * kRows + kRows * hd) * 4;
+           warps * 2 * rows * (2 + hd) * 4;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream) {

@@ -520,6 +520,106 @@ def test_attn_magnitudes(dtype, k_size, v_size, q_size):
     check_attn([300, 1000], [1, 2], 16, 2, 128, 16, dtype, k_size=k_size, v_size=v_size, q_size=q_size, seed=3)
 
 
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd", (64, 128, 256))
+def test_attn_sixteen_heads_of_a_kv_head(hd, dtype):
+    """Groups of 16: short, long and empty requests, several queries, a window with pages given back."""
+    check_attn([2500, 0, 1, 47, 300], [1, 1, 1, 3, 2], 32, 2, hd, 32, dtype, seed=21)
+    check_attn([900, 16, 333], [2, 1, 5], 16, 1, hd, 16, dtype, sink=20, win=130, spare=hd, pad=2, seed=22)
+    check_attn([6000], [1], 16, 1, hd, 64, dtype, seed=23)
+    check_attn(np.random.default_rng(24).integers(0, 60, 170).tolist(), [1] * 170, 16, 1, hd, 16, dtype, seed=24)
+
+
+@pytest.mark.parametrize("hd,hq", [(64, 8), (128, 16), (256, 8)])
+def test_attn_pages_that_requests_share(hd, hq):
+    """Requests with a common beginning hold the same pages; one of them even twice."""
+    m = fa()
+    rng = np.random.default_rng(hd)
+    P = 16
+    pages, table, ks, vs = filled(m, rng, [160, 48], 1, hd, P)
+    both = np.full((3, 13), -1)
+    both[0, :10] = table[0, :10]                              # 160 rows
+    both[1, :9] = np.r_[table[0, :6], table[1, :3]]           # 96 of them and the other's 48
+    both[2, :13] = np.r_[table[1, :3], table[0, :10]]
+    lens = [160, 140, 205]
+    rows = [(ks[0], vs[0]), tuple(np.concatenate([a[:96], b]) for a, b in ((ks[0], ks[1]), (vs[0], vs[1]))),
+            tuple(np.concatenate([b, a]) for a, b in ((ks[0], ks[1]), (vs[0], vs[1])))]
+    q, qx = on_gpu(rng.standard_normal((3, hq, hd)), "f32")
+    got = host(call_attn(m, q, ints(both), pages, ints(lens), ints([0, 1, 2, 3]), 1, P))
+    for r, L in enumerate(lens):
+        k, v = (x[:L] for x in rows[r])
+        want, _ = ref.attend(qx[r:r + 1], L, k, v, L - 1, 0, 0, 1 / math.sqrt(hd))
+        assert np.linalg.norm(got[r] - want[0]) <= 2.0 ** -17 * np.linalg.norm(want)
+    both[0, 1] = both[0, 0]                                   # the same page twice in a request
+    got = host(call_attn(m, q, ints(both), pages, ints(lens), ints([0, 1, 2, 3]), 1, P))
+    k, v = (np.concatenate([x[:16], x[:16], x[32:]]) for x in (ks[0], vs[0]))
+    want, _ = ref.attend(qx[:1], 160, k, v, 159, 0, 0, 1 / math.sqrt(hd))
+    assert np.linalg.norm(got[0] - want[0]) <= 2.0 ** -17 * np.linalg.norm(want)
+    assert m.get_device_error() == m.OK
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 32), (128, 8), (256, 16)])
+def test_attn_infinities_and_nan_stay_in_their_rows(hd, hq, dtype):
+    """A NaN or infinity in a query reaches that row alone, an infinity in a page's row the queries that attend it."""
+    m = fa()
+    rng = np.random.default_rng(hd)
+    hkv, P, lens, nqs = 2, 16, [90, 400, 33], [2, 2, 2]
+    pages, table, _, _ = filled(m, rng, lens, hkv, hd, P)
+    args = ints(table), pages, ints(lens), ints(np.r_[0, np.cumsum(nqs)]), hkv, P
+    q, _ = on_gpu(rng.standard_normal((6, hq, hd)), dtype)
+    clean = call_attn(m, q, *args)
+    for bad in (math.nan, math.inf):
+        dirty = q.clone()
+        dirty[2, 1, 5] = bad
+        got = call_attn(m, dirty, *args)
+        same = (got == clean).all(-1)
+        same[2, 1] = True
+        assert bool(same.all()) and bool(got[2, 1].isnan().all())
+    k = torch.full((1, hkv, hd), 1.0, device="cuda")
+    k[:, :, 3] = math.inf
+    last = int(table[1, 399 // P]) * P + 399 % P              # the newest row of request 1: its second query's own
+    v = torch.full_like(k, 1.0)
+    v[:, :, 40] = math.inf
+    append(m, pages, k, v, [last], P)
+    got = call_attn(m, q, *args)
+    keep = [0, 1, 2, 4, 5]
+    assert torch.equal(got[keep], clean[keep])
+    assert bool(got[3].isnan().all())
+    assert m.get_device_error() == m.OK
+
+
+def test_attn_refuses_more_work_than_it_counts():
+    """Lengths of 2^30 rows for 65536 queries: flagged, nothing read or written."""
+    m = fa()
+    T, hd = 1 << 16, 64
+    q = torch.zeros(T, 16, hd, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    table = torch.zeros(1, 1 << 22, dtype=torch.int32, device="cuda")
+    call_attn(m, q, table, pool_of(m, 1, 1, hd, 256), ints([1 << 30]), ints([0, T]), 1, 256, out=out)
+    assert m.get_device_error() == m.ERR_DEVICE
+    assert bool((out == 7.0).all())
+
+
+def test_nothing_to_do():
+    """No requests, no tokens: the plan still says so, the other calls return at once."""
+    m = fa()
+    e = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")  # noqa: E731
+    ring, state, cu, slots, pos = ints([1, 0]), ints([-9] * 3), ints([-9]), ints([-9] * 5), ints([-9] * 5)
+    m.page_plan(e(0), e(0), ring, ints([1, 2]), e(0, 3), state, e(0), cu, slots, pos, page_rows=16)
+    assert state.tolist() == [1, 2, 0] and cu.tolist() == [0] and slots.tolist() == [-1] * 5 and pos.tolist() == [0] * 5
+    pages = pool_of(m, 1, 1, 64, 16)
+    x = torch.zeros(0, 1, 64, device="cuda")
+    m.paged_append(x, x, e(0), pages, page_rows=16)
+    m.paged_attn(x, torch.zeros_like(x), e(1), e(0), e(0, 3), pages, n_kv_heads=1, page_rows=16,
+                 workspace=torch.empty(m.paged_attn_workspace_bytes(64), dtype=torch.uint8, device="cuda"))
+    q = torch.full((3, 8, 64), 7.0, device="cuda")            # tokens, but none of a request
+    out = call_attn(m, q, e(2, 1), pages, e(2), e(3), 1, 16, out=q.clone())
+    assert torch.equal(out, q)
+    check_guards(("pages", pages))
+    assert m.get_device_error() == m.OK
+
+
 def test_attn_many_requests_of_every_length():
     rng = np.random.default_rng(8)
     lens = rng.integers(0, 200, 300).tolist()
@@ -661,6 +761,60 @@ def test_attn_graphs_and_streams():
             call_attn(m, q, t, pages, n, cu, hkv, P, out=o, ws=w, stream=s)
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs)
+
+
+def test_a_captured_step_replays():
+    """Plan, rotation, append and attention as one graph, twice over the same workspace: each replay goes on from
+    the state that the one before it left, and the results are those of separate calls, bit for bit."""
+    m = fa()
+    R, P, max_pages, n_pages, hq, hkv, hd, T = 3, 16, 6, 14, 16, 2, 128, 24
+    rope = m.rope_table(1e4 ** (-np.arange(hd // 2) / (hd // 2)))
+    fresh_of = [[10, 4, 10], [1, 20, 1], [-1, 1, 1], [17, 1, 1], [1, 1, 5], [0, 0, 1]]
+
+    def world():
+        rng = np.random.default_rng(5)
+        w = dict(ring=ints(rng.permutation(n_pages)), table=ints(np.full((R, max_pages), -1)),
+                 lens=[ints([0] * R), ints([0] * R)], state=[ints([3, n_pages, 0]), ints([0, 0, 0])], fresh=ints([0] * R),
+                 cu=ints([0] * (R + 1)), slots=ints([0] * T), pos=ints([0] * T), pages=pool_of(m, n_pages, hkv, hd, P),
+                 q=torch.zeros(T, hq, hd, dtype=torch.bfloat16, device="cuda"),
+                 k=torch.zeros(T, hkv, hd, dtype=torch.bfloat16, device="cuda"),
+                 ws=torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda"),
+                 out=torch.full((T, hq, hd), 7.0, dtype=torch.bfloat16, device="cuda"))
+        w["v"] = torch.zeros_like(w["k"])
+        return w
+
+    def step(w, i):
+        now, after = i % 2, 1 - i % 2
+        m.page_plan(w["lens"][now], w["fresh"], w["ring"], w["state"][now][:2], w["table"], w["state"][after],
+                    w["lens"][after], w["cu"], w["slots"], w["pos"], page_rows=P)
+        m.rope(w["q"], w["k"], w["q"], w["k"], w["pos"], rope)
+        m.paged_append(w["k"], w["v"], w["slots"], w["pages"], page_rows=P)
+        m.paged_attn(w["q"], w["out"], w["cu"], w["lens"][after], w["table"], w["pages"], n_kv_heads=hkv, page_rows=P,
+                     workspace=w["ws"])
+
+    captured, plain = world(), world()
+    step(world(), 0)                                          # the first call sets kernels up
+    torch.cuda.synchronize()
+    graphs = []
+    for i in (0, 1):                                          # one for each side of the double buffers
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            step(captured, i)
+    gen = torch.Generator("cuda").manual_seed(3)
+    for i, fresh in enumerate(fresh_of):
+        new = [torch.randn(T, h, hd, generator=gen, device="cuda").bfloat16() for h in (hq, hkv, hkv)]
+        for w in (captured, plain):
+            w["fresh"].copy_(torch.tensor(fresh, dtype=torch.int32))
+            for name, x in zip("qkv", new):
+                w[name].copy_(x)
+        graphs[i % 2].replay()
+        step(plain, i)
+        torch.cuda.synchronize()
+        for name in ("out", "table", "ring", "slots", "pos", "cu", "pages"):
+            assert torch.equal(captured[name], plain[name]), (i, name)
+        used = sum(max(f, 0) for f in fresh)
+        assert bool((plain["out"][:used].float() != 7.0).any(-1).all()) and bool(torch.isfinite(plain["out"].float()).all())
+    assert m.get_device_error() == m.OK
 
 
 def test_paged_refuses_shapes_and_types():
