@@ -1,16 +1,22 @@
 // paged_kv.cu -- 4-bit pages written and read back (include/fa.h,
 // fa_paged_append and fa_paged_gather; byte order in paged_layout.cuh).
 //
-// Append: one row of K or V of one kv head takes head_dim / 8 lanes, 8
-// consecutive values each (one word of codes). A 32-value block is four lanes:
-// amax by two shuffles, d = amax / -8, code = round(x / d) + 8 as in the Q4_0
+// Append: one token's rows of K and V of one kv head take head_dim / 16 lanes, 16
+// consecutive values of each a lane (two words of codes). A 32-value block is two lanes:
+// amax by a shuffle, d = amax / -8, code = round(x / d) + 8 as in the Q4_0
 // planes; the row's largest d, by shuffles over its lanes, gives the row's
-// power-of-two factor. One pass, bound by HBM on long prompts.
+// power-of-two factor. One pass, bound by the instructions that a value costs:
+// 131072 tokens of 2 kv heads x 256 in bf16 take 72 us, 4.8 TB/s (8 values a lane,
+// each converted and clamped as an integer, with K and V in different lanes and a
+// division for each row's place: 143 us; with K and V in one lane, 100).
 //
 // Gather: one warp per 16-row group reads its fragments with 16-byte loads and
 // writes the dequantised rows, rounded to binary16, into fp16 planes that
-// fa_prefill_chunk reads in place. Bound by HBM (it writes 3.5 bytes for each
-// byte read).
+// fa_prefill_chunk reads in place. Bound by HBM, and there by its writes, 3.5
+// bytes for each byte read: 12 requests of 9517 rows (8 kv heads x 128), 632 MB with the
+// append, take 105 us, 6.0 TB/s (a copy reaches 6.8, a fill alone 4.0). Dequantising
+// in fp32 instead of packed binary16 took 114 us, scalar loads of the scales 16.5 instead
+// of 14.5 us for 8192 rows.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -22,7 +28,8 @@
 namespace fa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;        // of the gather
+constexpr int kAppendThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ void load8(const T *p, float *x);
@@ -55,70 +62,114 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, flo
     }
 }
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendArgs a) {
-    constexpr int LANES = HD / 8;  // lanes of a row
-    const long long id = blockIdx.x * static_cast<long long>(kThreads) + threadIdx.x;
-    const long long row = id / LANES;  // (token, kv head, part): part fastest
-    const int l = static_cast<int>(id) & (LANES - 1);
-    const int part = static_cast<int>(row & 1);
-    const long long th = row >> 1;
-    const int tok = static_cast<int>(th / a.n_kv), h = static_cast<int>(th % a.n_kv);
-    const bool in = tok < a.n_tokens;
-    const int slot = in ? __ldg(a.slot_map + tok) : -1;
-    const int page = slot >> a.page_shift;
-    const bool live = slot >= 0 && page < a.n_pages;
-    if (in && slot != -1 && !live && l == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
-    float x[8];
-    if (live) {
-        const T *src = static_cast<const T *>(part ? a.v : a.k) +
-                       tok * (part ? a.v_stride : a.k_stride) + static_cast<long long>(h) * HD;
-        load8<T>(src + 8 * l, x);
-    } else {
+// max(a, |x|), NaN if either is one.
+__device__ __forceinline__ float max_abs(float a, float x) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(x)));
+    return d;
+}
+
+// 16 values of a row, half a block, as codes (two words), their block's scale and the row's
+// factor. With finite values and a finite 1 / d the products lie in [-8, 8] but for a rounding,
+// so that one minimum clamps them, and the sum with 1.5 * 2^23 + 8 rounds half to even and has
+// the code in its lowest 4 bits.
+template <int LANES>
+__device__ __forceinline__ void quantise16(const float *x, uint32_t *word, __half *scale, uint16_t *factor) {
+    float most = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) most = max_abs(most, x[i]);
+    most = max_abs(most, __shfl_xor_sync(~0u, most, 1));
+    float amax = most;
+    if (most != most) {  // a NaN never raises the largest magnitude
+        amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
     }
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
     amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 1));
-    amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, 2));
-    const float d = __fdiv_rn(amax, -8.0f);
+    const float d = __fmul_rn(amax, -0.125f);  // amax / -8, rounded alike
     const float inv = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
-    uint32_t word = 0;
+    if (fabsf(inv) <= 3.4e38f && most <= 3.4e38f) {  // and not a NaN
+        constexpr float kMagic = 12582920.0f;
+        constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;  // what the sums' other bits add up to
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int c = min(max(__float2int_rn(__fmul_rn(x[i], inv)), -8), 7) + 8;
-        word |= static_cast<uint32_t>(c) << (4 * i);
+        for (int j = 0; j < 2; ++j) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 7; i >= 0; --i)
+                w = w * 16u + __float_as_uint(__fadd_rn(fminf(__fmul_rn(x[8 * j + i], inv), 7.0f), kMagic));
+            word[j] = w - kBits;
+        }
+    } else {
+        // as Q4_0's encoder for anything: a NaN product is 0, +-inf the last code of its side
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            word[j] = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = min(max(__float2int_rn(__fmul_rn(x[8 * j + i], inv)), -8), 7) + 8;
+                word[j] |= static_cast<uint32_t>(c) << (4 * i);
+            }
+        }
     }
     // the row's factor: the power of two at or below its largest |d|, kept
     // inside the normal range so that it and its inverse are exact
     float top = fabsf(d);
 #pragma unroll
-    for (int m = 4; m < LANES; m <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
-    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 1u), 254u);
-    const float factor = top > 0.0f ? __uint_as_float(ex << 23) : 1.0f;
-    const __half scale = __float2half_rn(__fdiv_rn(d, factor));
+    for (int m = 2; m < LANES; m <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, m));
+    const uint32_t ex = top > 0.0f ? min(max(__float_as_uint(top) >> 23, 1u), 254u) : 127u;
+    // 2^(127 - ex), the factor's inverse: for ex = 254 it is below the normal range
+    const float down = ex < 254u ? __uint_as_float((254u - ex) << 23) : __uint_as_float(1u << 22);
+    *scale = __float2half_rn(__fmul_rn(d, down));
+    *factor = static_cast<uint16_t>(ex << 7);
+}
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedAppendArgs a) {
+    constexpr int LANES = HD / 16;  // lanes of a row
+    const int tok = blockIdx.x * (kAppendThreads / LANES) + threadIdx.x / LANES, h = blockIdx.y;
+    const int l = threadIdx.x & (LANES - 1);
+    const bool in = tok < a.n_tokens;
+    const int slot = in ? __ldg(a.slot_map + tok) : -1;
+    const int page = slot >> a.page_shift;
+    const bool live = slot >= 0 && page < a.n_pages;
+    if (in && slot != -1 && !live && l == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
+    float k[16] = {}, v[16] = {};
+    if (live) {
+        const long long at = static_cast<long long>(h) * HD + 16 * l;
+        const T *src = static_cast<const T *>(a.k) + tok * a.k_stride + at;
+        load8<T>(src, k);
+        load8<T>(src + 8, k + 8);
+        src = static_cast<const T *>(a.v) + tok * a.v_stride + at;
+        load8<T>(src, v);
+        load8<T>(src + 8, v + 8);
+    }
+    uint32_t kw[2], vw[2];
+    __half ks, vs;
+    uint16_t kf, vf;
+    quantise16<LANES>(k, kw, &ks, &kf);
+    quantise16<LANES>(v, vw, &vs, &vf);
     if (!live) return;
     const int pos = slot & ((1 << a.page_shift) - 1);
-    const int r = pos & (kGroupRows - 1), b = l >> 2, t = l & 3;
+    const int r = pos & (kGroupRows - 1), b = l >> 1, t = 2 * (l & 1);
     uint8_t *dst = a.pages + ((static_cast<size_t>(page) * a.n_kv + h) *
                                   ((1 << a.page_shift) / kGroupRows) + pos / kGroupRows) *
-                                 group_bytes(HD) + part * part_bytes(HD);
-    if (part == 0) {
-        *reinterpret_cast<uint32_t *>(dst + k_word_at<HD>(r, b, t)) = word;
-    } else {
-        *reinterpret_cast<uint16_t *>(dst + v_half_at<HD>(r, b, 2 * t)) =
-            static_cast<uint16_t>(word);
-        *reinterpret_cast<uint16_t *>(dst + v_half_at<HD>(r, b, 2 * t + 1)) =
-            static_cast<uint16_t>(word >> 16);
+                                 group_bytes(HD);
+    uint8_t *dv = dst + part_bytes(HD);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<uint32_t *>(dst + k_word_at<HD>(r, b, t + j)) = kw[j];
+        *reinterpret_cast<uint16_t *>(dv + v_half_at<HD>(r, b, 2 * (t + j))) = static_cast<uint16_t>(vw[j]);
+        *reinterpret_cast<uint16_t *>(dv + v_half_at<HD>(r, b, 2 * (t + j) + 1)) =
+            static_cast<uint16_t>(vw[j] >> 16);
     }
-    if (t == 0)
-        *reinterpret_cast<__half *>(
-            dst + (part == 0 ? k_scale_at<HD>(r, b) : v_scale_at<HD>(r, b))) = scale;
-    if (l == 0)
-        *reinterpret_cast<uint16_t *>(dst + factor_offset(HD) + 2 * r) =
-            static_cast<uint16_t>(__float_as_uint(factor) >> 16);
+    if (t == 0) {
+        *reinterpret_cast<__half *>(dst + k_scale_at<HD>(r, b)) = ks;
+        *reinterpret_cast<__half *>(dv + v_scale_at<HD>(r, b)) = vs;
+    }
+    if (l == 0) {
+        *reinterpret_cast<uint16_t *>(dst + factor_offset(HD) + 2 * r) = kf;
+        *reinterpret_cast<uint16_t *>(dv + factor_offset(HD) + 2 * r) = vf;
+    }
 }
 
 // 8 codes c of a word -> (c - 8) * s rounded to binary16, in order. The product
@@ -240,13 +291,12 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherArgs 
 
 template <typename T>
 cudaError_t append_type(const PagedAppendArgs &a, int hd, cudaStream_t stream) {
-    const long long threads = 2ll * a.n_tokens * a.n_kv * (hd / 8);
-    const long long blocks = (threads + kThreads - 1) / kThreads;
-    if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    const int rows = kAppendThreads / (hd / 16);  // tokens of a block, one kv head of each
+    const dim3 grid((a.n_tokens - 1) / rows + 1, a.n_kv);
     auto kernel = hd == 64    ? paged_append_kernel<T, 64>
                   : hd == 128 ? paged_append_kernel<T, 128>
                               : paged_append_kernel<T, 256>;
-    kernel<<<static_cast<unsigned>(blocks), kThreads, 0, stream>>>(a);
+    kernel<<<grid, kAppendThreads, 0, stream>>>(a);
     return cudaGetLastError();
 }
 

@@ -438,7 +438,9 @@ size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
  * Pages are handed out in request order from the head. A request whose new
  * pages are not all left, counting those of every request before it, gets none:
  * its tokens' slots are -1 and its seq_lens entry stays at cached. Pages given
- * back in this step are handed out from the next one on.
+ * back in this step are handed out from the next one on. A page that two
+ * requests hold would be given back by both: tables with shared pages (which
+ * the other calls read like any other) need a caller that keeps them itself.
  *
  * FA_ERR_DEVICE is flagged for lengths out of range (cached < 0, fresh < -1,
  * more than max_pages pages: the request gets no slots and length 0), a state

@@ -327,6 +327,48 @@ def test_append_any_magnitude_and_values_without_one():
             assert np.array_equal(got[places], want[places])
 
 
+@pytest.mark.parametrize("hd", (64, 128, 256))
+def test_append_bytes_of_odd_rows(hd):
+    """Subnormal and largest values, ties, NaN and infinities anywhere: codes as Q4_0's encoder defines them (amax
+    ignores NaN; a NaN product is 0, products beyond the codes are clamped), scales and factors of the same amax."""
+    m = fa()
+    rng = np.random.default_rng(hd)
+    T = 320
+    x = (rng.standard_normal((T, hd // 32, 32)) * 10.0 ** rng.uniform(-46, 37, (T, 1, 1))
+         * 10.0 ** rng.uniform(-3, 0, (T, hd // 32, 1))).astype(np.float32)
+    ties = rng.integers(-16, 16, x.shape).astype(np.float32) / 2
+    ties[..., 0] = -8
+    x[:40] = ties[:40] * np.exp2(rng.integers(-140, 120, (40, 1, 1))).astype(np.float32)
+    for rows, value in ((range(40, 80), np.nan), (range(70, 100), np.inf), (range(100, 120), -np.inf),
+                        (range(120, 140), np.finfo(np.float32).max), (range(140, 160), 2.0 ** -149), (range(150, 180), 0)):
+        for r in rows:
+            x[r][rng.random(x[r].shape) < rng.choice([0.02, 0.3, 1.0])] = value
+    with np.errstate(all="ignore"):
+        d = np.fmax.reduce(np.abs(x), -1, initial=0) / np.float32(-8)
+        inv = np.where(d != 0, np.float32(1) / np.where(d != 0, d, np.float32(1)), np.float32(0)).astype(np.float32)
+        p = (x * inv[..., None]).astype(np.float32)
+        codes = np.clip(np.rint(np.where(np.isnan(p), 0, p)), -8, 7) + 8
+        top = np.abs(d).max(-1)
+        e = np.where(np.isinf(top), 127, np.clip(np.frexp(np.where((top > 0) & ~np.isinf(top), top, 1))[1] - 1, -126, 127))
+        factors = np.where(top > 0, np.exp2(e.astype(np.float64)), 1.0).astype(np.float32)
+        scales = (d / factors[:, None]).astype(np.float16)
+    pages = pool_of(m, T // 16, 1, hd, 16)
+    t = torch.from_numpy(x.reshape(T, 1, hd)).cuda()
+    append(m, pages, t, t, range(T), 16)
+    got = pages.cpu().numpy().reshape(T // 16, 2, -1)
+    for v in (0, 1):
+        places = [ref.code_place(hd, r, i, v) for r in range(16) for i in range(hd)]
+        at, shift = (np.array(a).reshape(16, hd) for a in zip(*places))
+        assert np.array_equal((got[:, v][:, at] >> shift & 15).reshape(T, hd), codes.reshape(T, hd))
+        at = np.array([[ref.scale_place(hd, r, b, v) for b in range(hd // 32)] for r in range(16)])
+        have = (got[:, v][:, at] | got[:, v][:, at + 1].astype(np.uint16) << 8).reshape(T, -1)
+        assert np.array_equal(have, scales.view(np.uint16))
+        at = 9 * hd + 2 * np.arange(16)
+        have = (got[:, v][:, at] | got[:, v][:, at + 1].astype(np.uint32) << 8).reshape(T)
+        assert np.array_equal(have << 16, factors.view(np.uint32))
+    assert m.get_device_error() == m.OK
+
+
 def test_append_slots_out_of_range():
     m = fa()
     pages = pool_of(m, 2, 1, 64, 16)
