@@ -13,8 +13,9 @@
 // sums over all requests for itself (in shared memory, 12 bytes a request;
 // the lengths come from L2), and then takes its share of the flattened list
 // of tokens, new pages and returned pages, each found by bisection. 256 decodes
-// take 6.3 us, 4096 requests with prompt chunks among them 12.0 (13.1 with a
-// scan over the whole block instead of one a warp).
+// take 6.3 us, 4096 requests with prompt chunks among them (341000 tokens) 11.5
+// (12.4 with one block an SM instead of two, 13.5 with a scan over the whole
+// block instead of one a warp).
 #include <algorithm>
 
 #include "fa_device.cuh"
@@ -70,7 +71,7 @@ __device__ __forceinline__ int find(const int *start, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
+__global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) {
     extern __shared__ int sm[];
     int *tok0 = sm, *need0 = sm + a.n_reqs + 1, *back0 = need0 + a.n_reqs + 1;
     const int R = a.n_reqs, N = a.n_pages;
@@ -210,7 +211,7 @@ cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
     }
     const int items = std::max(a.max_tokens, a.n_reqs);
-    const int blocks = std::min(device_sm_count(), (items + kPlanThreads - 1) / kPlanThreads);
+    const int blocks = std::min(2 * device_sm_count(), (items + kPlanThreads - 1) / kPlanThreads);
     page_plan_kernel<<<std::max(blocks, 1), kPlanThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
