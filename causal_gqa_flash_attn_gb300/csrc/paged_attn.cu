@@ -110,12 +110,14 @@ struct Req {
     bool bad;
 };
 
+// Lengths, tables and q are read by ordinary loads, not as read-only data: the
+// kernel may have been launched while the one before it still wrote them.
 template <int ROWS>
 __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_group) {
     Req q;
-    q.q0 = __ldg(a.cu_q + r);
-    const int q1 = __ldg(a.cu_q + r + 1);
-    q.rows = __ldg(a.seq_lens + r);
+    q.q0 = a.cu_q[r];
+    const int q1 = a.cu_q[r + 1];
+    q.rows = a.seq_lens[r];
     const long long room = static_cast<long long>(a.pages.max_pages) * a.pages.groups * kGroupRows;
     q.bad = q.q0 < 0 || q1 < q.q0 || q1 > a.n_tokens || q.rows < 0 || q.rows > room;
     q.nq = q.bad ? 0 : q1 - q.q0;
@@ -835,7 +837,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         int page = 0, group = 0, made = 0, stage = 0;
         auto look = [&]() {  // the table entry of the next tile, one step before its copy
             group = ci < ns ? ci : ci + skip;
-            page = any ? __ldg(table + (group >> a.pages.group_shift)) : -2;
+            page = any ? table[group >> a.pages.group_shift] : -2;
         };
         if (left > 0) look();
         volatile Piece *its = pieces + min(lane, C::WARPS - 1);
@@ -863,7 +865,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
                     k += run;
                     if (k == n) break;
                     group += run;
-                    page = __ldg(table + (group >> a.pages.group_shift));
+                    page = table[group >> a.pages.group_shift];
                 }
                 dead[lane * S + stage] = holes;
                 if (holes) its->holes = 1;
