@@ -49,6 +49,7 @@
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "paged_launch.cuh"
 #include "paged_layout.cuh"
 
 namespace fa {
@@ -110,8 +111,6 @@ struct Req {
     bool bad;
 };
 
-// Lengths, tables and q are read by ordinary loads, not as read-only data: the
-// kernel may have been launched while the one before it still wrote them.
 template <int ROWS>
 __device__ __forceinline__ Req load_req(const PagedAttnArgs &a, int r, int log_group) {
     Req q;
@@ -715,7 +714,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
     mbar_fence_init();
     // programmatic dependent launch: what came before is done from here on, and
     // the join may be set up while this kernel drains
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the cut: sums over all requests, each thread a run of them
@@ -1209,7 +1208,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
     __shared__ float4 part_o[kJoinWarps][32];
     __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const Ws ws = carve(a.workspace, gridDim.x);
     // the tasks, in order of the warps
@@ -1322,22 +1321,6 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
         if (in && slice == 0)
             write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
     }
-}
-
-template <typename K>
-cudaError_t launch_after(K *kernel, int blocks, int threads, size_t smem, cudaStream_t stream,
-                         const PagedAttnArgs &a) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
 template <typename T, int HD, int NT>

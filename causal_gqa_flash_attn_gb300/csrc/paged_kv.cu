@@ -6,7 +6,7 @@
 // amax by a shuffle, d = amax / -8, code = round(x / d) + 8 as in the Q4_0
 // planes; the row's largest d, by shuffles over its lanes, gives the row's
 // power-of-two factor. One pass, bound by the instructions that a value costs:
-// 131072 tokens of 2 kv heads x 256 in bf16 take 72 us, 4.8 TB/s (8 values a lane,
+// 131072 tokens of 2 kv heads x 256 in bf16 take 69 us, 5.0 TB/s (8 values a lane,
 // each converted and clamped as an integer, with K and V in different lanes and a
 // division for each row's place: 143 us; with K and V in one lane, 100).
 //
@@ -14,7 +14,7 @@
 // writes the dequantised rows, rounded to binary16, into fp16 planes that
 // fa_prefill_chunk reads in place. Bound by HBM, and there by its writes, 3.5
 // bytes for each byte read: 12 requests of 9517 rows (8 kv heads x 128), 632 MB with the
-// append, take 105 us, 6.0 TB/s (a copy reaches 6.8, a fill alone 4.0). Dequantising
+// append, take 99.5 us, 6.35 TB/s (a copy reaches 6.8, a fill alone 4.0). Dequantising
 // in fp32 instead of packed binary16 took 114 us, scalar loads of the scales 16.5 instead
 // of 14.5 us for 8192 rows.
 #include <algorithm>
@@ -23,6 +23,7 @@
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "paged_launch.cuh"
 #include "paged_layout.cuh"
 
 namespace fa {
@@ -35,14 +36,14 @@ template <typename T>
 __device__ __forceinline__ void load8(const T *p, float *x);
 template <>
 __device__ __forceinline__ void load8<float>(const float *p, float *x) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p));
-    const float4 b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    const float4 a = load(reinterpret_cast<const float4 *>(p));
+    const float4 b = load(reinterpret_cast<const float4 *>(p) + 1);
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
 }
 template <>
 __device__ __forceinline__ void load8<__half>(const __half *p, float *x) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 w = load(reinterpret_cast<const uint4 *>(p));
     const __half2 *h = reinterpret_cast<const __half2 *>(&w);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -53,7 +54,7 @@ __device__ __forceinline__ void load8<__half>(const __half *p, float *x) {
 }
 template <>
 __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16 *p, float *x) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
+    const uint4 w = load(reinterpret_cast<const uint4 *>(p));
     const uint32_t h[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -125,11 +126,12 @@ __device__ __forceinline__ void quantise16(const float *x, uint32_t *word, __hal
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedAppendArgs a) {
+    wait_for_stream();
     constexpr int LANES = HD / 16;  // lanes of a row
     const int tok = blockIdx.x * (kAppendThreads / LANES) + threadIdx.x / LANES, h = blockIdx.y;
     const int l = threadIdx.x & (LANES - 1);
     const bool in = tok < a.n_tokens;
-    const int slot = in ? __ldg(a.slot_map + tok) : -1;
+    const int slot = in ? load(a.slot_map + tok) : -1;
     const int page = slot >> a.page_shift;
     const bool live = slot >= 0 && page < a.n_pages;
     if (in && slot != -1 && !live && l == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
@@ -216,22 +218,23 @@ __device__ __forceinline__ float factor_of(uint32_t w, int hi) {  // bfloat16
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t *w, const uint8_t *p) {
     if constexpr (N == 4) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p));
+        const uint4 x = load(reinterpret_cast<const uint4 *>(p));
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     } else if constexpr (N == 2) {
-        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p));
+        const uint2 x = load(reinterpret_cast<const uint2 *>(p));
         w[0] = x.x; w[1] = x.y;
     } else {
-        w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        w[0] = load(reinterpret_cast<const uint32_t *>(p));
     }
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherArgs a) {
+    wait_for_stream();
     constexpr int NB = HD / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int h = blockIdx.y, r = blockIdx.z;
-    int rows = __ldg(a.seq_lens + r);
+    int rows = load(a.seq_lens + r);
     const long long room = min(static_cast<long long>(a.max_seq),
                                static_cast<long long>(a.pages.max_pages) * a.pages.groups *
                                    kGroupRows);
@@ -260,8 +263,8 @@ __global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherArgs 
         load_words<NB / 2>(ks + NB / 2, src + scale_offset(HD) + (g + 8) * (2 * NB));
         const uint16_t *kf = reinterpret_cast<const uint16_t *>(src + factor_offset(HD)) + g;
         const uint32_t *vf = reinterpret_cast<const uint32_t *>(sv + factor_offset(HD)) + t;
-        const uint32_t kf01 = __ldg(kf) | static_cast<uint32_t>(__ldg(kf + 8)) << 16;
-        const uint32_t vf01 = __ldg(vf), vf23 = __ldg(vf + 4);
+        const uint32_t kf01 = load(kf) | static_cast<uint32_t>(load(kf + 8)) << 16;
+        const uint32_t vf01 = load(vf), vf23 = load(vf + 4);
         // K: the lane's word (row g or g + 8, block b) is dims 32 b + 8 t ..
 #pragma unroll
         for (int j = 0; j < 2 * NB; ++j) {
@@ -296,8 +299,7 @@ cudaError_t append_type(const PagedAppendArgs &a, int hd, cudaStream_t stream) {
     auto kernel = hd == 64    ? paged_append_kernel<T, 64>
                   : hd == 128 ? paged_append_kernel<T, 128>
                               : paged_append_kernel<T, 256>;
-    kernel<<<grid, kAppendThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, kAppendThreads, 0, stream, a);
 }
 
 }  // namespace
@@ -320,8 +322,7 @@ cudaError_t launch_paged_gather(const PagedGatherArgs &a, int n_reqs, int hd,
     auto kernel = hd == 64    ? paged_gather_kernel<64>
                   : hd == 128 ? paged_gather_kernel<128>
                               : paged_gather_kernel<256>;
-    kernel<<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kernel, grid, kThreads, 0, stream, a);
 }
 
 }  // namespace fa

@@ -18,6 +18,7 @@
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "paged_launch.cuh"
 
 namespace fa {
 
@@ -88,7 +89,7 @@ struct PagedAttnArgs {
 template <int HD>
 __device__ __forceinline__ const uint8_t *group_at(const Pages &P, int r, int h, int i,
                                                    unsigned *err) {
-    const int page = __ldg(P.table + static_cast<size_t>(r) * P.max_pages + (i >> P.group_shift));
+    const int page = load(P.table + static_cast<size_t>(r) * P.max_pages + (i >> P.group_shift));
     if (page < 0 || page >= P.n_pages) {
         flag_error(err, FA_ERRBIT_DEVICE);
         return nullptr;

@@ -13,13 +13,14 @@
 // sums over all requests for itself (in shared memory, 12 bytes a request;
 // the lengths come from L2), and then takes its share of the flattened list
 // of tokens, new pages and returned pages, each found by bisection. 256 decodes
-// take 6.3 us, 4096 requests with prompt chunks among them (341000 tokens) 11.5
-// (12.4 with one block an SM instead of two, 13.5 with a scan over the whole
-// block instead of one a warp).
+// take 4.3 us, 4096 requests with prompt chunks among them (341000 tokens) 9.4
+// (about 1 us more with one block an SM instead of two, and 1 more with a scan over
+// the whole block instead of one a warp).
 #include <algorithm>
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "paged_launch.cuh"
 
 namespace fa {
 namespace {
@@ -72,10 +73,11 @@ __device__ __forceinline__ int find(const int *start, int n, int x) {
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) {
+    wait_for_stream();
     extern __shared__ int sm[];
     int *tok0 = sm, *need0 = sm + a.n_reqs + 1, *back0 = need0 + a.n_reqs + 1;
     const int R = a.n_reqs, N = a.n_pages;
-    int head = __ldg(a.state), count = __ldg(a.state + 1);
+    int head = load(a.state), count = load(a.state + 1);
     const bool bad_ring = head < 0 || head >= N || count < 0 || count > N;
     if (bad_ring) head = count = 0;  // hand out nothing, take nothing back
     // Each warp takes a run of requests, 32 at a time, and leaves the sums before
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
     for (int b = r0; b < r1; b += 32) {
         const int r = b + lane;
         Len3 p{{0, 0, 0}, false};
-        if (r < r1) p = plan_len(a, __ldg(a.cached + r), __ldg(a.fresh + r));
+        if (r < r1) p = plan_len(a, load(a.cached + r), load(a.fresh + r));
         bad |= p.bad;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
     }
     const int i0 = blockIdx.x * kPlanThreads + threadIdx.x, step = gridDim.x * kPlanThreads;
     for (int r = i0; r < R; r += step) {
-        const int c = __ldg(a.cached + r), f = __ldg(a.fresh + r);
+        const int c = load(a.cached + r), f = load(a.fresh + r);
         const Len3 p = plan_len(a, c, f);
         const bool fits = !p.bad && (p.v[1] == 0 || need0[r + 1] <= count);
         a.seq_lens[r] = p.bad || f < 0 ? 0
@@ -168,8 +170,8 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
         int slot = -1, pos = 0;
         if (t < tok0[R]) {
             const int r = find(tok0, R, t);
-            const int c = __ldg(a.cached + r);
-            const Len3 p = plan_len(a, c, __ldg(a.fresh + r));
+            const int c = load(a.cached + r);
+            const Len3 p = plan_len(a, c, load(a.fresh + r));
             if (!p.bad) {
                 pos = c + (t - tok0[r]);
                 if (p.v[1] == 0 || need0[r + 1] <= count) {
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
     }
     for (int i = i0; i < taken; i += step) {
         const int r = find(need0, R, i);
-        const int used = (__ldg(a.cached + r) + mask) >> a.page_shift;
+        const int used = (load(a.cached + r) + mask) >> a.page_shift;
         a.block_table[static_cast<size_t>(r) * a.max_pages + used + (i - need0[r])] =
             a.ring[ring_at(i)];
     }
@@ -212,8 +214,7 @@ cudaError_t launch_page_plan(const PlanArgs &a, cudaStream_t stream) {
     }
     const int items = std::max(a.max_tokens, a.n_reqs);
     const int blocks = std::min(2 * device_sm_count(), (items + kPlanThreads - 1) / kPlanThreads);
-    page_plan_kernel<<<std::max(blocks, 1), kPlanThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(page_plan_kernel, dim3(std::max(blocks, 1)), kPlanThreads, smem, stream, a);
 }
 
 }  // namespace fa

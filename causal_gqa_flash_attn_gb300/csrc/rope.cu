@@ -17,14 +17,15 @@
 // have few registers: with two or four heads in flight per thread (64 and 100
 // registers), 20011 tokens of 40 heads took 71 and 105 us against 66. Sines in
 // registers, a thread walking all heads of its pairs, took 88 us.
-// 8192 tokens x 18 heads x 256 in bf16, a quarter rotated: 31 us (0.72 of HBM;
-// launch and the sines take 5 us of it); 20011 x 40 x 128 in fp16: 66 us (0.92).
+// 8192 tokens x 18 heads x 256 in bf16, a quarter rotated: 28.7 us (0.78 of HBM;
+// the start and the sines take 3 us of it); 20011 x 40 x 128 in fp16: 66 us (0.92).
 #include <algorithm>
 
 #include <cuda_bf16.h>
 
 #include "fa_device.cuh"
 #include "fa_internal.h"
+#include "paged_launch.cuh"
 
 namespace fa {
 namespace {
@@ -56,6 +57,7 @@ struct alignas(V * sizeof(T)) Vec {
 // a pointer is not a multiple of that.
 template <typename T, int V, bool ADJ>
 __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
+    wait_for_stream();
     using W = Vec<T, V>;
     extern __shared__ float4 rope_smem[];
     const int half = a.rotary_dim / 2;
@@ -67,9 +69,9 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     const int n_tok = min(a.tokens_per_block, a.n_tokens - tok0);
     for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
         const int tok = i / half, pair = i - tok * half;
-        const uint4 f = __ldg(static_cast<const uint4 *>(a.table) + pair);
+        const uint4 f = load(static_cast<const uint4 *>(a.table) + pair);
         const int axis = min(static_cast<int>(f.z), a.n_axes - 1);
-        const long long pos = __ldg(a.positions + axis * a.pos_stride + tok0 + tok);
+        const long long pos = load(a.positions + axis * a.pos_stride + tok0 + tok);
         const unsigned long long F = (static_cast<unsigned long long>(f.y) << 32) | f.x;
         const unsigned long long turn = static_cast<unsigned long long>(pos) * F;
         const int top = static_cast<int>((turn + 0x80000000ull) >> 32);
@@ -154,10 +156,8 @@ cudaError_t launch(RopeArgs a, cudaStream_t stream) {
     const dim3 grid(static_cast<unsigned>(blocks), parts);
     const size_t smem = static_cast<size_t>(tokens) * half * 8;
     if (a.adjacent)
-        rope_kernel<T, V, true><<<grid, kRopeThreads, smem, stream>>>(a);
-    else
-        rope_kernel<T, V, false><<<grid, kRopeThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+        return launch_after(rope_kernel<T, V, true>, grid, kRopeThreads, smem, stream, a);
+    return launch_after(rope_kernel<T, V, false>, grid, kRopeThreads, smem, stream, a);
 }
 
 template <typename T>

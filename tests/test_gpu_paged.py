@@ -859,6 +859,77 @@ def test_a_captured_step_replays():
     assert m.get_device_error() == m.OK
 
 
+@pytest.mark.parametrize("captured", (False, True))
+def test_calls_wait_for_all_that_comes_before(captured):
+    """Each call's kernel may be placed before the work ahead of it is done, and has to wait for it: for copies and
+    fills, for kernels of other streams, for a large kernel that still writes its input; and what follows waits too."""
+    m = fa()
+    R, P, hq, hkv, hd, L = 4, 16, 8, 2, 64, 40
+    T, n_pages = R * L, R * 3
+    rope = m.rope_table(1e4 ** (-np.arange(hd // 2) / (hd // 2)))
+    gen = torch.Generator("cuda").manual_seed(11)
+    src = [torch.randn(T, h, hd, generator=gen, device="cuda") for h in (hq, hkv, hkv)]
+    big = torch.zeros(64 << 20, dtype=torch.float32, device="cuda")
+    first = ints(np.arange(n_pages))
+    pb = m.kv_plane_bytes(m.KV_F16, hkv, L, hd)
+    ws = torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda")
+
+    def buffers():
+        return dict(q=torch.zeros_like(src[0]), k=torch.zeros_like(src[1]), v=torch.zeros_like(src[2]),
+                    fresh=ints([0] * R), ring=ints([0] * n_pages), table=ints(np.full((R, 3), -1)), lens=ints([9] * R),
+                    state=ints([0] * 3), cu=ints([0] * (R + 1)), slots=ints([0] * T), pos=ints([0] * T),
+                    pages=pool_of(m, n_pages, hkv, hd, P), out=torch.zeros_like(src[0]),
+                    planes=torch.zeros(2, R * pb, dtype=torch.uint8, device="cuda"), lens0=ints([0] * R),
+                    state0=ints([0, n_pages]), sum=torch.zeros(4, dtype=torch.float64, device="cuda"))
+
+    def work(b, wait):
+        """wait: the host waits after every step, so that nothing can overlap."""
+        def next_():
+            if wait:
+                torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):                     # q and v come from another stream, late
+            big.add_(1.0)
+            b["q"].copy_(src[0]); b["v"].copy_(src[2])
+        b["fresh"].fill_(L); next_()
+        b["ring"].copy_(first); next_()
+        m.page_plan(b["lens0"], b["fresh"], b["ring"], b["state0"], b["table"], b["state"], b["lens"], b["cu"],
+                    b["slots"], b["pos"], page_rows=P); next_()
+        b["k"].copy_(src[1])
+        torch.cuda.current_stream().wait_stream(side); next_()
+        m.rope(b["q"], b["k"], b["q"], b["k"], b["pos"], rope); next_()
+        m.paged_append(b["k"], b["v"], b["slots"], b["pages"], page_rows=P); next_()
+        m.paged_gather(b["pages"], b["table"], b["lens"], *b["planes"], n_kv_heads=hkv, head_dim=hd, page_rows=P,
+                       max_seq=L); next_()
+        m.paged_attn(b["q"], b["out"], b["cu"], b["lens"], b["table"], b["pages"], n_kv_heads=hkv, page_rows=P,
+                     workspace=ws); next_()
+        b["sum"][0] = b["out"].double().sum()
+        b["q"].zero_(); next_()                           # the queries may be overwritten after the call
+        m.rope(b["out"], None, b["q"], None, b["pos"], rope, inverse=True); next_()
+        b["sum"][1] = b["q"].double().sum()
+        big.mul_(0.5)
+
+    want, got = buffers(), buffers()
+    work(want, True)
+    torch.cuda.synchronize()
+    if captured:
+        work(buffers(), False)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            work(got, False)
+        for _ in range(3):
+            graph.replay()
+    else:
+        work(got, False)
+    torch.cuda.synchronize()
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    assert bool(torch.isfinite(want["sum"][:2]).all()) and float(want["sum"][0]) != 0
+    assert m.get_device_error() == m.OK
+
+
 def test_paged_refuses_shapes_and_types():
     m = fa()
     P, hkv, hd = 16, 2, 64
