@@ -74,11 +74,13 @@ struct Cfg {
     static constexpr int NB = HD / 32;
     static constexpr int GB = group_bytes(HD);
     // Warps that compute (and one more that copies), groups that are taken at once (TILE) and
-    // tiles of a warp's ring, as measured: as many warps as have registers for their state, and
-    // tiles that give the copying warp few copies to issue. Head_dim 256, bf16: 11 warps 109 us
-    // (32 x 32768 rows, 2 kv heads), 15 112, 7 130, 11 with tiles of 2 114; head_dim 128, fp32: 11
-    // warps 82 us (32 x 16384 rows, 4 kv heads), 15 with single groups 84; head_dim 64, bf16:
-    // single groups 124 us (64 x 16384 rows, 4 kv heads), tiles of 4 68.
+    // tiles of a warp's ring, as measured: as many warps as have registers for their state, with
+    // the copying one a multiple of the SM's four schedulers, and tiles that give that one few
+    // copies to issue. Head_dim 256, bf16 (32 x 32768 rows, 2 kv heads): 11 warps 112 us, 10 120,
+    // 12 124, 13 128, 7 130, 11 with tiles of two groups 2% slower; head_dim 128 (32 x 16384 rows,
+    // 8 kv heads): bf16 15 warps 114 us, 14 121, 13 127, fp32 11 warps 158 us, 12 162, 10 171,
+    // 13 with single groups 183; head_dim 64, bf16 (64 x 16384 rows, 4 kv heads): tiles of four
+    // groups 69 us, single groups 124.
     static constexpr int WARPS = HD == 256 || (HD == 128 ? PSPLIT || NT == 2 : PSPLIT && NT == 2) ? 11 : 15;
     static constexpr int TILE = HD == 256 ? 1 : HD == 128 || NT == 2 ? 2 : 4;
     static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : HD == 64 && NT == 2 ? 4 : 2;
