@@ -82,7 +82,8 @@ fa_status fa_page_plan(const int32_t *cached, const int32_t *fresh, int n_reqs,
     if (n_reqs < 0 || max_tokens < 0 || page_shift(page_rows) < 0 ||
         !good_pages(n_pages, max_pages, page_rows))
         return FA_ERR_INVALID;
-    if (n_reqs > fa::kPlanMaxReqs) return FA_ERR_UNSUPPORTED;
+    // a thread's next token is counted in 31 bits
+    if (n_reqs > fa::kPlanMaxReqs || max_tokens > 1 << 30) return FA_ERR_UNSUPPORTED;
     if (!free_ring || !ring_state || !ring_state_out || !cu_fresh) return FA_ERR_INVALID;
     if (n_reqs > 0 && (!cached || !fresh || !block_table || !seq_lens)) return FA_ERR_INVALID;
     if (max_tokens > 0 && (!slot_map || !positions)) return FA_ERR_INVALID;
@@ -207,6 +208,7 @@ fa_status fa_paged_append(const void *k_new, const void *v_new, int dtype, int64
     if (st != FA_OK) return st;
     if (!known_type(dtype) || n_tokens < 0 || !good_pages(n_pages, 1, page_rows))
         return FA_ERR_INVALID;
+    if (n_tokens > 1 << 30) return FA_ERR_UNSUPPORTED;  // a block's last token in 31 bits
     if (n_tokens == 0) return FA_OK;
     if (!k_new || !v_new || !slot_map || !pages || !aligned4(slot_map) || !aligned(pages, 16) ||
         !good_stride(k_stride, n_kv_heads, head_dim, n_tokens) ||
@@ -238,7 +240,7 @@ fa_status fa_paged_gather(const void *pages, int n_pages, const int32_t *block_t
     if (st != FA_OK) return st;
     if (n_reqs < 0 || max_seq < 1 || !good_pages(n_pages, max_pages, page_rows))
         return FA_ERR_INVALID;
-    if (n_reqs > 65535) return FA_ERR_UNSUPPORTED;
+    if (n_reqs > 65535 || max_seq > 1 << 30) return FA_ERR_UNSUPPORTED;
     if (n_reqs == 0) return FA_OK;
     if (!pages || !block_table || !seq_lens || !k_planes || !v_planes || !aligned(pages, 16) ||
         !aligned4(block_table) || !aligned4(seq_lens) || !aligned(k_planes, 16) ||

@@ -448,8 +448,8 @@ size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
  * the ring has room for, a table entry outside [0, n_pages) under a fresh token
  * (slot -1), or more than max_tokens tokens (cu_fresh is cut there).
  * No output may overlap an input or another output; free_ring and block_table
- * are updated in place. n_reqs <= 16384 (FA_ERR_UNSUPPORTED); max_pages *
- * page_rows <= 2^30, n_pages * page_rows < 2^31. */
+ * are updated in place. n_reqs <= 16384 and max_tokens <= 2^30
+ * (FA_ERR_UNSUPPORTED); max_pages * page_rows <= 2^30, n_pages * page_rows < 2^31. */
 fa_status fa_page_plan(const int32_t *cached, const int32_t *fresh, int n_reqs,
                        int32_t *free_ring, int n_pages, const int32_t *ring_state,
                        int32_t *ring_state_out, int32_t *block_table, int max_pages,
@@ -496,7 +496,8 @@ fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dt
  *              and are left out. Slots of one call must differ (those of
  *              fa_page_plan do): a row written twice by one call holds a mixture
  *              of both.
- *   pages      n_pages pages of this geometry. */
+ *   pages      n_pages pages of this geometry.
+ * n_tokens <= 2^30, n_kv_heads <= 65535 (FA_ERR_UNSUPPORTED). */
 fa_status fa_paged_append(const void *k_new, const void *v_new, int dtype, int64_t k_stride,
                           int64_t v_stride, const int32_t *slot_map, int n_tokens, void *pages,
                           int n_pages, int n_kv_heads, int head_dim, int page_rows,
@@ -507,7 +508,8 @@ fa_status fa_paged_append(const void *k_new, const void *v_new, int dtype, int64
  * 0 .. seq_lens[r] - 1 of each; the other rows stay as they are. Values past the
  * binary16 range become infinite. A length below 0, above max_seq or above the
  * table's rows is cut and flags FA_ERR_DEVICE; a table entry outside [0,
- * n_pages) flags it too, and its rows stay as they are. n_reqs <= 65535. */
+ * n_pages) flags it too, and its rows stay as they are. n_reqs <= 65535,
+ * max_seq <= 2^30. */
 fa_status fa_paged_gather(const void *pages, int n_pages, const int32_t *block_table,
                           int max_pages, const int32_t *seq_lens, int n_reqs, int n_kv_heads,
                           int head_dim, int page_rows, void *k_planes, void *v_planes,

@@ -48,6 +48,7 @@ def test_plan_refusals(fa):
                 dict(pos=None), dict(cached=18), dict(pos=18), dict(state_out=16), dict(lens=16)):
         assert call(**bad) == fa.ERR_INVALID, bad
     assert call(n=16385) == fa.ERR_UNSUPPORTED
+    assert call(max_tokens=(1 << 30) + 1) == fa.ERR_UNSUPPORTED
 
 
 def test_rope_refusals(fa):
@@ -98,6 +99,8 @@ def test_append_refusals(fa):
                 dict(rows=24)):
         assert call(**bad) == fa.ERR_INVALID, bad
     assert call(hd=96) == fa.ERR_UNSUPPORTED
+    assert call(n=(1 << 30) + 1) == fa.ERR_UNSUPPORTED
+    assert call(hkv=65536, ks=1 << 22, vs=1 << 22) == fa.ERR_UNSUPPORTED
     assert call(n=0) == fa.OK
 
 
@@ -111,6 +114,7 @@ def test_gather_refusals(fa):
         assert call(**bad) == fa.ERR_INVALID, bad
     assert call(hd=96) == fa.ERR_UNSUPPORTED
     assert call(n=65536) == fa.ERR_UNSUPPORTED
+    assert call(max_seq=(1 << 30) + 1) == fa.ERR_UNSUPPORTED
     assert call(n=0) == fa.OK
 
 
