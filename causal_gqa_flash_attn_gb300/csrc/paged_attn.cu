@@ -37,9 +37,10 @@
 // group) units, are cut into equal runs, one per warp of one block per SM; a
 // warp streams its run through its own ring of bulk copies, which one more warp
 // issues. A unit inside one warp's run is written directly. Pieces of longer
-// units are joined: those that end the runs of neighbouring warps of a block in
-// shared memory, the others (at most two per warp) through the workspace by a
-// second kernel, in a fixed order.
+// units are joined by their block: they end the runs of neighbouring warps and
+// lie in their rings, but for a last one that begins a run, which waits in the
+// workspace (TAILS). Units that several blocks share are joined by a second
+// kernel. All in a fixed order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -89,6 +90,11 @@ struct Cfg {
     static constexpr int WARPS = HD == 256 || (HD == 128 ? PSPLIT || NT == 2 : PSPLIT && NT == 2) ? 11 : 15;
     static constexpr int TILE = HD == 256 ? 1 : HD == 128 || NT == 2 ? 2 : 4;
     static constexpr int STAGES = HD == 256 ? (QSPLIT ? 2 : 3) : HD == 64 && NT == 2 ? 4 : 2;
+    // What a warp begins its run with is joined by its block, if that has the unit's other pieces:
+    // 256 x 300 rows of 8 kv heads x 128, 41.1 -> 35.3 us, when each unit has such an end. With
+    // head_dim 256 the second kernel does it better (128 windowed requests 19.5 us, 23.4 here; 32
+    // requests of 32768 rows 109.3 and 114.1).
+    static constexpr bool TAILS = HD < 256;
     static constexpr int STAGE = TILE * GB;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int QF = NB * 32 * 16;           // q as B fragments
@@ -194,8 +200,8 @@ __device__ __forceinline__ Cut make_cut(long long N, int blocks) {
 // holds its first group. Where its pieces lie is one word:
 //   bits 0-8    the blocks that hold joined pieces (0: no task)
 //   bits 9-13   the warps of a block that work
-//   bits 14-26  1 + the warp (over all blocks) that begins its run with the unit's
-//               last piece and goes on, or 0
+//   bits 14-26  1 + the warp (over all blocks) that begins its run with the unit's last piece
+//               and goes on, where its block does not join that piece, or 0
 struct Task {
     int h, rg;
     Req q;
@@ -1162,61 +1168,72 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
     const unsigned same = __ballot_sync(~0u, lane < C::WARPS && pieces[min(lane, C::WARPS - 1)].fin_unit == unit &&
                                                  pieces[min(lane, C::WARPS - 1)].fin_r == r);
     const int w0 = __ffs(same) - 1, w1 = 32 - __clz(same);
-    const int id0 = blockIdx.x * cut.A + w0;
-    const bool from_start = cut.start(blockIdx.x, w0) <= first;
-    const bool direct = from_start && cut.start(blockIdx.x, w1) >= last;
+    // The unit's end may be what the next warp began its run with: in the workspace, and joined
+    // here too, if that warp is the block's (whose last parts may be empty; TAILS).
+    const bool from_start = cut.start(blockIdx.x, w0) <= first, more = cut.start(blockIdx.x, w1) < last;
+    const bool tail_here = C::TAILS && more && w1 < cut.A && cut.start(blockIdx.x, w1 + 1) > cut.start(blockIdx.x, w1);
+    const bool direct = from_start && (tail_here || !more);
     const Req q = load_req<ROWS>(a, r, log_group);
     const int h = unit / q.rgs, rg = unit - h * q.rgs;
-    float *dst = ws.partial + static_cast<size_t>(id0) * 2 * C::PARTIAL;
+    float *dst = ws.partial + static_cast<size_t>(blockIdx.x * cut.A + w0) * 2 * C::PARTIAL;
+    const float *tail = ws.partial + (static_cast<size_t>(blockIdx.x * cut.A + w1) * 2 + 1) * C::PARTIAL;
     if (from_start && !direct && warp == w0 && lane == 0) {
         const int e = cut.warp_of(last - 1);  // the warp that holds the unit's last group
-        const bool tail = cut.start(e / cut.A, e % cut.A + 1) > last + kUnitCost;  // whose run goes on
+        // its run goes on, and its block does not join what it began with: a piece for the join
+        const bool alone = (!C::TAILS || e % cut.A == 0) && cut.start(e / cut.A, e % cut.A + 1) > last + kUnitCost;
         ws.pieces[blockIdx.x * kMostWarps + warp] =
-            pack_pieces((tail ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1, cut.A, tail ? e : -1);
+            pack_pieces((alone ? e - 1 : e) / cut.A - static_cast<int>(blockIdx.x) + 1, cut.A, alone ? e : -1);
         ws.tasks[blockIdx.x * kMostWarps + warp] = Task{h, rg, q};
     }
-#pragma unroll 1
-    for (int e = 0; e < NT; ++e) {
-        float M[2], L[2], f[2][C::WARPS];  // of columns 8 e + 2 t + 0, 1
+    // Factors of the pieces, one lane for each column and every (32 / ROWS)-th piece, into the
+    // memory of q: factor[piece][column], the tail's after the others, and then M and L.
+    float *factor = reinterpret_cast<float *>(qs);
+    static_assert((C::WARPS + 3) * ROWS * 4 <= C::QB, "the factors fit the memory of q");
+    const int n_pieces = w1 - w0 + (tail_here ? 1 : 0);
+    {
+        constexpr int STEP = 32 / ROWS;
+        const int n = lane % ROWS;
+        auto m_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].m[n] : tail[n]; };
+        float M = kLowest, L = 0.0f;
+        for (int k = lane / ROWS; k < n_pieces; k += STEP) M = fmaxf(M, m_of(k));
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            const int n = 8 * e + 2 * t + c;
-            M[c] = kLowest;
-            L[c] = 0.0f;
+        for (int d = ROWS; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+        for (int k = lane / ROWS; k < n_pieces; k += STEP) {
+            const float f = ex2(m_of(k) - M);
+            factor[k * ROWS + n] = f;
+            L = fmaf(k < w1 - w0 ? pieces[w0 + k].l[n] : tail[ROWS + n], f, L);
+        }
 #pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) {
-                f[c][w] = w >= w0 && w < w1 ? pieces[w].m[n] : kLowest;
-                M[c] = fmaxf(M[c], f[c][w]);
-            }
-#pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) {
-                f[c][w] = ex2(f[c][w] - M[c]);
-                if (w >= w0 && w < w1) L[c] = fmaf(pieces[w].l[n], f[c][w], L[c]);
-            }
-            if (!direct && warp == w0 && g == 0) {
-                dst[n] = M[c];
-                dst[ROWS + n] = L[c];
+        for (int d = ROWS; d < 32; d <<= 1) L += __shfl_xor_sync(~0u, L, d);
+        if (lane < ROWS) {
+            factor[(C::WARPS + 1) * ROWS + n] = M;
+            factor[(C::WARPS + 2) * ROWS + n] = L;
+            if (!direct && warp == w0) {
+                dst[n] = M;
+                dst[ROWS + n] = L;
             }
         }
-        for (int i = warp - w0; i < 2 * NB; i += w1 - w0) {  // (block, column) pairs
-            const int b = i >> 1, c = i & 1, at = st.quad_at(e, b, c) * 32 + lane;
-            float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int w = 0; w < C::WARPS; ++w) {
-                if (w < w0 || w >= w1) continue;
-                const float4 y = *(reinterpret_cast<const float4 *>(smem + w * C::RING) + at);
-                const float k = c ? f[1][w] : f[0][w];
-                x.x = fmaf(y.x, k, x.x);
-                x.y = fmaf(y.y, k, x.y);
-                x.z = fmaf(y.z, k, x.z);
-                x.w = fmaf(y.w, k, x.w);
-            }
-            if (direct)
-                write_row<T>(a, column<ROWS>(q, rg, 8 * e + 2 * t + c, h, log_group), HD, 32 * b + 4 * g, x,
-                             c ? M[1] : M[0], c ? L[1] : L[0]);
-            else
-                *(reinterpret_cast<float4 *>(dst + 2 * ROWS) + at) = x;
+        __syncwarp();
+    }
+    for (int i = warp - w0; i < 2 * NB * NT; i += w1 - w0) {  // (eight, block, column) triples
+        const int n = 8 * (i / (2 * NB)) + 2 * t + (i & 1), b = (i >> 1) % NB, at = i * 32 + lane;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (tail_here)
+            x = scaled(*(reinterpret_cast<const float4 *>(tail + 2 * ROWS) + at), factor[(w1 - w0) * ROWS + n]);
+#pragma unroll 4
+        for (int w = w0; w < w1; ++w) {
+            const float4 y = *(reinterpret_cast<const float4 *>(smem + w * C::RING) + at);
+            const float k = factor[(w - w0) * ROWS + n];
+            x.x = fmaf(y.x, k, x.x);
+            x.y = fmaf(y.y, k, x.y);
+            x.z = fmaf(y.z, k, x.z);
+            x.w = fmaf(y.w, k, x.w);
         }
+        if (direct)
+            write_row<T>(a, column<ROWS>(q, rg, n, h, log_group), HD, 32 * b + 4 * g, x,
+                         factor[(C::WARPS + 1) * ROWS + n], factor[(C::WARPS + 2) * ROWS + n]);
+        else
+            *(reinterpret_cast<float4 *>(dst + 2 * ROWS) + at) = x;
     }
 }
 

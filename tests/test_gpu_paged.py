@@ -670,6 +670,20 @@ def test_attn_many_requests_of_every_length():
     check_attn(lens, [1] * 60, 16, 2, 256, 32, "bf16")
 
 
+@pytest.mark.parametrize("dtype,hd,rows", [("f32", 128, range(4000, 4700, 48)), ("bf16", 64, range(5300, 6300, 64))])
+def test_attn_cuts_with_and_without_rest(dtype, hd, rows):
+    """40 equal units whose lengths pass over every remainder of the cut, empty last parts of a block among them."""
+    for L in rows:
+        check_attn([L] * 5, [1] * 5, 8, 8, hd, 32, dtype, seed=L)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+def test_attn_cuts_of_short_units(dtype):
+    """Units about as long as a warp's part, shorter and longer: most are shared by two warps."""
+    for L, R, hkv in ((20, 1030, 2), (45, 700, 1), (300, 130, 2), (320, 77, 4)):
+        check_attn([L] * R, [1] * R, 16 * hkv if dtype != "f32" else 4 * hkv, hkv, 128, 16, dtype, seed=L)
+
+
 def test_attn_more_requests_than_threads():
     rng = np.random.default_rng(12)
     n = 3000
