@@ -62,7 +62,9 @@ constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 // The start and end of a unit (its rows of q as operands, its output) cost a
 // warp about as much as kUnitCost groups: 6000 against 2200 cycles.
 constexpr int kUnitCost = 3;
-constexpr int kMinWork = 6;       // work per warp below which fewer warps work; > kUnitCost
+// Work per warp below which fewer warps work; > kUnitCost. One request of 600 rows 11.7 us
+// (12.3 with 6, 13.9 with 9), 32 of 64 rows 13.5 (15.3, 17.5), long ones alike.
+constexpr int kMinWork = 4;
 // Requests that each warp sums by itself, one a lane, without a step of the whole
 // block: 32 requests of 2048 rows 21.2 us instead of 22.0, one of 600 rows 12.6 instead
 // of 13.2. With several requests a lane nothing is left of that (64: 21.9 and 22.1, 256:
