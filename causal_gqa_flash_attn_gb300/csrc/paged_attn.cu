@@ -20,11 +20,17 @@
 //     times as many tokens as fit ("row group"; 16 rows where 16 heads share).
 //   - V's block scales multiply the softmax weights (8 columns) instead of the
 //     codes; each V row's power-of-two factor 2^e is added to its score's
-//     exponent, so the scaled weights stay in binary16's range whatever the
-//     values' magnitude. The sum of weights takes 2^-e back out.
-//   - The reference that scores are taken relative to is moved only when a score
+//     exponent, so the scaled weights 2^(s + e - m) stay in binary16's range
+//     whatever the values' magnitude.
+//   - The reference m that these are taken relative to is moved only when one
 //     passes it by 2^14 (kLift above the last maximum, up to binary16's range):
 //     one vote per tile instead of a reduction.
+//   - The sum of weights has nothing to do with V. While every e is within
+//     +-kNear a scaled weight times 2^-e is what it needs, relative to the same m:
+//     at most 2^44, and one that fp32 loses on the way is below 2^-72 of the
+//     largest. Columns that see other rows take the weights of such a group from
+//     the scores, and have a reference r of these for their sums where m is not near
+//     enough to serve (sum_apart).
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
 // the scaled weights. Their codes become (c - 8) * 2^-9 (one AND and one packed
 // multiply-add for two): the tensor core aligns a sum's terms by their
@@ -45,6 +51,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <type_traits>
 
@@ -59,6 +66,8 @@ namespace {
 constexpr float kLowest = -1e30f;  // reference of a row that has seen no key
 constexpr float kLift = 6.0f;      // log2 of the largest weight right after a move
 constexpr float kMost = 14.0f;     // log2 weight that moves the reference
+constexpr int kNear = 30;          // |e| of V's rows whose scaled weights the sum of weights can use
+constexpr int kBias = 127;         // of fp32's exponents
 // The start and end of a unit (its rows of q as operands, its output) cost a
 // warp about as much as kUnitCost groups: 6000 against 2200 cycles.
 constexpr int kUnitCost = 3;
@@ -108,8 +117,9 @@ struct Cfg {
     static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 8;
     static constexpr int SMEM = OFF_DEAD + WARPS * STAGES * 4;
     static constexpr int THREADS = (WARPS + 1) * 32;
-    // a partial: m and l of the rows, then O as the lanes hold it
-    static constexpr int PARTIAL = 2 * ROWS + ROWS * HD;  // floats
+    // a partial, in floats: m, l and r of the rows, then O as the lanes hold it
+    static constexpr int HEAD = 3 * ROWS;
+    static constexpr int PARTIAL = HEAD + ROWS * HD;
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
     static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
     static_assert(kMinWork > kUnitCost, "a part of the cut has a group, but for a block's last");
@@ -375,7 +385,7 @@ __device__ __forceinline__ Col column(const Req &q, int rg, int n, int h, int lo
     return c;
 }
 
-// The state of one piece: O, reference and weight sum of the lane's columns
+// The state of one piece: O, references and weight sum of the lane's columns
 // 8 e + 2 t and 8 e + 2 t + 1 (O: dims 32 b + 4 g + 0, 2 in rows g of tiles 0, 1
 // and 32 b + 4 g + 1, 3 in rows g + 8).
 template <typename C>
@@ -384,7 +394,7 @@ struct State {
     // the codes' factors come out of rows g and g + 8
     static constexpr float U0 = C::PSPLIT ? 512.0f : 16777216.0f, U1 = C::PSPLIT ? 512.0f : 1048576.0f;
     float o[NT][NB][2][4];
-    float m[NT][2], l[NT][2];
+    float m[NT][2], l[NT][2];  // (r is m, or in the Piece)
     __device__ __forceinline__ void clear() {
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
@@ -418,16 +428,23 @@ __device__ __forceinline__ float4 scaled(float4 v, float s) {
     return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
 }
 
-// Four dims of a finished row, and with the first ones its log-sum-exp.
+__device__ __forceinline__ float power_of_two(int n) {  // -126 <= n <= 127
+    return __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
+}
+
+// Four dims of a finished row, x 2^(m - r) / l, and with the first ones its log-sum-exp.
 template <typename T>
 __device__ __forceinline__ void write_row(const PagedAttnArgs &a, const Col &col, int hd, int dim,
-                                          float4 x, float m, float l) {
+                                          float4 x, float m, float l, float r) {
     if (col.token < 0) return;
+    // in two steps, as V may be near either end of the exponents
+    const int n = static_cast<int>(fminf(fmaxf(m - r, -250.0f), 250.0f)), half = n / 2;
+    x = scaled(x, l > 0.0f ? 1.0f / l : l);  // nothing attended: 0 (a NaN stays one)
     store4<T>(static_cast<T *>(a.out) + col.token * a.out_stride +
                   static_cast<long long>(col.head) * hd + dim,
-              scaled(x, l > 0.0f ? 1.0f / l : l));  // nothing attended: 0 (a NaN stays one)
+              scaled(scaled(x, power_of_two(half)), power_of_two(n - half)));
     if (a.lse && dim == 0)
-        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (m + log2f(l)) * kLn2;
+        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (r + log2f(l)) * kLn2;
 }
 
 // Groups that are taken at once from group i of a unit on, which is read up to
@@ -454,15 +471,88 @@ struct Piece {
     int fin_r, fin_unit;        // the piece that ends the run, if other warps have more of its unit (else -1)
     long long fin_first, fin_last;  // that unit's groups in the cut's measure
     float m[16], l[16];         // and the piece's references and sums
+    uint32_t own;               // columns whose r is not m (a bit for each)
+    float base[16];             // their r, and that of all columns of the piece that ends the run
 };
+
+// The new reference where the largest value is u. Whole numbers: 2^(m - r) is then exact.
+__device__ __forceinline__ float moved(float from, float u) { return u - from > kMost ? floorf(u) - kLift : from; }
+
+__device__ __forceinline__ int exponent(float inv) {  // e of 2^-e
+    return kBias - static_cast<int>(__float_as_uint(inv) >> 23);
+}
+
+__device__ __forceinline__ float highest(float a, float b) {  // of a column's values in all its lanes
+    float u = fmaxf(a, b);
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) u = fmaxf(u, __shfl_xor_sync(~0u, u, d));
+    return u;
+}
+
+// The sum's weights of two rows in a column, from their scaled ones (which are 0 for an unseen row,
+// whose factor may be anything).
+template <bool EDGE>
+__device__ __forceinline__ float weight_of(float dA, float dB, float invA, float invB) {
+    return fmaf(dA, EDGE && dA == 0.0f ? 0.0f : invA, EDGE && dB == 0.0f ? 0.0f : dB * invB);
+}
+
+// A group's weights for columns that see a row of V beyond kNear, into their sums: from the scores,
+// relative to a reference r that follows the scores alone. Where m comes out near that, the sum
+// goes back to m. What enters a column's sum, and how, depends on what that column sees and not on
+// its neighbours.
+// False, and nothing done, if no column sees such a row.
+template <int NT>
+struct Group {
+    float y[NT][4], inv[2];    // s + e and 2^-e of the lane's rows
+    float m[NT][2], l[NT][2];  // as in State, before the group; l: after it
+};
+template <int NT>
+__device__ __forceinline__ bool sum_apart(Group<NT> *group, volatile Piece *pc) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t had = pc->own;
+    uint32_t apart = had, own = 0;  // columns summed here, and columns whose r stays their own
+    for (int e = 0; e < NT; ++e)
+        for (int c = 0; c < 2; ++c) {
+            bool far = false;
+            for (int i = 0; i < 2; ++i)
+                far |= abs(exponent(group->inv[i])) > kNear && group->y[e][2 * i + c] != -INFINITY;
+            if (__ballot_sync(~0u, far) >> t & 0x11111111u) apart |= 1u << (8 * e + 2 * t + c);
+        }
+    if (!__any_sync(~0u, apart != 0)) return false;
+    for (int e = 0; e < NT; ++e)
+        for (int c = 0; c < 2; ++c) {
+            const int col = 8 * e + 2 * t + c;
+            const bool its = apart >> col & 1;
+            const float yA = group->y[e][c], yB = group->y[e][2 + c];
+            const float sA = yA - exponent(group->inv[0]), sB = yB - exponent(group->inv[1]);
+            const float m = group->m[e][c], n = moved(m, highest(yA, yB)), v = highest(sA, sB);
+            const float from = had >> col & 1 ? pc->base[col] : m, r = its ? moved(from, v) : n;
+            float l = group->l[e][c] * ex2(from - r);
+            l += its ? ex2(sA - r) + ex2(sB - r)
+                     : weight_of<true>(ex2(yA - n), ex2(yB - n), group->inv[0], group->inv[1]);
+            if (fabsf(n - r) <= kNear)
+                l *= ex2(r - n);
+            else
+                own |= 1u << col;  // (a NaN too)
+            group->l[e][c] = l;
+            __syncwarp();  // every lane has read the old r
+            if (g == 0) pc->base[col] = r;
+        }
+    own = __reduce_or_sync(~0u, own);
+    if (lane == 0) pc->own = own;
+    __syncwarp();
+    return true;
+}
 
 // M groups of the run, at kp[0..M-1] in shared memory: scores, weights, O.
 // EDGE: not every row of the unit sees the (one) group whole; j0 is its first
-// key and pc says what is seen.
+// key and pc says what is seen. Rows of V beyond kNear are looked at in edges
+// alone. True: the groups have to be taken as such, one by one, and nothing is done; or,
+// of an edge, those that follow in the piece, as a column's sum has its own reference.
 template <typename C, int M, bool EDGE>
-__device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
+__device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], const uint8_t *qs,
                                      const uint8_t *bias, const float (&km)[C::NT][2],
-                                     const volatile Piece *pc, int j0, int sink, int win) {
+                                     volatile Piece *pc, int j0, int sink, int win) {
     constexpr int NB = C::NB, HD = NB * 32, NT = C::NT;
     static_assert(M == 1 || !EDGE, "edges are taken one by one");
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -534,6 +624,7 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
         }
     }
     float iA[M], iB[M];  // 2^-e of V's rows
+    int least = 255;     // of their biased exponents
 #pragma unroll
     for (int k = 0; k < M; ++k) {
         const uint8_t *kf = kp[k] + factor_offset(HD) + 2 * g, *vf = kf + part_bytes(HD);
@@ -542,6 +633,7 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
         const float eA = static_cast<float>(xA - 127), eB = static_cast<float>(xB - 127);
         iA[k] = __uint_as_float(static_cast<uint32_t>(254 - xA) << 23);
         iB[k] = __uint_as_float(static_cast<uint32_t>(254 - xB) << 23);
+        least = min(least, min(xA, xB));
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             y[k][e][0] = fmaf(y[k][e][0] * fA, km[e][0], eA);
@@ -569,7 +661,30 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
         for (int e = 0; e < NT; ++e)
             top = fmaxf(top, fmaxf(fmaxf(y[k][e][0], y[k][e][2]) - st.m[e][0],
                                    fmaxf(y[k][e][1], y[k][e][3]) - st.m[e][1]));
-    if (__any_sync(~0u, top > kMost)) {
+    bool apart = false;
+    if (__any_sync(~0u, least < kBias - kNear || (EDGE && pc->own) || top > kMost)) {
+        bool far = EDGE && pc->own;
+#pragma unroll
+        for (int k = 0; k < M; ++k) far |= abs(exponent(iA[k])) > kNear || abs(exponent(iB[k])) > kNear;
+        if (__any_sync(~0u, far)) {
+            if (!EDGE) return true;
+            Group<NT> group{{}, {iA[0], iB[0]}};
+#pragma unroll
+            for (int e = 0; e < NT; ++e) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) group.y[e][i] = y[0][e][i];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) group.m[e][c] = st.m[e][c], group.l[e][c] = st.l[e][c];
+            }
+            apart = sum_apart<NT>(&group, pc);
+            if (apart) {
+#pragma unroll
+                for (int e = 0; e < NT; ++e)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) st.l[e][c] = group.l[e][c];
+                iA[0] = iB[0] = 0.0f;  // these weights are in the sums
+            }
+        }
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             float u0 = y[0][e][0], u1 = y[0][e][1];
@@ -578,18 +693,14 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
                 u0 = fmaxf(u0, fmaxf(y[k][e][0], y[k][e][2]));
                 u1 = fmaxf(u1, fmaxf(y[k][e][1], y[k][e][3]));
             }
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) {
-                u0 = fmaxf(u0, __shfl_xor_sync(~0u, u0, d));
-                u1 = fmaxf(u1, __shfl_xor_sync(~0u, u1, d));
-            }
-            const float n0 = u0 - st.m[e][0] > kMost ? u0 - kLift : st.m[e][0];
-            const float n1 = u1 - st.m[e][1] > kMost ? u1 - kLift : st.m[e][1];
+            const float n0 = moved(st.m[e][0], highest(u0, u0)), n1 = moved(st.m[e][1], highest(u1, u1));
             const float c0 = ex2(st.m[e][0] - n0), c1 = ex2(st.m[e][1] - n1);
             st.m[e][0] = n0;
             st.m[e][1] = n1;
-            st.l[e][0] *= c0;
-            st.l[e][1] *= c1;
+            if (!apart) {
+                st.l[e][0] *= c0;
+                st.l[e][1] *= c1;
+            }
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -608,8 +719,8 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
         for (int e = 0; e < NT; ++e) {
             const float d0 = ex2(y[k][e][0] - st.m[e][0]), d1 = ex2(y[k][e][1] - st.m[e][1]);
             const float d2 = ex2(y[k][e][2] - st.m[e][0]), d3 = ex2(y[k][e][3] - st.m[e][1]);
-            st.l[e][0] += fmaf(d0, EDGE && d0 == 0.0f ? 0.0f : iA[k], EDGE && d2 == 0.0f ? 0.0f : d2 * iB[k]);
-            st.l[e][1] += fmaf(d1, EDGE && d1 == 0.0f ? 0.0f : iA[k], EDGE && d3 == 0.0f ? 0.0f : d3 * iB[k]);
+            st.l[e][0] += weight_of<EDGE>(d0, d2, iA[k], iB[k]);
+            st.l[e][1] += weight_of<EDGE>(d1, d3, iA[k], iB[k]);
             const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
             b0[k][e] = movmatrix_trans(hA);
             b1[k][e] = movmatrix_trans(hB);
@@ -699,6 +810,7 @@ __device__ __forceinline__ void step(State<C> &st, uint8_t *const (&kp)[M], cons
             }
         }
     }
+    return EDGE && apart && pc->own;
 }
 
 template <typename T, int HD, int NT>
@@ -1040,6 +1152,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
                                   min(q.nq - 1, (rg * ROWS + ROWS - 1) >> log_group);
                 if (lane < ROWS) pc->pos[lane] = column<ROWS>(q, rg, lane, h, log_group).pos;
                 if (lane == 0) {
+                    pc->own = 0;
                     pc->n = n;
                     pc->end = g_end;
                     pc->ns = q.ns;
@@ -1061,19 +1174,22 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
                 if (ok) ok = mbar_wait(bars + stage, phase, &abort_flag, a.err);
                 if (ok) {
                     const uint32_t holes = pc->holes ? dead[warp * S + stage] : 0u;
-                    if (n == C::TILE && !holes && gi >= f0 && gi + n <= f1) {
+                    bool edges = n < C::TILE || holes || gi < f0 || gi + n > f1;
+                    if (!edges) {
                         uint8_t *tile[C::TILE];
 #pragma unroll
                         for (int k = 0; k < C::TILE; ++k) tile[k] = kp + k * C::GB;
-                        step<C, C::TILE, false>(st, tile, qs, bias, km, pc, 0, a.sink, a.win);
-                    } else {
+                        edges = step<C, C::TILE, false>(st, tile, qs, bias, km, pc, 0, a.sink, a.win);
+                    }
+                    if (edges) {
 #pragma unroll 1
                         for (int k = 0; k < n; ++k) {
                             if (holes >> k & 1) continue;
                             const int i = gi + k;
                             uint8_t *const one[1] = {kp + k * C::GB};
-                            step<C, 1, true>(st, one, qs, bias, km, pc,
-                                             (i < pc->ns ? i : i + pc->skip) * kGroupRows, a.sink, a.win);
+                            if (step<C, 1, true>(st, one, qs, bias, km, pc,
+                                                 (i < pc->ns ? i : i + pc->skip) * kGroupRows, a.sink, a.win))
+                                f1 = INT_MIN;
                         }
                     }
                 }
@@ -1086,6 +1202,10 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
 
             // ---- the piece is done
             st.sum_lanes();
+            const uint32_t own = pc->own;
+            auto base_of = [&](int e, int c) {  // r
+                return own >> (8 * e + 2 * t + c) & 1 ? pc->base[8 * e + 2 * t + c] : st.m[e][c];
+            };
             const int r = pc->r, unit = pc->unit, n = pc->n, first = pc->gi, end = pc->end;
             const int todo = pc->todo - (end - first);
             if (first == 0 && end == n) {
@@ -1096,9 +1216,11 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const Col col = column<ROWS>(q, rg, 8 * e + 2 * t + c, h, log_group);
+                        const float base = base_of(e, c);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
-                            write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(e, b, c), st.m[e][c], st.l[e][c]);
+                            write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(e, b, c), st.m[e][c], st.l[e][c],
+                                         base);
                     }
             } else {
                 // the start of the run: to the workspace; its end: into the ring, whose copies
@@ -1115,13 +1237,15 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
                             if (start) {
                                 dst[i] = st.m[e][c];
                                 dst[ROWS + i] = st.l[e][c];
+                                dst[2 * ROWS + i] = base_of(e, c);
                             } else {
                                 pc->m[i] = st.m[e][c];
                                 pc->l[i] = st.l[e][c];
+                                pc->base[i] = base_of(e, c);
                             }
                         }
                 }
-                float4 *quads = start ? reinterpret_cast<float4 *>(dst + 2 * ROWS)
+                float4 *quads = start ? reinterpret_cast<float4 *>(dst + C::HEAD)
                                       : reinterpret_cast<float4 *>(ring);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
@@ -1188,31 +1312,37 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         ws.tasks[blockIdx.x * kMostWarps + warp] = Task{h, rg, q};
     }
     // Factors of the pieces, one lane for each column and every (32 / ROWS)-th piece, into the
-    // memory of q: factor[piece][column], the tail's after the others, and then M and L.
+    // memory of q: factor[piece][column], the tail's after the others, and then M, L and R.
     float *factor = reinterpret_cast<float *>(qs);
-    static_assert((C::WARPS + 3) * ROWS * 4 <= C::QB, "the factors fit the memory of q");
+    static_assert((C::WARPS + 4) * ROWS * 4 <= C::QB, "the factors fit the memory of q");
     const int n_pieces = w1 - w0 + (tail_here ? 1 : 0);
     {
         constexpr int STEP = 32 / ROWS;
         const int n = lane % ROWS;
         auto m_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].m[n] : tail[n]; };
-        float M = kLowest, L = 0.0f;
-        for (int k = lane / ROWS; k < n_pieces; k += STEP) M = fmaxf(M, m_of(k));
+        auto l_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].l[n] : tail[ROWS + n]; };
+        auto r_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].base[n] : tail[2 * ROWS + n]; };
+        float M = kLowest, L = 0.0f, R = kLowest;
+        for (int k = lane / ROWS; k < n_pieces; k += STEP) M = fmaxf(M, m_of(k)), R = fmaxf(R, r_of(k));
 #pragma unroll
-        for (int d = ROWS; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+        for (int d = ROWS; d < 32; d <<= 1) {
+            M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
+            R = fmaxf(R, __shfl_xor_sync(~0u, R, d));
+        }
         for (int k = lane / ROWS; k < n_pieces; k += STEP) {
-            const float f = ex2(m_of(k) - M);
-            factor[k * ROWS + n] = f;
-            L = fmaf(k < w1 - w0 ? pieces[w0 + k].l[n] : tail[ROWS + n], f, L);
+            factor[k * ROWS + n] = ex2(m_of(k) - M);
+            L = fmaf(l_of(k), ex2(r_of(k) - R), L);
         }
 #pragma unroll
         for (int d = ROWS; d < 32; d <<= 1) L += __shfl_xor_sync(~0u, L, d);
         if (lane < ROWS) {
             factor[(C::WARPS + 1) * ROWS + n] = M;
             factor[(C::WARPS + 2) * ROWS + n] = L;
+            factor[(C::WARPS + 3) * ROWS + n] = R;
             if (!direct && warp == w0) {
                 dst[n] = M;
                 dst[ROWS + n] = L;
+                dst[2 * ROWS + n] = R;
             }
         }
         __syncwarp();
@@ -1221,7 +1351,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         const int n = 8 * (i / (2 * NB)) + 2 * t + (i & 1), b = (i >> 1) % NB, at = i * 32 + lane;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (tail_here)
-            x = scaled(*(reinterpret_cast<const float4 *>(tail + 2 * ROWS) + at), factor[(w1 - w0) * ROWS + n]);
+            x = scaled(*(reinterpret_cast<const float4 *>(tail + C::HEAD) + at), factor[(w1 - w0) * ROWS + n]);
 #pragma unroll 4
         for (int w = w0; w < w1; ++w) {
             const float4 y = *(reinterpret_cast<const float4 *>(smem + w * C::RING) + at);
@@ -1233,9 +1363,10 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         }
         if (direct)
             write_row<T>(a, column<ROWS>(q, rg, n, h, log_group), HD, 32 * b + 4 * g, x,
-                         factor[(C::WARPS + 1) * ROWS + n], factor[(C::WARPS + 2) * ROWS + n]);
+                         factor[(C::WARPS + 1) * ROWS + n], factor[(C::WARPS + 2) * ROWS + n],
+                         factor[(C::WARPS + 3) * ROWS + n]);
         else
-            *(reinterpret_cast<float4 *>(dst + 2 * ROWS) + at) = x;
+            *(reinterpret_cast<float4 *>(dst + C::HEAD) + at) = x;
     }
 }
 
@@ -1259,7 +1390,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                       kMostWarps < 32 && kMostWarps % 4 == 0,
                   "a thread reads a block's words, whose fields hold these");
     __shared__ float4 part_o[kJoinWarps][32];
-    __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4];
+    __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4], part_r[kJoinWarps][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1321,30 +1452,31 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                                           : tail * 2 + 1;
             return ws.partial + static_cast<size_t>(slot) * C::PARTIAL;
         };
-        float M = kLowest, L = 0.0f;
+        float M = kLowest, L = 0.0f, R = kLowest;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int eb = e0; in && eb < e1; eb += BATCH) {
-            float m[BATCH], l[BATCH];
+            float m[BATCH], l[BATCH], r[BATCH];
             float4 y[BATCH];
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
                 const float *p = piece(min(eb + e, e1 - 1));
                 m[e] = p[n];
                 l[e] = p[C::ROWS + n];
-                y[e] = *reinterpret_cast<const float4 *>(p + 2 * C::ROWS + (i * 32 + lane) * 4);
+                r[e] = p[2 * C::ROWS + n];
+                y[e] = *reinterpret_cast<const float4 *>(p + C::HEAD + (i * 32 + lane) * 4);
             }
-            float top = M;
+            float top = M, top_r = R;
 #pragma unroll
-            for (int e = 0; e < BATCH; ++e) top = fmaxf(top, m[e]);
-            const float s = ex2(M - top);
+            for (int e = 0; e < BATCH; ++e) top = fmaxf(top, m[e]), top_r = fmaxf(top_r, r[e]);
+            x = scaled(x, ex2(M - top));
+            L *= ex2(R - top_r);
             M = top;
-            L *= s;
-            x = scaled(x, s);
+            R = top_r;
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
                 if (eb + e >= e1) continue;
                 const float f = ex2(m[e] - top);
-                L = fmaf(l[e], f, L);
+                L = fmaf(l[e], ex2(r[e] - top_r), L);
                 x.x = fmaf(y[e].x, f, x.x);
                 x.y = fmaf(y[e].y, f, x.y);
                 x.z = fmaf(y[e].z, f, x.z);
@@ -1357,22 +1489,25 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
             if (g == 0) {
                 part_m[warp][t] = M;
                 part_l[warp][t] = L;
+                part_r[warp][t] = R;
             }
             __syncthreads();
             if (slice == 0) {
                 for (int s = 1; s < slices; ++s) {
                     const float m = part_m[warp + s][t], top = fmaxf(M, m);
                     const float f0 = ex2(M - top), f1 = ex2(m - top);
+                    const float r = part_r[warp + s][t], top_r = fmaxf(R, r);
                     const float4 y = part_o[warp + s][lane];
                     M = top;
-                    L = fmaf(part_l[warp + s][t], f1, L * f0);
+                    L = fmaf(part_l[warp + s][t], ex2(r - top_r), L * ex2(R - top_r));
+                    R = top_r;
                     x = make_float4(fmaf(y.x, f1, x.x * f0), fmaf(y.y, f1, x.y * f0),
                                     fmaf(y.z, f1, x.z * f0), fmaf(y.w, f1, x.w * f0));
                 }
             }
         }
         if (in && slice == 0)
-            write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
+            write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L, R);
     }
 }
 
@@ -1425,7 +1560,7 @@ size_t paged_attn_ws_bytes(int hd) {
     const size_t warps = static_cast<size_t>(device_sm_count()) * kMostWarps;
     const size_t rows = hd < 256 ? 16 : 8;  // of a unit
     return ws_head(device_sm_count(), 4) + ws_head(device_sm_count(), sizeof(Task)) +
-           warps * 2 * rows * (2 + hd) * 4;
+           warps * 2 * rows * (3 + hd) * 4;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream) {

@@ -1057,3 +1057,28 @@ def test_serving_steps(oracle_mod):
                 assert np.abs(host(o) - want).max() <= 5e-3  # the prefill's own tolerance (fp16 operands)
                 assert m.get_device_error() == m.OK
             t += f
+
+
+# ------------------------------- sums and references whatever the values are
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 16), (128, 8), (256, 16)])
+def test_attn_sums_do_not_depend_on_the_size_of_v(hd, hq, dtype):
+    """V next to the smallest and the largest fp32 numbers: the log-sum-exp and the weights know nothing of it.
+    (1e-36: outputs are averages, still above 1.2e-38, where a half step would no longer be relative.)"""
+    for lens, v_size in (([8192], 1e-33), ([600, 40], 1e-34), ([300], 1e-36), ([700], 1e30), ([300, 7], 3e37)):
+        if dtype == "f16" and v_size > 1:
+            continue  # not binary16 numbers
+        check_attn(lens, [1] * len(lens), hq, 1, hd, 16, dtype, v_size=v_size, seed=41)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 16), (128, 4), (256, 8)])
+def test_attn_rows_of_v_of_all_sizes(hd, hq, dtype):
+    """Rows of 1e-36 before, behind and among ordinary ones."""
+    rng = np.random.default_rng(3)
+    L = 1024
+    small_first = np.where(np.arange(L) < 16, 1e-36, 1.0)
+    some = 10.0 ** rng.uniform(-30, 3, L)
+    for sizes in (small_first, small_first[::-1], np.where(np.arange(L) % 64 < 63, 1e-36, 1.0), some):
+        check_attn([L], [2], hq, 1, hd, 16, dtype, v_size=sizes[:, None, None], seed=43)
