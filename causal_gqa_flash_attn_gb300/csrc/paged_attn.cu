@@ -31,6 +31,8 @@
 //     largest. Columns that see other rows take the weights of such a group from
 //     the scores, and have a reference r of these for their sums where m is not near
 //     enough to serve (sum_apart).
+//   - A row of zeros (a null token) is stored with e = 0, which says nothing of its
+//     V: it does not move m, below which smaller rows would be lost.
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
 // the scaled weights. Their codes become (c - 8) * 2^-9 (one AND and one packed
 // multiply-add for two): the tensor core aligns a sum's terms by their
@@ -496,26 +498,38 @@ __device__ __forceinline__ float weight_of(float dA, float dB, float invA, float
     return fmaf(dA, EDGE && dA == 0.0f ? 0.0f : invA, EDGE && dB == 0.0f ? 0.0f : dB * invB);
 }
 
-// A group's weights for columns that see a row of V beyond kNear, into their sums: from the scores,
-// relative to a reference r that follows the scores alone. Where m comes out near that, the sum
-// goes back to m. What enters a column's sum, and how, depends on what that column sees and not on
+// Whether rows g (bit 0) and g + 8 (bit 1) of a V part have a block scale that is not 0: lane t
+// looks at two blocks of both.
+template <int HD>
+__device__ __forceinline__ uint32_t with_content(const uint8_t *vp) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint4 w = lds_v4(vp + scale_offset(HD) + ((t & (HD / 64 - 1)) * 4 + (g >> 1)) * 16);
+    auto not_zero = [&](uint32_t h) { return (h >> 16 * (g & 1) & 0x7fffu) != 0; };
+    uint32_t has = (not_zero(w.x) || not_zero(w.z) ? 1u : 0u) | (not_zero(w.y) || not_zero(w.w) ? 2u : 0u);
+    has |= __shfl_xor_sync(~0u, has, 1);
+    return has | __shfl_xor_sync(~0u, has, 2);
+}
+
+// A group's weights for columns that see a row of V beyond kNear, or of zeros, into their sums: from the
+// scores, relative to a reference r that follows the scores alone. Where m comes out near that, the sum
+// goes back to m. The scaled weights of rows of zeros become 0. What enters a column's sum, and how, depends on what that column sees and not on
 // its neighbours.
 // False, and nothing done, if no column sees such a row.
 template <int NT>
 struct Group {
-    float y[NT][4], inv[2];    // s + e and 2^-e of the lane's rows
+    float y[NT][4], inv[2];    // s + e (then -inf for rows of zeros) and 2^-e of the lane's rows
     float m[NT][2], l[NT][2];  // as in State, before the group; l: after it
 };
-template <int NT>
-__device__ __forceinline__ bool sum_apart(Group<NT> *group, volatile Piece *pc) {
+template <int HD, int NT>
+__device__ __forceinline__ bool sum_apart(Group<NT> *group, const uint8_t *kp, volatile Piece *pc) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t had = pc->own;
+    const uint32_t had = pc->own, full = with_content<HD>(kp + part_bytes(HD));
     uint32_t apart = had, own = 0;  // columns summed here, and columns whose r stays their own
     for (int e = 0; e < NT; ++e)
         for (int c = 0; c < 2; ++c) {
             bool far = false;
             for (int i = 0; i < 2; ++i)
-                far |= abs(exponent(group->inv[i])) > kNear && group->y[e][2 * i + c] != -INFINITY;
+                far |= (abs(exponent(group->inv[i])) > kNear || !(full >> i & 1)) && group->y[e][2 * i + c] != -INFINITY;
             if (__ballot_sync(~0u, far) >> t & 0x11111111u) apart |= 1u << (8 * e + 2 * t + c);
         }
     if (!__any_sync(~0u, apart != 0)) return false;
@@ -523,8 +537,10 @@ __device__ __forceinline__ bool sum_apart(Group<NT> *group, volatile Piece *pc) 
         for (int c = 0; c < 2; ++c) {
             const int col = 8 * e + 2 * t + c;
             const bool its = apart >> col & 1;
-            const float yA = group->y[e][c], yB = group->y[e][2 + c];
+            float &yA = group->y[e][c], &yB = group->y[e][2 + c];
             const float sA = yA - exponent(group->inv[0]), sB = yB - exponent(group->inv[1]);
+            if (!(full & 1)) yA = -INFINITY;
+            if (!(full & 2)) yB = -INFINITY;
             const float m = group->m[e][c], n = moved(m, highest(yA, yB)), v = highest(sA, sB);
             const float from = had >> col & 1 ? pc->base[col] : m, r = its ? moved(from, v) : n;
             float l = group->l[e][c] * ex2(from - r);
@@ -546,7 +562,7 @@ __device__ __forceinline__ bool sum_apart(Group<NT> *group, volatile Piece *pc) 
 
 // M groups of the run, at kp[0..M-1] in shared memory: scores, weights, O.
 // EDGE: not every row of the unit sees the (one) group whole; j0 is its first
-// key and pc says what is seen. Rows of V beyond kNear are looked at in edges
+// key and pc says what is seen. Rows of V beyond kNear or of zeros are looked at in edges
 // alone. True: the groups have to be taken as such, one by one, and nothing is done; or,
 // of an edge, those that follow in the piece, as a column's sum has its own reference.
 template <typename C, int M, bool EDGE>
@@ -663,9 +679,10 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
                                    fmaxf(y[k][e][1], y[k][e][3]) - st.m[e][1]));
     bool apart = false;
     if (__any_sync(~0u, least < kBias - kNear || (EDGE && pc->own) || top > kMost)) {
+        auto far_or_zeros = [](int e) { return e == 0 || abs(e) > kNear; };
         bool far = EDGE && pc->own;
 #pragma unroll
-        for (int k = 0; k < M; ++k) far |= abs(exponent(iA[k])) > kNear || abs(exponent(iB[k])) > kNear;
+        for (int k = 0; k < M; ++k) far |= far_or_zeros(exponent(iA[k])) || far_or_zeros(exponent(iB[k]));
         if (__any_sync(~0u, far)) {
             if (!EDGE) return true;
             Group<NT> group{{}, {iA[0], iB[0]}};
@@ -676,12 +693,16 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
 #pragma unroll
                 for (int c = 0; c < 2; ++c) group.m[e][c] = st.m[e][c], group.l[e][c] = st.l[e][c];
             }
-            apart = sum_apart<NT>(&group, pc);
+            apart = sum_apart<HD>(&group, kp[0], pc);
             if (apart) {
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) st.l[e][c] = group.l[e][c];
+#pragma unroll
+                for (int e = 0; e < NT; ++e)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) y[0][e][i] = group.y[e][i];
                 iA[0] = iB[0] = 0.0f;  // these weights are in the sums
             }
         }

@@ -1082,3 +1082,44 @@ def test_attn_rows_of_v_of_all_sizes(hd, hq, dtype):
     some = 10.0 ** rng.uniform(-30, 3, L)
     for sizes in (small_first, small_first[::-1], np.where(np.arange(L) % 64 < 63, 1e-36, 1.0), some):
         check_attn([L], [2], hq, 1, hd, 16, dtype, v_size=sizes[:, None, None], seed=43)
+
+
+def attend_filled(m, rng, k, v, hq, hkv, hd, page_rows, dtype, n_q, q=None):
+    """One request of rows k, v [L][hkv][hd] and n_q queries: (out [n_q][hq][hd], lse [hq][n_q], q as rounded)."""
+    L = len(k)
+    used = -(-L // page_rows)
+    pages = pool_of(m, used + 1, hkv, hd, page_rows)
+    table = rng.permutation(used + 1)[:used][None]
+    p = np.arange(L)
+    append(m, pages, torch.from_numpy(k.astype(np.float32)).cuda(), torch.from_numpy(v.astype(np.float32)).cuda(),
+           table[0, p // page_rows] * page_rows + p % page_rows, page_rows)
+    q, qx = on_gpu(rng.standard_normal((n_q, hq, hd)) if q is None else q, dtype)
+    lse = guarded((hq, n_q), torch.float32, fill=7.0)
+    out = call_attn(m, q, ints(table), pages, ints([L]), ints([0, n_q]), hkv, page_rows, lse=lse)
+    assert m.get_device_error() == m.OK
+    check_guards(("lse", lse))
+    return host(out), host(lse), qx
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 16), (128, 4), (256, 8)])
+def test_attn_rows_of_zeros_do_not_hide_the_others(hd, hq, dtype):
+    """A null token whose V is zero and whose score is far above all others: what the others give keeps its bits."""
+    m = fa()
+    rng = np.random.default_rng(hd)
+    for L, bits, size in ((8192, 20, 1e-2), (8192, 20, 1e-3), (2000, 11, 1e-5), (100, 3, 1e-20), (40, 6, 0.0)):
+        k = 0.02 * rng.standard_normal((L, 1, hd))
+        k[0] = bits * math.log(2) / math.sqrt(hd)             # q . k0 / sqrt(hd) is `bits` powers of two above the rest
+        v = size * (1 + 0.3 * rng.standard_normal((L, 1, hd)))
+        v[[0, L // 2, L - 1]] = 0
+        got, lse, qx = attend_filled(m, rng, k, v, hq, 1, hd, 32, dtype, 2, q=1 + 0.1 * rng.standard_normal((2, hq, hd)))
+        kx, vx = (ref.decode(*ref.encode(x.astype(np.float32))) for x in (k, v))
+        want, wl = ref.attend(qx, L, kx, vx, L - 2, 0, 0, 1 / math.sqrt(hd))
+        # The largest score has an error of at most 16 half steps at its size (the sums of 8 blocks, their products in
+        # the tensor core, the scale and the exponent): 16 * bits * 2^-24 of its weight. The 16-bit types' scores have
+        # their codes' offset in the sums besides, 9 * 2^-23 * 23 / 7 of the score; then their output's rounding.
+        tol = {"f32": bits * 2.0 ** -20 + 2.0 ** -17, "f16": bits * 2.0 ** -18 + 2.0 ** -10,
+               "bf16": bits * 2.0 ** -18 + 2.0 ** -8}[dtype]
+        floor = 2.0 ** -25 * math.sqrt(want.size) if dtype == "f16" else 0.0
+        assert np.linalg.norm(got - want) <= tol * np.linalg.norm(want) + floor, (L, bits, size)
+        assert np.all(np.abs(lse - wl) <= (bits + 1) * 2.0 ** -18 + np.abs(wl) * 2.0 ** -22)
