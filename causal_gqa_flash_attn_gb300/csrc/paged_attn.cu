@@ -32,7 +32,9 @@
 //     the scores, and have a reference r of these for their sums where m is not near
 //     enough to serve (sum_apart).
 //   - A row of zeros (a null token) is stored with e = 0, which says nothing of its
-//     V: it does not move m, below which smaller rows would be lost.
+//     V: it does not move m, below which smaller rows would be lost. Nor does a row
+//     whose blocks are infinite or 0 (an infinity makes e 127): 0 times its infinite
+//     scales is the NaN that these blocks stand for.
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
 // the scaled weights. Their codes become (c - 8) * 2^-9 (one AND and one packed
 // multiply-add for two): the tensor core aligns a sum's terms by their
@@ -320,9 +322,9 @@ __device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
     asm("{.reg .b32 n; neg.f16x2 n, %3; fma.rn.f16x2 %0, %1, %2, n;}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-// All bits of each half that is not zero (or a NaN).
-__device__ __forceinline__ uint32_t not_zero2(uint32_t h) {
-    return (h & 0x7fffu ? 0xffffu : 0u) | (h & 0x7fff0000u ? 0xffff0000u : 0u);
+// All bits of each half that is not -0, which stands for the weight of an unseen row.
+__device__ __forceinline__ uint32_t seen2(uint32_t h) {
+    return ((h & 0xffffu) != 0x8000u ? 0xffffu : 0u) | (h >> 16 != 0x8000u ? 0xffff0000u : 0u);
 }
 __device__ __forceinline__ float2 half2_f(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
@@ -498,26 +500,26 @@ __device__ __forceinline__ float weight_of(float dA, float dB, float invA, float
     return fmaf(dA, EDGE && dA == 0.0f ? 0.0f : invA, EDGE && dB == 0.0f ? 0.0f : dB * invB);
 }
 
-// Whether rows g (bit 0) and g + 8 (bit 1) of a V part have a block scale that is not 0: lane t
-// looks at two blocks of both.
+// Whether rows g (bit 0) and g + 8 (bit 1) of a V part have a block scale that is finite and not 0:
+// lane t looks at two blocks of both.
 template <int HD>
 __device__ __forceinline__ uint32_t with_content(const uint8_t *vp) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint4 w = lds_v4(vp + scale_offset(HD) + ((t & (HD / 64 - 1)) * 4 + (g >> 1)) * 16);
-    auto not_zero = [&](uint32_t h) { return (h >> 16 * (g & 1) & 0x7fffu) != 0; };
-    uint32_t has = (not_zero(w.x) || not_zero(w.z) ? 1u : 0u) | (not_zero(w.y) || not_zero(w.w) ? 2u : 0u);
+    auto fine = [&](uint32_t h) { return (h >> 16 * (g & 1) & 0x7fffu) - 1u < 0x7bffu; };
+    uint32_t has = (fine(w.x) || fine(w.z) ? 1u : 0u) | (fine(w.y) || fine(w.w) ? 2u : 0u);
     has |= __shfl_xor_sync(~0u, has, 1);
     return has | __shfl_xor_sync(~0u, has, 2);
 }
 
-// A group's weights for columns that see a row of V beyond kNear, or of zeros, into their sums: from the
-// scores, relative to a reference r that follows the scores alone. Where m comes out near that, the sum
-// goes back to m. The scaled weights of rows of zeros become 0. What enters a column's sum, and how, depends on what that column sees and not on
+// A group's weights for columns that see a row of V beyond kNear, or without content, into their sums: from
+// the scores, relative to a reference r that follows the scores alone. Where m comes out near that, the sum
+// goes back to m. The scaled weights of rows without content become 0. What enters a column's sum, and how, depends on what that column sees and not on
 // its neighbours.
 // False, and nothing done, if no column sees such a row.
 template <int NT>
 struct Group {
-    float y[NT][4], inv[2];    // s + e (then -inf for rows of zeros) and 2^-e of the lane's rows
+    float y[NT][4], inv[2];    // s + e (then -inf for rows without content) and 2^-e of the lane's rows
     float m[NT][2], l[NT][2];  // as in State, before the group; l: after it
 };
 template <int HD, int NT>
@@ -562,7 +564,7 @@ __device__ __forceinline__ bool sum_apart(Group<NT> *group, const uint8_t *kp, v
 
 // M groups of the run, at kp[0..M-1] in shared memory: scores, weights, O.
 // EDGE: not every row of the unit sees the (one) group whole; j0 is its first
-// key and pc says what is seen. Rows of V beyond kNear or of zeros are looked at in edges
+// key and pc says what is seen. Rows of V beyond kNear or without content are looked at in edges
 // alone. True: the groups have to be taken as such, one by one, and nothing is done; or,
 // of an edge, those that follow in the piece, as a column's sum has its own reference.
 template <typename C, int M, bool EDGE>
@@ -658,15 +660,17 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
             y[k][e][3] = fmaf(y[k][e][3] * fB, km[e][1], eB);
         }
     }
+    uint32_t unseen = 0;  // bit 4 e + i: y[0][e][i]
     if (EDGE) {
         const int jA = j0 + g, jB = jA + 8;
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             const int p0 = pc->pos[8 * e + 2 * t], p1 = pc->pos[8 * e + 2 * t + 1];
-            if (!key_visible(p0, jA, sink, win)) y[0][e][0] = -INFINITY;
-            if (!key_visible(p1, jA, sink, win)) y[0][e][1] = -INFINITY;
-            if (!key_visible(p0, jB, sink, win)) y[0][e][2] = -INFINITY;
-            if (!key_visible(p1, jB, sink, win)) y[0][e][3] = -INFINITY;
+            unseen |= ((key_visible(p0, jA, sink, win) ? 0u : 1u) | (key_visible(p1, jA, sink, win) ? 0u : 2u) |
+                       (key_visible(p0, jB, sink, win) ? 0u : 4u) | (key_visible(p1, jB, sink, win) ? 0u : 8u)) << 4 * e;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (unseen >> (4 * e + i) & 1) y[0][e][i] = -INFINITY;
         }
     }
     // ---- weights relative to the reference
@@ -738,8 +742,10 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
     for (int k = 0; k < M; ++k)
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
-            const float d0 = ex2(y[k][e][0] - st.m[e][0]), d1 = ex2(y[k][e][1] - st.m[e][1]);
-            const float d2 = ex2(y[k][e][2] - st.m[e][0]), d3 = ex2(y[k][e][3] - st.m[e][1]);
+            auto weight = [&](int i) {
+                return EDGE && unseen >> (4 * e + i) & 1 ? -0.0f : ex2(y[k][e][i] - st.m[e][i & 1]);
+            };
+            const float d0 = weight(0), d1 = weight(1), d2 = weight(2), d3 = weight(3);
             st.l[e][0] += weight_of<EDGE>(d0, d2, iA[k], iB[k]);
             st.l[e][1] += weight_of<EDGE>(d1, d3, iA[k], iB[k]);
             const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
@@ -783,7 +789,7 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
                     const uint32_t p0 = b0[k0 + k][e], p1 = b1[k0 + k][e];
                     // rows that a query does not see may hold anything, also where another of the
                     // unit sees them: what they give is 0 even if their scales are not finite
-                    const uint32_t n0 = EDGE ? not_zero2(p0) : ~0u, n1 = EDGE ? not_zero2(p1) : ~0u;
+                    const uint32_t n0 = EDGE ? seen2(p0) : ~0u, n1 = EDGE ? seen2(p1) : ~0u;
                     w0[e] = hmul2(p0, s01) & n0;
                     w1[e] = hmul2(p1, s23) & n1;
                     if (C::PSPLIT) {

@@ -1123,3 +1123,31 @@ def test_attn_rows_of_zeros_do_not_hide_the_others(hd, hq, dtype):
         floor = 2.0 ** -25 * math.sqrt(want.size) if dtype == "f16" else 0.0
         assert np.linalg.norm(got - want) <= tol * np.linalg.norm(want) + floor, (L, bits, size)
         assert np.all(np.abs(lse - wl) <= (bits + 1) * 2.0 ** -18 + np.abs(wl) * 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "f16", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 32), (128, 8), (256, 16)])
+def test_attn_an_infinity_in_v_reaches_its_block_alone(hd, hq, dtype):
+    """V with an infinity in one block of a row: that block is NaN for the queries that attend the row, also where its
+    weight is nothing; the other blocks (0 in such a row) and the log-sum-exp are what the definition gives."""
+    m = fa()
+    hkv, L, n_q = 2, 300, 3
+    for row, low in ((150, False), (L - 1, False), (L - 2, True), (20, True)):
+        rng = np.random.default_rng(hd + row)
+        k, v = rng.standard_normal((2, L, hkv, hd))
+        q = 1 + 0.5 * rng.standard_normal((n_q, hq, hd))
+        if low:
+            k[row] = -60                                      # a score of about -60 sqrt(hd): its weight is 0 in fp32
+        v[row, :, 40] = math.inf
+        got, lse, qx = attend_filled(m, rng, k, v, hq, hkv, hd, 16, dtype, n_q, q=q)
+        v[row] = 0
+        kx, vx = (ref.decode(*ref.encode(x.astype(np.float32))) for x in (k, v))
+        want, wl = ref.attend(qx, L, kx, vx, L - n_q, 0, 0, 1 / math.sqrt(hd))
+        tol, ltol = attn_bounds(qx, kx, vx, dtype, 1 / math.sqrt(hd))
+        tol = tol + ref.HALF_STEP[dtype] * (np.abs(want) + tol) + (2.0 ** -25 if dtype == "f16" else 0.0)
+        sees = np.arange(n_q) + L - n_q >= row
+        bad = np.zeros(got.shape, bool)
+        bad[sees, :, 32:64] = True
+        assert np.array_equal(np.isnan(got), bad), (row, low)
+        assert np.all(np.abs(got - want)[~bad] <= tol[~bad]), (row, low)
+        assert np.all(np.abs(lse - wl) <= ltol.T + np.abs(wl) * 2.0 ** -22), (row, low)
