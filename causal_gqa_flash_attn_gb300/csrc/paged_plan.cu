@@ -131,10 +131,17 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
         back0[R] = static_cast<int>(all[2]);
     }
     __syncthreads();
-    // the pages handed out: those of the requests whose whole need is left
+    // a request of `fresh` tokens that are not all below max_tokens (then none behind it that has some are)
+    auto cut = [&](int r, unsigned fresh) { return fresh > room - static_cast<unsigned>(tok0[r]); };
+    // one that gets its slots: its pages are left, and none of its tokens is cut off
+    auto fits = [&](int r, const Len3 &p) {
+        return !p.bad && (p.v[1] == 0 || need0[r + 1] <= count) && !cut(r, p.v[0]);
+    };
+    // the pages handed out: those of the requests that fit
     unsigned fits_to = 0;
     for (int r = threadIdx.x; r < R; r += kPlanThreads)
-        if (need0[r + 1] > need0[r] && need0[r + 1] <= count)
+        if (need0[r + 1] > need0[r] && need0[r + 1] <= count &&
+            !(all[0] > room && cut(r, static_cast<unsigned>(load(a.fresh + r)))))
             fits_to = max(fits_to, static_cast<unsigned>(need0[r + 1]));
     fits_to = __reduce_max_sync(~0u, fits_to);
     if (lane == 0 && fits_to) atomicMax(&taken_sh, fits_to);
@@ -156,9 +163,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
     for (int r = i0; r < R; r += step) {
         const int c = load(a.cached + r), f = load(a.fresh + r);
         const Len3 p = plan_len(a, c, f);
-        const bool fits = !p.bad && (p.v[1] == 0 || need0[r + 1] <= count);
-        a.seq_lens[r] = p.bad || f < 0 ? 0
-                        : fits ? c + static_cast<int>(p.v[0]) : c;
+        a.seq_lens[r] = p.bad || f < 0 ? 0 : fits(r, p) ? c + static_cast<int>(p.v[0]) : c;
         a.cu_fresh[r] = tok0[r];
     }
     const int mask = (1 << a.page_shift) - 1;
@@ -174,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads, 2) page_plan_kernel(PlanArgs a) 
             const Len3 p = plan_len(a, c, load(a.fresh + r));
             if (!p.bad) {
                 pos = c + (t - tok0[r]);
-                if (p.v[1] == 0 || need0[r + 1] <= count) {
+                if (fits(r, p)) {
                     const int k = pos >> a.page_shift;
                     const int used = (c + mask) >> a.page_shift;
                     const int page =

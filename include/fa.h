@@ -424,7 +424,8 @@ size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
  *   free_ring  [n_pages] int32 (device): the free pages, a ring; read from its
  *              head, written behind its tail.
  *   ring_state [2] int32 (device): {head, count}. ring_state_out [3]: {head,
- *              count} after the step and the number of pages that were missing.
+ *              count} after the step and the number of pages that were asked for
+ *              and not handed out.
  *   block_table [n_reqs][max_pages] int32 (device): pages of each request in
  *              order; the entries of new pages are written, all others stay as
  *              they are (those of a finished request are stale).
@@ -437,7 +438,9 @@ size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
  *
  * Pages are handed out in request order from the head. A request whose new
  * pages are not all left, counting those of every request before it, gets none:
- * its tokens' slots are -1 and its seq_lens entry stays at cached. Pages given
+ * its tokens' slots are -1 and its seq_lens entry stays at cached. So does one
+ * whose tokens are not all below max_tokens: no row counts that has no slot. (What
+ * fa_paged_attn gives for such a request's tokens is of no use.) Pages given
  * back in this step are handed out from the next one on. A page that two
  * requests hold would be given back by both: tables with shared pages (which
  * the other calls read like any other) need a caller that keeps them itself.
@@ -446,7 +449,8 @@ size_t fa_page_bytes(int n_kv_heads, int head_dim, int page_rows);
  * more than max_pages pages: the request gets no slots and length 0), a state
  * out of range (nothing is handed out or taken back), more returned pages than
  * the ring has room for, a table entry outside [0, n_pages) under a fresh token
- * (slot -1), or more than max_tokens tokens (cu_fresh is cut there).
+ * (slot -1), or more than max_tokens tokens (cu_fresh is cut there, and the
+ * requests it cuts get nothing, as above).
  * No output may overlap an input or another output; free_ring and block_table
  * are updated in place. n_reqs <= 16384 and max_tokens <= 2^30
  * (FA_ERR_UNSUPPORTED); max_pages * page_rows <= 2^30, n_pages * page_rows < 2^31. */

@@ -1151,3 +1151,44 @@ def test_attn_an_infinity_in_v_reaches_its_block_alone(hd, hq, dtype):
         assert np.array_equal(np.isnan(got), bad), (row, low)
         assert np.all(np.abs(got - want)[~bad] <= tol[~bad]), (row, low)
         assert np.all(np.abs(lse - wl) <= ltol.T + np.abs(wl) * 2.0 ** -22), (row, low)
+
+
+@pytest.mark.parametrize("tokens", range(0, 75))
+def test_plan_with_too_few_tokens_gives_the_others_all(tokens):
+    """max_tokens below the step's tokens: a request that it cuts gets no page, no slot and no length, those before it
+    all of theirs, and lengths, offsets and the ring say the same. A step after that goes on from there."""
+    m = fa()
+    rng = np.random.default_rng(1)
+    cached, fresh = np.array([0, 16, 3, 31, 7, 7, 0, 60]), np.array([20, 1, 0, 2, -1, 9, 33, 5])
+    used = -(-cached // 16)
+    order, table, at = rng.permutation(40), np.full((8, 6), -1), 0
+    for r in range(8):
+        table[r, :used[r]] = order[at:at + used[r]]
+        at += used[r]
+    ring = np.full(40, -7)
+    ring[(35 + np.arange(40 - at)) % 40] = order[at:]
+    step = (cached, fresh, ring, [35, 40 - at], table)
+    ends = np.cumsum(np.maximum(fresh, 0))
+    gone = (fresh > 0) & (ends > tokens)
+    _, got = run_plan(*step, 16, tokens)
+    assert m.get_device_error() == (m.ERR_DEVICE if gone.any() else m.OK)
+    want = ref.plan(cached, np.where(gone, 0, fresh), *step[2:], 16, max(tokens, ends[-1]))
+    for name in ("ring", "table", "lens"):
+        assert got[name] == [list(map(int, x)) if name == "table" else int(x) for x in want[name]], name
+    needs = -(-(cached + np.maximum(fresh, 0)) // 16) - used
+    assert got["state"] == [int(x) for x in want["state"][:2]] + [int(needs[gone].sum())]
+    assert got["cu"] == [0] + np.minimum(ends, tokens).tolist()
+    kept = int(np.maximum(fresh[~gone], 0).sum())
+    assert got["slots"] == ([int(x) for x in want["slots"][:kept]] + [-1] * tokens)[:tokens]
+    pos = np.concatenate([np.arange(c, c + max(f, 0)) for c, f in zip(cached, fresh)])
+    assert got["positions"] == np.r_[pos, np.zeros(tokens, int)][:tokens].astype(int).tolist()
+    # the rest in a step of its own: every page is some request's or free, once
+    step = (np.array(got["lens"]), np.where(gone, fresh, 0), got["ring"], got["state"][:2], np.array(got["table"]))
+    _, then = run_plan(*step, 16, 80)
+    want = ref.plan(*step, 16, 80)
+    for name in want:
+        assert then[name] == [list(map(int, x)) if name == "table" else int(x) for x in want[name]], name
+    assert m.get_device_error() == m.OK
+    held = [p for r, n in enumerate(then["lens"]) for p in then["table"][r][:-(-n // 16)]]
+    head, count = then["state"][:2]
+    assert sorted(held + [then["ring"][(head + i) % 40] for i in range(count)]) == list(range(40))
