@@ -152,6 +152,7 @@ struct RopeArgs {
     int n_axes;
     const void *table;  // [rotary_dim / 2] entries of 16 bytes
     bool adjacent, inverse;
+    unsigned *err;
     int n_copy = 0, tokens_per_block = 0, heads_per_block = 0;  // set by the launch
 };
 cudaError_t launch_rope(const RopeArgs &a, cudaStream_t stream);

@@ -197,6 +197,8 @@ fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dt
     a.table = table;
     a.adjacent = adjacent != 0;
     a.inverse = inverse != 0;
+    a.err = fa::device_error_word();
+    if (!a.err) return FA_ERR_CUDA;
     return from_cuda(fa::launch_rope(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 

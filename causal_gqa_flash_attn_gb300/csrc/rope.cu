@@ -70,8 +70,9 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
         const int tok = i / half, pair = i - tok * half;
         const uint4 f = load(static_cast<const uint4 *>(a.table) + pair);
-        const int axis = min(static_cast<int>(f.z), a.n_axes - 1);
-        const long long pos = load(a.positions + axis * a.pos_stride + tok0 + tok);
+        const bool known = f.z < static_cast<unsigned>(a.n_axes);  // else a pair without positions stays as it is
+        if (!known) flag_error(a.err, FA_ERRBIT_DEVICE);
+        const long long pos = known ? load(a.positions + f.z * a.pos_stride + tok0 + tok) : 0;
         const unsigned long long F = (static_cast<unsigned long long>(f.y) << 32) | f.x;
         const unsigned long long turn = static_cast<unsigned long long>(pos) * F;
         const int top = static_cast<int>((turn + 0x80000000ull) >> 32);

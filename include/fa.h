@@ -485,7 +485,9 @@ fa_status fa_rope_table(uint32_t *table, const double *inv_freq, int pairs, cons
  *              moves 16 bytes at a time.
  *   head_dim   2..8192, rotary_dim even and at most head_dim.
  *   positions  [n_axes][pos_stride] int32 (device), n_axes 1..8, any value.
- *   table      [rotary_dim / 2] entries of fa_rope_table (device, 16-byte aligned). */
+ *   table      [rotary_dim / 2] entries of fa_rope_table (device, 16-byte aligned). One
+ *              whose axis is not below n_axes flags FA_ERR_DEVICE, and its pair is
+ *              not rotated. */
 fa_status fa_rope(const void *q, void *q_out, const void *k, void *k_out, int dtype, int n_tokens,
                   int n_q_heads, int n_kv_heads, int head_dim, int rotary_dim, int64_t q_stride,
                   int64_t q_out_stride, int64_t k_stride, int64_t k_out_stride,

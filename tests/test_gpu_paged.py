@@ -1192,3 +1192,35 @@ def test_plan_with_too_few_tokens_gives_the_others_all(tokens):
     held = [p for r, n in enumerate(then["lens"]) for p in then["table"][r][:-(-n // 16)]]
     head, count = then["state"][:2]
     assert sorted(held + [then["ring"][(head + i) % 40] for i in range(count)]) == list(range(40))
+
+
+@pytest.mark.parametrize("dtype,adjacent", [("f32", False), ("bf16", True)])
+def test_rope_table_of_more_axes_than_positions(dtype, adjacent):
+    """A table for three axes with positions of two, and one whose entries name no axis at all: flagged, and the
+    pairs that have no positions are left as they are."""
+    m = fa()
+    rng = np.random.default_rng(4)
+    T, H, hd, half = 9, 3, 64, 32
+    freq = 1e4 ** (-np.arange(half) / half)
+    sections = [12, 10, 10]
+    axis = ref.axes_of(half, sections, False)
+    x, exact = on_gpu(rng.standard_normal((T, H, hd)), dtype)
+    pos = rng.integers(0, 100, (3, T))
+    table = m.rope_table(freq, sections)
+    want = torch.empty_like(x)
+    m.rope(x, None, want, None, ints(pos), table, adjacent=adjacent)
+    assert m.get_device_error() == m.OK
+    i = np.arange(half)
+    lo, hi = (2 * i, 2 * i + 1) if adjacent else (i, i + half)
+    for entries, value in ((axis == 2, 2), (i % 5 == 0, -1), (i == 7, 2 ** 31 - 1), (i >= 30, -2 ** 31)):
+        bad = table.clone()
+        bad[torch.from_numpy(entries).cuda(), 2] = value
+        n_axes = 2 if value == 2 else 3
+        out = guarded((T, H, hd), DT[dtype], fill=float("nan"))
+        m.rope(x, None, out, None, ints(pos[:n_axes]), bad, adjacent=adjacent)
+        assert m.get_device_error() == m.ERR_DEVICE
+        check_guards(("out", out))
+        still = np.r_[lo[entries], hi[entries]]
+        assert np.array_equal(host(out)[..., still], exact[..., still])
+        rest = np.setdiff1d(np.arange(hd), still)
+        assert np.array_equal(host(out)[..., rest], host(want)[..., rest])
