@@ -75,7 +75,7 @@ constexpr int kBias = 127;         // of fp32's exponents
 // The start and end of a unit (its rows of q as operands, its output) cost a
 // warp about as much as kUnitCost groups: 6000 against 2200 cycles.
 constexpr int kUnitCost = 3;
-// Work per warp below which fewer warps work; > kUnitCost. One request of 600 rows 11.7 us
+// Work per warp below which fewer warps work. One request of 600 rows 11.7 us
 // (12.3 with 6, 13.9 with 9), 32 of 64 rows 13.5 (15.3, 17.5), long ones alike.
 constexpr int kMinWork = 4;
 // Requests that each warp sums by itself, one a lane, without a step of the whole
@@ -126,7 +126,6 @@ struct Cfg {
     static constexpr int PARTIAL = HEAD + ROWS * HD;
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
     static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
-    static_assert(kMinWork > kUnitCost, "a part of the cut has a group, but for a block's last");
     static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
     static_assert(RING >= ROWS * HD * 4, "a warp's O fits its ring");
     static_assert(SMEM <= 224 * 1024, "shared memory");
@@ -186,7 +185,10 @@ __device__ __forceinline__ long long quotient(long long n, int d) {
 // The cut of the work. Its measure is a group, and kUnitCost ahead of those of
 // each unit: N in all, c for each of B blocks, cw of those for each of A warps
 // (the last ones may have fewer, or none). A warp's run is the groups whose
-// measure lies in its part.
+// measure lies in its part. A part may have none: a block's last, or one that lies
+// wholly ahead of a unit's first group (parts are kUnitCost long where a block has 5, 6
+// or 9). Between two groups of a unit there is no such part, so that the warps of a
+// block that hold a unit's pieces are neighbours, as the joins take for granted.
 struct Cut {
     long long N, c;
     int cw, B, A;

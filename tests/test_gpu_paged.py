@@ -1224,3 +1224,14 @@ def test_rope_table_of_more_axes_than_positions(dtype, adjacent):
         assert np.array_equal(host(out)[..., still], exact[..., still])
         rest = np.setdiff1d(np.arange(hd), still)
         assert np.array_equal(host(out)[..., rest], host(want)[..., rest])
+
+
+@pytest.mark.parametrize("c", (1, 3, 4, 5, 6, 7, 8, 9, 13))
+def test_attn_parts_of_a_few_groups(c):
+    """About c measures of the cut (a unit's groups, and 3 for its start) for each block: with 5, 6 and 9 a warp's
+    part is as long as a unit's start, and some hold no group at all."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for groups in (1, 2, 5, 40):
+        for more in (-1, 0, 1):
+            n = max(1, c * sms // (groups + 3) + more)
+            check_attn([16 * groups - 3] * n, [1] * n, 4, 1, 64, 16, "f32", seed=groups)
