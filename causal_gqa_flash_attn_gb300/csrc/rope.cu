@@ -70,9 +70,9 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
         const int tok = i / half, pair = i - tok * half;
         const uint4 f = load(static_cast<const uint4 *>(a.table) + pair);
-        const bool known = f.z < static_cast<unsigned>(a.n_axes);  // else a pair without positions stays as it is
-        if (!known) flag_error(a.err, FA_ERRBIT_DEVICE);
-        const long long pos = known ? load(a.positions + f.z * a.pos_stride + tok0 + tok) : 0;
+        const int axis = static_cast<int>(min(f.z, static_cast<unsigned>(a.n_axes) - 1u));
+        long long pos = load(a.positions + axis * a.pos_stride + tok0 + tok);
+        if (f.z >= static_cast<unsigned>(a.n_axes)) pos = 0;  // a pair without positions stays as it is
         const unsigned long long F = (static_cast<unsigned long long>(f.y) << 32) | f.x;
         const unsigned long long turn = static_cast<unsigned long long>(pos) * F;
         const int top = static_cast<int>((turn + 0x80000000ull) >> 32);
@@ -81,6 +81,11 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
         cs[i] = c;
         sn[i] = a.inverse ? -s : s;
     }
+    // (flagged by one block alone: in the loop above it took 7 registers, and 29.4 us instead of 28.7)
+    if (blockIdx.x + blockIdx.y == 0)
+        for (int i = threadIdx.x; i < half; i += kRopeThreads)
+            if (load(static_cast<const uint4 *>(a.table) + i).z >= static_cast<unsigned>(a.n_axes))
+                flag_error(a.err, FA_ERRBIT_DEVICE);
     __syncthreads();
     const int h0 = blockIdx.y * a.heads_per_block;
     const int heads = min(a.heads_per_block, a.n_q_heads + a.n_kv_heads - h0);
