@@ -33,8 +33,8 @@
 //     enough to serve (sum_apart).
 //   - A row of zeros (a null token) is stored with e = 0, which says nothing of its
 //     V: it does not move m, below which smaller rows would be lost. Nor does a row
-//     whose blocks are infinite or 0 (an infinity makes e 127): 0 times its infinite
-//     scales is the NaN that these blocks stand for.
+//     whose blocks are infinite or 0 (an infinity makes e 127): any weight times its
+//     infinite scales is the NaN that these blocks stand for.
 // fp32 queries are split into two binary16 terms, and for fp32 and fp16 so are
 // the scaled weights. Their codes become (c - 8) * 2^-9 (one AND and one packed
 // multiply-add for two): the tensor core aligns a sum's terms by their
@@ -121,9 +121,8 @@ struct Cfg {
     static constexpr int OFF_DEAD = OFF_BAR + WARPS * STAGES * 8;
     static constexpr int SMEM = OFF_DEAD + WARPS * STAGES * 4;
     static constexpr int THREADS = (WARPS + 1) * 32;
-    // a partial, in floats: m, l and r of the rows, then O as the lanes hold it
-    static constexpr int HEAD = 3 * ROWS;
-    static constexpr int PARTIAL = HEAD + ROWS * HD;
+    // a partial: m and l of the rows, then O as the lanes hold it
+    static constexpr int PARTIAL = 2 * ROWS + ROWS * HD;  // floats
     static_assert(GB % 16 == 0 && OFF_BAR % 16 == 0, "alignment");
     static_assert(WARPS * STAGES <= THREADS && WARPS <= 32, "one thread per barrier, one lane per warp");
     static_assert(WARPS <= kMostWarps, "the workspace has room for every warp's pieces");
@@ -324,9 +323,9 @@ __device__ __forceinline__ uint32_t hfms2(uint32_t a, uint32_t b, uint32_t c) {
     asm("{.reg .b32 n; neg.f16x2 n, %3; fma.rn.f16x2 %0, %1, %2, n;}" : "=r"(d) : "r"(a), "r"(b), "r"(c));
     return d;
 }
-// All bits of each half that is not -0, which stands for the weight of an unseen row.
-__device__ __forceinline__ uint32_t seen2(uint32_t h) {
-    return ((h & 0xffffu) != 0x8000u ? 0xffffu : 0u) | (h >> 16 != 0x8000u ? 0xffff0000u : 0u);
+// All bits of each half that is not zero (or a NaN).
+__device__ __forceinline__ uint32_t not_zero2(uint32_t h) {
+    return (h & 0x7fffu ? 0xffffu : 0u) | (h & 0x7fff0000u ? 0xffff0000u : 0u);
 }
 __device__ __forceinline__ float2 half2_f(uint32_t h) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
@@ -426,6 +425,29 @@ struct State {
                 l[e][1] += __shfl_xor_sync(~0u, l[e][1], d);
             }
     }
+    // Columns with an r of their own get one reference for O and l, halfway between m and r: with 2^+-140
+    // between them at most (V's largest and smallest numbers), both stay far from the ends of fp32.
+    __device__ __forceinline__ void join_references(uint32_t own, const volatile float *base) {
+        const int t = threadIdx.x & 3;
+#pragma unroll
+        for (int e = 0; e < NT; ++e)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (!(own >> (8 * e + 2 * t + c) & 1)) continue;
+                // (if all rows were without content, m is kLowest and O 0)
+                const float ahead = fmaxf(m[e][c] - base[8 * e + 2 * t + c], -160.0f), up = floorf(0.5f * ahead);
+                const float f = ex2(up);
+                l[e][c] *= ex2(up - ahead);
+                m[e][c] = base[8 * e + 2 * t + c] + ahead - up;
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        o[e][b][i][c] *= f;
+                        o[e][b][i][2 + c] *= f;
+                    }
+            }
+    }
     // where quad(e, b, c) lies in a partial or a ring, in float4s of the warp's lanes
     __device__ __forceinline__ static int quad_at(int e, int b, int c) { return (e * NB + b) * 2 + c; }
 };
@@ -434,23 +456,16 @@ __device__ __forceinline__ float4 scaled(float4 v, float s) {
     return make_float4(v.x * s, v.y * s, v.z * s, v.w * s);
 }
 
-__device__ __forceinline__ float power_of_two(int n) {  // -126 <= n <= 127
-    return __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
-}
-
-// Four dims of a finished row, x 2^(m - r) / l, and with the first ones its log-sum-exp.
+// Four dims of a finished row, and with the first ones its log-sum-exp.
 template <typename T>
 __device__ __forceinline__ void write_row(const PagedAttnArgs &a, const Col &col, int hd, int dim,
-                                          float4 x, float m, float l, float r) {
+                                          float4 x, float m, float l) {
     if (col.token < 0) return;
-    // in two steps, as V may be near either end of the exponents
-    const int n = static_cast<int>(fminf(fmaxf(m - r, -250.0f), 250.0f)), half = n / 2;
-    x = scaled(x, l > 0.0f ? 1.0f / l : l);  // nothing attended: 0 (a NaN stays one)
     store4<T>(static_cast<T *>(a.out) + col.token * a.out_stride +
                   static_cast<long long>(col.head) * hd + dim,
-              scaled(scaled(x, power_of_two(half)), power_of_two(n - half)));
+              scaled(x, l > 0.0f ? 1.0f / l : l));  // nothing attended: 0 (a NaN stays one)
     if (a.lse && dim == 0)
-        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (r + log2f(l)) * kLn2;
+        a.lse[static_cast<size_t>(col.head) * a.n_tokens + col.token] = (m + log2f(l)) * kLn2;
 }
 
 // Groups that are taken at once from group i of a unit on, which is read up to
@@ -478,7 +493,7 @@ struct Piece {
     long long fin_first, fin_last;  // that unit's groups in the cut's measure
     float m[16], l[16];         // and the piece's references and sums
     uint32_t own;               // columns whose r is not m (a bit for each)
-    float base[16];             // their r, and that of all columns of the piece that ends the run
+    float base[16];             // and their r
 };
 
 // The new reference where the largest value is u. Whole numbers: 2^(m - r) is then exact.
@@ -514,18 +529,20 @@ __device__ __forceinline__ uint32_t with_content(const uint8_t *vp) {
     return has | __shfl_xor_sync(~0u, has, 2);
 }
 
-// A group's weights for columns that see a row of V beyond kNear, or without content, into their sums: from
-// the scores, relative to a reference r that follows the scores alone. Where m comes out near that, the sum
-// goes back to m. The scaled weights of rows without content become 0. What enters a column's sum, and how, depends on what that column sees and not on
-// its neighbours.
-// False, and nothing done, if no column sees such a row.
+// A group's weights for columns that see a row of V beyond kNear, or without content, into their sums:
+// from the scores, relative to a reference r that follows the scores alone. Where m comes out near that,
+// the sum goes back to m. The scaled weights of rows without content become binary16's least, which
+// keeps the NaN of infinite blocks apart from unseen rows, whose weights are 0. What enters a column's
+// sum, and how, depends on what that column sees and not on its neighbours.
+// False, and nothing done, if no column sees such a row. A call, as it is rare: inside step() the 199
+// ragged requests in fp32 take 113 us instead of 111.
 template <int NT>
 struct Group {
-    float y[NT][4], inv[2];    // s + e (then -inf for rows without content) and 2^-e of the lane's rows
+    float y[NT][4], inv[2];    // s + e (rows without content: also for their weight) and 2^-e of the lane's rows
     float m[NT][2], l[NT][2];  // as in State, before the group; l: after it
 };
 template <int HD, int NT>
-__device__ __forceinline__ bool sum_apart(Group<NT> *group, const uint8_t *kp, volatile Piece *pc) {
+__device__ __noinline__ bool sum_apart(Group<NT> *group, const uint8_t *kp, volatile Piece *pc) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t had = pc->own, full = with_content<HD>(kp + part_bytes(HD));
     uint32_t apart = had, own = 0;  // columns summed here, and columns whose r stays their own
@@ -541,15 +558,20 @@ __device__ __forceinline__ bool sum_apart(Group<NT> *group, const uint8_t *kp, v
         for (int c = 0; c < 2; ++c) {
             const int col = 8 * e + 2 * t + c;
             const bool its = apart >> col & 1;
-            float &yA = group->y[e][c], &yB = group->y[e][2 + c];
+            const float yA = group->y[e][c], yB = group->y[e][2 + c];
             const float sA = yA - exponent(group->inv[0]), sB = yB - exponent(group->inv[1]);
-            if (!(full & 1)) yA = -INFINITY;
-            if (!(full & 2)) yB = -INFINITY;
-            const float m = group->m[e][c], n = moved(m, highest(yA, yB)), v = highest(sA, sB);
+            const float m = group->m[e][c], v = highest(sA, sB);
+            const float n = moved(m, highest(full & 1 ? yA : -INFINITY, full & 2 ? yB : -INFINITY));
             const float from = had >> col & 1 ? pc->base[col] : m, r = its ? moved(from, v) : n;
             float l = group->l[e][c] * ex2(from - r);
             l += its ? ex2(sA - r) + ex2(sB - r)
                      : weight_of<true>(ex2(yA - n), ex2(yB - n), group->inv[0], group->inv[1]);
+            for (int i = 0; i < 2; ++i) {
+                float &y = group->y[e][2 * i + c];
+                if (y == -INFINITY) continue;
+                if (!(full >> i & 1)) y = n - 24.0f;
+                if (exponent(group->inv[i]) > 126) y = fmaxf(y, n - 24.0f);  // content and an infinity
+            }
             if (fabsf(n - r) <= kNear)
                 l *= ex2(r - n);
             else
@@ -644,7 +666,7 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
         }
     }
     float iA[M], iB[M];  // 2^-e of V's rows
-    int least = 255;     // of their biased exponents
+    int least = 255, most = 0;  // of their biased exponents
 #pragma unroll
     for (int k = 0; k < M; ++k) {
         const uint8_t *kf = kp[k] + factor_offset(HD) + 2 * g, *vf = kf + part_bytes(HD);
@@ -654,6 +676,7 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
         iA[k] = __uint_as_float(static_cast<uint32_t>(254 - xA) << 23);
         iB[k] = __uint_as_float(static_cast<uint32_t>(254 - xB) << 23);
         least = min(least, min(xA, xB));
+        most = max(most, max(xA, xB));
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             y[k][e][0] = fmaf(y[k][e][0] * fA, km[e][0], eA);
@@ -662,17 +685,15 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
             y[k][e][3] = fmaf(y[k][e][3] * fB, km[e][1], eB);
         }
     }
-    uint32_t unseen = 0;  // bit 4 e + i: y[0][e][i]
     if (EDGE) {
         const int jA = j0 + g, jB = jA + 8;
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
             const int p0 = pc->pos[8 * e + 2 * t], p1 = pc->pos[8 * e + 2 * t + 1];
-            unseen |= ((key_visible(p0, jA, sink, win) ? 0u : 1u) | (key_visible(p1, jA, sink, win) ? 0u : 2u) |
-                       (key_visible(p0, jB, sink, win) ? 0u : 4u) | (key_visible(p1, jB, sink, win) ? 0u : 8u)) << 4 * e;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (unseen >> (4 * e + i) & 1) y[0][e][i] = -INFINITY;
+            if (!key_visible(p0, jA, sink, win)) y[0][e][0] = -INFINITY;
+            if (!key_visible(p1, jA, sink, win)) y[0][e][1] = -INFINITY;
+            if (!key_visible(p0, jB, sink, win)) y[0][e][2] = -INFINITY;
+            if (!key_visible(p1, jB, sink, win)) y[0][e][3] = -INFINITY;
         }
     }
     // ---- weights relative to the reference
@@ -684,9 +705,11 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
             top = fmaxf(top, fmaxf(fmaxf(y[k][e][0], y[k][e][2]) - st.m[e][0],
                                    fmaxf(y[k][e][1], y[k][e][3]) - st.m[e][1]));
     bool apart = false;
-    if (__any_sync(~0u, least < kBias - kNear || (EDGE && pc->own) || top > kMost)) {
+    // (an edge looks at every row with an infinity: its weight must not become 0)
+    const bool looks = EDGE && (most > 253 || pc->own);
+    if (__any_sync(~0u, least < kBias - kNear || looks || top > kMost)) {
         auto far_or_zeros = [](int e) { return e == 0 || abs(e) > kNear; };
-        bool far = EDGE && pc->own;
+        bool far = looks;
 #pragma unroll
         for (int k = 0; k < M; ++k) far |= far_or_zeros(exponent(iA[k])) || far_or_zeros(exponent(iB[k]));
         if (__any_sync(~0u, far)) {
@@ -744,10 +767,8 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
     for (int k = 0; k < M; ++k)
 #pragma unroll
         for (int e = 0; e < NT; ++e) {
-            auto weight = [&](int i) {
-                return EDGE && unseen >> (4 * e + i) & 1 ? -0.0f : ex2(y[k][e][i] - st.m[e][i & 1]);
-            };
-            const float d0 = weight(0), d1 = weight(1), d2 = weight(2), d3 = weight(3);
+            const float d0 = ex2(y[k][e][0] - st.m[e][0]), d1 = ex2(y[k][e][1] - st.m[e][1]);
+            const float d2 = ex2(y[k][e][2] - st.m[e][0]), d3 = ex2(y[k][e][3] - st.m[e][1]);
             st.l[e][0] += weight_of<EDGE>(d0, d2, iA[k], iB[k]);
             st.l[e][1] += weight_of<EDGE>(d1, d3, iA[k], iB[k]);
             const uint32_t hA = pack_half2(d0, d1), hB = pack_half2(d2, d3);
@@ -791,7 +812,7 @@ __device__ __forceinline__ bool step(State<C> &st, uint8_t *const (&kp)[M], cons
                     const uint32_t p0 = b0[k0 + k][e], p1 = b1[k0 + k][e];
                     // rows that a query does not see may hold anything, also where another of the
                     // unit sees them: what they give is 0 even if their scales are not finite
-                    const uint32_t n0 = EDGE ? seen2(p0) : ~0u, n1 = EDGE ? seen2(p1) : ~0u;
+                    const uint32_t n0 = EDGE ? not_zero2(p0) : ~0u, n1 = EDGE ? not_zero2(p1) : ~0u;
                     w0[e] = hmul2(p0, s01) & n0;
                     w1[e] = hmul2(p1, s23) & n1;
                     if (C::PSPLIT) {
@@ -1231,10 +1252,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
 
             // ---- the piece is done
             st.sum_lanes();
-            const uint32_t own = pc->own;
-            auto base_of = [&](int e, int c) {  // r
-                return own >> (8 * e + 2 * t + c) & 1 ? pc->base[8 * e + 2 * t + c] : st.m[e][c];
-            };
+            if (pc->own) st.join_references(pc->own, pc->base);
             const int r = pc->r, unit = pc->unit, n = pc->n, first = pc->gi, end = pc->end;
             const int todo = pc->todo - (end - first);
             if (first == 0 && end == n) {
@@ -1245,11 +1263,9 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const Col col = column<ROWS>(q, rg, 8 * e + 2 * t + c, h, log_group);
-                        const float base = base_of(e, c);
 #pragma unroll
                         for (int b = 0; b < NB; ++b)
-                            write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(e, b, c), st.m[e][c], st.l[e][c],
-                                         base);
+                            write_row<T>(a, col, HD, 32 * b + 4 * g, st.quad(e, b, c), st.m[e][c], st.l[e][c]);
                     }
             } else {
                 // the start of the run: to the workspace; its end: into the ring, whose copies
@@ -1266,15 +1282,13 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
                             if (start) {
                                 dst[i] = st.m[e][c];
                                 dst[ROWS + i] = st.l[e][c];
-                                dst[2 * ROWS + i] = base_of(e, c);
                             } else {
                                 pc->m[i] = st.m[e][c];
                                 pc->l[i] = st.l[e][c];
-                                pc->base[i] = base_of(e, c);
                             }
                         }
                 }
-                float4 *quads = start ? reinterpret_cast<float4 *>(dst + C::HEAD)
+                float4 *quads = start ? reinterpret_cast<float4 *>(dst + 2 * ROWS)
                                       : reinterpret_cast<float4 *>(ring);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
@@ -1341,37 +1355,31 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         ws.tasks[blockIdx.x * kMostWarps + warp] = Task{h, rg, q};
     }
     // Factors of the pieces, one lane for each column and every (32 / ROWS)-th piece, into the
-    // memory of q: factor[piece][column], the tail's after the others, and then M, L and R.
+    // memory of q: factor[piece][column], the tail's after the others, and then M and L.
     float *factor = reinterpret_cast<float *>(qs);
-    static_assert((C::WARPS + 4) * ROWS * 4 <= C::QB, "the factors fit the memory of q");
+    static_assert((C::WARPS + 3) * ROWS * 4 <= C::QB, "the factors fit the memory of q");
     const int n_pieces = w1 - w0 + (tail_here ? 1 : 0);
     {
         constexpr int STEP = 32 / ROWS;
         const int n = lane % ROWS;
         auto m_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].m[n] : tail[n]; };
-        auto l_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].l[n] : tail[ROWS + n]; };
-        auto r_of = [&](int k) { return k < w1 - w0 ? pieces[w0 + k].base[n] : tail[2 * ROWS + n]; };
-        float M = kLowest, L = 0.0f, R = kLowest;
-        for (int k = lane / ROWS; k < n_pieces; k += STEP) M = fmaxf(M, m_of(k)), R = fmaxf(R, r_of(k));
+        float M = kLowest, L = 0.0f;
+        for (int k = lane / ROWS; k < n_pieces; k += STEP) M = fmaxf(M, m_of(k));
 #pragma unroll
-        for (int d = ROWS; d < 32; d <<= 1) {
-            M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
-            R = fmaxf(R, __shfl_xor_sync(~0u, R, d));
-        }
+        for (int d = ROWS; d < 32; d <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, d));
         for (int k = lane / ROWS; k < n_pieces; k += STEP) {
-            factor[k * ROWS + n] = ex2(m_of(k) - M);
-            L = fmaf(l_of(k), ex2(r_of(k) - R), L);
+            const float f = ex2(m_of(k) - M);
+            factor[k * ROWS + n] = f;
+            L = fmaf(k < w1 - w0 ? pieces[w0 + k].l[n] : tail[ROWS + n], f, L);
         }
 #pragma unroll
         for (int d = ROWS; d < 32; d <<= 1) L += __shfl_xor_sync(~0u, L, d);
         if (lane < ROWS) {
             factor[(C::WARPS + 1) * ROWS + n] = M;
             factor[(C::WARPS + 2) * ROWS + n] = L;
-            factor[(C::WARPS + 3) * ROWS + n] = R;
             if (!direct && warp == w0) {
                 dst[n] = M;
                 dst[ROWS + n] = L;
-                dst[2 * ROWS + n] = R;
             }
         }
         __syncwarp();
@@ -1380,7 +1388,7 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         const int n = 8 * (i / (2 * NB)) + 2 * t + (i & 1), b = (i >> 1) % NB, at = i * 32 + lane;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (tail_here)
-            x = scaled(*(reinterpret_cast<const float4 *>(tail + C::HEAD) + at), factor[(w1 - w0) * ROWS + n]);
+            x = scaled(*(reinterpret_cast<const float4 *>(tail + 2 * ROWS) + at), factor[(w1 - w0) * ROWS + n]);
 #pragma unroll 4
         for (int w = w0; w < w1; ++w) {
             const float4 y = *(reinterpret_cast<const float4 *>(smem + w * C::RING) + at);
@@ -1392,10 +1400,9 @@ __global__ void __launch_bounds__((Cfg<T, HD, NT>::THREADS), 1) paged_attn_kerne
         }
         if (direct)
             write_row<T>(a, column<ROWS>(q, rg, n, h, log_group), HD, 32 * b + 4 * g, x,
-                         factor[(C::WARPS + 1) * ROWS + n], factor[(C::WARPS + 2) * ROWS + n],
-                         factor[(C::WARPS + 3) * ROWS + n]);
+                         factor[(C::WARPS + 1) * ROWS + n], factor[(C::WARPS + 2) * ROWS + n]);
         else
-            *(reinterpret_cast<float4 *>(dst + C::HEAD) + at) = x;
+            *(reinterpret_cast<float4 *>(dst + 2 * ROWS) + at) = x;
     }
 }
 
@@ -1419,7 +1426,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                       kMostWarps < 32 && kMostWarps % 4 == 0,
                   "a thread reads a block's words, whose fields hold these");
     __shared__ float4 part_o[kJoinWarps][32];
-    __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4], part_r[kJoinWarps][4];
+    __shared__ float part_m[kJoinWarps][4], part_l[kJoinWarps][4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     wait_for_stream();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -1481,31 +1488,30 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
                                           : tail * 2 + 1;
             return ws.partial + static_cast<size_t>(slot) * C::PARTIAL;
         };
-        float M = kLowest, L = 0.0f, R = kLowest;
+        float M = kLowest, L = 0.0f;
         float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         for (int eb = e0; in && eb < e1; eb += BATCH) {
-            float m[BATCH], l[BATCH], r[BATCH];
+            float m[BATCH], l[BATCH];
             float4 y[BATCH];
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
                 const float *p = piece(min(eb + e, e1 - 1));
                 m[e] = p[n];
                 l[e] = p[C::ROWS + n];
-                r[e] = p[2 * C::ROWS + n];
-                y[e] = *reinterpret_cast<const float4 *>(p + C::HEAD + (i * 32 + lane) * 4);
+                y[e] = *reinterpret_cast<const float4 *>(p + 2 * C::ROWS + (i * 32 + lane) * 4);
             }
-            float top = M, top_r = R;
+            float top = M;
 #pragma unroll
-            for (int e = 0; e < BATCH; ++e) top = fmaxf(top, m[e]), top_r = fmaxf(top_r, r[e]);
-            x = scaled(x, ex2(M - top));
-            L *= ex2(R - top_r);
+            for (int e = 0; e < BATCH; ++e) top = fmaxf(top, m[e]);
+            const float s = ex2(M - top);
             M = top;
-            R = top_r;
+            L *= s;
+            x = scaled(x, s);
 #pragma unroll
             for (int e = 0; e < BATCH; ++e) {
                 if (eb + e >= e1) continue;
                 const float f = ex2(m[e] - top);
-                L = fmaf(l[e], ex2(r[e] - top_r), L);
+                L = fmaf(l[e], f, L);
                 x.x = fmaf(y[e].x, f, x.x);
                 x.y = fmaf(y[e].y, f, x.y);
                 x.z = fmaf(y[e].z, f, x.z);
@@ -1518,25 +1524,22 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(PagedAttnArgs 
             if (g == 0) {
                 part_m[warp][t] = M;
                 part_l[warp][t] = L;
-                part_r[warp][t] = R;
             }
             __syncthreads();
             if (slice == 0) {
                 for (int s = 1; s < slices; ++s) {
                     const float m = part_m[warp + s][t], top = fmaxf(M, m);
                     const float f0 = ex2(M - top), f1 = ex2(m - top);
-                    const float r = part_r[warp + s][t], top_r = fmaxf(R, r);
                     const float4 y = part_o[warp + s][lane];
                     M = top;
-                    L = fmaf(part_l[warp + s][t], ex2(r - top_r), L * ex2(R - top_r));
-                    R = top_r;
+                    L = fmaf(part_l[warp + s][t], f1, L * f0);
                     x = make_float4(fmaf(y.x, f1, x.x * f0), fmaf(y.y, f1, x.y * f0),
                                     fmaf(y.z, f1, x.z * f0), fmaf(y.w, f1, x.w * f0));
                 }
             }
         }
         if (in && slice == 0)
-            write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L, R);
+            write_row<T>(a, column<C::ROWS>(k.q, k.rg, n, k.h, log_group_of(a)), HD, 32 * b + 4 * g, x, M, L);
     }
 }
 
@@ -1589,7 +1592,7 @@ size_t paged_attn_ws_bytes(int hd) {
     const size_t warps = static_cast<size_t>(device_sm_count()) * kMostWarps;
     const size_t rows = hd < 256 ? 16 : 8;  // of a unit
     return ws_head(device_sm_count(), 4) + ws_head(device_sm_count(), sizeof(Task)) +
-           warps * 2 * rows * (3 + hd) * 4;
+           warps * 2 * rows * (2 + hd) * 4;
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream) {
