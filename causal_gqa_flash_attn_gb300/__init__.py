@@ -468,10 +468,10 @@ def rope(q, k, q_out, k_out, positions, table, *, adjacent: bool = False, invers
         kp, ks = _heads(k, "k", dtype, shape, here)
         ko, kos = (kp, ks) if k_out is k else _heads(k_out, "k_out", dtype, shape, here)
     where = positions.shape
-    axes = 1 if len(where) == 1 else where[0]
-    if len(where) > 2 or where[-1] != T:
+    axes = where[0] if len(where) == 2 else 1
+    if len(where) not in (1, 2) or where[-1] != T:
         raise ValueError(f"positions must have shape (n_axes, {T}), got {tuple(where)}")
-    pairs = table.shape[0]
+    pairs = table.shape[0] if table.dim() else 0
     _check(lib().fa_rope(
         qp, qo, kp, ko, code, T, hq, hkv, hd, 2 * pairs, qs, qos, ks, kos,
         _arg(positions, "positions", _I32, None, here), T, axes,

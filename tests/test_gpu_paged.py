@@ -1235,3 +1235,13 @@ def test_attn_parts_of_a_few_groups(c):
         for more in (-1, 0, 1):
             n = max(1, c * sms // (groups + 3) + more)
             check_attn([16 * groups - 3] * n, [1] * n, 4, 1, 64, 16, "f32", seed=groups)
+
+
+def test_rope_refuses_positions_and_tables_without_dims():
+    m = fa()
+    table = m.rope_table([1.0] * 16)
+    x = torch.zeros(4, 2, 32, device="cuda")
+    pos = torch.zeros(4, dtype=torch.int32, device="cuda")
+    for p, t in ((pos[0], table), (pos[None, None], table), (pos, table[0, 0]), (pos, table[0])):
+        with pytest.raises(ValueError):
+            m.rope(x, None, x, None, p, t)
