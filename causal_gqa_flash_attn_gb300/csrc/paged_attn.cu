@@ -79,8 +79,8 @@ constexpr int kUnitCost = 3;
 // (12.3 with 6, 13.9 with 9), 32 of 64 rows 13.5 (15.3, 17.5), long ones alike.
 constexpr int kMinWork = 4;
 // Requests that each warp sums by itself, one a lane, without a step of the whole
-// block: 32 requests of 2048 rows 21.2 us instead of 22.0, one of 600 rows 12.6 instead
-// of 13.2. With several requests a lane nothing is left of that (64: 21.9 and 22.1, 256:
+// block: 32 requests of 2048 rows 21.1 us instead of 22.0, one of 600 rows 12.7 instead
+// of 13.4 (when measured). With several requests a lane nothing is left of that (64: 21.9 and 22.1, 256:
 // 42.5 and 41.3, 1000: 75 and 58).
 constexpr int kFewReqs = 32;
 constexpr int kMostBlocks = 256;   // blocks, whose warps' tasks the join lists

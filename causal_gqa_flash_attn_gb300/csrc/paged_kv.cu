@@ -177,7 +177,8 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(PagedAppen
 // 8 codes c of a word -> (c - 8) * s rounded to binary16, in order. The product
 // is exact in fp32 (4 bits times 11); in binary16 arithmetic it is the same,
 // rounded once, where s itself is a binary16 number. A code in bits 0-3 or 4-7
-// of a half word under the bits of 1024 is 1024 + c or 1024 + 16 c.
+// of a half word under the bits of 1024 is 1024 + c or 1024 + 16 c: a well-known way
+// of 4-bit products, whose constants (1032, 72 = 64 + 8) follow from binary16.
 __device__ __forceinline__ uint32_t lop_or(uint32_t w, uint32_t mask, uint32_t bits) {
     return (w & mask) | bits;
 }

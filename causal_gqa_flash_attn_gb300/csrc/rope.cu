@@ -6,9 +6,10 @@
 //   x' = x cos a - y sin a,   y' = x sin a + y cos a.
 // The angle is taken modulo a turn in exact integer arithmetic: the table
 // holds F_i = 2^64 f_i / (2 pi), and the top 32 bits of pos * F_i mod 2^64 are
-// the angle in 2^-32 turns, off by less than |pos| 2^-64 + 2^-32 turns however
-// far the position is, without the 64-bit floating-point units (a few per SM).
-// sincospif then sees an argument in [-1, 1).
+// the angle in 2^-32 turns, without the 64-bit floating-point units (a few per
+// SM). sincospif then sees an argument in [-1, 1). In turns the angle is off by
+// |pos| (2^-64 + 2^-53 f_i / (2 pi)) at most from the table's entry, which is formed
+// in double, by 2^-33 from the 32 bits and by 2^-26 from becoming an fp32 argument.
 //
 // The call is bound by HBM: every element is read and written once. A block
 // takes a few tokens, puts their sines and cosines into shared memory (one for
@@ -17,8 +18,8 @@
 // have few registers: with two or four heads in flight per thread (64 and 100
 // registers), 20011 tokens of 40 heads took 71 and 105 us against 66. Sines in
 // registers, a thread walking all heads of its pairs, took 88 us.
-// 8192 tokens x 18 heads x 256 in bf16, a quarter rotated: 28.7 us (0.78 of HBM;
-// the start and the sines take 3 us of it); 20011 x 40 x 128 in fp16: 66 us (0.92).
+// 8192 tokens x 18 heads x 256 in bf16, a quarter rotated: 28.6 us (0.78 of HBM;
+// the start and the sines take 3 us of it); 20011 x 40 x 128 in fp16: 67 us (0.90).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -81,7 +82,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
         cs[i] = c;
         sn[i] = a.inverse ? -s : s;
     }
-    // (flagged by one block alone: in the loop above it took 7 registers, and 29.4 us instead of 28.7)
+    // (flagged by one block alone: in the loop above it took 7 registers, and 29.4 us instead of 28.6)
     if (blockIdx.x + blockIdx.y == 0)
         for (int i = threadIdx.x; i < half; i += kRopeThreads)
             if (load(static_cast<const uint4 *>(a.table) + i).z >= static_cast<unsigned>(a.n_axes))

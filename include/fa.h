@@ -377,7 +377,9 @@ fa_status fa_decode_noalloc(const float *q, const void *k_planes, const void *v_
  * are rotated to the tokens' positions (fa_rope), the new rows are written by
  * slot (fa_paged_append), and attention reads the pages through the block
  * table (fa_paged_attn). For long chunks the pages become fp16 planes
- * (fa_paged_gather) that fa_prefill_chunk reads in place.
+ * (fa_paged_gather) that fa_prefill_chunk reads in place: from about 120 queries
+ * of a request on in bf16, 70 to 80 in fp32 (8192 rows), a gather and
+ * fa_prefill_chunk are faster than fa_paged_attn.
  *
  * Element types of activations: */
 enum { FA_T_F32 = 0, FA_T_F16 = 1, FA_T_BF16 = 2 };
@@ -394,8 +396,12 @@ enum { FA_T_F32 = 0, FA_T_F16 = 1, FA_T_BF16 = 2 };
  * and a value is (code - 8) * scale * factor, the product in fp32. The encoder
  * is that of FA_KV_Q4_0 (d = amax / -8, code = clamp(round_half_even(x / d) +
  * 8, 0, 15) with the fp32 reciprocal 1 / d), with the row's largest |d| brought
- * into [1, 2) by the factor: rows of any magnitude keep their precision. As
- * there, a NaN is stored as 0, and an infinity makes its block's values NaN.
+ * into [1, 2) by the factor: rows of any magnitude keep their precision (a row
+ * of zeros has the factor 1). As there, a NaN is stored as 0, and an infinity
+ * makes its block's values NaN; the factor of such a row is 2^127, beside which
+ * its other blocks, below about 1e31, are stored as 0. Pages that another program
+ * writes should keep a row's largest scale in [1, 2] too: fa_paged_attn takes
+ * scales times weights of up to 2^14 as binary16 numbers.
  *
  * Byte order inside a part (nb = head_dim / 32, row r = 0..15, block b, dims
  * counted from 0 inside a block; the lower dim has the lower 4 bits of a byte):
@@ -529,7 +535,8 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  * requests of every length: decode steps, a few rows to verify a draft, short
  * chunks.
  *   q          token t's heads start at element t * q_stride, [n_q_heads]
- *              [head_dim] values of dtype; 16-byte aligned rows.
+ *              [head_dim] values of dtype below 2^107 in magnitude; 16-byte
+ *              aligned rows.
  *   out        written, the same layout with out_stride; may not overlap an input.
  *   lse        [n_q_heads][n_tokens] fp32 (device) or NULL, written: the natural
  *              log-sum-exp of each row's scores (-inf where nothing is attended).
@@ -540,7 +547,9 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  *              included: with n queries, query i sits at position
  *              seq_lens[r] - n + i (below 0: it attends nothing).
  *   block_table [n_reqs][max_pages] int32 (device). Only entries of pages with an
- *              attended row are read: pages that left the window may be given back.
+ *              attended row are read, so that a caller that keeps its own free list
+ *              may take back pages that left the window (fa_page_plan returns those
+ *              of finished requests alone).
  *   sink, win  the attended set, as for fa_prefill.
  *   scale      of q . k, > 0; 0 means 1 / sqrt(head_dim).
  *   workspace  >= fa_paged_attn_workspace_bytes(head_dim), 16-byte aligned; scratch.
@@ -549,7 +558,11 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  * fp32. With FA_T_F32 queries and the softmax weights of V's products are pairs
  * of binary16 terms, and so are the weights with FA_T_F16 (both exact to about
  * 2^-21); with FA_T_BF16 a weight is rounded to binary16, and again after its
- * product with V's block scale.
+ * product with V's block scale. To each weight comes, as binary16 ends there, an
+ * error of up to 2^-31 of the largest product of a weight and its V row's largest
+ * block (rows of zeros and of infinities do not count for it): a block in which all
+ * rows are far smaller than some row is elsewhere in the head keeps fewer bits. The
+ * log-sum-exp does not depend on V.
  * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_reqs <= 65536,
  * n_tokens <= 2^26, n_tokens * n_q_heads <= 2^30.
  * FA_ERR_DEVICE is flagged for a request whose cu_q or seq_lens are out of range
