@@ -559,7 +559,7 @@ size_t fa_paged_attn_workspace_bytes(int head_dim);
  * of binary16 terms, and so are the weights with FA_T_F16 (both exact to about
  * 2^-21); with FA_T_BF16 a weight is rounded to binary16, and again after its
  * product with V's block scale. To each weight comes, as binary16 ends there, an
- * error of up to 2^-31 of the largest product of a weight and its V row's largest
+ * error of up to 2^-30 of the largest product of a weight and its V row's largest
  * block (rows of zeros and of infinities do not count for it): a block in which all
  * rows are far smaller than some row is elsewhere in the head keeps fewer bits. The
  * log-sum-exp does not depend on V.
