@@ -67,7 +67,7 @@
 namespace fa {
 namespace {
 
-constexpr float kLowest = -1e30f;  // reference of a row that has seen no key
+constexpr float kLowest = -3e38f;  // reference of a row that has seen no key: below any score
 constexpr float kLift = 6.0f;      // log2 of the largest weight right after a move
 constexpr float kMost = 14.0f;     // log2 weight that moves the reference
 constexpr int kNear = 30;          // |e| of V's rows whose scaled weights the sum of weights can use

@@ -1245,3 +1245,25 @@ def test_rope_refuses_positions_and_tables_without_dims():
     for p, t in ((pos[0], table), (pos[None, None], table), (pos, table[0, 0]), (pos, table[0])):
         with pytest.raises(ValueError):
             m.rope(x, None, x, None, p, t)
+
+
+@pytest.mark.parametrize("dtype", ("f32", "bf16"))
+@pytest.mark.parametrize("hd,hq", [(64, 16), (256, 4)])
+def test_attn_scores_far_below_zero(hd, hq, dtype):
+    """Scores of about -1e31, and of 1e31: rows are attended, and the log-sum-exp is of the scores' size."""
+    m = fa()
+    rng = np.random.default_rng(hd)
+    for L in (5, 700):
+        for sign in (-1.0, 1.0):
+            k = np.full((L, 1, hd), sign * 2.0 ** 50)
+            v = rng.standard_normal((L, 1, hd))
+            got, lse, qx = attend_filled(m, rng, k, v, hq, 1, hd, 16, dtype, 2, q=np.full((2, hq, hd), 2.0 ** 50))
+            kx, vx = (ref.decode(*ref.encode(x.astype(np.float32))) for x in (k, v))
+            _, wl = ref.attend(qx, L, kx, vx, L - 2, 0, 0, 1 / math.sqrt(hd))
+            # A score of this size has an error of up to half an fp32 step, 2^-24 of 2^103: a weight, 2 to the power of
+            # it, may be any, V's exponent next to the score included. What is left of the definition: outputs are
+            # averages of the seen rows, to the type's rounding (and fp32 sums' 2^-17), and lse has its score's rounding.
+            slack = {"f32": 2.0 ** -17, "bf16": 2.0 ** -7}[dtype] * np.abs(vx).max()
+            assert np.all(got <= vx.max(0) + slack) and np.all(got >= vx.min(0) - slack)
+            assert np.all(np.abs(got).max(-1) >= slack)
+            assert np.all(np.abs(lse - wl) <= 2.0 ** -19 * np.abs(wl))
