@@ -67,6 +67,9 @@ SIGNATURES = {
     "fa_paged_attn_workspace_bytes": (_SZ, [_I]),
     "fa_paged_attn": (_I, [_P, _P, _P, _I, _L, _L, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
                            _I, _I, _I, _F, _P, _SZ, _P]),
+    "fa_packed_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_packed_attn": (_I, [_P, _P, _P, _P, _P, _I, _L, _L, _L, _L, _P, _P, _I, _I, _I, _I, _I, _I,
+                            _I, _F, _F, _P, _P, _SZ, _P]),
     "fa_set_kernel_events": (_I, [_P, _P]),
     "fa_get_device_error": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -533,6 +536,47 @@ def paged_attn(q, out, cu_q, seq_lens, block_table, pages, *, n_kv_heads: int, p
         table, max_pages, pp, n_pages, page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale,
         _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
         _raw_stream(stream, here)), "fa_paged_attn")
+
+
+# -------------------------------------------------------- packed documents
+
+def packed_attn_workspace_bytes(n_docs: int, n_tokens: int, n_q_heads: int, n_kv_heads: int,
+                                head_dim: int) -> int:
+    return int(lib().fa_packed_attn_workspace_bytes(n_docs, n_tokens, n_q_heads, n_kv_heads,
+                                                    head_dim))
+
+
+def _packed_rule(cu_docs, prefix, slopes, hq: int, here: int):
+    """(documents, pointers of cu_docs, prefix and slopes) of a packed call."""
+    D = cu_docs.numel() - 1
+    if D < 0 or cu_docs.dim() != 1:
+        raise ValueError(f"cu_docs must have shape (n_docs + 1,), got {tuple(cu_docs.shape)}")
+    return (D, _arg(cu_docs, "cu_docs", _I32, None, here),
+            None if prefix is None else _arg(prefix, "prefix", _I32, (D,), here),
+            None if slopes is None else _arg(slopes, "slopes", _F32, (hq,), here))
+
+
+def packed_attn(q, k, v, out, cu_docs, *, prefix=None, sink: int = 0, win: int = 0,
+                scale: float = 0.0, cap: float = 0.0, slopes=None, lse=None, workspace,
+                stream=None):
+    """fa_packed_attn: q, out [T][Hq][hd] and k, v [T][Hkv][hd] float16 or bfloat16
+    (tokens may lie apart), cu_docs [docs + 1] int32, prefix [docs] int32 or None,
+    slopes [Hq] fp32 or None, lse [Hq][T] fp32 or None."""
+    here = _here(q, "q")
+    code, dtype, shape = _type(q, "q"), q.dtype, q.shape
+    T, hq, hd = shape
+    _type(k, "k")
+    hkv = k.shape[1]
+    qp, qs = _heads(q, "q", dtype, shape, here)
+    kp, ks = _heads(k, "k", dtype, (T, hkv, hd), here)
+    vp, vs = _heads(v, "v", dtype, (T, hkv, hd), here)
+    op, os_ = _heads(out, "out", dtype, shape, here)
+    D, cu, pre, sl = _packed_rule(cu_docs, prefix, slopes, hq, here)
+    _check(lib().fa_packed_attn(
+        qp, kp, vp, op, None if lse is None else _arg(lse, "lse", _F32, (hq, T), here), code, qs,
+        ks, vs, os_, cu, pre, D, T, hq, hkv, hd, sink, win, scale, cap, sl,
+        _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
+        _raw_stream(stream, here)), "fa_packed_attn")
 
 
 def set_kernel_events(start, stop):

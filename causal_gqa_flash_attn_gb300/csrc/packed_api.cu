@@ -1,0 +1,179 @@
+// packed_api.cu -- the C ABI of packed attention (include/fa.h): argument checks,
+// the workspace's parts and the tensor maps. Host code only.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "../../include/fa.h"
+#include "packed_common.cuh"
+
+namespace {
+
+bool aligned(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+fa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? FA_OK : FA_ERR_CUDA; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+int log2_of(int n) {
+    int s = 0;
+    while (1 << s < n) ++s;
+    return s;
+}
+
+fa_status check_sizes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim) {
+    if (n_docs < 0 || n_tokens < 0 || n_kv_heads < 1 || n_q_heads < 1 || n_q_heads % n_kv_heads ||
+        head_dim < 32 || head_dim % 32)
+        return FA_ERR_INVALID;
+    const int group = n_q_heads / n_kv_heads;
+    if ((head_dim != 64 && head_dim != 128 && head_dim != 256) || group > 16 || (group & (group - 1)) ||
+        n_docs > 65536 || n_tokens > 1 << 26 || static_cast<long long>(n_tokens) * n_q_heads > 1 << 30)
+        return FA_ERR_UNSUPPORTED;
+    return FA_OK;
+}
+
+// Where the parts of a workspace lie; `rows` is the rows of a row tile.
+struct Layout {
+    size_t row_tiles, key_tiles, doc_tiles, doc_most, stats, bytes;
+    int most_rows, most_keys;
+    size_t blocks;  // 128-row blocks of a kv head
+};
+Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int rows, bool grad) {
+    Layout w;
+    const int group = n_q_heads / n_kv_heads;
+    w.most_rows = static_cast<int>(static_cast<long long>(n_tokens) * group / rows) + n_docs;
+    w.most_keys = grad ? n_tokens / 128 + n_docs : 0;
+    w.blocks = static_cast<size_t>(n_tokens) * group / 128 + n_docs;
+    size_t at = sizeof(fa::PackedHeader);
+    auto take = [&](size_t n) {
+        const size_t from = at;
+        at += up256(n);
+        return from;
+    };
+    w.row_tiles = take(sizeof(fa::PackedTile) * w.most_rows);
+    w.key_tiles = take(sizeof(fa::PackedTile) * w.most_keys);
+    w.doc_tiles = take(sizeof(int) * 3 * (static_cast<size_t>(n_docs) + 1));
+    w.doc_most = take(grad ? sizeof(unsigned) * 2 * n_docs : 0);
+    w.stats = take(grad ? sizeof(float) * 2 * n_kv_heads * w.blocks * 128 : 0);
+    w.bytes = at;
+    return w;
+}
+
+bool good_heads(const void *p, int64_t stride, int heads, int head_dim, int n_tokens) {
+    const int64_t row = static_cast<int64_t>(heads) * head_dim;
+    return p && aligned(p, 16) && stride % 8 == 0 && stride >= row &&
+           stride <= (int64_t(1) << 38) / (n_tokens > 0 ? n_tokens : 1);  // a tensor map's strides: below 2^40 bytes
+}
+
+// What both directions check beside their tensors.
+fa_status check_rule(int dtype, const int32_t *cu, const int32_t *prefix, int sink, float scale, float cap,
+                     const float *slopes, const void *workspace) {
+    if (sink < 0 || !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap))
+        return FA_ERR_INVALID;
+    if (dtype == FA_T_F32) return FA_ERR_UNSUPPORTED;
+    if (dtype != FA_T_F16 && dtype != FA_T_BF16) return FA_ERR_INVALID;
+    if (!aligned(cu, 4) || !aligned(prefix, 4) || !aligned(slopes, 4) || !aligned(workspace, 16))
+        return FA_ERR_INVALID;
+    return FA_OK;
+}
+
+// q-like rows: tiles of `rows` rows, 64 dims wide, tokens of all heads of a group.
+bool map_rows(CUtensorMap *m, int dtype, const void *p, int64_t stride, int n_tokens, int n_kv, int group,
+              int hd, int rows) {
+    const uint64_t dims[4] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(group), static_cast<uint64_t>(n_kv),
+                              static_cast<uint64_t>(n_tokens)};
+    const uint64_t strides[3] = {2ull * hd, 2ull * hd * group, 2ull * stride};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(group), 1, static_cast<uint32_t>(rows / group)};
+    return fa::encode_tiled(m, dtype == FA_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            4, p, dims, strides, box);
+}
+// k-like rows: tiles of `rows` tokens of one kv head.
+bool map_keys(CUtensorMap *m, int dtype, const void *p, int64_t stride, int n_tokens, int n_kv, int hd, int rows) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(hd), static_cast<uint64_t>(n_kv), static_cast<uint64_t>(n_tokens)};
+    const uint64_t strides[2] = {2ull * hd, 2ull * stride};
+    const uint32_t box[3] = {64, 1, static_cast<uint32_t>(rows)};
+    return fa::encode_tiled(m, dtype == FA_T_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                            3, p, dims, strides, box);
+}
+
+int bounded(int n) { return std::min(std::max(n, 0), 1 << 30); }
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_packed_attn_workspace_bytes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim) {
+    if (check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim) != FA_OK) return 0;
+    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128 * fa::packed_fwd_tiles(head_dim), false).bytes;
+}
+
+fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out, float *lse, int dtype,
+                         int64_t q_stride, int64_t k_stride, int64_t v_stride, int64_t out_stride,
+                         const int32_t *cu_docs, const int32_t *prefix, int n_docs, int n_tokens, int n_q_heads,
+                         int n_kv_heads, int head_dim, int sink, int win, float scale, float cap,
+                         const float *slopes, void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+    fa_status st = check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim);
+    if (st != FA_OK) return st;
+    st = check_rule(dtype, cu_docs, prefix, sink, scale, cap, slopes, workspace);
+    if (st != FA_OK) return st;
+    if (n_docs == 0 || n_tokens == 0) return FA_OK;
+    if (!cu_docs || !workspace || !aligned(lse, 4) || !good_heads(q, q_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_heads(k, k_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_heads(v, v_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_heads(out, out_stride, n_q_heads, head_dim, n_tokens))
+        return FA_ERR_INVALID;
+    if (out == q || out == k || out == v) return FA_ERR_INVALID;
+    const int group = n_q_heads / n_kv_heads, rows = 128 * fa::packed_fwd_tiles(head_dim);
+    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, rows, false);
+    if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+    unsigned *err = fa::device_error_word();
+    if (!err) return FA_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    fa::PackedPlanArgs p;
+    p.cu = cu_docs;
+    p.prefix = prefix;
+    p.n_docs = n_docs;
+    p.n_tokens = n_tokens;
+    p.sink = bounded(sink);
+    p.win = bounded(win);
+    p.row_tokens = rows / group;
+    p.block_tokens_log = 7 - log2_of(group);
+    p.key_tile = 128;
+    p.most_rows = w.most_rows;
+    p.most_keys = 0;
+    p.header = reinterpret_cast<fa::PackedHeader *>(ws);
+    p.rows = reinterpret_cast<fa::PackedTile *>(ws + w.row_tiles);
+    p.keys = nullptr;
+    p.doc_tiles = reinterpret_cast<int *>(ws + w.doc_tiles);
+    p.doc_most = nullptr;
+    p.err = err;
+
+    fa::PackedFwdArgs a;
+    if (!map_rows(&a.q, dtype, q, q_stride, n_tokens, n_kv_heads, group, head_dim, 128) ||
+        !map_keys(&a.k, dtype, k, k_stride, n_tokens, n_kv_heads, head_dim, 128) ||
+        !map_keys(&a.v, dtype, v, v_stride, n_tokens, n_kv_heads, head_dim, 128))
+        return FA_ERR_CUDA;
+    a.header = p.header;
+    a.rows = p.rows;
+    a.counter = &p.header->counters[0];
+    a.out = out;
+    a.out_stride = out_stride;
+    a.lse = lse;
+    a.slopes = slopes;
+    a.n_tokens = n_tokens;
+    a.n_kv = n_kv_heads;
+    a.log_group = log2_of(group);
+    a.sink = p.sink;
+    a.win = p.win;
+    a.score = fa::score_rule(scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim)), cap);
+    a.err = err;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = fa::launch_packed_plan(p, s);
+    if (e != cudaSuccess) return from_cuda(e);
+    const int blocks = static_cast<int>(
+        std::min<long long>(fa::device_sm_count(), static_cast<long long>(w.most_rows) * n_kv_heads));
+    return from_cuda(dtype == FA_T_BF16 ? fa::launch_packed_fwd_bf16(a, head_dim, cap > 0.0f, blocks, s)
+                                        : fa::launch_packed_fwd_f16(a, head_dim, cap > 0.0f, blocks, s));
+}
+
+}  // extern "C"

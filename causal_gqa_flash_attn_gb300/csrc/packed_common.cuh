@@ -1,0 +1,192 @@
+// packed_common.cuh -- what the kernels of packed attention and of its gradient
+// share: the batch, the tiles of its documents, the attended set and the scores
+// (include/fa.h, fa_packed_attn).
+//
+// Rows. The q heads of one kv head are rows of one matrix: row i * G + h is
+// token i of the document and head h of the group of G, so that a tile of 128
+// rows holds 128 / G tokens of all G heads. A unit's rows then share their keys
+// whatever the group is, the gradients of K and V sum over the group inside the
+// products, and a short document fills its tiles G times better than head by head.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <type_traits>
+
+#include "fa_device.cuh"
+#include "fa_internal.h"
+#include "paged_launch.cuh"
+
+namespace fa {
+
+constexpr float kPackedLog2e = 1.4426950408889634f;
+constexpr float kPackedLn2 = 0.69314718055994531f;
+
+// A tile of a document, of its rows or of its keys.
+struct PackedTile {
+    int tok0, len;   // the document's first token in the batch, and its tokens
+    int p0;          // position of the tile's first token
+    int prefix;      // keys that every query of the document sees
+    int rb;          // 128-row blocks of the documents before this one
+    int doc;
+    int head;        // kv head (set by the kernel that takes the unit)
+    int pad;
+};
+static_assert(sizeof(PackedTile) == 32, "two 16-byte loads");
+
+// Key tiles of BK that the queries at positions p0 .. p1 see any key of, in
+// ascending order: those of the prefix and the sinks, then the window's (or all).
+struct KeyTiles {
+    int ns, lo, count;
+    __device__ __forceinline__ int at(int i) const { return i < ns ? i : lo + (i - ns); }
+};
+template <int BK>
+__device__ __forceinline__ KeyTiles key_tiles(int p0, int p1, int prefix, int sink, int win) {
+    KeyTiles t;
+    const int head = max(prefix, win > 0 ? min(sink, p1 + 1) : 0);
+    t.ns = (head + BK - 1) / BK;
+    t.lo = max(win > 0 ? max(0, p0 - win + 1) / BK : 0, t.ns);
+    t.count = t.ns + max(0, p1 / BK - t.lo + 1);
+    return t;
+}
+// Every query in [p0, p1] sees every key in [j0, j1] (j0 > j1 or queries past the end: never mind).
+__device__ __forceinline__ bool sees_all(int p0, int p1, int j0, int j1, int prefix, int sink, int win) {
+    if (j1 < prefix) return true;
+    return j1 <= p0 && (win <= 0 || j1 < sink || j0 > p1 - win);
+}
+
+// Queries that see any key of [j0, j1], one run of positions: [first, last].
+__device__ __forceinline__ void query_range(int j0, int j1, int len, int prefix, int sink, int win,
+                                            int *first, int *last) {
+    *first = j0 < prefix ? 0 : j0;
+    *last = win <= 0 || j0 < max(prefix, sink) ? len - 1 : min(len - 1, j1 + win - 1);
+}
+
+// The score in the exp2 domain from the product s of q and k.
+//   no cap: s * a          (a = scale * log2 e)
+//   cap:    b * tanh(..)   = b - 2 b / (1 + 2^(s * a)),  a = 2 scale log2 e / cap, b = cap log2 e
+// The quotient's error, 2^-22 or so of b, is that of fp32 scores of the cap's size.
+__device__ __forceinline__ float rcp_approx(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+struct ScoreRule {
+    float a, b;
+};
+inline ScoreRule score_rule(float scale, float cap) {
+    ScoreRule r;
+    r.a = cap > 0.0f ? 2.0f * scale * kPackedLog2e / cap : scale * kPackedLog2e;
+    r.b = cap > 0.0f ? cap * kPackedLog2e : 0.0f;
+    return r;
+}
+__device__ __forceinline__ float capped(float s, const ScoreRule &c) {
+    const float r = rcp_approx(1.0f + ex2(s * c.a));
+    return fmaf(-2.0f * c.b, r, c.b);
+}
+// And the derivative of cap * tanh(x / cap): 1 - tanh^2 = 4 r (1 - r).
+__device__ __forceinline__ float capped(float s, const ScoreRule &c, float *slope) {
+    const float r = rcp_approx(1.0f + ex2(s * c.a));
+    *slope = 4.0f * fmaf(-r, r, r);
+    return fmaf(-2.0f * c.b, r, c.b);
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return pack_half2(lo, hi);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    if (BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// Instruction descriptor with both operands fp16 or both bf16.
+template <bool BF16>
+__host__ __device__ constexpr uint32_t idesc_16(int M, int N, int a_mn_major, int b_mn_major) {
+    return idesc_f16(M, N, a_mn_major, b_mn_major) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// Wait ignoring the abort flag (still bounded): lets copies and MMAs in flight
+// finish before a block that gave up releases its TMEM and exits.
+__device__ __forceinline__ void wait_out(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!mbar_try_wait(bar, parity))
+        if (clock64() - t0 > kSpinCycles) return;
+}
+
+// A barrier of copies whose arrivals are counted, so that a block that gives up
+// knows which copies it has to wait out.
+struct Arms {
+    int n = 0;
+    __device__ __forceinline__ void drain(uint64_t *bar) const {
+        if (n) wait_out(bar, (n - 1) & 1);
+    }
+};
+
+// Rows [from, rows) of a tile of `chunks` 128-byte-wide pieces become zeros (the
+// swizzle keeps a row's 128 bytes together). All lanes of the warp.
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int chunks, int chunk_bytes, int from, int rows) {
+    const int lane = threadIdx.x & 31;
+    for (int c = 0; c < chunks; ++c)
+        for (int at = from * 128 + lane * 16; at < rows * 128; at += 512)
+            *reinterpret_cast<uint4 *>(tile + c * chunk_bytes + at) = make_uint4(0, 0, 0, 0);
+}
+
+// Units of a persistent kernel: block b starts with unit b, later ones come from
+// a counter; the producer warp hands them on through a ring in shared memory.
+constexpr int kPackedRing = 4;
+struct UnitRing {
+    uint64_t full[kPackedRing], empty[kPackedRing];
+    PackedTile unit[kPackedRing];  // head < 0: no more
+};
+
+// ---- packed_plan.cu
+// What the plan leaves in the workspace: counts, the work counters (zeroed) and
+// the tiles, heaviest first.
+struct PackedHeader {
+    int row_tiles, key_tiles;  // in the lists
+    unsigned counters[4];
+    int pad[58];
+};
+static_assert(sizeof(PackedHeader) == 256, "header");
+
+struct PackedPlanArgs {
+    const int32_t *cu, *prefix;
+    int n_docs, n_tokens, sink, win;
+    int row_tokens;       // tokens of a row tile
+    int block_tokens_log; // log2 of the tokens of 128 rows
+    int key_tile;         // keys of a row tile's key tiles, for the weights
+    int most_rows, most_keys;  // room in the lists (most_keys 0: no key tiles)
+    PackedHeader *header;
+    PackedTile *rows, *keys;
+    int *doc_tiles;       // [3][n_docs + 1]: row tiles, key tiles and 128-row blocks before each document
+    unsigned *doc_most;   // [2][n_docs], zeroed, or null
+    unsigned *err;
+};
+cudaError_t launch_packed_plan(const PackedPlanArgs &a, cudaStream_t stream);
+
+// ---- packed_fwd.cuh
+struct PackedFwdArgs {
+    CUtensorMap q, k, v;
+    const PackedHeader *header;
+    const PackedTile *rows;
+    unsigned *counter;
+    void *out;
+    long long out_stride;
+    float *lse;           // [n_q_heads][n_tokens] or null
+    const float *slopes;  // [n_q_heads] or null
+    int n_tokens, n_kv, log_group, sink, win;
+    ScoreRule score;
+    unsigned *err;
+};
+cudaError_t launch_packed_fwd_bf16(const PackedFwdArgs &a, int hd, bool cap, int blocks, cudaStream_t stream);
+cudaError_t launch_packed_fwd_f16(const PackedFwdArgs &a, int hd, bool cap, int blocks, cudaStream_t stream);
+// Row tiles of 128 that a block of the forward kernel works on at once.
+constexpr int packed_fwd_tiles(int hd) { return hd == 256 ? 1 : 2; }
+
+}  // namespace fa

@@ -1,0 +1,517 @@
+// packed_fwd.cuh -- attention of packed documents on sm_103a tensor cores
+// (include/fa.h, fa_packed_attn); instantiated in packed_fwd_*.cu.
+//
+// For the query at position i of a document, over the keys j that it sees,
+//   x_j = f(scale q . k_j) - slope |i - j|,  f(s) = s or cap tanh(s / cap),
+//   out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),  lse = m + log sum_j e^(x_j - m).
+//
+// A persistent block takes units, 256 rows (two tiles of 128; one with head_dim 256)
+// of one kv head, and streams the key tiles past them:
+//   warp 0      copies Q, K and V tiles (TMA, 128-byte swizzle). In the last tile of a
+//               document V's rows past its end become zeros, as other documents and
+//               padding may hold anything and 0 * inf is not 0.
+//   warp 1      issues the products: S = Q K^T into TMEM, O += P V with P from TMEM.
+//   warps 4..   softmax, one thread a row: the running maximum in the exp2 domain, which
+//               moves only when a score passes it by 2^8, P rounded to the inputs' type
+//               over S, sums of the unrounded weights in fp32, and the output.
+// With two tiles the products of one run under the softmax of the other.
+#pragma once
+
+#include "packed_common.cuh"
+
+namespace fa {
+namespace {
+
+constexpr float kFwdLift = 8.0f;   // log2 growth of a score that moves the reference
+constexpr float kFwdShift = 6.0f;  // log2 of a weight at the reference: fp16 has its normal range below
+
+template <int HD_>
+struct FwdCfg {
+    static constexpr int HD = HD_;
+    static constexpr int NT = packed_fwd_tiles(HD);
+    static constexpr int BK = 128;
+    static constexpr int NCHUNK = HD / 64;
+    static constexpr uint32_t CHUNK = 128 * 128;  // 128 rows of 128 bytes
+    static constexpr uint32_t TILE = NCHUNK * CHUNK;
+    static constexpr int NS = HD == 256 ? 1 : 2;  // stages of K and of V
+    static constexpr uint32_t OFF_K = NT * TILE;
+    static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
+    static constexpr uint32_t OFF_END = OFF_V + NS * TILE;
+    // one block an SM, which owns all of TMEM
+    static constexpr uint32_t SMEM = (OFF_END + 1024 > 120u * 1024u) ? OFF_END + 1024 : 120u * 1024u;
+    static constexpr uint32_t S_COL = 256;  // O in columns 0 .. 255
+    static constexpr int THREADS = 128 + 128 * NT;
+};
+
+struct FwdBars {
+    uint64_t q_full, q_empty;
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_last[2], o_free[2];
+    uint64_t o_done, patch, drain;
+    UnitRing ring;
+    uint32_t tmem_base;
+    int abort;
+};
+
+template <int HD, bool BF16, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
+    packed_fwd_kernel(const __grid_constant__ PackedFwdArgs a) {
+    using C = FwdCfg<HD>;
+    constexpr int NT = C::NT, NS = C::NS, BK = C::BK;
+    constexpr uint32_t IDESC_QK = idesc_16<BF16>(128, BK, 0, 0);
+    constexpr uint32_t IDESC_PV = idesc_16<BF16>(128, HD, 0, 1);
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ FwdBars bars;
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    volatile int *abort = &bars.abort;
+    unsigned *err = a.err;
+
+    if (threadIdx.x == 0) {
+        mbar_init(&bars.q_full, 1);
+        mbar_init(&bars.q_empty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&bars.k_full[s], 1);
+            mbar_init(&bars.k_empty[s], 1);
+            mbar_init(&bars.v_full[s], 1);
+            mbar_init(&bars.v_empty[s], 1);
+            mbar_init(&bars.s_full[s], 1);
+            mbar_init(&bars.p_full[s], 128);
+            mbar_init(&bars.o_last[s], 1);
+            mbar_init(&bars.o_free[s], 128);
+        }
+        mbar_init(&bars.o_done, 1);
+        mbar_init(&bars.patch, 1);
+        mbar_init(&bars.drain, 1);
+        for (int k = 0; k < kPackedRing; ++k) {
+            mbar_init(&bars.ring.full[k], 1);
+            mbar_init(&bars.ring.empty[k], 1 + 4 * NT);  // the MMA thread and the softmax warps
+        }
+        bars.abort = 0;
+        mbar_fence_init();
+        tma_prefetch_desc(&a.q);
+        tma_prefetch_desc(&a.k);
+        tma_prefetch_desc(&a.v);
+    }
+    if (warp == 1) {
+        tmem_alloc(&bars.tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars.tmem_base;
+    wait_for_stream();
+
+    // the j-th unit of this block; false at the end of the work
+    auto next_unit = [&](int j, PackedTile *u) -> bool {
+        const int slot = j % kPackedRing;
+        if (!mbar_wait(&bars.ring.full[slot], (j / kPackedRing) & 1, abort, err)) return false;
+        *u = bars.ring.unit[slot];
+        return u->head >= 0;
+    };
+    const int row_tokens = (128 * NT) >> a.log_group;  // tokens of a unit
+    auto last_of = [&](const PackedTile &u) { return min(u.p0 + row_tokens, u.len) - 1; };
+    auto plan_of = [&](const PackedTile &u) {
+        return key_tiles<BK>(u.p0, last_of(u), u.prefix, a.sink, a.win);
+    };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- copies
+        const int units = a.header->row_tiles * a.n_kv;
+        Arms q_arms, k_arms[2], v_arms[2];
+        int patches = 0;
+        bool ok = true;
+        auto fetch = [&](int w, PackedTile *u) {
+            u->head = -1;
+            if (w >= units) return false;
+            *u = a.rows[w / a.n_kv];
+            u->head = w % a.n_kv;
+            return true;
+        };
+        auto publish = [&](int j, const PackedTile &u) {
+            const int slot = j % kPackedRing;
+            if (j >= kPackedRing &&
+                !mbar_wait(&bars.ring.empty[slot], ((j / kPackedRing) - 1) & 1, abort, err))
+                return false;
+            if (lane == 0) {
+                bars.ring.unit[slot] = u;
+                mbar_arrive(&bars.ring.full[slot]);
+            }
+            return true;
+        };
+        auto load_q = [&](int j, const PackedTile &u) {
+            if (j > 0 && !mbar_wait(&bars.q_empty, (j - 1) & 1, abort, err)) return false;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&bars.q_full, NT * C::TILE);
+                for (int t = 0; t < NT; ++t)
+                    for (int c = 0; c < C::NCHUNK; ++c)
+                        tma_load_4d(smem + t * C::TILE + c * C::CHUNK, &a.q, &bars.q_full, c * 64, 0, u.head,
+                                    u.tok0 + u.p0 + t * (row_tokens / NT));
+            }
+            ++q_arms.n;
+            return true;
+        };
+        auto load_kv = [&](int tt, int kt, const PackedTile &u, bool is_k) {
+            const int st = tt % NS;
+            if (tt >= NS && !mbar_wait(is_k ? &bars.k_empty[st] : &bars.v_empty[st], ((tt / NS) - 1) & 1, abort, err))
+                return false;
+            uint64_t *full = is_k ? &bars.k_full[st] : &bars.v_full[st];
+            uint8_t *dst = smem + (is_k ? C::OFF_K : C::OFF_V) + st * C::TILE;
+            const int rows = min(BK, u.len - kt * BK);
+            // columns of S past the end are masked, but V's rows are summed
+            const bool patch = !is_k && rows < BK;
+            uint64_t *bar = patch ? &bars.patch : full;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, C::TILE);
+                for (int c = 0; c < C::NCHUNK; ++c)
+                    tma_load_3d(dst + c * C::CHUNK, is_k ? &a.k : &a.v, bar, c * 64, u.head, u.tok0 + kt * BK);
+            }
+            if (patch) {
+                if (!mbar_wait(bar, patches++ & 1, abort, err)) return false;
+                zero_rows(dst, C::NCHUNK, C::CHUNK, rows, BK);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            }
+            if (is_k) ++k_arms[st].n; else ++v_arms[st].n;
+            return true;
+        };
+        int t = 0, w = blockIdx.x;
+        PackedTile u, un;
+        bool have = fetch(w, &u);
+        ok = publish(0, u);
+        if (have && ok) ok = load_q(0, u);
+        for (int j = 0; have && ok; ++j) {
+            const KeyTiles plan = plan_of(u);
+            const int cnt = plan.count;
+            bool more = false;
+            for (int i = 0; i < cnt && ok; ++i) {
+                ok = load_kv(t + i, plan.at(i), u, true);
+                if (ok && i == cnt - 1) {  // the next unit, under the waits for the last tiles
+                    if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                    w = __shfl_sync(~0u, w, 0);
+                    more = fetch(w, &un);
+                }
+                if (ok && i >= 1) ok = load_kv(t + i - 1, plan.at(i - 1), u, false);
+            }
+            if (ok) ok = load_kv(t + cnt - 1, plan.at(cnt - 1), u, false);
+            t += cnt;
+            if (!ok) break;
+            ok = publish(j + 1, un);
+            have = more;
+            if (have && ok) ok = load_q(j + 1, un);
+            u = un;
+        }
+        if (!ok) {  // copies already issued land before the block exits
+            q_arms.drain(&bars.q_full);
+            for (int s = 0; s < 2; ++s) {
+                k_arms[s].drain(&bars.k_full[s]);
+                v_arms[s].drain(&bars.v_full[s]);
+            }
+            if (patches) wait_out(&bars.patch, (patches - 1) & 1);
+        }
+    } else if (warp == 1) {
+        // ----------------------------------------------------------- products
+        if (lane == 0) {
+            const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
+            auto issue_s = [&](int tile, int tt, uint32_t col) {
+                const int st = tt % NS;
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
+                    mma_ss(tmem + col, desc_sw128(sQ + tile * C::TILE + off, 16, 1024),
+                           desc_sw128(sK + st * C::TILE + off, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
+                }
+            };
+            auto issue_pv = [&](int tile, int tt, uint32_t col, bool first) {
+                const int st = tt % NS;
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                    mma_ts(tmem + tile * HD, tmem + col + kk * 8,
+                           desc_sw128(sV + st * C::TILE + kk * 2048, C::CHUNK, 1024), IDESC_PV,
+                           (!first || kk > 0) ? 1u : 0u);
+            };
+            int t = 0;
+            bool ok = true;
+            PackedTile u;
+            for (int j = 0; ok && next_unit(j, &u); ++j) {
+                mbar_arrive(&bars.ring.empty[j % kPackedRing]);
+                const int count = plan_of(u).count;
+                if (!(ok = mbar_wait(&bars.q_full, j & 1, abort, err))) break;
+                tc_fence_after();
+                // P of tile tt is there, and O free for a unit's first product
+                auto wait_p = [&](int tile, int tt, bool first, uint32_t bar, uint32_t parity) {
+                    if (!mbar_wait(&bars.p_full[bar], parity, abort, err)) return false;
+                    if (first && j > 0 && !mbar_wait(&bars.o_free[tile], (j - 1) & 1, abort, err)) return false;
+                    return true;
+                };
+                auto wait_kv = [&](uint64_t *full, int tt) {
+                    return mbar_wait(full + tt % NS, (tt / NS) & 1, abort, err);
+                };
+                if (NT == 2) {
+                    // one S for each tile: its next product follows the one that reads its P
+                    for (int i = 0; i <= count && ok; ++i) {
+                        const int tt = t + i;
+                        if (i < count && !(ok = wait_kv(bars.k_full, tt))) break;
+#pragma unroll
+                        for (int tile = 0; tile < 2; ++tile) {
+                            const uint32_t col = C::S_COL + tile * 128;
+                            if (i > 0) {
+                                ok = ok && wait_p(tile, tt - 1, i == 1, tile, (tt - 1) & 1);
+                                if (ok && tile == 0) ok = wait_kv(bars.v_full, tt - 1);
+                                if (!ok) break;
+                                tc_fence_after();
+                                issue_pv(tile, tt - 1, col, i == 1);
+                                if (tile == 1) tc_commit(&bars.v_empty[(tt - 1) % NS]);
+                                if (i == count) tc_commit(&bars.o_last[tile]);
+                            }
+                            if (i < count) {
+                                tc_fence_after();
+                                issue_s(tile, tt, col);
+                                tc_commit(&bars.s_full[tile]);
+                                if (tile == 1) {
+                                    tc_commit(&bars.k_empty[tt % NS]);
+                                    if (i == count - 1) tc_commit(&bars.q_empty);
+                                }
+                            }
+                        }
+                    }
+                } else {
+                    // two S for the tile, which take turns
+                    for (int i = 0; i <= count && ok; ++i) {
+                        const int tt = t + i;
+                        if (i < count) {
+                            if (!(ok = wait_kv(bars.k_full, tt))) break;
+                            tc_fence_after();
+                            issue_s(0, tt, C::S_COL + (tt & 1) * 128);
+                            tc_commit(&bars.k_empty[tt % NS]);
+                            tc_commit(&bars.s_full[tt & 1]);
+                            if (i == count - 1) tc_commit(&bars.q_empty);
+                        }
+                        if (i > 0) {
+                            const int pt = tt - 1;
+                            if (!(ok = wait_p(0, pt, i == 1, pt & 1, (pt >> 1) & 1) && wait_kv(bars.v_full, pt))) break;
+                            tc_fence_after();
+                            issue_pv(0, pt, C::S_COL + (pt & 1) * 128, i == 1);
+                            tc_commit(&bars.v_empty[pt % NS]);
+                            tc_commit(&bars.o_done);
+                            if (i == count) tc_commit(&bars.o_last[0]);
+                        }
+                    }
+                }
+                t += count;
+            }
+            // every product issued completes before TMEM is released
+            tc_commit(&bars.drain);
+            wait_out(&bars.drain, 0);
+        }
+    } else if (warp >= 4) {
+        // ------------------------------------------------- softmax and output
+        const int tile = (warp - 4) >> 2;  // this warp's tile of the unit
+        const int r = threadIdx.x - 128 - 128 * tile;  // row of the tile: TMEM lane
+        const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const int lg = a.log_group, tile_tokens = 128 >> lg;
+        const ScoreRule rule = a.score;
+        int t = 0;
+        bool ok = true;
+        PackedTile u;
+        for (int j = 0; ok; ++j) {
+            const bool have = next_unit(j, &u);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.ring.empty[j % kPackedRing]);
+            if (!__all_sync(~0u, have)) break;
+            const KeyTiles plan = plan_of(u);
+            const int p0 = u.p0 + tile * tile_tokens;                // of this tile
+            const int p1 = min(p0 + tile_tokens, u.len) - 1;         // (below p0: no rows)
+            const int p = p0 + (r >> lg);
+            const int head = (u.head << lg) + (r & ((1 << lg) - 1));
+            const float slope2 = BIAS ? load(a.slopes + head) * kPackedLog2e : 0.0f;
+            float m_used = -INFINITY;  // reference of O and l
+            float l = 0.0f;
+            for (int i = 0; i < plan.count; ++i) {
+                const int tt = t + i;
+                const int bar = NT == 2 ? tile : tt & 1;
+                ok = mbar_wait(&bars.s_full[bar], (NT == 2 ? tt : tt >> 1) & 1, abort, err);
+                ok = __all_sync(~0u, ok);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t scol = tmem + lane_base + C::S_COL + bar * 128;
+                uint32_t s[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, s + 32 * c);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) reg_fence32(s + 32 * c);
+
+                const int j0 = plan.at(i) * BK, j1 = j0 + BK - 1;
+                if (CAP) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(capped(__uint_as_float(s[c]), rule));
+                }
+                float mx = -INFINITY;
+                const bool whole = sees_all(p0, p1, j0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= p0);
+                if (BIAS) {
+                    const float far = static_cast<float>(p - j0);  // exact: below 2^26 apart
+                    if (whole) {
+                        const float base = -slope2 * far;
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) {
+                            const float b = fmaf(slope2, static_cast<float>(c), base);
+                            s[c] = __float_as_uint(CAP ? __uint_as_float(s[c]) + b
+                                                       : fmaf(__uint_as_float(s[c]), rule.a, b));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) {
+                            const float b = -slope2 * fabsf(far - static_cast<float>(c));
+                            s[c] = __float_as_uint(CAP ? __uint_as_float(s[c]) + b
+                                                       : fmaf(__uint_as_float(s[c]), rule.a, b));
+                        }
+                    }
+                }
+                if (whole) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
+                } else {
+                    // key j0 + c is seen iff c < head or lo <= c <= hi
+                    const int hi = p - j0;
+                    const int lo = a.win > 0 ? p - a.win + 1 - j0 : 0;
+                    const int first = max(u.prefix - j0, a.win > 0 ? min(a.sink - j0, hi + 1) : 0);
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) {
+                        const bool seen = (c < first) | ((c >= lo) & (c <= hi));
+                        const float v = seen ? __uint_as_float(s[c]) : -INFINITY;
+                        s[c] = __float_as_uint(v);
+                        mx = fmaxf(mx, v);
+                    }
+                }
+                constexpr bool kScaled = CAP || BIAS;  // s is in the exp2 domain already
+                const float m_new = fmaxf(m_used, kScaled ? mx : mx * rule.a);
+                float corr = 1.0f;
+                bool moves = false;
+                if (m_new > m_used + kFwdLift) {
+                    if (m_used != -INFINITY) {
+                        corr = ex2(m_used - m_new);
+                        moves = true;
+                        l *= corr;
+                    }
+                    m_used = m_new;
+                }
+                const float ref = m_used == -INFINITY ? 0.0f : m_used - kFwdShift;
+                uint32_t pk[64];
+                float sum0 = 0.0f, sum1 = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
+                    const float w0 = ex2(kScaled ? s0 - ref : fmaf(s0, rule.a, -ref));
+                    const float w1 = ex2(kScaled ? s1 - ref : fmaf(s1, rule.a, -ref));
+                    sum0 += w0;
+                    sum1 += w1;
+                    pk[c] = pack2<BF16>(w0, w1);
+                }
+                l += sum0 + sum1;
+                // O is rescaled when every product into it is done. With one S a tile that
+                // holds already: S(tt) was issued after them. With two, PV(tt - 1) may still run.
+                const bool any = __any_sync(~0u, moves);
+                if (NT == 1 && any) {
+                    ok = mbar_wait(&bars.o_done, (tt - 1) & 1, abort, err);
+                    ok = __all_sync(~0u, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                __syncwarp();
+                if (any) {
+#pragma unroll 1
+                    for (int c = 0; c < HD / 32; ++c) {
+                        uint32_t o[32];
+                        const uint32_t oc = tmem + lane_base + tile * HD + 32 * c;
+                        tmem_ld32(oc, o);
+                        tmem_wait_ld();
+                        reg_fence32(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * corr);
+                        tmem_st32(oc, o);
+                    }
+                }
+                tmem_st32(scol, pk);
+                tmem_st32(scol + 32, pk + 32);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&bars.p_full[bar]);
+            }
+            if (!ok) break;
+            t += plan.count;
+            ok = mbar_wait(&bars.o_last[tile], j & 1, abort, err);
+            ok = __all_sync(~0u, ok);
+            if (!ok) break;
+            tc_fence_after();
+            const bool live = p < u.len;
+            const float inv = 1.0f / l;  // a row sees itself, so that l > 0 (or a NaN)
+            if (a.lse && live)
+                a.lse[static_cast<size_t>(head) * a.n_tokens + u.tok0 + p] =
+                    (m_used - kFwdShift + log2f(l)) * kPackedLn2;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + (static_cast<long long>(u.tok0) + p) * a.out_stride +
+                            static_cast<long long>(head) * HD;
+#pragma unroll 1
+            for (int c = 0; c < HD / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tmem + lane_base + tile * HD + 32 * c, o);
+                tmem_wait_ld();
+                reg_fence32(o);
+                if (c == HD / 32 - 1) {  // read whole: the next unit may overwrite it
+                    tc_fence_before();
+                    mbar_arrive(&bars.o_free[tile]);
+                }
+                if (live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * inv,
+                                               __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int HD, bool BF16, bool CAP, bool BIAS>
+cudaError_t launch_fwd(const PackedFwdArgs &a, int blocks, cudaStream_t stream) {
+    using C = FwdCfg<HD>;
+    auto kernel = packed_fwd_kernel<HD, BF16, CAP, BIAS>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_after(kernel, dim3(blocks), C::THREADS, C::SMEM, stream, a);
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_fwd_rule(const PackedFwdArgs &a, bool cap, int blocks, cudaStream_t stream) {
+    if (cap)
+        return a.slopes ? launch_fwd<HD, BF16, true, true>(a, blocks, stream)
+                        : launch_fwd<HD, BF16, true, false>(a, blocks, stream);
+    return a.slopes ? launch_fwd<HD, BF16, false, true>(a, blocks, stream)
+                    : launch_fwd<HD, BF16, false, false>(a, blocks, stream);
+}
+
+template <bool BF16>
+cudaError_t launch_fwd_type(const PackedFwdArgs &a, int hd, bool cap, int blocks, cudaStream_t stream) {
+    switch (hd) {
+        case 64: return launch_fwd_rule<64, BF16>(a, cap, blocks, stream);
+        case 128: return launch_fwd_rule<128, BF16>(a, cap, blocks, stream);
+        default: return launch_fwd_rule<256, BF16>(a, cap, blocks, stream);
+    }
+}
+
+}  // namespace
+}  // namespace fa

@@ -1,0 +1,170 @@
+// packed_plan.cu -- the tiles of a packed batch, heaviest first, and the work
+// counters of the kernels that walk them (include/fa.h, fa_packed_attn).
+//
+// One block. Documents are summed (tiles before each of them), then the tiles are
+// counted into bins of their number of key tiles (or row tiles, for a tile of keys)
+// and put into the lists from the heaviest bin on. Within a bin the order may differ
+// from call to call: units do not depend on each other, so that no result does.
+#include "packed_common.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr int kBins = 1024;
+constexpr int kDocsInSmem = 2048;
+
+// Sums of a, b, c over the threads before this one, and over all.
+__device__ __forceinline__ void scan3(int &a, int &b, int &c, int *sum, int (*part)[32]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int v[3] = {a, b, c}, own[3] = {a, b, c};
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const int o = __shfl_up_sync(~0u, v[k], d);
+            if (lane >= d) v[k] += o;
+        }
+    if (lane == 31)
+        for (int k = 0; k < 3; ++k) part[k][warp] = v[k];
+    __syncthreads();
+    if (warp < 3) {
+        int x = part[warp][lane], s = x;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(~0u, s, d);
+            if (lane >= d) s += o;
+        }
+        part[warp][lane] = s - x;
+        if (lane == 31) sum[warp] = s;
+    }
+    __syncthreads();
+    a = v[0] - own[0] + part[0][warp];
+    b = v[1] - own[1] + part[1][warp];
+    c = v[2] - own[2] + part[2][warp];
+}
+
+// The document that holds tile x: the last one with before[d] <= x that has tiles.
+__device__ __forceinline__ int find_doc(const int *before, int n, int x) {
+    int lo = 0, hi = n;  // before[lo] <= x < before[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (before[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArgs a) {
+    wait_for_stream();
+    __shared__ int part[3][32], sum[3];
+    __shared__ int bins[kBins];
+    __shared__ int small[3][kDocsInSmem + 1];
+    __shared__ int bad_docs;
+    const int tid = threadIdx.x, D = a.n_docs;
+    const bool fits = D <= kDocsInSmem;
+    int *before[3];
+    for (int k = 0; k < 3; ++k) before[k] = fits ? small[k] : a.doc_tiles + static_cast<size_t>(k) * (D + 1);
+    if (tid == 0) bad_docs = 0;
+    if (tid < 4) a.header->counters[tid] = 0;
+    __syncthreads();
+
+    // ---- tiles before each document: a thread sums a run of documents
+    const int per = (D + kPlanThreads - 1) / kPlanThreads;
+    const int d0 = min(D, tid * per), d1 = min(D, d0 + per);
+    int nr = 0, nk = 0, nb = 0;
+    bool bad = false;
+    auto length = [&](int d) {
+        const int from = load(a.cu + d), to = load(a.cu + d + 1);
+        if (from < 0 || to < from || to > a.n_tokens) {
+            bad = true;
+            return 0;
+        }
+        return to - from;
+    };
+    auto tiles = [&](int n, int *r, int *k, int *b) {
+        *r = (n + a.row_tokens - 1) / a.row_tokens;
+        *k = a.most_keys ? (n + 127) / 128 : 0;
+        *b = (n + (1 << a.block_tokens_log) - 1) >> a.block_tokens_log;
+    };
+    for (int d = d0; d < d1; ++d) {
+        int r, k, b;
+        tiles(length(d), &r, &k, &b);
+        nr += r, nk += k, nb += b;
+        if (a.doc_most) a.doc_most[d] = a.doc_most[D + d] = 0u;
+    }
+    if (bad) bad_docs = 1;
+    scan3(nr, nk, nb, sum, part);
+    for (int d = d0; d < d1; ++d) {
+        before[0][d] = nr, before[1][d] = nk, before[2][d] = nb;
+        int r, k, b;
+        tiles(length(d), &r, &k, &b);
+        nr += r, nk += k, nb += b;
+    }
+    if (tid == 0)
+        for (int k = 0; k < 3; ++k) before[k][D] = sum[k];
+    __syncthreads();
+    // documents that overlap (cu decreases) could have more tiles than there is room for
+    int total[2] = {sum[0], sum[1]};
+    if (bad_docs || total[0] > a.most_rows || total[1] > a.most_keys) {
+        total[0] = total[1] = 0;
+        if (tid == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
+    }
+    if (tid == 0) {
+        a.header->row_tiles = total[0];
+        a.header->key_tiles = total[1];
+    }
+
+    // ---- the lists
+    for (int list = 0; list < 2; ++list) {
+        const int n = total[list];
+        if (n == 0) continue;
+        int shift = 0;  // bins of a power of two of key (or row) tiles
+        const int step = list ? a.row_tokens : a.key_tile;
+        while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
+        auto tile = [&](int x, PackedTile *t) {
+            const int d = find_doc(before[list], D, x);
+            t->tok0 = load(a.cu + d);
+            t->len = load(a.cu + d + 1) - t->tok0;
+            t->p0 = (x - before[list][d]) * (list ? 128 : a.row_tokens);
+            t->prefix = a.prefix ? min(max(load(a.prefix + d), 0), t->len) : 0;
+            t->rb = before[2][d];
+            t->doc = d;
+            t->head = t->pad = 0;
+            int w;
+            if (list) {
+                int first, last;
+                query_range(t->p0, min(t->p0 + 128, t->len) - 1, t->len, t->prefix, a.sink, a.win, &first, &last);
+                w = last / a.row_tokens - first / a.row_tokens + 1;
+            } else {
+                const int p1 = min(t->p0 + a.row_tokens, t->len) - 1;
+                w = a.key_tile == 64 ? key_tiles<64>(t->p0, p1, t->prefix, a.sink, a.win).count
+                                     : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
+            }
+            return kBins - 1 - min(w >> shift, kBins - 1);  // heaviest first
+        };
+        for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
+        __syncthreads();
+        PackedTile t;
+        for (int x = tid; x < n; x += kPlanThreads) atomicAdd(&bins[tile(x, &t)], 1);
+        __syncthreads();
+        static_assert(kBins == kPlanThreads, "a bin for each thread");
+        int at = bins[tid], z0 = 0, z1 = 0;
+        scan3(at, z0, z1, sum, part);
+        bins[tid] = at;
+        __syncthreads();
+        PackedTile *out = list ? a.keys : a.rows;
+        for (int x = tid; x < n; x += kPlanThreads) {
+            const int bin = tile(x, &t);
+            out[atomicAdd(&bins[bin], 1)] = t;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_packed_plan(const PackedPlanArgs &a, cudaStream_t stream) {
+    return launch_after(packed_plan_kernel, dim3(1), kPlanThreads, 0, stream, a);
+}
+
+}  // namespace fa

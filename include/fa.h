@@ -576,6 +576,53 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
                         int head_dim, int sink, int win, float scale, void *workspace,
                         size_t workspace_bytes, fa_stream_t stream);
 
+/* -------------------------------------------------------- packed documents
+ *
+ * Attention of documents that lie packed one behind another, as a training step
+ * or the first pass over prompts has them, and its gradient. Scores may be capped
+ * and may fall with the distance; a query sees its own document alone.
+ *
+ * For the query at position i and the key at position j of a document (counted
+ * from its first token), with s = scale * q . k:
+ *   score = cap * tanh(s / cap) (s itself where cap is 0) - slopes[head] * |i - j|
+ * and the query attends key j iff
+ *   j < prefix[doc], or j <= i and (win <= 0 or j < sink or j > i - win).
+ * Every query attends itself. Within a document an infinity or a NaN in q, k or v
+ * may reach any of its results; other documents and padding never do.
+ *
+ *   q, k, v    token t's heads start at element t * stride, [n_q_heads] (k, v:
+ *              [n_kv_heads]) [head_dim] values of dtype, FA_T_F16 or FA_T_BF16
+ *              (FA_T_F32: FA_ERR_UNSUPPORTED). Rows are 16-byte aligned, strides
+ *              multiples of 8, and n_tokens * stride is at most 2^38.
+ *   cu_docs    [n_docs + 1] int32 (device), not decreasing: document d is tokens
+ *              cu_docs[d] .. cu_docs[d+1]-1. Tokens outside every document
+ *              (padding) are not used and their results not written. An entry below the one
+ *              before it or outside [0, n_tokens] flags FA_ERR_DEVICE, and nothing
+ *              is written.
+ *   prefix     [n_docs] int32 (device) or NULL (none): keys of each document that
+ *              all its queries attend, cut to [0, its tokens].
+ *   scale      > 0; 0 means 1 / sqrt(head_dim). cap: >= 0, 0 for none.
+ *   slopes     [n_q_heads] fp32 (device) or NULL for no bias. (They get no gradient.)
+ *   workspace  >= the call's workspace bytes, 16-byte aligned; scratch. Calls that
+ *              share a workspace must not overlap on the GPU.
+ * Supported: head_dim, n_q_heads and n_kv_heads as for fa_prefill; n_docs <= 65536,
+ * n_tokens <= 2^26, n_tokens * n_q_heads <= 2^30. No output may overlap an input. */
+
+/* Workspace bytes of fa_packed_attn, or 0 for unsupported sizes. */
+size_t fa_packed_attn_workspace_bytes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads,
+                                      int head_dim);
+
+/* out [n_tokens][n_q_heads][head_dim] of dtype (out_stride elements between
+ * tokens) and lse [n_q_heads][n_tokens] fp32 or NULL: the natural log-sum-exp of
+ * each row's scores. Scores, softmax and sums are fp32; the weights are rounded to
+ * dtype for their products with V, their sum is not. */
+fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out, float *lse,
+                         int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                         int64_t out_stride, const int32_t *cu_docs, const int32_t *prefix,
+                         int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                         int sink, int win, float scale, float cap, const float *slopes,
+                         void *workspace, size_t workspace_bytes, fa_stream_t stream);
+
 /* ---------------------------------------------------------------- profiling */
 
 /* Optional timing hook. While both events are non-NULL (cudaEvent_t handles
