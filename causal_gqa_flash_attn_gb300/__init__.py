@@ -70,6 +70,9 @@ SIGNATURES = {
     "fa_packed_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_packed_attn": (_I, [_P, _P, _P, _P, _P, _I, _L, _L, _L, _L, _P, _P, _I, _I, _I, _I, _I, _I,
                             _I, _F, _F, _P, _P, _SZ, _P]),
+    "fa_packed_attn_grad_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
+    "fa_packed_attn_grad": (_I, [_P] * 9 + [_I] + [_L] * 8 + [_P, _P, _I, _I, _I, _I, _I, _I, _I,
+                                                              _F, _F, _P, _P, _SZ, _P]),
     "fa_set_kernel_events": (_I, [_P, _P]),
     "fa_get_device_error": (_I, [_P]),
     "fa_status_string": (ctypes.c_char_p, [_I]),
@@ -577,6 +580,35 @@ def packed_attn(q, k, v, out, cu_docs, *, prefix=None, sink: int = 0, win: int =
         ks, vs, os_, cu, pre, D, T, hq, hkv, hd, sink, win, scale, cap, sl,
         _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
         _raw_stream(stream, here)), "fa_packed_attn")
+
+
+def packed_attn_grad_workspace_bytes(n_docs: int, n_tokens: int, n_q_heads: int, n_kv_heads: int,
+                                     head_dim: int) -> int:
+    return int(lib().fa_packed_attn_grad_workspace_bytes(n_docs, n_tokens, n_q_heads, n_kv_heads,
+                                                         head_dim))
+
+
+def packed_attn_grad(q, k, v, out, lse, dout, dq, dk, dv, cu_docs, *, prefix=None, sink: int = 0,
+                     win: int = 0, scale: float = 0.0, cap: float = 0.0, slopes=None, workspace,
+                     stream=None):
+    """fa_packed_attn_grad: dq, dk, dv (like q, k, v) from dout (like out), with the
+    inputs, out and lse of the packed_attn call and its cu_docs, prefix and scores."""
+    here = _here(q, "q")
+    code, dtype, shape = _type(q, "q"), q.dtype, q.shape
+    T, hq, hd = shape
+    _type(k, "k")
+    hkv = k.shape[1]
+    kv = (T, hkv, hd)
+    tensors = (("q", q, shape), ("k", k, kv), ("v", v, kv), ("out", out, shape),
+               ("dout", dout, shape), ("dq", dq, shape), ("dk", dk, kv), ("dv", dv, kv))
+    (qp, qs), (kp, ks), (vp, vs), (op, os_), (dop, dos), (dqp, dqs), (dkp, dks), (dvp, dvs) = (
+        _heads(t, name, dtype, its, here) for name, t, its in tensors)
+    D, cu, pre, sl = _packed_rule(cu_docs, prefix, slopes, hq, here)
+    _check(lib().fa_packed_attn_grad(
+        qp, kp, vp, op, _arg(lse, "lse", _F32, (hq, T), here), dop, dqp, dkp, dvp, code, qs, ks,
+        vs, os_, dos, dqs, dks, dvs, cu, pre, D, T, hq, hkv, hd, sink, win, scale, cap, sl,
+        _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
+        _raw_stream(stream, here)), "fa_packed_attn_grad")
 
 
 def set_kernel_events(start, stop):

@@ -176,4 +176,145 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
                                         : fa::launch_packed_fwd_f16(a, head_dim, cap > 0.0f, blocks, s));
 }
 
+size_t fa_packed_attn_grad_workspace_bytes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads,
+                                           int head_dim) {
+    if (check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim) != FA_OK) return 0;
+    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128, true).bytes;
+}
+
+fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const void *out, const float *lse,
+                              const void *dout, void *dq, void *dk, void *dv, int dtype, int64_t q_stride,
+                              int64_t k_stride, int64_t v_stride, int64_t out_stride, int64_t dout_stride,
+                              int64_t dq_stride, int64_t dk_stride, int64_t dv_stride, const int32_t *cu_docs,
+                              const int32_t *prefix, int n_docs, int n_tokens, int n_q_heads, int n_kv_heads,
+                              int head_dim, int sink, int win, float scale, float cap, const float *slopes,
+                              void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+    fa_status st = check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim);
+    if (st != FA_OK) return st;
+    st = check_rule(dtype, cu_docs, prefix, sink, scale, cap, slopes, workspace);
+    if (st != FA_OK) return st;
+    if (n_docs == 0 || n_tokens == 0) return FA_OK;
+    if (!cu_docs || !workspace || !lse || !aligned(lse, 4) ||
+        !good_heads(q, q_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_heads(k, k_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_heads(v, v_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_heads(out, out_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_heads(dout, dout_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_heads(dq, dq_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_heads(dk, dk_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_heads(dv, dv_stride, n_kv_heads, head_dim, n_tokens))
+        return FA_ERR_INVALID;
+    const void *in[5] = {q, k, v, out, dout};
+    const void *made[3] = {dq, dk, dv};
+    for (int i = 0; i < 3; ++i) {
+        for (int k2 = 0; k2 < 5; ++k2)
+            if (made[i] == in[k2]) return FA_ERR_INVALID;
+        if (made[i] == made[(i + 1) % 3]) return FA_ERR_INVALID;
+    }
+    const int group = n_q_heads / n_kv_heads, step = fa::packed_grad_rows(head_dim);
+    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128, true);
+    if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
+    unsigned *err = fa::device_error_word();
+    if (!err) return FA_ERR_CUDA;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+
+    fa::PackedPlanArgs p;
+    p.cu = cu_docs;
+    p.prefix = prefix;
+    p.n_docs = n_docs;
+    p.n_tokens = n_tokens;
+    p.sink = bounded(sink);
+    p.win = bounded(win);
+    p.row_tokens = 128 / group;
+    p.block_tokens_log = 7 - log2_of(group);
+    p.key_tile = step;
+    p.most_rows = w.most_rows;
+    p.most_keys = w.most_keys;
+    p.header = reinterpret_cast<fa::PackedHeader *>(ws);
+    p.rows = reinterpret_cast<fa::PackedTile *>(ws + w.row_tiles);
+    p.keys = reinterpret_cast<fa::PackedTile *>(ws + w.key_tiles);
+    p.doc_tiles = reinterpret_cast<int *>(ws + w.doc_tiles);
+    p.doc_most = reinterpret_cast<unsigned *>(ws + w.doc_most);
+    p.err = err;
+
+    fa::PackedStatsArgs t;
+    t.header = p.header;
+    t.rows = p.rows;
+    t.out = out;
+    t.dout = dout;
+    t.v = v;
+    t.out_stride = out_stride;
+    t.dout_stride = dout_stride;
+    t.v_stride = v_stride;
+    t.lse = lse;
+    t.n_tokens = n_tokens;
+    t.n_kv = n_kv_heads;
+    t.log_group = log2_of(group);
+    t.n_docs = n_docs;
+    t.blocks = static_cast<long long>(w.blocks);
+    t.L = reinterpret_cast<float *>(ws + w.stats);
+    t.D = t.L + static_cast<size_t>(n_kv_heads) * w.blocks * 128;
+    t.doc_most = p.doc_most;
+
+    fa::PackedGradArgs a;
+    a.header = p.header;
+    a.L = t.L;
+    a.D = t.D;
+    a.blocks = t.blocks;
+    a.doc_most = p.doc_most;
+    a.slopes = slopes;
+    a.n_docs = n_docs;
+    a.n_kv = n_kv_heads;
+    a.log_group = t.log_group;
+    a.sink = p.sink;
+    a.win = p.win;
+    a.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    a.score = fa::score_rule(a.scale, cap);
+    a.err = err;
+    fa::PackedGradArgs b = a;  // of dk and dv
+    a.tiles = p.rows;
+    a.n_tiles = &p.header->row_tiles;
+    a.counter = &p.header->counters[0];
+    a.g1 = dq;
+    a.g1_stride = dq_stride;
+    a.g2 = nullptr;
+    a.g2_stride = 0;
+    b.tiles = p.keys;
+    b.n_tiles = &p.header->key_tiles;
+    b.counter = &p.header->counters[1];
+    b.g1 = dk;
+    b.g1_stride = dk_stride;
+    b.g2 = dv;
+    b.g2_stride = dv_stride;
+    if (!map_rows(&a.x1, dtype, q, q_stride, n_tokens, n_kv_heads, group, head_dim, 128) ||
+        !map_rows(&a.x2, dtype, dout, dout_stride, n_tokens, n_kv_heads, group, head_dim, 128) ||
+        !map_keys(&a.y1, dtype, k, k_stride, n_tokens, n_kv_heads, head_dim, step) ||
+        !map_keys(&a.y2, dtype, v, v_stride, n_tokens, n_kv_heads, head_dim, step) ||
+        !map_keys(&b.x1, dtype, k, k_stride, n_tokens, n_kv_heads, head_dim, 128) ||
+        !map_keys(&b.x2, dtype, v, v_stride, n_tokens, n_kv_heads, head_dim, 128) ||
+        !map_rows(&b.y1, dtype, q, q_stride, n_tokens, n_kv_heads, group, head_dim, step) ||
+        !map_rows(&b.y2, dtype, dout, dout_stride, n_tokens, n_kv_heads, group, head_dim, step))
+        return FA_ERR_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int sms = fa::device_sm_count();
+    auto blocks_of = [&](int tiles, int most) {
+        return static_cast<int>(std::min<long long>(most, static_cast<long long>(tiles) * n_kv_heads));
+    };
+    auto launch = [&](const fa::PackedGradArgs &g, int mode, int blocks) {
+        return dtype == FA_T_BF16 ? fa::launch_packed_grad_bf16(g, mode, head_dim, cap > 0.0f, blocks, s)
+                                  : fa::launch_packed_grad_f16(g, mode, head_dim, cap > 0.0f, blocks, s);
+    };
+    cudaError_t e = fa::launch_packed_plan(p, s);
+    if (e == cudaSuccess) e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, 8 * sms), s);
+    if (e == cudaSuccess) e = launch(a, fa::kGradQ, blocks_of(w.most_rows, sms));
+    if (head_dim < 256) {
+        if (e == cudaSuccess) e = launch(b, fa::kGradKV, blocks_of(w.most_keys, sms));
+    } else {
+        if (e == cudaSuccess) e = launch(b, fa::kGradK, blocks_of(w.most_keys, sms));
+        b.counter = &p.header->counters[2];
+        if (e == cudaSuccess) e = launch(b, fa::kGradV, blocks_of(w.most_keys, sms));
+    }
+    return from_cuda(e);
+}
+
 }  // extern "C"

@@ -189,4 +189,48 @@ cudaError_t launch_packed_fwd_f16(const PackedFwdArgs &a, int hd, bool cap, int 
 // Row tiles of 128 that a block of the forward kernel works on at once.
 constexpr int packed_fwd_tiles(int hd) { return hd == 256 ? 1 : 2; }
 
+// ---- packed_stats.cu
+// What the gradient needs of each row: L, its log-sum-exp in the exp2 domain (less
+// kGradShift for binary16), and D = dout . out; and of each document, for binary16,
+// the largest row of dout and of V.
+struct PackedStatsArgs {
+    const PackedHeader *header;
+    const PackedTile *rows;  // tiles of 128 rows
+    const void *out, *dout, *v;
+    long long out_stride, dout_stride, v_stride;
+    const float *lse;
+    int n_tokens, n_kv, log_group, n_docs;
+    long long blocks;        // 128-row blocks of a kv head
+    float *L, *D;            // [n_kv][blocks][128]
+    unsigned *doc_most;      // [2][n_docs]: bits of the largest |dout row|^2 and |v row|^2
+};
+cudaError_t launch_packed_stats(const PackedStatsArgs &a, int dtype, int hd, int blocks, cudaStream_t stream);
+constexpr float kGradShift = 14.0f;
+
+// ---- packed_bwd.cuh
+struct PackedGradArgs {
+    // Stationary tiles x1, x2 and moving ones y1, y2: q, dout and k, v for dq; the other way round
+    // for dk and dv.
+    CUtensorMap x1, x2, y1, y2;
+    const PackedHeader *header;
+    const PackedTile *tiles;
+    const int *n_tiles;
+    unsigned *counter;
+    void *g1, *g2;           // dq; or dk and dv (one of them null where a kernel makes the other)
+    long long g1_stride, g2_stride;
+    const float *L, *D;
+    long long blocks;
+    const unsigned *doc_most;
+    const float *slopes;
+    int n_docs, n_kv, log_group, sink, win;
+    float scale;
+    ScoreRule score;
+    unsigned *err;
+};
+enum { kGradQ = 0, kGradKV = 1, kGradK = 2, kGradV = 3 };
+// Rows (or keys) of a moving tile.
+constexpr int packed_grad_rows(int hd) { return hd == 256 ? 64 : 128; }
+cudaError_t launch_packed_grad_bf16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream);
+cudaError_t launch_packed_grad_f16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream);
+
 }  // namespace fa

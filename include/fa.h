@@ -623,6 +623,28 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
                          int sink, int win, float scale, float cap, const float *slopes,
                          void *workspace, size_t workspace_bytes, fa_stream_t stream);
 
+/* Workspace bytes of fa_packed_attn_grad, or 0 for unsupported sizes. */
+size_t fa_packed_attn_grad_workspace_bytes(int n_docs, int n_tokens, int n_q_heads,
+                                           int n_kv_heads, int head_dim);
+
+/* The gradient of fa_packed_attn: from dout, that of out (laid out like it, with
+ * its own stride), the out and lse that fa_packed_attn gave and its inputs, dq
+ * like q and dk, dv like k and v (each with its own stride; dk and dv are the sums
+ * over the q heads of their kv head). Sums are fp32 and in a fixed order, so that
+ * equal calls give equal bits; the weights and the gradients of the scores are
+ * rounded to dtype for their products. With FA_T_F16 a document's score gradients
+ * are scaled by a power of two from the largest rows of its dout and v, so that
+ * they keep their precision whatever dout's magnitude. */
+fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const void *out,
+                              const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                              int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                              int64_t out_stride, int64_t dout_stride, int64_t dq_stride,
+                              int64_t dk_stride, int64_t dv_stride, const int32_t *cu_docs,
+                              const int32_t *prefix, int n_docs, int n_tokens, int n_q_heads,
+                              int n_kv_heads, int head_dim, int sink, int win, float scale,
+                              float cap, const float *slopes, void *workspace,
+                              size_t workspace_bytes, fa_stream_t stream);
+
 /* ---------------------------------------------------------------- profiling */
 
 /* Optional timing hook. While both events are non-NULL (cudaEvent_t handles
