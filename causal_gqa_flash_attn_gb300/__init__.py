@@ -63,10 +63,14 @@ SIGNATURES = {
     "fa_rope": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _L, _P, _L, _I, _P, _I,
                      _I, _P]),
     "fa_paged_append": (_I, [_P, _P, _I, _L, _L, _P, _I, _P, _I, _I, _I, _I, _P]),
+    "fa_rope_append": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _L, _L, _L, _L, _P, _L, _I, _P,
+                            _I, _P, _P, _I, _I, _P]),
     "fa_paged_gather": (_I, [_P, _I, _P, _I, _P, _I, _I, _I, _I, _P, _P, _I, _P]),
     "fa_paged_attn_workspace_bytes": (_SZ, [_I]),
     "fa_paged_attn": (_I, [_P, _P, _P, _I, _L, _L, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
                            _I, _I, _I, _F, _P, _SZ, _P]),
+    "fa_paged_attn_scored": (_I, [_P, _P, _P, _I, _L, _L, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I,
+                                  _I, _I, _I, _I, _F, _F, _P, _P, _SZ, _P]),
     "fa_packed_attn_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "fa_packed_attn": (_I, [_P, _P, _P, _P, _P, _I, _L, _L, _L, _L, _P, _P, _I, _I, _I, _I, _I, _I,
                             _I, _F, _F, _P, _P, _SZ, _P]),
@@ -498,6 +502,39 @@ def paged_append(k_new, v_new, slot_map, pages, *, page_rows: int, stream=None):
            "fa_paged_append")
 
 
+def rope_append(q, k_new, v_new, q_out, positions, table, slot_map, pages, *, page_rows: int,
+                adjacent: bool = False, stream=None):
+    """fa_rope_append: q [T][Hq][hd] (or None) rotated into q_out (the same tensor: in
+    place), and k_new, rotated, and v_new [T][Hkv][hd] into the rows slot_map [T] int32;
+    positions and table as for rope."""
+    here = _here(k_new, "k_new")
+    code, dtype, shape = _type(k_new, "k_new"), k_new.dtype, k_new.shape
+    T, hkv, hd = shape
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    qp = qo = None
+    hq = qs = qos = 0
+    if q is not None:
+        _type(q, "q")
+        hq = q.shape[1]
+        qp, qs = _heads(q, "q", dtype, (T, hq, hd), here)
+        qo, qos = (qp, qs) if q_out is q else _heads(q_out, "q_out", dtype, (T, hq, hd), here)
+    kp, ks = _heads(k_new, "k_new", dtype, shape, here)
+    vp, vs = _heads(v_new, "v_new", dtype, shape, here)
+    where = positions.shape
+    axes = where[0] if len(where) == 2 else 1
+    if len(where) not in (1, 2) or where[-1] != T:
+        raise ValueError(f"positions must have shape (n_axes, {T}), got {tuple(where)}")
+    pairs = table.shape[0] if table.dim() else 0
+    pp, n_pages = _pages(pages, hkv, hd, page_rows, here)
+    _check(lib().fa_rope_append(
+        qp, qo, kp, vp, code, T, hq, hkv, hd, 2 * pairs, qs, qos, ks, vs,
+        _arg(positions, "positions", _I32, None, here), T, axes,
+        _arg(table, "table", _I32, (pairs, 4), here), adjacent,
+        _arg(slot_map, "slot_map", _I32, (T,), here), pp, n_pages, page_rows,
+        _raw_stream(stream, here)), "fa_rope_append")
+
+
 def paged_gather(pages, block_table, seq_lens, k_planes, v_planes, *, n_kv_heads: int,
                  head_dim: int, page_rows: int, max_seq: int, stream=None):
     """fa_paged_gather: rows 0 .. seq_lens[r]-1 of each request into KV_F16 planes
@@ -522,9 +559,10 @@ def paged_attn_workspace_bytes(head_dim: int) -> int:
 
 def paged_attn(q, out, cu_q, seq_lens, block_table, pages, *, n_kv_heads: int, page_rows: int,
                sink: int = 0, win: int = 0, scale: float = 0.0, lse=None, workspace,
-               stream=None):
+               stream=None, cap: float = 0.0, slopes=None):
     """fa_paged_attn: q, out [T][Hq][hd] (tokens may lie apart), cu_q [R + 1] and
-    seq_lens [R] int32, block_table [R][max_pages] int32, lse [Hq][T] fp32 or None."""
+    seq_lens [R] int32, block_table [R][max_pages] int32, lse [Hq][T] fp32 or None;
+    with a cap or slopes [Hq] fp32, fa_paged_attn_scored."""
     here = _here(q, "q")
     code, dtype, shape = _type(q, "q"), q.dtype, q.shape
     T, hq, hd = shape
@@ -533,12 +571,17 @@ def paged_attn(q, out, cu_q, seq_lens, block_table, pages, *, n_kv_heads: int, p
     op, os_ = _heads(out, "out", dtype, shape, here)
     pp, n_pages = _pages(pages, n_kv_heads, hd, page_rows, here)
     table, max_pages = _table(block_table, R, here)
-    _check(lib().fa_paged_attn(
-        qp, op, None if lse is None else _arg(lse, "lse", _F32, (hq, T), here), code, qs, os_,
-        _arg(cu_q, "cu_q", _I32, (R + 1,), here), _arg(seq_lens, "seq_lens", _I32, (R,), here),
-        table, max_pages, pp, n_pages, page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale,
-        _arg(workspace, "workspace", _U8, None, here), workspace.numel(),
-        _raw_stream(stream, here)), "fa_paged_attn")
+    head = (qp, op, None if lse is None else _arg(lse, "lse", _F32, (hq, T), here), code, qs, os_,
+            _arg(cu_q, "cu_q", _I32, (R + 1,), here), _arg(seq_lens, "seq_lens", _I32, (R,), here),
+            table, max_pages, pp, n_pages, page_rows, R, T, hq, n_kv_heads, hd, sink, win, scale)
+    tail = (_arg(workspace, "workspace", _U8, None, here), workspace.numel(),
+            _raw_stream(stream, here))
+    if cap == 0.0 and slopes is None:
+        _check(lib().fa_paged_attn(*head, *tail), "fa_paged_attn")
+    else:
+        _check(lib().fa_paged_attn_scored(
+            *head, cap, None if slopes is None else _arg(slopes, "slopes", _F32, (hq,), here),
+            *tail), "fa_paged_attn_scored")
 
 
 # -------------------------------------------------------- packed documents

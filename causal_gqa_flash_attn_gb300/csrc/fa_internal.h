@@ -169,12 +169,20 @@ struct PagedAppendArgs {
     unsigned *err;
 };
 cudaError_t launch_paged_append(const PagedAppendArgs &a, int dtype, int hd, cudaStream_t stream);
+// ---- rope_append.cu
+struct RopeAppendArgs {
+    RopeArgs rope;  // q alone
+    PagedAppendArgs append;
+};
+cudaError_t launch_rope_append(const RopeAppendArgs &b, cudaStream_t stream);
 struct PagedGatherArgs;
 cudaError_t launch_paged_gather(const PagedGatherArgs &a, int n_reqs, int hd,
                                 cudaStream_t stream);
 struct PagedAttnArgs;
 size_t paged_attn_ws_bytes(int hd);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream);
+// The same with capped scores, or scores that fall with the distance (paged_attn_scored.cu).
+cudaError_t launch_paged_attn_scored(const PagedAttnArgs &a, int dtype, int hd, cudaStream_t stream);
 
 // ---- decode.cu
 struct DecodeArgs {

@@ -1,6 +1,6 @@
 // paged_api.cu -- the C ABI of paged serving (include/fa.h): argument checks
-// and the arguments of the kernels in paged_plan.cu, rope.cu, paged_kv.cu and
-// paged_attn.cu. Host code only.
+// and the arguments of the kernels in paged_plan.cu, rope.cu, rope_append.cu,
+// paged_kv.cu and paged_attn.cuh. Host code only.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -62,6 +62,59 @@ fa::Pages make_pages(const void *pages, const int32_t *table, int n_pages, int n
     P.groups = page_rows / fa::kGroupRows;
     P.group_shift = page_shift(page_rows) - 4;
     return P;
+}
+
+fa_status paged_attn(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
+                     int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
+                     const int32_t *block_table, int max_pages, const void *pages, int n_pages,
+                     int page_rows, int n_reqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                     int head_dim, int sink, int win, float scale, float cap, const float *slopes,
+                     void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+    fa_status st = check_geometry(n_kv_heads, head_dim, page_rows);
+    if (st != FA_OK) return st;
+    if (n_q_heads < 1 || n_q_heads % n_kv_heads || !known_type(dtype) || n_reqs < 0 ||
+        n_tokens < 0 || sink < 0 || !good_pages(n_pages, max_pages, page_rows) ||
+        !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap) ||
+        !aligned4(slopes))
+        return FA_ERR_INVALID;
+    const int group = n_q_heads / n_kv_heads;
+    if (group > 16 || (group & (group - 1)) || n_reqs > 65536 || n_tokens > 1 << 26 ||
+        static_cast<long long>(n_tokens) * n_q_heads > 1 << 30)
+        return FA_ERR_UNSUPPORTED;
+    if (n_reqs == 0 || n_tokens == 0) return FA_OK;
+    if (!q || !out || !cu_q || !seq_lens || !block_table || !pages || !workspace ||
+        !aligned4(lse) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(block_table) ||
+        !aligned(pages, 16) || !aligned(workspace, 16) ||
+        !good_stride(q_stride, n_q_heads, head_dim, n_tokens) ||
+        !good_stride(out_stride, n_q_heads, head_dim, n_tokens) ||
+        !row_aligned(q, q_stride, dtype) || !row_aligned(out, out_stride, dtype))
+        return FA_ERR_INVALID;
+    if (workspace_bytes < fa::paged_attn_ws_bytes(head_dim)) return FA_ERR_WORKSPACE;
+    if (q == out) return FA_ERR_INVALID;  // a row's q may be read after its neighbours' out is written
+    fa::PagedAttnArgs a;
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.q_stride = q_stride;
+    a.out_stride = out_stride;
+    a.cu_q = cu_q;
+    a.seq_lens = seq_lens;
+    a.pages = make_pages(pages, block_table, n_pages, n_kv_heads, max_pages, page_rows);
+    a.n_reqs = n_reqs;
+    a.n_tokens = n_tokens;
+    a.n_q_heads = n_q_heads;
+    a.sink = sink;
+    a.win = win < 1 << 30 ? win : 1 << 30;  // the most rows a request can have
+    a.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
+    a.workspace = static_cast<uint8_t *>(workspace);
+    a.err = fa::device_error_word();
+    if (!a.err) return FA_ERR_CUDA;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (cap == 0.0f && !slopes) return from_cuda(fa::launch_paged_attn(a, dtype, head_dim, s));
+    a.cap = cap;
+    if (cap > 0.0f) a.cap_in = dtype == FA_T_F32 ? 1.0f / (cap * 1.4426950408889634f) : 2.0f / cap;
+    a.slopes = slopes;
+    return from_cuda(fa::launch_paged_attn_scored(a, dtype, head_dim, s));
 }
 
 }  // namespace
@@ -274,46 +327,77 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
                         int page_rows, int n_reqs, int n_tokens, int n_q_heads, int n_kv_heads,
                         int head_dim, int sink, int win, float scale, void *workspace,
                         size_t workspace_bytes, fa_stream_t stream) {
+    return paged_attn(q, out, lse, dtype, q_stride, out_stride, cu_q, seq_lens, block_table, max_pages, pages,
+                      n_pages, page_rows, n_reqs, n_tokens, n_q_heads, n_kv_heads, head_dim, sink, win, scale,
+                      0.0f, nullptr, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_paged_attn_scored(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
+                               int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
+                               const int32_t *block_table, int max_pages, const void *pages, int n_pages,
+                               int page_rows, int n_reqs, int n_tokens, int n_q_heads, int n_kv_heads,
+                               int head_dim, int sink, int win, float scale, float cap, const float *slopes,
+                               void *workspace, size_t workspace_bytes, fa_stream_t stream) {
+    return paged_attn(q, out, lse, dtype, q_stride, out_stride, cu_q, seq_lens, block_table, max_pages, pages,
+                      n_pages, page_rows, n_reqs, n_tokens, n_q_heads, n_kv_heads, head_dim, sink, win, scale,
+                      cap, slopes, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_rope_append(const void *q, void *q_out, const void *k_new, const void *v_new, int dtype, int n_tokens,
+                         int n_q_heads, int n_kv_heads, int head_dim, int rotary_dim, int64_t q_stride,
+                         int64_t q_out_stride, int64_t k_stride, int64_t v_stride, const int32_t *positions,
+                         int64_t pos_stride, int n_axes, const void *table, int adjacent, const int32_t *slot_map,
+                         void *pages, int n_pages, int page_rows, fa_stream_t stream) {
     fa_status st = check_geometry(n_kv_heads, head_dim, page_rows);
     if (st != FA_OK) return st;
-    if (n_q_heads < 1 || n_q_heads % n_kv_heads || !known_type(dtype) || n_reqs < 0 ||
-        n_tokens < 0 || sink < 0 || !good_pages(n_pages, max_pages, page_rows) ||
-        !(scale >= 0.0f) || !std::isfinite(scale))
+    if (!known_type(dtype) || n_tokens < 0 || n_q_heads < 0 || n_q_heads > 65536 || rotary_dim < 2 ||
+        rotary_dim % 2 || rotary_dim > head_dim || n_axes < 1 || n_axes > 8 || !good_pages(n_pages, 1, page_rows))
         return FA_ERR_INVALID;
-    const int group = n_q_heads / n_kv_heads;
-    if (group > 16 || (group & (group - 1)) || n_reqs > 65536 || n_tokens > 1 << 26 ||
-        static_cast<long long>(n_tokens) * n_q_heads > 1 << 30)
-        return FA_ERR_UNSUPPORTED;
-    if (n_reqs == 0 || n_tokens == 0) return FA_OK;
-    if (!q || !out || !cu_q || !seq_lens || !block_table || !pages || !workspace ||
-        !aligned4(lse) || !aligned4(cu_q) || !aligned4(seq_lens) || !aligned4(block_table) ||
-        !aligned(pages, 16) || !aligned(workspace, 16) ||
-        !good_stride(q_stride, n_q_heads, head_dim, n_tokens) ||
-        !good_stride(out_stride, n_q_heads, head_dim, n_tokens) ||
-        !row_aligned(q, q_stride, dtype) || !row_aligned(out, out_stride, dtype))
+    if (n_tokens > 1 << 30) return FA_ERR_UNSUPPORTED;  // a block's last token in 31 bits
+    if (n_tokens == 0) return FA_OK;
+    if (n_q_heads > 0 && (!q || !q_out || !good_stride(q_stride, n_q_heads, head_dim, n_tokens) ||
+                          !good_stride(q_out_stride, n_q_heads, head_dim, n_tokens) ||
+                          !row_aligned(q, q_stride, dtype) || !row_aligned(q_out, q_out_stride, dtype) ||
+                          (q == q_out && q_stride != q_out_stride)))
         return FA_ERR_INVALID;
-    if (workspace_bytes < fa::paged_attn_ws_bytes(head_dim)) return FA_ERR_WORKSPACE;
-    if (q == out) return FA_ERR_INVALID;  // a row's q may be read after its neighbours' out is written
-    fa::PagedAttnArgs a;
-    a.q = q;
-    a.out = out;
-    a.lse = lse;
-    a.q_stride = q_stride;
-    a.out_stride = out_stride;
-    a.cu_q = cu_q;
-    a.seq_lens = seq_lens;
-    a.pages = make_pages(pages, block_table, n_pages, n_kv_heads, max_pages, page_rows);
-    a.n_reqs = n_reqs;
-    a.n_tokens = n_tokens;
-    a.n_q_heads = n_q_heads;
-    a.sink = sink;
-    a.win = win < 1 << 30 ? win : 1 << 30;  // the most rows a request can have
-    a.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
-    a.workspace = static_cast<uint8_t *>(workspace);
-    a.err = fa::device_error_word();
-    if (!a.err) return FA_ERR_CUDA;
-    return from_cuda(
-        fa::launch_paged_attn(a, dtype, head_dim, reinterpret_cast<cudaStream_t>(stream)));
+    if (!k_new || !v_new || !slot_map || !pages || !aligned4(slot_map) || !aligned(pages, 16) ||
+        !good_stride(k_stride, n_kv_heads, head_dim, n_tokens) ||
+        !good_stride(v_stride, n_kv_heads, head_dim, n_tokens) || !row_aligned(k_new, k_stride, dtype) ||
+        !row_aligned(v_new, v_stride, dtype) || !positions || !table || !aligned4(positions) ||
+        !aligned(table, 16) || pos_stride < n_tokens || pos_stride > (int64_t(1) << 58))
+        return FA_ERR_INVALID;
+    fa::RopeAppendArgs b;
+    b.rope.q = n_q_heads ? q : nullptr;
+    b.rope.q_out = n_q_heads ? q_out : nullptr;
+    b.rope.k = b.rope.k_out = nullptr;
+    b.rope.q_stride = n_q_heads ? q_stride : 0;
+    b.rope.q_out_stride = n_q_heads ? q_out_stride : 0;
+    b.rope.k_stride = b.rope.k_out_stride = 0;
+    b.rope.dtype = dtype;
+    b.rope.n_tokens = n_tokens;
+    b.rope.n_q_heads = n_q_heads;
+    b.rope.n_kv_heads = 0;
+    b.rope.head_dim = head_dim;
+    b.rope.rotary_dim = rotary_dim;
+    b.rope.positions = positions;
+    b.rope.pos_stride = pos_stride;
+    b.rope.n_axes = n_axes;
+    b.rope.table = table;
+    b.rope.adjacent = adjacent != 0;
+    b.rope.inverse = false;
+    b.append.k = k_new;
+    b.append.v = v_new;
+    b.append.k_stride = k_stride;
+    b.append.v_stride = v_stride;
+    b.append.slot_map = slot_map;
+    b.append.n_tokens = n_tokens;
+    b.append.n_kv = n_kv_heads;
+    b.append.pages = static_cast<uint8_t *>(pages);
+    b.append.n_pages = n_pages;
+    b.append.page_shift = page_shift(page_rows);
+    b.rope.err = b.append.err = fa::device_error_word();
+    if (!b.rope.err) return FA_ERR_CUDA;
+    return from_cuda(fa::launch_rope_append(b, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

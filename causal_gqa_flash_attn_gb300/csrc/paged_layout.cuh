@@ -82,6 +82,10 @@ struct PagedAttnArgs {
     float scale;
     uint8_t *workspace;
     unsigned *err;
+    // fa_paged_attn_scored
+    float cap = 0.0f;     // 0: none
+    float cap_in = 0.0f;  // of a score in the exp2 domain: 2 / cap, or 1 / (cap log2 e) for fp32
+    const float *slopes = nullptr;
 };
 
 // Address of group `i` of kv head h of request r, or nullptr (flagged) where

@@ -1,0 +1,163 @@
+// rope_append.cu -- q and k rotated to their positions, and the new rows of K and
+// V written into 4-bit pages, in one pass (include/fa.h, fa_rope_append).
+//
+// What fa_rope and fa_paged_append do one after the other, bit for bit: k is rotated
+// in fp32, rounded to its type and encoded. The rotated k is not written and read
+// back, and a step has one launch less. A block takes a few tokens: their sines and
+// cosines into shared memory, the q heads through them as in rope.cu, then each row
+// of K and V by head_dim / 16 lanes as in paged_kv.cu, where a lane reads its 16
+// values of k and the 16 that they are paired with.
+#include <algorithm>
+
+#include "paged_encode.cuh"
+#include "rope_turn.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kItems = 1024;  // items (two vectors of q, or a lane's values of K and V) of a block
+
+template <typename T, int HD, int V, bool ADJ>
+__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppendArgs b) {
+    wait_for_stream();
+    const RopeArgs &a = b.rope;
+    const PagedAppendArgs &p = b.append;
+    extern __shared__ float4 rope_smem[];
+    constexpr int LANES = HD / 16;  // lanes of a row
+    const int rd = a.rotary_dim, half = rd / 2;
+    float *cs = reinterpret_cast<float *>(rope_smem);  // [tokens][half] cosines, then sines
+    float *sn = cs + a.tokens_per_block * half;
+    const int tok0 = blockIdx.x * a.tokens_per_block;
+    const int n_tok = min(a.tokens_per_block, a.n_tokens - tok0);
+    turn_table(a, half, tok0, n_tok, cs, sn);
+    if (blockIdx.x + blockIdx.y == 0)
+        for (int i = threadIdx.x; i < half; i += kRopeThreads)
+            if (load(static_cast<const uint4 *>(a.table) + i).z >= static_cast<unsigned>(a.n_axes))
+                flag_error(a.err, FA_ERRBIT_DEVICE);
+    __syncthreads();
+    // this block's heads: of the q heads, and then of the kv heads
+    const int h0 = blockIdx.y * a.heads_per_block, h1 = min(h0 + a.heads_per_block, a.n_q_heads + p.n_kv);
+    const int q_end = min(h1, a.n_q_heads);
+    // ---- K and V
+    const int kv0 = max(h0, a.n_q_heads) - a.n_q_heads, n_kv = h1 - a.n_q_heads - kv0;
+    if (n_kv > 0) {
+        const int rows = n_tok * n_kv, l = threadIdx.x & (LANES - 1);
+        for (int r0 = 0; r0 < rows; r0 += kRopeThreads / LANES) {
+            const int row = r0 + threadIdx.x / LANES;
+            const int tok = row < rows ? row / n_kv : 0, h = kv0 + (row < rows ? row - tok * n_kv : 0);
+            const int slot = row < rows ? load(p.slot_map + tok0 + tok) : -1;
+            const int page = slot >> p.page_shift;
+            const bool live = slot >= 0 && page < p.n_pages;
+            if (slot != -1 && !live && l == 0) flag_error(p.err, FA_ERRBIT_DEVICE);
+            float k[16] = {}, v[16] = {};
+            if (live) {
+                const long long t = tok0 + tok;
+                const T *src = static_cast<const T *>(p.v) + t * p.v_stride + static_cast<long long>(h) * HD;
+                load8<T>(src + 16 * l, v);
+                load8<T>(src + 16 * l + 8, v + 8);
+                src = static_cast<const T *>(p.k) + t * p.k_stride + static_cast<long long>(h) * HD;
+                load8<T>(src + 16 * l, k);
+                load8<T>(src + 16 * l + 8, k + 8);
+                const float *c = cs + tok * half, *s = sn + tok * half;
+                if (ADJ) {
+#pragma unroll
+                    for (int i = 0; i < 16; i += 2) {
+                        const int pair = 8 * l + i / 2;
+                        if (pair < half) {
+                            const float u0 = k[i], u1 = k[i + 1];
+                            k[i] = Conv<T>::get(Conv<T>::put(u0 * c[pair] - u1 * s[pair]));
+                            k[i + 1] = Conv<T>::get(Conv<T>::put(u0 * s[pair] + u1 * c[pair]));
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        const int d = 16 * l + e;
+                        if (half % 8 == 0) {  // eight values on one side
+                            if (d < rd) {
+                                const bool low = d < half;
+                                float o[8];
+                                load8<T>(src + (low ? d + half : d - half), o);
+                                const int pair = low ? d : d - half;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float u0 = low ? k[e + i] : o[i], u1 = low ? o[i] : k[e + i];
+                                    const float x = u0 * c[pair + i] - u1 * s[pair + i];
+                                    const float y = u0 * s[pair + i] + u1 * c[pair + i];
+                                    k[e + i] = Conv<T>::get(Conv<T>::put(low ? x : y));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                if (d + i >= rd) continue;
+                                const bool low = d + i < half;
+                                const float o = Conv<T>::get(src[low ? d + i + half : d + i - half]);
+                                const int pair = low ? d + i : d + i - half;
+                                const float u0 = low ? k[e + i] : o, u1 = low ? o : k[e + i];
+                                const float x = u0 * c[pair] - u1 * s[pair], y = u0 * s[pair] + u1 * c[pair];
+                                k[e + i] = Conv<T>::get(Conv<T>::put(low ? x : y));
+                            }
+                        }
+                    }
+                }
+            }
+            encode_rows<HD>(p, k, v, live, slot, page, h, l);
+        }
+    }
+    // ---- q
+    if (h0 < q_end) turn_heads<T, V, ADJ>(a, half, half / V, half / V + a.n_copy, tok0, n_tok, h0, q_end - h0, cs, sn);
+}
+
+template <typename T, int HD, int V>
+cudaError_t launch(RopeAppendArgs b, cudaStream_t stream) {
+    RopeArgs &a = b.rope;
+    const int rest = a.head_dim - a.rotary_dim, half = a.rotary_dim / 2;
+    a.n_copy = a.n_q_heads == 0 || a.q == a.q_out ? 0 : (rest / V + 1) / 2;
+    const int heads = a.n_q_heads + b.append.n_kv;
+    const long long row = static_cast<long long>(a.n_q_heads) * (half / V + a.n_copy) +
+                          static_cast<long long>(b.append.n_kv) * (HD / 16);  // items of a token
+    const int fit = std::min<int>(kRopeTokens, 48 * 1024 / (half * 8));
+    int tokens = static_cast<int>(std::min<long long>(fit, std::max<long long>(1, kItems / row)));
+    // few tokens: a block takes one, and the heads are split over blocks too, as in rope.cu
+    const int sms = device_sm_count();
+    if (a.n_tokens <= sms * tokens) tokens = std::max(1, a.n_tokens / sms);
+    a.tokens_per_block = tokens;
+    const int blocks = (a.n_tokens - 1) / tokens + 1;
+    int parts = std::max(1, std::min(sms * 2 / blocks, heads / 2));
+    a.heads_per_block = (heads + parts - 1) / parts;
+    parts = (heads + a.heads_per_block - 1) / a.heads_per_block;
+    const dim3 grid(static_cast<unsigned>(blocks), parts);
+    const size_t smem = static_cast<size_t>(tokens) * half * 8;
+    if (a.adjacent)
+        return launch_after(rope_append_kernel<T, HD, V, true>, grid, kRopeThreads, smem, stream, b);
+    return launch_after(rope_append_kernel<T, HD, V, false>, grid, kRopeThreads, smem, stream, b);
+}
+
+// q moves 16 bytes at a time where a vector of it lies on one side of its pairs.
+template <typename T, int HD>
+cudaError_t launch_hd(const RopeAppendArgs &b, cudaStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    return b.rope.rotary_dim / 2 % V == 0 ? launch<T, HD, V>(b, stream) : launch<T, HD, 1>(b, stream);
+}
+
+template <typename T>
+cudaError_t launch_type(const RopeAppendArgs &b, cudaStream_t stream) {
+    switch (b.rope.head_dim) {
+        case 64: return launch_hd<T, 64>(b, stream);
+        case 128: return launch_hd<T, 128>(b, stream);
+        default: return launch_hd<T, 256>(b, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeAppendArgs &b, cudaStream_t stream) {
+    switch (b.rope.dtype) {
+        case kTypeF32: return launch_type<float>(b, stream);
+        case kTypeF16: return launch_type<__half>(b, stream);
+        default: return launch_type<__nv_bfloat16>(b, stream);
+    }
+}
+
+}  // namespace fa

@@ -515,6 +515,20 @@ fa_status fa_paged_append(const void *k_new, const void *v_new, int dtype, int64
                           int n_pages, int n_kv_heads, int head_dim, int page_rows,
                           fa_stream_t stream);
 
+/* fa_rope of q into q_out and fa_paged_append of the rotated k and of v in one
+ * launch, with their bits: q rotated and rounded to dtype, k rotated, rounded to
+ * dtype and written into its pages with v. The k of the caller stays as it is. Arguments
+ * as for those two calls (one table for q and k; n_q_heads may be 0, q and q_out
+ * then NULL; q_out may be q), with rows 16-byte aligned throughout and head_dim, n_kv_heads and n_tokens
+ * limited as for fa_paged_append. A token without a slot (-1) has its q rotated and
+ * its k and v left out. */
+fa_status fa_rope_append(const void *q, void *q_out, const void *k_new, const void *v_new,
+                         int dtype, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim,
+                         int rotary_dim, int64_t q_stride, int64_t q_out_stride, int64_t k_stride,
+                         int64_t v_stride, const int32_t *positions, int64_t pos_stride,
+                         int n_axes, const void *table, int adjacent, const int32_t *slot_map,
+                         void *pages, int n_pages, int page_rows, fa_stream_t stream);
+
 /* Dequantise the pages of n_reqs requests into FA_KV_F16 planes (n_reqs
  * consecutive K planes and V planes of [n_kv_heads][max_seq][head_dim]), rows
  * 0 .. seq_lens[r] - 1 of each; the other rows stay as they are. Values past the
@@ -575,6 +589,20 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
                         int page_rows, int n_reqs, int n_tokens, int n_q_heads, int n_kv_heads,
                         int head_dim, int sink, int win, float scale, void *workspace,
                         size_t workspace_bytes, fa_stream_t stream);
+
+/* fa_paged_attn with changed scores: with s = scale * q . k, a key at distance d
+ * (the query's position less the key's) scores cap * tanh(s / cap) (s itself where
+ * cap is 0) - slopes[head] * d. cap >= 0; slopes is [n_q_heads] fp32 (device) or
+ * NULL. All else is as there, the log-sum-exp that of these scores; with neither cap nor
+ * slopes it is that call. The tanh costs scores of FA_T_F16 and FA_T_BF16 calls up to
+ * 2^-22 cap. */
+fa_status fa_paged_attn_scored(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
+                               int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
+                               const int32_t *block_table, int max_pages, const void *pages,
+                               int n_pages, int page_rows, int n_reqs, int n_tokens, int n_q_heads,
+                               int n_kv_heads, int head_dim, int sink, int win, float scale,
+                               float cap, const float *slopes, void *workspace,
+                               size_t workspace_bytes, fa_stream_t stream);
 
 /* -------------------------------------------------------- packed documents
  *
