@@ -18,7 +18,8 @@
 //   warp 0      copies: X1, X2 of a unit, then Y1, Y2 and (for dk, dv) L and D of the rows.
 //               Rows past a document's end become zeros where a product sums over them.
 //   warp 1      issues the products, so that those of one tile run under the weights of another:
-//               dk, dv: acc2(i), S(i + 1), acc1(i), T(i + 1); dq, dk: S(i + 1), acc1(i), T(i + 1).
+//               dk, dv: acc2(i), S(i + 1), acc1(i), T(i + 1); dq, dk: S(i + 1), acc1(i), T(i + 1); where
+//               TMEM has room for a second T it precedes acc1.
 //   warps 4-11  weights: a thread has one lane of TMEM and half of a tile's columns.
 //
 // binary16: P has 2^14 of its weight and t a power of two per document that brings the largest
@@ -50,9 +51,12 @@ struct GradCfg {
     static constexpr uint32_t OFF_Y2 = OFF_Y1 + N1 * YTILE;
     static constexpr uint32_t OFF_END = OFF_Y2 + N2 * YTILE;
     static constexpr uint32_t SMEM = (OFF_END + 1024 > 120u * 1024u) ? OFF_END + 1024 : 120u * 1024u;
-    // TMEM: S, T (dv alone: a second S), acc1, acc2
+    // TMEM: S, T (dv alone: a second S), acc1, acc2; a second T where there is room
+    static constexpr int NT = HAS_T && 256 + HD * (MODE == kGradKV ? 2 : 1) + 128 <= 512 ? 2 : 1;
     static constexpr uint32_t S_COL = 0, T_COL = 128;
     static constexpr uint32_t ACC1 = 256, ACC2 = MODE == kGradKV ? 256 + HD : 256;
+    static constexpr uint32_t T2_COL = 384;
+    __host__ __device__ static constexpr uint32_t t_col(int tt) { return NT == 2 && (tt & 1) ? T2_COL : T_COL; }
     static constexpr int THREADS = 384;
     static_assert(OFF_END <= 224u * 1024u, "shared memory");
 };
@@ -61,7 +65,7 @@ struct GradBars {
     uint64_t x_full, x_empty;
     uint64_t y1_full[3], y1_empty[3], y2_full[3], y2_empty[3];
     uint64_t l_full[2], l_empty[2];
-    uint64_t s_full[2], s_free, p_full[2], t_full, dt_full;
+    uint64_t s_full[2], s_free, p_full[2], t_full[2], dt_full[2];
     uint64_t acc_last, acc_free;
     uint64_t patch, drain;
     UnitRing ring;
@@ -78,6 +82,8 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ GradBars bars;
     __shared__ __align__(16) float stats[C::ROWS_STAY ? 1 : C::NL][2][C::ROWS_STAY ? 4 : BN];
+    // keys stay and scores fall with the distance: slopes of a tile's columns, and their tokens
+    __shared__ __align__(16) float bias_s[2][BIAS && !C::ROWS_STAY ? BN : 4];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -98,10 +104,10 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
             mbar_init(&bars.l_empty[s], 8);
             mbar_init(&bars.s_full[s], 1);
             mbar_init(&bars.p_full[s], 256);
+            mbar_init(&bars.t_full[s], 1);
+            mbar_init(&bars.dt_full[s], 256);
         }
         mbar_init(&bars.s_free, 256);
-        mbar_init(&bars.t_full, 1);
-        mbar_init(&bars.dt_full, 256);
         mbar_init(&bars.acc_last, 1);
         mbar_init(&bars.acc_free, 256);
         mbar_init(&bars.patch, 1);
@@ -149,6 +155,9 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
         t.count = last / step_tokens - t.lo + 1;
         return t;
     };
+    // Rows from the last to the first: without a window the units of a document begin with the same
+    // rows then, and find them in L2.
+    auto place = [&](const KeyTiles &t, int i) { return C::ROWS_STAY ? t.at(i) : t.lo + t.count - 1 - i; };
 
     if (warp == 0) {
         // ------------------------------------------------------------- copies
@@ -241,7 +250,7 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
             const int cnt = plan.count;
             bool more = false;
             for (int i = 0; i < cnt && ok; ++i) {
-                const int at = plan.at(i);
+                const int at = place(plan, i);
                 ok = load_y(t + i, at, u, true);
                 if (ok && !C::ROWS_STAY) ok = load_stats(t + i, at, u);
                 if (ok) ok = load_y(t + i, at, u, false);
@@ -313,8 +322,8 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                     const int tt = t + i, st = tt % N2;
                     if (!mbar_wait(&bars.y2_full[st], (tt / N2) & 1, abort, err)) return false;
                     tc_fence_after();
-                    scores(sX + C::XTILE, sY2 + st * C::YTILE, C::T_COL);
-                    tc_commit(&bars.t_full);
+                    scores(sX + C::XTILE, sY2 + st * C::YTILE, C::t_col(tt));
+                    tc_commit(&bars.t_full[tt % C::NT]);
                     if (!C::HAS_P) tc_commit(&bars.y2_empty[st]);
                     if (i == count - 1) tc_commit(&bars.x_empty);
                     return true;
@@ -333,9 +342,9 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 };
                 auto do_acc1 = [&](int i) {
                     const int tt = t + i, st = tt % N1;
-                    if (!mbar_wait(&bars.dt_full, tt & 1, abort, err) || !acc_ready(i)) return false;
+                    if (!mbar_wait(&bars.dt_full[tt % C::NT], (tt / C::NT) & 1, abort, err) || !acc_ready(i)) return false;
                     tc_fence_after();
-                    gather(C::T_COL, sY1 + st * C::YTILE, C::ACC1, i == 0);
+                    gather(C::t_col(tt), sY1 + st * C::YTILE, C::ACC1, i == 0);
                     tc_commit(&bars.y1_empty[st]);
                     return true;
                 };
@@ -349,8 +358,9 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                     for (int i = 0; i < count && ok; ++i) {
                         if (C::HAS_P) ok = do_acc2(i);
                         if (ok && i + 1 < count) ok = do_s(i + 1);
+                        if (C::NT == 2 && ok && i + 1 < count) ok = do_t(i + 1);
                         ok = ok && do_acc1(i);
-                        if (ok && i + 1 < count) ok = do_t(i + 1);
+                        if (C::NT == 1 && ok && i + 1 < count) ok = do_t(i + 1);
                     }
                 }
                 if (ok) tc_commit(&bars.acc_last);
@@ -387,6 +397,15 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 D = load(a.D + at);
                 if (BIAS) slope2 = load(a.slopes + head) * kPackedLog2e;
             }
+            if (BIAS && !C::ROWS_STAY) {  // (the slopes of the last unit have been used)
+                named_barrier_sync(1, 256);
+                const int c = threadIdx.x - 128;
+                if (c < BN) {
+                    bias_s[0][c] = load(a.slopes + (u.head << lg) + (c & (group - 1))) * kPackedLog2e;
+                    bias_s[1][c] = static_cast<float>(c >> lg);
+                }
+                named_barrier_sync(1, 256);
+            }
             float up = 1.0f;  // the document's power of two
             if (!BF16) {
                 const float b = 2.0f * sqrtf(__uint_as_float(load(a.doc_most + u.doc))) *
@@ -406,7 +425,7 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t scol = tmem + lane_base + C::S_COL + sb * 128 + half * HALF;
-                const uint32_t tcol = tmem + lane_base + C::T_COL + half * HALF;
+                const uint32_t tcol = tmem + lane_base + C::t_col(tt) + half * HALF;
                 uint32_t s[HALF];
 #pragma unroll
                 for (int c = 0; c < HALF; c += 32) tmem_ld32(scol + c, s + c);
@@ -423,15 +442,17 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 float far;         // query less key at column 0
                 const int c0 = half * HALF;
                 if (C::ROWS_STAY) {
-                    const int j0 = plan.at(i) * BN + c0, j1 = j0 + HALF - 1;
-                    whole = sees_all(u.p0, min(u.p0 + tile_tokens, u.len) - 1, j0, j1, u.prefix, a.sink, a.win);
+                    const int j0 = place(plan, i) * BN + c0, j1 = j0 + HALF - 1;
+                    whole = sees_all(u.p0, min(u.p0 + tile_tokens, u.len) - 1, j0, j1, u.prefix, a.sink, a.win) &&
+                            (!BIAS || j1 <= u.p0);
                     hi = mine - j0;
                     lo = a.win > 0 ? mine - a.win + 1 - j0 : 0;
                     first = max(u.prefix - j0, a.win > 0 ? min(a.sink - j0, hi + 1) : 0);
                     far = static_cast<float>(mine - j0);
                 } else {
-                    const int i0 = plan.at(i) * step_tokens, i1 = min(i0 + step_tokens, u.len) - 1;
-                    whole = sees_all(i0, i1, u.p0, min(u.p0 + 128, u.len) - 1, u.prefix, a.sink, a.win);
+                    const int i0 = place(plan, i) * step_tokens, i1 = min(i0 + step_tokens, u.len) - 1;
+                    const int j1 = min(u.p0 + 128, u.len) - 1;
+                    whole = sees_all(i0, i1, u.p0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= i0);
                     const bool always = mine < u.prefix;
                     lo = (min(max(always ? 0 : mine - i0, 0), BN) << lg) - c0;
                     hi = always || a.win <= 0 || mine < a.sink
@@ -442,40 +463,44 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 const float *Ls = stats[C::ROWS_STAY ? 0 : ls][0] + c0, *Ds = stats[C::ROWS_STAY ? 0 : ls][1] + c0;
                 // ---- P, and with capped scores P f' (in s)
                 uint32_t pk[HALF / 2];
+                auto weights = [&](auto masks) {
+                    constexpr bool MASK = decltype(masks)::value;
+                    const float base = slope2 * far;
 #pragma unroll
-                for (int c = 0; c < HALF; c += 4) {
-                    float4 lv = make_float4(L, L, L, L);
-                    if (!C::ROWS_STAY) lv = lds_f4(Ls + c);
-                    const float l4[4] = {lv.x, lv.y, lv.z, lv.w};
-                    float w[4];
+                    for (int c = 0; c < HALF; c += 4) {
+                        float4 lv = make_float4(L, L, L, L), sv, tv;
+                        if (!C::ROWS_STAY) {
+                            lv = lds_f4(Ls + c);
+                            if (BIAS) sv = lds_f4(bias_s[0] + c0 + c), tv = lds_f4(bias_s[1] + c0 + c);
+                        }
+                        const float l4[4] = {lv.x, lv.y, lv.z, lv.w};
+                        float w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float x = __uint_as_float(s[c + e]), down = 1.0f;
-                        if (CAP)
-                            x = capped(x, rule, &down) - l4[e];
-                        else
-                            x = fmaf(x, rule.a, -l4[e]);
-                        if (BIAS) {
-                            if (C::ROWS_STAY) {
-                                x = fmaf(-slope2, fabsf(far - static_cast<float>(c + e)), x);
-                            } else {
-                                const int row = c0 + c + e;
-                                const float sl = load(a.slopes + (u.head << lg) + (row & (group - 1))) * kPackedLog2e;
-                                x = fmaf(-sl, fabsf(far + static_cast<float>(row >> lg)), x);
+                        for (int e = 0; e < 4; ++e) {
+                            float x = __uint_as_float(s[c + e]), down = 1.0f, off = l4[e];
+                            if (BIAS && C::ROWS_STAY) {
+                                off += MASK ? slope2 * fabsf(far - static_cast<float>(c + e))
+                                            : fmaf(-slope2, static_cast<float>(c + e), base);
+                            } else if (BIAS) {
+                                const float s4[4] = {sv.x, sv.y, sv.z, sv.w}, t4[4] = {tv.x, tv.y, tv.z, tv.w};
+                                const float d = far + t4[e];
+                                off = fmaf(s4[e], MASK ? fabsf(d) : d, off);
                             }
+                            x = CAP ? capped(x, rule, &down) - off : fmaf(x, rule.a, -off);
+                            if (MASK) {
+                                const bool seen = (c + e < first) | ((c + e >= lo) & (c + e <= hi));
+                                x = seen ? x : -INFINITY;
+                            }
+                            w[e] = ex2(x);
+                            s[c + e] = __float_as_uint(CAP ? w[e] * down : w[e]);
                         }
-                        if (!whole) {
-                            const bool seen = (c + e < first) | ((c + e >= lo) & (c + e <= hi));
-                            x = seen ? x : -INFINITY;
+                        if (C::HAS_P) {
+                            pk[c / 2] = pack2<BF16>(w[0], w[1]);
+                            pk[c / 2 + 1] = pack2<BF16>(w[2], w[3]);
                         }
-                        w[e] = ex2(x);
-                        s[c + e] = __float_as_uint(CAP ? w[e] * down : w[e]);
                     }
-                    if (C::HAS_P) {
-                        pk[c / 2] = pack2<BF16>(w[0], w[1]);
-                        pk[c / 2 + 1] = pack2<BF16>(w[2], w[3]);
-                    }
-                }
+                };
+                if (whole) weights(std::false_type{}); else weights(std::true_type{});
                 if (C::HAS_P) {
                     if (HALF == 64) tmem_st32(scol, pk); else tmem_st16(scol, pk);
                     tmem_wait_st();
@@ -483,7 +508,7 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                     mbar_arrive(&bars.p_full[sb]);
                 }
                 if (C::HAS_T) {
-                    ok = mbar_wait(&bars.t_full, tt & 1, abort, err);
+                    ok = mbar_wait(&bars.t_full[tt % C::NT], (tt / C::NT) & 1, abort, err);
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     tc_fence_after();
@@ -493,27 +518,31 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                     tmem_wait_ld();
 #pragma unroll
                     for (int c = 0; c < HALF; c += 32) reg_fence32(d + c);
+                    auto slopes_of = [&](auto masks) {
+                        constexpr bool MASK = decltype(masks)::value;
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 4) {
-                        float4 dv = make_float4(D, D, D, D);
-                        if (!C::ROWS_STAY) dv = lds_f4(Ds + c);
-                        const float d4[4] = {dv.x, dv.y, dv.z, dv.w};
-                        float x[4];
+                        for (int c = 0; c < HALF; c += 4) {
+                            float4 dv = make_float4(D, D, D, D);
+                            if (!C::ROWS_STAY) dv = lds_f4(Ds + c);
+                            const float d4[4] = {dv.x, dv.y, dv.z, dv.w};
+                            float x[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float w = __uint_as_float(s[c + e]);
-                            x[e] = w * (__uint_as_float(d[c + e]) - d4[e]);
-                            if (!BF16) x[e] *= t_scale;
-                            // V past the document's end may hold anything
-                            if (C::ROWS_STAY && !whole) x[e] = w == 0.0f ? 0.0f : x[e];
+                            for (int e = 0; e < 4; ++e) {
+                                const float w = __uint_as_float(s[c + e]);
+                                x[e] = w * (__uint_as_float(d[c + e]) - d4[e]);
+                                if (!BF16) x[e] *= t_scale;
+                                if (MASK) x[e] = w == 0.0f ? 0.0f : x[e];
+                            }
+                            d[c / 2] = pack2<BF16>(x[0], x[1]);
+                            d[c / 2 + 1] = pack2<BF16>(x[2], x[3]);
                         }
-                        d[c / 2] = pack2<BF16>(x[0], x[1]);
-                        d[c / 2 + 1] = pack2<BF16>(x[2], x[3]);
-                    }
+                    };
+                    // V past the document's end may hold anything
+                    if (C::ROWS_STAY && !whole) slopes_of(std::true_type{}); else slopes_of(std::false_type{});
                     if (HALF == 64) tmem_st32(tcol, d); else tmem_st16(tcol, d);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(&bars.dt_full);
+                    mbar_arrive(&bars.dt_full[tt % C::NT]);
                 }
                 if (!C::ROWS_STAY) {
                     __syncwarp();
