@@ -38,27 +38,32 @@ struct GradCfg {
     static constexpr bool ROWS_STAY = MODE == kGradQ;  // the stationary tile is of query rows
     static constexpr bool HAS_T = MODE != kGradV, HAS_P = MODE == kGradKV || MODE == kGradV;
     static constexpr int BN = packed_grad_rows(HD);    // rows of a moving tile
-    static constexpr int HALF = BN / 2;                // columns of a thread
+    static constexpr int NWG = 2;                      // warpgroups that compute weights
+    static constexpr int PART = BN / NWG;              // columns of a thread
     static constexpr int NCHUNK = HD / 64;
     static constexpr uint32_t XCHUNK = 128 * 128, YCHUNK = BN * 128;
     static constexpr uint32_t XTILE = NCHUNK * XCHUNK, YTILE = NCHUNK * YCHUNK;
     static constexpr int NX = HAS_T ? 2 : 1;
     // Stages of Y1 and Y2: Y2 of dq and dk alone is read once, right after it lands.
-    static constexpr int N1 = HD == 64 ? 3 : 2;
+    static constexpr int N1 = HD == 256 ? 2 : 3;
     static constexpr int N2 = HD == 64 ? 3 : HD == 256 && HAS_T ? 1 : 2;
     static constexpr int NL = 2;                       // stages of L and D
     static constexpr uint32_t OFF_Y1 = NX * XTILE;
     static constexpr uint32_t OFF_Y2 = OFF_Y1 + N1 * YTILE;
     static constexpr uint32_t OFF_END = OFF_Y2 + N2 * YTILE;
-    static constexpr uint32_t SMEM = (OFF_END + 1024 > 120u * 1024u) ? OFF_END + 1024 : 120u * 1024u;
+    static constexpr uint32_t OFF_STATS = OFF_END;     // [NL][2][BN] L and D of a tile's rows
+    static constexpr uint32_t OFF_BIAS = OFF_STATS + (ROWS_STAY ? 0 : NL * 2 * BN * 4);  // [2][16]
+    static constexpr uint32_t OFF_BARS = OFF_BIAS + 128;
+    static constexpr uint32_t SMEM = OFF_BARS + 512 > 120u * 1024u ? OFF_BARS + 512 : 120u * 1024u;
     // TMEM: S, T (dv alone: a second S), acc1, acc2; a second T where there is room
     static constexpr int NT = HAS_T && 256 + HD * (MODE == kGradKV ? 2 : 1) + 128 <= 512 ? 2 : 1;
     static constexpr uint32_t S_COL = 0, T_COL = 128;
     static constexpr uint32_t ACC1 = 256, ACC2 = MODE == kGradKV ? 256 + HD : 256;
     static constexpr uint32_t T2_COL = 384;
     __host__ __device__ static constexpr uint32_t t_col(int tt) { return NT == 2 && (tt & 1) ? T2_COL : T_COL; }
-    static constexpr int THREADS = 384;
-    static_assert(OFF_END <= 224u * 1024u, "shared memory");
+    static constexpr int COMPUTE = 128 * NWG;          // threads that compute weights
+    static constexpr int THREADS = 128 + COMPUTE;
+    static_assert(SMEM <= 227u * 1024u, "shared memory");
 };
 
 struct GradBars {
@@ -72,23 +77,29 @@ struct GradBars {
     uint32_t tmem_base;
     int abort;
 };
+static_assert(sizeof(GradBars) <= 512, "barrier block");
 
 template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
-__global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_constant__ PackedGradArgs a) {
+__global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
+    packed_grad_kernel(const __grid_constant__ PackedGradArgs a) {
     using C = GradCfg<HD, MODE>;
-    constexpr int BN = C::BN, HALF = C::HALF, N1 = C::N1, N2 = C::N2;
+    constexpr int BN = C::BN, PART = C::PART, N1 = C::N1, N2 = C::N2;
     constexpr uint32_t IDESC_S = idesc_16<BF16>(128, BN, 0, 0);
     constexpr uint32_t IDESC_ACC = idesc_16<BF16>(128, HD, 0, 1);
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ GradBars bars;
-    __shared__ __align__(16) float stats[C::ROWS_STAY ? 1 : C::NL][2][C::ROWS_STAY ? 4 : BN];
-    // keys stay and scores fall with the distance: slopes of a tile's columns, and their tokens
-    __shared__ __align__(16) float bias_s[2][BIAS && !C::ROWS_STAY ? BN : 4];
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // All of it dynamic: the tiles, which want 1024 bytes, begin where a block's shared memory does.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    GradBars &bars = *reinterpret_cast<GradBars *>(smem + C::OFF_BARS);
+    float *stats = reinterpret_cast<float *>(smem + C::OFF_STATS);
+    // keys stay and scores fall with the distance: slopes of 16 columns, and their tokens (a group is 16
+    // heads at most, so that all columns repeat these)
+    float *bias_s = reinterpret_cast<float *>(smem + C::OFF_BIAS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &bars.abort;
     unsigned *err = a.err;
+    if (smem_u32(smem) & 1023u) {  // (never so far: nothing static lies before it)
+        flag_error(err, FA_ERRBIT_DEVICE);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(&bars.x_full, 1);
@@ -101,20 +112,20 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&bars.l_full[s], 1);
-            mbar_init(&bars.l_empty[s], 8);
+            mbar_init(&bars.l_empty[s], 4 * C::NWG);
             mbar_init(&bars.s_full[s], 1);
-            mbar_init(&bars.p_full[s], 256);
+            mbar_init(&bars.p_full[s], C::COMPUTE / 32);
             mbar_init(&bars.t_full[s], 1);
-            mbar_init(&bars.dt_full[s], 256);
+            mbar_init(&bars.dt_full[s], C::COMPUTE / 32);
         }
-        mbar_init(&bars.s_free, 256);
+        mbar_init(&bars.s_free, C::COMPUTE / 32);
         mbar_init(&bars.acc_last, 1);
-        mbar_init(&bars.acc_free, 256);
+        mbar_init(&bars.acc_free, C::COMPUTE / 32);
         mbar_init(&bars.patch, 1);
         mbar_init(&bars.drain, 1);
         for (int k = 0; k < kPackedRing; ++k) {
             mbar_init(&bars.ring.full[k], 1);
-            mbar_init(&bars.ring.empty[k], 1 + 8);
+            mbar_init(&bars.ring.empty[k], 1 + 4 * C::NWG);
         }
         bars.abort = 0;
         mbar_fence_init();
@@ -159,220 +170,238 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
     // rows then, and find them in L2.
     auto place = [&](const KeyTiles &t, int i) { return C::ROWS_STAY ? t.at(i) : t.lo + t.count - 1 - i; };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------- copies
-        const int units = *a.n_tiles * a.n_kv;
-        Arms x_arms, y1_arms[3], y2_arms[3], l_arms[2];
-        int patches = 0;
-        bool ok = true;
-        auto fetch = [&](int w, PackedTile *u) {
-            u->head = -1;
-            if (w >= units) return false;
-            *u = a.tiles[w / a.n_kv];
-            u->head = w % a.n_kv;
-            return true;
-        };
-        auto publish = [&](int j, const PackedTile &u) {
-            const int slot = j % kPackedRing;
-            if (j >= kPackedRing &&
-                !mbar_wait(&bars.ring.empty[slot], ((j / kPackedRing) - 1) & 1, abort, err))
-                return false;
-            if (lane == 0) {
-                bars.ring.unit[slot] = u;
-                mbar_arrive(&bars.ring.full[slot]);
-            }
-            return true;
-        };
-        // tokens from `tok` on: rows of the whole group, or keys
-        auto copy = [&](const CUtensorMap *map, uint8_t *dst, uint32_t chunk, uint64_t *bar, bool rows, int head,
-                        int tok) {
-            for (int c = 0; c < C::NCHUNK; ++c) {
-                if (rows)
-                    tma_load_4d(dst + c * chunk, map, bar, c * 64, 0, head, tok);
-                else
-                    tma_load_3d(dst + c * chunk, map, bar, c * 64, head, tok);
-            }
-        };
-        auto load_x = [&](int j, const PackedTile &u) {
-            if (j > 0 && !mbar_wait(&bars.x_empty, (j - 1) & 1, abort, err)) return false;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars.x_full, C::NX * C::XTILE);
-                copy(&a.x1, smem, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
-                if (C::NX == 2)
-                    copy(&a.x2, smem + C::XTILE, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
-            }
-            ++x_arms.n;
-            return true;
-        };
-        auto load_y = [&](int tt, int at, const PackedTile &u, bool first) {
-            const int n = first ? N1 : N2, st = tt % n;
-            uint64_t *full = first ? bars.y1_full : bars.y2_full, *empty = first ? bars.y1_empty : bars.y2_empty;
-            if (tt >= n && !mbar_wait(empty + st, ((tt / n) - 1) & 1, abort, err)) return false;
-            uint8_t *dst = smem + (first ? C::OFF_Y1 : C::OFF_Y2) + st * C::YTILE;
-            const int p = at * (C::ROWS_STAY ? BN : step_tokens);  // its first token's position
-            const int rows = min(BN, (u.len - p) << (C::ROWS_STAY ? 0 : lg));
-            // a product sums over the rows of this tile (or they meet weights that are not masked)
-            const bool patch = rows < BN && (first || !C::ROWS_STAY);
-            uint64_t *bar = patch ? &bars.patch : full + st;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, C::YTILE);
-                copy(first ? &a.y1 : &a.y2, dst, C::YCHUNK, bar, !C::ROWS_STAY, u.head, u.tok0 + p);
-            }
-            if (patch) {
-                if (!mbar_wait(bar, patches++ & 1, abort, err)) return false;
-                zero_rows(dst, C::NCHUNK, C::YCHUNK, rows, BN);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full + st);
-            }
-            if (first) ++y1_arms[st].n; else ++y2_arms[st].n;
-            return true;
-        };
-        auto load_stats = [&](int tt, int at, const PackedTile &u) {
-            const int st = tt % C::NL;
-            if (tt >= C::NL && !mbar_wait(&bars.l_empty[st], ((tt / C::NL) - 1) & 1, abort, err)) return false;
-            if (lane == 0) {
-                const size_t from = (static_cast<size_t>(u.head) * a.blocks + u.rb) * 128 + static_cast<size_t>(at) * BN;
-                mbar_arrive_expect_tx(&bars.l_full[st], 2 * BN * 4);
-                bulk_copy_g2s(stats[st][0], a.L + from, BN * 4, &bars.l_full[st]);
-                bulk_copy_g2s(stats[st][1], a.D + from, BN * 4, &bars.l_full[st]);
-            }
-            ++l_arms[st].n;
-            return true;
-        };
-        int t = 0, w = blockIdx.x;
-        PackedTile u, un;
-        bool have = fetch(w, &u);
-        ok = publish(0, u);
-        if (have && ok) ok = load_x(0, u);
-        for (int j = 0; have && ok; ++j) {
-            const KeyTiles plan = plan_of(u);
-            const int cnt = plan.count;
-            bool more = false;
-            for (int i = 0; i < cnt && ok; ++i) {
-                const int at = place(plan, i);
-                ok = load_y(t + i, at, u, true);
-                if (ok && !C::ROWS_STAY) ok = load_stats(t + i, at, u);
-                if (ok) ok = load_y(t + i, at, u, false);
-                if (ok && i == cnt - 1) {
-                    if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
-                    w = __shfl_sync(~0u, w, 0);
-                    more = fetch(w, &un);
-                }
-            }
-            t += cnt;
-            if (!ok) break;
-            ok = publish(j + 1, un);
-            have = more;
-            if (have && ok) ok = load_x(j + 1, un);
-            u = un;
-        }
-        if (!ok) {  // copies already issued land before the block exits
-            x_arms.drain(&bars.x_full);
-            for (int s = 0; s < 3; ++s) {
-                y1_arms[s].drain(&bars.y1_full[s]);
-                y2_arms[s].drain(&bars.y2_full[s]);
-                if (s < 2) l_arms[s].drain(&bars.l_full[s]);
-            }
-            if (patches) wait_out(&bars.patch, (patches - 1) & 1);
-        }
-    } else if (warp == 1) {
-        // ----------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t sX = smem_u32(smem), sY1 = smem_u32(smem + C::OFF_Y1), sY2 = smem_u32(smem + C::OFF_Y2);
-            // scores: X (128 rows) times a moving tile's rows, summed over head_dim
-            auto scores = [&](uint32_t x, uint32_t y, uint32_t col) {
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk)
-                    mma_ss(tmem + col, desc_sw128(x + (kk >> 2) * C::XCHUNK + (kk & 3) * 32, 16, 1024),
-                           desc_sw128(y + (kk >> 2) * C::YCHUNK + (kk & 3) * 32, 16, 1024), IDESC_S, kk > 0 ? 1u : 0u);
-            };
-            // weights in TMEM (each half of the columns where its threads wrote them) times the tile itself
-            auto gather = [&](uint32_t col, uint32_t y, uint32_t acc, bool first) {
-#pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk) {
-                    constexpr int per = HALF / 16;
-                    mma_ts(tmem + acc, tmem + col + (kk / per) * HALF + (kk % per) * 8,
-                           desc_sw128(y + kk * 2048, C::YCHUNK, 1024), IDESC_ACC, (!first || kk > 0) ? 1u : 0u);
-                }
-            };
-            int t = 0;
+    if (warp < 4) {
+        fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
+        if (warp == 0) {
+            // ------------------------------------------------------------- copies
+            const int units = *a.n_tiles * a.n_kv;
+            Arms x_arms, y1_arms[3], y2_arms[3], l_arms[2];
+            int patches = 0;
             bool ok = true;
-            PackedTile u;
-            for (int j = 0; ok && next_unit(j, &u); ++j) {
-                mbar_arrive(&bars.ring.empty[j % kPackedRing]);
-                const int count = plan_of(u).count;
-                if (!(ok = mbar_wait(&bars.x_full, j & 1, abort, err))) break;
-                tc_fence_after();
-                auto do_s = [&](int i) {
-                    const int tt = t + i, st = tt % N1;
-                    if (!mbar_wait(&bars.y1_full[st], (tt / N1) & 1, abort, err)) return false;
-                    // S is read whole: in the others its P was, or a product in between waited for it
-                    if (!C::HAS_P && tt > 0 && !mbar_wait(&bars.s_free, (tt - 1) & 1, abort, err)) return false;
-                    tc_fence_after();
-                    scores(sX, sY1 + st * C::YTILE, C::S_COL + (C::HAS_T ? 0 : (tt & 1) * 128));
-                    tc_commit(&bars.s_full[C::HAS_T ? 0 : tt & 1]);
-                    if (!C::HAS_T) {
-                        tc_commit(&bars.y1_empty[st]);
-                        if (i == count - 1) tc_commit(&bars.x_empty);
-                    }
-                    return true;
-                };
-                auto do_t = [&](int i) {
-                    const int tt = t + i, st = tt % N2;
-                    if (!mbar_wait(&bars.y2_full[st], (tt / N2) & 1, abort, err)) return false;
-                    tc_fence_after();
-                    scores(sX + C::XTILE, sY2 + st * C::YTILE, C::t_col(tt));
-                    tc_commit(&bars.t_full[tt % C::NT]);
-                    if (!C::HAS_P) tc_commit(&bars.y2_empty[st]);
-                    if (i == count - 1) tc_commit(&bars.x_empty);
-                    return true;
-                };
-                auto acc_ready = [&](int i) {
-                    return i > 0 || j == 0 || mbar_wait(&bars.acc_free, (j - 1) & 1, abort, err);
-                };
-                auto do_acc2 = [&](int i) {
-                    const int tt = t + i, st = tt % N2, b = C::HAS_T ? 0 : tt & 1;
-                    if (!mbar_wait(&bars.p_full[b], (C::HAS_T ? tt : tt >> 1) & 1, abort, err) || !acc_ready(i)) return false;
-                    if (!C::HAS_T && !mbar_wait(&bars.y2_full[st], (tt / N2) & 1, abort, err)) return false;
-                    tc_fence_after();
-                    gather(C::S_COL + b * 128, sY2 + st * C::YTILE, C::ACC2, i == 0);
-                    tc_commit(&bars.y2_empty[st]);
-                    return true;
-                };
-                auto do_acc1 = [&](int i) {
-                    const int tt = t + i, st = tt % N1;
-                    if (!mbar_wait(&bars.dt_full[tt % C::NT], (tt / C::NT) & 1, abort, err) || !acc_ready(i)) return false;
-                    tc_fence_after();
-                    gather(C::t_col(tt), sY1 + st * C::YTILE, C::ACC1, i == 0);
-                    tc_commit(&bars.y1_empty[st]);
-                    return true;
-                };
-                if (MODE == kGradV) {
-                    for (int i = 0; i <= count && ok; ++i) {
-                        if (i < count) ok = do_s(i);
-                        if (ok && i > 0) ok = do_acc2(i - 1);
-                    }
-                } else {
-                    ok = do_s(0) && do_t(0);
-                    for (int i = 0; i < count && ok; ++i) {
-                        if (C::HAS_P) ok = do_acc2(i);
-                        if (ok && i + 1 < count) ok = do_s(i + 1);
-                        if (C::NT == 2 && ok && i + 1 < count) ok = do_t(i + 1);
-                        ok = ok && do_acc1(i);
-                        if (C::NT == 1 && ok && i + 1 < count) ok = do_t(i + 1);
+            auto fetch = [&](int w, PackedTile *u) {
+                u->head = -1;
+                if (w >= units) return false;
+                *u = a.tiles[w / a.n_kv];
+                u->head = w % a.n_kv;
+                return true;
+            };
+            auto publish = [&](int j, const PackedTile &u) {
+                const int slot = j % kPackedRing;
+                if (j >= kPackedRing &&
+                    !mbar_wait(&bars.ring.empty[slot], ((j / kPackedRing) - 1) & 1, abort, err))
+                    return false;
+                if (lane == 0) {
+                    bars.ring.unit[slot] = u;
+                    mbar_arrive(&bars.ring.full[slot]);
+                }
+                return true;
+            };
+            // tokens from `tok` on: rows of the whole group, or keys
+            auto copy = [&](const CUtensorMap *map, uint8_t *dst, uint32_t chunk, uint64_t *bar, bool rows, int head,
+                            int tok) {
+                for (int c = 0; c < C::NCHUNK; ++c) {
+                    if (rows)
+                        tma_load_4d(dst + c * chunk, map, bar, c * 64, 0, head, tok);
+                    else
+                        tma_load_3d(dst + c * chunk, map, bar, c * 64, head, tok);
+                }
+            };
+            auto load_x = [&](int j, const PackedTile &u) {
+                if (j > 0 && !mbar_wait(&bars.x_empty, (j - 1) & 1, abort, err)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.x_full, C::NX * C::XTILE);
+                    copy(&a.x1, smem, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                    if (C::NX == 2)
+                        copy(&a.x2, smem + C::XTILE, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                }
+                ++x_arms.n;
+                return true;
+            };
+            auto load_y = [&](int tt, int at, const PackedTile &u, bool first) {
+                const int n = first ? N1 : N2, st = tt % n;
+                uint64_t *full = first ? bars.y1_full : bars.y2_full, *empty = first ? bars.y1_empty : bars.y2_empty;
+                if (tt >= n && !mbar_wait(empty + st, ((tt / n) - 1) & 1, abort, err)) return false;
+                uint8_t *dst = smem + (first ? C::OFF_Y1 : C::OFF_Y2) + st * C::YTILE;
+                const int p = at * (C::ROWS_STAY ? BN : step_tokens);  // its first token's position
+                const int rows = min(BN, (u.len - p) << (C::ROWS_STAY ? 0 : lg));
+                // a product sums over the rows of this tile (or they meet weights that are not masked)
+                const bool patch = rows < BN && (first || !C::ROWS_STAY);
+                uint64_t *bar = patch ? &bars.patch : full + st;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, C::YTILE);
+                    copy(first ? &a.y1 : &a.y2, dst, C::YCHUNK, bar, !C::ROWS_STAY, u.head, u.tok0 + p);
+                }
+                if (patch) {
+                    if (!mbar_wait(bar, patches++ & 1, abort, err)) return false;
+                    zero_rows(dst, C::NCHUNK, C::YCHUNK, rows, BN);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full + st);
+                }
+                if (first) ++y1_arms[st].n; else ++y2_arms[st].n;
+                return true;
+            };
+            auto load_stats = [&](int tt, int at, const PackedTile &u) {
+                const int st = tt % C::NL;
+                if (tt >= C::NL && !mbar_wait(&bars.l_empty[st], ((tt / C::NL) - 1) & 1, abort, err)) return false;
+                if (lane == 0) {
+                    const size_t from = (static_cast<size_t>(u.head) * a.blocks + u.rb) * 128 + static_cast<size_t>(at) * BN;
+                    mbar_arrive_expect_tx(&bars.l_full[st], 2 * BN * 4);
+                    bulk_copy_g2s(stats + st * 2 * BN, a.L + from, BN * 4, &bars.l_full[st]);
+                    bulk_copy_g2s(stats + st * 2 * BN + BN, a.D + from, BN * 4, &bars.l_full[st]);
+                }
+                ++l_arms[st].n;
+                return true;
+            };
+            int t = 0, w = blockIdx.x;
+            PackedTile u, un;
+            bool have = fetch(w, &u);
+            ok = publish(0, u);
+            if (have && ok) ok = load_x(0, u);
+            for (int j = 0; have && ok; ++j) {
+                const KeyTiles plan = plan_of(u);
+                const int cnt = plan.count;
+                bool more = false;
+                for (int i = 0; i < cnt && ok; ++i) {
+                    const int at = place(plan, i);
+                    ok = load_y(t + i, at, u, true);
+                    if (ok && !C::ROWS_STAY) ok = load_stats(t + i, at, u);
+                    if (ok) ok = load_y(t + i, at, u, false);
+                    if (ok && i == cnt - 1) {
+                        if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                        w = __shfl_sync(~0u, w, 0);
+                        more = fetch(w, &un);
                     }
                 }
-                if (ok) tc_commit(&bars.acc_last);
-                t += count;
+                t += cnt;
+                if (!ok) break;
+                ok = publish(j + 1, un);
+                have = more;
+                if (have && ok) ok = load_x(j + 1, un);
+                u = un;
             }
-            // every product issued completes before TMEM is released
-            tc_commit(&bars.drain);
-            wait_out(&bars.drain, 0);
+            if (!ok) {  // copies already issued land before the block exits
+                x_arms.drain(&bars.x_full);
+                for (int s = 0; s < 3; ++s) {
+                    y1_arms[s].drain(&bars.y1_full[s]);
+                    y2_arms[s].drain(&bars.y2_full[s]);
+                    if (s < 2) l_arms[s].drain(&bars.l_full[s]);
+                }
+                if (patches) wait_out(&bars.patch, (patches - 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ----------------------------------------------------------- products
+            {
+                const bool one = elect_lane();
+                const uint32_t tmem = uniform(static_cast<int>(bars.tmem_base));
+                // descriptors of the tiles' beginnings: an offset is added to their address field
+                const uint64_t x1 = desc_sw128(smem_u32(smem), 16, 1024), x2 = x1 + (C::XTILE >> 4);
+                const uint64_t y1 = desc_sw128(smem_u32(smem + C::OFF_Y1), 16, 1024);   // rows as they lie
+                const uint64_t y2 = desc_sw128(smem_u32(smem + C::OFF_Y2), 16, 1024);
+                const uint64_t g1 = desc_sw128(smem_u32(smem + C::OFF_Y1), C::YCHUNK, 1024);  // dims as columns
+                const uint64_t g2 = desc_sw128(smem_u32(smem + C::OFF_Y2), C::YCHUNK, 1024);
+                constexpr uint32_t STAGE = C::YTILE >> 4;
+                // scores: X (128 rows) times a moving tile's rows, summed over head_dim
+                auto scores = [&](uint64_t x, uint64_t y, uint32_t col) {
+                    if (one)
+#pragma unroll
+                        for (int kk = 0; kk < HD / 16; ++kk)
+                            mma_ss(tmem + col, x + (((kk >> 2) * C::XCHUNK + (kk & 3) * 32) >> 4),
+                                   y + (((kk >> 2) * C::YCHUNK + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+                };
+                // weights in TMEM (a part of the columns where its threads wrote them) times the tile itself
+                auto gather = [&](uint32_t col, uint64_t y, uint32_t acc, bool first) {
+                    constexpr int per = PART / 16;
+                    if (one)
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            mma_ts(tmem + acc, tmem + col + (kk / per) * PART + (kk % per) * 8, y + (kk * 2048 >> 4),
+                                   IDESC_ACC, (!first || kk > 0) ? 1u : 0u);
+                };
+                auto wait = [&](uint64_t *bar, uint32_t parity) { return uniform(mbar_wait(bar, parity, abort, err)); };
+                auto commit = [&](uint64_t *bar) {
+                    if (one) tc_commit(bar);
+                };
+                int t = 0;
+                bool ok = true;
+                PackedTile u;
+                for (int j = 0; ok && uniform(next_unit(j, &u)); ++j) {
+                    const int count = uniform(plan_of(u).count);
+                    warp_arrive(&bars.ring.empty[j % kPackedRing]);
+                    if (!(ok = wait(&bars.x_full, j & 1))) break;
+                    tc_fence_after();
+                    auto do_s = [&](int i) {
+                        const int tt = t + i, st = tt % N1;
+                        if (!wait(&bars.y1_full[st], (tt / N1) & 1)) return false;
+                        // S is read whole: in the others its P was, or a product in between waited for it
+                        if (!C::HAS_P && tt > 0 && !wait(&bars.s_free, (tt - 1) & 1)) return false;
+                        tc_fence_after();
+                        scores(x1, y1 + st * STAGE, C::S_COL + (C::HAS_T ? 0 : (tt & 1) * 128));
+                        commit(&bars.s_full[C::HAS_T ? 0 : tt & 1]);
+                        if (!C::HAS_T) {
+                            commit(&bars.y1_empty[st]);
+                            if (i == count - 1) commit(&bars.x_empty);
+                        }
+                        return true;
+                    };
+                    auto do_t = [&](int i) {
+                        const int tt = t + i, st = tt % N2;
+                        if (!wait(&bars.y2_full[st], (tt / N2) & 1)) return false;
+                        tc_fence_after();
+                        scores(x2, y2 + st * STAGE, C::t_col(tt));
+                        commit(&bars.t_full[tt % C::NT]);
+                        if (!C::HAS_P) commit(&bars.y2_empty[st]);
+                        if (i == count - 1) commit(&bars.x_empty);
+                        return true;
+                    };
+                    auto acc_ready = [&](int i) {
+                        return i > 0 || j == 0 || wait(&bars.acc_free, (j - 1) & 1);
+                    };
+                    auto do_acc2 = [&](int i) {
+                        const int tt = t + i, st = tt % N2, b = C::HAS_T ? 0 : tt & 1;
+                        if (!wait(&bars.p_full[b], (C::HAS_T ? tt : tt >> 1) & 1) || !acc_ready(i)) return false;
+                        if (!C::HAS_T && !wait(&bars.y2_full[st], (tt / N2) & 1)) return false;
+                        tc_fence_after();
+                        gather(C::S_COL + b * 128, g2 + st * STAGE, C::ACC2, i == 0);
+                        commit(&bars.y2_empty[st]);
+                        return true;
+                    };
+                    auto do_acc1 = [&](int i) {
+                        const int tt = t + i, st = tt % N1;
+                        if (!wait(&bars.dt_full[tt % C::NT], (tt / C::NT) & 1) || !acc_ready(i)) return false;
+                        tc_fence_after();
+                        gather(C::t_col(tt), g1 + st * STAGE, C::ACC1, i == 0);
+                        commit(&bars.y1_empty[st]);
+                        return true;
+                    };
+                    if (MODE == kGradV) {
+                        for (int i = 0; i <= count && ok; ++i) {
+                            if (i < count) ok = do_s(i);
+                            if (ok && i > 0) ok = do_acc2(i - 1);
+                        }
+                    } else {
+                        ok = do_s(0) && do_t(0);
+                        for (int i = 0; i < count && ok; ++i) {
+                            if (C::HAS_P) ok = do_acc2(i);
+                            if (ok && i + 1 < count) ok = do_s(i + 1);
+                            if (C::NT == 2 && ok && i + 1 < count) ok = do_t(i + 1);
+                            ok = ok && do_acc1(i);
+                            if (C::NT == 1 && ok && i + 1 < count) ok = do_t(i + 1);
+                        }
+                    }
+                    if (ok) commit(&bars.acc_last);
+                    t += count;
+                }
+                // every product issued completes before TMEM is released
+                commit(&bars.drain);
+                wait_out(&bars.drain, 0);
+                __syncwarp();
+            }
         }
-    } else if (warp >= 4) {
+    } else {
+        more_registers<216>();
         // -------------------------------------------------- weights and output
-        const int half = (warp - 4) >> 2;           // this thread's half of a tile's columns
+        const int part = (warp - 4) >> 2;           // this thread's part of a tile's columns
         const int r = threadIdx.x & 127;            // its lane of TMEM: row of the stationary tile
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int group = 1 << lg;
@@ -395,16 +424,16 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                                   (static_cast<size_t>(u.p0) << lg) + r;
                 L = load(a.L + at);
                 D = load(a.D + at);
-                if (BIAS) slope2 = load(a.slopes + head) * kPackedLog2e;
+                if (BIAS) slope2 = load(a.slopes + head) * -kPackedLog2e;
             }
             if (BIAS && !C::ROWS_STAY) {  // (the slopes of the last unit have been used)
-                named_barrier_sync(1, 256);
+                named_barrier_sync(1, C::COMPUTE);
                 const int c = threadIdx.x - 128;
-                if (c < BN) {
-                    bias_s[0][c] = load(a.slopes + (u.head << lg) + (c & (group - 1))) * kPackedLog2e;
-                    bias_s[1][c] = static_cast<float>(c >> lg);
+                if (c < 16) {
+                    bias_s[c] = load(a.slopes + (u.head << lg) + (c & (group - 1))) * -kPackedLog2e;
+                    bias_s[16 + c] = static_cast<float>(c >> lg);
                 }
-                named_barrier_sync(1, 256);
+                named_barrier_sync(1, C::COMPUTE);
             }
             float up = 1.0f;  // the document's power of two
             if (!BF16) {
@@ -424,25 +453,23 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t scol = tmem + lane_base + C::S_COL + sb * 128 + half * HALF;
-                const uint32_t tcol = tmem + lane_base + C::t_col(tt) + half * HALF;
-                uint32_t s[HALF];
-#pragma unroll
-                for (int c = 0; c < HALF; c += 32) tmem_ld32(scol + c, s + c);
+                const uint32_t scol = tmem + lane_base + C::S_COL + sb * 128 + part * PART;
+                const uint32_t tcol = tmem + lane_base + C::t_col(tt) + part * PART;
+                uint32_t s[PART];
+                tmem_ld<PART>(scol, s);
                 tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < HALF; c += 32) reg_fence32(s + c);
+                reg_fence<PART>(s);
                 if (!C::HAS_P) {  // S may be overwritten
                     tc_fence_before();
-                    mbar_arrive(&bars.s_free);
+                    warp_arrive(&bars.s_free);
                 }
-                // ---- what is seen of this half: columns [lo, hi], and those below `first`
+                // ---- what is seen of this part: columns [lo, hi], and those below `first`
                 int first = 0, lo, hi;
                 bool whole;
                 float far;         // query less key at column 0
-                const int c0 = half * HALF;
+                const int c0 = part * PART;
                 if (C::ROWS_STAY) {
-                    const int j0 = place(plan, i) * BN + c0, j1 = j0 + HALF - 1;
+                    const int j0 = place(plan, i) * BN + c0, j1 = j0 + PART - 1;
                     whole = sees_all(u.p0, min(u.p0 + tile_tokens, u.len) - 1, j0, j1, u.prefix, a.sink, a.win) &&
                             (!BIAS || j1 <= u.p0);
                     hi = mine - j0;
@@ -460,93 +487,108 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
                              : (max(min(mine + a.win - 1 - i0, BN), -1) + 1 << lg) - 1 - c0;
                     far = static_cast<float>(i0 - mine);
                 }
-                const float *Ls = stats[C::ROWS_STAY ? 0 : ls][0] + c0, *Ds = stats[C::ROWS_STAY ? 0 : ls][1] + c0;
-                // ---- P, and with capped scores P f' (in s)
-                uint32_t pk[HALF / 2];
+                const float *Ls = stats + ls * 2 * BN + c0, *Ds = Ls + BN;
+                // ---- P, and with capped scores P f' / 4 (in s)
+                uint32_t pk[PART / 2];
                 auto weights = [&](auto masks) {
                     constexpr bool MASK = decltype(masks)::value;
-                    const float base = slope2 * far;
+                    float far_at[(PART + 15) / 16];
 #pragma unroll
-                    for (int c = 0; c < HALF; c += 4) {
+                    for (int c = 0; c < (PART + 15) / 16; ++c)
+                        far_at[c] = far + static_cast<float>((c0 + 16 * c) >> lg);
+#pragma unroll
+                    for (int c = 0; c < PART; c += 4) {
                         float4 lv = make_float4(L, L, L, L), sv, tv;
                         if (!C::ROWS_STAY) {
                             lv = lds_f4(Ls + c);
-                            if (BIAS) sv = lds_f4(bias_s[0] + c0 + c), tv = lds_f4(bias_s[1] + c0 + c);
+                            if (BIAS) sv = lds_f4(bias_s + (c & 15)), tv = lds_f4(bias_s + 16 + (c & 15));
                         }
-                        const float l4[4] = {lv.x, lv.y, lv.z, lv.w};
-                        float w[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float x = __uint_as_float(s[c + e]), down = 1.0f, off = l4[e];
-                            if (BIAS && C::ROWS_STAY) {
-                                off += MASK ? slope2 * fabsf(far - static_cast<float>(c + e))
-                                            : fmaf(-slope2, static_cast<float>(c + e), base);
-                            } else if (BIAS) {
-                                const float s4[4] = {sv.x, sv.y, sv.z, sv.w}, t4[4] = {tv.x, tv.y, tv.z, tv.w};
-                                const float d = far + t4[e];
-                                off = fmaf(s4[e], MASK ? fabsf(d) : d, off);
+                        for (int e = 0; e < 4; e += 2) {
+                            Two x = two(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]));
+                            Two off = e ? two(lv.z, lv.w) : two(lv.x, lv.y), down;
+                            if (BIAS) {  // (slopes are negative here)
+                                Two d, sl = two(slope2);
+                                if (C::ROWS_STAY) {
+                                    d = two(far) + two(-static_cast<float>(c + e), -static_cast<float>(c + e + 1));
+                                } else {
+                                    d = two(far_at[c / 16]) + (e ? two(tv.z, tv.w) : two(tv.x, tv.y));
+                                    sl = e ? two(sv.z, sv.w) : two(sv.x, sv.y);
+                                }
+                                if (MASK) {
+                                    const float2 f = both(d);
+                                    d = two(fabsf(f.x), fabsf(f.y));
+                                }
+                                off = fma2(sl, d, off);
                             }
-                            x = CAP ? capped(x, rule, &down) - off : fmaf(x, rule.a, -off);
+                            if (CAP) {
+                                const Two q = cap_r(x, rule);
+                                down = cap_slope(q);
+                                x = capped(q, rule) + off;
+                            } else {
+                                x = fma2(x, two(rule.a), off);
+                            }
+                            float2 f = both(x);
                             if (MASK) {
-                                const bool seen = (c + e < first) | ((c + e >= lo) & (c + e <= hi));
-                                x = seen ? x : -INFINITY;
+                                const int k = c + e;
+                                if (!((k < first) | ((k >= lo) & (k <= hi)))) f.x = -INFINITY;
+                                if (!((k + 1 < first) | ((k + 1 >= lo) & (k + 1 <= hi)))) f.y = -INFINITY;
                             }
-                            w[e] = ex2(x);
-                            s[c + e] = __float_as_uint(CAP ? w[e] * down : w[e]);
-                        }
-                        if (C::HAS_P) {
-                            pk[c / 2] = pack2<BF16>(w[0], w[1]);
-                            pk[c / 2 + 1] = pack2<BF16>(w[2], w[3]);
+                            f = make_float2(ex2(f.x), ex2(f.y));
+                            if (C::HAS_P) pk[(c + e) / 2] = pack2<BF16>(f.x, f.y);
+                            if (CAP) f = both(two(f.x, f.y) * down);
+                            s[c + e] = __float_as_uint(f.x);
+                            s[c + e + 1] = __float_as_uint(f.y);
                         }
                     }
                 };
                 if (whole) weights(std::false_type{}); else weights(std::true_type{});
                 if (C::HAS_P) {
-                    if (HALF == 64) tmem_st32(scol, pk); else tmem_st16(scol, pk);
+                    tmem_st<PART / 2>(scol, pk);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(&bars.p_full[sb]);
+                    warp_arrive(&bars.p_full[sb]);
                 }
                 if (C::HAS_T) {
                     ok = mbar_wait(&bars.t_full[tt % C::NT], (tt / C::NT) & 1, abort, err);
                     ok = __all_sync(~0u, ok);
                     if (!ok) break;
                     tc_fence_after();
-                    uint32_t d[HALF];
-#pragma unroll
-                    for (int c = 0; c < HALF; c += 32) tmem_ld32(tcol + c, d + c);
+                    uint32_t d[PART];
+                    tmem_ld<PART>(tcol, d);
                     tmem_wait_ld();
-#pragma unroll
-                    for (int c = 0; c < HALF; c += 32) reg_fence32(d + c);
+                    reg_fence<PART>(d);
                     auto slopes_of = [&](auto masks) {
                         constexpr bool MASK = decltype(masks)::value;
 #pragma unroll
-                        for (int c = 0; c < HALF; c += 4) {
+                        for (int c = 0; c < PART; c += 4) {
                             float4 dv = make_float4(D, D, D, D);
                             if (!C::ROWS_STAY) dv = lds_f4(Ds + c);
-                            const float d4[4] = {dv.x, dv.y, dv.z, dv.w};
-                            float x[4];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float w = __uint_as_float(s[c + e]);
-                                x[e] = w * (__uint_as_float(d[c + e]) - d4[e]);
-                                if (!BF16) x[e] *= t_scale;
-                                if (MASK) x[e] = w == 0.0f ? 0.0f : x[e];
+                            for (int e = 0; e < 4; e += 2) {
+                                const Two w = two(__uint_as_float(s[c + e]), __uint_as_float(s[c + e + 1]));
+                                Two x = two(__uint_as_float(d[c + e]), __uint_as_float(d[c + e + 1])) +
+                                        (e ? two(dv.z, dv.w) : two(dv.x, dv.y));
+                                x = x * w;
+                                if (!BF16) x = x * two(t_scale);
+                                float2 f = both(x);
+                                if (MASK) {
+                                    if (s[c + e] == 0u) f.x = 0.0f;
+                                    if (s[c + e + 1] == 0u) f.y = 0.0f;
+                                }
+                                d[(c + e) / 2] = pack2<BF16>(f.x, f.y);
                             }
-                            d[c / 2] = pack2<BF16>(x[0], x[1]);
-                            d[c / 2 + 1] = pack2<BF16>(x[2], x[3]);
                         }
                     };
                     // V past the document's end may hold anything
                     if (C::ROWS_STAY && !whole) slopes_of(std::true_type{}); else slopes_of(std::false_type{});
-                    if (HALF == 64) tmem_st32(tcol, d); else tmem_st16(tcol, d);
+                    tmem_st<PART / 2>(tcol, d);
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(&bars.dt_full[tt % C::NT]);
+                    warp_arrive(&bars.dt_full[tt % C::NT]);
                 }
                 if (!C::ROWS_STAY) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars.l_empty[ls]);
+                    warp_arrive(&bars.l_empty[ls]);
                 }
             }
             if (!ok) break;
@@ -556,35 +598,35 @@ __global__ void __launch_bounds__(384, 1) packed_grad_kernel(const __grid_consta
             if (!ok) break;
             tc_fence_after();
             const bool live = mine < u.len;
-            // the first half of the threads stores dk and the other dv, or each half its columns
+            // half of the threads store dk and half dv, or all of them the one gradient
             constexpr bool BOTH = MODE == kGradKV;
-            constexpr int COLS = BOTH ? HD : HD / 2;
-            const bool of_v = BOTH ? half == 1 : MODE == kGradV;
-            const int col0 = BOTH ? 0 : half * COLS;
-            const float factor = of_v ? (BF16 ? 1.0f : 6.103515625e-05f) : a.scale / up;
+            constexpr int COLS = HD / (BOTH ? C::NWG / 2 : C::NWG);
+            const bool of_v = BOTH ? part >= C::NWG / 2 : MODE == kGradV;
+            const int col0 = (BOTH ? part % (C::NWG / 2) : part) * COLS;
+            const float factor = of_v ? (BF16 ? 1.0f : 6.103515625e-05f) : (CAP ? 4.0f : 1.0f) * a.scale / up;
             const long long stride = of_v ? a.g2_stride : a.g1_stride;
             uint16_t *out = static_cast<uint16_t *>(of_v ? a.g2 : a.g1) +
                             (static_cast<long long>(u.tok0) + mine) * stride +
                             static_cast<long long>(C::ROWS_STAY ? head : u.head) * HD + col0;
 #pragma unroll 1
-            for (int c = 0; c < COLS / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_base + (of_v ? C::ACC2 : C::ACC1) + col0 + 32 * c, o);
+            for (int c = 0; c < COLS / 16; ++c) {
+                uint32_t o[16];
+                tmem_ld16(tmem + lane_base + (of_v ? C::ACC2 : C::ACC1) + col0 + 16 * c, o);
                 tmem_wait_ld();
-                reg_fence32(o);
-                if (c == COLS / 32 - 1) {
+                reg_fence<16>(o);
+                if (c == COLS / 16 - 1) {
                     tc_fence_before();
-                    mbar_arrive(&bars.acc_free);
+                    warp_arrive(&bars.acc_free);
                 }
                 if (live) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    for (int k = 0; k < 2; ++k) {
                         uint32_t w[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * factor,
                                                __uint_as_float(o[8 * k + 2 * e + 1]) * factor);
-                        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        *reinterpret_cast<uint4 *>(out + 16 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
             }

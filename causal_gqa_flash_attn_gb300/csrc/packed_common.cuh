@@ -62,10 +62,47 @@ __device__ __forceinline__ void query_range(int j0, int j1, int len, int prefix,
     *last = win <= 0 || j0 < max(prefix, sink) ? len - 1 : min(len - 1, j1 + win - 1);
 }
 
+// Two fp32 values in a pair of registers: one instruction for both. The pipes take as long as for two,
+// but the issue slots that this leaves are what the warp that feeds the tensor cores lives on.
+struct Two {
+    uint64_t v;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+    Two t;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(t.v) : "f"(x), "f"(y));
+    return t;
+}
+__device__ __forceinline__ Two two(float x) { return two(x, x); }
+__device__ __forceinline__ float2 both(Two t) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(t.v));
+    return f;
+}
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    Two t;
+    asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
+    return t;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two t;
+    asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(t.v) : "l"(a.v), "l"(b.v));
+    return t;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two t;
+    asm("fma.rn.ftz.f32x2 %0, %1, %2, %3;" : "=l"(t.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return t;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // The score in the exp2 domain from the product s of q and k.
 //   no cap: s * a          (a = scale * log2 e)
-//   cap:    b * tanh(..)   = b - 2 b / (1 + 2^(s * a)),  a = 2 scale log2 e / cap, b = cap log2 e
-// The quotient's error, 2^-22 or so of b, is that of fp32 scores of the cap's size.
+//   cap:    b * tanh(..)   = b - 2 b r, r = 1 / (1 + 2^(s * a)),  a = 2 scale log2 e / cap, b = cap log2 e
+// off by 2^-21 of b, as fp32 scores of the cap's size are.
 __device__ __forceinline__ float rcp_approx(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -80,16 +117,22 @@ inline ScoreRule score_rule(float scale, float cap) {
     r.b = cap > 0.0f ? cap * kPackedLog2e : 0.0f;
     return r;
 }
-__device__ __forceinline__ float capped(float s, const ScoreRule &c) {
-    const float r = rcp_approx(1.0f + ex2(s * c.a));
-    return fmaf(-2.0f * c.b, r, c.b);
+__device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either is one
+    float d;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(x), "f"(y));
+    return d;
 }
-// And the derivative of cap * tanh(x / cap): 1 - tanh^2 = 4 r (1 - r).
-__device__ __forceinline__ float capped(float s, const ScoreRule &c, float *slope) {
-    const float r = rcp_approx(1.0f + ex2(s * c.a));
-    *slope = 4.0f * fmaf(-r, r, r);
-    return fmaf(-2.0f * c.b, r, c.b);
+// r of two scores. Their reciprocals from that of the product, as a reciprocal costs the special units
+// what two exponentials do; 2^63 is where tanh has long been 1.
+__device__ __forceinline__ Two cap_r(Two s, const ScoreRule &c) {
+    const float2 z = both(s * two(c.a));
+    const Two p = two(ex2(min_nan(z.x, 63.0f)), ex2(min_nan(z.y, 63.0f))) + two(1.0f);
+    const float2 q = both(p);
+    return two(q.y, q.x) * two(rcp_approx(q.x * q.y));
 }
+__device__ __forceinline__ Two capped(Two r, const ScoreRule &c) { return fma2(r, two(-2.0f * c.b), two(c.b)); }
+// A quarter of the derivative of cap * tanh(x / cap): (1 - tanh^2) / 4 = r (1 - r).
+__device__ __forceinline__ Two cap_slope(Two r) { return r * fma2(r, two(-1.0f), two(1.0f)); }
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -109,6 +152,57 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
 template <bool BF16>
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N, int a_mn_major, int b_mn_major) {
     return idesc_f16(M, N, a_mn_major, b_mn_major) | (BF16 ? (1u << 7) | (1u << 10) : 0u);
+}
+
+// One arrival for a warp, behind what all of its lanes did. (An arrival of every thread costs the
+// shared memory's atomics more than the products they announce.)
+__device__ __forceinline__ void warp_arrive(uint64_t *bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+}
+
+// N columns of this thread's lane of TMEM.
+template <int N>
+__device__ __forceinline__ void tmem_ld(uint32_t col, uint32_t *r) {
+    if constexpr (N == 16) tmem_ld16(col, r);
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tmem_ld32(col + i, r + i);
+}
+template <int N>
+__device__ __forceinline__ void tmem_st(uint32_t col, const uint32_t *r) {
+    if constexpr (N == 8) tmem_st8(col, r);
+    else if constexpr (N == 16) tmem_st16(col, r);
+    else
+#pragma unroll
+        for (int i = 0; i < N; i += 32) tmem_st32(col + i, r + i);
+}
+
+// Products are issued by a warp whose lanes all walk the same loop, so that descriptors live in uniform
+// registers, with one lane that issues. (A single lane in a branch of its own, with the descriptors
+// computed in its registers, took 100 cycles a product instead of the 64 that the tensor cores take.)
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t yes;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(yes));
+    return yes != 0;
+}
+// A value that all lanes share, known as such to the compiler.
+__device__ __forceinline__ int uniform(int x) { return __reduce_max_sync(~0u, x); }
+__device__ __forceinline__ bool uniform(bool x) { return __all_sync(~0u, x); }
+
+// Registers of this warp's threads from here on: all four warps of a warpgroup, and in sum at most what
+// the block was launched with.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Wait ignoring the abort flag (still bounded): lets copies and MMAs in flight
@@ -190,8 +284,8 @@ cudaError_t launch_packed_fwd_f16(const PackedFwdArgs &a, int hd, bool cap, int 
 constexpr int packed_fwd_tiles(int hd) { return hd == 256 ? 1 : 2; }
 
 // ---- packed_stats.cu
-// What the gradient needs of each row: L, its log-sum-exp in the exp2 domain (less
-// kGradShift for binary16), and D = dout . out; and of each document, for binary16,
+// What the gradient needs of each row: L, less its log-sum-exp in the exp2 domain (plus
+// kGradShift for binary16), and D = -dout . out; and of each document, for binary16,
 // the largest row of dout and of V.
 struct PackedStatsArgs {
     const PackedHeader *header;

@@ -77,9 +77,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.s_full[s], 1);
-            mbar_init(&bars.p_full[s], 128);
+            mbar_init(&bars.p_full[s], 4);
             mbar_init(&bars.o_last[s], 1);
-            mbar_init(&bars.o_free[s], 128);
+            mbar_init(&bars.o_free[s], 4);
         }
         mbar_init(&bars.o_done, 1);
         mbar_init(&bars.patch, 1);
@@ -117,197 +117,212 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
         return key_tiles<BK>(u.p0, last_of(u), u.prefix, a.sink, a.win);
     };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------- copies
-        const int units = a.header->row_tiles * a.n_kv;
-        Arms q_arms, k_arms[2], v_arms[2];
-        int patches = 0;
-        bool ok = true;
-        auto fetch = [&](int w, PackedTile *u) {
-            u->head = -1;
-            if (w >= units) return false;
-            *u = a.rows[w / a.n_kv];
-            u->head = w % a.n_kv;
-            return true;
-        };
-        auto publish = [&](int j, const PackedTile &u) {
-            const int slot = j % kPackedRing;
-            if (j >= kPackedRing &&
-                !mbar_wait(&bars.ring.empty[slot], ((j / kPackedRing) - 1) & 1, abort, err))
-                return false;
-            if (lane == 0) {
-                bars.ring.unit[slot] = u;
-                mbar_arrive(&bars.ring.full[slot]);
-            }
-            return true;
-        };
-        auto load_q = [&](int j, const PackedTile &u) {
-            if (j > 0 && !mbar_wait(&bars.q_empty, (j - 1) & 1, abort, err)) return false;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(&bars.q_full, NT * C::TILE);
-                for (int t = 0; t < NT; ++t)
-                    for (int c = 0; c < C::NCHUNK; ++c)
-                        tma_load_4d(smem + t * C::TILE + c * C::CHUNK, &a.q, &bars.q_full, c * 64, 0, u.head,
-                                    u.tok0 + u.p0 + t * (row_tokens / NT));
-            }
-            ++q_arms.n;
-            return true;
-        };
-        auto load_kv = [&](int tt, int kt, const PackedTile &u, bool is_k) {
-            const int st = tt % NS;
-            if (tt >= NS && !mbar_wait(is_k ? &bars.k_empty[st] : &bars.v_empty[st], ((tt / NS) - 1) & 1, abort, err))
-                return false;
-            uint64_t *full = is_k ? &bars.k_full[st] : &bars.v_full[st];
-            uint8_t *dst = smem + (is_k ? C::OFF_K : C::OFF_V) + st * C::TILE;
-            const int rows = min(BK, u.len - kt * BK);
-            // columns of S past the end are masked, but V's rows are summed
-            const bool patch = !is_k && rows < BK;
-            uint64_t *bar = patch ? &bars.patch : full;
-            if (lane == 0) {
-                mbar_arrive_expect_tx(bar, C::TILE);
-                for (int c = 0; c < C::NCHUNK; ++c)
-                    tma_load_3d(dst + c * C::CHUNK, is_k ? &a.k : &a.v, bar, c * 64, u.head, u.tok0 + kt * BK);
-            }
-            if (patch) {
-                if (!mbar_wait(bar, patches++ & 1, abort, err)) return false;
-                zero_rows(dst, C::NCHUNK, C::CHUNK, rows, BK);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
-            }
-            if (is_k) ++k_arms[st].n; else ++v_arms[st].n;
-            return true;
-        };
-        int t = 0, w = blockIdx.x;
-        PackedTile u, un;
-        bool have = fetch(w, &u);
-        ok = publish(0, u);
-        if (have && ok) ok = load_q(0, u);
-        for (int j = 0; have && ok; ++j) {
-            const KeyTiles plan = plan_of(u);
-            const int cnt = plan.count;
-            bool more = false;
-            for (int i = 0; i < cnt && ok; ++i) {
-                ok = load_kv(t + i, plan.at(i), u, true);
-                if (ok && i == cnt - 1) {  // the next unit, under the waits for the last tiles
-                    if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
-                    w = __shfl_sync(~0u, w, 0);
-                    more = fetch(w, &un);
-                }
-                if (ok && i >= 1) ok = load_kv(t + i - 1, plan.at(i - 1), u, false);
-            }
-            if (ok) ok = load_kv(t + cnt - 1, plan.at(cnt - 1), u, false);
-            t += cnt;
-            if (!ok) break;
-            ok = publish(j + 1, un);
-            have = more;
-            if (have && ok) ok = load_q(j + 1, un);
-            u = un;
-        }
-        if (!ok) {  // copies already issued land before the block exits
-            q_arms.drain(&bars.q_full);
-            for (int s = 0; s < 2; ++s) {
-                k_arms[s].drain(&bars.k_full[s]);
-                v_arms[s].drain(&bars.v_full[s]);
-            }
-            if (patches) wait_out(&bars.patch, (patches - 1) & 1);
-        }
-    } else if (warp == 1) {
-        // ----------------------------------------------------------- products
-        if (lane == 0) {
-            const uint32_t sQ = smem_u32(smem), sK = smem_u32(smem + C::OFF_K), sV = smem_u32(smem + C::OFF_V);
-            auto issue_s = [&](int tile, int tt, uint32_t col) {
-                const int st = tt % NS;
-#pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * C::CHUNK + (kk & 3) * 32;
-                    mma_ss(tmem + col, desc_sw128(sQ + tile * C::TILE + off, 16, 1024),
-                           desc_sw128(sK + st * C::TILE + off, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
-                }
-            };
-            auto issue_pv = [&](int tile, int tt, uint32_t col, bool first) {
-                const int st = tt % NS;
-#pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk)
-                    mma_ts(tmem + tile * HD, tmem + col + kk * 8,
-                           desc_sw128(sV + st * C::TILE + kk * 2048, C::CHUNK, 1024), IDESC_PV,
-                           (!first || kk > 0) ? 1u : 0u);
-            };
-            int t = 0;
+    if (warp < 4) {
+        if constexpr (NT == 2) fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
+        if (warp == 0) {
+            // ------------------------------------------------------------- copies
+            const int units = a.header->row_tiles * a.n_kv;
+            Arms q_arms, k_arms[2], v_arms[2];
+            int patches = 0;
             bool ok = true;
-            PackedTile u;
-            for (int j = 0; ok && next_unit(j, &u); ++j) {
-                mbar_arrive(&bars.ring.empty[j % kPackedRing]);
-                const int count = plan_of(u).count;
-                if (!(ok = mbar_wait(&bars.q_full, j & 1, abort, err))) break;
-                tc_fence_after();
-                // P of tile tt is there, and O free for a unit's first product
-                auto wait_p = [&](int tile, int tt, bool first, uint32_t bar, uint32_t parity) {
-                    if (!mbar_wait(&bars.p_full[bar], parity, abort, err)) return false;
-                    if (first && j > 0 && !mbar_wait(&bars.o_free[tile], (j - 1) & 1, abort, err)) return false;
-                    return true;
-                };
-                auto wait_kv = [&](uint64_t *full, int tt) {
-                    return mbar_wait(full + tt % NS, (tt / NS) & 1, abort, err);
-                };
-                if (NT == 2) {
-                    // one S for each tile: its next product follows the one that reads its P
-                    for (int i = 0; i <= count && ok; ++i) {
-                        const int tt = t + i;
-                        if (i < count && !(ok = wait_kv(bars.k_full, tt))) break;
+            auto fetch = [&](int w, PackedTile *u) {
+                u->head = -1;
+                if (w >= units) return false;
+                *u = a.rows[w / a.n_kv];
+                u->head = w % a.n_kv;
+                return true;
+            };
+            auto publish = [&](int j, const PackedTile &u) {
+                const int slot = j % kPackedRing;
+                if (j >= kPackedRing &&
+                    !mbar_wait(&bars.ring.empty[slot], ((j / kPackedRing) - 1) & 1, abort, err))
+                    return false;
+                if (lane == 0) {
+                    bars.ring.unit[slot] = u;
+                    mbar_arrive(&bars.ring.full[slot]);
+                }
+                return true;
+            };
+            auto load_q = [&](int j, const PackedTile &u) {
+                if (j > 0 && !mbar_wait(&bars.q_empty, (j - 1) & 1, abort, err)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.q_full, NT * C::TILE);
+                    for (int t = 0; t < NT; ++t)
+                        for (int c = 0; c < C::NCHUNK; ++c)
+                            tma_load_4d(smem + t * C::TILE + c * C::CHUNK, &a.q, &bars.q_full, c * 64, 0, u.head,
+                                        u.tok0 + u.p0 + t * (row_tokens / NT));
+                }
+                ++q_arms.n;
+                return true;
+            };
+            auto load_kv = [&](int tt, int kt, const PackedTile &u, bool is_k) {
+                const int st = tt % NS;
+                if (tt >= NS && !mbar_wait(is_k ? &bars.k_empty[st] : &bars.v_empty[st], ((tt / NS) - 1) & 1, abort, err))
+                    return false;
+                uint64_t *full = is_k ? &bars.k_full[st] : &bars.v_full[st];
+                uint8_t *dst = smem + (is_k ? C::OFF_K : C::OFF_V) + st * C::TILE;
+                const int rows = min(BK, u.len - kt * BK);
+                // columns of S past the end are masked, but V's rows are summed
+                const bool patch = !is_k && rows < BK;
+                uint64_t *bar = patch ? &bars.patch : full;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, C::TILE);
+                    for (int c = 0; c < C::NCHUNK; ++c)
+                        tma_load_3d(dst + c * C::CHUNK, is_k ? &a.k : &a.v, bar, c * 64, u.head, u.tok0 + kt * BK);
+                }
+                if (patch) {
+                    if (!mbar_wait(bar, patches++ & 1, abort, err)) return false;
+                    zero_rows(dst, C::NCHUNK, C::CHUNK, rows, BK);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
+                }
+                if (is_k) ++k_arms[st].n; else ++v_arms[st].n;
+                return true;
+            };
+            int t = 0, w = blockIdx.x;
+            PackedTile u, un;
+            bool have = fetch(w, &u);
+            ok = publish(0, u);
+            if (have && ok) ok = load_q(0, u);
+            for (int j = 0; have && ok; ++j) {
+                const KeyTiles plan = plan_of(u);
+                const int cnt = plan.count;
+                bool more = false;
+                for (int i = 0; i < cnt && ok; ++i) {
+                    ok = load_kv(t + i, plan.at(i), u, true);
+                    if (ok && i == cnt - 1) {  // the next unit, under the waits for the last tiles
+                        if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                        w = __shfl_sync(~0u, w, 0);
+                        more = fetch(w, &un);
+                    }
+                    if (ok && i >= 1) ok = load_kv(t + i - 1, plan.at(i - 1), u, false);
+                }
+                if (ok) ok = load_kv(t + cnt - 1, plan.at(cnt - 1), u, false);
+                t += cnt;
+                if (!ok) break;
+                ok = publish(j + 1, un);
+                have = more;
+                if (have && ok) ok = load_q(j + 1, un);
+                u = un;
+            }
+            if (!ok) {  // copies already issued land before the block exits
+                q_arms.drain(&bars.q_full);
+                for (int s = 0; s < 2; ++s) {
+                    k_arms[s].drain(&bars.k_full[s]);
+                    v_arms[s].drain(&bars.v_full[s]);
+                }
+                if (patches) wait_out(&bars.patch, (patches - 1) & 1);
+            }
+        } else if (warp == 1) {
+            // ----------------------------------------------------------- products
+            {
+                const bool one = elect_lane();
+                const uint32_t tmem = uniform(static_cast<int>(bars.tmem_base));
+                // descriptors of the tiles' beginnings: an offset is added to their address field
+                const uint64_t dq = desc_sw128(smem_u32(smem), 16, 1024);
+                const uint64_t dk = desc_sw128(smem_u32(smem + C::OFF_K), 16, 1024);
+                const uint64_t dv = desc_sw128(smem_u32(smem + C::OFF_V), C::CHUNK, 1024);  // dims as columns
+                // which: the tile of the unit, or with one tile the S
+                auto issue_s = [&](int which, int tt) {
+                    const uint64_t q = dq + (NT == 2 ? which * C::TILE >> 4 : 0), k = dk + (tt % NS) * (C::TILE >> 4);
+                    const uint32_t col = tmem + C::S_COL + which * 128;
+                    if (one)
 #pragma unroll
-                        for (int tile = 0; tile < 2; ++tile) {
-                            const uint32_t col = C::S_COL + tile * 128;
-                            if (i > 0) {
-                                ok = ok && wait_p(tile, tt - 1, i == 1, tile, (tt - 1) & 1);
-                                if (ok && tile == 0) ok = wait_kv(bars.v_full, tt - 1);
-                                if (!ok) break;
-                                tc_fence_after();
-                                issue_pv(tile, tt - 1, col, i == 1);
-                                if (tile == 1) tc_commit(&bars.v_empty[(tt - 1) % NS]);
-                                if (i == count) tc_commit(&bars.o_last[tile]);
-                            }
-                            if (i < count) {
-                                tc_fence_after();
-                                issue_s(tile, tt, col);
-                                tc_commit(&bars.s_full[tile]);
-                                if (tile == 1) {
-                                    tc_commit(&bars.k_empty[tt % NS]);
-                                    if (i == count - 1) tc_commit(&bars.q_empty);
+                        for (int kk = 0; kk < HD / 16; ++kk) {
+                            const uint32_t off = ((kk >> 2) * C::CHUNK + (kk & 3) * 32) >> 4;
+                            mma_ss(col, q + off, k + off, IDESC_QK, kk > 0 ? 1u : 0u);
+                        }
+                };
+                auto issue_pv = [&](int which, int tt, bool first) {
+                    const uint64_t v = dv + (tt % NS) * (C::TILE >> 4);
+                    const uint32_t o = tmem + (NT == 2 ? which * HD : 0), p = tmem + C::S_COL + which * 128;
+                    if (one)
+#pragma unroll
+                        for (int kk = 0; kk < BK / 16; ++kk)
+                            mma_ts(o, p + kk * 8, v + (kk * 2048 >> 4), IDESC_PV, (!first || kk > 0) ? 1u : 0u);
+                };
+                auto wait = [&](uint64_t *bar, uint32_t parity) { return uniform(mbar_wait(bar, parity, abort, err)); };
+                auto commit = [&](uint64_t *bar) {
+                    if (one) tc_commit(bar);
+                };
+                int t = 0;
+                bool ok = true;
+                PackedTile u;
+                for (int j = 0; ok && uniform(next_unit(j, &u)); ++j) {
+                    const int count = uniform(plan_of(u).count);
+                    warp_arrive(&bars.ring.empty[j % kPackedRing]);
+                    if (!(ok = wait(&bars.q_full, j & 1))) break;
+                    tc_fence_after();
+                    // P of tile tt is there, and O free for a unit's first product
+                    auto wait_p = [&](int tile, int tt, bool first, uint32_t bar, uint32_t parity) {
+                        if (!wait(&bars.p_full[bar], parity)) return false;
+                        if (first && j > 0 && !wait(&bars.o_free[tile], (j - 1) & 1)) return false;
+                        return true;
+                    };
+                    auto wait_kv = [&](uint64_t *full, int tt) {
+                        return wait(full + tt % NS, (tt / NS) & 1);
+                    };
+                    if (NT == 2) {
+                        // one S for each tile: its next product follows the one that reads its P
+                        for (int i = 0; i <= count && ok; ++i) {
+                            const int tt = t + i;
+                            if (i < count && !(ok = wait_kv(bars.k_full, tt))) break;
+#pragma unroll
+                            for (int tile = 0; tile < 2; ++tile) {
+                                if (i > 0) {
+                                    ok = ok && wait_p(tile, tt - 1, i == 1, tile, (tt - 1) & 1);
+                                    if (ok && tile == 0) ok = wait_kv(bars.v_full, tt - 1);
+                                    if (!ok) break;
+                                    tc_fence_after();
+                                    issue_pv(tile, tt - 1, i == 1);
+                                    if (tile == 1) commit(&bars.v_empty[(tt - 1) % NS]);
+                                    if (i == count) commit(&bars.o_last[tile]);
+                                }
+                                if (i < count) {
+                                    tc_fence_after();
+                                    issue_s(tile, tt);
+                                    commit(&bars.s_full[tile]);
+                                    if (tile == 1) {
+                                        commit(&bars.k_empty[tt % NS]);
+                                        if (i == count - 1) commit(&bars.q_empty);
+                                    }
                                 }
                             }
                         }
-                    }
-                } else {
-                    // two S for the tile, which take turns
-                    for (int i = 0; i <= count && ok; ++i) {
-                        const int tt = t + i;
-                        if (i < count) {
-                            if (!(ok = wait_kv(bars.k_full, tt))) break;
-                            tc_fence_after();
-                            issue_s(0, tt, C::S_COL + (tt & 1) * 128);
-                            tc_commit(&bars.k_empty[tt % NS]);
-                            tc_commit(&bars.s_full[tt & 1]);
-                            if (i == count - 1) tc_commit(&bars.q_empty);
+                    } else {
+                        // two S for the tile, which take turns
+                        for (int i = 0; i <= count && ok; ++i) {
+                            const int tt = t + i;
+                            if (i < count) {
+                                if (!(ok = wait_kv(bars.k_full, tt))) break;
+                                tc_fence_after();
+                                issue_s(tt & 1, tt);
+                                commit(&bars.k_empty[tt % NS]);
+                                commit(&bars.s_full[tt & 1]);
+                                if (i == count - 1) commit(&bars.q_empty);
+                            }
+                            if (i > 0) {
+                                const int pt = tt - 1;
+                                if (!(ok = wait_p(0, pt, i == 1, pt & 1, (pt >> 1) & 1) && wait_kv(bars.v_full, pt))) break;
+                                tc_fence_after();
+                                issue_pv(pt & 1, pt, i == 1);
+                                commit(&bars.v_empty[pt % NS]);
+                                commit(&bars.o_done);
+                                if (i == count) commit(&bars.o_last[0]);
+                            }
                         }
-                        if (i > 0) {
-                            const int pt = tt - 1;
-                            if (!(ok = wait_p(0, pt, i == 1, pt & 1, (pt >> 1) & 1) && wait_kv(bars.v_full, pt))) break;
-                            tc_fence_after();
-                            issue_pv(0, pt, C::S_COL + (pt & 1) * 128, i == 1);
-                            tc_commit(&bars.v_empty[pt % NS]);
-                            tc_commit(&bars.o_done);
-                            if (i == count) tc_commit(&bars.o_last[0]);
-                        }
                     }
+                    t += count;
                 }
-                t += count;
+                // every product issued completes before TMEM is released
+                commit(&bars.drain);
+                wait_out(&bars.drain, 0);
+                __syncwarp();
             }
-            // every product issued completes before TMEM is released
-            tc_commit(&bars.drain);
-            wait_out(&bars.drain, 0);
         }
-    } else if (warp >= 4) {
+    } else {
+        if constexpr (NT == 2) more_registers<216>();
         // ------------------------------------------------- softmax and output
         const int tile = (warp - 4) >> 2;  // this warp's tile of the unit
         const int r = threadIdx.x - 128 - 128 * tile;  // row of the tile: TMEM lane
@@ -346,48 +361,54 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 for (int c = 0; c < 4; ++c) reg_fence32(s + 32 * c);
 
                 const int j0 = plan.at(i) * BK, j1 = j0 + BK - 1;
-                if (CAP) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) s[c] = __float_as_uint(capped(__uint_as_float(s[c]), rule));
-                }
-                float mx = -INFINITY;
                 const bool whole = sees_all(p0, p1, j0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= p0);
-                if (BIAS) {
+                constexpr bool kScaled = CAP || BIAS;  // s goes to the exp2 domain first
+                if (kScaled) {
                     const float far = static_cast<float>(p - j0);  // exact: below 2^26 apart
-                    if (whole) {
-                        const float base = -slope2 * far;
+                    auto score = [&](auto masks) {
+                        constexpr bool MASK = decltype(masks)::value;
 #pragma unroll
-                        for (int c = 0; c < 128; ++c) {
-                            const float b = fmaf(slope2, static_cast<float>(c), base);
-                            s[c] = __float_as_uint(CAP ? __uint_as_float(s[c]) + b
-                                                       : fmaf(__uint_as_float(s[c]), rule.a, b));
+                        for (int c = 0; c < 128; c += 2) {
+                            Two x = two(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), off = two(0.0f);
+                            if (BIAS) {
+                                Two d = two(far) + two(-static_cast<float>(c), -static_cast<float>(c + 1));
+                                if (MASK) {
+                                    const float2 f = both(d);
+                                    d = two(fabsf(f.x), fabsf(f.y));
+                                }
+                                off = two(-slope2) * d;
+                            }
+                            if (CAP)
+                                x = BIAS ? capped(cap_r(x, rule), rule) + off : capped(cap_r(x, rule), rule);
+                            else
+                                x = fma2(x, two(rule.a), off);
+                            const float2 f = both(x);
+                            s[c] = __float_as_uint(f.x);
+                            s[c + 1] = __float_as_uint(f.y);
                         }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) {
-                            const float b = -slope2 * fabsf(far - static_cast<float>(c));
-                            s[c] = __float_as_uint(CAP ? __uint_as_float(s[c]) + b
-                                                       : fmaf(__uint_as_float(s[c]), rule.a, b));
-                        }
-                    }
+                    };
+                    if (!BIAS || whole) score(std::false_type{}); else score(std::true_type{});
                 }
-                if (whole) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) mx = fmaxf(mx, __uint_as_float(s[c]));
-                } else {
+                if (!whole) {
                     // key j0 + c is seen iff c < head or lo <= c <= hi
                     const int hi = p - j0;
                     const int lo = a.win > 0 ? p - a.win + 1 - j0 : 0;
                     const int first = max(u.prefix - j0, a.win > 0 ? min(a.sink - j0, hi + 1) : 0);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) {
-                        const bool seen = (c < first) | ((c >= lo) & (c <= hi));
-                        const float v = seen ? __uint_as_float(s[c]) : -INFINITY;
-                        s[c] = __float_as_uint(v);
-                        mx = fmaxf(mx, v);
-                    }
+                    for (int c = 0; c < 128; ++c)
+                        if (!((c < first) | ((c >= lo) & (c <= hi)))) s[c] = __float_as_uint(-INFINITY);
                 }
-                constexpr bool kScaled = CAP || BIAS;  // s is in the exp2 domain already
+                // four chains, so that none of them is waited for
+                float mx4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx4[e] = __uint_as_float(s[e]);
+#pragma unroll
+                for (int c = 4; c < 124; c += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        mx4[e] = max3(mx4[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
+                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), max3(mx4[3], __uint_as_float(s[124]), __uint_as_float(s[125])),
+                                      fmaxf(__uint_as_float(s[126]), __uint_as_float(s[127])));
                 const float m_new = fmaxf(m_used, kScaled ? mx : mx * rule.a);
                 float corr = 1.0f;
                 bool moves = false;
@@ -399,19 +420,19 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                     }
                     m_used = m_new;
                 }
-                const float ref = m_used == -INFINITY ? 0.0f : m_used - kFwdShift;
+                const Two ref = two(m_used == -INFINITY ? 0.0f : kFwdShift - m_used);
                 uint32_t pk[64];
-                float sum0 = 0.0f, sum1 = 0.0f;
+                Two sums[2] = {two(0.0f), two(0.0f)};
 #pragma unroll
                 for (int c = 0; c < 64; ++c) {
-                    const float s0 = __uint_as_float(s[2 * c]), s1 = __uint_as_float(s[2 * c + 1]);
-                    const float w0 = ex2(kScaled ? s0 - ref : fmaf(s0, rule.a, -ref));
-                    const float w1 = ex2(kScaled ? s1 - ref : fmaf(s1, rule.a, -ref));
-                    sum0 += w0;
-                    sum1 += w1;
-                    pk[c] = pack2<BF16>(w0, w1);
+                    const Two x = two(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
+                    float2 f = both(kScaled ? x + ref : fma2(x, two(rule.a), ref));
+                    f = make_float2(ex2(f.x), ex2(f.y));
+                    sums[c & 1] = sums[c & 1] + two(f.x, f.y);
+                    pk[c] = pack2<BF16>(f.x, f.y);
                 }
-                l += sum0 + sum1;
+                const float2 sum = both(sums[0] + sums[1]);
+                l += sum.x + sum.y;
                 // O is rescaled when every product into it is done. With one S a tile that
                 // holds already: S(tt) was issued after them. With two, PV(tt - 1) may still run.
                 const bool any = __any_sync(~0u, moves);
@@ -439,7 +460,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 tmem_st32(scol + 32, pk + 32);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&bars.p_full[bar]);
+                warp_arrive(&bars.p_full[bar]);
             }
             if (!ok) break;
             t += plan.count;
@@ -462,7 +483,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 reg_fence32(o);
                 if (c == HD / 32 - 1) {  // read whole: the next unit may overwrite it
                     tc_fence_before();
-                    mbar_arrive(&bars.o_free[tile]);
+                    warp_arrive(&bars.o_free[tile]);
                 }
                 if (live) {
 #pragma unroll

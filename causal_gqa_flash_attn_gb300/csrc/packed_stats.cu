@@ -1,7 +1,8 @@
 // packed_stats.cu -- what the gradient of packed attention needs of each row
 // (include/fa.h, fa_packed_attn_grad): the log-sum-exp in the exp2 domain and
-// D = dout . out, in the order of the rows, 128-row blocks a document. Rows of a
-// block past the document's end get an L that makes every weight 0.
+// D = dout . out, both negative as they are added, in the order of the rows, 128-row
+// blocks a document. Rows of a block past the document's end get an L that makes
+// every weight 0.
 //
 // One pass over out and dout, a row by HD / 8 lanes with 16-byte loads; bound by HBM.
 #include "packed_common.cuh"
@@ -10,7 +11,7 @@ namespace fa {
 namespace {
 
 constexpr int kStatsThreads = 256;
-constexpr float kNoRow = 1e30f;
+constexpr float kNoRow = -1e30f;
 
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kStatsThreads) packed_stats_kernel(PackedStatsArgs a) {
@@ -57,9 +58,9 @@ __global__ void __launch_bounds__(kStatsThreads) packed_stats_kernel(PackedStats
                 most = n > most || n != n ? n : most;  // a NaN stays
             }
             if (l == 0) {
-                a.D[base + r] = D;
-                a.L[base + r] = live ? fmaf(load(a.lse + static_cast<size_t>(head) * a.n_tokens + t), kPackedLog2e,
-                                            BF16 ? 0.0f : -kGradShift)
+                a.D[base + r] = -D;
+                a.L[base + r] = live ? fmaf(load(a.lse + static_cast<size_t>(head) * a.n_tokens + t), -kPackedLog2e,
+                                            BF16 ? 0.0f : kGradShift)
                                      : kNoRow;
             }
         }
