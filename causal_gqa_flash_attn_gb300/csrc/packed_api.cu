@@ -33,15 +33,26 @@ fa_status check_sizes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, i
 
 // Where the parts of a workspace lie; `rows` is the rows of a row tile.
 struct Layout {
-    size_t row_tiles, key_tiles, doc_tiles, doc_most, stats, bytes;
-    int most_rows, most_keys;
+    size_t row_tiles, key_tiles, doc_tiles, doc_most, stats, arrived, partial, bytes;
+    int most_rows, most_keys, slots;
     size_t blocks;  // 128-row blocks of a kv head
 };
-Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int rows, bool grad) {
+constexpr size_t kPartialBytes = 48 << 20;  // of partial sums at most
+constexpr int kParts = 2;  // pieces of the work of dk and dv an SM, about
+
+Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int rows, bool grad) {
     Layout w;
     const int group = n_q_heads / n_kv_heads;
+    // Tiles of keys are cut where one has more than a few row tiles and there are not enough of them for
+    // all SMs: into no more pieces than there are slots for.
+    const long long tiles = static_cast<long long>(n_tokens / 128 + n_docs) * n_kv_heads;
+    const long long row_tiles = static_cast<long long>(n_tokens) * group / fa::packed_grad_rows(head_dim) + 1;
+    const size_t slot = sizeof(float) * 128 * head_dim * (head_dim < 256 ? 2 : 1);
+    w.slots = 0;
+    if (grad && row_tiles > fa::kPackedLeastPiece)
+        w.slots = static_cast<int>(std::min<long long>(kPartialBytes / slot, tiles * (row_tiles / fa::kPackedLeastPiece + 1)));
     w.most_rows = static_cast<int>(static_cast<long long>(n_tokens) * group / rows) + n_docs;
-    w.most_keys = grad ? n_tokens / 128 + n_docs : 0;
+    w.most_keys = grad ? n_tokens / 128 + n_docs + w.slots : 0;
     w.blocks = static_cast<size_t>(n_tokens) * group / 128 + n_docs;
     size_t at = sizeof(fa::PackedHeader);
     auto take = [&](size_t n) {
@@ -54,6 +65,8 @@ Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int rows,
     w.doc_tiles = take(sizeof(int) * 3 * (static_cast<size_t>(n_docs) + 1));
     w.doc_most = take(grad ? sizeof(unsigned) * 2 * n_docs : 0);
     w.stats = take(grad ? sizeof(float) * 2 * n_kv_heads * w.blocks * 128 : 0);
+    w.arrived = take(sizeof(int) * w.slots);
+    w.partial = take(slot * w.slots);
     w.bytes = at;
     return w;
 }
@@ -103,7 +116,7 @@ extern "C" {
 
 size_t fa_packed_attn_workspace_bytes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim) {
     if (check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim) != FA_OK) return 0;
-    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128 * fa::packed_fwd_tiles(head_dim), false).bytes;
+    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim, 128 * fa::packed_fwd_tiles(head_dim), false).bytes;
 }
 
 fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out, float *lse, int dtype,
@@ -123,7 +136,7 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
         return FA_ERR_INVALID;
     if (out == q || out == k || out == v) return FA_ERR_INVALID;
     const int group = n_q_heads / n_kv_heads, rows = 128 * fa::packed_fwd_tiles(head_dim);
-    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, rows, false);
+    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim, rows, false);
     if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
     unsigned *err = fa::device_error_word();
     if (!err) return FA_ERR_CUDA;
@@ -139,8 +152,13 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
     p.row_tokens = rows / group;
     p.block_tokens_log = 7 - log2_of(group);
     p.key_tile = 128;
+    p.step_tokens = 1;
+    p.n_kv = n_kv_heads;
+    p.parts = 1;
     p.most_rows = w.most_rows;
     p.most_keys = 0;
+    p.slots = 0;
+    p.arrived = nullptr;
     p.header = reinterpret_cast<fa::PackedHeader *>(ws);
     p.rows = reinterpret_cast<fa::PackedTile *>(ws + w.row_tiles);
     p.keys = nullptr;
@@ -179,7 +197,7 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
 size_t fa_packed_attn_grad_workspace_bytes(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads,
                                            int head_dim) {
     if (check_sizes(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim) != FA_OK) return 0;
-    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128, true).bytes;
+    return layout(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim, 128, true).bytes;
 }
 
 fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const void *out, const float *lse,
@@ -212,7 +230,7 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
         if (made[i] == made[(i + 1) % 3]) return FA_ERR_INVALID;
     }
     const int group = n_q_heads / n_kv_heads, step = fa::packed_grad_rows(head_dim);
-    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, 128, true);
+    const Layout w = layout(n_docs, n_tokens, n_q_heads, n_kv_heads, head_dim, 128, true);
     if (workspace_bytes < w.bytes) return FA_ERR_WORKSPACE;
     unsigned *err = fa::device_error_word();
     if (!err) return FA_ERR_CUDA;
@@ -228,8 +246,13 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     p.row_tokens = 128 / group;
     p.block_tokens_log = 7 - log2_of(group);
     p.key_tile = step;
+    p.step_tokens = step / group;
+    p.n_kv = n_kv_heads;
+    p.parts = kParts * fa::device_sm_count();
     p.most_rows = w.most_rows;
     p.most_keys = w.most_keys;
+    p.slots = w.slots;
+    p.arrived = reinterpret_cast<int *>(ws + w.arrived);
     p.header = reinterpret_cast<fa::PackedHeader *>(ws);
     p.rows = reinterpret_cast<fa::PackedTile *>(ws + w.row_tiles);
     p.keys = reinterpret_cast<fa::PackedTile *>(ws + w.key_tiles);
@@ -261,6 +284,8 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     a.L = t.L;
     a.D = t.D;
     a.blocks = t.blocks;
+    a.partial = reinterpret_cast<float *>(ws + w.partial);
+    a.arrived = p.arrived;
     a.doc_most = p.doc_most;
     a.slopes = slopes;
     a.n_docs = n_docs;

@@ -6,7 +6,7 @@
 //   t_ij = P_ij (dout_i . v_j - D_i) f'(s_ij)        (f' = 1 - tanh^2 where scores are capped)
 //   dq_i = scale sum_j t_ij k_j,   dk_j = scale sum_i t_ij q_i.
 //
-// Sums in a fixed order, without atomics: one kernel holds 128 rows of queries and
+// Sums in a fixed order: one kernel holds 128 rows of queries and
 // streams the keys past them (dq), one holds 128 keys and streams the rows of queries
 // past them, the heads of the group among them (dk and dv; with head_dim 256, whose
 // accumulators take half of TMEM each, a kernel for dk and one for dv). The price is
@@ -54,7 +54,7 @@ struct GradCfg {
     static constexpr uint32_t OFF_STATS = OFF_END;     // [NL][2][BN] L and D of a tile's rows
     static constexpr uint32_t OFF_BIAS = OFF_STATS + (ROWS_STAY ? 0 : NL * 2 * BN * 4);  // [2][16]
     static constexpr uint32_t OFF_BARS = OFF_BIAS + 128;
-    static constexpr uint32_t SMEM = OFF_BARS + 512 > 120u * 1024u ? OFF_BARS + 512 : 120u * 1024u;
+    static constexpr uint32_t SMEM = OFF_BARS + 576 > 120u * 1024u ? OFF_BARS + 576 : 120u * 1024u;
     // TMEM: S, T (dv alone: a second S), acc1, acc2; a second T where there is room
     static constexpr int NT = HAS_T && 256 + HD * (MODE == kGradKV ? 2 : 1) + 128 <= 512 ? 2 : 1;
     static constexpr uint32_t S_COL = 0, T_COL = 128;
@@ -75,9 +75,9 @@ struct GradBars {
     uint64_t patch, drain;
     UnitRing ring;
     uint32_t tmem_base;
-    int abort;
+    int abort, last;
 };
-static_assert(sizeof(GradBars) <= 512, "barrier block");
+static_assert(sizeof(GradBars) <= 576, "barrier block");
 
 template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
 __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
@@ -153,17 +153,14 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
     const int lg = a.log_group;
     const int tile_tokens = 128 >> lg;  // of a row tile
     const int step_tokens = BN >> lg;   // of a moving tile of rows
-    // The moving tiles of a unit: of keys, or of rows (from the first query that sees a key of the
-    // tile to the last).
+    // The moving tiles of a unit: of keys, or of rows (of queries that see a key of the tile).
     auto plan_of = [&](const PackedTile &u) {
         if (C::ROWS_STAY)
             return key_tiles<BN>(u.p0, min(u.p0 + tile_tokens, u.len) - 1, u.prefix, a.sink, a.win);
-        int first, last;
-        query_range(u.p0, min(u.p0 + 128, u.len) - 1, u.len, u.prefix, a.sink, a.win, &first, &last);
         KeyTiles t;
         t.ns = 0;
-        t.lo = first / step_tokens;
-        t.count = last / step_tokens - t.lo + 1;
+        t.lo = u.from;
+        t.count = u.rows;
         return t;
     };
     // Rows from the last to the first: without a window the units of a document begin with the same
@@ -608,6 +605,23 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             uint16_t *out = static_cast<uint16_t *>(of_v ? a.g2 : a.g1) +
                             (static_cast<long long>(u.tok0) + mine) * stride +
                             static_cast<long long>(C::ROWS_STAY ? head : u.head) * HD + col0;
+            auto store = [&](int c, const uint32_t *o) {
+                if (!live) return;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * factor,
+                                           __uint_as_float(o[8 * k + 2 * e + 1]) * factor);
+                    *reinterpret_cast<uint4 *>(out + 16 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            };
+            const bool alone = C::ROWS_STAY || u.pieces == 1;
+            // pieces of this tile and head lie one behind another, [column][lane] of each
+            constexpr int SLOT = (BOTH ? 2 : 1) * HD * 128;
+            const int slot0 = alone ? 0 : u.slot + u.head * u.pieces;
+            float *sums = a.partial + static_cast<size_t>(slot0) * SLOT + ((BOTH && of_v ? HD : 0) + col0) * 128 + r;
 #pragma unroll 1
             for (int c = 0; c < COLS / 16; ++c) {
                 uint32_t o[16];
@@ -618,15 +632,38 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     tc_fence_before();
                     warp_arrive(&bars.acc_free);
                 }
-                if (live) {
+                if (alone) {
+                    store(c, o);
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        uint32_t w[4];
+                    for (int k = 0; k < 16; ++k)
+                        __stcg(sums + static_cast<size_t>(u.piece) * SLOT + (16 * c + k) * 128, __uint_as_float(o[k]));
+                }
+            }
+            if (!alone) {
+                // the block that is done last adds the pieces, in their order
+                __threadfence();
+                named_barrier_sync(1, C::COMPUTE);
+                if (threadIdx.x == 128) {
+                    bars.last = atomicAdd(a.arrived + slot0, 1) == u.pieces - 1;
+                    if (bars.last) a.arrived[slot0] = 0;  // for the next kernel
+                    __threadfence();
+                }
+                named_barrier_sync(1, C::COMPUTE);
+                if (*static_cast<volatile int *>(&bars.last)) {
+                    __threadfence();
+#pragma unroll 1
+                    for (int c = 0; c < COLS / 16; ++c) {
+                        float x[16] = {};
+#pragma unroll 1
+                        for (int k = 0; k < u.pieces; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * factor,
-                                               __uint_as_float(o[8 * k + 2 * e + 1]) * factor);
-                        *reinterpret_cast<uint4 *>(out + 16 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 16; ++e)
+                                x[e] += __ldcg(sums + static_cast<size_t>(k) * SLOT + (16 * c + e) * 128);
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(x[e]);
+                        store(c, o);
                     }
                 }
             }

@@ -30,9 +30,11 @@ struct PackedTile {
     int rb;          // 128-row blocks of the documents before this one
     int doc;
     int head;        // kv head (set by the kernel that takes the unit)
-    int pad;
+    // Tiles of keys: the row tiles of this piece, [from, from + rows), the pieces of the tile, and
+    // where their partial sums go (piece 0 of kv head 0; -1: there is one piece).
+    int from, rows, piece, pieces, slot;
 };
-static_assert(sizeof(PackedTile) == 32, "two 16-byte loads");
+static_assert(sizeof(PackedTile) == 48, "three 16-byte loads");
 
 // Key tiles of BK that the queries at positions p0 .. p1 see any key of, in
 // ascending order: those of the prefix and the sinks, then the window's (or all).
@@ -255,7 +257,11 @@ struct PackedPlanArgs {
     int row_tokens;       // tokens of a row tile
     int block_tokens_log; // log2 of the tokens of 128 rows
     int key_tile;         // keys of a row tile's key tiles, for the weights
+    int step_tokens;      // tokens of the row tiles that move past a tile of keys
+    int n_kv, parts;      // a key tile's row tiles are cut into pieces of about 1 / parts of the work
     int most_rows, most_keys;  // room in the lists (most_keys 0: no key tiles)
+    int slots;            // partial sums that there is room for
+    int *arrived;         // [slots], zeroed
     PackedHeader *header;
     PackedTile *rows, *keys;
     int *doc_tiles;       // [3][n_docs + 1]: row tiles, key tiles and 128-row blocks before each document
@@ -314,6 +320,8 @@ struct PackedGradArgs {
     long long g1_stride, g2_stride;
     const float *L, *D;
     long long blocks;
+    float *partial;          // [slots][dk, dv or one of them][head_dim][128]
+    int *arrived;            // [slots]: pieces of the tile that are done, at the slot of its first
     const unsigned *doc_most;
     const float *slopes;
     int n_docs, n_kv, log_group, sink, win;
@@ -322,6 +330,8 @@ struct PackedGradArgs {
     unsigned *err;
 };
 enum { kGradQ = 0, kGradKV = 1, kGradK = 2, kGradV = 3 };
+// Pieces of a key tile are no smaller than this many row tiles.
+constexpr int kPackedLeastPiece = 4;
 // Rows (or keys) of a moving tile.
 constexpr int packed_grad_rows(int hd) { return hd == 256 ? 64 : 128; }
 cudaError_t launch_packed_grad_bf16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream);

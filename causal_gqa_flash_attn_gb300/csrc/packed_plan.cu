@@ -5,6 +5,10 @@
 // counted into bins of their number of key tiles (or row tiles, for a tile of keys)
 // and put into the lists from the heaviest bin on. Within a bin the order may differ
 // from call to call: units do not depend on each other, so that no result does.
+//
+// A tile of keys whose rows are many (the first keys of a long document are seen by all of it) is
+// cut into pieces, so that a few such tiles do not keep a few SMs busy alone; their sums are
+// added in the order of the pieces.
 #include "packed_common.cuh"
 
 namespace fa {
@@ -59,13 +63,15 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     __shared__ int part[3][32], sum[3];
     __shared__ int bins[kBins];
     __shared__ int small[3][kDocsInSmem + 1];
-    __shared__ int bad_docs;
+    __shared__ int bad_docs, n_slots;
+    __shared__ unsigned long long all_rows;
     const int tid = threadIdx.x, D = a.n_docs;
     const bool fits = D <= kDocsInSmem;
     int *before[3];
     for (int k = 0; k < 3; ++k) before[k] = fits ? small[k] : a.doc_tiles + static_cast<size_t>(k) * (D + 1);
     if (tid == 0) bad_docs = 0;
     if (tid < 4) a.header->counters[tid] = 0;
+    for (int i = tid; i < a.slots; i += kPlanThreads) a.arrived[i] = 0;
     __syncthreads();
 
     // ---- tiles before each document: a thread sums a run of documents
@@ -109,18 +115,12 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
         total[0] = total[1] = 0;
         if (tid == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
     }
-    if (tid == 0) {
-        a.header->row_tiles = total[0];
-        a.header->key_tiles = total[1];
-    }
-
     // ---- the lists
     for (int list = 0; list < 2; ++list) {
         const int n = total[list];
-        if (n == 0) continue;
-        int shift = 0;  // bins of a power of two of key (or row) tiles
-        const int step = list ? a.row_tokens : a.key_tile;
-        while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
+        PackedTile *out = list ? a.keys : a.rows;
+        const int room = list ? a.most_keys : a.most_rows;
+        // tile x, and how many tiles move past it
         auto tile = [&](int x, PackedTile *t) {
             const int d = find_doc(before[list], D, x);
             t->tok0 = load(a.cu + d);
@@ -129,33 +129,86 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
             t->prefix = a.prefix ? min(max(load(a.prefix + d), 0), t->len) : 0;
             t->rb = before[2][d];
             t->doc = d;
-            t->head = t->pad = 0;
-            int w;
+            t->head = t->from = t->piece = 0;
+            t->pieces = 1;
+            t->slot = -1;
             if (list) {
                 int first, last;
                 query_range(t->p0, min(t->p0 + 128, t->len) - 1, t->len, t->prefix, a.sink, a.win, &first, &last);
-                w = last / a.row_tokens - first / a.row_tokens + 1;
+                t->from = first / a.step_tokens;
+                t->rows = last / a.step_tokens - t->from + 1;
             } else {
                 const int p1 = min(t->p0 + a.row_tokens, t->len) - 1;
-                w = a.key_tile == 64 ? key_tiles<64>(t->p0, p1, t->prefix, a.sink, a.win).count
-                                     : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
+                t->rows = a.key_tile == 64 ? key_tiles<64>(t->p0, p1, t->prefix, a.sink, a.win).count
+                                           : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
             }
-            return kBins - 1 - min(w >> shift, kBins - 1);  // heaviest first
         };
+        PackedTile t;
+        // the largest piece: at first 1 / parts of all row tiles, then what there is room for
+        int most = 1 << 30;
+        if (list && a.slots > 0 && n > 0) {
+            if (tid == 0) all_rows = 0;
+            __syncthreads();
+            unsigned long long mine = 0;
+            for (int x = tid; x < n; x += kPlanThreads) {
+                tile(x, &t);
+                mine += t.rows;
+            }
+            atomicAdd(&all_rows, mine);
+            __syncthreads();
+            most = max(kPackedLeastPiece, static_cast<int>((all_rows * a.n_kv + a.parts - 1) / a.parts));
+        }
+        auto pieces_of = [&](int rows) { return rows > most ? (rows + most - 1) / most : 1; };
+        int entries = n;
+        while (list && a.slots > 0 && n > 0) {
+            if (tid == 0) n_slots = 0;
+            int need = 0, more = 0, zero = 0;
+            for (int x = tid; x < n; x += kPlanThreads) {
+                tile(x, &t);
+                const int p = pieces_of(t.rows);
+                more += p - 1;
+                if (p > 1) need += p;
+            }
+            scan3(need, more, zero, sum, part);
+            const bool fits = static_cast<long long>(sum[0]) * a.n_kv <= a.slots && n + sum[1] <= room;
+            entries = n + sum[1];
+            __syncthreads();
+            if (fits) break;
+            most *= 2;
+        }
+        if (tid == 0) (list ? a.header->key_tiles : a.header->row_tiles) = entries;
+        if (n == 0) continue;
+        int shift = 0;  // bins of a power of two of tiles
+        const int step = list ? a.step_tokens : a.key_tile;
+        while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
+        auto bin_of = [&](int rows) { return kBins - 1 - min(rows >> shift, kBins - 1); };  // heaviest first
         for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
         __syncthreads();
-        PackedTile t;
-        for (int x = tid; x < n; x += kPlanThreads) atomicAdd(&bins[tile(x, &t)], 1);
+        // the pieces of a tile differ by one row tile at most, and share a bin
+        for (int x = tid; x < n; x += kPlanThreads) {
+            tile(x, &t);
+            const int p = pieces_of(t.rows);
+            atomicAdd(&bins[bin_of((t.rows + p - 1) / p)], p);
+        }
         __syncthreads();
         static_assert(kBins == kPlanThreads, "a bin for each thread");
         int at = bins[tid], z0 = 0, z1 = 0;
         scan3(at, z0, z1, sum, part);
         bins[tid] = at;
         __syncthreads();
-        PackedTile *out = list ? a.keys : a.rows;
         for (int x = tid; x < n; x += kPlanThreads) {
-            const int bin = tile(x, &t);
-            out[atomicAdd(&bins[bin], 1)] = t;
+            tile(x, &t);
+            const int p = pieces_of(t.rows), rows = t.rows, from = t.from;
+            const int place = atomicAdd(&bins[bin_of((rows + p - 1) / p)], p);
+            t.pieces = p;
+            if (p > 1) t.slot = atomicAdd(&n_slots, p * a.n_kv);
+            for (int k = 0; k < p; ++k) {
+                const int r0 = static_cast<int>(static_cast<long long>(rows) * k / p);
+                t.piece = k;
+                t.from = from + r0;
+                t.rows = static_cast<int>(static_cast<long long>(rows) * (k + 1) / p) - r0;
+                out[place + k] = t;
+            }
         }
         __syncthreads();
     }
