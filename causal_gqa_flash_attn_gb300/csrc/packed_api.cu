@@ -62,7 +62,7 @@ Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_
     };
     w.row_tiles = take(sizeof(fa::PackedTile) * w.most_rows);
     w.key_tiles = take(sizeof(fa::PackedTile) * w.most_keys);
-    w.doc_tiles = take(sizeof(int) * 3 * (static_cast<size_t>(n_docs) + 1));
+    w.doc_tiles = take(sizeof(int) * 3 * (grad ? 2 : 1) * (static_cast<size_t>(n_docs) + 1));
     w.doc_most = take(grad ? sizeof(unsigned) * 2 * n_docs : 0);
     w.stats = take(grad ? sizeof(float) * 2 * n_kv_heads * w.blocks * 128 : 0);
     w.arrived = take(sizeof(int) * w.slots);

@@ -327,11 +327,19 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     warp_arrive(&bars.ring.empty[j % kPackedRing]);
                     if (!(ok = wait(&bars.x_full, j & 1))) break;
                     tc_fence_after();
+                    // Two barriers at once, each looked at by half of the lanes: a look takes a hundred cycles
+                    // and more (dq, 16384 tokens, 8/2 heads x 128: 530 -> 504 us; where P is made, too, waiting
+                    // for more than the next product wants costs as much as it saves).
+                    auto wait2 = [&](uint64_t *b0, uint32_t p0, uint64_t *b1, uint32_t p1) {
+                        return wait(lane & 1 ? b1 : b0, lane & 1 ? p1 : p0);
+                    };
                     auto do_s = [&](int i) {
                         const int tt = t + i, st = tt % N1;
-                        if (!wait(&bars.y1_full[st], (tt / N1) & 1)) return false;
+                        uint64_t *there = &bars.y1_full[st];
+                        const uint32_t phase = (tt / N1) & 1;
                         // S is read whole: in the others its P was, or a product in between waited for it
-                        if (!C::HAS_P && tt > 0 && !wait(&bars.s_free, (tt - 1) & 1)) return false;
+                        if (!C::HAS_P && tt > 0 ? !wait2(there, phase, &bars.s_free, (tt - 1) & 1) : !wait(there, phase))
+                            return false;
                         tc_fence_after();
                         scores(x1, y1 + st * STAGE, C::S_COL + (C::HAS_T ? 0 : (tt & 1) * 128));
                         commit(&bars.s_full[C::HAS_T ? 0 : tt & 1]);

@@ -264,7 +264,7 @@ struct PackedPlanArgs {
     int *arrived;         // [slots], zeroed
     PackedHeader *header;
     PackedTile *rows, *keys;
-    int *doc_tiles;       // [3][n_docs + 1]: row tiles, key tiles and 128-row blocks before each document
+    int *doc_tiles;       // [lists][3][n_docs + 1]: row tiles, key tiles and 128-row blocks before each document
     unsigned *doc_most;   // [2][n_docs], zeroed, or null
     unsigned *err;
 };

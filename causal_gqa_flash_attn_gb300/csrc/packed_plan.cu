@@ -1,7 +1,7 @@
 // packed_plan.cu -- the tiles of a packed batch, heaviest first, and the work
 // counters of the kernels that walk them (include/fa.h, fa_packed_attn).
 //
-// One block. Documents are summed (tiles before each of them), then the tiles are
+// A block for each list. Documents are summed (tiles before each of them), then the tiles are
 // counted into bins of their number of key tiles (or row tiles, for a tile of keys)
 // and put into the lists from the heaviest bin on. Within a bin the order may differ
 // from call to call: units do not depend on each other, so that no result does.
@@ -65,13 +65,14 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     __shared__ int small[3][kDocsInSmem + 1];
     __shared__ int bad_docs, n_slots;
     __shared__ unsigned long long all_rows;
-    const int tid = threadIdx.x, D = a.n_docs;
+    const int tid = threadIdx.x, D = a.n_docs, list = blockIdx.x;
     const bool fits = D <= kDocsInSmem;
     int *before[3];
-    for (int k = 0; k < 3; ++k) before[k] = fits ? small[k] : a.doc_tiles + static_cast<size_t>(k) * (D + 1);
+    for (int k = 0; k < 3; ++k) before[k] = fits ? small[k] : a.doc_tiles + static_cast<size_t>(3 * list + k) * (D + 1);
     if (tid == 0) bad_docs = 0;
-    if (tid < 4) a.header->counters[tid] = 0;
-    for (int i = tid; i < a.slots; i += kPlanThreads) a.arrived[i] = 0;
+    if (list == 0 && tid < 4) a.header->counters[tid] = 0;
+    if (list == 1)
+        for (int i = tid; i < a.slots; i += kPlanThreads) a.arrived[i] = 0;
     __syncthreads();
 
     // ---- tiles before each document: a thread sums a run of documents
@@ -96,7 +97,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
         int r, k, b;
         tiles(length(d), &r, &k, &b);
         nr += r, nk += k, nb += b;
-        if (a.doc_most) a.doc_most[d] = a.doc_most[D + d] = 0u;
+        if (list == 0 && a.doc_most) a.doc_most[d] = a.doc_most[D + d] = 0u;
     }
     if (bad) bad_docs = 1;
     scan3(nr, nk, nb, sum, part);
@@ -110,14 +111,11 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
         for (int k = 0; k < 3; ++k) before[k][D] = sum[k];
     __syncthreads();
     // documents that overlap (cu decreases) could have more tiles than there is room for
-    int total[2] = {sum[0], sum[1]};
-    if (bad_docs || total[0] > a.most_rows || total[1] > a.most_keys) {
-        total[0] = total[1] = 0;
-        if (tid == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
-    }
-    // ---- the lists
-    for (int list = 0; list < 2; ++list) {
-        const int n = total[list];
+    const bool wrong = bad_docs || sum[0] > a.most_rows || sum[1] > a.most_keys;
+    if (wrong && tid == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
+    const int n = wrong ? 0 : sum[list];
+
+    {
         PackedTile *out = list ? a.keys : a.rows;
         const int room = list ? a.most_keys : a.most_rows;
         // tile x, and how many tiles move past it
@@ -143,7 +141,10 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
                                            : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
             }
         };
+        // few tiles: each thread makes its own once
+        const bool once = n <= kPlanThreads;
         PackedTile t;
+        if (once && tid < n) tile(tid, &t);
         // the largest piece: at first 1 / parts of all row tiles, then what there is room for
         int most = 1 << 30;
         if (list && a.slots > 0 && n > 0) {
@@ -151,10 +152,12 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
             __syncthreads();
             unsigned long long mine = 0;
             for (int x = tid; x < n; x += kPlanThreads) {
-                tile(x, &t);
+                if (!once) tile(x, &t);
                 mine += t.rows;
             }
-            atomicAdd(&all_rows, mine);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
+            if ((tid & 31) == 0 && mine > 0) atomicAdd(&all_rows, mine);
             __syncthreads();
             most = max(kPackedLeastPiece, static_cast<int>((all_rows * a.n_kv + a.parts - 1) / a.parts));
         }
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
             if (tid == 0) n_slots = 0;
             int need = 0, more = 0, zero = 0;
             for (int x = tid; x < n; x += kPlanThreads) {
-                tile(x, &t);
+                if (!once) tile(x, &t);
                 const int p = pieces_of(t.rows);
                 more += p - 1;
                 if (p > 1) need += p;
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
             most *= 2;
         }
         if (tid == 0) (list ? a.header->key_tiles : a.header->row_tiles) = entries;
-        if (n == 0) continue;
+        if (n == 0) return;
         int shift = 0;  // bins of a power of two of tiles
         const int step = list ? a.step_tokens : a.key_tile;
         while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
         __syncthreads();
         // the pieces of a tile differ by one row tile at most, and share a bin
         for (int x = tid; x < n; x += kPlanThreads) {
-            tile(x, &t);
+            if (!once) tile(x, &t);
             const int p = pieces_of(t.rows);
             atomicAdd(&bins[bin_of((t.rows + p - 1) / p)], p);
         }
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
         bins[tid] = at;
         __syncthreads();
         for (int x = tid; x < n; x += kPlanThreads) {
-            tile(x, &t);
+            if (!once) tile(x, &t);
             const int p = pieces_of(t.rows), rows = t.rows, from = t.from;
             const int place = atomicAdd(&bins[bin_of((rows + p - 1) / p)], p);
             t.pieces = p;
@@ -210,14 +213,13 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
                 out[place + k] = t;
             }
         }
-        __syncthreads();
     }
 }
 
 }  // namespace
 
 cudaError_t launch_packed_plan(const PackedPlanArgs &a, cudaStream_t stream) {
-    return launch_after(packed_plan_kernel, dim3(1), kPlanThreads, 0, stream, a);
+    return launch_after(packed_plan_kernel, dim3(a.most_keys ? 2 : 1), kPlanThreads, 0, stream, a);
 }
 
 }  // namespace fa

@@ -138,4 +138,30 @@ __device__ __forceinline__ void encode_rows(const PagedAppendArgs &a, const floa
     }
 }
 
+// The same for one of both: 16 values of a row of K (or V).
+template <int HD, bool V>
+__device__ __forceinline__ void encode_row(const PagedAppendArgs &a, const float *x, bool live, int slot, int page,
+                                           int h, int l) {
+    uint32_t w[2];
+    __half scale;
+    uint16_t factor;
+    quantise16<HD / 16>(x, w, &scale, &factor);
+    if (!live) return;
+    const int pos = slot & ((1 << a.page_shift) - 1);
+    const int r = pos & (kGroupRows - 1), b = l >> 1, t = 2 * (l & 1);
+    uint8_t *dst = a.pages + ((static_cast<size_t>(page) * a.n_kv + h) * ((1 << a.page_shift) / kGroupRows) +
+                              pos / kGroupRows) * group_bytes(HD) + (V ? part_bytes(HD) : 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        if (V) {
+            *reinterpret_cast<uint16_t *>(dst + v_half_at<HD>(r, b, 2 * (t + j))) = static_cast<uint16_t>(w[j]);
+            *reinterpret_cast<uint16_t *>(dst + v_half_at<HD>(r, b, 2 * (t + j) + 1)) = static_cast<uint16_t>(w[j] >> 16);
+        } else {
+            *reinterpret_cast<uint32_t *>(dst + k_word_at<HD>(r, b, t + j)) = w[j];
+        }
+    }
+    if (t == 0) *reinterpret_cast<__half *>(dst + (V ? v_scale_at<HD>(r, b) : k_scale_at<HD>(r, b))) = scale;
+    if (l == 0) *reinterpret_cast<uint16_t *>(dst + factor_offset(HD) + 2 * r) = factor;
+}
+
 }  // namespace fa

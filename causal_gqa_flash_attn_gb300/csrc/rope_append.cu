@@ -15,10 +15,14 @@
 namespace fa {
 namespace {
 
+// Blocks of an SM: what hides q's latency is the number of threads, as in rope.cu (30000 tokens, 16/4 heads x 128
+// in bf16: 122 us with 2 blocks, 90 with 3, 78 with 4, 70 with 6, 78 with 8; fp32 104 with 4, 114 with 6).
+template <typename T>
+constexpr int kRopeBlocks = sizeof(T) == 4 ? 4 : 6;
 constexpr int kItems = 1024;  // items (two vectors of q, or a lane's values of K and V) of a block
 
 template <typename T, int HD, int V, bool ADJ>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppendArgs b) {
+__global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kernel(RopeAppendArgs b) {
     wait_for_stream();
     const RopeArgs &a = b.rope;
     const PagedAppendArgs &p = b.append;
@@ -44,65 +48,74 @@ __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(RopeAppendArg
         const int rows = n_tok * n_kv, l = threadIdx.x & (LANES - 1);
         for (int r0 = 0; r0 < rows; r0 += kRopeThreads / LANES) {
             const int row = r0 + threadIdx.x / LANES;
-            const int tok = row < rows ? row / n_kv : 0, h = kv0 + (row < rows ? row - tok * n_kv : 0);
+            // tokens first: a warp's rows are neighbours in a page, whose words they share
+            const int nth = row < rows ? row / n_tok : 0, tok = row < rows ? row - nth * n_tok : 0, h = kv0 + nth;
             const int slot = row < rows ? load(p.slot_map + tok0 + tok) : -1;
             const int page = slot >> p.page_shift;
             const bool live = slot >= 0 && page < p.n_pages;
             if (slot != -1 && !live && l == 0) flag_error(p.err, FA_ERRBIT_DEVICE);
-            float k[16] = {}, v[16] = {};
+            const long long t = tok0 + tok;
+            float x[16] = {};
+            const T *src = static_cast<const T *>(p.v) + t * p.v_stride + static_cast<long long>(h) * HD;
             if (live) {
-                const long long t = tok0 + tok;
-                const T *src = static_cast<const T *>(p.v) + t * p.v_stride + static_cast<long long>(h) * HD;
-                load8<T>(src + 16 * l, v);
-                load8<T>(src + 16 * l + 8, v + 8);
-                src = static_cast<const T *>(p.k) + t * p.k_stride + static_cast<long long>(h) * HD;
-                load8<T>(src + 16 * l, k);
-                load8<T>(src + 16 * l + 8, k + 8);
+                load8<T>(src + 16 * l, x);
+                load8<T>(src + 16 * l + 8, x + 8);
+            }
+            encode_row<HD, true>(p, x, live, slot, page, h, l);
+            src = static_cast<const T *>(p.k) + t * p.k_stride + static_cast<long long>(h) * HD;
+            if (live) {
+                load8<T>(src + 16 * l, x);
+                load8<T>(src + 16 * l + 8, x + 8);
                 const float *c = cs + tok * half, *s = sn + tok * half;
                 if (ADJ) {
 #pragma unroll
                     for (int i = 0; i < 16; i += 2) {
                         const int pair = 8 * l + i / 2;
                         if (pair < half) {
-                            const float u0 = k[i], u1 = k[i + 1];
-                            k[i] = Conv<T>::get(Conv<T>::put(u0 * c[pair] - u1 * s[pair]));
-                            k[i + 1] = Conv<T>::get(Conv<T>::put(u0 * s[pair] + u1 * c[pair]));
+                            const float u0 = x[i], u1 = x[i + 1];
+                            x[i] = Conv<T>::get(Conv<T>::put(u0 * c[pair] - u1 * s[pair]));
+                            x[i + 1] = Conv<T>::get(Conv<T>::put(u0 * s[pair] + u1 * c[pair]));
+                        }
+                    }
+                } else if (V > 1) {  // half is a multiple of 8: eight values on one side
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8) {
+                        const int d = 16 * l + e;
+                        if (d >= rd) continue;
+                        // The low side is fma(own, cos, -(other * sin)), the high one fma(other, sin, own * cos):
+                        // what the compiler makes of rope.cu's sums.
+                        const bool low = d < half;
+                        const int pair = low ? d : d - half;
+                        const float *f = (low ? c : s) + pair, *g = (low ? s : c) + pair;
+                        float o[8];
+                        load8<T>(src + (low ? d + half : d - half), o);
+#pragma unroll
+                        for (int i = 0; i < 8; i += 4) {
+                            const float4 fv = lds_f4(f + i), gv = lds_f4(g + i);
+                            const float f4[4] = {fv.x, fv.y, fv.z, fv.w}, g4[4] = {gv.x, gv.y, gv.z, gv.w};
+#pragma unroll
+                            for (int m = 0; m < 4; ++m) {
+                                const float own = x[e + i + m], other = o[i + m];
+                                const float r = fmaf(low ? own : other, f4[m], (low ? -other : own) * g4[m]);
+                                x[e + i + m] = Conv<T>::get(Conv<T>::put(r));
+                            }
                         }
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8) {
-                        const int d = 16 * l + e;
-                        if (half % 8 == 0) {  // eight values on one side
-                            if (d < rd) {
-                                const bool low = d < half;
-                                float o[8];
-                                load8<T>(src + (low ? d + half : d - half), o);
-                                const int pair = low ? d : d - half;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    const float u0 = low ? k[e + i] : o[i], u1 = low ? o[i] : k[e + i];
-                                    const float x = u0 * c[pair + i] - u1 * s[pair + i];
-                                    const float y = u0 * s[pair + i] + u1 * c[pair + i];
-                                    k[e + i] = Conv<T>::get(Conv<T>::put(low ? x : y));
-                                }
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (d + i >= rd) continue;
-                                const bool low = d + i < half;
-                                const float o = Conv<T>::get(src[low ? d + i + half : d + i - half]);
-                                const int pair = low ? d + i : d + i - half;
-                                const float u0 = low ? k[e + i] : o, u1 = low ? o : k[e + i];
-                                const float x = u0 * c[pair] - u1 * s[pair], y = u0 * s[pair] + u1 * c[pair];
-                                k[e + i] = Conv<T>::get(Conv<T>::put(low ? x : y));
-                            }
-                        }
+                    for (int i = 0; i < 16; ++i) {
+                        const int d = 16 * l + i;
+                        if (d >= rd) continue;
+                        const bool low = d < half;
+                        const float o = Conv<T>::get(src[low ? d + half : d - half]);
+                        const int pair = low ? d : d - half;
+                        const float u0 = low ? x[i] : o, u1 = low ? o : x[i];
+                        const float x0 = u0 * c[pair] - u1 * s[pair], x1 = u0 * s[pair] + u1 * c[pair];
+                        x[i] = Conv<T>::get(Conv<T>::put(low ? x0 : x1));
                     }
                 }
             }
-            encode_rows<HD>(p, k, v, live, slot, page, h, l);
+            encode_row<HD, false>(p, x, live, slot, page, h, l);
         }
     }
     // ---- q
@@ -119,6 +132,7 @@ cudaError_t launch(RopeAppendArgs b, cudaStream_t stream) {
                           static_cast<long long>(b.append.n_kv) * (HD / 16);  // items of a token
     const int fit = std::min<int>(kRopeTokens, 48 * 1024 / (half * 8));
     int tokens = static_cast<int>(std::min<long long>(fit, std::max<long long>(1, kItems / row)));
+    if (a.n_tokens >= 2 * fit * device_sm_count()) tokens = fit;
     // few tokens: a block takes one, and the heads are split over blocks too, as in rope.cu
     const int sms = device_sm_count();
     if (a.n_tokens <= sms * tokens) tokens = std::max(1, a.n_tokens / sms);
@@ -134,11 +148,11 @@ cudaError_t launch(RopeAppendArgs b, cudaStream_t stream) {
     return launch_after(rope_append_kernel<T, HD, V, false>, grid, kRopeThreads, smem, stream, b);
 }
 
-// q moves 16 bytes at a time where a vector of it lies on one side of its pairs.
+// q moves 16 bytes at a time, and k's values eight at a time, where those lie on one side of their pairs.
 template <typename T, int HD>
 cudaError_t launch_hd(const RopeAppendArgs &b, cudaStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    return b.rope.rotary_dim / 2 % V == 0 ? launch<T, HD, V>(b, stream) : launch<T, HD, 1>(b, stream);
+    return b.rope.rotary_dim / 2 % 8 == 0 ? launch<T, HD, V>(b, stream) : launch<T, HD, 1>(b, stream);
 }
 
 template <typename T>
