@@ -49,7 +49,7 @@ Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_
     const long long row_tiles = static_cast<long long>(n_tokens) * group / fa::packed_grad_rows(head_dim) + 1;
     const size_t slot = sizeof(float) * 128 * head_dim * (head_dim < 256 ? 2 : 1);
     w.slots = 0;
-    if (grad && row_tiles > fa::kPackedLeastPiece)
+    if (grad && row_tiles > 2 * fa::kPackedLeastPiece)
         w.slots = static_cast<int>(std::min<long long>(kPartialBytes / slot, tiles * (row_tiles / fa::kPackedLeastPiece + 1)));
     w.most_rows = static_cast<int>(static_cast<long long>(n_tokens) * group / rows) + n_docs;
     w.most_keys = grad ? n_tokens / 128 + n_docs + w.slots : 0;
@@ -63,7 +63,7 @@ Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_
     w.row_tiles = take(sizeof(fa::PackedTile) * w.most_rows);
     w.key_tiles = take(sizeof(fa::PackedTile) * w.most_keys);
     w.doc_tiles = take(sizeof(int) * 3 * (grad ? 2 : 1) * (static_cast<size_t>(n_docs) + 1));
-    w.doc_most = take(grad ? sizeof(unsigned) * 2 * n_docs : 0);
+    w.doc_most = take(grad ? sizeof(unsigned) * 2 * std::max<size_t>(n_docs, n_kv_heads * w.blocks) : 0);
     w.stats = take(grad ? sizeof(float) * 2 * n_kv_heads * w.blocks * 128 : 0);
     w.arrived = take(sizeof(int) * w.slots);
     w.partial = take(slot * w.slots);
@@ -186,10 +186,15 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
     a.score = fa::score_rule(scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim)), cap);
     a.err = err;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = fa::launch_packed_plan(p, s);
-    if (e != cudaSuccess) return from_cuda(e);
-    const int blocks = static_cast<int>(
-        std::min<long long>(fa::device_sm_count(), static_cast<long long>(w.most_rows) * n_kv_heads));
+    const long long units = static_cast<long long>(w.most_rows) * n_kv_heads;
+    const int blocks = static_cast<int>(std::min<long long>(fa::device_sm_count(), units));
+    a.direct = fa::PackedDirect{};
+    if (n_docs <= fa::kDirectDocs && units <= fa::device_sm_count()) {
+        a.direct = fa::PackedDirect{cu_docs, prefix, n_docs, n_tokens};
+    } else {
+        const cudaError_t e = fa::launch_packed_plan(p, s);
+        if (e != cudaSuccess) return from_cuda(e);
+    }
     return from_cuda(dtype == FA_T_BF16 ? fa::launch_packed_fwd_bf16(a, head_dim, cap > 0.0f, blocks, s)
                                         : fa::launch_packed_fwd_f16(a, head_dim, cap > 0.0f, blocks, s));
 }
@@ -278,12 +283,22 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     t.L = reinterpret_cast<float *>(ws + w.stats);
     t.D = t.L + static_cast<size_t>(n_kv_heads) * w.blocks * 128;
     t.doc_most = p.doc_most;
+    t.sink = p.sink;
+    t.win = p.win;
+    t.err = err;
+    // no plan where every unit has a block of its own and no tile of keys has rows enough to be cut
+    const int sms = fa::device_sm_count();
+    const bool direct = n_docs <= fa::kDirectDocs && w.slots == 0 &&
+                        static_cast<long long>(w.most_rows) * n_kv_heads <= sms &&
+                        static_cast<long long>(w.most_keys) * n_kv_heads <= sms;
+    t.direct = direct ? fa::PackedDirect{cu_docs, prefix, n_docs, n_tokens} : fa::PackedDirect{};
 
     fa::PackedGradArgs a;
     a.header = p.header;
     a.L = t.L;
     a.D = t.D;
     a.blocks = t.blocks;
+    a.direct = t.direct;
     a.partial = reinterpret_cast<float *>(ws + w.partial);
     a.arrived = p.arrived;
     a.doc_most = p.doc_most;
@@ -321,7 +336,6 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
         !map_rows(&b.y2, dtype, dout, dout_stride, n_tokens, n_kv_heads, group, head_dim, step))
         return FA_ERR_CUDA;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int sms = fa::device_sm_count();
     auto blocks_of = [&](int tiles, int most) {
         return static_cast<int>(std::min<long long>(most, static_cast<long long>(tiles) * n_kv_heads));
     };
@@ -329,8 +343,9 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
         return dtype == FA_T_BF16 ? fa::launch_packed_grad_bf16(g, mode, head_dim, cap > 0.0f, blocks, s)
                                   : fa::launch_packed_grad_f16(g, mode, head_dim, cap > 0.0f, blocks, s);
     };
-    cudaError_t e = fa::launch_packed_plan(p, s);
-    if (e == cudaSuccess) e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, 8 * sms), s);
+    cudaError_t e = direct ? cudaSuccess : fa::launch_packed_plan(p, s);
+    if (e == cudaSuccess)
+        e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, direct ? sms : 8 * sms), s);
     if (e == cudaSuccess) e = launch(a, fa::kGradQ, blocks_of(w.most_rows, sms));
     if (head_dim < 256) {
         if (e == cudaSuccess) e = launch(b, fa::kGradKV, blocks_of(w.most_keys, sms));

@@ -171,14 +171,19 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
         if (warp == 0) {
             // ------------------------------------------------------------- copies
-            const int units = *a.n_tiles * a.n_kv;
+            // without a plan: the one unit of this block
+            const bool direct = a.direct.cu != nullptr;
+            PackedTile own;
+            const int units = a.n_kv * (direct ? direct_tile<!C::ROWS_STAY>(a.direct, blockIdx.x / a.n_kv, tile_tokens, step_tokens,
+                                                                            7 - lg, a.sink, a.win, err, &own)
+                                               : *a.n_tiles);
             Arms x_arms, y1_arms[3], y2_arms[3], l_arms[2];
             int patches = 0;
             bool ok = true;
             auto fetch = [&](int w, PackedTile *u) {
                 u->head = -1;
-                if (w >= units) return false;
-                *u = a.tiles[w / a.n_kv];
+                if (w >= units || (direct && w != static_cast<int>(blockIdx.x))) return false;
+                *u = direct ? own : a.tiles[w / a.n_kv];
                 u->head = w % a.n_kv;
                 return true;
             };
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     if (ok && !C::ROWS_STAY) ok = load_stats(t + i, at, u);
                     if (ok) ok = load_y(t + i, at, u, false);
                     if (ok && i == cnt - 1) {
-                        if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                        if (lane == 0) w = direct ? units : static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
                         w = __shfl_sync(~0u, w, 0);
                         more = fetch(w, &un);
                     }
@@ -442,8 +447,20 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             }
             float up = 1.0f;  // the document's power of two
             if (!BF16) {
-                const float b = 2.0f * sqrtf(__uint_as_float(load(a.doc_most + u.doc))) *
-                                sqrtf(__uint_as_float(load(a.doc_most + a.n_docs + u.doc)));
+                unsigned most[2];
+                if (a.direct.cu) {  // of all blocks of the document
+                    const int blocks = ((u.len << lg) + 127) >> 7;
+                    for (int k = 0; k < 2; ++k) {
+                        unsigned m = 0;
+                        for (int e = lane; e < blocks * a.n_kv; e += 32)
+                            m = max(m, load(a.doc_most + (static_cast<size_t>(k) * a.n_kv + e / blocks) * a.blocks + u.rb + e % blocks));
+                        most[k] = __reduce_max_sync(~0u, m);
+                    }
+                } else {
+                    most[0] = load(a.doc_most + u.doc);
+                    most[1] = load(a.doc_most + a.n_docs + u.doc);
+                }
+                const float b = 2.0f * sqrtf(__uint_as_float(most[0])) * sqrtf(__uint_as_float(most[1]));
                 if (b > 0.0f && b < 3e38f) {
                     const int e = static_cast<int>(__float_as_uint(b) >> 23) - 127;  // b < 2^(e + 1)
                     up = __uint_as_float(static_cast<uint32_t>(127 + min(max(13 - e, -100), 100)) << 23);

@@ -121,14 +121,19 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
         if constexpr (NT == 2) fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
         if (warp == 0) {
             // ------------------------------------------------------------- copies
-            const int units = a.header->row_tiles * a.n_kv;
+            // without a plan: the one unit of this block
+            const bool direct = a.direct.cu != nullptr;
+            PackedTile own;
+            const int units = a.n_kv * (direct ? direct_tile<false>(a.direct, blockIdx.x / a.n_kv, row_tokens, 1,
+                                                                    7 - a.log_group, a.sink, a.win, err, &own)
+                                               : a.header->row_tiles);
             Arms q_arms, k_arms[2], v_arms[2];
             int patches = 0;
             bool ok = true;
             auto fetch = [&](int w, PackedTile *u) {
                 u->head = -1;
-                if (w >= units) return false;
-                *u = a.rows[w / a.n_kv];
+                if (w >= units || (direct && w != static_cast<int>(blockIdx.x))) return false;
+                *u = direct ? own : a.rows[w / a.n_kv];
                 u->head = w % a.n_kv;
                 return true;
             };
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 for (int i = 0; i < cnt && ok; ++i) {
                     ok = load_kv(t + i, plan.at(i), u, true);
                     if (ok && i == cnt - 1) {  // the next unit, under the waits for the last tiles
-                        if (lane == 0) w = static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                        if (lane == 0) w = direct ? units : static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
                         w = __shfl_sync(~0u, w, 0);
                         more = fetch(w, &un);
                     }
@@ -267,20 +272,23 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                         // one S for each tile: its next product follows the one that reads its P
                         for (int i = 0; i <= count && ok; ++i) {
                             const int tt = t + i;
-                            if (i < count && !(ok = wait_kv(bars.k_full, tt))) break;
+                            // K of this step and V of the last one, each looked at by half of the lanes
+                            const int kt = i < count ? tt : tt - 1, vt = i > 0 ? tt - 1 : tt;
+                            const bool on_k = i == 0 || (i < count && (lane & 1));
+                            if (!(ok = wait(on_k ? &bars.k_full[kt % NS] : &bars.v_full[vt % NS],
+                                            ((on_k ? kt : vt) / NS) & 1)))
+                                break;
+                            tc_fence_after();
 #pragma unroll
                             for (int tile = 0; tile < 2; ++tile) {
                                 if (i > 0) {
-                                    ok = ok && wait_p(tile, tt - 1, i == 1, tile, (tt - 1) & 1);
-                                    if (ok && tile == 0) ok = wait_kv(bars.v_full, tt - 1);
-                                    if (!ok) break;
+                                    if (!(ok = wait_p(tile, tt - 1, i == 1, tile, (tt - 1) & 1))) break;
                                     tc_fence_after();
                                     issue_pv(tile, tt - 1, i == 1);
                                     if (tile == 1) commit(&bars.v_empty[(tt - 1) % NS]);
                                     if (i == count) commit(&bars.o_last[tile]);
                                 }
                                 if (i < count) {
-                                    tc_fence_after();
                                     issue_s(tile, tt);
                                     commit(&bars.s_full[tile]);
                                     if (tile == 1) {
@@ -348,6 +356,8 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             for (int i = 0; i < plan.count; ++i) {
                 const int tt = t + i;
                 const int bar = NT == 2 ? tile : tt & 1;
+                const int j0 = plan.at(i) * BK, j1 = j0 + BK - 1;
+                const bool whole = sees_all(p0, p1, j0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= p0);
                 ok = mbar_wait(&bars.s_full[bar], (NT == 2 ? tt : tt >> 1) & 1, abort, err);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
@@ -360,8 +370,6 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) reg_fence32(s + 32 * c);
 
-                const int j0 = plan.at(i) * BK, j1 = j0 + BK - 1;
-                const bool whole = sees_all(p0, p1, j0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= p0);
                 constexpr bool kScaled = CAP || BIAS;  // s goes to the exp2 domain first
                 if (kScaled) {
                     const float far = static_cast<float>(p - j0);  // exact: below 2^26 apart
@@ -420,30 +428,15 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                     }
                     m_used = m_new;
                 }
-                const Two ref = two(m_used == -INFINITY ? 0.0f : kFwdShift - m_used);
-                uint32_t pk[64];
-                Two sums[2] = {two(0.0f), two(0.0f)};
-#pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    const Two x = two(__uint_as_float(s[2 * c]), __uint_as_float(s[2 * c + 1]));
-                    float2 f = both(kScaled ? x + ref : fma2(x, two(rule.a), ref));
-                    f = make_float2(ex2(f.x), ex2(f.y));
-                    sums[c & 1] = sums[c & 1] + two(f.x, f.y);
-                    pk[c] = pack2<BF16>(f.x, f.y);
-                }
-                const float2 sum = both(sums[0] + sums[1]);
-                l += sum.x + sum.y;
                 // O is rescaled when every product into it is done. With one S a tile that
                 // holds already: S(tt) was issued after them. With two, PV(tt - 1) may still run.
-                const bool any = __any_sync(~0u, moves);
-                if (NT == 1 && any) {
-                    ok = mbar_wait(&bars.o_done, (tt - 1) & 1, abort, err);
-                    ok = __all_sync(~0u, ok);
-                    if (!ok) break;
-                    tc_fence_after();
-                }
-                __syncwarp();
-                if (any) {
+                if (__any_sync(~0u, moves)) {
+                    if (NT == 1) {
+                        ok = mbar_wait(&bars.o_done, (tt - 1) & 1, abort, err);
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
 #pragma unroll 1
                     for (int c = 0; c < HD / 32; ++c) {
                         uint32_t o[32];
@@ -456,8 +449,23 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                         tmem_st32(oc, o);
                     }
                 }
-                tmem_st32(scol, pk);
-                tmem_st32(scol + 32, pk + 32);
+                const Two ref = two(m_used == -INFINITY ? 0.0f : kFwdShift - m_used);
+                Two sums[2] = {two(0.0f), two(0.0f)};
+#pragma unroll
+                for (int half = 0; half < 128; half += 64) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const Two x = two(__uint_as_float(s[half + 2 * c]), __uint_as_float(s[half + 2 * c + 1]));
+                        float2 f = both(kScaled ? x + ref : fma2(x, two(rule.a), ref));
+                        f = make_float2(ex2(f.x), ex2(f.y));
+                        sums[c & 1] = sums[c & 1] + two(f.x, f.y);
+                        pk[c] = pack2<BF16>(f.x, f.y);
+                    }
+                    tmem_st32(scol + half / 2, pk);
+                }
+                const float2 sum = both(sums[0] + sums[1]);
+                l += sum.x + sum.y;
                 tmem_wait_st();
                 tc_fence_before();
                 warp_arrive(&bars.p_full[bar]);

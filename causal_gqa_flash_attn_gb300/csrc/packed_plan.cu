@@ -60,6 +60,7 @@ __device__ __forceinline__ int find_doc(const int *before, int n, int x) {
 
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArgs a) {
     wait_for_stream();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel sets itself up meanwhile
     __shared__ int part[3][32], sum[3];
     __shared__ int bins[kBins];
     __shared__ int small[3][kDocsInSmem + 1];

@@ -16,10 +16,17 @@ constexpr float kNoRow = -1e30f;
 template <int HD, bool BF16>
 __global__ void __launch_bounds__(kStatsThreads) packed_stats_kernel(PackedStatsArgs a) {
     wait_for_stream();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel sets itself up meanwhile
     constexpr int LANES = HD / 8, ROWS = kStatsThreads / LANES;  // lanes of a row, rows at once
     const int row0 = threadIdx.x / LANES, l = threadIdx.x % LANES, lane = threadIdx.x & 31;
     const int lg = a.log_group;
-    const int units = a.header->row_tiles * a.n_kv;
+    const bool direct = a.direct.cu != nullptr;
+    __shared__ unsigned most_of[2];
+    PackedTile own;  // without a plan: the block's one tile
+    int n_tiles = 0;
+    if (direct)
+        n_tiles = direct_tile<false>(a.direct, blockIdx.x / a.n_kv, 128 >> lg, 1, 7 - lg, a.sink, a.win, a.err, &own);
+    const int units = a.n_kv * (direct ? n_tiles : a.header->row_tiles);
     auto dot = [](uint4 x, uint4 y) {
         const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
         float s = 0.0f;
@@ -37,11 +44,11 @@ __global__ void __launch_bounds__(kStatsThreads) packed_stats_kernel(PackedStats
         return x;
     };
     for (int w = blockIdx.x; w < units; w += gridDim.x) {
-        const PackedTile u = a.rows[w / a.n_kv];
+        const PackedTile u = direct ? own : a.rows[w / a.n_kv];
         const int g = w % a.n_kv;
         const size_t base = (static_cast<size_t>(g) * a.blocks + u.rb + (static_cast<long long>(u.p0) << lg >> 7)) * 128;
         float most = 0.0f, most_v = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
         for (int r = row0; r < 128; r += ROWS) {
             const int tok = u.p0 + (r >> lg), head = (g << lg) + (r & ((1 << lg) - 1));
             const bool live = tok < u.len;
@@ -79,7 +86,17 @@ __global__ void __launch_bounds__(kStatsThreads) packed_stats_kernel(PackedStats
             // largest bits: those of numbers that are not negative are in their order, a NaN above them
             const unsigned md = __reduce_max_sync(~0u, __float_as_uint(most) & 0x7fffffffu);
             const unsigned mv = __reduce_max_sync(~0u, __float_as_uint(most_v) & 0x7fffffffu);
-            if (lane == 0) {
+            if (direct) {
+                if (threadIdx.x < 2) most_of[threadIdx.x] = 0;
+                __syncthreads();
+                if (lane == 0) {
+                    atomicMax(most_of, md);
+                    atomicMax(most_of + 1, mv);
+                }
+                __syncthreads();
+                if (threadIdx.x < 2)
+                    a.doc_most[(static_cast<size_t>(threadIdx.x) * a.n_kv) * a.blocks + base / 128] = most_of[threadIdx.x];
+            } else if (lane == 0) {
                 atomicMax(a.doc_most + u.doc, md);
                 atomicMax(a.doc_most + a.n_docs + u.doc, mv);
             }
