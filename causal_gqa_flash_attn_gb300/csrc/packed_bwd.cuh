@@ -142,7 +142,12 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem_base;
-    wait_for_stream();
+    // dk (and dv) do not use dq: their blocks take the SMs that dq's leave. They begin when dq's have seen
+    // the row numbers, which are all that they need, and end when dq's have, so that what follows them in
+    // the stream follows dq as well. (dv alone uses dk's partial sums, and comes after it.)
+    constexpr bool FOLLOWS = MODE == kGradKV || MODE == kGradK;
+    if (!FOLLOWS) wait_for_stream();
+    if (MODE == kGradQ) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     auto next_unit = [&](int j, PackedTile *u) -> bool {
         const int slot = j % kPackedRing;
@@ -700,6 +705,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (FOLLOWS) wait_for_stream();
 }
 
 template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
