@@ -71,7 +71,7 @@ struct GradBars {
     uint64_t y1_full[3], y1_empty[3], y2_full[3], y2_empty[3];
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full[2], s_free, p_full[2], t_full[2], dt_full[2];
-    uint64_t acc_last, acc_free;
+    uint64_t acc_last, acc_free, meet;
     uint64_t patch, drain;
     UnitRing ring;
     uint32_t tmem_base;
@@ -120,6 +120,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         }
         mbar_init(&bars.s_free, C::COMPUTE / 32);
         mbar_init(&bars.acc_last, 1);
+        mbar_init(&bars.meet, C::COMPUTE / 32);
         mbar_init(&bars.acc_free, C::COMPUTE / 32);
         mbar_init(&bars.patch, 1);
         mbar_init(&bars.drain, 1);
@@ -421,6 +422,12 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int group = 1 << lg;
         const ScoreRule rule = a.score;
+        // all of these threads: what each wrote before is there for the others (a wait with a bound)
+        int meets = 0;
+        auto meet = [&]() {
+            warp_arrive(&bars.meet);
+            return static_cast<bool>(__all_sync(~0u, mbar_wait(&bars.meet, meets++ & 1, abort, err)));
+        };
         int t = 0;
         bool ok = true;
         PackedTile u;
@@ -442,13 +449,13 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 if (BIAS) slope2 = load(a.slopes + head) * -kPackedLog2e;
             }
             if (BIAS && !C::ROWS_STAY) {  // (the slopes of the last unit have been used)
-                named_barrier_sync(1, C::COMPUTE);
+                if (!(ok = meet())) break;
                 const int c = threadIdx.x - 128;
                 if (c < 16) {
                     bias_s[c] = load(a.slopes + (u.head << lg) + (c & (group - 1))) * -kPackedLog2e;
                     bias_s[16 + c] = static_cast<float>(c >> lg);
                 }
-                named_barrier_sync(1, C::COMPUTE);
+                if (!(ok = meet())) break;
             }
             float up = 1.0f;  // the document's power of two
             if (!BF16) {
@@ -673,13 +680,13 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             if (!alone) {
                 // the block that is done last adds the pieces, in their order
                 __threadfence();
-                named_barrier_sync(1, C::COMPUTE);
+                if (!(ok = meet())) break;
                 if (threadIdx.x == 128) {
                     bars.last = atomicAdd(a.arrived + slot0, 1) == u.pieces - 1;
                     if (bars.last) a.arrived[slot0] = 0;  // for the next kernel
                     __threadfence();
                 }
-                named_barrier_sync(1, C::COMPUTE);
+                if (!(ok = meet())) break;
                 if (*static_cast<volatile int *>(&bars.last)) {
                     __threadfence();
 #pragma unroll 1

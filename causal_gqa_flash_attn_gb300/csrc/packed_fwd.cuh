@@ -40,14 +40,18 @@ struct FwdCfg {
     // one block an SM, which owns all of TMEM
     static constexpr uint32_t SMEM = (OFF_END + 1024 > 120u * 1024u) ? OFF_END + 1024 : 120u * 1024u;
     static constexpr uint32_t S_COL = 256;  // O in columns 0 .. 255
-    static constexpr int THREADS = 128 + 128 * NT;
+    static constexpr int THREADS = 384;
+    // Two warpgroups: one for each tile, or with one tile each half of its columns.
+    static constexpr int COLS = NT == 2 ? 128 : 64;  // columns of S of a thread
+    static constexpr int DIMS = NT == 2 ? HD : HD / 2;  // and of O
+    static constexpr int ARRIVE = NT == 2 ? 4 : 8;   // warps that a tile's barriers wait for
 };
 
 struct FwdBars {
     uint64_t q_full, q_empty;
     uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
     uint64_t s_full[2], p_full[2], o_last[2], o_free[2];
-    uint64_t o_done, patch, drain;
+    uint64_t o_done, patch, drain, meet;
     UnitRing ring;
     uint32_t tmem_base;
     int abort;
@@ -62,6 +66,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
     constexpr uint32_t IDESC_PV = idesc_16<BF16>(128, HD, 0, 1);
     extern __shared__ uint8_t smem_raw[];
     __shared__ FwdBars bars;
+    __shared__ float shared_max[NT == 2 ? 1 : 2][2][NT == 2 ? 1 : 128];  // one tile: of a row's two halves
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -77,16 +82,17 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             mbar_init(&bars.v_full[s], 1);
             mbar_init(&bars.v_empty[s], 1);
             mbar_init(&bars.s_full[s], 1);
-            mbar_init(&bars.p_full[s], 4);
+            mbar_init(&bars.p_full[s], C::ARRIVE);
             mbar_init(&bars.o_last[s], 1);
-            mbar_init(&bars.o_free[s], 4);
+            mbar_init(&bars.o_free[s], C::ARRIVE);
         }
         mbar_init(&bars.o_done, 1);
         mbar_init(&bars.patch, 1);
         mbar_init(&bars.drain, 1);
+        mbar_init(&bars.meet, 8);
         for (int k = 0; k < kPackedRing; ++k) {
             mbar_init(&bars.ring.full[k], 1);
-            mbar_init(&bars.ring.empty[k], 1 + 4 * NT);  // the MMA thread and the softmax warps
+            mbar_init(&bars.ring.empty[k], 1 + 8);  // the MMA thread and the softmax warps
         }
         bars.abort = 0;
         mbar_fence_init();
@@ -118,7 +124,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
     };
 
     if (warp < 4) {
-        if constexpr (NT == 2) fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
+        fewer_registers<72>();  // 128 x 72 + 256 x 216 = the launch's 384 x 168
         if (warp == 0) {
             // ------------------------------------------------------------- copies
             // without a plan: the one unit of this block
@@ -330,13 +336,25 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             }
         }
     } else {
-        if constexpr (NT == 2) more_registers<216>();
+        more_registers<216>();
         // ------------------------------------------------- softmax and output
-        const int tile = (warp - 4) >> 2;  // this warp's tile of the unit
-        const int r = threadIdx.x - 128 - 128 * tile;  // row of the tile: TMEM lane
+        constexpr int COLS = C::COLS, DIMS = C::DIMS;
+        const int group = (warp - 4) >> 2;
+        const int tile = NT == 2 ? group : 0;  // this warp's tile of the unit
+        const int part = NT == 2 ? 0 : group;  // and its half of the columns
+        const int r = threadIdx.x & 127;       // row of the tile: TMEM lane
         const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const int lg = a.log_group, tile_tokens = 128 >> lg;
         const ScoreRule rule = a.score;
+        // both halves' threads: what each wrote before is there for the other (a wait with a bound)
+        int meets = 0;
+        auto meet = [&]() {
+            tc_fence_before();
+            warp_arrive(&bars.meet);
+            const bool got = mbar_wait(&bars.meet, meets++ & 1, abort, err);
+            tc_fence_after();
+            return static_cast<bool>(__all_sync(~0u, got));
+        };
         int t = 0;
         bool ok = true;
         PackedTile u;
@@ -356,19 +374,17 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             for (int i = 0; i < plan.count; ++i) {
                 const int tt = t + i;
                 const int bar = NT == 2 ? tile : tt & 1;
-                const int j0 = plan.at(i) * BK, j1 = j0 + BK - 1;
+                const int j0 = plan.at(i) * BK + part * COLS, j1 = j0 + COLS - 1;  // its keys
                 const bool whole = sees_all(p0, p1, j0, j1, u.prefix, a.sink, a.win) && (!BIAS || j1 <= p0);
                 ok = mbar_wait(&bars.s_full[bar], (NT == 2 ? tt : tt >> 1) & 1, abort, err);
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t scol = tmem + lane_base + C::S_COL + bar * 128;
-                uint32_t s[128];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) tmem_ld32(scol + 32 * c, s + 32 * c);
+                uint32_t s[COLS];
+                tmem_ld<COLS>(scol + part * COLS, s);
                 tmem_wait_ld();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) reg_fence32(s + 32 * c);
+                reg_fence<COLS>(s);
 
                 constexpr bool kScaled = CAP || BIAS;  // s goes to the exp2 domain first
                 if (kScaled) {
@@ -376,7 +392,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                     auto score = [&](auto masks) {
                         constexpr bool MASK = decltype(masks)::value;
 #pragma unroll
-                        for (int c = 0; c < 128; c += 2) {
+                        for (int c = 0; c < COLS; c += 2) {
                             Two x = two(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), off = two(0.0f);
                             if (BIAS) {
                                 Two d = two(far) + two(-static_cast<float>(c), -static_cast<float>(c + 1));
@@ -403,7 +419,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                     const int lo = a.win > 0 ? p - a.win + 1 - j0 : 0;
                     const int first = max(u.prefix - j0, a.win > 0 ? min(a.sink - j0, hi + 1) : 0);
 #pragma unroll
-                    for (int c = 0; c < 128; ++c)
+                    for (int c = 0; c < COLS; ++c)
                         if (!((c < first) | ((c >= lo) & (c <= hi)))) s[c] = __float_as_uint(-INFINITY);
                 }
                 // four chains, so that none of them is waited for
@@ -411,13 +427,20 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx4[e] = __uint_as_float(s[e]);
 #pragma unroll
-                for (int c = 4; c < 124; c += 8)
+                for (int c = 4; c < COLS - 4; c += 8)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         mx4[e] = max3(mx4[e], __uint_as_float(s[c + 2 * e]), __uint_as_float(s[c + 2 * e + 1]));
-                const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), max3(mx4[3], __uint_as_float(s[124]), __uint_as_float(s[125])),
-                                      fmaxf(__uint_as_float(s[126]), __uint_as_float(s[127])));
-                const float m_new = fmaxf(m_used, kScaled ? mx : mx * rule.a);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], __uint_as_float(s[COLS - 4 + e]));
+                float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
+                if (!kScaled) mx *= rule.a;
+                if (NT == 1) {  // of the whole row; and every S of the tile is read, where P goes
+                    shared_max[tt & 1][part][r] = mx;
+                    if (!(ok = meet())) break;
+                    mx = fmaxf(mx, shared_max[tt & 1][part ^ 1][r]);
+                }
+                const float m_new = fmaxf(m_used, mx);
                 float corr = 1.0f;
                 bool moves = false;
                 if (m_new > m_used + kFwdLift) {
@@ -438,9 +461,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                         tc_fence_after();
                     }
 #pragma unroll 1
-                    for (int c = 0; c < HD / 32; ++c) {
+                    for (int c = 0; c < DIMS / 32; ++c) {
                         uint32_t o[32];
-                        const uint32_t oc = tmem + lane_base + tile * HD + 32 * c;
+                        const uint32_t oc = tmem + lane_base + tile * HD + part * DIMS + 32 * c;
                         tmem_ld32(oc, o);
                         tmem_wait_ld();
                         reg_fence32(o);
@@ -452,7 +475,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 const Two ref = two(m_used == -INFINITY ? 0.0f : kFwdShift - m_used);
                 Two sums[2] = {two(0.0f), two(0.0f)};
 #pragma unroll
-                for (int half = 0; half < 128; half += 64) {
+                for (int half = 0; half < COLS; half += 64) {
                     uint32_t pk[32];
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
@@ -462,7 +485,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                         sums[c & 1] = sums[c & 1] + two(f.x, f.y);
                         pk[c] = pack2<BF16>(f.x, f.y);
                     }
-                    tmem_st32(scol + half / 2, pk);
+                    tmem_st32(scol + part * (COLS / 2) + half / 2, pk);
                 }
                 const float2 sum = both(sums[0] + sums[1]);
                 l += sum.x + sum.y;
@@ -476,20 +499,27 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             ok = __all_sync(~0u, ok);
             if (!ok) break;
             tc_fence_after();
+            if (NT == 1) {
+                // (the buffer that the next tile does not begin with: who is there has read this one)
+                shared_max[(t & 1) ^ 1][part][r] = l;
+                if (!(ok = meet())) break;
+                const float other = shared_max[(t & 1) ^ 1][part ^ 1][r];
+                l = part ? other + l : l + other;
+            }
             const bool live = p < u.len;
             const float inv = 1.0f / l;  // a row sees itself, so that l > 0 (or a NaN)
-            if (a.lse && live)
+            if (a.lse && live && part == 0)
                 a.lse[static_cast<size_t>(head) * a.n_tokens + u.tok0 + p] =
                     (m_used - kFwdShift + log2f(l)) * kPackedLn2;
             uint16_t *out = static_cast<uint16_t *>(a.out) + (static_cast<long long>(u.tok0) + p) * a.out_stride +
-                            static_cast<long long>(head) * HD;
+                            static_cast<long long>(head) * HD + part * DIMS;
 #pragma unroll 1
-            for (int c = 0; c < HD / 32; ++c) {
+            for (int c = 0; c < DIMS / 32; ++c) {
                 uint32_t o[32];
-                tmem_ld32(tmem + lane_base + tile * HD + 32 * c, o);
+                tmem_ld32(tmem + lane_base + tile * HD + part * DIMS + 32 * c, o);
                 tmem_wait_ld();
                 reg_fence32(o);
-                if (c == HD / 32 - 1) {  // read whole: the next unit may overwrite it
+                if (c == DIMS / 32 - 1) {  // read whole: the next unit may overwrite it
                     tc_fence_before();
                     warp_arrive(&bars.o_free[tile]);
                 }
