@@ -642,17 +642,14 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             uint16_t *out = static_cast<uint16_t *>(of_v ? a.g2 : a.g1) +
                             (static_cast<long long>(u.tok0) + mine) * stride +
                             static_cast<long long>(C::ROWS_STAY ? head : u.head) * HD + col0;
+            const bool wide = wide_rows(of_v ? a.g2 : a.g1, stride);
             auto store = [&](int c, const uint32_t *o) {
                 if (!live) return;
+                uint32_t w[8];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * factor,
-                                           __uint_as_float(o[8 * k + 2 * e + 1]) * factor);
-                    *reinterpret_cast<uint4 *>(out + 16 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int e = 0; e < 8; ++e)
+                    w[e] = pack2<BF16>(__uint_as_float(o[2 * e]) * factor, __uint_as_float(o[2 * e + 1]) * factor);
+                store16(out + 16 * c, w, wide);
             };
             const bool alone = C::ROWS_STAY || u.pieces == 1;
             // pieces of this tile and head lie one behind another, [column][lane] of each

@@ -201,6 +201,22 @@ __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
+// 16 values of a row as two 16-byte stores, or one of 32 bytes where rows allow it: threads hold a row each, and
+// a store that fills a 32-byte sector is worth two that fill half of one.
+__device__ __forceinline__ void store16(uint16_t *p, const uint32_t *w, bool wide) {
+    if (wide)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    else
+#pragma unroll
+        for (int k = 0; k < 8; k += 4)
+            *reinterpret_cast<uint4 *>(p + 2 * k) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+}
+__device__ __forceinline__ bool wide_rows(const void *p, long long stride) {
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride) * 2) & 31) == 0;
+}
+
 // Instruction descriptor with both operands fp16 or both bf16.
 template <bool BF16>
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N, int a_mn_major, int b_mn_major) {

@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 const float other = shared_max[(t & 1) ^ 1][part ^ 1][r];
                 l = part ? other + l : l + other;
             }
-            const bool live = p < u.len;
+            const bool live = p < u.len, wide = wide_rows(a.out, a.out_stride);
             const float inv = 1.0f / l;  // a row sees itself, so that l > 0 (or a NaN)
             if (a.lse && live && part == 0)
                 a.lse[static_cast<size_t>(head) * a.n_tokens + u.tok0 + p] =
@@ -525,13 +525,12 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 }
                 if (live) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t w[4];
+                    for (int k = 0; k < 32; k += 16) {
+                        uint32_t w[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack2<BF16>(__uint_as_float(o[8 * k + 2 * e]) * inv,
-                                               __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                        *reinterpret_cast<uint4 *>(out + 32 * c + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int e = 0; e < 8; ++e)
+                            w[e] = pack2<BF16>(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
+                        store16(out + 32 * c + k, w, wide);
                     }
                 }
             }
