@@ -169,7 +169,8 @@ fa_status fa_packed_attn(const void *q, const void *k, const void *v, void *out,
     fa::PackedFwdArgs a;
     if (!map_rows(&a.q, dtype, q, q_stride, n_tokens, n_kv_heads, group, head_dim, 128) ||
         !map_keys(&a.k, dtype, k, k_stride, n_tokens, n_kv_heads, head_dim, 128) ||
-        !map_keys(&a.v, dtype, v, v_stride, n_tokens, n_kv_heads, head_dim, 128))
+        !map_keys(&a.v, dtype, v, v_stride, n_tokens, n_kv_heads, head_dim, 128) ||
+        !map_rows(&a.o, dtype, out, out_stride, n_tokens, n_kv_heads, group, head_dim, 32))
         return FA_ERR_CUDA;
     a.header = p.header;
     a.rows = p.rows;

@@ -339,7 +339,7 @@ cudaError_t launch_packed_plan(const PackedPlanArgs &a, cudaStream_t stream);
 
 // ---- packed_fwd.cuh
 struct PackedFwdArgs {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, o;  // o: boxes of 32 rows
     PackedDirect direct;
     const PackedHeader *header;
     const PackedTile *rows;

@@ -36,9 +36,12 @@ struct FwdCfg {
     static constexpr int NS = HD == 256 ? 1 : 2;  // stages of K and of V
     static constexpr uint32_t OFF_K = NT * TILE;
     static constexpr uint32_t OFF_V = OFF_K + NS * TILE;
-    static constexpr uint32_t OFF_END = OFF_V + NS * TILE;
+    static constexpr uint32_t OFF_OUT = OFF_V + NS * TILE;  // a box of 32 rows of 128 bytes for each warp
+    static constexpr uint32_t OFF_END = OFF_OUT + 8 * 4096;
+    static constexpr uint32_t OFF_BARS = OFF_END + (NT == 2 ? 0 : 2 * 2 * 128 * 4);  // behind a row's two maxima
     // one block an SM, which owns all of TMEM
-    static constexpr uint32_t SMEM = (OFF_END + 1024 > 120u * 1024u) ? OFF_END + 1024 : 120u * 1024u;
+    static constexpr uint32_t SMEM = OFF_BARS + 512 > 120u * 1024u ? OFF_BARS + 512 : 120u * 1024u;
+    static_assert(SMEM <= 227u * 1024u, "shared memory");
     static constexpr uint32_t S_COL = 256;  // O in columns 0 .. 255
     static constexpr int THREADS = 384;
     // Two warpgroups: one for each tile, or with one tile each half of its columns.
@@ -56,6 +59,7 @@ struct FwdBars {
     uint32_t tmem_base;
     int abort;
 };
+static_assert(sizeof(FwdBars) <= 512, "barrier block");
 
 template <int HD, bool BF16, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
@@ -64,14 +68,18 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
     constexpr int NT = C::NT, NS = C::NS, BK = C::BK;
     constexpr uint32_t IDESC_QK = idesc_16<BF16>(128, BK, 0, 0);
     constexpr uint32_t IDESC_PV = idesc_16<BF16>(128, HD, 0, 1);
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ FwdBars bars;
-    __shared__ float shared_max[NT == 2 ? 1 : 2][2][NT == 2 ? 1 : 128];  // one tile: of a row's two halves
-    uint8_t *smem = reinterpret_cast<uint8_t *>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    // All of it dynamic: the tiles, which want 1024 bytes, begin where a block's shared memory does.
+    extern __shared__ __align__(1024) uint8_t smem[];
+    FwdBars &bars = *reinterpret_cast<FwdBars *>(smem + C::OFF_BARS);
+    // one tile: [turn][half][row], maxima of a row's two halves
+    volatile float *row_max = reinterpret_cast<float *>(smem + C::OFF_END);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     volatile int *abort = &bars.abort;
     unsigned *err = a.err;
+    if (smem_u32(smem) & 1023u) {  // (never so far: nothing static lies before it)
+        flag_error(err, FA_ERRBIT_DEVICE);
+        return;
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(&bars.q_full, 1);
@@ -99,6 +107,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
         tma_prefetch_desc(&a.q);
         tma_prefetch_desc(&a.k);
         tma_prefetch_desc(&a.v);
+        tma_prefetch_desc(&a.o);
     }
     if (warp == 1) {
         tmem_alloc(&bars.tmem_base, 512);
@@ -436,9 +445,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 float mx = max3(mx4[0], mx4[1], fmaxf(mx4[2], mx4[3]));
                 if (!kScaled) mx *= rule.a;
                 if (NT == 1) {  // of the whole row; and every S of the tile is read, where P goes
-                    shared_max[tt & 1][part][r] = mx;
+                    row_max[((tt & 1) * 2 + part) * 128 + r] = mx;
                     if (!(ok = meet())) break;
-                    mx = fmaxf(mx, shared_max[tt & 1][part ^ 1][r]);
+                    mx = fmaxf(mx, row_max[((tt & 1) * 2 + (part ^ 1)) * 128 + r]);
                 }
                 const float m_new = fmaxf(m_used, mx);
                 float corr = 1.0f;
@@ -501,9 +510,9 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
             tc_fence_after();
             if (NT == 1) {
                 // (the buffer that the next tile does not begin with: who is there has read this one)
-                shared_max[(t & 1) ^ 1][part][r] = l;
+                row_max[(((t & 1) ^ 1) * 2 + part) * 128 + r] = l;
                 if (!(ok = meet())) break;
-                const float other = shared_max[(t & 1) ^ 1][part ^ 1][r];
+                const float other = row_max[(((t & 1) ^ 1) * 2 + (part ^ 1)) * 128 + r];
                 l = part ? other + l : l + other;
             }
             const bool live = p < u.len, wide = wide_rows(a.out, a.out_stride);
@@ -513,28 +522,45 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                     (m_used - kFwdShift + log2f(l)) * kPackedLn2;
             uint16_t *out = static_cast<uint16_t *>(a.out) + (static_cast<long long>(u.tok0) + p) * a.out_stride +
                             static_cast<long long>(head) * HD + part * DIMS;
+            // 32 rows that are all there leave through this warp's box (128-byte swizzle) by a tensor copy; at
+            // a document's end each thread stores its own. (Threads' stores, each to a row of its own, took
+            // 3.5 us of a unit with head_dim 256.)
+            const int row0 = (warp & 3) * 32;
+            const bool full = p0 + ((row0 + 31) >> lg) < u.len;
+            uint8_t *box = smem + C::OFF_OUT + (warp - 4) * 4096;
 #pragma unroll 1
-            for (int c = 0; c < DIMS / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld32(tmem + lane_base + tile * HD + part * DIMS + 32 * c, o);
+            for (int c = 0; c < DIMS / 64; ++c) {
+                uint32_t o[64], w[32];
+                tmem_ld<64>(tmem + lane_base + tile * HD + part * DIMS + 64 * c, o);
                 tmem_wait_ld();
-                reg_fence32(o);
-                if (c == DIMS / 32 - 1) {  // read whole: the next unit may overwrite it
+                reg_fence<64>(o);
+                if (c == DIMS / 64 - 1) {  // read whole: the next unit may overwrite it
                     tc_fence_before();
                     warp_arrive(&bars.o_free[tile]);
                 }
-                if (live) {
 #pragma unroll
-                    for (int k = 0; k < 32; k += 16) {
-                        uint32_t w[8];
+                for (int e = 0; e < 32; ++e)
+                    w[e] = pack2<BF16>(__uint_as_float(o[2 * e]) * inv, __uint_as_float(o[2 * e + 1]) * inv);
+                if (full) {
+                    if (lane == 0) bulk_wait_group_read<0>();  // the box has been copied
+                    __syncwarp();
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            w[e] = pack2<BF16>(__uint_as_float(o[k + 2 * e]) * inv, __uint_as_float(o[k + 2 * e + 1]) * inv);
-                        store16(out + 32 * c + k, w, wide);
+                    for (int k = 0; k < 8; ++k)
+                        *reinterpret_cast<uint4 *>(box + lane * 128 + ((k ^ (lane & 7)) << 4)) =
+                            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tma_store_4d(&a.o, box, part * DIMS + 64 * c, 0, u.head, u.tok0 + p0 + (row0 >> lg));
+                        bulk_commit_group();
                     }
+                } else if (live) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) store16(out + 64 * c + 16 * k, w + 8 * k, wide);
                 }
             }
         }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
