@@ -43,10 +43,13 @@ struct GradCfg {
     static constexpr int NCHUNK = HD / 64;
     static constexpr uint32_t XCHUNK = 128 * 128, YCHUNK = BN * 128;
     static constexpr uint32_t XTILE = NCHUNK * XCHUNK, YTILE = NCHUNK * YCHUNK;
-    static constexpr int NX = HAS_T ? 2 : 1;
-    // Stages of Y1 and Y2: Y2 of dq and dk alone is read once, right after it lands.
-    static constexpr int N1 = HD == 256 ? 2 : 3;
-    static constexpr int N2 = HD == 64 ? 3 : HD == 256 && HAS_T ? 1 : 2;
+    // Stationary tiles in shared memory: with head_dim 256 X1 is in TMEM, where the scores take it from as
+    // their left operand. That leaves room for more stages, and the products less to fetch.
+    static constexpr bool X1_TMEM = HD == 256;
+    static constexpr int NX = (HAS_T ? 1 : 0) + (X1_TMEM ? 0 : 1);
+    static constexpr uint32_t OFF_X2 = X1_TMEM ? 0 : XTILE;
+    static constexpr int N1 = 3;                       // stages of Y1 and Y2
+    static constexpr int N2 = HD == 64 || !HAS_T ? 3 : 2;
     static constexpr int NL = 2;                       // stages of L and D
     static constexpr uint32_t OFF_Y1 = NX * XTILE;
     static constexpr uint32_t OFF_Y2 = OFF_Y1 + N1 * YTILE;
@@ -57,7 +60,8 @@ struct GradCfg {
     static constexpr uint32_t SMEM = OFF_BARS + 576 > 120u * 1024u ? OFF_BARS + 576 : 120u * 1024u;
     // TMEM: S, T (dv alone: a second S), acc1, acc2; a second T where there is room
     static constexpr int NT = HAS_T && 256 + HD * (MODE == kGradKV ? 2 : 1) + 128 <= 512 ? 2 : 1;
-    static constexpr uint32_t S_COL = 0, T_COL = 128;
+    static constexpr uint32_t S_COL = 0, T_COL = BN, S2_COL = BN;
+    static constexpr uint32_t X1_COL = 128;
     static constexpr uint32_t ACC1 = 256, ACC2 = MODE == kGradKV ? 256 + HD : 256;
     static constexpr uint32_t T2_COL = 384;
     __host__ __device__ static constexpr uint32_t t_col(int tt) { return NT == 2 && (tt & 1) ? T2_COL : T_COL; }
@@ -67,7 +71,7 @@ struct GradCfg {
 };
 
 struct GradBars {
-    uint64_t x_full, x_empty;
+    uint64_t x_full, x_empty, x1_full;
     uint64_t y1_full[3], y1_empty[3], y2_full[3], y2_empty[3];
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full[2], s_free, p_full[2], t_full[2], dt_full[2];
@@ -104,6 +108,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
     if (threadIdx.x == 0) {
         mbar_init(&bars.x_full, 1);
         mbar_init(&bars.x_empty, 1);
+        mbar_init(&bars.x1_full, C::COMPUTE / 32);
         for (int s = 0; s < 3; ++s) {
             mbar_init(&bars.y1_full[s], 1);
             mbar_init(&bars.y1_empty[s], 1);
@@ -215,12 +220,14 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 }
             };
             auto load_x = [&](int j, const PackedTile &u) {
+                if (C::NX == 0) return true;
                 if (j > 0 && !mbar_wait(&bars.x_empty, (j - 1) & 1, abort, err)) return false;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&bars.x_full, C::NX * C::XTILE);
-                    copy(&a.x1, smem, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
-                    if (C::NX == 2)
-                        copy(&a.x2, smem + C::XTILE, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                    if (!C::X1_TMEM)
+                        copy(&a.x1, smem, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                    if (C::HAS_T)
+                        copy(&a.x2, smem + C::OFF_X2, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
                 }
                 ++x_arms.n;
                 return true;
@@ -303,7 +310,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 const bool one = elect_lane();
                 const uint32_t tmem = uniform(static_cast<int>(bars.tmem_base));
                 // descriptors of the tiles' beginnings: an offset is added to their address field
-                const uint64_t x1 = desc_sw128(smem_u32(smem), 16, 1024), x2 = x1 + (C::XTILE >> 4);
+                const uint64_t x1 = desc_sw128(smem_u32(smem), 16, 1024), x2 = x1 + (C::OFF_X2 >> 4);
                 const uint64_t y1 = desc_sw128(smem_u32(smem + C::OFF_Y1), 16, 1024);   // rows as they lie
                 const uint64_t y2 = desc_sw128(smem_u32(smem + C::OFF_Y2), 16, 1024);
                 const uint64_t g1 = desc_sw128(smem_u32(smem + C::OFF_Y1), C::YCHUNK, 1024);  // dims as columns
@@ -316,6 +323,14 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                         for (int kk = 0; kk < HD / 16; ++kk)
                             mma_ss(tmem + col, x + (((kk >> 2) * C::XCHUNK + (kk & 3) * 32) >> 4),
                                    y + (((kk >> 2) * C::YCHUNK + (kk & 3) * 32) >> 4), IDESC_S, kk > 0 ? 1u : 0u);
+                };
+                // the same with X in TMEM
+                auto scores_tmem = [&](uint32_t x, uint64_t y, uint32_t col) {
+                    if (one)
+#pragma unroll
+                        for (int kk = 0; kk < HD / 16; ++kk)
+                            mma_ts(tmem + col, tmem + x + kk * 8, y + (((kk >> 2) * C::YCHUNK + (kk & 3) * 32) >> 4),
+                                   IDESC_S, kk > 0 ? 1u : 0u);
                 };
                 // weights in TMEM (a part of the columns where its threads wrote them) times the tile itself
                 auto gather = [&](uint32_t col, uint64_t y, uint32_t acc, bool first) {
@@ -336,7 +351,8 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 for (int j = 0; ok && uniform(next_unit(j, &u)); ++j) {
                     const int count = uniform(plan_of(u).count);
                     warp_arrive(&bars.ring.empty[j % kPackedRing]);
-                    if (!(ok = wait(&bars.x_full, j & 1))) break;
+                    if (C::NX > 0 && !(ok = wait(&bars.x_full, j & 1))) break;
+                    if (C::X1_TMEM && !(ok = wait(&bars.x1_full, j & 1))) break;
                     tc_fence_after();
                     // Two barriers at once, each looked at by half of the lanes: a look takes a hundred cycles
                     // and more (dq, 16384 tokens, 8/2 heads x 128: 530 -> 504 us; where P is made, too, waiting
@@ -352,7 +368,11 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                         if (!C::HAS_P && tt > 0 ? !wait2(there, phase, &bars.s_free, (tt - 1) & 1) : !wait(there, phase))
                             return false;
                         tc_fence_after();
-                        scores(x1, y1 + st * STAGE, C::S_COL + (C::HAS_T ? 0 : (tt & 1) * 128));
+                        const uint32_t col = C::S_COL + (C::HAS_T ? 0 : (tt & 1) * C::S2_COL);
+                        if (C::X1_TMEM)
+                            scores_tmem(C::X1_COL, y1 + st * STAGE, col);
+                        else
+                            scores(x1, y1 + st * STAGE, col);
                         commit(&bars.s_full[C::HAS_T ? 0 : tt & 1]);
                         if (!C::HAS_T) {
                             commit(&bars.y1_empty[st]);
@@ -378,7 +398,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                         if (!wait(&bars.p_full[b], (C::HAS_T ? tt : tt >> 1) & 1) || !acc_ready(i)) return false;
                         if (!C::HAS_T && !wait(&bars.y2_full[st], (tt / N2) & 1)) return false;
                         tc_fence_after();
-                        gather(C::S_COL + b * 128, g2 + st * STAGE, C::ACC2, i == 0);
+                        gather(C::S_COL + b * C::S2_COL, g2 + st * STAGE, C::ACC2, i == 0);
                         commit(&bars.y2_empty[st]);
                         return true;
                     };
@@ -428,14 +448,38 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             warp_arrive(&bars.meet);
             return static_cast<bool>(__all_sync(~0u, mbar_wait(&bars.meet, meets++ & 1, abort, err)));
         };
+        auto take = [&](int j, PackedTile *u) {
+            const bool got = next_unit(j, u);
+            warp_arrive(&bars.ring.empty[j % kPackedRing]);
+            return static_cast<bool>(__all_sync(~0u, got));
+        };
+        // This thread's row of X1, a half of its dims, into TMEM. Every S of the unit before is done.
+        auto load_x1 = [&](const PackedTile &u) {
+            const int tok = u.p0 + (C::ROWS_STAY ? r >> lg : r);
+            const int h = C::ROWS_STAY ? (u.head << lg) + (r & (group - 1)) : u.head;
+            const uint4 *src = reinterpret_cast<const uint4 *>(
+                static_cast<const uint16_t *>(a.x1_rows) + (static_cast<long long>(u.tok0) + tok) * a.x1_stride +
+                static_cast<long long>(h) * HD + part * (HD / 2));
+#pragma unroll
+            for (int c = 0; c < HD / 4; c += 32) {
+                uint32_t w[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 x = tok < u.len ? load(src + c / 4 + k) : make_uint4(0, 0, 0, 0);
+                    w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
+                }
+                tmem_st32(tmem + lane_base + C::X1_COL + part * (HD / 4) + c, w);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            warp_arrive(&bars.x1_full);
+        };
         int t = 0;
         bool ok = true;
-        PackedTile u;
-        for (int j = 0; ok; ++j) {
-            const bool have = next_unit(j, &u);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.ring.empty[j % kPackedRing]);
-            if (!__all_sync(~0u, have)) break;
+        PackedTile u, un;
+        bool have = take(0, &u);
+        if (C::X1_TMEM && have) load_x1(u);
+        for (int j = 0; have && ok; ++j) {
             const KeyTiles plan = plan_of(u);
             // rows stay: this thread's query; keys stay: its key
             const int mine = u.p0 + (C::ROWS_STAY ? r >> lg : r);
@@ -487,7 +531,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 ok = __all_sync(~0u, ok);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t scol = tmem + lane_base + C::S_COL + sb * 128 + part * PART;
+                const uint32_t scol = tmem + lane_base + C::S_COL + sb * C::S2_COL + part * PART;
                 const uint32_t tcol = tmem + lane_base + C::t_col(tt) + part * PART;
                 uint32_t s[PART];
                 tmem_ld<PART>(scol, s);
@@ -627,6 +671,9 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             }
             if (!ok) break;
             t += plan.count;
+            // the next unit's first scores run under this one's output
+            have = take(j + 1, &un);
+            if (C::X1_TMEM && have) load_x1(un);
             ok = mbar_wait(&bars.acc_last, j & 1, abort, err);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
@@ -701,6 +748,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     }
                 }
             }
+            u = un;
         }
     }
     tc_fence_before();
