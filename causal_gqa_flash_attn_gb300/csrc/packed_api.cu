@@ -316,8 +316,6 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     a.tiles = p.rows;
     a.n_tiles = &p.header->row_tiles;
     a.counter = &p.header->counters[0];
-    a.x1_rows = q;
-    a.x1_stride = q_stride;
     a.g1 = dq;
     a.g1_stride = dq_stride;
     a.g2 = nullptr;
@@ -325,8 +323,6 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     b.tiles = p.keys;
     b.n_tiles = &p.header->key_tiles;
     b.counter = &p.header->counters[1];
-    b.x1_rows = k;
-    b.x1_stride = k_stride;
     b.g1 = dk;
     b.g1_stride = dk_stride;
     b.g2 = dv;

@@ -43,12 +43,13 @@ struct GradCfg {
     static constexpr int NCHUNK = HD / 64;
     static constexpr uint32_t XCHUNK = 128 * 128, YCHUNK = BN * 128;
     static constexpr uint32_t XTILE = NCHUNK * XCHUNK, YTILE = NCHUNK * YCHUNK;
-    // Stationary tiles in shared memory: with head_dim 256 X1 is in TMEM, where the scores take it from as
-    // their left operand. That leaves room for more stages, and the products less to fetch.
+    // Stationary tiles in shared memory. With head_dim 256 X1 is in TMEM, where the scores take it from as their
+    // left operand: that leaves room for more stages, and the products less to fetch. On its way there it
+    // passes through where X2 goes next, or for dv a place of its own.
     static constexpr bool X1_TMEM = HD == 256;
-    static constexpr int NX = (HAS_T ? 1 : 0) + (X1_TMEM ? 0 : 1);
+    static constexpr int NX = X1_TMEM ? 1 : 2;
     static constexpr uint32_t OFF_X2 = X1_TMEM ? 0 : XTILE;
-    static constexpr int N1 = 3;                       // stages of Y1 and Y2
+    static constexpr int N1 = HAS_T ? 3 : 2;           // stages of Y1 and Y2
     static constexpr int N2 = HD == 64 || !HAS_T ? 3 : 2;
     static constexpr int NL = 2;                       // stages of L and D
     static constexpr uint32_t OFF_Y1 = NX * XTILE;
@@ -57,7 +58,7 @@ struct GradCfg {
     static constexpr uint32_t OFF_STATS = OFF_END;     // [NL][2][BN] L and D of a tile's rows
     static constexpr uint32_t OFF_BIAS = OFF_STATS + (ROWS_STAY ? 0 : NL * 2 * BN * 4);  // [2][16]
     static constexpr uint32_t OFF_BARS = OFF_BIAS + 128;
-    static constexpr uint32_t SMEM = OFF_BARS + 576 > 120u * 1024u ? OFF_BARS + 576 : 120u * 1024u;
+    static constexpr uint32_t SMEM = OFF_BARS + 640 > 120u * 1024u ? OFF_BARS + 640 : 120u * 1024u;
     // TMEM: S, T (dv alone: a second S), acc1, acc2; a second T where there is room
     static constexpr int NT = HAS_T && 256 + HD * (MODE == kGradKV ? 2 : 1) + 128 <= 512 ? 2 : 1;
     static constexpr uint32_t S_COL = 0, T_COL = BN, S2_COL = BN;
@@ -71,7 +72,7 @@ struct GradCfg {
 };
 
 struct GradBars {
-    uint64_t x_full, x_empty, x1_full;
+    uint64_t x_full, x_empty, x1_full, xs_full, xs_free;
     uint64_t y1_full[3], y1_empty[3], y2_full[3], y2_empty[3];
     uint64_t l_full[2], l_empty[2];
     uint64_t s_full[2], s_free, p_full[2], t_full[2], dt_full[2];
@@ -81,7 +82,7 @@ struct GradBars {
     uint32_t tmem_base;
     int abort, last;
 };
-static_assert(sizeof(GradBars) <= 576, "barrier block");
+static_assert(sizeof(GradBars) <= 640, "barrier block");
 
 template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
 __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
@@ -109,6 +110,8 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         mbar_init(&bars.x_full, 1);
         mbar_init(&bars.x_empty, 1);
         mbar_init(&bars.x1_full, C::COMPUTE / 32);
+        mbar_init(&bars.xs_full, 1);
+        mbar_init(&bars.xs_free, C::COMPUTE / 32);
         for (int s = 0; s < 3; ++s) {
             mbar_init(&bars.y1_full[s], 1);
             mbar_init(&bars.y1_empty[s], 1);
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             const int units = a.n_kv * (direct ? direct_tile<!C::ROWS_STAY>(a.direct, blockIdx.x / a.n_kv, tile_tokens, step_tokens,
                                                                             7 - lg, a.sink, a.win, err, &own)
                                                : *a.n_tiles);
-            Arms x_arms, y1_arms[3], y2_arms[3], l_arms[2];
+            Arms x_arms, xs_arms, y1_arms[3], y2_arms[3], l_arms[2];
             int patches = 0;
             bool ok = true;
             auto fetch = [&](int w, PackedTile *u) {
@@ -219,15 +222,25 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                         tma_load_3d(dst + c * chunk, map, bar, c * 64, head, tok);
                 }
             };
+            // X1 on its way to TMEM, or both
             auto load_x = [&](int j, const PackedTile &u) {
-                if (C::NX == 0) return true;
-                if (j > 0 && !mbar_wait(&bars.x_empty, (j - 1) & 1, abort, err)) return false;
+                if (j > 0 && !mbar_wait(C::HAS_T ? &bars.x_empty : &bars.xs_free, (j - 1) & 1, abort, err)) return false;
+                uint64_t *bar = C::X1_TMEM ? &bars.xs_full : &bars.x_full;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&bars.x_full, C::NX * C::XTILE);
+                    mbar_arrive_expect_tx(bar, C::NX * C::XTILE);
+                    copy(&a.x1, smem, C::XCHUNK, bar, C::ROWS_STAY, u.head, u.tok0 + u.p0);
                     if (!C::X1_TMEM)
-                        copy(&a.x1, smem, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
-                    if (C::HAS_T)
-                        copy(&a.x2, smem + C::OFF_X2, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                        copy(&a.x2, smem + C::OFF_X2, C::XCHUNK, bar, C::ROWS_STAY, u.head, u.tok0 + u.p0);
+                }
+                if (C::X1_TMEM) ++xs_arms.n; else ++x_arms.n;
+                return true;
+            };
+            // X2 behind X1
+            auto load_x2 = [&](int j, const PackedTile &u) {
+                if (!mbar_wait(&bars.xs_free, j & 1, abort, err)) return false;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bars.x_full, C::XTILE);
+                    copy(&a.x2, smem + C::OFF_X2, C::XCHUNK, &bars.x_full, C::ROWS_STAY, u.head, u.tok0 + u.p0);
                 }
                 ++x_arms.n;
                 return true;
@@ -282,6 +295,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     ok = load_y(t + i, at, u, true);
                     if (ok && !C::ROWS_STAY) ok = load_stats(t + i, at, u);
                     if (ok) ok = load_y(t + i, at, u, false);
+                    if (C::X1_TMEM && C::HAS_T && ok && i == 0) ok = load_x2(j, u);
                     if (ok && i == cnt - 1) {
                         if (lane == 0) w = direct ? units : static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
                         w = __shfl_sync(~0u, w, 0);
@@ -297,6 +311,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             }
             if (!ok) {  // copies already issued land before the block exits
                 x_arms.drain(&bars.x_full);
+                xs_arms.drain(&bars.xs_full);
                 for (int s = 0; s < 3; ++s) {
                     y1_arms[s].drain(&bars.y1_full[s]);
                     y2_arms[s].drain(&bars.y2_full[s]);
@@ -351,8 +366,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 for (int j = 0; ok && uniform(next_unit(j, &u)); ++j) {
                     const int count = uniform(plan_of(u).count);
                     warp_arrive(&bars.ring.empty[j % kPackedRing]);
-                    if (C::NX > 0 && !(ok = wait(&bars.x_full, j & 1))) break;
-                    if (C::X1_TMEM && !(ok = wait(&bars.x1_full, j & 1))) break;
+                    if (!(ok = wait(C::X1_TMEM ? &bars.x1_full : &bars.x_full, j & 1))) break;
                     tc_fence_after();
                     // Two barriers at once, each looked at by half of the lanes: a look takes a hundred cycles
                     // and more (dq, 16384 tokens, 8/2 heads x 128: 530 -> 504 us; where P is made, too, waiting
@@ -382,6 +396,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     };
                     auto do_t = [&](int i) {
                         const int tt = t + i, st = tt % N2;
+                        if (C::X1_TMEM && i == 0 && !wait(&bars.x_full, j & 1)) return false;
                         if (!wait(&bars.y2_full[st], (tt / N2) & 1)) return false;
                         tc_fence_after();
                         scores(x2, y2 + st * STAGE, C::t_col(tt));
@@ -453,33 +468,33 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             warp_arrive(&bars.ring.empty[j % kPackedRing]);
             return static_cast<bool>(__all_sync(~0u, got));
         };
-        // This thread's row of X1, a half of its dims, into TMEM. Every S of the unit before is done.
-        auto load_x1 = [&](const PackedTile &u) {
-            const int tok = u.p0 + (C::ROWS_STAY ? r >> lg : r);
-            const int h = C::ROWS_STAY ? (u.head << lg) + (r & (group - 1)) : u.head;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                static_cast<const uint16_t *>(a.x1_rows) + (static_cast<long long>(u.tok0) + tok) * a.x1_stride +
-                static_cast<long long>(h) * HD + part * (HD / 2));
+        // This thread's row of X1, a half of its dims, from shared memory into TMEM. Every S of the unit
+        // before is done. (Rows straight from memory, each by its thread, took 5 us.)
+        auto load_x1 = [&](int j) {
+            const bool got = mbar_wait(&bars.xs_full, j & 1, abort, err);
+            if (!__all_sync(~0u, got)) return false;
 #pragma unroll
-            for (int c = 0; c < HD / 4; c += 32) {
+            for (int c = 0; c < HD / 2; c += 64) {  // 64 dims: a chunk's row
+                const uint8_t *row = smem + ((part * (HD / 2) + c) / 64) * C::XCHUNK + r * 128;
                 uint32_t w[32];
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const uint4 x = tok < u.len ? load(src + c / 4 + k) : make_uint4(0, 0, 0, 0);
+                    const uint4 x = lds_v4(row + ((k ^ (r & 7)) << 4));
                     w[4 * k] = x.x, w[4 * k + 1] = x.y, w[4 * k + 2] = x.z, w[4 * k + 3] = x.w;
                 }
-                tmem_st32(tmem + lane_base + C::X1_COL + part * (HD / 4) + c, w);
+                tmem_st32(tmem + lane_base + C::X1_COL + (part * (HD / 2) + c) / 2, w);
             }
             tmem_wait_st();
             tc_fence_before();
             warp_arrive(&bars.x1_full);
+            if (lane == 0) mbar_arrive(&bars.xs_free);
+            return true;
         };
         int t = 0;
         bool ok = true;
-        PackedTile u, un;
-        bool have = take(0, &u);
-        if (C::X1_TMEM && have) load_x1(u);
-        for (int j = 0; have && ok; ++j) {
+        PackedTile u;
+        for (int j = 0; ok && take(j, &u); ++j) {
+            if (C::X1_TMEM && !(ok = load_x1(j))) break;
             const KeyTiles plan = plan_of(u);
             // rows stay: this thread's query; keys stay: its key
             const int mine = u.p0 + (C::ROWS_STAY ? r >> lg : r);
@@ -671,9 +686,6 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             }
             if (!ok) break;
             t += plan.count;
-            // the next unit's first scores run under this one's output
-            have = take(j + 1, &un);
-            if (C::X1_TMEM && have) load_x1(un);
             ok = mbar_wait(&bars.acc_last, j & 1, abort, err);
             ok = __all_sync(~0u, ok);
             if (!ok) break;
@@ -734,21 +746,21 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 if (*static_cast<volatile int *>(&bars.last)) {
                     __threadfence();
 #pragma unroll 1
-                    for (int c = 0; c < COLS / 16; ++c) {
-                        float x[16] = {};
+                    for (int c = 0; c < COLS / 32; ++c) {
+                        float x[32] = {};
 #pragma unroll 1
                         for (int k = 0; k < u.pieces; ++k)
 #pragma unroll
-                            for (int e = 0; e < 16; ++e)
-                                x[e] += __ldcg(sums + static_cast<size_t>(k) * SLOT + (16 * c + e) * 128);
-                        uint32_t o[16];
+                            for (int e = 0; e < 32; ++e)
+                                x[e] += __ldcg(sums + static_cast<size_t>(k) * SLOT + (32 * c + e) * 128);
+                        uint32_t o[32];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(x[e]);
-                        store(c, o);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(x[e]);
+                        store(2 * c, o);
+                        store(2 * c + 1, o + 16);
                     }
                 }
             }
-            u = un;
         }
     }
     tc_fence_before();

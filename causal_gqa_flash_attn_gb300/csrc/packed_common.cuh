@@ -385,8 +385,6 @@ struct PackedGradArgs {
     // Stationary tiles x1, x2 and moving ones y1, y2: q, dout and k, v for dq; the other way round
     // for dk and dv.
     CUtensorMap x1, x2, y1, y2;
-    const void *x1_rows;     // x1 itself
-    long long x1_stride;
     PackedDirect direct;
     const PackedHeader *header;
     const PackedTile *tiles;
