@@ -124,6 +124,9 @@ constexpr int kTypeF32 = 0;
 constexpr int kTypeF16 = 1;
 constexpr int kTypeBF16 = 2;
 
+// A cap on scores costs them up to 2^-20 of it: beyond this one, more than their weights' rounding.
+constexpr float kMostCap = 4096.0f;
+
 // ---- paged_plan.cu
 struct PlanArgs {
     const int32_t *cached, *fresh;  // [n_reqs]

@@ -82,7 +82,8 @@ fa_status check_rule(int dtype, const int32_t *cu, const int32_t *prefix, int si
                      const float *slopes, const void *workspace) {
     if (sink < 0 || !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap))
         return FA_ERR_INVALID;
-    if (dtype == FA_T_F32) return FA_ERR_UNSUPPORTED;
+    if (cap > 0.0f && !std::isfinite(4.0f / cap)) return FA_ERR_INVALID;
+    if (dtype == FA_T_F32 || cap > fa::kMostCap) return FA_ERR_UNSUPPORTED;
     if (dtype != FA_T_F16 && dtype != FA_T_BF16) return FA_ERR_INVALID;
     if (!aligned(cu, 4) || !aligned(prefix, 4) || !aligned(slopes, 4) || !aligned(workspace, 16))
         return FA_ERR_INVALID;

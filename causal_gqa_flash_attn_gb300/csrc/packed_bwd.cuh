@@ -776,7 +776,8 @@ template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
 cudaError_t launch_grad(const PackedGradArgs &a, int blocks, cudaStream_t stream) {
     using C = GradCfg<HD, MODE>;
     auto kernel = packed_grad_kernel<HD, BF16, CAP, BIAS, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> made{0};
+    const cudaError_t e = allow_smem(kernel, C::SMEM, &made);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(blocks), C::THREADS, C::SMEM, stream, a);
 }

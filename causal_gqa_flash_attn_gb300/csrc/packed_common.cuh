@@ -11,6 +11,7 @@
 
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "fa_device.cuh"
@@ -215,6 +216,19 @@ __device__ __forceinline__ void store16(uint16_t *p, const uint32_t *w, bool wid
 }
 __device__ __forceinline__ bool wide_rows(const void *p, long long stride) {
     return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(stride) * 2) & 31) == 0;
+}
+
+// The shared memory that a kernel may have, set once for each device, as the call takes a microsecond (two threads that
+// are first may both make it).
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t bytes, std::atomic<uint64_t> *made) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && (dev >= 64 || !(made->load(std::memory_order_acquire) >> dev & 1))) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+        if (e == cudaSuccess && dev < 64) made->fetch_or(1ull << dev, std::memory_order_release);
+    }
+    return e;
 }
 
 // Instruction descriptor with both operands fp16 or both bf16.

@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
 
                 constexpr bool kScaled = CAP || BIAS;  // s goes to the exp2 domain first
                 if (kScaled) {
-                    const float far = static_cast<float>(p - j0);  // exact: below 2^26 apart
+                    const float far = static_cast<float>(p - j0);  // exact up to 2^24
                     auto score = [&](auto masks) {
                         constexpr bool MASK = decltype(masks)::value;
 #pragma unroll
@@ -574,7 +574,8 @@ template <int HD, bool BF16, bool CAP, bool BIAS>
 cudaError_t launch_fwd(const PackedFwdArgs &a, int blocks, cudaStream_t stream) {
     using C = FwdCfg<HD>;
     auto kernel = packed_fwd_kernel<HD, BF16, CAP, BIAS>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    static std::atomic<uint64_t> made{0};
+    const cudaError_t e = allow_smem(kernel, C::SMEM, &made);
     if (e != cudaSuccess) return e;
     return launch_after(kernel, dim3(blocks), C::THREADS, C::SMEM, stream, a);
 }

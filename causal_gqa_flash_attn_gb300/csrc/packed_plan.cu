@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the next kernel sets itself up meanwhile
     __shared__ int part[3][32], sum[3];
     __shared__ int bins[kBins];
-    __shared__ int small[3][kDocsInSmem + 1];
+    __shared__ int small[3][kDocsInSmem + 1], cu_s[kDocsInSmem + 1];
     __shared__ int bad_docs, n_slots;
     __shared__ unsigned long long all_rows;
     const int tid = threadIdx.x, D = a.n_docs, list = blockIdx.x;
@@ -71,6 +71,9 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     int *before[3];
     for (int k = 0; k < 3; ++k) before[k] = fits ? small[k] : a.doc_tiles + static_cast<size_t>(3 * list + k) * (D + 1);
     if (tid == 0) bad_docs = 0;
+    if (fits)
+        for (int d = tid; d <= D; d += kPlanThreads) cu_s[d] = load(a.cu + d);
+    const int32_t *cu = fits ? cu_s : a.cu;
     if (list == 0 && tid < 4) a.header->counters[tid] = 0;
     if (list == 1)
         for (int i = tid; i < a.slots; i += kPlanThreads) a.arrived[i] = 0;
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     int nr = 0, nk = 0, nb = 0;
     bool bad = false;
     auto length = [&](int d) {
-        const int from = load(a.cu + d), to = load(a.cu + d + 1);
+        const int from = cu[d], to = cu[d + 1];
         if (from < 0 || to < from || to > a.n_tokens) {
             bad = true;
             return 0;
@@ -116,103 +119,102 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(PackedPlanArg
     if (wrong && tid == 0) flag_error(a.err, FA_ERRBIT_DEVICE);
     const int n = wrong ? 0 : sum[list];
 
-    {
-        PackedTile *out = list ? a.keys : a.rows;
-        const int room = list ? a.most_keys : a.most_rows;
-        // tile x, and how many tiles move past it
-        auto tile = [&](int x, PackedTile *t) {
-            const int d = find_doc(before[list], D, x);
-            t->tok0 = load(a.cu + d);
-            t->len = load(a.cu + d + 1) - t->tok0;
-            t->p0 = (x - before[list][d]) * (list ? 128 : a.row_tokens);
-            t->prefix = a.prefix ? min(max(load(a.prefix + d), 0), t->len) : 0;
-            t->rb = before[2][d];
-            t->doc = d;
-            t->head = t->from = t->piece = 0;
-            t->pieces = 1;
-            t->slot = -1;
-            if (list) {
-                int first, last;
-                query_range(t->p0, min(t->p0 + 128, t->len) - 1, t->len, t->prefix, a.sink, a.win, &first, &last);
-                t->from = first / a.step_tokens;
-                t->rows = last / a.step_tokens - t->from + 1;
-            } else {
-                const int p1 = min(t->p0 + a.row_tokens, t->len) - 1;
-                t->rows = a.key_tile == 64 ? key_tiles<64>(t->p0, p1, t->prefix, a.sink, a.win).count
-                                           : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
-            }
-        };
-        // few tiles: each thread makes its own once
-        const bool once = n <= kPlanThreads;
-        PackedTile t;
-        if (once && tid < n) tile(tid, &t);
-        // the largest piece: at first 1 / parts of all row tiles, then what there is room for
-        int most = 1 << 30;
-        if (list && a.slots > 0 && n > 0) {
-            if (tid == 0) all_rows = 0;
-            __syncthreads();
-            unsigned long long mine = 0;
-            for (int x = tid; x < n; x += kPlanThreads) {
-                if (!once) tile(x, &t);
-                mine += t.rows;
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
-            if ((tid & 31) == 0 && mine > 0) atomicAdd(&all_rows, mine);
-            __syncthreads();
-            most = max(kPackedLeastPiece, static_cast<int>((all_rows * a.n_kv + a.parts - 1) / a.parts));
+    PackedTile *out = list ? a.keys : a.rows;
+    const int room = list ? a.most_keys : a.most_rows;
+    // tile x, and how many tiles move past it
+    auto tile = [&](int x, PackedTile *t) {
+        const int d = find_doc(before[list], D, x);
+        t->tok0 = cu[d];
+        t->len = cu[d + 1] - t->tok0;
+        t->p0 = (x - before[list][d]) * (list ? 128 : a.row_tokens);
+        t->prefix = a.prefix ? min(max(load(a.prefix + d), 0), t->len) : 0;
+        t->rb = before[2][d];
+        t->doc = d;
+        t->head = t->from = t->piece = 0;
+        t->pieces = 1;
+        t->slot = -1;
+        if (list) {
+            int first, last;
+            query_range(t->p0, min(t->p0 + 128, t->len) - 1, t->len, t->prefix, a.sink, a.win, &first, &last);
+            t->from = first / a.step_tokens;
+            t->rows = last / a.step_tokens - t->from + 1;
+        } else {
+            const int p1 = min(t->p0 + a.row_tokens, t->len) - 1;
+            t->rows = a.key_tile == 64 ? key_tiles<64>(t->p0, p1, t->prefix, a.sink, a.win).count
+                                       : key_tiles<128>(t->p0, p1, t->prefix, a.sink, a.win).count;
         }
-        auto pieces_of = [&](int rows) { return rows > most ? (rows + most - 1) / most : 1; };
-        int entries = n;
-        while (list && a.slots > 0 && n > 0) {
-            if (tid == 0) n_slots = 0;
-            int need = 0, more = 0, zero = 0;
-            for (int x = tid; x < n; x += kPlanThreads) {
-                if (!once) tile(x, &t);
-                const int p = pieces_of(t.rows);
-                more += p - 1;
-                if (p > 1) need += p;
-            }
-            scan3(need, more, zero, sum, part);
-            const bool fits = static_cast<long long>(sum[0]) * a.n_kv <= a.slots && n + sum[1] <= room;
-            entries = n + sum[1];
-            __syncthreads();
-            if (fits) break;
-            most *= 2;
-        }
-        if (tid == 0) (list ? a.header->key_tiles : a.header->row_tiles) = entries;
-        if (n == 0) return;
-        int shift = 0;  // bins of a power of two of tiles
-        const int step = list ? a.step_tokens : a.key_tile;
-        while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
-        auto bin_of = [&](int rows) { return kBins - 1 - min(rows >> shift, kBins - 1); };  // heaviest first
-        for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
+    };
+    // few tiles: each thread makes its own once
+    const bool once = n <= kPlanThreads;
+    PackedTile t;
+    if (once && tid < n) tile(tid, &t);
+    // the largest piece: at first 1 / parts of all row tiles, then what there is room for
+    int most = 1 << 30;
+    if (list && a.slots > 0 && n > 0) {
+        if (tid == 0) all_rows = 0;
         __syncthreads();
-        // the pieces of a tile differ by one row tile at most, and share a bin
+        unsigned long long mine = 0;
+        for (int x = tid; x < n; x += kPlanThreads) {
+            if (!once) tile(x, &t);
+            mine += t.rows;
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mine += __shfl_xor_sync(~0u, mine, d);
+        if ((tid & 31) == 0 && mine > 0) atomicAdd(&all_rows, mine);
+        __syncthreads();
+        const unsigned long long each = (all_rows * a.n_kv + a.parts - 1) / a.parts;
+        most = max(kPackedLeastPiece, static_cast<int>(min(each, 1ull << 30)));
+    }
+    auto pieces_of = [&](int rows) { return rows > most ? (rows + most - 1) / most : 1; };
+    int entries = n;
+    while (list && a.slots > 0 && n > 0) {
+        if (tid == 0) n_slots = 0;
+        int need = 0, more = 0, zero = 0;
         for (int x = tid; x < n; x += kPlanThreads) {
             if (!once) tile(x, &t);
             const int p = pieces_of(t.rows);
-            atomicAdd(&bins[bin_of((t.rows + p - 1) / p)], p);
+            more += p - 1;
+            if (p > 1) need += p;
         }
+        scan3(need, more, zero, sum, part);
+        const bool fits = static_cast<long long>(sum[0]) * a.n_kv <= a.slots && n + sum[1] <= room;
+        entries = n + sum[1];
         __syncthreads();
-        static_assert(kBins == kPlanThreads, "a bin for each thread");
-        int at = bins[tid], z0 = 0, z1 = 0;
-        scan3(at, z0, z1, sum, part);
-        bins[tid] = at;
-        __syncthreads();
-        for (int x = tid; x < n; x += kPlanThreads) {
-            if (!once) tile(x, &t);
-            const int p = pieces_of(t.rows), rows = t.rows, from = t.from;
-            const int place = atomicAdd(&bins[bin_of((rows + p - 1) / p)], p);
-            t.pieces = p;
-            if (p > 1) t.slot = atomicAdd(&n_slots, p * a.n_kv);
-            for (int k = 0; k < p; ++k) {
-                const int r0 = static_cast<int>(static_cast<long long>(rows) * k / p);
-                t.piece = k;
-                t.from = from + r0;
-                t.rows = static_cast<int>(static_cast<long long>(rows) * (k + 1) / p) - r0;
-                out[place + k] = t;
-            }
+        if (fits) break;
+        most *= 2;
+    }
+    if (tid == 0) (list ? a.header->key_tiles : a.header->row_tiles) = entries;
+    if (n == 0) return;
+    int shift = 0;  // bins of a power of two of tiles
+    const int step = list ? a.step_tokens : a.key_tile;
+    while ((a.n_tokens / step + 1) >> shift >= kBins) ++shift;
+    auto bin_of = [&](int rows) { return kBins - 1 - min(rows >> shift, kBins - 1); };  // heaviest first
+    for (int i = tid; i < kBins; i += kPlanThreads) bins[i] = 0;
+    __syncthreads();
+    // the pieces of a tile differ by one row tile at most, and share a bin
+    for (int x = tid; x < n; x += kPlanThreads) {
+        if (!once) tile(x, &t);
+        const int p = pieces_of(t.rows);
+        atomicAdd(&bins[bin_of((t.rows + p - 1) / p)], p);
+    }
+    __syncthreads();
+    static_assert(kBins == kPlanThreads, "a bin for each thread");
+    int at = bins[tid], z0 = 0, z1 = 0;
+    scan3(at, z0, z1, sum, part);
+    bins[tid] = at;
+    __syncthreads();
+    for (int x = tid; x < n; x += kPlanThreads) {
+        if (!once) tile(x, &t);
+        const int p = pieces_of(t.rows), rows = t.rows, from = t.from;
+        const int place = atomicAdd(&bins[bin_of((rows + p - 1) / p)], p);
+        t.pieces = p;
+        if (p > 1) t.slot = atomicAdd(&n_slots, p * a.n_kv);
+        for (int k = 0; k < p; ++k) {
+            const int r0 = static_cast<int>(static_cast<long long>(rows) * k / p);
+            t.piece = k;
+            t.from = from + r0;
+            t.rows = static_cast<int>(static_cast<long long>(rows) * (k + 1) / p) - r0;
+            out[place + k] = t;
         }
     }
 }

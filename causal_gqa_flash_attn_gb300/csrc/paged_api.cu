@@ -75,8 +75,9 @@ fa_status paged_attn(const void *q, void *out, float *lse, int dtype, int64_t q_
     if (n_q_heads < 1 || n_q_heads % n_kv_heads || !known_type(dtype) || n_reqs < 0 ||
         n_tokens < 0 || sink < 0 || !good_pages(n_pages, max_pages, page_rows) ||
         !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap) ||
-        !aligned4(slopes))
+        (cap > 0.0f && !std::isfinite(4.0f / cap)) || !aligned4(slopes))
         return FA_ERR_INVALID;
+    if (cap > fa::kMostCap) return FA_ERR_UNSUPPORTED;
     const int group = n_q_heads / n_kv_heads;
     if (group > 16 || (group & (group - 1)) || n_reqs > 65536 || n_tokens > 1 << 26 ||
         static_cast<long long>(n_tokens) * n_q_heads > 1 << 30)

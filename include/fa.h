@@ -592,7 +592,8 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
 
 /* fa_paged_attn with changed scores: with s = scale * q . k, a key at distance d
  * (the query's position less the key's) scores cap * tanh(s / cap) (s itself where
- * cap is 0) - slopes[head] * d. cap >= 0; slopes is [n_q_heads] fp32 (device) or
+ * cap is 0) - slopes[head] * d. cap is 0 or up to 4096 (FA_ERR_UNSUPPORTED beyond,
+ * FA_ERR_INVALID where 4 / cap is not finite); slopes is [n_q_heads] fp32 (device) or
  * NULL. All else is as there, the log-sum-exp that of these scores; with neither cap nor
  * slopes it is that call. The tanh costs scores of FA_T_F16 and FA_T_BF16 calls up to
  * 2^-22 cap. */
@@ -629,7 +630,9 @@ fa_status fa_paged_attn_scored(const void *q, void *out, float *lse, int dtype, 
  *              is written.
  *   prefix     [n_docs] int32 (device) or NULL (none): keys of each document that
  *              all its queries attend, cut to [0, its tokens].
- *   scale      > 0; 0 means 1 / sqrt(head_dim). cap: >= 0, 0 for none.
+ *   scale      > 0; 0 means 1 / sqrt(head_dim).
+ *   cap        0 for none, or up to 4096 (FA_ERR_UNSUPPORTED beyond, FA_ERR_INVALID
+ *              where 4 / cap is not finite). Capped scores are off by up to 2^-21 cap.
  *   slopes     [n_q_heads] fp32 (device) or NULL for no bias. (They get no gradient.)
  *   workspace  >= the call's workspace bytes, 16-byte aligned; scratch. Calls that
  *              share a workspace must not overlap on the GPU.

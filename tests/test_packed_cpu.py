@@ -31,9 +31,9 @@ SHARED = dict(type=2, cu=16, prefix=None, docs=3, T=40, hq=8, hkv=2, hd=64, sink
               ws=16, wsb=1 << 40, stream=None)
 RULES = (dict(type=3), dict(type=-1), dict(docs=-1), dict(T=-1), dict(hq=0), dict(hkv=0), dict(hq=9), dict(hd=16),
          dict(hd=100), dict(sink=-1), dict(scale=-1.0), dict(scale=math.nan), dict(scale=math.inf), dict(cap=-1.0),
-         dict(cap=math.nan), dict(cap=math.inf), dict(cu=None), dict(cu=18), dict(prefix=18), dict(slopes=18),
+         dict(cap=math.nan), dict(cap=math.inf), dict(cap=1e-39), dict(cu=None), dict(cu=18), dict(prefix=18), dict(slopes=18),
          dict(ws=None), dict(ws=24))
-UNSUPPORTED = (dict(type=0), dict(hd=96), dict(hd=32), dict(hq=24), dict(hq=64, hkv=2), dict(docs=65537),
+UNSUPPORTED = (dict(type=0), dict(cap=4097.0), dict(hd=96), dict(hd=32), dict(hq=24), dict(hq=64, hkv=2), dict(docs=65537),
                dict(T=(1 << 26) + 1), dict(T=1 << 26, hq=32, hkv=2))
 
 
@@ -72,10 +72,16 @@ def test_packed_workspaces(fa):
     for size in (fa.packed_attn_workspace_bytes, fa.packed_attn_grad_workspace_bytes):
         assert size(3, 40, 8, 2, 96) == 0 and size(-1, 40, 8, 2, 64) == 0 and size(1, 40, 9, 2, 64) == 0
         assert 0 < size(0, 0, 8, 2, 64) < size(1, 1, 8, 2, 64) <= size(1, 5000, 8, 2, 64)
-    # the gradient keeps two numbers for each row, and one tile more a document
+    # the gradient keeps two numbers for each row, and partial sums, 48 MiB at most
     rows = 8192 * 16
-    assert fa.packed_attn_grad_workspace_bytes(1, 8192, 16, 2, 256) >= 8 * rows
-    assert fa.packed_attn_grad_workspace_bytes(1, 8192, 16, 2, 256) < 16 * rows
+    assert 8 * rows <= fa.packed_attn_grad_workspace_bytes(1, 8192, 16, 2, 256) < 16 * rows + (48 << 20)
+    assert fa.packed_attn_grad_workspace_bytes(1, 300, 4, 4, 64) < 1 << 18
+    for n in (1, 200, 5000, 1 << 20):
+        for docs in (1, 7, 5000):
+            for hq, hkv, hd in ((1, 1, 64), (16, 1, 128), (32, 8, 256)):
+                assert fa.packed_attn_workspace_bytes(docs, n, hq, hkv, hd) < (1 << 20) + 8 * n * hq + 512 * docs
+                assert (fa.packed_attn_grad_workspace_bytes(docs, n, hq, hkv, hd)
+                        < (50 << 20) + 16 * n * hq + 2048 * hkv * docs)
 
 
 def test_scored_refusals(fa):
@@ -87,7 +93,8 @@ def test_scored_refusals(fa):
     for bad in (dict(cap=-1.0), dict(cap=math.nan), dict(cap=math.inf), dict(slopes=18), dict(q=None), dict(rows=24),
                 dict(out=16), dict(scale=-1.0), dict(type=3), dict(sink=-1)):
         assert call(**bad) == fa.ERR_INVALID, bad
-    assert call(hd=96) == fa.ERR_UNSUPPORTED
+    assert call(cap=1e-39) == fa.ERR_INVALID
+    assert call(hd=96) == fa.ERR_UNSUPPORTED and call(cap=5000.0) == fa.ERR_UNSUPPORTED
     assert call(T=0) == fa.OK
 
 
