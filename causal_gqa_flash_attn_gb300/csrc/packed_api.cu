@@ -37,8 +37,8 @@ struct Layout {
     int most_rows, most_keys, slots;
     size_t blocks;  // 128-row blocks of a kv head
 };
-constexpr size_t kPartialBytes = 48 << 20;  // of partial sums at most
-constexpr int kParts = 2;  // pieces of the work of dk and dv an SM, about
+constexpr size_t kPartialBytes = 48 << 20;  // of partial sums at most, so that they stay in L2
+constexpr int kParts = 2;  // pieces of the work of dk and dv an SM, about; more of them cost joins
 
 Layout layout(int n_docs, int n_tokens, int n_q_heads, int n_kv_heads, int head_dim, int rows, bool grad) {
     Layout w;

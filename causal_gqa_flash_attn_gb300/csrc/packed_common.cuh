@@ -418,7 +418,8 @@ struct PackedGradArgs {
     unsigned *err;
 };
 enum { kGradQ = 0, kGradKV = 1, kGradK = 2, kGradV = 3 };
-// Pieces of a key tile are no smaller than this many row tiles.
+// Pieces of a key tile are no smaller than this many row tiles: each writes 128 x head_dim
+// fp32 sums of dk and of dv, which are read again, and begins with copies that nothing hides.
 constexpr int kPackedLeastPiece = 4;
 // Rows (or keys) of a moving tile.
 constexpr int packed_grad_rows(int hd) { return hd == 256 ? 64 : 128; }

@@ -11,10 +11,22 @@
 //               document V's rows past its end become zeros, as other documents and
 //               padding may hold anything and 0 * inf is not 0.
 //   warp 1      issues the products: S = Q K^T into TMEM, O += P V with P from TMEM.
-//   warps 4..   softmax, one thread a row: the running maximum in the exp2 domain, which
-//               moves only when a score passes it by 2^8, P rounded to the inputs' type
-//               over S, sums of the unrounded weights in fp32, and the output.
-// With two tiles the products of one run under the softmax of the other.
+//   warps 4-11  softmax, one thread a row and tile (or, with one tile, two threads a row, each
+//               with half of the columns): the running maximum in the exp2 domain, which moves
+//               only when a score passes it by 2^8, so that O is seldom rescaled; P, rounded to
+//               the inputs' type as the products take it (half a step of P, the plain form's own
+//               rounding), over S; sums of the unrounded weights in fp32; and the output.
+// With two tiles the products of one run under the softmax of the other; with one (whose O takes
+// half of TMEM) S has two places, and S(i + 1) runs under the softmax of S(i). TMEM is full either
+// way: 2 x (O 128 + S 128) columns, or O 256 + 2 x S 128.
+//
+// What bounds it: at head_dim 128 the chain S -> softmax -> P V of each tile, of which TMEM holds
+// two and no third (16384 tokens, 8/2 heads: 370 us, 1486 TFLOP/s of 1921 measured for bf16); at
+// 256 the tensor cores (8192 tokens, 16/2 heads: 327 us, 1680 TFLOP/s); at 64, and wherever scores
+// are capped, the special units, which take 32 exponentials or 16 reciprocals a clock and SM (64:
+// 279 us; 128 capped: 588 us). Documents of a few tiles spend as long on a unit's first copies and
+// its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 76 us, 674
+// TFLOP/s).
 #pragma once
 
 #include "packed_common.cuh"

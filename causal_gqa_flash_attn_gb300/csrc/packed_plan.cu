@@ -9,6 +9,10 @@
 // A tile of keys whose rows are many (the first keys of a long document are seen by all of it) is
 // cut into pieces, so that a few such tiles do not keep a few SMs busy alone; their sums are
 // added in the order of the pieces.
+//
+// Bound by latency: a launch, dependent reads and shared atomics (9 us of 23 documents),
+// of which the kernel behind it hides its start. Batches of up to 32 documents whose units all have
+// an SM go without (direct_tile).
 #include "packed_common.cuh"
 
 namespace fa {

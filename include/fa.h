@@ -596,7 +596,7 @@ fa_status fa_paged_attn(const void *q, void *out, float *lse, int dtype, int64_t
  * FA_ERR_INVALID where 4 / cap is not finite); slopes is [n_q_heads] fp32 (device) or
  * NULL. All else is as there, the log-sum-exp that of these scores; with neither cap nor
  * slopes it is that call. The tanh costs scores of FA_T_F16 and FA_T_BF16 calls up to
- * 2^-22 cap. */
+ * 2^-21 cap. */
 fa_status fa_paged_attn_scored(const void *q, void *out, float *lse, int dtype, int64_t q_stride,
                                int64_t out_stride, const int32_t *cu_q, const int32_t *seq_lens,
                                const int32_t *block_table, int max_pages, const void *pages,
