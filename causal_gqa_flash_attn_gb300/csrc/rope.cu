@@ -41,8 +41,6 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     wait_for_stream();
     extern __shared__ float4 rope_smem[];
     const int half = a.rotary_dim / 2;
-    const int n_rot = half / V;            // items of V pairs
-    const int n_items = n_rot + a.n_copy;  // and of 2 V values that stay as they are
     float *cs = reinterpret_cast<float *>(rope_smem);  // [tokens][half] cosines, then sines
     float *sn = cs + a.tokens_per_block * half;
     const int tok0 = blockIdx.x * a.tokens_per_block;
@@ -56,7 +54,7 @@ __global__ void __launch_bounds__(kRopeThreads, 6) rope_kernel(RopeArgs a) {
     __syncthreads();
     const int h0 = blockIdx.y * a.heads_per_block;
     const int heads = min(a.heads_per_block, a.n_q_heads + a.n_kv_heads - h0);
-    turn_heads<T, V, ADJ>(a, half, n_rot, n_items, tok0, n_tok, h0, heads, cs, sn);
+    turn_heads<T, V, ADJ>(a, half, tok0, n_tok, h0, heads, cs, sn);
 }
 
 template <typename T, int V>

@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kern
         }
     }
     // ---- q
-    if (h0 < q_end) turn_heads<T, V, ADJ>(a, half, half / V, half / V + a.n_copy, tok0, n_tok, h0, q_end - h0, cs, sn);
+    if (h0 < q_end) turn_heads<T, V, ADJ>(a, half, tok0, n_tok, h0, q_end - h0, cs, sn);
 }
 
 template <typename T, int HD, int V>

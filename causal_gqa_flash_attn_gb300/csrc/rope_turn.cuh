@@ -51,17 +51,17 @@ __device__ __forceinline__ void turn_table(const RopeArgs &a, int half, int tok0
 }
 
 // Heads h0 .. h0 + heads - 1 (the q heads, then the k heads) of the block's tokens through the
-// table, by all of its threads: n_rot items of V pairs, and up to n_items of 2 V values that stay
-// as they are.
+// table, by all of its threads.
 template <typename T, int V, bool ADJ>
-__device__ __forceinline__ void turn_heads(const RopeArgs &a, int half, int n_rot, int n_items, int tok0, int n_tok,
-                                           int h0, int heads, const float *cs, const float *sn) {
+__device__ __forceinline__ void turn_heads(const RopeArgs &a, int half, int tok0, int n_tok, int h0, int heads,
+                                           const float *cs, const float *sn) {
     using W = Vec<T, V>;
+    const int n_rot = half / V;            // items of V pairs
+    const int n_items = n_rot + a.n_copy;  // and of 2 V values that stay as they are
     // threads of a head, heads that the block takes at once, and this thread's first one
     const int lanes = min(n_items, kRopeThreads), rows = kRopeThreads / lanes;
     const int row = threadIdx.x / lanes, lane = threadIdx.x - row * lanes;
-    if (row >= rows) return;
-    int tok = row / heads, head = row - tok * heads;
+    int tok = row < rows ? row / heads : n_tok, head = row - tok * heads;
     while (tok < n_tok) {
         const int hh = h0 + head;
         const bool isq = hh < a.n_q_heads;
