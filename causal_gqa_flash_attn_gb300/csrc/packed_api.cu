@@ -347,7 +347,7 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     };
     cudaError_t e = direct ? cudaSuccess : fa::launch_packed_plan(p, s);
     if (e == cudaSuccess)
-        e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, direct ? sms : 8 * sms), s);
+        e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, direct ? sms : 64 * sms), s);
     if (e == cudaSuccess) e = launch(a, fa::kGradQ, blocks_of(w.most_rows, sms));
     if (head_dim < 256) {
         if (e == cudaSuccess) e = launch(b, fa::kGradKV, blocks_of(w.most_keys, sms));
