@@ -23,8 +23,9 @@
 // What bounds it: at head_dim 128 the chain S -> softmax -> P V of each tile, of which TMEM holds
 // two and no third (16384 tokens, 8/2 heads: 370 us, 1486 TFLOP/s of 1921 measured for bf16); at
 // 256 the tensor cores (8192 tokens, 16/2 heads: 327 us, 1680 TFLOP/s); at 64, and wherever scores
-// are capped, the special units, which take 32 exponentials or 16 reciprocals a clock and SM (64:
-// 279 us; 128 capped: 588 us). Documents of a few tiles spend as long on a unit's first copies and
+// are capped, the softmax warps, two a scheduler, with issue slots and special units half full each
+// and the latter's slow ones (a clock and SM: 32 exponentials, but 16 reciprocals) behind one another
+// (64: 279 us; 128 capped: 588 us). Documents of a few tiles spend as long on a unit's first copies and
 // its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 76 us, 674
 // TFLOP/s).
 #pragma once

@@ -7,6 +7,10 @@
 // cosines into shared memory, the q heads through them as in rope.cu, then each row
 // of K and V by head_dim / 16 lanes as in paged_kv.cu, where a lane reads its 16
 // values of k and the 16 that they are paired with.
+//
+// Bound by HBM and, close behind, by instructions (two thirds of the issue slots): 30000 tokens, 16/4 heads x 128 in
+// bf16 68 us, 0.70 of HBM (fa_rope and fa_paged_append one behind the other 70.5: the rotated k stays in L2);
+// 15000 tokens, 16/2 x 256 in fp32 97 (103); 30 tokens 3.7 (4.5), and one call less on the host.
 #include <algorithm>
 
 #include "paged_encode.cuh"
@@ -15,10 +19,11 @@
 namespace fa {
 namespace {
 
-// Blocks of an SM: what hides q's latency is the number of threads, as in rope.cu (30000 tokens, 16/4 heads x 128
-// in bf16: 122 us with 2 blocks, 90 with 3, 78 with 4, 70 with 6, 78 with 8; fp32 104 with 4, 114 with 6).
+// Blocks of an SM: what hides q's latency is the number of threads, as in rope.cu (30000 tokens, 16/4 heads x 128,
+// blocks of 16 tokens, in bf16: 122 us with 2 blocks, 90 with 3, 78 with 4, 70 with 6, 78 with 8; blocks of 8 tokens
+// 71 with 5, 68 with 6; in fp32 105 with 5, 114 with 4).
 template <typename T>
-constexpr int kRopeBlocks = sizeof(T) == 4 ? 4 : 6;
+constexpr int kRopeBlocks = sizeof(T) == 4 ? 5 : 6;
 constexpr int kItems = 1024;  // items (two vectors of q, or a lane's values of K and V) of a block
 
 template <typename T, int HD, int V, bool ADJ>
@@ -132,7 +137,9 @@ cudaError_t launch(RopeAppendArgs b, cudaStream_t stream) {
                           static_cast<long long>(b.append.n_kv) * (HD / 16);  // items of a token
     const int fit = std::min<int>(kRopeTokens, 48 * 1024 / (half * 8));
     int tokens = static_cast<int>(std::min<long long>(fit, std::max<long long>(1, kItems / row)));
-    if (a.n_tokens >= 2 * fit * device_sm_count()) tokens = fit;
+    // many tokens: blocks of 8, which share a page's words and a start, and are many enough to end together (30000
+    // tokens, 16/4 heads x 128 in bf16: 76.6 us with 4, 67.7 with 8, 72.0 with 16; 20000, 16/2 x 256: 81, 77, 82)
+    if (a.n_tokens >= 2 * kRopeTokens * device_sm_count()) tokens = std::min(fit, 8);
     // few tokens: a block takes one, and the heads are split over blocks too, as in rope.cu
     const int sms = device_sm_count();
     if (a.n_tokens <= sms * tokens) tokens = std::max(1, a.n_tokens / sms);
