@@ -53,8 +53,9 @@ def document(q, k, v, slope, *, prefix=0, sink=0, win=0, scale=0.0, cap=0.0, dou
         # D from the rounded out, and sums in 32 bits
         D_sum = (dout * out).abs().sum(-1, keepdim=True)
         rest = 2.0 ** -21 * (dout.abs() @ v.abs().T + D_sum)
+        # (down: 1 - tanh^2 is off by 2^-52 in 64 bits, and the library's is 2^-61 at least)
         made.update(dq=scale * t @ k, dk=scale * t.T @ q, dv=w.T @ dout,
-                    t=t, w=w, D_sum=D_sum, t_err=2 * t.abs() * ds + w * rest * down + w * (dw - D).abs() * 2.0 ** -20,
+                    t=t, w=w, D_sum=D_sum, t_err=2 * t.abs() * ds + w * rest * (down + 2.0 ** -50) + w * (dw - D).abs() * 2.0 ** -20,
                     w_err=2 * wrong, scale=scale, down=down)
     return made
 

@@ -44,11 +44,13 @@ def pages_of(rng, rows, hkv, hd, page_rows, strong=1.0):
 
 
 def attend(q, first, k, v, cap, slopes, sink, win, scale):
-    """Queries q [n][Hq][hd] at positions first.. over rows k, v [L][Hkv][hd]: out, lse, the sums of w |v| and
-    the scores' error by their 32-bit sums."""
+    """Queries q [n][Hq][hd] at positions first.. over rows k, v [L][Hkv][hd]: out, lse, the sums of w |v|,
+    what the scores' 32-bit sums add up, and what K's codes add to that with their offset."""
     n, hq, hd = q.shape
     g = hq // k.shape[1]
     out, lse, size, off = np.zeros(q.shape), np.full((hq, n), -math.inf), np.zeros(q.shape), np.zeros((hq, n))
+    codes = np.zeros((hq, n))
+    step = np.repeat(np.abs(k).reshape(*k.shape[:2], hd // 32, 32).max(-1) / 7, 32, -1)
     for i in range(n):
         p, j = first + i, np.arange(k.shape[0])
         see = j <= p
@@ -68,7 +70,8 @@ def attend(q, first, k, v, cap, slopes, sink, win, scale):
             # tensor cores): relative to what is added up
             e = np.abs(kk) @ np.abs(q[i, h]) * scale + np.abs(x) + (slopes[h] * (p - j[see]) if slopes is not None else 0)
             off[h, i] = (w * e).sum() + abs(lse[h, i]) + 1
-    return out, lse, size, off
+            codes[h, i] = (w * (16 * step[see, h // g] @ np.abs(q[i, h]) * scale)).sum()
+    return out, lse, size, off, codes
 
 
 def run_paged(rng, dtype, rows, nq, hq, hkv, hd, page_rows, cap=0.0, bias=False, sink=0, win=0, gain=1.0, scale=0.0):
@@ -92,7 +95,7 @@ def run_paged(rng, dtype, rows, nq, hq, hkv, hd, page_rows, cap=0.0, bias=False,
     half = ref.HALF_STEP[dtype]
     for r, n in enumerate(rows):
         a, b = cu[r], cu[r + 1]
-        want, wlse, size, off = attend(q[a:b], n - (b - a), *held[r], cap, slopes, sink, win,
+        want, wlse, size, off, codes = attend(q[a:b], n - (b - a), *held[r], cap, slopes, sink, win,
                                        scale or 1 / math.sqrt(hd))
         # scores: 2^-21 of what they add up; the tanh 2^-21 of the cap (2^-23 for fp32, by tanhf)
         ds = off * 2.0 ** -21 + cap * (2.0 ** -23 if dtype == "f32" else 2.0 ** -21)
@@ -110,6 +113,9 @@ def run_paged(rng, dtype, rows, nq, hq, hkv, hd, page_rows, cap=0.0, bias=False,
         assert (np.abs(got[a:b] - want) <= tol).all(), (r, np.abs(got[a:b] - want).max())
         live = np.isfinite(wlse)
         assert np.array_equal(live, np.isfinite(glse[:, a:b])) and (glse[:, a:b][~live] == -math.inf).all()
+        # K's codes enter the products with 16-bit queries with their offset 8, too: terms of up to 16 code steps
+        # (a seventh of a block's largest value or less), whose sum is cut like the scores' own
+        ds = ds + (0.0 if dtype == "f32" else codes * 2.0 ** -21)
         assert (np.abs(glse[:, a:b] - wlse)[live] <= ds[live] + 2.0 ** -21).all(), r
 
 
