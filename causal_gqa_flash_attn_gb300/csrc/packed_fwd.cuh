@@ -26,7 +26,7 @@
 // are capped, the softmax warps, two a scheduler, with issue slots and special units half full each
 // and the latter's slow ones (a clock and SM: 32 exponentials, but 16 reciprocals) behind one another
 // (64: 279 us; 128 capped: 588 us). Documents of a few tiles spend as long on a unit's first copies and
-// its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 76 us, 674
+// its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 73 us, 702
 // TFLOP/s).
 #pragma once
 

@@ -10,7 +10,7 @@
 // cut into pieces, so that a few such tiles do not keep a few SMs busy alone; their sums are
 // added in the order of the pieces.
 //
-// Bound by latency: a launch, dependent reads and shared atomics (9 us of 23 documents),
+// Bound by latency: a launch, dependent reads and shared atomics (7 us of 23 documents),
 // of which the kernel behind it hides its start. Batches of up to 32 documents whose units all have
 // an SM go without (direct_tile).
 #include "packed_common.cuh"

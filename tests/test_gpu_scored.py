@@ -116,7 +116,7 @@ def run_paged(rng, dtype, rows, nq, hq, hkv, hd, page_rows, cap=0.0, bias=False,
         # K's codes enter the products with 16-bit queries with their offset 8, too: terms of up to 16 code steps
         # (a seventh of a block's largest value or less), whose sum is cut like the scores' own
         ds = ds + (0.0 if dtype == "f32" else codes * 2.0 ** -21)
-        assert (np.abs(glse[:, a:b] - wlse)[live] <= ds[live] + 2.0 ** -21).all(), r
+        assert (np.abs(glse[:, a:b][live] - wlse[live]) <= ds[live] + 2.0 ** -21).all(), r
 
 
 @pytest.mark.parametrize("cap,bias", [(0.0, True), (20.0, False), (3.0, True)])
