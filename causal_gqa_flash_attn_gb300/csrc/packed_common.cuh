@@ -178,7 +178,8 @@ __device__ __forceinline__ float min_nan(float x, float y) {  // NaN if either i
     return d;
 }
 // r of two scores. Their reciprocals from that of the product, as a reciprocal costs the special units
-// what two exponentials do; 2^63 is where tanh has long been 1.
+// what two exponentials do; 2^63 is where tanh has long been 1. A NaN in one makes both NaN, so that
+// both have to be the document's own (or 0), even where one of them is masked afterwards.
 __device__ __forceinline__ Two cap_r(Two s, const ScoreRule &c) {
     const float2 z = both(s * two(c.a));
     const Two p = two(ex2(min_nan(z.x, 63.0f)), ex2(min_nan(z.y, 63.0f))) + two(1.0f);

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 uint64_t *full = is_k ? &bars.k_full[st] : &bars.v_full[st];
                 uint8_t *dst = smem + (is_k ? C::OFF_K : C::OFF_V) + st * C::TILE;
                 const int rows = min(BK, u.len - kt * BK);
-                // columns of S past the end are masked, but V's rows are summed
+                // scores past the end are masked, but V's rows are summed
                 const bool patch = !is_k && rows < BK;
                 uint64_t *bar = patch ? &bars.patch : full;
                 if (lane == 0) {
@@ -408,6 +408,16 @@ __global__ void __launch_bounds__(FwdCfg<HD>::THREADS, 1)
                 tmem_wait_ld();
                 reg_fence<COLS>(s);
 
+                if (CAP && !whole) {
+                    // A reciprocal serves two columns: what lies behind an odd document, masked further down, must
+                    // not reach the document's last key. (Zeros in K's tile instead, as in V's, keep the copies
+                    // waiting: 8192 tokens in 23 documents, 16/2 heads x 256, 75.5 us for 73.)
+                    const int past = u.len - j0;  // the first column behind it
+                    if ((past & 1) && past > 0 && past < COLS) {
+#pragma unroll
+                        for (int c = 1; c < COLS; c += 2) s[c] = c == past ? 0u : s[c];
+                    }
+                }
                 constexpr bool kScaled = CAP || BIAS;  // s goes to the exp2 domain first
                 if (kScaled) {
                     const float far = static_cast<float>(p - j0);  // exact up to 2^24

@@ -187,6 +187,34 @@ def test_other_documents_and_padding_may_hold_anything(dtype, hd):
         assert torch.equal(a[keep], b[keep]), name
 
 
+@pytest.mark.parametrize("rule", [*RULES, "capped prefix"])
+@pytest.mark.parametrize("hd", [64, 128, 256])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_neighbours_of_a_document_change_no_bit(dtype, hd, rule):
+    """Documents of odd and even lengths between others that hold NaN, infinities or the largest values, under every
+    rule (the last one: capped scores, and a prefix of the whole document)."""
+    largest = torch.finfo(DT[dtype]).max
+    for n, hq, hkv in ((1, 2, 2), (37, 4, 1), (127, 2, 2), (129, 4, 1), (130, 2, 2), (131, 8, 2)):
+        lens = [70, n, 45]
+        given = dict(cap=20.0, prefix=lens) if rule == "capped prefix" else rule_of(rule, hq, lens)
+        q, k, v, dout, cu = batch(lens, hq, hkv, hd, dtype, pad=9, lead=5)
+        out, lse = forward(q, k, v, cu, **given)
+        made = backward(q, k, v, out, lse, dout, cu, **given)
+        keep = torch.zeros(q.shape[0], dtype=torch.bool, device="cuda")
+        keep[cu[1]:cu[2]] = True
+        for junk in ((math.nan, math.inf, -math.inf), (largest, -largest, 0.0)):
+            bad = torch.tensor(junk, device="cuda", dtype=DT[dtype])
+            q2, k2, v2, dout2, out2 = (
+                torch.where(keep[:, None, None], t, bad[torch.arange(t.numel(), device="cuda") % 3].view(t.shape))
+                for t in (q, k, v, dout, out))
+            lse2 = torch.where(keep, lse, torch.nan)
+            again = forward(q2, k2, v2, cu, **given)
+            assert torch.equal(again[0][keep], out[keep]) and torch.equal(again[1][:, keep], lse[:, keep]), (n, junk)
+            for name, a, b in zip(("dq", "dk", "dv"), backward(q2, k2, v2, out2, lse2, dout2, cu, **given), made):
+                assert torch.equal(a[keep], b[keep]), (name, n, junk)
+    assert fa().get_device_error() == fa().OK
+
+
 def test_gradient_against_differences():
     """The gradient along a direction against central differences of the definition in 64 bits."""
     lens, rule = [60, 33], dict(cap=4.0, sink=2, win=20, prefix=[9, 0])
