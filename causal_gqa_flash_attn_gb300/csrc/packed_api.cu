@@ -82,7 +82,9 @@ fa_status check_rule(int dtype, const int32_t *cu, const int32_t *prefix, int si
                      const float *slopes, const void *workspace) {
     if (sink < 0 || !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap))
         return FA_ERR_INVALID;
-    if (cap > 0.0f && !std::isfinite(4.0f / cap)) return FA_ERR_INVALID;
+    // the factor of a score (score_rule): an infinite one would make scores of 0 a NaN
+    if (!std::isfinite(4.0f * scale) || (cap > 0.0f && !std::isfinite(4.0f * std::fmax(scale, 1.0f) / cap)))
+        return FA_ERR_INVALID;
     if (dtype == FA_T_F32 || cap > fa::kMostCap) return FA_ERR_UNSUPPORTED;
     if (dtype != FA_T_F16 && dtype != FA_T_BF16) return FA_ERR_INVALID;
     if (!aligned(cu, 4) || !aligned(prefix, 4) || !aligned(slopes, 4) || !aligned(workspace, 16))
