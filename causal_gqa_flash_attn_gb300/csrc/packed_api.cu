@@ -297,7 +297,8 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
                         static_cast<long long>(w.most_keys) * n_kv_heads <= sms;
     t.direct = direct ? fa::PackedDirect{cu_docs, prefix, n_docs, n_tokens} : fa::PackedDirect{};
 
-    fa::PackedGradArgs a;
+    fa::PackedGradPair pair;
+    fa::PackedGradArgs &a = pair.q, &b = pair.k;  // of dq, and of dk and dv
     a.header = p.header;
     a.L = t.L;
     a.D = t.D;
@@ -315,7 +316,7 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     a.scale = scale > 0.0f ? scale : 1.0f / sqrtf(static_cast<float>(head_dim));
     a.score = fa::score_rule(a.scale, cap);
     a.err = err;
-    fa::PackedGradArgs b = a;  // of dk and dv
+    b = a;
     a.tiles = p.rows;
     a.n_tiles = &p.header->row_tiles;
     a.counter = &p.header->counters[0];
@@ -343,21 +344,16 @@ fa_status fa_packed_attn_grad(const void *q, const void *k, const void *v, const
     auto blocks_of = [&](int tiles, int most) {
         return static_cast<int>(std::min<long long>(most, static_cast<long long>(tiles) * n_kv_heads));
     };
-    auto launch = [&](const fa::PackedGradArgs &g, int mode, int blocks) {
-        return dtype == FA_T_BF16 ? fa::launch_packed_grad_bf16(g, mode, head_dim, cap > 0.0f, blocks, s)
-                                  : fa::launch_packed_grad_f16(g, mode, head_dim, cap > 0.0f, blocks, s);
-    };
+    pair.q_blocks = blocks_of(w.most_rows, sms);
+    pair.k_blocks = blocks_of(w.most_keys, sms);
+    fa::PackedGradArgs dv_alone = b;  // head_dim 256
+    dv_alone.counter = &p.header->counters[2];
     cudaError_t e = direct ? cudaSuccess : fa::launch_packed_plan(p, s);
     if (e == cudaSuccess)
         e = fa::launch_packed_stats(t, dtype, head_dim, blocks_of(w.most_rows, direct ? sms : 64 * sms), s);
-    if (e == cudaSuccess) e = launch(a, fa::kGradQ, blocks_of(w.most_rows, sms));
-    if (head_dim < 256) {
-        if (e == cudaSuccess) e = launch(b, fa::kGradKV, blocks_of(w.most_keys, sms));
-    } else {
-        if (e == cudaSuccess) e = launch(b, fa::kGradK, blocks_of(w.most_keys, sms));
-        b.counter = &p.header->counters[2];
-        if (e == cudaSuccess) e = launch(b, fa::kGradV, blocks_of(w.most_keys, sms));
-    }
+    if (e == cudaSuccess)
+        e = dtype == FA_T_BF16 ? fa::launch_packed_grad_bf16(pair, &dv_alone, head_dim, cap > 0.0f, s)
+                               : fa::launch_packed_grad_f16(pair, &dv_alone, head_dim, cap > 0.0f, s);
     return from_cuda(e);
 }
 

@@ -6,10 +6,10 @@
 //   t_ij = P_ij (dout_i . v_j - D_i) f'(s_ij)        (f' = 1 - tanh^2 where scores are capped)
 //   dq_i = scale sum_j t_ij k_j,   dk_j = scale sum_i t_ij q_i.
 //
-// Sums in a fixed order: one kernel holds 128 rows of queries and
-// streams the keys past them (dq), one holds 128 keys and streams the rows of queries
+// Sums in a fixed order: some blocks hold 128 rows of queries and
+// stream the keys past them (dq), others hold 128 keys and stream the rows of queries
 // past them, the heads of the group among them (dk and dv; with head_dim 256, whose
-// accumulators take half of TMEM each, a kernel for dk and one for dv). The price is
+// accumulators take half of TMEM each, dk here and dv in a kernel of its own). The price is
 // that S and dout V^T are made twice: 7 products instead of 5 (8 with head_dim 256).
 // All are one template: with stationary tiles X1, X2 and moving tiles Y1, Y2,
 //   S = X1 Y1^T, T = X2 Y2^T,  acc1 += t Y1 (dq or dk),  acc2 += P Y2 (dv)
@@ -91,9 +91,9 @@ struct GradBars {
 };
 static_assert(sizeof(GradBars) <= 640, "barrier block");
 
+// The units of one gradient (or of dk and dv), for block `block` of `blocks` that share them.
 template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
-__global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
-    packed_grad_kernel(const __grid_constant__ PackedGradArgs a) {
+__device__ __forceinline__ void grad_units(const PackedGradArgs &a, int block, int blocks) {
     using C = GradCfg<HD, MODE>;
     constexpr int BN = C::BN, PART = C::PART, N1 = C::N1, N2 = C::N2;
     constexpr uint32_t IDESC_S = idesc_16<BF16>(128, BN, 0, 0);
@@ -158,12 +158,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars.tmem_base;
-    // dk (and dv) do not use dq: their blocks take the SMs that dq's leave. They begin when dq's have seen
-    // the row numbers, which are all that they need, and end when dq's have, so that what follows them in
-    // the stream follows dq as well. (dv alone uses dk's partial sums, and comes after it.)
-    constexpr bool FOLLOWS = MODE == kGradKV || MODE == kGradK;
-    if (!FOLLOWS) wait_for_stream();
-    if (MODE == kGradQ) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    wait_for_stream();
 
     auto next_unit = [&](int j, PackedTile *u) -> bool {
         const int slot = j % kPackedRing;
@@ -195,7 +190,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             // without a plan: the one unit of this block
             const bool direct = a.direct.cu != nullptr;
             PackedTile own;
-            const int units = a.n_kv * (direct ? direct_tile<!C::ROWS_STAY>(a.direct, blockIdx.x / a.n_kv, tile_tokens, step_tokens,
+            const int units = a.n_kv * (direct ? direct_tile<!C::ROWS_STAY>(a.direct, block / a.n_kv, tile_tokens, step_tokens,
                                                                             7 - lg, a.sink, a.win, err, &own)
                                                : *a.n_tiles);
             Arms x_arms, xs_arms, y1_arms[3], y2_arms[3], l_arms[2];
@@ -203,7 +198,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
             bool ok = true;
             auto fetch = [&](int w, PackedTile *u) {
                 u->head = -1;
-                if (w >= units || (direct && w != static_cast<int>(blockIdx.x))) return false;
+                if (w >= units || (direct && w != block)) return false;
                 *u = direct ? own : a.tiles[w / a.n_kv];
                 u->head = w % a.n_kv;
                 return true;
@@ -288,7 +283,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                 ++l_arms[st].n;
                 return true;
             };
-            int t = 0, w = blockIdx.x;
+            int t = 0, w = block;
             PackedTile u, un;
             bool have = fetch(w, &u);
             ok = publish(0, u);
@@ -304,7 +299,7 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
                     if (ok) ok = load_y(t + i, at, u, false);
                     if (C::X1_TMEM && C::HAS_T && ok && i == 0) ok = load_x2(j, u);
                     if (ok && i == cnt - 1) {
-                        if (lane == 0) w = direct ? units : static_cast<int>(gridDim.x + atomicAdd(a.counter, 1u));
+                        if (lane == 0) w = direct ? units : blocks + static_cast<int>(atomicAdd(a.counter, 1u));
                         w = __shfl_sync(~0u, w, 0);
                         more = fetch(w, &un);
                     }
@@ -776,41 +771,60 @@ __global__ void __launch_bounds__((GradCfg<HD, MODE>::THREADS), 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-    if (FOLLOWS) wait_for_stream();
 }
 
-template <int HD, bool BF16, bool CAP, bool BIAS, int MODE>
-cudaError_t launch_grad(const PackedGradArgs &a, int blocks, cudaStream_t stream) {
-    using C = GradCfg<HD, MODE>;
-    auto kernel = packed_grad_kernel<HD, BF16, CAP, BIAS, MODE>;
-    static std::atomic<uint64_t> made{0};
-    const cudaError_t e = allow_smem(kernel, C::SMEM, &made);
-    if (e != cudaSuccess) return e;
-    return launch_after(kernel, dim3(blocks), C::THREADS, C::SMEM, stream, a);
+// One launch for both, as neither uses what the other makes: the blocks of dk (and dv) are those behind dq's, and take
+// the SMs that dq's leave. (As a kernel that dq's let begin early they would have to do without the wait for what is
+// before dq in the stream, which is what makes the rows' sums visible to them.)
+template <int HD, bool BF16, bool CAP, bool BIAS, int SECOND>
+__global__ void __launch_bounds__((GradCfg<HD, kGradQ>::THREADS), 1)
+    packed_grad_kernel(const __grid_constant__ PackedGradPair p) {
+    const int block = blockIdx.x;
+    if (block < p.q_blocks)
+        grad_units<HD, BF16, CAP, BIAS, kGradQ>(p.q, block, p.q_blocks);
+    else
+        grad_units<HD, BF16, CAP, BIAS, SECOND>(p.k, block - p.q_blocks, p.k_blocks);
+}
+// dv of head_dim 256, which uses dk's partial sums after it.
+template <int HD, bool BF16, bool CAP, bool BIAS>
+__global__ void __launch_bounds__((GradCfg<HD, kGradV>::THREADS), 1)
+    packed_grad_v_kernel(const __grid_constant__ PackedGradArgs a) {
+    grad_units<HD, BF16, CAP, BIAS, kGradV>(a, blockIdx.x, gridDim.x);
 }
 
-template <int HD, bool BF16, int MODE>
-cudaError_t launch_grad_rule(const PackedGradArgs &a, bool cap, int blocks, cudaStream_t stream) {
+template <int HD, bool BF16, bool CAP, bool BIAS>
+cudaError_t launch_grad(const PackedGradPair &p, const PackedGradArgs *v, cudaStream_t stream) {
+    constexpr int SECOND = HD < 256 ? kGradKV : kGradK;
+    using Q = GradCfg<HD, kGradQ>;
+    using K = GradCfg<HD, SECOND>;
+    using V = GradCfg<HD, kGradV>;
+    static_assert(Q::THREADS == K::THREADS, "one launch");
+    constexpr size_t SMEM = Q::SMEM > K::SMEM ? Q::SMEM : K::SMEM;
+    static std::atomic<uint64_t> made{0}, made_v{0};
+    auto kernel = packed_grad_kernel<HD, BF16, CAP, BIAS, SECOND>;
+    cudaError_t e = allow_smem(kernel, SMEM, &made);
+    if (e == cudaSuccess) e = launch_after(kernel, dim3(p.q_blocks + p.k_blocks), Q::THREADS, SMEM, stream, p);
+    if constexpr (HD == 256) {
+        auto kernel_v = packed_grad_v_kernel<HD, BF16, CAP, BIAS>;
+        if (e == cudaSuccess) e = allow_smem(kernel_v, V::SMEM, &made_v);
+        if (e == cudaSuccess) e = launch_after(kernel_v, dim3(p.k_blocks), V::THREADS, V::SMEM, stream, *v);
+    }
+    return e;
+}
+
+template <int HD, bool BF16>
+cudaError_t launch_grad_rule(const PackedGradPair &p, const PackedGradArgs *v, bool cap, cudaStream_t stream) {
     if (cap)
-        return a.slopes ? launch_grad<HD, BF16, true, true, MODE>(a, blocks, stream)
-                        : launch_grad<HD, BF16, true, false, MODE>(a, blocks, stream);
-    return a.slopes ? launch_grad<HD, BF16, false, true, MODE>(a, blocks, stream)
-                    : launch_grad<HD, BF16, false, false, MODE>(a, blocks, stream);
+        return p.q.slopes ? launch_grad<HD, BF16, true, true>(p, v, stream) : launch_grad<HD, BF16, true, false>(p, v, stream);
+    return p.q.slopes ? launch_grad<HD, BF16, false, true>(p, v, stream) : launch_grad<HD, BF16, false, false>(p, v, stream);
 }
 
-// Head_dim 64 and 128 have dq, and dk with dv; 256 has each by itself.
 template <bool BF16>
-cudaError_t launch_grad_type(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream) {
-    if (hd == 64)
-        return mode == kGradQ ? launch_grad_rule<64, BF16, kGradQ>(a, cap, blocks, stream)
-                              : launch_grad_rule<64, BF16, kGradKV>(a, cap, blocks, stream);
-    if (hd == 128)
-        return mode == kGradQ ? launch_grad_rule<128, BF16, kGradQ>(a, cap, blocks, stream)
-                              : launch_grad_rule<128, BF16, kGradKV>(a, cap, blocks, stream);
-    switch (mode) {
-        case kGradQ: return launch_grad_rule<256, BF16, kGradQ>(a, cap, blocks, stream);
-        case kGradK: return launch_grad_rule<256, BF16, kGradK>(a, cap, blocks, stream);
-        default: return launch_grad_rule<256, BF16, kGradV>(a, cap, blocks, stream);
+cudaError_t launch_grad_type(const PackedGradPair &p, const PackedGradArgs *v, int hd, bool cap, cudaStream_t stream) {
+    switch (hd) {
+        case 64: return launch_grad_rule<64, BF16>(p, v, cap, stream);
+        case 128: return launch_grad_rule<128, BF16>(p, v, cap, stream);
+        default: return launch_grad_rule<256, BF16>(p, v, cap, stream);
     }
 }
 

@@ -2,7 +2,7 @@
 #include "packed_bwd.cuh"
 
 namespace fa {
-cudaError_t launch_packed_grad_f16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream) {
-    return launch_grad_type<false>(a, mode, hd, cap, blocks, stream);
+cudaError_t launch_packed_grad_f16(const PackedGradPair &p, const PackedGradArgs *v, int hd, bool cap, cudaStream_t stream) {
+    return launch_grad_type<false>(p, v, hd, cap, stream);
 }
 }  // namespace fa

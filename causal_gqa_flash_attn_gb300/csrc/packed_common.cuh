@@ -420,12 +420,18 @@ struct PackedGradArgs {
     unsigned *err;
 };
 enum { kGradQ = 0, kGradKV = 1, kGradK = 2, kGradV = 3 };
+// One launch: dq, and dk with dv (head_dim 256: dk alone).
+struct PackedGradPair {
+    PackedGradArgs q, k;
+    int q_blocks, k_blocks;
+};
 // Pieces of a key tile are no smaller than this many row tiles: each writes 128 x head_dim
 // fp32 sums of dk and of dv, which are read again, and begins with copies that nothing hides.
 constexpr int kPackedLeastPiece = 4;
 // Rows (or keys) of a moving tile.
 constexpr int packed_grad_rows(int hd) { return hd == 256 ? 64 : 128; }
-cudaError_t launch_packed_grad_bf16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream);
-cudaError_t launch_packed_grad_f16(const PackedGradArgs &a, int mode, int hd, bool cap, int blocks, cudaStream_t stream);
+// v: of dv, for head_dim 256.
+cudaError_t launch_packed_grad_bf16(const PackedGradPair &p, const PackedGradArgs *v, int hd, bool cap, cudaStream_t stream);
+cudaError_t launch_packed_grad_f16(const PackedGradPair &p, const PackedGradArgs *v, int hd, bool cap, cudaStream_t stream);
 
 }  // namespace fa

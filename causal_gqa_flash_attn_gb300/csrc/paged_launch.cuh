@@ -1,7 +1,7 @@
 // paged_launch.cuh -- launches that overlap the end of the kernel before them in
 // the stream (programmatic dependent launch). The kernel's blocks may be placed
-// while that one drains; its first statement is wait_for_stream(), behind which
-// everything before it is done and visible.
+// while that one drains; they call wait_for_stream() before they touch any memory but
+// their own (barriers, TMEM), and behind it everything before them is done and visible.
 #pragma once
 
 #include <cuda_runtime.h>
