@@ -77,9 +77,10 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kern
                     for (int i = 0; i < 16; i += 2) {
                         const int pair = 8 * l + i / 2;
                         if (pair < half) {
-                            const float u0 = x[i], u1 = x[i + 1];
-                            x[i] = Conv<T>::get(Conv<T>::put(u0 * c[pair] - u1 * s[pair]));
-                            x[i + 1] = Conv<T>::get(Conv<T>::put(u0 * s[pair] + u1 * c[pair]));
+                            float x0, x1;
+                            turn(x[i], x[i + 1], c[pair], s[pair], &x0, &x1);
+                            x[i] = Conv<T>::get(Conv<T>::put(x0));
+                            x[i + 1] = Conv<T>::get(Conv<T>::put(x1));
                         }
                     }
                 } else if (V > 1) {  // half is a multiple of 8: eight values on one side
@@ -87,8 +88,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kern
                     for (int e = 0; e < 16; e += 8) {
                         const int d = 16 * l + e;
                         if (d >= rd) continue;
-                        // The low side is fma(own, cos, -(other * sin)), the high one fma(other, sin, own * cos):
-                        // what the compiler makes of rope.cu's sums.
+                        // One side of turn(): the low one fma(own, cos, -(other * sin)), the high one
+                        // fma(other, sin, own * cos).
                         const bool low = d < half;
                         const int pair = low ? d : d - half;
                         const float *f = (low ? c : s) + pair, *g = (low ? s : c) + pair;
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kern
 #pragma unroll
                             for (int m = 0; m < 4; ++m) {
                                 const float own = x[e + i + m], other = o[i + m];
-                                const float r = fmaf(low ? own : other, f4[m], (low ? -other : own) * g4[m]);
+                                const float r = fmaf(low ? own : other, f4[m], __fmul_rn(low ? -other : own, g4[m]));
                                 x[e + i + m] = Conv<T>::get(Conv<T>::put(r));
                             }
                         }
@@ -114,8 +115,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeBlocks<T>) rope_append_kern
                         const bool low = d < half;
                         const float o = Conv<T>::get(src[low ? d + half : d - half]);
                         const int pair = low ? d : d - half;
-                        const float u0 = low ? x[i] : o, u1 = low ? o : x[i];
-                        const float x0 = u0 * c[pair] - u1 * s[pair], x1 = u0 * s[pair] + u1 * c[pair];
+                        float x0, x1;
+                        turn(low ? x[i] : o, low ? o : x[i], c[pair], s[pair], &x0, &x1);
                         x[i] = Conv<T>::get(Conv<T>::put(low ? x0 : x1));
                     }
                 }

@@ -32,6 +32,13 @@ struct alignas(V * sizeof(T)) Vec {
     T x[V];
 };
 
+// A pair turned by the angle of c and s, with its roundings spelt out, as several kernels have to give the same bits:
+// x0 = fma(u0, c, -(u1 s)) and x1 = fma(u0, s, u1 c), the products rounded.
+__device__ __forceinline__ void turn(float u0, float u1, float c, float s, float *x0, float *x1) {
+    *x0 = fmaf(u0, c, -__fmul_rn(u1, s));
+    *x1 = fmaf(u0, s, __fmul_rn(u1, c));
+}
+
 // Cosines cs [tokens][half] and sines sn of tokens tok0 .. tok0 + n_tok - 1.
 __device__ __forceinline__ void turn_table(const RopeArgs &a, int half, int tok0, int n_tok, float *cs, float *sn) {
     for (int i = threadIdx.x; i < n_tok * half; i += kRopeThreads) {
@@ -97,8 +104,10 @@ __device__ __forceinline__ void turn_heads(const RopeArgs &a, int half, int tok0
                     T *p = ADJ && V > 1 ? (k < V / 2 ? x.x + 2 * k : y.x + 2 * k - V) : x.x + k;
                     T *q = ADJ && V > 1 ? p + 1 : y.x + k;
                     const float u0 = Conv<T>::get(*p), u1 = Conv<T>::get(*q);
-                    *p = Conv<T>::put(u0 * c[pair] - u1 * s[pair]);
-                    *q = Conv<T>::put(u0 * s[pair] + u1 * c[pair]);
+                    float x0, x1;
+                    turn(u0, u1, c[pair], s[pair], &x0, &x1);
+                    *p = Conv<T>::put(x0);
+                    *q = Conv<T>::put(x1);
                 }
             }
             *reinterpret_cast<W *>(out + o0) = x;

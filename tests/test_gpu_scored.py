@@ -238,6 +238,40 @@ def test_rope_append_is_rope_and_append(dtype, hd, rd, adjacent):
     assert m.get_device_error() == m.OK
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("hd,rd", [(64, 64), (128, 40), (128, 6), (256, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_a_pair_turns_with_the_stated_roundings(dtype, hd, rd, adjacent):
+    """x0 = fma(u0, c, -(u1 s)) and x1 = fma(u0, s, u1 c) in 32 bits, from the sines and cosines that a pair (1, 0)
+    turns into; and the same bits in the pages of the append that rotates."""
+    m = fa()
+    half, n = rd // 2, 50
+    table = m.rope_table(1e4 ** (-np.arange(half) / half))
+    pos = ints(np.random.default_rng(rd).integers(-9, 1 << 20, n))
+    first = slice(0, rd, 2) if adjacent else slice(0, half)
+    second = slice(1, rd, 2) if adjacent else slice(half, rd)
+    unit = torch.zeros(n, 1, hd, device="cuda")
+    unit[..., first] = 1.0
+    m.rope(unit, None, unit, None, pos, table, adjacent=adjacent)
+    c, s = unit[..., first], unit[..., second]
+    x = torch.randn(n, 3, hd, device="cuda", generator=torch.Generator("cuda").manual_seed(hd + rd)).to(DT[dtype])
+    u0, u1 = x[..., first].float(), x[..., second].float()
+    # (in 64 bits the product is exact, and the sum is rounded to 53 bits before it is rounded to 24: these values
+    # do not lie within 2^-29 of a step from the middle between two)
+    fma = lambda a, b, d: (a.double() * b.double() + d.double()).float()  # noqa: E731
+    want = x.clone()
+    want[..., first] = fma(u0, c, -(u1 * s)).to(DT[dtype])
+    want[..., second] = fma(u0, s, u1 * c).to(DT[dtype])
+    got = torch.empty_like(x)
+    m.rope(x, None, got, None, pos, table, adjacent=adjacent)
+    assert torch.equal(got, want)
+    slots = ints(np.arange(n))
+    pages = [m.alloc_pages(4, 3, hd, 16).fill_(0x5a) for _ in range(2)]
+    m.rope_append(None, x, x, None, pos, table, slots, pages[0], page_rows=16, adjacent=adjacent)
+    m.paged_append(want, x, slots, pages[1], page_rows=16)
+    assert torch.equal(*pages)
+
+
 def test_rope_append_of_many_tokens():
     m = fa()
     T, hq, hkv, hd = 5003, 4, 2, 128
