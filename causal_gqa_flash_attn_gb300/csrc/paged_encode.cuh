@@ -103,50 +103,10 @@ __device__ __forceinline__ void quantise16(const float *x, uint32_t *word, __hal
     *factor = static_cast<uint16_t>(ex << 7);
 }
 
-// 16 values of K and of V of a token's row of kv head h, those of lane l, into the pages. All
-// lanes of a row, and of the warp, call; rows that are not live are encoded and left out.
-template <int HD>
-__device__ __forceinline__ void encode_rows(const PagedAppendArgs &a, const float *k, const float *v, bool live,
-                                            int slot, int page, int h, int l) {
-    constexpr int LANES = HD / 16;  // lanes of a row
-    uint32_t kw[2], vw[2];
-    __half ks, vs;
-    uint16_t kf, vf;
-    quantise16<LANES>(k, kw, &ks, &kf);
-    quantise16<LANES>(v, vw, &vs, &vf);
-    if (!live) return;
-    const int pos = slot & ((1 << a.page_shift) - 1);
-    const int r = pos & (kGroupRows - 1), b = l >> 1, t = 2 * (l & 1);
-    uint8_t *dst = a.pages + ((static_cast<size_t>(page) * a.n_kv + h) *
-                                  ((1 << a.page_shift) / kGroupRows) + pos / kGroupRows) *
-                                 group_bytes(HD);
-    uint8_t *dv = dst + part_bytes(HD);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        *reinterpret_cast<uint32_t *>(dst + k_word_at<HD>(r, b, t + j)) = kw[j];
-        *reinterpret_cast<uint16_t *>(dv + v_half_at<HD>(r, b, 2 * (t + j))) = static_cast<uint16_t>(vw[j]);
-        *reinterpret_cast<uint16_t *>(dv + v_half_at<HD>(r, b, 2 * (t + j) + 1)) =
-            static_cast<uint16_t>(vw[j] >> 16);
-    }
-    if (t == 0) {
-        *reinterpret_cast<__half *>(dst + k_scale_at<HD>(r, b)) = ks;
-        *reinterpret_cast<__half *>(dv + v_scale_at<HD>(r, b)) = vs;
-    }
-    if (l == 0) {
-        *reinterpret_cast<uint16_t *>(dst + factor_offset(HD) + 2 * r) = kf;
-        *reinterpret_cast<uint16_t *>(dv + factor_offset(HD) + 2 * r) = vf;
-    }
-}
-
-// The same for one of both: 16 values of a row of K (or V).
+// A row's 16 values of lane l, quantised, into the K (or V) part of its page.
 template <int HD, bool V>
-__device__ __forceinline__ void encode_row(const PagedAppendArgs &a, const float *x, bool live, int slot, int page,
-                                           int h, int l) {
-    uint32_t w[2];
-    __half scale;
-    uint16_t factor;
-    quantise16<HD / 16>(x, w, &scale, &factor);
-    if (!live) return;
+__device__ __forceinline__ void put_row(const PagedAppendArgs &a, const uint32_t *w, __half scale, uint16_t factor,
+                                        int slot, int page, int h, int l) {
     const int pos = slot & ((1 << a.page_shift) - 1);
     const int r = pos & (kGroupRows - 1), b = l >> 1, t = 2 * (l & 1);
     uint8_t *dst = a.pages + ((static_cast<size_t>(page) * a.n_kv + h) * ((1 << a.page_shift) / kGroupRows) +
@@ -162,6 +122,32 @@ __device__ __forceinline__ void encode_row(const PagedAppendArgs &a, const float
     }
     if (t == 0) *reinterpret_cast<__half *>(dst + (V ? v_scale_at<HD>(r, b) : k_scale_at<HD>(r, b))) = scale;
     if (l == 0) *reinterpret_cast<uint16_t *>(dst + factor_offset(HD) + 2 * r) = factor;
+}
+
+// 16 values of K and of V of a token's row of kv head h, those of lane l, into the pages. All
+// lanes of a row, and of the warp, call; rows that are not live are encoded and left out.
+template <int HD>
+__device__ __forceinline__ void encode_rows(const PagedAppendArgs &a, const float *k, const float *v, bool live,
+                                            int slot, int page, int h, int l) {
+    uint32_t kw[2], vw[2];
+    __half ks, vs;
+    uint16_t kf, vf;
+    quantise16<HD / 16>(k, kw, &ks, &kf);
+    quantise16<HD / 16>(v, vw, &vs, &vf);
+    if (!live) return;
+    put_row<HD, false>(a, kw, ks, kf, slot, page, h, l);
+    put_row<HD, true>(a, vw, vs, vf, slot, page, h, l);
+}
+
+// The same for one of both: 16 values of a row of K (or V).
+template <int HD, bool V>
+__device__ __forceinline__ void encode_row(const PagedAppendArgs &a, const float *x, bool live, int slot, int page,
+                                           int h, int l) {
+    uint32_t w[2];
+    __half scale;
+    uint16_t factor;
+    quantise16<HD / 16>(x, w, &scale, &factor);
+    if (live) put_row<HD, V>(a, w, scale, factor, slot, page, h, l);
 }
 
 }  // namespace fa
