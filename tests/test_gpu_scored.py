@@ -379,3 +379,73 @@ def test_prompts_then_steps(hd, cap, bias):
         assert ((lse - wlse[:, at]).abs() <= 2.0 ** -20 * (hd + cap + 160)).all(), step
         state, now = after, new
     assert m.get_device_error() == m.OK
+
+
+@pytest.mark.parametrize("hd", [64, 256])
+def test_rotated_prompts_then_steps(hd):
+    """What a server of a rotary model with capped scores runs: the prompts' heads are rotated (fa_rope), attend packed, and
+    their rows enter the pages (fa_paged_append: packed attention wants the rotated k, which fa_rope_append keeps to
+    itself); then tokens follow one at a time, rotated and appended in one call, and attend over the pages."""
+    m = fa()
+    hq, hkv, page_rows, steps, cap = 4, 2, 16, 4, 12.0
+    lens = [40, 1, 133]
+    R = len(lens)
+    full = [n + steps for n in lens]
+    cu = np.concatenate([[0], np.cumsum(full)])
+    g = torch.Generator("cuda").manual_seed(hd)
+    q, k, v = torch.randn(sum(full), hq + 2 * hkv, hd, device="cuda", generator=g).bfloat16().split([hq, hkv, hkv], 1)
+    rope = m.rope_table(1e4 ** (-np.arange(hd // 2) / (hd // 2)))
+    qr, kr = torch.empty_like(q), torch.empty_like(k)
+    m.rope(q, k, qr, kr, ints(np.concatenate([np.arange(n) for n in full])), rope)
+    # what the pages hold of each request's rows
+    held = [[ref.decode(*ref.encode(x[cu[r]:cu[r + 1]].float().cpu().numpy())) for x in (kr, v)] for r in range(R)]
+    slopes = np.array([0.5, 0.25, 0.1, 0.01], np.float32)
+    bias = torch.from_numpy(slopes).cuda()
+
+    n_pages = 64
+    pages = m.alloc_pages(n_pages, hkv, hd, page_rows)
+    ring = ints(np.random.default_rng(1).permutation(n_pages))
+    state, table = ints([0, n_pages, 0]), ints(np.full((R, 12), -1))
+    ws = torch.empty(m.paged_attn_workspace_bytes(hd), dtype=torch.uint8, device="cuda")
+    now = ints([0] * R)
+    for step in range(steps + 1):
+        fresh = lens if step == 0 else [1] * R
+        first = [0 if step == 0 else n + step - 1 for n in lens]
+        at = torch.cat([torch.arange(cu[r] + first[r], cu[r] + first[r] + fresh[r]) for r in range(R)]).cuda()
+        T = at.numel()
+        new, after = ints([0] * R), ints([0, 0, 0])
+        cuq, slots, pos = ints([0] * (R + 1)), ints([0] * T), ints([0] * T)
+        m.page_plan(now, ints(fresh), ring, state[:2].clone(), table, after, new, cuq, slots, pos, page_rows=page_rows)
+        qs, ks, vs = q[at], k[at], v[at]
+        out, lse = torch.empty_like(qs), torch.empty(hq, T, device="cuda")
+        if step == 0:
+            m.rope(qs, ks, qs, ks, pos, rope)
+            m.packed_attn(qs, ks, vs, out, cuq, cap=cap, slopes=bias, lse=lse, workspace=torch.empty(
+                m.packed_attn_workspace_bytes(R, T, hq, hkv, hd), dtype=torch.uint8, device="cuda"))
+            m.paged_append(ks, vs, slots, pages, page_rows=page_rows)
+            assert torch.equal(qs, qr[at]) and torch.equal(ks, kr[at])
+            want = packed_ref.packed(qs, ks, vs, cuq.tolist(), slopes=bias, cap=cap)
+            assert ((out.double() - want["out"]).abs() <= want["out_err"]).all()
+            assert ((lse.double() - want["lse"]).abs() <= want["lse_err"]).all()
+        else:
+            m.rope_append(qs, ks, vs, qs, pos, rope, slots, pages, page_rows=page_rows)
+            assert torch.equal(qs, qr[at])
+            m.paged_attn(qs, out, cuq, new, table, pages, n_kv_heads=hkv, page_rows=page_rows, cap=cap, slopes=bias,
+                         lse=lse, workspace=ws)
+            for r in range(R):
+                n = first[r] + 1
+                kp, vp = (x[:n] for x in held[r])
+                want, wlse, size, off, codes = attend(qs[r:r + 1].double().cpu().numpy(), n - 1, kp, vp, cap, slopes, 0, 0,
+                                                      1 / math.sqrt(hd))
+                # the bounds of run_paged for bf16
+                ds = off * 2.0 ** -21 + cap * 2.0 ** -21
+                block = np.abs(vp).reshape(n, hkv, hd // 32, 32).max(-1) / 7
+                block = np.repeat(np.repeat(block, 32, -1), hq // hkv, 1).max(0)
+                tol = size * (2.0 ** -10 * (1 + 2.0 ** -11) + 2 * ds.T[:, :, None]) + 2.0 ** -24
+                tol = tol + 2 * (-(-n // 16) + 40) * 2.0 ** -23 * 16 * block
+                tol = tol + 2.0 ** -8 * (np.abs(want) + tol)
+                assert (np.abs(out[r:r + 1].double().cpu().numpy() - want) <= tol).all(), (step, r)
+                ds = ds + codes * 2.0 ** -21
+                assert (np.abs(lse[:, r:r + 1].double().cpu().numpy() - wlse) <= ds + 2.0 ** -21).all(), (step, r)
+        state, now = after, new
+    assert m.get_device_error() == m.OK
