@@ -124,7 +124,9 @@ constexpr int kTypeF32 = 0;
 constexpr int kTypeF16 = 1;
 constexpr int kTypeBF16 = 2;
 
-// A cap on scores costs them up to 2^-20 of it: beyond this one, more than their weights' rounding.
+// A cap costs scores up to 2^-21 of it (packed_common.cuh, paged_attn.cuh), their weights as much relatively: 2^-9 at this
+// one, half of bfloat16's rounding of them. binary16 rounds weights by 2^-11, which caps from 1024 on exceed, and
+// fp32 pages' tanhf has no such error; the limit is the same for all types.
 constexpr float kMostCap = 4096.0f;
 
 // ---- paged_plan.cu

@@ -26,12 +26,13 @@
 // operands of S and T and one of the others (128 bytes a clock: a product of 128 x 128 x 128 with
 // both of them there takes 517 clocks either way, so that the copies into it and the reads of L and
 // D come on top), and for dq the chain S, T -> t -> acc1. 16384 tokens, 8/2 heads x 128 in bf16:
-// 1202 us, 1144 TFLOP/s counted as 5 products, 1601 as the 7 that run, of 1921 measured. 8192
-// tokens in 23 documents, 16/2 heads x 256 capped: 316 us; there the ends of units (first copies, joins, output) show.
+// 1211 us, 1135 TFLOP/s counted as 5 products, 1589 as the 7 that run, of 1921 measured (call after call for a
+// second 1278 us: at 1330 W the power limit takes the clock from 2070 to 1950 MHz). 8192
+// tokens in 23 documents, 16/2 heads x 256 capped: 318 us; there the ends of units (first copies, joins, output) show.
 //
 // binary16: P has 2^14 of its weight and t a power of two per document that brings the largest
 // |dout| |v| near 2^13, so that neither leaves binary16's normal range on either side; bfloat16
-// has the range.
+// has the range. Both are rounded to the inputs' type, half a step each, as the products take operands of one type.
 #pragma once
 
 #include "packed_common.cuh"

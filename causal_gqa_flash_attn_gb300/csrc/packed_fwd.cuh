@@ -13,20 +13,22 @@
 //   warp 1      issues the products: S = Q K^T into TMEM, O += P V with P from TMEM.
 //   warps 4-11  softmax, one thread a row and tile (or, with one tile, two threads a row, each
 //               with half of the columns): the running maximum in the exp2 domain, which moves
-//               only when a score passes it by 2^8, so that O is seldom rescaled; P, rounded to
-//               the inputs' type as the products take it (half a step of P, the plain form's own
-//               rounding), over S; sums of the unrounded weights in fp32; and the output.
+//               only when a score passes it by 2^8, so that O is seldom rescaled; P over S, rounded
+//               to the inputs' type, as a product's operands have one type (half a step of each
+//               weight: results are 1.1 to 1.4 times as far from 64 bits as with fp32 weights);
+//               sums of the unrounded weights in fp32; and the output.
 // With two tiles the products of one run under the softmax of the other; with one (whose O takes
-// half of TMEM) S has two places, and S(i + 1) runs under the softmax of S(i). TMEM is full either
-// way: 2 x (O 128 + S 128) columns, or O 256 + 2 x S 128.
+// half of TMEM) S has two places, and S(i + 1) runs under the softmax of S(i). TMEM is full at
+// 128 and 256: 2 x (O 128 + S 128) columns, or O 256 + 2 x S 128. At 64 a quarter of it is free (columns 128 to 255):
+// a third S or the next unit's O would fit there.
 //
 // What bounds it: at head_dim 128 the chain S -> softmax -> P V of each tile, of which TMEM holds
-// two and no third (16384 tokens, 8/2 heads: 370 us, 1486 TFLOP/s of 1921 measured for bf16); at
+// two and no third (16384 tokens, 8/2 heads: 370 us, 1485 TFLOP/s of 1921 measured for bf16); at
 // 256 the tensor cores (8192 tokens, 16/2 heads: 327 us, 1680 TFLOP/s); at 64, and wherever scores
 // are capped, the softmax warps, two a scheduler, with issue slots and special units half full each
 // and the latter's slow ones (a clock and SM: 32 exponentials, but 16 reciprocals) behind one another
-// (64: 279 us; 128 capped: 588 us). Documents of a few tiles spend as long on a unit's first copies and
-// its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 73 us, 702
+// (64: 279 us; 128 capped: 597 us). Documents of a few tiles spend as long on a unit's first copies and
+// its output as on the products (8192 tokens in 23 documents, 16/2 heads x 256 capped: 74 us, 692
 // TFLOP/s).
 #pragma once
 
