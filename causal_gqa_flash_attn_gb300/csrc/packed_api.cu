@@ -82,8 +82,10 @@ fa_status check_rule(int dtype, const int32_t *cu, const int32_t *prefix, int si
                      const float *slopes, const void *workspace) {
     if (sink < 0 || !(scale >= 0.0f) || !std::isfinite(scale) || !(cap >= 0.0f) || !std::isfinite(cap))
         return FA_ERR_INVALID;
-    // the factor of a score (score_rule): an infinite one would make scores of 0 a NaN
-    if (!std::isfinite(4.0f * scale) || (cap > 0.0f && !std::isfinite(4.0f * std::fmax(scale, 1.0f) / cap)))
+    // The factor of a score (score_rule): an infinite one would make scores of 0 a NaN, and one below the normal range,
+    // which counts as 0, the -inf of masked ones.
+    if ((scale > 0.0f && !std::isnormal(scale)) || !std::isfinite(4.0f * scale) ||
+        (cap > 0.0f && !std::isfinite(4.0f * std::fmax(scale, 1.0f) / cap)))
         return FA_ERR_INVALID;
     if (dtype == FA_T_F32 || cap > fa::kMostCap) return FA_ERR_UNSUPPORTED;
     if (dtype != FA_T_F16 && dtype != FA_T_BF16) return FA_ERR_INVALID;

@@ -630,7 +630,7 @@ fa_status fa_paged_attn_scored(const void *q, void *out, float *lse, int dtype, 
  *              is written.
  *   prefix     [n_docs] int32 (device) or NULL (none): keys of each document that
  *              all its queries attend, cut to [0, its tokens].
- *   scale      > 0, 4 * scale finite; 0 means 1 / sqrt(head_dim).
+ *   scale      >= 2^-126 (the normal range), 4 * scale finite; 0 means 1 / sqrt(head_dim).
  *   cap        0 for none, or up to 4096 (FA_ERR_UNSUPPORTED beyond, FA_ERR_INVALID
  *              where 4 / cap or 4 * scale / cap is not finite). Capped scores are off by up to 2^-21 cap.
  *   slopes     [n_q_heads] fp32 (device) or NULL for no bias. (They get no gradient.)

@@ -86,7 +86,8 @@ def test_packed_workspaces(fa):
 
 def test_packed_factors_of_scores_are_finite(fa):
     """scale * log2 e, and 2 * scale * log2 e / cap where scores are capped: an infinite one times a score of 0 is a
-    NaN, so that such calls are refused. Without a workspace, what is taken goes no further than its absence."""
+    NaN, and so is 0 times the -inf of a masked score, where a factor below the normal range is flushed; such calls
+    are refused. Without a workspace, what is taken goes no further than its absence."""
     names = ("q k v out lse type qs ks vs os cu prefix docs T hq hkv hd sink win scale cap slopes ws wsb stream").split()
     call = caller(fa.lib().fa_packed_attn, names, q=16, k=32, v=48, out=64, lse=16, qs=512, ks=128, vs=128, os=512,
                   **SHARED)
@@ -95,9 +96,10 @@ def test_packed_factors_of_scores_are_finite(fa):
     grad = caller(fa.lib().fa_packed_attn_grad, names, q=16, k=32, v=48, out=64, lse=16, dout=80, dq=96, dk=112, dv=128,
                   qs=512, ks=128, vs=128, os=512, dos=512, dqs=512, dks=128, dvs=128, **SHARED)
     for f in (call, grad):
-        for bad in (dict(scale=9e37), dict(scale=1e3, cap=1e-36), dict(scale=8.0, cap=9e-38), dict(scale=9e37, cap=1.0)):
+        for bad in (dict(scale=9e37), dict(scale=1e3, cap=1e-36), dict(scale=8.0, cap=9e-38), dict(scale=9e37, cap=1.0),
+                    dict(scale=1.1e-38), dict(scale=1e-45), dict(scale=1.1e-38, cap=3.0)):
             assert f(wsb=0, **bad) == fa.ERR_INVALID, bad
-        for good in (dict(scale=8e37), dict(scale=1e3, cap=2e-35), dict(cap=2e-38), dict(scale=8.0, cap=1e-37),
+        for good in (dict(scale=8e37), dict(scale=1.2e-38), dict(scale=1e3, cap=2e-35), dict(cap=2e-38), dict(scale=8.0, cap=1e-37),
                      dict(scale=8e37, cap=4096.0)):
             assert f(wsb=0, **good) == fa.ERR_WORKSPACE, good
 
