@@ -786,7 +786,7 @@ __global__ void __launch_bounds__((GradCfg<HD, kGradQ>::THREADS), 1)
     else
         grad_units<HD, BF16, CAP, BIAS, SECOND>(p.k, block - p.q_blocks, p.k_blocks);
 }
-// dv of head_dim 256, which uses dk's partial sums after it.
+// dv of head_dim 256, whose partial sums take the places of dk's: a launch after it.
 template <int HD, bool BF16, bool CAP, bool BIAS>
 __global__ void __launch_bounds__((GradCfg<HD, kGradV>::THREADS), 1)
     packed_grad_v_kernel(const __grid_constant__ PackedGradArgs a) {
